@@ -465,6 +465,100 @@ int dpg_step_noalloc(const dpg_plan_t* plan, const void* const* grads, int32_t g
                      float* exp_avg_sq, void* const* param_views, int32_t n_views,
                      float* bucket_sqnorm, int64_t* bucket_nonfinite, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Matrix-orthogonalising optimizer (Muon: Jordan et al. 2024, "Muon: An
+ * optimizer for hidden layers in neural networks"; the pages name Adam only)
+ *
+ * Hidden weight MATRICES are updated by the orthogonalised momentum of their
+ * reduced gradient instead of by Adam; embeddings, gains and the head stay
+ * with dpg_step on a plan of their own.  All functions work on the flat
+ * buffers of one bucket plan whose parameters are matrices (or stacks of
+ * equally shaped matrices: the experts of a layer, the parts of a fused
+ * projection).
+ *
+ * dpg_muon_hparams
+ *   momentum   mu in [0, 1); nesterov != 0: look-ahead update
+ *   n_steps    Newton-Schulz steps, 1..DPG_MAX_NS_STEPS, step k with the
+ *              quintic coefficients coeffs[k] = {a, b, c}
+ *   eps        >= 1e-30: floor of the Frobenius norm a matrix is divided by
+ *   lr, weight_decay, scale_rule: see dpg_muon_apply
+ * ------------------------------------------------------------------------- */
+#define DPG_MAX_NS_STEPS 16
+#define DPG_SCALE_SPECTRAL 0 /* sqrt(max(1, rows / cols))   */
+#define DPG_SCALE_RMS 1      /* 0.2 * sqrt(max(rows, cols)) */
+typedef struct {
+    double lr, momentum, weight_decay, eps;
+    double coeffs[DPG_MAX_NS_STEPS][3];
+    int32_t n_steps, nesterov, scale_rule, reserved;
+} dpg_muon_hparams;
+
+/* The matrices of a plan.  rows[p], cols[p] (HOST arrays, n_params entries,
+ * each >= 1): parameter p is numel_p / (rows[p] * cols[p]) row-major matrices
+ * one after the other; a numel that is not a multiple of rows * cols is
+ * DPG_ERR_INVALID_ARG, a zero-size parameter holds no matrix.  The object
+ * keeps what it needs of the plan (which may be destroyed before it), the
+ * tile tables, and a device workspace of workspace_bytes that it allocates on
+ * its first device call or in dpg_matrices_upload (call that before a stream
+ * capture).  It serves one device; calls that use one object must not overlap
+ * on the GPU.  Free with dpg_matrices_destroy. */
+typedef struct dpg_matrices dpg_matrices_t;
+int dpg_plan_matrices(const dpg_plan_t* plan, const int64_t* rows, const int64_t* cols,
+                      dpg_matrices_t** out);
+void dpg_matrices_destroy(dpg_matrices_t* mats);
+int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* workspace_bytes);
+int dpg_matrices_upload(dpg_matrices_t* mats);
+
+/* Momentum of the reduced gradient, buckets [b0, b1), in one pass (binary32,
+ * no FMA; s and g as in dpg_reduce_scatter_adam):
+ *   g = (x_0 + ... + x_{R-1}) * fp32(1/G)
+ *   momentum[i] = mu * momentum[i] + (1 - mu) * g
+ *   update[i]   = nesterov ? (1 - mu) * g + mu * momentum[i] : momentum[i]
+ * grads, grads_dtype, last_micro_bf16, valid_tokens: as
+ * dpg_reduce_scatter_adam (device or page-locked host gradients).  momentum:
+ * flat fp32, updated in place.  update: flat buffer of update_dtype (DPG_BF16,
+ * rounded to nearest even, 16-byte aligned; or DPG_F32, 32-byte aligned).
+ * mu and 1 - mu are computed in double and rounded once. */
+int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t grads_dtype,
+                      const void* const* last_micro_bf16, const int64_t* valid_tokens,
+                      int32_t n_counts, const dpg_muon_hparams* hp, float* momentum, void* update,
+                      int32_t update_dtype, int32_t b0, int32_t b1, void* stream);
+
+/* Orthogonalisation of every matrix U of the flat buffer `update`
+ * (DPG_BF16 or DPG_F32) by n_steps Newton-Schulz steps:
+ *   X = U / max(||U||_F, eps);  A = X X^T;  X <- a X + (b A + c A^2) X
+ * (on U^T when rows > cols, so that A has the shorter side), written to
+ * ortho_bf16 (flat bf16; may be `update` itself when that is bf16, and may be
+ * the start of `update`'s memory when that is fp32).  Padding slots are
+ * neither read nor written.
+ * Arithmetic: X is held as a pair of fp16 numbers under a power-of-two scale
+ * (22 bits), the off-diagonal parts of A and bA + cA^2 in one fp16 number,
+ * their diagonals and every sum in fp32.  The result is within about 1e-3
+ * (relative Frobenius norm) of the exact one, also for matrices of low rank;
+ * see the tests for the bound.  A matrix that holds a NaN or an infinity
+ * gives NaN everywhere, a zero matrix zeros; other matrices are not affected.
+ * Coefficients under which the iteration could leave fp16's range (singular
+ * values above 32 starting from [0, 1]) are DPG_ERR_INVALID_ARG. */
+int dpg_orthogonalize(dpg_matrices_t* mats, const void* update, int32_t update_dtype,
+                      const dpg_muon_hparams* hp, void* ortho_bf16, void* stream);
+
+/* Weight update from the orthogonalised update o (flat bf16), every element
+ * of every matrix, binary32, no FMA:
+ *   w <- w - fp32(lr * weight_decay) * w     (if weight_decay != 0)
+ *   w <- w - fp32(lr * scale) * o            scale by scale_rule and shape
+ *   param_views[k] = bf16_rne(w)             (k < n_views <= DPG_MAX_VIEWS) */
+int dpg_muon_apply(dpg_matrices_t* mats, const void* ortho_bf16, const dpg_muon_hparams* hp,
+                   float* master, void* const* param_views, int32_t n_views, void* stream);
+
+/* One whole step over every matrix of the plan: dpg_muon_momentum into
+ * `update` (caller's flat buffer of update_dtype), dpg_orthogonalize in place
+ * in it (bf16 results at its start), dpg_muon_apply.  All arguments are
+ * checked before anything is launched; mats must be of `plan`. */
+int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* const* grads,
+                  int32_t grads_dtype, const void* const* last_micro_bf16,
+                  const int64_t* valid_tokens, int32_t n_counts, const dpg_muon_hparams* hp,
+                  float* master, float* momentum, void* update, int32_t update_dtype,
+                  void* const* param_views, int32_t n_views, void* stream);
+
 /* Launch shape -------------------------------------------------------------- */
 /* By default the fused passes (dpg_step, dpg_reduce_scatter_adam,
  * dpg_step_fold2, dpg_adam_from_reduced, dpg_allreduce_grads and

@@ -32,6 +32,9 @@ DPG_BF16 = 0
 DPG_F32 = 1
 DPG_MAX_REPLICAS = 64
 DPG_MAX_VIEWS = 64
+DPG_MAX_NS_STEPS = 16
+DPG_SCALE_SPECTRAL = 0
+DPG_SCALE_RMS = 1
 
 # symbols declared in include/dpg.h
 EXPORTED = (
@@ -45,6 +48,8 @@ EXPORTED = (
     "dpg_accumulate_pair", "dpg_step_fold2", "dpg_set_fused_max_ctas",
     "dpg_set_programmatic_launch", "dpg_reduce_scatter_adam_when_ready", "dpg_step_deferred",
     "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit",
+    "dpg_plan_matrices", "dpg_matrices_destroy", "dpg_matrices_info", "dpg_matrices_upload",
+    "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply", "dpg_muon_step",
 )
 DPG_MAX_STATE_ARRAYS = 8
 DPG_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -79,6 +84,35 @@ class HParams:
     def c(self) -> dpg_hparams:
         return dpg_hparams(self.lr, self.beta1, self.beta2, self.eps, self.weight_decay,
                            int(self.step))
+
+
+class dpg_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("eps", ctypes.c_double),
+                ("coeffs", (ctypes.c_double * 3) * DPG_MAX_NS_STEPS),
+                ("n_steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
+                ("scale_rule", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+@dataclass
+class MuonHParams:
+    """Hyper-parameters of the matrix-orthogonalising step; ``coeffs`` holds one
+    (a, b, c) per Newton-Schulz step (default: five steps of Jordan et al.)."""
+    lr: float = 0.02
+    momentum: float = 0.95
+    weight_decay: float = 0.0
+    eps: float = 1e-7
+    nesterov: bool = True
+    coeffs: Sequence[Sequence[float]] = ((3.4445, -4.7750, 2.0315),) * 5
+    scale_rule: int = DPG_SCALE_SPECTRAL
+
+    def c(self) -> dpg_muon_hparams:
+        h = dpg_muon_hparams(lr=self.lr, momentum=self.momentum, weight_decay=self.weight_decay,
+                             eps=self.eps, n_steps=len(self.coeffs), nesterov=int(self.nesterov),
+                             scale_rule=int(self.scale_rule))
+        for k, abc in enumerate(list(self.coeffs)[:DPG_MAX_NS_STEPS]):
+            h.coeffs[k][:] = [float(x) for x in abc]
+        return h
 
 
 _lib = None
@@ -137,6 +171,15 @@ def lib() -> ctypes.CDLL:
         L.dpg_plan_shards.argtypes = [P, ctypes.POINTER(P)]
         L.dpg_debug_checks.argtypes = [P, P, P]
         L.dpg_debug_set_limit.argtypes = [i64]
+        L.dpg_plan_matrices.argtypes = [P, P, P, ctypes.POINTER(P)]
+        L.dpg_matrices_destroy.argtypes = [P]
+        L.dpg_matrices_destroy.restype = None
+        L.dpg_matrices_info.argtypes = [P, P, P]
+        L.dpg_matrices_upload.argtypes = [P]
+        L.dpg_muon_momentum.argtypes = [P, P, i32, P, P, i32, P, P, P, i32, i32, i32, P]
+        L.dpg_orthogonalize.argtypes = [P, P, i32, P, P, P]
+        L.dpg_muon_apply.argtypes = [P, P, P, P, P, i32, P]
+        L.dpg_muon_step.argtypes = [P, P, P, i32, P, P, i32, P, P, P, P, i32, P, i32, P]
         L.dpg_time_next_fused_launch.restype = c_int
         for name in ("dpg_plan_buckets", "dpg_plan_info", "dpg_plan_bucket", "dpg_plan_param",
                      "dpg_plan_export", "dpg_plan_upload", "dpg_pack", "dpg_unpack",
@@ -147,7 +190,10 @@ def lib() -> ctypes.CDLL:
                      "dpg_gather_params_bf16", "dpg_accumulate_pair", "dpg_step_fold2",
                      "dpg_set_fused_max_ctas", "dpg_set_programmatic_launch",
                      "dpg_reduce_scatter_adam_when_ready", "dpg_step_deferred",
-                     "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit"):
+                     "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit",
+                     "dpg_plan_matrices", "dpg_matrices_info", "dpg_matrices_upload",
+                     "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply",
+                     "dpg_muon_step"):
             getattr(L, name).restype = c_int
         _lib = L
     return _lib
@@ -690,6 +736,142 @@ def dpg_gather_params_bf16(plan: Plan, param_bf16: Ptr, param_views: Sequence[Pt
     _check(lib().dpg_gather_params_bf16(plan.handle, _ptr(param_bf16), _ptrs(param_views),
                                         len(param_views), b0, plan.n_buckets if b1 is None else b1,
                                         _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# matrix-orthogonalising optimizer (see include/dpg.h)
+# --------------------------------------------------------------------------
+class Matrices:
+    """Owning handle of a dpg_matrices_t: the matrices of a plan's parameters."""
+
+    def __init__(self, handle: int, total_padded: int):
+        self._h = ctypes.c_void_p(handle)
+        self.total_padded = total_padded
+        n, ws = ctypes.c_int32(), ctypes.c_int64()
+        _check(lib().dpg_matrices_info(self._h, ctypes.byref(n), ctypes.byref(ws)))
+        self.n_matrices, self.workspace_bytes = n.value, ws.value
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        if self._h is None:
+            raise ValueError("matrices have been destroyed")
+        return self._h
+
+    def destroy(self):
+        if getattr(self, "_h", None) is not None and _lib is not None:
+            _lib.dpg_matrices_destroy(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def dpg_plan_matrices(plan: Plan, rows: Sequence[int], cols: Sequence[int]) -> Matrices:
+    """Parameter p of `plan` as row-major rows[p] x cols[p] matrices, stacked
+    when its numel is a multiple of rows[p] * cols[p]."""
+    r = np.ascontiguousarray(np.asarray(rows, dtype=np.int64).reshape(-1))
+    c = np.ascontiguousarray(np.asarray(cols, dtype=np.int64).reshape(-1))
+    if r.size != plan.n_params or c.size != plan.n_params:
+        raise ValueError(f"need {plan.n_params} shapes, got {r.size} rows and {c.size} cols")
+    out = ctypes.c_void_p()
+    _check(lib().dpg_plan_matrices(plan.handle, r.ctypes.data if r.size else None,
+                                   c.ctypes.data if c.size else None, ctypes.byref(out)))
+    return Matrices(out.value, plan.total_padded)
+
+
+def dpg_matrices_upload(mats: Matrices):
+    _check(lib().dpg_matrices_upload(mats.handle))
+
+
+def _flat_dtype(t, dtype, numel: int, what: str) -> int:
+    """DPG_BF16 or DPG_F32 of a flat tensor (or the given one of a raw pointer)."""
+    if t is None or isinstance(t, int):
+        if dtype is None:
+            raise TypeError(f"pass the dtype of {what} explicitly with a raw pointer")
+        return dtype
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    dt = DPG_BF16 if t.dtype == torch.bfloat16 else DPG_F32
+    _need(t, "bf16" if dt == DPG_BF16 else "f32", numel, what)
+    return dt
+
+
+def _muon_grads(plan: Plan, grads, last_micro, grads_dtype) -> int:
+    if len(grads) != plan.R:
+        raise ValueError(f"need R={plan.R} gradient buffers, got {len(grads)}")
+    if last_micro is not None and len(last_micro) != plan.R:
+        raise ValueError(f"need R={plan.R} last microbatches, got {len(last_micro)}")
+    gd = _grad_dtype(grads) if grads_dtype is None else grads_dtype
+    for k, g in enumerate(grads):
+        _need_in(g, "bf16" if gd == DPG_BF16 else "f32", plan.total_padded, f"grads[{k}]")
+    for k, g in enumerate(last_micro or ()):
+        _need_in(g, "bf16", plan.total_padded, f"last_micro[{k}]")
+    return gd
+
+
+def dpg_muon_momentum(plan: Plan, grads: Sequence[Ptr], valid_tokens, hp: MuonHParams,
+                      momentum: Ptr, update: Ptr, *, last_micro: Sequence[Ptr] = None, b0: int = 0,
+                      b1: Optional[int] = None, grads_dtype: Optional[int] = None,
+                      update_dtype: Optional[int] = None, stream=None):
+    """momentum <- mu momentum + (1 - mu) g of the reduced, normalised gradient
+    g; update (bf16 or fp32) <- the look-ahead (nesterov) or the momentum."""
+    gd = _muon_grads(plan, grads, last_micro, grads_dtype)
+    _need(momentum, "f32", plan.total_padded, "momentum")
+    ud = _flat_dtype(update, update_dtype, plan.total_padded, "update")
+    tok, n_tok = _tokens(valid_tokens)
+    hpc = hp.c()
+    _check(lib().dpg_muon_momentum(
+        plan.handle, _ptrs(grads), gd, None if last_micro is None else _ptrs(last_micro),
+        tok.ctypes.data, n_tok, ctypes.byref(hpc), _ptr(momentum), _ptr(update), ud, b0,
+        plan.n_buckets if b1 is None else b1, _stream(stream)))
+
+
+def dpg_orthogonalize(mats: Matrices, update: Ptr, hp: MuonHParams, ortho: Ptr, *,
+                      update_dtype: Optional[int] = None, stream=None):
+    """ortho (flat bf16) <- every matrix of `update` (bf16 or fp32) after the
+    Newton-Schulz steps hp.coeffs."""
+    ud = _flat_dtype(update, update_dtype, mats.total_padded, "update")
+    _need(ortho, "bf16", mats.total_padded, "ortho")
+    hpc = hp.c()
+    _check(lib().dpg_orthogonalize(mats.handle, _ptr(update), ud, ctypes.byref(hpc), _ptr(ortho),
+                                   _stream(stream)))
+
+
+def dpg_muon_apply(mats: Matrices, ortho: Ptr, hp: MuonHParams, master: Ptr,
+                   param_views: Sequence[Ptr] = (), *, stream=None):
+    """Weight decay and the orthogonalised update on master; bf16 views."""
+    _need(ortho, "bf16", mats.total_padded, "ortho")
+    _need(master, "f32", mats.total_padded, "master")
+    for k, t in enumerate(param_views):
+        _need(t, "bf16", mats.total_padded, f"param_views[{k}]")
+    hpc = hp.c()
+    _check(lib().dpg_muon_apply(mats.handle, _ptr(ortho), ctypes.byref(hpc), _ptr(master),
+                                _ptrs(param_views), len(param_views), _stream(stream)))
+
+
+def dpg_muon_step(plan: Plan, mats: Matrices, grads: Sequence[Ptr], valid_tokens, hp: MuonHParams,
+                  master: Ptr, momentum: Ptr, update: Ptr, param_views: Sequence[Ptr] = (), *,
+                  last_micro: Sequence[Ptr] = None, grads_dtype: Optional[int] = None,
+                  update_dtype: Optional[int] = None, stream=None):
+    """One whole step: momentum, orthogonalisation in place in `update` (bf16
+    results at its start), weight update."""
+    gd = _muon_grads(plan, grads, last_micro, grads_dtype)
+    for name, t in (("master", master), ("momentum", momentum)):
+        _need(t, "f32", plan.total_padded, name)
+    ud = _flat_dtype(update, update_dtype, plan.total_padded, "update")
+    for k, t in enumerate(param_views):
+        _need(t, "bf16", plan.total_padded, f"param_views[{k}]")
+    tok, n_tok = _tokens(valid_tokens)
+    hpc = hp.c()
+    _check(lib().dpg_muon_step(
+        plan.handle, mats.handle, _ptrs(grads), gd,
+        None if last_micro is None else _ptrs(last_micro), tok.ctypes.data, n_tok,
+        ctypes.byref(hpc), _ptr(master), _ptr(momentum), _ptr(update), ud, _ptrs(param_views),
+        len(param_views), _stream(stream)))
 
 
 def dpg_set_fused_max_ctas(max_ctas: int = 0):

@@ -1,0 +1,237 @@
+// dpg_matrices.cpp -- host tables of a plan's matrices (shapes, workspace
+// layout, tiles, work items) and the constants of the Newton-Schulz steps.
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <new>
+
+#include "dpg_ortho.h"
+
+namespace dpg {
+
+static int64_t ceil_div(int64_t x, int64_t d) { return (x + d - 1) / d; }
+static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
+
+// Lays the matrices out; false when an index would leave its type.
+static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Matrices& M) {
+    M.total_padded = p.total_padded;
+    M.n_params = p.n_params;
+    M.param_offset = p.param_offset;
+    M.numels = p.numels;
+    M.scales.assign(2 * size_t(p.n_params), 1.0);
+    for (int32_t q = p.n_params - 1; q >= 0; --q) {   // flat order
+        const double r = double(rows[q]), c = double(cols[q]);
+        M.scales[2 * size_t(q)] = std::sqrt(std::max(1.0, r / c));
+        M.scales[2 * size_t(q) + 1] = 0.2 * std::sqrt(std::max(r, c));
+        const int64_t numel = p.numels[q];
+        for (int64_t e = 0; e < numel; e += kApplyChunk)
+            M.apply_items.push_back({p.param_offset[q] + e,
+                                     int32_t(std::min<int64_t>(kApplyChunk, numel - e)), q});
+        const int64_t one = rows[q] * cols[q];
+        for (int64_t e = 0; e < numel; e += one) {
+            MatDesc d{};
+            d.off = p.param_offset[q] + e;
+            d.rows = int32_t(rows[q]);
+            d.cols = int32_t(cols[q]);
+            d.tall = rows[q] > cols[q];
+            d.m = int32_t(std::min(rows[q], cols[q]));
+            d.n = int32_t(std::max(rows[q], cols[q]));
+            d.kn = int32_t(ceil_div(d.n, kBlkCols));
+            d.km = int32_t(ceil_div(d.m, kBlkCols));
+            const int64_t tm = ceil_div(d.m, kOrthoTile), tn = ceil_div(d.n, kOrthoTile);
+            if (tm > 0x7FFF || tn > 0x7FFF) return false;
+            const int64_t rb = tm * (kOrthoTile / kBlkRows);
+            d.cbx = int32_t(tn * (kOrthoTile / kBlkCols));
+            d.cba = int32_t(tm * (kOrthoTile / kBlkCols));
+            const int64_t xb = rb * d.cbx, ab = rb * d.cba;
+            d.x[0] = M.n_blocks;
+            d.x[1] = d.x[0] + xb;
+            d.lo = d.x[1] + xb;
+            d.a = d.lo + xb;
+            d.b = d.a + ab;
+            M.n_blocks = d.b + ab;
+            // a block's first 128-byte row is a 32-bit coordinate of the copies
+            if (M.n_blocks * kBlkRows > 0x7FFFFFFFll) return false;
+            d.diag = M.n_diag;
+            d.rows_pad = int32_t(tm * kOrthoTile);
+            M.n_diag += d.rows_pad;
+            d.rowsq = M.n_rowsq;
+            M.n_rowsq += int64_t(d.rows_pad) * d.cbx;
+            const int32_t mat = int32_t(M.mats.size());
+            d.norm0 = int32_t(M.norm_items.size());
+            for (int64_t s = 0; s < one; s += kNormChunk)
+                M.norm_items.push_back({mat, int32_t(std::min<int64_t>(kNormChunk, one - s)), s});
+            d.norm1 = int32_t(M.norm_items.size());
+            for (int64_t i = 0; i < rb; ++i)
+                for (int64_t j = 0; j < d.cbx; ++j)
+                    M.conv_items.push_back({mat, int32_t(i), int32_t(j), 0});
+            for (int64_t i = 0; i < tm; ++i) {
+                for (int64_t j = i; j < tm; ++j) {   // A and A^2 are symmetric
+                    M.tiles[kProdA].push_back({mat, int16_t(i), int16_t(j)});
+                    M.tiles[kProdB].push_back({mat, int16_t(i), int16_t(j)});
+                }
+                for (int64_t j = 0; j < tn; ++j) M.tiles[kProdX].push_back({mat, int16_t(i), int16_t(j)});
+            }
+            M.mats.push_back(d);
+        }
+    }
+    // the tiles with the longest sums first, so that a launch ends on short ones
+    for (int k = 0; k < 3; ++k)
+        std::stable_sort(M.tiles[k].begin(), M.tiles[k].end(),
+                         [&](const OrthoTile& x, const OrthoTile& y) {
+                             const MatDesc &u = M.mats[size_t(x.mat)], &v = M.mats[size_t(y.mat)];
+                             return k == kProdA ? u.kn > v.kn : u.km > v.km;
+                         });
+    int64_t o = M.n_blocks * kBlkBytes;
+    M.o_diag = o;   // three vectors: diagonals of A, of B, and the part of B's that X's low half sees
+    o += up256(3 * M.n_diag * int64_t(sizeof(float)));
+    M.o_rowsq = o;
+    o += up256(M.n_rowsq * int64_t(sizeof(float)));
+    M.o_part = o;
+    o += up256(int64_t(M.norm_items.size()) * int64_t(sizeof(double)));
+    M.o_scal = o;   // per matrix: power-of-two scale of X, 1 / (norm times it)
+    o += up256(int64_t(M.mats.size()) * 2 * int64_t(sizeof(float)));
+    M.o_count = o;  // per matrix: arrivals of its norm items
+    o += up256(int64_t(M.mats.size()) * int64_t(sizeof(int32_t)));
+    M.o_status = o;
+    o += 256;
+    M.workspace_bytes = o;
+    return M.norm_items.size() < 0x7FFFFFFF && M.conv_items.size() < 0x7FFFFFFF &&
+           M.apply_items.size() < 0x7FFFFFFF;
+}
+
+// Largest |a s + b s^3 + c s^5| for s in [0, hi]: at an end or where the
+// derivative a + 3 b s^2 + 5 c s^4 vanishes.
+static double largest_odd(double a, double b, double c, double hi) {
+    auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
+    double best = p(hi);
+    const double A = 5.0 * c, B = 3.0 * b;
+    double root[2];
+    int n = 0;
+    if (A != 0.0) {
+        const double disc = B * B - 4.0 * A * a;
+        if (disc >= 0.0) {
+            root[n++] = (-B + std::sqrt(disc)) / (2.0 * A);
+            root[n++] = (-B - std::sqrt(disc)) / (2.0 * A);
+        }
+    } else if (B != 0.0) {
+        root[n++] = -a / B;
+    }
+    for (int k = 0; k < n; ++k)
+        if (root[k] > 0.0 && root[k] < hi * hi) best = std::max(best, p(std::sqrt(root[k])));
+    return best;
+}
+
+// Largest |b l + c l^2| for l in [0, hi].
+static double largest_quad(double b, double c, double hi) {
+    double best = std::fabs(b * hi + c * hi * hi);
+    if (c != 0.0) {
+        const double l = -b / (2.0 * c);
+        if (l > 0.0 && l < hi) best = std::max(best, std::fabs(b * l + c * l * l));
+    }
+    return best;
+}
+
+// The power of two that maps values up to `most` below 2^15 with a factor of
+// two to spare for rounding (fp16 ends at 65504).
+static float scale_for(double most) {
+    int e = 0;
+    std::frexp(std::max(most, 1e-12), &e);   // most < 2^e
+    return float(std::ldexp(1.0, 14 - e));
+}
+
+int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who) {
+    if (!hp) return fail(DPG_ERR_INVALID_ARG, "%s: hparams is NULL", who);
+    if (hp->n_steps < 1 || hp->n_steps > DPG_MAX_NS_STEPS)
+        return fail(DPG_ERR_INVALID_ARG, "%s: n_steps %d outside [1, %d]", who, hp->n_steps,
+                    DPG_MAX_NS_STEPS);
+    if (!(hp->eps >= 1e-30) || !std::isfinite(hp->eps))
+        return fail(DPG_ERR_INVALID_ARG, "%s: eps must be finite and >= 1e-30", who);
+    // Every entry of a matrix is at most its largest singular value, which is
+    // at most 1 for X_0 and at most largest_odd() of the previous bound after
+    // a step; the entries of A and of bA + cA^2 follow.  The 1% covers what
+    // the roundings of a step can add.
+    double top = 1.0;
+    float sx = 0.0f;
+    for (int k = 0; k < hp->n_steps; ++k) {
+        const double a = hp->coeffs[k][0], b = hp->coeffs[k][1], c = hp->coeffs[k][2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+            return fail(DPG_ERR_INVALID_ARG, "%s: coeffs[%d] not finite", who, k);
+        OrthoStep& s = steps[k];
+        s.a = float(a);
+        s.b = float(b);
+        s.c = float(c);
+        s.inv_sx = k == 0 ? 0.0f : 1.0f / sx;
+        s.sa = scale_for(top * top);
+        s.inv_sa = 1.0f / s.sa;
+        s.sb = scale_for(largest_quad(b, c, top * top));
+        s.inv_sb = 1.0f / s.sb;
+        top = std::max(largest_odd(a, b, c, top) * 1.01, 1e-6);
+        if (!(top <= 32.0))
+            return fail(DPG_ERR_INVALID_ARG, "%s: after step %d singular values may reach %g", who, k, top);
+        s.sx_next = sx = scale_for(top);
+    }
+    return DPG_OK;
+}
+
+}  // namespace dpg
+
+using dpg::fail;
+
+extern "C" {
+
+int dpg_plan_matrices(const dpg_plan_t* plan, const int64_t* rows, const int64_t* cols,
+                      dpg_matrices_t** out) {
+    dpg::clear_error();
+    if (!out) return fail(DPG_ERR_INVALID_ARG, "dpg_plan_matrices: out is NULL");
+    *out = nullptr;
+    if (!plan) return fail(DPG_ERR_INVALID_ARG, "dpg_plan_matrices: plan is NULL");
+    const dpg::Plan& p = plan->p;
+    if (p.n_params > 0 && (!rows || !cols))
+        return fail(DPG_ERR_INVALID_ARG, "dpg_plan_matrices: rows or cols is NULL");
+    for (int32_t q = 0; q < p.n_params; ++q) {
+        if (rows[q] < 1 || cols[q] < 1 || rows[q] > (1 << 23) || cols[q] > (1 << 23))
+            return fail(DPG_ERR_INVALID_ARG, "dpg_plan_matrices: parameter %d: shape outside [1, 2^23]", q);
+        if (p.numels[q] % (rows[q] * cols[q]) != 0)
+            return fail(DPG_ERR_INVALID_ARG,
+                        "dpg_plan_matrices: parameter %d: %lld elements are no stack of %lld x %lld", q,
+                        (long long)p.numels[q], (long long)rows[q], (long long)cols[q]);
+    }
+    dpg_matrices* h = new (std::nothrow) dpg_matrices();
+    if (!h) return fail(DPG_ERR_OOM, "dpg_plan_matrices: out of host memory");
+    bool ok = false;
+    try {
+        ok = dpg::lay_out(p, rows, cols, h->m);
+    } catch (const std::exception&) {
+        delete h;
+        return fail(DPG_ERR_OOM, "dpg_plan_matrices: out of host memory");
+    }
+    if (!ok) {
+        delete h;
+        return fail(DPG_ERR_INVALID_ARG, "dpg_plan_matrices: matrices too large for one object");
+    }
+    *out = h;
+    return DPG_OK;
+}
+
+void dpg_matrices_destroy(dpg_matrices_t* mats) {
+    if (!mats) return;
+    dpg::release_matrices(mats->m);
+    delete mats;
+}
+
+int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* workspace_bytes) {
+    dpg::clear_error();
+    if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_matrices_info: mats is NULL");
+    if (n_matrices) *n_matrices = int32_t(mats->m.mats.size());
+    if (workspace_bytes) *workspace_bytes = mats->m.workspace_bytes;
+    return DPG_OK;
+}
+
+int dpg_matrices_upload(dpg_matrices_t* mats) {
+    dpg::clear_error();
+    if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_matrices_upload: mats is NULL");
+    return dpg::upload_matrices(mats->m);
+}
+
+}  // extern "C"

@@ -1,0 +1,117 @@
+// dpg_ortho.h -- the matrices of a plan and their Newton-Schulz workspace:
+// declarations shared by the host tables (dpg_matrices.cpp), the
+// orthogonalisation (dpg_ortho.cu) and the momentum / apply passes
+// (dpg_muon.cu).
+#pragma once
+
+#include <cstdint>
+#include <mutex>
+#include <vector>
+
+#include "dpg_internal.h"
+
+namespace dpg {
+
+// Workspace matrices are stored as blocks of 128 rows x 64 columns of fp16,
+// 16 KB each: row r of a block is 128 bytes, whose eight 16-byte chunks are
+// permuted by chunk ^ (r mod 8).  That is the shared-memory image the tensor
+// cores read with a 128-byte swizzle, both as rows of K (a block of 128 rows,
+// 64 deep) and as columns (64 columns, 128 -- or 64 -- deep), so a block
+// moves between HBM and shared memory as one contiguous copy and the same
+// stored X serves X X^T and B X.  Rows are padded to 256 and columns to 256
+// with zeros: an output tile of 256 x 256 always exists.
+constexpr int kBlkRows = 128;
+constexpr int kBlkCols = 64;
+constexpr int64_t kBlkBytes = int64_t(kBlkRows) * kBlkCols * 2;
+constexpr int kOrthoTile = 256;
+
+struct MatDesc {
+    int64_t off;          // first element in the flat buffer
+    int32_t rows, cols;   // as stored by the user
+    int32_t m, n;         // shorter and longer side: X is m x n
+    int32_t tall;         // rows > cols: X is the transpose of the stored matrix
+    int32_t kn, km;       // 64-deep blocks of a sum over n, over m
+    int32_t cbx, cba;     // 64-column blocks in a row of X, of A
+    int64_t x[2], lo;     // first block of the two X buffers and of X's low part
+    int64_t a, b;         // first block of A and of bA + cA^2 (off-diagonal parts)
+    int64_t diag;         // first entry of the per-row vectors (see OrthoArgs)
+    int64_t rowsq;        // first entry of X's row sums of squares, [cbx][padded rows]
+    int32_t rows_pad;     // rows of X padded to 256
+    int32_t norm0, norm1; // its items in the norm table
+};
+
+// One 256 x 256 output tile of one product of one matrix.
+struct OrthoTile {
+    int32_t mat;
+    int16_t i, j;
+};
+
+// Items of the norm and conversion passes and of the weight update.
+struct NormItem {
+    int32_t mat, count;   // elements [start, start + count) of the matrix
+    int64_t start;
+};
+struct ConvItem {
+    int32_t mat, i, j, pad;   // block (i, j) of X
+};
+struct ApplyItem {
+    int64_t off;          // flat offset, a multiple of 8
+    int32_t count;        // <= kApplyChunk elements of one parameter
+    int32_t param;
+};
+constexpr int kNormChunk = 16384;
+constexpr int kApplyChunk = 1024;
+
+// Products of a step, in order: A = X X^T, B = bA + cA^2, X' = aX + BX.
+enum : int { kProdA = 0, kProdB = 1, kProdX = 2 };
+
+// Constants of one Newton-Schulz step.  Stored fp16 values are the true ones
+// times a power of two that keeps the largest the step can produce below 2^15.
+struct OrthoStep {
+    float a, b, c;
+    float inv_sx;      // 1 / scale of X (step 0: the matrix's own, on the device)
+    float sx_next;     // scale of the new X
+    float sa, inv_sa;  // scale of A
+    float sb, inv_sb;  // scale of bA + cA^2
+};
+
+struct Matrices {
+    int64_t total_padded = 0;
+    int32_t n_params = 0;
+    std::vector<int64_t> param_offset, numels;
+    std::vector<MatDesc> mats;
+    std::vector<OrthoTile> tiles[3];
+    std::vector<NormItem> norm_items;
+    std::vector<ConvItem> conv_items;
+    std::vector<ApplyItem> apply_items;
+    std::vector<double> scales;        // 2 per parameter: spectral, rms
+    int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0;
+    int64_t workspace_bytes = 0;
+    // byte offsets in the workspace
+    int64_t o_diag = 0, o_rowsq = 0, o_part = 0, o_scal = 0, o_count = 0, o_status = 0;
+
+    std::mutex mu;
+    int device = -1;
+    unsigned char* ws = nullptr;       // workspace_bytes
+    unsigned char* d_tables = nullptr; // one allocation, sections below
+    MatDesc* d_mats = nullptr;
+    OrthoTile* d_tiles[3] = {nullptr, nullptr, nullptr};
+    NormItem* d_norm_items = nullptr;
+    ConvItem* d_conv_items = nullptr;
+    ApplyItem* d_apply_items = nullptr;
+    double* d_scales = nullptr;
+};
+
+// device side (dpg_ortho.cu)
+int upload_matrices(Matrices& m);
+void release_matrices(Matrices& m);
+// validates hp for the orthogonalisation and fills steps[0 .. hp->n_steps)
+int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who);
+int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
+                 void* out, void* stream, const char* who);
+
+}  // namespace dpg
+
+struct dpg_matrices {
+    dpg::Matrices m;
+};
