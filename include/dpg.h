@@ -507,6 +507,11 @@ int dpg_plan_matrices(const dpg_plan_t* plan, const int64_t* rows, const int64_t
 void dpg_matrices_destroy(dpg_matrices_t* mats);
 int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* workspace_bytes);
 int dpg_matrices_upload(dpg_matrices_t* mats);
+/* Every device-side wait of the orthogonalisation is bounded (2 s).  One that
+ * runs out ends the call's kernels with incomplete results and records
+ * DPG_ERR_DEVICE_TIMEOUT; this synchronises `stream` and returns the record
+ * (DPG_OK if there is none), clearing it. */
+int dpg_matrices_status(dpg_matrices_t* mats, void* stream);
 
 /* Momentum of the reduced gradient, buckets [b0, b1), in one pass (binary32,
  * no FMA; s and g as in dpg_reduce_scatter_adam):

@@ -49,7 +49,7 @@ EXPORTED = (
     "dpg_set_programmatic_launch", "dpg_reduce_scatter_adam_when_ready", "dpg_step_deferred",
     "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit",
     "dpg_plan_matrices", "dpg_matrices_destroy", "dpg_matrices_info", "dpg_matrices_upload",
-    "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply", "dpg_muon_step",
+    "dpg_matrices_status", "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply", "dpg_muon_step",
 )
 DPG_MAX_STATE_ARRAYS = 8
 DPG_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -176,6 +176,7 @@ def lib() -> ctypes.CDLL:
         L.dpg_matrices_destroy.restype = None
         L.dpg_matrices_info.argtypes = [P, P, P]
         L.dpg_matrices_upload.argtypes = [P]
+        L.dpg_matrices_status.argtypes = [P, P]
         L.dpg_muon_momentum.argtypes = [P, P, i32, P, P, i32, P, P, P, i32, i32, i32, P]
         L.dpg_orthogonalize.argtypes = [P, P, i32, P, P, P]
         L.dpg_muon_apply.argtypes = [P, P, P, P, P, i32, P]
@@ -192,7 +193,7 @@ def lib() -> ctypes.CDLL:
                      "dpg_reduce_scatter_adam_when_ready", "dpg_step_deferred",
                      "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit",
                      "dpg_plan_matrices", "dpg_matrices_info", "dpg_matrices_upload",
-                     "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply",
+                     "dpg_matrices_status", "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply",
                      "dpg_muon_step"):
             getattr(L, name).restype = c_int
         _lib = L
@@ -784,6 +785,11 @@ def dpg_plan_matrices(plan: Plan, rows: Sequence[int], cols: Sequence[int]) -> M
 
 def dpg_matrices_upload(mats: Matrices):
     _check(lib().dpg_matrices_upload(mats.handle))
+
+
+def dpg_matrices_status(mats: Matrices, stream=None):
+    """Synchronise the stream; raise DpgError if an orthogonalisation timed out."""
+    _check(lib().dpg_matrices_status(mats.handle, _stream(stream)))
 
 
 def _flat_dtype(t, dtype, numel: int, what: str) -> int:

@@ -228,6 +228,12 @@ int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* 
     return DPG_OK;
 }
 
+int dpg_matrices_status(dpg_matrices_t* mats, void* stream) {
+    dpg::clear_error();
+    if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_matrices_status: mats is NULL");
+    return dpg::check_matrices(mats->m, stream);
+}
+
 int dpg_matrices_upload(dpg_matrices_t* mats) {
     dpg::clear_error();
     if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_matrices_upload: mats is NULL");

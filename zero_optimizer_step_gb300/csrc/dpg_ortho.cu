@@ -38,11 +38,13 @@
 // Together 3e-4 to 1.3e-3 of relative Frobenius error over Gaussian, spiked,
 // constant and low-rank matrices, below the rounding of the bf16 result itself
 // (1.7e-3).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "dpg_host.h"
 #include "dpg_ortho.h"
@@ -62,6 +64,7 @@ struct OrthoArgs {
     double* part;            // norm partials, one per norm item
     float2* scal;            // per matrix: {power-of-two scale of X_0, 1 / (norm * scale)}
     int32_t* count;          // per matrix: norm items done (zero between launches)
+    int32_t* status;         // 0, or the error of the first wait that ran out
     const void* update;
     int32_t f32;             // update holds fp32 (else bf16)
     int32_t step, n_steps;
@@ -294,10 +297,11 @@ __device__ __forceinline__ float row_square(const OrthoArgs& a, const MatDesc& d
     return s;
 }
 
-// Returns the new X's sum of squares over the 32 columns (kProdX).
+// diag: the row's sum of squares of X, where the columns hold the diagonal of
+// A.  Returns the new X's sum of squares over the 32 columns (kProdX).
 template <int PROD>
 __device__ __forceinline__ float finish32(const OrthoArgs& a, const MatDesc& d, int mat, int r, int c0,
-                                         float* acc, bool mirror) {
+                                          float* acc, bool mirror, float diag) {
     const OrthoStep& s = a.st;
     const float inv_sx = a.step == 0 ? a.scal[mat].y : s.inv_sx;
     if constexpr (PROD == kProdA) {
@@ -306,7 +310,7 @@ __device__ __forceinline__ float finish32(const OrthoArgs& a, const MatDesc& d, 
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float v = acc[j] * k;
-            if (c0 + j == r) a.diag_a[d.diag + r] = row_square(a, d, r) * k;
+            if (c0 + j == r) a.diag_a[d.diag + r] = diag * k;
             acc[j] = c0 + j == r ? 0.0f : v * rs.v[j & 3];
         }
         store_sym(a, d, d.a, r, c0, acc, mirror);
@@ -395,54 +399,292 @@ __device__ __forceinline__ float finish32(const OrthoArgs& a, const MatDesc& d, 
 }
 
 // ---------------------------------------------------------------------------
-// One product of one step, plain form: a CTA per 256 x 256 tile, a thread per
-// row, 32 columns at a time.
+// Tensor-core products.  A pair of CTAs on two SMs (a cluster of 2) computes a
+// 256 x 256 tile: CTA r holds rows 128 r .. of the left operand and columns
+// 128 r .. of the right one, 32 KB per 64-deep stage and SM, and the pair's
+// tcgen05.mma (cta_group::2) reads both halves.  A 128 x 256 tile on one SM
+// would need 48 KB per stage for the same arithmetic, more than L2 delivers.
+// Persistent: every pair takes tiles cluster, cluster + clusters, ...
+// Roles per CTA: warp 0 copies (TMA, kStages ahead), warp 1 of CTA 0 issues
+// the products into one of two 256-column accumulators, warps 2..9 finish the
+// other accumulator meanwhile (warp w reads tensor-memory lanes 32 (w mod 4)).
 // ---------------------------------------------------------------------------
-template <int PROD>
-__global__ void __launch_bounds__(256) k_ortho_product(const __grid_constant__ OrthoArgs a,
-                                                      const OrthoTile* tiles) {
-    __shared__ float sb[kBlkCols][33];
+constexpr int kStages = 6;
+constexpr int kHalfBytes = 128 * 64 * 2;              // one operand of one stage in one CTA
+constexpr int kStageBytes = 2 * kHalfBytes;
+constexpr int kEpiWarps = 8;
+constexpr int kOrthoThreads = 32 * (2 + kEpiWarps);
+constexpr int kOrthoSmem = kStages * kStageBytes + 1024;   // + alignment to 1 KB
+constexpr uint64_t kWaitNs = 2000000000ull;           // bound of every wait
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t global_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// the address of `addr` (this CTA's shared memory) in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n"
+                 " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+// What the roles of a CTA share.
+struct OrthoShared {
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+    uint32_t tmem;
+    volatile int abort;     // some wait of this CTA ran out
+};
+
+// true once the phase of `parity` completed; false when the bound ran out or
+// another role gave up (recorded in *status, the tiles after it are skipped)
+__device__ __forceinline__ bool wait_bounded(OrthoShared& sh, uint64_t* bar, uint32_t parity, int32_t* status) {
+    const uint32_t at = smem_u32(bar);
+    if (try_wait(at, parity)) return true;
+    const uint64_t until = global_ns() + kWaitNs;
+    while (!try_wait(at, parity)) {
+        if (sh.abort) return false;
+        if (global_ns() > until) {
+            sh.abort = 1;
+            atomicCAS(status, 0, DPG_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
+}
+
+// Shared-memory descriptors of the 128-byte swizzle: rows of 64 K-values (8
+// rows every 1024 bytes), or 64-column groups (8 K-rows every 1024 bytes, the
+// next 64 columns 8192 bytes on).
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool by_column) {
+    return uint64_t(addr >> 4) | (uint64_t(by_column ? 8192 >> 4 : 1) << 16) |
+           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// fp16 operands, fp32 sums, 256 x 256; right operand by rows or by columns
+__device__ __forceinline__ uint32_t mma_shape(bool by_column) {
+    return (1u << 4) | (by_column ? 1u << 16 : 0u) | (uint32_t(kOrthoTile >> 3) << 17) |
+           (uint32_t(kOrthoTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u) : "memory");
+}
+// arrives at `bar` of both CTAs once every product issued so far is done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+}
+__device__ __forceinline__ void load_acc32(uint32_t tmem, float* v) {
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+                 " tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                   "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+                   "=r"(r[31])
+                 : "r"(tmem) : "memory");
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+// Where the operands of a tile start, in blocks.
+struct TileOperands {
+    int64_t left, right;    // first block of the left operand's rows; of the right operand
+    int right_step;         // kProdX: blocks in a row of X
+    int kblocks;
+};
+__device__ __forceinline__ TileOperands operands_of(const MatDesc& d, int prod, int step, const OrthoTile& t,
+                                                    int rank) {
+    TileOperands o;
+    const int64_t x = d.x[step & 1];
+    const int64_t from = prod == kProdA ? x : prod == kProdB ? d.a : d.b;
+    const int cb = prod == kProdA ? d.cbx : d.cba;
+    o.kblocks = prod == kProdA ? d.kn : d.km;
+    o.left = from + int64_t(t.i * 2 + rank) * cb;
+    o.right = prod == kProdX ? x + t.j * 4 + rank * 2 : from + int64_t(t.j * 2 + rank) * cb;
+    o.right_step = d.cbx;
+    return o;
+}
+
+__global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
+k_ortho_product(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
+                const __grid_constant__ CUtensorMap rows64, const OrthoTile* tiles, int n_tiles,
+                int prod) {
+    extern __shared__ unsigned char dyn[];
+    __shared__ OrthoShared sh;
+    const uint32_t stage0 = (smem_u32(dyn) + 1023u) & ~1023u;
+    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const uint32_t rank = cluster_rank();
+    const int pairs = int(gridDim.x >> 1), pair = int(blockIdx.x >> 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(smem_u32(&sh.full[s])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(smem_u32(&sh.empty[s])) : "memory");
+        }
+        for (int b = 0; b < 2; ++b) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(smem_u32(&sh.tfull[b])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;"
+                         :: "r"(smem_u32(&sh.tempty[b])), "r"(2 * kEpiWarps) : "memory");
+        }
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     pdl_enter();
-    const OrthoTile t = tiles[blockIdx.x];
-    const MatDesc& d = a.mats[t.mat];
-    const int r = t.i * kOrthoTile + int(threadIdx.x);
-    const int64_t x = d.x[a.step & 1];
-    const int64_t pa = PROD == kProdA ? x : PROD == kProdB ? d.a : d.b;
-    const int ca = PROD == kProdA ? d.cbx : d.cba;
-    const int kblocks = PROD == kProdA ? d.kn : d.km;
-    float sq = 0.0f;
-    for (int g = 0; g < kOrthoTile / 32; ++g) {
-        const int c0 = t.j * kOrthoTile + g * 32;
-        float acc[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[j] = 0.0f;
-        for (int kb = 0; kb < kblocks; ++kb) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < kBlkCols * 32; e += 256) {
-                const int k = PROD == kProdX ? e >> 5 : e & 63, c = PROD == kProdX ? e & 31 : e >> 6;
-                const int64_t at = PROD == kProdX ? blk_at(x, d.cbx, kb * 64 + k, c0 + c)
-                                                  : blk_at(pa, ca, c0 + c, kb * 64 + k);
-                sb[k][c] = __half2float(*reinterpret_cast<const __half*>(a.ws + at));
-            }
-            __syncthreads();
-            for (int k8 = 0; k8 < 8; ++k8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(a.ws + blk_at(pa, ca, r, kb * 64 + k8 * 8));
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 p = unpack_half2(u[k >> 1]);
-                    const float f = (k & 1) ? p.y : p.x;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = fmaf(f, sb[k8 * 8 + k][j], acc[j]);
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 0 && lane == 0) {
+        // ---- copies ----
+        int s = 0;
+        uint32_t par = 1;             // the first pass over the ring finds it empty
+        bool ok = true;
+        for (int t = pair; t < n_tiles && ok; t += pairs) {
+            const OrthoTile tile = tiles[t];
+            const MatDesc& d = a.mats[tile.mat];
+            const TileOperands o = operands_of(d, prod, a.step, tile, int(rank));
+            for (int kb = 0; kb < o.kblocks; ++kb) {
+                if (!(ok = wait_bounded(sh, &sh.empty[s], par, a.status))) break;
+                const uint32_t bar = map_to(smem_u32(&sh.full[s]), 0);
+                if (rank == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                                 :: "r"(smem_u32(&sh.full[s])), "r"(2 * kStageBytes) : "memory");
+                const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
+                copy_box(dst, &rows128, int((o.left + kb) * kBlkRows), bar);
+                if (prod == kProdX) {
+                    const int64_t blk = o.right + int64_t(kb >> 1) * o.right_step;
+                    const int row = int(blk * kBlkRows) + (kb & 1) * 64;
+                    copy_box(dst + kHalfBytes, &rows64, row, bar);
+                    copy_box(dst + kHalfBytes + 8192, &rows64, row + kBlkRows, bar);
+                } else {
+                    copy_box(dst + kHalfBytes, &rows128, int((o.right + kb) * kBlkRows), bar);
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    par ^= 1;
                 }
             }
         }
-        const float s = finish32<PROD>(a, d, t.mat, r, c0, acc, PROD != kProdX && t.j > t.i);
-        if (PROD == kProdX) {
-            sq = (g & 1) ? sq + s : s;
-            if (g & 1) a.rowsq[d.rowsq + int64_t(c0 >> 6) * d.rows_pad + r] = sq;
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- products ----
+        const bool by_column = prod == kProdX;
+        const uint32_t shape = mma_shape(by_column);
+        int s = 0, it = 0;
+        uint32_t par = 0;
+        bool ok = true;
+        for (int t = pair; t < n_tiles && ok; t += pairs, ++it) {
+            const MatDesc& d = a.mats[tiles[t].mat];
+            const int kblocks = prod == kProdA ? d.kn : d.km;
+            const int buf = it & 1;
+            if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a.status))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!(ok = wait_bounded(sh, &sh.full[s], par, a.status))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t at = stage0 + uint32_t(s) * kStageBytes;
+                const uint64_t left = desc_of(at, false), right = desc_of(at + kHalfBytes, by_column);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // 16 deep each
+                    mma_pair(tmem + uint32_t(buf) * kOrthoTile, left + 2 * k,
+                             right + (by_column ? 128 : 2) * k, shape, (kb | k) != 0);
+                commit_pair(&sh.empty[s]);
+                if (++s == kStages) {
+                    s = 0;
+                    par ^= 1;
+                }
+            }
+            if (ok) commit_pair(&sh.tfull[buf]);
+        }
+    } else if (warp >= 2) {
+        // ---- epilogue ----
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        int it = 0;
+        for (int t = pair; t < n_tiles; t += pairs, ++it) {
+            const OrthoTile tile = tiles[t];
+            const MatDesc& d = a.mats[tile.mat];
+            const int buf = it & 1;
+            const int r = tile.i * kOrthoTile + int(rank) * 128 + quad * 32 + lane;
+            const bool mirror = prod != kProdX && tile.j > tile.i;
+            float diag = 0.0f;
+            if (prod == kProdA && tile.i == tile.j && half == int(rank)) diag = row_square(a, d, r);
+            const bool ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            float sq = 0.0f;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                const int col = half * 128 + g * 32;
+                float acc[32];
+                load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(quad * 32) << 16), acc);
+                if (g == 3) {         // the accumulator is free for the tile after next
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                                     :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
+                }
+                const int c0 = tile.j * kOrthoTile + col;
+                if (prod == kProdA) {
+                    finish32<kProdA>(a, d, tile.mat, r, c0, acc, mirror, diag);
+                } else if (prod == kProdB) {
+                    finish32<kProdB>(a, d, tile.mat, r, c0, acc, mirror, diag);
+                } else {
+                    sq += finish32<kProdX>(a, d, tile.mat, r, c0, acc, mirror, diag);
+                    if (g & 1) {
+                        a.rowsq[d.rowsq + int64_t(c0 >> 6) * d.rows_pad + r] = sq;
+                        sq = 0.0f;
+                    }
+                }
+            }
         }
     }
+    __syncwarp();
+    if (sh.abort) {   // the copies this CTA has in flight land within this time
+        const uint64_t until = global_ns() + 2000000ull;
+        while (global_ns() < until) {}
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -454,6 +696,28 @@ static cudaError_t put(unsigned char* base, size_t* at, const std::vector<T>& v,
     const size_t bytes = v.size() * sizeof(T);
     *at += round256(bytes);
     return bytes ? cudaMemcpy(*out, v.data(), bytes, cudaMemcpyHostToDevice) : cudaSuccess;
+}
+
+// The workspace as rows of 64 fp16 values, copied `box_rows` rows at a time
+// with no re-arrangement: the blocks are stored as shared memory wants them.
+static int encode_map(CUtensorMap* map, void* base, int64_t rows, uint32_t box_rows) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                CUtensorMapFloatOOBfill);
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    DPG_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                                  &found));
+    if (found != cudaDriverEntryPointSuccess || !fn)
+        return fail(DPG_ERR_CUDA, "matrices upload: the driver has no tensor maps");
+    const cuuint64_t dims[2] = {kBlkCols, cuuint64_t(rows)}, strides[1] = {kBlkCols * 2};
+    const cuuint32_t box[2] = {kBlkCols, box_rows}, step[2] = {1, 1};
+    const CUresult e = reinterpret_cast<Encode>(fn)(
+        map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, step,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? DPG_OK : fail(DPG_ERR_CUDA, "matrices upload: tensor map error %d", int(e));
 }
 
 int upload_matrices(Matrices& m) {
@@ -496,9 +760,54 @@ int upload_matrices(Matrices& m) {
         return fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA,
                     "matrices upload: %s", cudaGetErrorString(e));
     }
+    int clusters = 0;
+    if (m.n_blocks > 0) {
+        static_assert(sizeof(CUtensorMap) == sizeof(m.maps[0]), "room for a tensor map");
+        CUtensorMap map;
+        for (int k = 0; k < 2; ++k) {
+            const int st = encode_map(&map, ws, m.n_blocks * kBlkRows, k ? 64 : 128);
+            if (st != DPG_OK) {
+                cudaFree(tables);
+                cudaFree(ws);
+                return st;
+            }
+            std::memcpy(m.maps[k], &map, sizeof map);
+        }
+        e = cudaFuncSetAttribute(k_ortho_product, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kOrthoThreads);
+        cfg.dynamicSmemBytes = kOrthoSmem;
+        cudaLaunchAttribute pair[1];
+        pair[0].id = cudaLaunchAttributeClusterDimension;
+        pair[0].val.clusterDim.x = 2;
+        pair[0].val.clusterDim.y = pair[0].val.clusterDim.z = 1;
+        cfg.attrs = pair;
+        cfg.numAttrs = 1;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, k_ortho_product, &cfg);
+        if (e != cudaSuccess || clusters < 1) {
+            cudaFree(tables);
+            cudaFree(ws);
+            cudaGetLastError();
+            return fail(DPG_ERR_CUDA, "matrices upload: %s", cudaGetErrorString(e));
+        }
+    }
+    m.clusters = clusters;
     m.d_tables = t;
     m.ws = static_cast<unsigned char*>(ws);
     m.device = dev;
+    return DPG_OK;
+}
+
+int check_matrices(Matrices& m, void* stream) {
+    if (m.device < 0) return DPG_OK;   // nothing has run
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int32_t word = 0;
+    DPG_CUDA_TRY(cudaMemcpyAsync(&word, m.ws + m.o_status, sizeof word, cudaMemcpyDeviceToHost, s));
+    DPG_CUDA_TRY(cudaMemsetAsync(m.ws + m.o_status, 0, sizeof word, s));
+    DPG_CUDA_TRY(cudaStreamSynchronize(s));
+    if (word != 0)
+        return fail(word, "orthogonalisation: a wait on the device ran out; its results are incomplete");
     return DPG_OK;
 }
 
@@ -516,6 +825,29 @@ void release_matrices(Matrices& m) {
     m.device = -1;
 }
 
+static int launch_product(const Matrices& m, const OrthoArgs& a, int prod, cudaStream_t s, const char* who) {
+    CUtensorMap map[2];
+    std::memcpy(map, m.maps, sizeof map);
+    const int n = int(m.tiles[prod].size());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * (n < m.clusters ? n : m.clusters)));
+    cfg.blockDim = dim3(kOrthoThreads);
+    cfg.dynamicSmemBytes = kOrthoSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = t_programmatic ? 1 : 0;
+    const OrthoTile* tiles = m.d_tiles[prod];
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_product, a, map[0], map[1], tiles, n, prod);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    }
+    return after_launch(who);
+}
+
 int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
                  void* out, void* stream, const char* who) {
     OrthoStep steps[DPG_MAX_NS_STEPS];
@@ -531,6 +863,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.part = reinterpret_cast<double*>(m.ws + m.o_part);
     a.scal = reinterpret_cast<float2*>(m.ws + m.o_scal);
     a.count = reinterpret_cast<int32_t*>(m.ws + m.o_count);
+    a.status = reinterpret_cast<int32_t*>(m.ws + m.o_status);
     a.update = update;
     a.f32 = update_dtype == DPG_F32;
     a.n_steps = hp->n_steps;
@@ -545,12 +878,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     for (int k = 0; k < hp->n_steps && st == DPG_OK; ++k) {
         a.step = k;
         a.st = steps[k];
-        const OrthoTile* const* t = m.d_tiles;
-        st = launch_k(k_ortho_product<kProdA>, unsigned(m.tiles[0].size()), 256, s, who, a, t[0]);
-        if (st == DPG_OK)
-            st = launch_k(k_ortho_product<kProdB>, unsigned(m.tiles[1].size()), 256, s, who, a, t[1]);
-        if (st == DPG_OK)
-            st = launch_k(k_ortho_product<kProdX>, unsigned(m.tiles[2].size()), 256, s, who, a, t[2]);
+        for (int prod = 0; prod < 3 && st == DPG_OK; ++prod) st = launch_product(m, a, prod, s, who);
     }
     return st;
 }

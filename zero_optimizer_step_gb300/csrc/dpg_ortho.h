@@ -100,11 +100,14 @@ struct Matrices {
     ConvItem* d_conv_items = nullptr;
     ApplyItem* d_apply_items = nullptr;
     double* d_scales = nullptr;
+    alignas(64) unsigned char maps[2][128];   // tensor maps of the workspace: 128 and 64 rows a copy
+    int clusters = 0;                         // CTA pairs resident at once
 };
 
 // device side (dpg_ortho.cu)
 int upload_matrices(Matrices& m);
 void release_matrices(Matrices& m);
+int check_matrices(Matrices& m, void* stream);
 // validates hp for the orthogonalisation and fills steps[0 .. hp->n_steps)
 int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who);
 int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
