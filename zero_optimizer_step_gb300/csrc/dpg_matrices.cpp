@@ -3,7 +3,10 @@
 #include <algorithm>
 #include <cmath>
 #include <exception>
+#include <functional>
 #include <new>
+#include <queue>
+#include <utility>
 
 #include "dpg_ortho.h"
 
@@ -56,32 +59,21 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.rows_pad = int32_t(tm * kOrthoTile);
             M.n_diag += d.rows_pad;
             d.rowsq = M.n_rowsq;
-            M.n_rowsq += int64_t(d.rows_pad) * d.cbx;
+            M.n_rowsq += int64_t(d.rows_pad) * (d.cbx / 2);
+            if (tm * tn > 0x3FFFFFF) return false;   // counts of a call stay in 32 bits
+            d.tiles_sym = int32_t(tm * (tm + 1) / 2);
+            d.tiles_x = int32_t(tm * tn);
             const int32_t mat = int32_t(M.mats.size());
             d.norm0 = int32_t(M.norm_items.size());
             for (int64_t s = 0; s < one; s += kNormChunk)
                 M.norm_items.push_back({mat, int32_t(std::min<int64_t>(kNormChunk, one - s)), s});
             d.norm1 = int32_t(M.norm_items.size());
             for (int64_t i = 0; i < rb; ++i)
-                for (int64_t j = 0; j < d.cbx; ++j)
+                for (int64_t j = 0; j < d.cbx / 2; ++j)
                     M.conv_items.push_back({mat, int32_t(i), int32_t(j), 0});
-            for (int64_t i = 0; i < tm; ++i) {
-                for (int64_t j = i; j < tm; ++j) {   // A and A^2 are symmetric
-                    M.tiles[kProdA].push_back({mat, int16_t(i), int16_t(j)});
-                    M.tiles[kProdB].push_back({mat, int16_t(i), int16_t(j)});
-                }
-                for (int64_t j = 0; j < tn; ++j) M.tiles[kProdX].push_back({mat, int16_t(i), int16_t(j)});
-            }
             M.mats.push_back(d);
         }
     }
-    // the tiles with the longest sums first, so that a launch ends on short ones
-    for (int k = 0; k < 3; ++k)
-        std::stable_sort(M.tiles[k].begin(), M.tiles[k].end(),
-                         [&](const OrthoTile& x, const OrthoTile& y) {
-                             const MatDesc &u = M.mats[size_t(x.mat)], &v = M.mats[size_t(y.mat)];
-                             return k == kProdA ? u.kn > v.kn : u.km > v.km;
-                         });
     int64_t o = M.n_blocks * kBlkBytes;
     M.o_diag = o;   // three vectors: diagonals of A, of B, and the part of B's that X's low half sees
     o += up256(3 * M.n_diag * int64_t(sizeof(float)));
@@ -93,11 +85,72 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
     o += up256(int64_t(M.mats.size()) * 2 * int64_t(sizeof(float)));
     M.o_count = o;  // per matrix: arrivals of its norm items
     o += up256(int64_t(M.mats.size()) * int64_t(sizeof(int32_t)));
+    M.o_done = o;   // per matrix and product: tiles finished in this call
+    o += up256(int64_t(M.mats.size()) * 3 * int64_t(sizeof(int32_t)));
     M.o_status = o;
     o += 256;
     M.workspace_bytes = o;
     return M.norm_items.size() < 0x7FFFFFFF && M.conv_items.size() < 0x7FFFFFFF &&
            M.apply_items.size() < 0x7FFFFFFF;
+}
+
+// The tiles of one step -- A tiles, B tiles, X tiles of all matrices, larger
+// matrices first -- dealt out to the pairs in this order, each to the pair that
+// could start it first.  The model behind "first": a tile takes 0.3 us per 64
+// of its sum (the tensor cores' rate) and at least 2.5 us (its finish), and
+// starts after its matrix's tiles of the product before.  It only balances the
+// queues; the kernel waits for what has really happened.
+void lay_queue(Matrices& M, int clusters) {
+    constexpr int kShare = 3;
+    std::vector<int32_t> order(M.mats.size());
+    for (size_t k = 0; k < order.size(); ++k) order[k] = int32_t(k);
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
+        const MatDesc &u = M.mats[size_t(x)], &v = M.mats[size_t(y)];
+        return u.m != v.m ? u.m > v.m : u.n > v.n;
+    });
+    std::vector<OrthoTile> all;
+    size_t most = 0;
+    for (int prod = 0; prod < 3; ++prod) {
+        const size_t before = all.size();
+        for (int32_t k : order) {
+            const MatDesc& d = M.mats[size_t(k)];
+            const int tm = d.cba / 4, tn = d.cbx / 4;
+            const int rows = tm, cols = prod == kProdX ? tn : tm;
+            for (int ib = 0; ib < rows; ib += kShare)
+                for (int jb = 0; jb < cols; jb += kShare)
+                    for (int j = jb; j < cols && j < jb + kShare; ++j)
+                        for (int i = ib; i < rows && i < ib + kShare; ++i)
+                            if (prod == kProdX || j >= i) all.push_back({k, int16_t(i), int16_t(j), prod});
+        }
+        most = std::max(most, all.size() - before);
+    }
+    M.pairs = int32_t(std::min<size_t>(size_t(clusters), std::max<size_t>(most, 1)));
+    std::vector<std::vector<OrthoTile>> mine(size_t(M.pairs));
+    std::vector<int64_t> ready(M.mats.size() * 4, 0);   // when the tiles of a product can start
+    constexpr int kGroups = 8;
+    std::vector<int32_t> turn;
+    for (int32_t g = 0; g < kGroups; ++g)
+        for (int32_t p = g; p < M.pairs; p += kGroups) turn.push_back(p);
+    using Free = std::pair<int64_t, int32_t>;
+    std::priority_queue<Free, std::vector<Free>, std::greater<Free>> idle;   // {time, pair}
+    for (int32_t p = 0; p < M.pairs; ++p) idle.push({0, p});
+    for (const OrthoTile& t : all) {
+        const MatDesc& d = M.mats[size_t(t.mat)];
+        const Free f = idle.top();
+        idle.pop();
+        const int64_t start = std::max(f.first, ready[size_t(t.mat) * 4 + size_t(t.prod)]);
+        const int64_t end = start + std::max<int64_t>(3 * (t.prod == kProdA ? d.kn : d.km), 25) + 2;
+        int64_t& next = ready[size_t(t.mat) * 4 + size_t(t.prod) + 1];
+        next = std::max(next, end);
+        mine[size_t(turn[size_t(f.second)])].push_back(t);
+        idle.push({end, f.second});
+    }
+    M.queue.clear();
+    M.queue_first.assign(1, 0);
+    for (const auto& q : mine) {
+        M.queue.insert(M.queue.end(), q.begin(), q.end());
+        M.queue_first.push_back(int32_t(M.queue.size()));
+    }
 }
 
 // Largest |a s + b s^3 + c s^5| for s in [0, hi]: at an end or where the

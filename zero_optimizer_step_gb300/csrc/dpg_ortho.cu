@@ -45,6 +45,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <exception>
 
 #include "dpg_host.h"
 #include "dpg_ortho.h"
@@ -60,43 +61,38 @@ struct OrthoArgs {
     float* diag_a;           // per row: A_rr
     float* diag_b;           // B_rr
     float* diag_t;           // t_r B_rr
-    float* rowsq;            // per 64 columns of X and row: sum of squares (scaled as hi)
+    float* rowsq;            // per 128 columns of X and row: sum of squares (scaled as hi)
     double* part;            // norm partials, one per norm item
     float2* scal;            // per matrix: {power-of-two scale of X_0, 1 / (norm * scale)}
     int32_t* count;          // per matrix: norm items done (zero between launches)
     int32_t* status;         // 0, or the error of the first wait that ran out
+    int32_t* done;           // per matrix and product: CTA tiles finished in this call
+    const OrthoTile* queue;  // tiles of a step, pair p's at [queue_first[p], queue_first[p + 1])
+    const int32_t* queue_first;
     const void* update;
     int32_t f32;             // update holds fp32 (else bf16)
-    int32_t step, n_steps;
+    int32_t n_steps;
     double eps;
-    OrthoStep st;
     uint16_t* out;           // flat bf16
+    OrthoStep st[DPG_MAX_NS_STEPS];
 };
 
+template <bool F32>
 __device__ __forceinline__ float load_update(const OrthoArgs& a, int64_t i) {
-    if (a.f32) return __ldg(static_cast<const float*>(a.update) + i);
+    if (F32) return __ldg(static_cast<const float*>(a.update) + i);
     return __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + i)) << 16);
 }
 
-// eight consecutive elements from i; vec: i is a multiple of 8
-__device__ __forceinline__ void load_update8(const OrthoArgs& a, int64_t i, bool vec, float* x) {
-    if (vec && !a.f32) {
-        widen8(ld_grad_u4(static_cast<const uint16_t*>(a.update) + i), x);
-    } else if (vec) {
+// eight consecutive elements from i, a multiple of 8
+template <bool F32>
+__device__ __forceinline__ void load_update8(const OrthoArgs& a, int64_t i, float* x) {
+    if (F32) {
         const F8 v = ld_grad_f8(static_cast<const float*>(a.update) + i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = v.v[j];
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = load_update(a, i + j);
+        widen8(ld_grad_u4(static_cast<const uint16_t*>(a.update) + i), x);
     }
-}
-
-// byte offset of (row, col) in a blocked matrix of `cb` column blocks per row
-// of blocks that starts at block `base`
-__device__ __forceinline__ int64_t blk_at(int64_t base, int cb, int row, int col) {
-    return (base + int64_t(row >> 7) * cb + (col >> 6)) * kBlkBytes + (row & 127) * 128 +
-           ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float x, float y) {
@@ -142,6 +138,19 @@ __device__ __forceinline__ double block_sum(double x, double* sh) {
     return t;
 }
 
+// the sum of eight squares
+__device__ __forceinline__ double square8(const float* x) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
+    if (s > 1e-30f && s < 1e30f) return double(s);
+    double t = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += double(x[j]) * double(x[j]);
+    return t;
+}
+
+template <bool F32>
 __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_constant__ OrthoArgs a,
                                                             const NormItem* items) {
     __shared__ double sh[2][kNormThreads / 32];
@@ -150,24 +159,25 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
     const NormItem it = items[blockIdx.x];
     const MatDesc& d = a.mats[it.mat];
     const int64_t base = d.off + it.start;
-    const bool vec = (base & 7) == 0;
+    constexpr int kPer = kNormChunk / (kNormThreads * 8), kFly = F32 ? 4 : 8;   // vectors per thread, in flight
+    static_assert(kPer % kFly == 0, "whole batches");
     double acc = 0.0;
-    for (int e = int(threadIdx.x) * 8; e < it.count; e += kNormThreads * 8) {
-        float x[8];
-        if (e + 8 <= it.count) {
-            load_update8(a, base + e, vec, x);
-        } else {
+    if (it.count == kNormChunk && (base & 7) == 0) {
+#pragma unroll 1
+        for (int k = 0; k < kPer; k += kFly) {
+            float x[kFly][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = e + j < it.count ? load_update(a, base + e + j) : 0.0f;
+            for (int u = 0; u < kFly; ++u)
+                load_update8<F32>(a, base + (int64_t(k + u) * kNormThreads + threadIdx.x) * 8, x[u]);
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) acc += square8(x[u]);
         }
-        float s = 0.0f;
+    } else {
+        for (int e = int(threadIdx.x) * 8; e < it.count; e += kNormThreads * 8) {
+            float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-        if (s > 1e-30f && s < 1e30f) {
-            acc += double(s);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc += double(x[j]) * double(x[j]);
+            for (int j = 0; j < 8; ++j) x[j] = e + j < it.count ? load_update<F32>(a, base + e + j) : 0.0f;
+            acc += square8(x);
         }
     }
     const double tot = block_sum(acc, sh[0]);
@@ -199,222 +209,123 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// U -> X_0 as fp16 blocks (hi and lo), zero in the padding.  One CTA per
-// block.  A tall matrix is transposed on the way: lanes then run along X's
-// rows, which are contiguous in U.
+// U -> X_0 as fp16 blocks (hi and lo), zero in the padding.  One CTA per two
+// neighbouring blocks (128 x 128).  A tall matrix is transposed on the way:
+// lanes then run along X's rows, which are contiguous in U.  Moves 4 bytes per
+// element of a bf16 update (lo, all zero, is left out), 8 of an fp32 one.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ OrthoArgs a,
-                                                   const ConvItem* items) {
-    pdl_enter();
-    const ConvItem it = items[blockIdx.x];
-    const MatDesc& d = a.mats[it.mat];
+template <bool F32, bool TALL>
+__device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d, const ConvItem& it) {
     const float sc = a.scal[it.mat].x;
-    const int64_t blk = int64_t(it.i) * d.cbx + it.j;
+    const int64_t blk = int64_t(it.i) * d.cbx + it.j * 2;
     unsigned char* hi = a.ws + (d.x[0] + blk) * kBlkBytes;
     unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
-    const bool vec = !d.tall && (d.off & 7) == 0 && (d.n & 7) == 0;
-    __shared__ float half_sq[kBlkRows];
-    float sq = 0.0f;
+    const bool vec = !TALL && ((d.off | d.n) & 7) == 0;
+    // by rows: sixteen lanes hold a row's sixteen chunks of 8; tall: a thread
+    // holds eight chunks of one row
+    float x[8][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int q = int(threadIdx.x) + 256 * i;
-        const int row = d.tall ? q & 127 : q >> 3;
-        const int ch = d.tall ? 4 * (int(threadIdx.x) >> 7) + i : q & 7;
-        const int r = it.i * kBlkRows + row, c = it.j * kBlkCols + ch * 8;
-        float x[8];
-        if (r < d.m && c + 8 <= d.n && vec) {
-            load_update8(a, d.off + int64_t(r) * d.n + c, true, x);
+    for (int i = 0; i < 8; ++i) {
+        const int row = TALL ? int(threadIdx.x) & 127 : 16 * i + (int(threadIdx.x) >> 4);
+        const int ch = TALL ? 8 * (int(threadIdx.x) >> 7) + i : int(threadIdx.x) & 15;
+        const int r = it.i * kBlkRows + row, c = it.j * 2 * kBlkCols + ch * 8;
+        if (vec && r < d.m && c < d.n) {
+            load_update8<F32>(a, d.off + int64_t(r) * d.n + c, x[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[j] = r < d.m && c + j < d.n
-                           ? load_update(a, d.off + (d.tall ? int64_t(c + j) * d.m + r
-                                                            : int64_t(r) * d.n + c + j))
-                           : 0.0f;
+                x[i][j] = r < d.m && c + j < d.n
+                              ? load_update<F32>(a, d.off + (TALL ? int64_t(c + j) * d.m + r
+                                                                  : int64_t(r) * d.n + c + j))
+                              : 0.0f;
         }
-        RoundScale rs(1.0f, row);
-        if (!a.f32) rs.v[0] = rs.v[1] = rs.v[2] = rs.v[3] = 1.0f;   // bf16 is exact as it is
+    }
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = TALL ? int(threadIdx.x) & 127 : 16 * i + (int(threadIdx.x) >> 4);
+        const int ch = TALL ? 8 * (int(threadIdx.x) >> 7) + i : int(threadIdx.x) & 15;
+        const int r = it.i * kBlkRows + row, c = it.j * 2 * kBlkCols + ch * 8;
+        const RoundScale rs(1.0f, row);
         uint32_t h[4], l[4];
-        if (!d.tall) sq = 0.0f;
+        if (!TALL) sq = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float u = r < d.m && c + 2 * j < d.n ? x[2 * j] * sc : 0.0f;
-            const float v = r < d.m && c + 2 * j + 1 < d.n ? x[2 * j + 1] * sc : 0.0f;
+            // (sc is a NaN for a matrix that is not finite: padding stays zero)
+            const float u = r < d.m && c + 2 * j < d.n ? x[i][2 * j] * sc : 0.0f;
+            const float v = r < d.m && c + 2 * j + 1 < d.n ? x[i][2 * j + 1] * sc : 0.0f;
             sq = fmaf(u, u, fmaf(v, v, sq));
-            h[j] = pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]);
+            // a scaled bf16 value is an fp16 value: nothing to round, lo is 0
+            h[j] = F32 ? pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]) : pack_half2(u, v);
             const float2 f = unpack_half2(h[j]);
             l[j] = pack_half2((u - f.x) * kLoScale, (v - f.y) * kLoScale);
         }
-        const int at = row * 128 + ((ch ^ (row & 7)) << 4);
+        const int64_t at = (ch >> 3) * kBlkBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
         *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-        if (!d.tall) {   // a row's eight chunks lie in eight lanes
-            sq += __shfl_xor_sync(0xFFFFFFFFu, sq, 1);
-            sq += __shfl_xor_sync(0xFFFFFFFFu, sq, 2);
-            sq += __shfl_xor_sync(0xFFFFFFFFu, sq, 4);
+        if (F32) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        if (!TALL) {
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
             if (ch == 0) a.rowsq[d.rowsq + int64_t(it.j) * d.rows_pad + r] = sq;
         }
     }
-    if (d.tall) {        // and here in two threads
-        if (threadIdx.x >= 128) half_sq[threadIdx.x & 127] = sq;
+    if (TALL) {
+        __shared__ float other[kBlkRows];
+        if (threadIdx.x >= 128) other[threadIdx.x & 127] = sq;
         __syncthreads();
         if (threadIdx.x < 128)
             a.rowsq[d.rowsq + int64_t(it.j) * d.rows_pad + it.i * kBlkRows + int(threadIdx.x)] =
-                sq + half_sq[threadIdx.x];
+                sq + other[threadIdx.x];
     }
 }
 
-// ---------------------------------------------------------------------------
-// What a product does with 32 consecutive sums acc of row r, columns c0 ..
-// c0 + 31 (c0 a multiple of 32).  mirror: the tile lies above the diagonal,
-// its transpose is written too (a warp's lanes are 32 consecutive rows).
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void store_sym(const OrthoArgs& a, const MatDesc& d, int64_t base, int r,
-                                          int c0, const float* v, bool mirror) {
-    uint32_t h[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4*>(a.ws + blk_at(base, d.cba, r, c0 + 8 * q)) =
-            make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-    if (mirror) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            *reinterpret_cast<uint16_t*>(a.ws + blk_at(base, d.cba, c0 + 2 * j, r)) = uint16_t(h[j]);
-            *reinterpret_cast<uint16_t*>(a.ws + blk_at(base, d.cba, c0 + 2 * j + 1, r)) =
-                uint16_t(h[j] >> 16);
-        }
-    }
-}
-
-// A_rr from the row's sums of squares
-__device__ __forceinline__ float row_square(const OrthoArgs& a, const MatDesc& d, int r) {
-    const float* p = a.rowsq + d.rowsq + r;
-    float s = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < d.kn; ++k) s += p[int64_t(k) * d.rows_pad];
-    return s;
-}
-
-// diag: the row's sum of squares of X, where the columns hold the diagonal of
-// A.  Returns the new X's sum of squares over the 32 columns (kProdX).
-template <int PROD>
-__device__ __forceinline__ float finish32(const OrthoArgs& a, const MatDesc& d, int mat, int r, int c0,
-                                          float* acc, bool mirror, float diag) {
-    const OrthoStep& s = a.st;
-    const float inv_sx = a.step == 0 ? a.scal[mat].y : s.inv_sx;
-    if constexpr (PROD == kProdA) {
-        const float k = inv_sx * inv_sx;
-        const RoundScale rs(s.sa, r);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float v = acc[j] * k;
-            if (c0 + j == r) a.diag_a[d.diag + r] = diag * k;
-            acc[j] = c0 + j == r ? 0.0f : v * rs.v[j & 3];
-        }
-        store_sym(a, d, d.a, r, c0, acc, mirror);
-    } else if constexpr (PROD == kProdB) {
-        const float dr = a.diag_a[d.diag + r];
-        const float k = s.c * s.inv_sa * s.inv_sa;
-        const RoundScale rs(s.sb, r);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint4 f4 = *reinterpret_cast<const uint4*>(a.ws + blk_at(d.a, d.cba, r, c0 + 8 * q));
-            const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 p = unpack_half2(f[j >> 1]);
-                const float fv = ((j & 1) ? p.y : p.x) * s.inv_sa;
-                const int c = c0 + 8 * q + j;
-                const float dc = a.diag_a[d.diag + c];
-                const float v = fmaf(k, acc[8 * q + j], fmaf(s.c, dr + dc, s.b) * fv);
-                // fv is 0 on the diagonal: v is c (F F^T)_rr there
-                if (c == r) {
-                    const float db = fmaf(fmaf(s.c, dr, s.b), dr, v), d2 = dr * dr;
-                    const float aa = fmaf(acc[8 * q + j] * s.inv_sa, s.inv_sa, d2);   // (A A^T)_rr
-                    a.diag_b[d.diag + r] = db;
-                    a.diag_t[d.diag + r] = aa > 0.0f ? db * (d2 / aa) : 0.0f;
-                }
-                acc[8 * q + j] = c == r ? 0.0f : v * rs.v[j & 3];
-            }
-        }
-        store_sym(a, d, d.b, r, c0, acc, mirror);
-    } else {
-        const float k = inv_sx * s.inv_sb;
-        const float bx = a.diag_b[d.diag + r] * inv_sx, ax = s.a * inv_sx;
-        const float al = fmaf(a.diag_t[d.diag + r], inv_sx, ax) * kInvLoScale, ah = ax + bx;
-        float sq = 0.0f;
-        const RoundScale rs(s.sx_next, r);
-        const bool last = a.step + 1 == a.n_steps;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = c0 + 8 * q;
-            const int64_t lo_at = blk_at(d.lo, d.cbx, r, c);
-            const uint4 h4 = *reinterpret_cast<const uint4*>(a.ws + blk_at(d.x[a.step & 1], d.cbx, r, c));
-            const uint4 l4 = *reinterpret_cast<const uint4*>(a.ws + lo_at);
-            const uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 u = unpack_half2(h[j]), w = unpack_half2(l[j]);
-                x[2 * j] = fmaf(ah, u.x, fmaf(al, w.x, k * acc[8 * q + 2 * j]));
-                x[2 * j + 1] = fmaf(ah, u.y, fmaf(al, w.y, k * acc[8 * q + 2 * j + 1]));
-            }
-            if (!last) {
-                uint32_t nh[4], nl[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float u = x[2 * j] * s.sx_next, w = x[2 * j + 1] * s.sx_next;
-                    sq = fmaf(u, u, fmaf(w, w, sq));
-                    nh[j] = pack_half2(x[2 * j] * rs.v[2 * j & 3], x[2 * j + 1] * rs.v[(2 * j + 1) & 3]);
-                    const float2 f = unpack_half2(nh[j]);
-                    nl[j] = pack_half2((u - f.x) * kLoScale, (w - f.y) * kLoScale);
-                }
-                *reinterpret_cast<uint4*>(a.ws + blk_at(d.x[(a.step + 1) & 1], d.cbx, r, c)) =
-                    make_uint4(nh[0], nh[1], nh[2], nh[3]);
-                *reinterpret_cast<uint4*>(a.ws + lo_at) = make_uint4(nl[0], nl[1], nl[2], nl[3]);
-            } else if (r < d.m) {
-                if (d.tall) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (c + j < d.n)
-                            a.out[d.off + int64_t(c + j) * d.m + r] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
-                } else {
-                    uint16_t* o = a.out + d.off + int64_t(r) * d.n + c;
-                    if (c + 8 <= d.n && ((d.off | d.n) & 7) == 0) {
-                        *reinterpret_cast<uint4*>(o) = narrow8(x);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (c + j < d.n) o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
-                    }
-                }
-            }
-        }
-        return sq;
-    }
-    return 0.0f;
+template <bool F32>
+__global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ OrthoArgs a, const ConvItem* items) {
+    pdl_enter();
+    const ConvItem it = items[blockIdx.x];
+    const MatDesc& d = a.mats[it.mat];
+    if (it.i == 0 && it.j == 0 && threadIdx.x < 3) a.done[3 * it.mat + int(threadIdx.x)] = 0;
+    if (d.tall)
+        load_blocks<F32, true>(a, d, it);
+    else
+        load_blocks<F32, false>(a, d, it);
 }
 
 // ---------------------------------------------------------------------------
-// Tensor-core products.  A pair of CTAs on two SMs (a cluster of 2) computes a
-// 256 x 256 tile: CTA r holds rows 128 r .. of the left operand and columns
-// 128 r .. of the right one, 32 KB per 64-deep stage and SM, and the pair's
-// tcgen05.mma (cta_group::2) reads both halves.  A 128 x 256 tile on one SM
-// would need 48 KB per stage for the same arithmetic, more than L2 delivers.
-// Persistent: every pair takes tiles cluster, cluster + clusters, ...
-// Roles per CTA: warp 0 copies (TMA, kStages ahead), warp 1 of CTA 0 issues
-// the products into one of two 256-column accumulators, warps 2..9 finish the
-// other accumulator meanwhile (warp w reads tensor-memory lanes 32 (w mod 4)).
+// The steps.  One persistent kernel runs every product of every step.  A pair
+// of CTAs on two SMs (a cluster of 2) computes 256 x 256 tiles: CTA r holds
+// rows 128 r .. of the left operand and columns 128 r .. of the right one, 32
+// KB per 64-deep stage and SM, and the pair's tcgen05.mma (cta_group::2) reads
+// both halves.  A 128 x 256 tile on one SM would need 48 KB per stage for the
+// same arithmetic, more than L2 delivers.
+//
+// Every pair works through a queue of tiles that the host laid out once
+// (balanced by cost), the same in every step: A tiles, B tiles, X tiles of all
+// matrices.  A tile starts when its matrix's tiles of the product before are
+// done (a counter per matrix and product in device memory), so matrices
+// overlap at the ends of their products and a step needs no launch.  Queues
+// follow one global order and all pairs are resident (cooperative launch), so
+// the oldest unfinished tile can always run.
+//
+// Roles per CTA:
+//   warp 0       copies operands (TMA, kStages ahead)
+//   warp 1       of CTA 0: issues the products into one of two accumulators
+//   warps 2..9   finish the other accumulator: 64 columns at a time in a
+//                shared-memory slot (warp w: tensor-memory lanes 32 (w mod 4),
+//                32 of the 64 columns)
+//   warp 10      fills the slots with what the finish needs (hi and lo of X,
+//                or the tile of A) and writes them out, as whole contiguous
+//                blocks; row-wise 16-byte accesses from the finishing warps
+//                themselves took 22 to 29 us per tile, four times the product
 // ---------------------------------------------------------------------------
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kHalfBytes = 128 * 64 * 2;              // one operand of one stage in one CTA
 constexpr int kStageBytes = 2 * kHalfBytes;
+constexpr int kSlots = 2;
+constexpr int kSlotBytes = 2 * int(kBlkBytes);        // hi | lo, or the tile | its transpose
 constexpr int kEpiWarps = 8;
-constexpr int kOrthoThreads = 32 * (2 + kEpiWarps);
-constexpr int kOrthoSmem = kStages * kStageBytes + 1024;   // + alignment to 1 KB
+constexpr int kSlotWarp = 2 + kEpiWarps;
+constexpr int kOrthoThreads = 32 * (kSlotWarp + 1);
 constexpr uint64_t kWaitNs = 2000000000ull;           // bound of every wait
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -439,6 +350,16 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void mbar_init(uint64_t* bar, int arrivals) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(smem_u32(bar)), "r"(arrivals) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                 :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n .reg .pred p;\n"
@@ -447,13 +368,26 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
                  : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done != 0;
 }
+__device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // What the roles of a CTA share.
 struct OrthoShared {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], in_full[kSlots], out_ready[kSlots];
+    float cols[kEpiWarps][32];   // a finishing warp's 32 values of A's diagonal
     uint32_t tmem;
-    volatile int abort;     // some wait of this CTA ran out
+    volatile int abort;     // some wait of this CTA ran out, or of another one
 };
+constexpr int kOrthoSmem = kStages * kStageBytes + kSlots * kSlotBytes + int(sizeof(OrthoShared));
+static_assert(kOrthoSmem <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ void give_up(OrthoShared& sh, int32_t* status) {
+    sh.abort = 1;
+    atomicCAS(status, 0, DPG_ERR_DEVICE_TIMEOUT);
+}
 
 // true once the phase of `parity` completed; false when the bound ran out or
 // another role gave up (recorded in *status, the tiles after it are skipped)
@@ -464,18 +398,44 @@ __device__ __forceinline__ bool wait_bounded(OrthoShared& sh, uint64_t* bar, uin
     while (!try_wait(at, parity)) {
         if (sh.abort) return false;
         if (global_ns() > until) {
-            sh.abort = 1;
-            atomicCAS(status, 0, DPG_ERR_DEVICE_TIMEOUT);
+            give_up(sh, status);
             return false;
         }
     }
     return true;
 }
 
+// The same for a counter in device memory that other CTAs raise to `target`.
+// What they wrote before is visible afterwards, to copies too.
+__device__ __forceinline__ bool wait_count(OrthoShared& sh, const int32_t* count, int32_t target, int32_t* status) {
+    if (target > 0 && load_acquire(count) < target) {
+        const uint64_t until = global_ns() + kWaitNs;
+        while (load_acquire(count) < target) {
+            if (sh.abort) return false;
+            if (load_acquire(status) != 0 || global_ns() > until) {
+                give_up(sh, status);
+                return false;
+            }
+        }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return true;
+}
+
+// rows of 128 bytes from `row` on into this CTA's shared memory; `bar` may be
+// the other CTA's
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_in(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_out(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                 :: "l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
 // Shared-memory descriptors of the 128-byte swizzle: rows of 64 K-values (8
@@ -517,44 +477,226 @@ __device__ __forceinline__ void load_acc32(uint32_t tmem, float* v) {
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
-// Where the operands of a tile start, in blocks.
-struct TileOperands {
-    int64_t left, right;    // first block of the left operand's rows; of the right operand
-    int right_step;         // kProdX: blocks in a row of X
-    int kblocks;
-};
-__device__ __forceinline__ TileOperands operands_of(const MatDesc& d, int prod, int step, const OrthoTile& t,
-                                                    int rank) {
-    TileOperands o;
-    const int64_t x = d.x[step & 1];
-    const int64_t from = prod == kProdA ? x : prod == kProdB ? d.a : d.b;
-    const int cb = prod == kProdA ? d.cbx : d.cba;
-    o.kblocks = prod == kProdA ? d.kn : d.km;
-    o.left = from + int64_t(t.i * 2 + rank) * cb;
-    o.right = prod == kProdX ? x + t.j * 4 + rank * 2 : from + int64_t(t.j * 2 + rank) * cb;
-    o.right_step = d.cbx;
-    return o;
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t x) {
+    asm volatile("st.shared.u16 [%0], %1;" :: "r"(at), "h"(uint16_t(x)) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// What a product does with 32 consecutive sums acc: row `row` (0..127) of the
+// CTA's rows, columns 32 h .. of the 64 in slot `slot`; r and c0 are the row
+// and first column in the matrix.
+// ---------------------------------------------------------------------------
+// writes 32 fp16 values into the block at `slot`, and transposed behind it:
+// two groups of 64 rows (the columns) by 64 columns (the rows)
+__device__ __forceinline__ void put_sym(uint32_t slot, int row, int h, const float* v, bool mirror) {
+    uint32_t x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = pack_half2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        sts128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4), x[4 * q], x[4 * q + 1], x[4 * q + 2],
+               x[4 * q + 3]);
+    if (mirror) {
+        const uint32_t base = slot + uint32_t(kBlkBytes) + uint32_t(row >> 6) * 8192 + uint32_t(row & 7) * 2 +
+                              uint32_t(h) * 32 * 128;
+        const uint32_t ch = uint32_t(row & 63) >> 3;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            sts16(base + j * 128 + ((ch ^ (j & 7)) << 4), (j & 1) ? x[j >> 1] >> 16 : x[j >> 1] & 0xFFFFu);
+    }
+}
+
+// A_rr from the row's sums of squares: sixteen loads at a time, or their
+// latencies add up to more than the product takes
+__device__ __forceinline__ float row_square(const OrthoArgs& a, const MatDesc& d, int r) {
+    const float* p = a.rowsq + d.rowsq + r;
+    const int n = d.cbx >> 1;
+    const int64_t pitch = d.rows_pad;
+    float s = 0.0f;
+    for (int k = 0; k < n; k += 16) {
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = k + u < n ? __ldcg(p + int64_t(k + u) * pitch) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) s += v[u];
+    }
+    return s;
+}
+
+// diag: the row's sum of squares of X where the columns hold A's diagonal
+__device__ __forceinline__ void finish_a(const OrthoArgs& a, const OrthoStep& s, const MatDesc& d, float inv_sx,
+                                         uint32_t slot, int row, int h, int r, int c0, float* acc,
+                                         bool mirror, float diag) {
+    const float k = inv_sx * inv_sx;
+    const RoundScale rs(s.sa * k, r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] *= rs.v[j & 3];
+    const int lane = row & 31;
+    if (r - lane == c0) {       // the warp's rows are these columns
+        a.diag_a[d.diag + r] = diag * k;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[j] = j == lane ? 0.0f : acc[j];
+    }
+    put_sym(slot, row, h, acc, mirror);
+}
+
+// dr: A_rr; cols: A_cc of the 32 columns, in shared memory
+__device__ __forceinline__ void finish_b(const OrthoArgs& a, const OrthoStep& s, const MatDesc& d, uint32_t slot,
+                                         int row, int h, int r, int c0, float* acc, bool mirror, float dr,
+                                         uint32_t cols) {
+    // c (F F^T) + (b + c (D_r + D_c)) F, F in fp16 under the scale of A
+    const float k = s.c * s.inv_sa * s.inv_sa, fb = fmaf(s.c, dr, s.b) * s.inv_sa, fc = s.c * s.inv_sa;
+    const int lane = row & 31;
+    const bool diag = r - lane == c0;   // the warp's rows are these columns
+    if (diag) {                         // F_rr is 0: only the sum counts
+        float ff = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) ff = j == lane ? acc[j] : ff;
+        const float d2 = dr * dr, aa = fmaf(ff * s.inv_sa, s.inv_sa, d2);   // (A A^T)_rr
+        const float db = fmaf(fmaf(s.c, dr, s.b), dr, k * ff);
+        a.diag_b[d.diag + r] = db;
+        a.diag_t[d.diag + r] = aa > 0.0f ? db * (d2 / aa) : 0.0f;
+    }
+    const RoundScale rs(s.sb, r);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 f4 = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
+        const uint4 e0 = lds128(cols + 32 * q), e1 = lds128(cols + 32 * q + 16);
+        const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
+        const uint32_t dc[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 p = unpack_half2(f[j >> 1]);
+            const float fv = (j & 1) ? p.y : p.x;
+            const float v = fmaf(k, acc[8 * q + j], fmaf(fc, __uint_as_float(dc[j]), fb) * fv);
+            acc[8 * q + j] = v * rs.v[j & 3];
+        }
+    }
+    if (diag) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[j] = j == lane ? 0.0f : acc[j];
+    }
+    put_sym(slot, row, h, acc, mirror);
+}
+
+// ah, al: factors of hi and lo; k: of the sums.  Returns the sum of squares of
+// the new (scaled) X.  The last step leaves bf16 values in the slot instead.
+__device__ __forceinline__ float finish_x(const OrthoStep& s, uint32_t slot, int row, int h, int r, float* acc,
+                                          float ah, float al, float k, bool has_lo, bool last) {
+    const RoundScale rs(s.sx_next, r);
+    float sq = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t at = slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4);
+        const uint4 h4 = lds128(at);
+        const uint4 l4 = has_lo ? lds128(at + uint32_t(kBlkBytes)) : make_uint4(0, 0, 0, 0);
+        const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w}, lo[4] = {l4.x, l4.y, l4.z, l4.w};
+        uint32_t nh[4], nl[4];
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 u = unpack_half2(hi[j]), w = unpack_half2(lo[j]);
+            x[2 * j] = fmaf(ah, u.x, fmaf(al, w.x, k * acc[8 * q + 2 * j]));
+            x[2 * j + 1] = fmaf(ah, u.y, fmaf(al, w.y, k * acc[8 * q + 2 * j + 1]));
+        }
+        if (last) {
+            const uint4 o = narrow8(x);
+            sts128(at, o.x, o.y, o.z, o.w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float u = x[2 * j] * s.sx_next, w = x[2 * j + 1] * s.sx_next;
+                sq = fmaf(u, u, fmaf(w, w, sq));
+                nh[j] = pack_half2(x[2 * j] * rs.v[2 * j & 3], x[2 * j + 1] * rs.v[(2 * j + 1) & 3]);
+                const float2 f = unpack_half2(nh[j]);
+                nl[j] = pack_half2((u - f.x) * kLoScale, (w - f.y) * kLoScale);
+            }
+            sts128(at, nh[0], nh[1], nh[2], nh[3]);
+            sts128(at + uint32_t(kBlkBytes), nl[0], nl[1], nl[2], nl[3]);
+        }
+    }
+    return sq;
+}
+
+// A warp's 32 rows x 32 columns of bf16 results from the slot to the flat
+// output.  By rows: four lanes per row.  A tall matrix: lanes along X's rows.
+__device__ __forceinline__ void write_out(const OrthoArgs& a, const MatDesc& d, uint32_t slot, int row0, int h,
+                                          int r0, int c0) {
+    __syncwarp();
+    const int lane = int(threadIdx.x & 31);
+    if (!d.tall) {
+        const bool vec = ((d.off | d.n) & 7) == 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int rr = 8 * p + (lane >> 2), q = lane & 3, row = row0 + rr;
+            const int r = r0 + rr, c = c0 + 8 * q;
+            if (r >= d.m || c >= d.n) continue;
+            const uint4 v = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
+            uint16_t* o = a.out + d.off + int64_t(r) * d.n + c;
+            if (vec) {
+                *reinterpret_cast<uint4*>(o) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < d.n) o[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+            }
+        }
+    } else {
+        const int row = row0 + lane, r = r0 + lane;
+        if (r < d.m) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 v = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = c0 + 8 * q + j;
+                    if (c < d.n) a.out[d.off + int64_t(c) * d.m + r] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+                }
+            }
+        }
+    }
+}
+
+// The count that must have been reached before a tile of (prod, step) starts.
+__device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& a, const MatDesc& d, int mat,
+                                              int prod, int step) {
+    const int before = prod == kProdA ? kProdX : prod - 1;
+    const int target = prod == kProdA ? step * 2 * d.tiles_x : (step + 1) * 2 * d.tiles_sym;
+    return wait_count(sh, a.done + 3 * mat + before, target, a.status);
 }
 
 __global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
-k_ortho_product(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
-                const __grid_constant__ CUtensorMap rows64, const OrthoTile* tiles, int n_tiles,
-                int prod) {
-    extern __shared__ unsigned char dyn[];
-    __shared__ OrthoShared sh;
-    const uint32_t stage0 = (smem_u32(dyn) + 1023u) & ~1023u;
+k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
+              const __grid_constant__ CUtensorMap rows64) {
+    // the kernel's only shared memory: starts on a multiple of 1 KB, as the swizzle wants it
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    OrthoShared& sh = *reinterpret_cast<OrthoShared*>(dyn + kStages * kStageBytes + kSlots * kSlotBytes);
+    const uint32_t stage0 = smem_u32(dyn);
+    const uint32_t slot0 = stage0 + uint32_t(kStages) * kStageBytes;
     const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
     const uint32_t rank = cluster_rank();
-    const int pairs = int(gridDim.x >> 1), pair = int(blockIdx.x >> 1);
+    const int pair = int(blockIdx.x >> 1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(smem_u32(&sh.full[s])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(smem_u32(&sh.empty[s])) : "memory");
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(smem_u32(&sh.tfull[b])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;"
-                         :: "r"(smem_u32(&sh.tempty[b])), "r"(2 * kEpiWarps) : "memory");
+            mbar_init(&sh.tfull[b], 1);
+            mbar_init(&sh.tempty[b], 2 * kEpiWarps);
+            mbar_init(&sh.in_full[b], 1);
+            mbar_init(&sh.out_ready[b], kEpiWarps);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -570,107 +712,218 @@ k_ortho_product(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUt
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     pdl_enter();
     const uint32_t tmem = sh.tmem;
+    const int q0 = __ldg(a.queue_first + pair), q1 = __ldg(a.queue_first + pair + 1);
 
     if (warp == 0 && lane == 0) {
-        // ---- copies ----
+        // ---- operands ----
+        // (what the loop over K needs is in registers: the copies' memory
+        // clobbers would have a value of the descriptor loaded again for each)
+        const uint32_t full0 = map_to(smem_u32(&sh.full[0]), 0);
         int s = 0;
         uint32_t par = 1;             // the first pass over the ring finds it empty
         bool ok = true;
-        for (int t = pair; t < n_tiles && ok; t += pairs) {
-            const OrthoTile tile = tiles[t];
-            const MatDesc& d = a.mats[tile.mat];
-            const TileOperands o = operands_of(d, prod, a.step, tile, int(rank));
-            for (int kb = 0; kb < o.kblocks; ++kb) {
-                if (!(ok = wait_bounded(sh, &sh.empty[s], par, a.status))) break;
-                const uint32_t bar = map_to(smem_u32(&sh.full[s]), 0);
-                if (rank == 0)
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                 :: "r"(smem_u32(&sh.full[s])), "r"(2 * kStageBytes) : "memory");
-                const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
-                copy_box(dst, &rows128, int((o.left + kb) * kBlkRows), bar);
-                if (prod == kProdX) {
-                    const int64_t blk = o.right + int64_t(kb >> 1) * o.right_step;
-                    const int row = int(blk * kBlkRows) + (kb & 1) * 64;
-                    copy_box(dst + kHalfBytes, &rows64, row, bar);
-                    copy_box(dst + kHalfBytes + 8192, &rows64, row + kBlkRows, bar);
-                } else {
-                    copy_box(dst + kHalfBytes, &rows128, int((o.right + kb) * kBlkRows), bar);
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    par ^= 1;
+        for (int step = 0; step < a.n_steps && ok; ++step) {
+            for (int t = q0; t < q1 && ok; ++t) {
+                const OrthoTile tile = a.queue[t];
+                const MatDesc& d = a.mats[tile.mat];
+                const int prod = tile.prod;
+                const int64_t x = d.x[step & 1];
+                const int64_t from = prod == kProdA ? x : prod == kProdB ? d.a : d.b;
+                const int cb = prod == kProdA ? d.cbx : d.cba, kblocks = prod == kProdA ? d.kn : d.km;
+                const int left = int((from + int64_t(tile.i * 2 + int(rank)) * cb) * kBlkRows);
+                const int right = int((prod == kProdX ? x + tile.j * 4 + int(rank) * 2
+                                                      : from + int64_t(tile.j * 2 + int(rank)) * cb) * kBlkRows);
+                const int pitch = d.cbx * kBlkRows;
+                if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!(ok = wait_bounded(sh, &sh.empty[s], par, a.status))) break;
+                    const uint32_t bar = full0 + uint32_t(s) * 8;
+                    if (rank == 0) mbar_expect(&sh.full[s], 2 * kStageBytes);
+                    const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
+                    copy_box(dst, &rows128, left + kb * kBlkRows, bar);
+                    if (prod == kProdX) {
+                        const int row = right + (kb >> 1) * pitch + (kb & 1) * 64;
+                        copy_box(dst + kHalfBytes, &rows64, row, bar);
+                        copy_box(dst + kHalfBytes + 8192, &rows64, row + kBlkRows, bar);
+                    } else {
+                        copy_box(dst + kHalfBytes, &rows128, right + kb * kBlkRows, bar);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        par ^= 1;
+                    }
                 }
             }
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- products ----
-        const bool by_column = prod == kProdX;
-        const uint32_t shape = mma_shape(by_column);
         int s = 0, it = 0;
         uint32_t par = 0;
         bool ok = true;
-        for (int t = pair; t < n_tiles && ok; t += pairs, ++it) {
-            const MatDesc& d = a.mats[tiles[t].mat];
-            const int kblocks = prod == kProdA ? d.kn : d.km;
-            const int buf = it & 1;
-            if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a.status))) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            for (int kb = 0; kb < kblocks; ++kb) {
-                if (!(ok = wait_bounded(sh, &sh.full[s], par, a.status))) break;
+        for (int step = 0; step < a.n_steps && ok; ++step) {
+            for (int t = q0; t < q1 && ok; ++t, ++it) {
+                const OrthoTile tile = a.queue[t];
+                const MatDesc& d = a.mats[tile.mat];
+                const bool by_column = tile.prod == kProdX;
+                const uint32_t shape = mma_shape(by_column);
+                const int kblocks = tile.prod == kProdA ? d.kn : d.km;
+                const int buf = it & 1;
+                if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a.status))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t at = stage0 + uint32_t(s) * kStageBytes;
-                const uint64_t left = desc_of(at, false), right = desc_of(at + kHalfBytes, by_column);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!(ok = wait_bounded(sh, &sh.full[s], par, a.status))) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t at = stage0 + uint32_t(s) * kStageBytes;
+                    const uint64_t left = desc_of(at, false), right = desc_of(at + kHalfBytes, by_column);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)   // 16 deep each
-                    mma_pair(tmem + uint32_t(buf) * kOrthoTile, left + 2 * k,
-                             right + (by_column ? 128 : 2) * k, shape, (kb | k) != 0);
-                commit_pair(&sh.empty[s]);
-                if (++s == kStages) {
-                    s = 0;
-                    par ^= 1;
-                }
-            }
-            if (ok) commit_pair(&sh.tfull[buf]);
-        }
-    } else if (warp >= 2) {
-        // ---- epilogue ----
-        const int quad = warp & 3, half = (warp - 2) >> 2;
-        int it = 0;
-        for (int t = pair; t < n_tiles; t += pairs, ++it) {
-            const OrthoTile tile = tiles[t];
-            const MatDesc& d = a.mats[tile.mat];
-            const int buf = it & 1;
-            const int r = tile.i * kOrthoTile + int(rank) * 128 + quad * 32 + lane;
-            const bool mirror = prod != kProdX && tile.j > tile.i;
-            float diag = 0.0f;
-            if (prod == kProdA && tile.i == tile.j && half == int(rank)) diag = row_square(a, d, r);
-            const bool ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            float sq = 0.0f;
-#pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-                const int col = half * 128 + g * 32;
-                float acc[32];
-                load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(quad * 32) << 16), acc);
-                if (g == 3) {         // the accumulator is free for the tile after next
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                                     :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
-                }
-                const int c0 = tile.j * kOrthoTile + col;
-                if (prod == kProdA) {
-                    finish32<kProdA>(a, d, tile.mat, r, c0, acc, mirror, diag);
-                } else if (prod == kProdB) {
-                    finish32<kProdB>(a, d, tile.mat, r, c0, acc, mirror, diag);
-                } else {
-                    sq += finish32<kProdX>(a, d, tile.mat, r, c0, acc, mirror, diag);
-                    if (g & 1) {
-                        a.rowsq[d.rowsq + int64_t(c0 >> 6) * d.rows_pad + r] = sq;
-                        sq = 0.0f;
+                    for (int k = 0; k < 4; ++k)   // 16 deep each
+                        mma_pair(tmem + uint32_t(buf) * kOrthoTile, left + 2 * k,
+                                 right + (by_column ? 128 : 2) * k, shape, (kb | k) != 0);
+                    commit_pair(&sh.empty[s]);
+                    if (++s == kStages) {
+                        s = 0;
+                        par ^= 1;
                     }
+                }
+                if (ok) commit_pair(&sh.tfull[buf]);
+            }
+        }
+    } else if (warp == kSlotWarp && lane == 0) {
+        // ---- slots ----
+        uint32_t n = 0;               // 64-column blocks so far; block n uses slot n mod 2
+        bool ok = true;
+        for (int step = 0; step < a.n_steps && ok; ++step) {
+            const bool last = step + 1 == a.n_steps;
+            const bool has_lo = step > 0 || a.f32;
+            for (int t = q0; t < q1 && ok; ++t) {
+                const OrthoTile tile = a.queue[t];
+                const MatDesc& d = a.mats[tile.mat];
+                const int prod = tile.prod;
+                if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
+                const bool mirror = prod != kProdX && tile.j > tile.i;
+                const int cb = prod == kProdX ? d.cbx : d.cba;
+                // the CTA's first block within the matrix
+                const int64_t blk = int64_t(tile.i * 2 + int(rank)) * cb + tile.j * 4;
+                for (int g = 0; g <= 4 && ok; ++g) {
+                    if (g < 4) {      // fill the slot of block g
+                        const uint32_t sl = (n + g) & 1, at = slot0 + sl * kSlotBytes;
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        if (prod == kProdA) {
+                            mbar_arrive(&sh.in_full[sl]);
+                        } else if (prod == kProdB) {
+                            mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes));
+                            copy_in(at, a.ws + (d.a + blk + g) * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
+                        } else {
+                            mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (has_lo ? 2 : 1));
+                            copy_in(at, a.ws + (d.x[step & 1] + blk + g) * kBlkBytes, uint32_t(kBlkBytes),
+                                    &sh.in_full[sl]);
+                            if (has_lo)
+                                copy_in(at + uint32_t(kBlkBytes), a.ws + (d.lo + blk + g) * kBlkBytes,
+                                        uint32_t(kBlkBytes), &sh.in_full[sl]);
+                        }
+                    }
+                    if (g > 0) {      // write out block g - 1
+                        const uint32_t k = n + uint32_t(g) - 1, sl = k & 1, at = slot0 + sl * kSlotBytes;
+                        if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (k >> 1) & 1, a.status))) break;
+                        if (prod != kProdX) {
+                            const int64_t to = prod == kProdA ? d.a : d.b;
+                            copy_out(a.ws + (to + blk + g - 1) * kBlkBytes, at, uint32_t(kBlkBytes));
+                            if (mirror) {   // 64 rows from column 64 (g - 1) of the tile, 2 x 64 columns
+                                unsigned char* m = a.ws + (to + int64_t(tile.j * 2 + ((g - 1) >> 1)) * cb +
+                                                           tile.i * 4 + int(rank) * 2) * kBlkBytes +
+                                                   ((g - 1) & 1) * 8192;
+                                copy_out(m, at + uint32_t(kBlkBytes), 8192);
+                                copy_out(m + kBlkBytes, at + uint32_t(kBlkBytes) + 8192, 8192);
+                            }
+                        } else if (!last) {
+                            copy_out(a.ws + (d.x[(step + 1) & 1] + blk + g - 1) * kBlkBytes, at, uint32_t(kBlkBytes));
+                            copy_out(a.ws + (d.lo + blk + g - 1) * kBlkBytes, at + uint32_t(kBlkBytes),
+                                     uint32_t(kBlkBytes));
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                }
+                n += 4;
+                if (!ok) break;
+                // all of the tile is in memory before its count
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                asm volatile("fence.proxy.async;" ::: "memory");
+                __threadfence();
+                asm volatile("red.release.gpu.global.add.s32 [%0], 1;"
+                             :: "l"(a.done + 3 * tile.mat + prod) : "memory");
+            }
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    } else if (warp >= 2 && warp < kSlotWarp) {
+        // ---- finish ----
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int row0 = quad * 32, row = row0 + lane;
+        int it = 0;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int step = 0; step < a.n_steps && ok; ++step) {
+            const OrthoStep& s = a.st[step];
+            const bool last = step + 1 == a.n_steps;
+            const bool has_lo = step > 0 || a.f32;
+            for (int t = q0; t < q1 && ok; ++t, ++it) {
+                const OrthoTile tile = a.queue[t];
+                const MatDesc& d = a.mats[tile.mat];
+                const int prod = tile.prod, buf = it & 1;
+                const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
+                const bool mirror = prod != kProdX && tile.j > tile.i;
+                if (lane == 0) ok = wait_operands(sh, a, d, tile.mat, prod, step);
+                if (!(ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0) != 0)) break;
+                // what the rows need, fetched while the product runs
+                const float inv_sx = step == 0 ? __ldcg(&a.scal[tile.mat].y) : s.inv_sx;
+                float p0 = 0.0f, p1 = 0.0f, dc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sq = 0.0f;
+                if (prod == kProdA) {
+                    // the two warps that hold the diagonal's 64-column block share its rows' sums
+                    if (tile.i == tile.j && half == (quad & 1)) p0 = row_square(a, d, r);
+                } else if (prod == kProdB) {
+                    p0 = __ldcg(a.diag_a + d.diag + r);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        dc[g] = __ldcg(a.diag_a + d.diag + tile.j * kOrthoTile + g * 64 + half * 32 + lane);
+                } else {
+                    p0 = fmaf(__ldcg(a.diag_b + d.diag + r), inv_sx, s.a * inv_sx);
+                    p1 = fmaf(__ldcg(a.diag_t + d.diag + r), inv_sx, s.a * inv_sx) * kInvLoScale;
+                }
+                ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g, ++n) {
+                    const int col = g * 64 + half * 32;
+                    const uint32_t sl = n & 1, slot = slot0 + sl * kSlotBytes;
+                    float acc[32];
+                    load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(row0) << 16), acc);
+                    if (g == 3) {     // the accumulator is free for the tile after next
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                                         :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
+                    }
+                    ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a.status);
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                    const int c0 = tile.j * kOrthoTile + col;
+                    if (prod == kProdA) {
+                        finish_a(a, s, d, inv_sx, slot, row, half, r, c0, acc, mirror, p0);
+                    } else if (prod == kProdB) {
+                        __syncwarp();
+                        sh.cols[warp - 2][lane] = g == 0 ? dc[0] : g == 1 ? dc[1] : g == 2 ? dc[2] : dc[3];
+                        __syncwarp();
+                        finish_b(a, s, d, slot, row, half, r, c0, acc, mirror, p0, smem_u32(sh.cols[warp - 2]));
+                    } else {
+                        sq += finish_x(s, slot, row, half, r, acc, p0, p1, inv_sx * s.inv_sb, has_lo, last);
+                        if (last)
+                            write_out(a, d, slot, row0, half, r0, c0);
+                        else if (g == 3)   // of the warp's 128 columns of the tile
+                            a.rowsq[d.rowsq + int64_t(tile.j * 2 + half) * d.rows_pad + r] = sq;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.out_ready[sl]);
                 }
             }
         }
@@ -730,10 +983,31 @@ int upload_matrices(Matrices& m) {
                         m.device, dev);
         return DPG_OK;
     }
+    // how many CTA pairs are resident at once decides the queues
+    int clusters = 1;
+    if (!m.mats.empty()) {
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kOrthoThreads);
+        cfg.dynamicSmemBytes = kOrthoSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps, &cfg));
+        if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no CTA pair fits this device");
+    }
+    try {
+        lay_queue(m, clusters);
+    } catch (const std::exception&) {
+        return fail(DPG_ERR_OOM, "matrices upload: out of host memory");
+    }
     const size_t bytes = round256(m.mats.size() * sizeof(MatDesc)) +
-                         round256(m.tiles[0].size() * sizeof(OrthoTile)) +
-                         round256(m.tiles[1].size() * sizeof(OrthoTile)) +
-                         round256(m.tiles[2].size() * sizeof(OrthoTile)) +
+                         round256(m.queue.size() * sizeof(OrthoTile)) +
+                         round256(m.queue_first.size() * sizeof(int32_t)) +
                          round256(m.norm_items.size() * sizeof(NormItem)) +
                          round256(m.conv_items.size() * sizeof(ConvItem)) +
                          round256(m.apply_items.size() * sizeof(ApplyItem)) +
@@ -744,7 +1018,8 @@ int upload_matrices(Matrices& m) {
     unsigned char* t = static_cast<unsigned char*>(tables);
     size_t at = 0;
     if (e == cudaSuccess) e = put(t, &at, m.mats, &m.d_mats);
-    for (int k = 0; k < 3 && e == cudaSuccess; ++k) e = put(t, &at, m.tiles[k], &m.d_tiles[k]);
+    if (e == cudaSuccess) e = put(t, &at, m.queue, &m.d_queue);
+    if (e == cudaSuccess) e = put(t, &at, m.queue_first, &m.d_queue_first);
     if (e == cudaSuccess) e = put(t, &at, m.norm_items, &m.d_norm_items);
     if (e == cudaSuccess) e = put(t, &at, m.conv_items, &m.d_conv_items);
     if (e == cudaSuccess) e = put(t, &at, m.apply_items, &m.d_apply_items);
@@ -753,46 +1028,23 @@ int upload_matrices(Matrices& m) {
     if (e == cudaSuccess)
         e = cudaMemset(static_cast<unsigned char*>(ws) + m.o_count, 0, size_t(m.workspace_bytes - m.o_count));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    int st = DPG_OK;
     if (e != cudaSuccess) {
+        cudaGetLastError();
+        st = fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA, "matrices upload: %s",
+                  cudaGetErrorString(e));
+    }
+    static_assert(sizeof(CUtensorMap) == sizeof(m.maps[0]), "room for a tensor map");
+    for (int k = 0; k < 2 && st == DPG_OK && m.n_blocks > 0; ++k) {
+        CUtensorMap map;
+        st = encode_map(&map, ws, m.n_blocks * kBlkRows, k ? 64 : 128);
+        std::memcpy(m.maps[k], &map, sizeof map);
+    }
+    if (st != DPG_OK) {
         cudaFree(tables);
         cudaFree(ws);
-        cudaGetLastError();
-        return fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA,
-                    "matrices upload: %s", cudaGetErrorString(e));
+        return st;
     }
-    int clusters = 0;
-    if (m.n_blocks > 0) {
-        static_assert(sizeof(CUtensorMap) == sizeof(m.maps[0]), "room for a tensor map");
-        CUtensorMap map;
-        for (int k = 0; k < 2; ++k) {
-            const int st = encode_map(&map, ws, m.n_blocks * kBlkRows, k ? 64 : 128);
-            if (st != DPG_OK) {
-                cudaFree(tables);
-                cudaFree(ws);
-                return st;
-            }
-            std::memcpy(m.maps[k], &map, sizeof map);
-        }
-        e = cudaFuncSetAttribute(k_ortho_product, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem);
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kOrthoThreads);
-        cfg.dynamicSmemBytes = kOrthoSmem;
-        cudaLaunchAttribute pair[1];
-        pair[0].id = cudaLaunchAttributeClusterDimension;
-        pair[0].val.clusterDim.x = 2;
-        pair[0].val.clusterDim.y = pair[0].val.clusterDim.z = 1;
-        cfg.attrs = pair;
-        cfg.numAttrs = 1;
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, k_ortho_product, &cfg);
-        if (e != cudaSuccess || clusters < 1) {
-            cudaFree(tables);
-            cudaFree(ws);
-            cudaGetLastError();
-            return fail(DPG_ERR_CUDA, "matrices upload: %s", cudaGetErrorString(e));
-        }
-    }
-    m.clusters = clusters;
     m.d_tables = t;
     m.ws = static_cast<unsigned char*>(ws);
     m.device = dev;
@@ -825,35 +1077,11 @@ void release_matrices(Matrices& m) {
     m.device = -1;
 }
 
-static int launch_product(const Matrices& m, const OrthoArgs& a, int prod, cudaStream_t s, const char* who) {
-    CUtensorMap map[2];
-    std::memcpy(map, m.maps, sizeof map);
-    const int n = int(m.tiles[prod].size());
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(2 * (n < m.clusters ? n : m.clusters)));
-    cfg.blockDim = dim3(kOrthoThreads);
-    cfg.dynamicSmemBytes = kOrthoSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = t_programmatic ? 1 : 0;
-    const OrthoTile* tiles = m.d_tiles[prod];
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_product, a, map[0], map[1], tiles, n, prod);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
-    }
-    return after_launch(who);
-}
-
 int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
                  void* out, void* stream, const char* who) {
-    OrthoStep steps[DPG_MAX_NS_STEPS];
-    int st = ortho_steps(hp, steps, who);
-    if (st != DPG_OK || m.mats.empty()) return st;
     OrthoArgs a{};
+    int st = ortho_steps(hp, a.st, who);
+    if (st != DPG_OK || m.mats.empty()) return st;
     a.mats = m.d_mats;
     a.ws = m.ws;
     a.diag_a = reinterpret_cast<float*>(m.ws + m.o_diag);
@@ -866,21 +1094,37 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.status = reinterpret_cast<int32_t*>(m.ws + m.o_status);
     a.update = update;
     a.f32 = update_dtype == DPG_F32;
+    a.done = reinterpret_cast<int32_t*>(m.ws + m.o_done);
+    a.queue = m.d_queue;
+    a.queue_first = m.d_queue_first;
     a.n_steps = hp->n_steps;
     a.eps = hp->eps;
     a.out = static_cast<uint16_t*>(out);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch_k(k_ortho_norm, unsigned(m.norm_items.size()), kNormThreads, s, who, a,
-                  static_cast<const NormItem*>(m.d_norm_items));
+    st = launch_k(a.f32 ? k_ortho_norm<true> : k_ortho_norm<false>, unsigned(m.norm_items.size()), kNormThreads,
+                  s, who, a, static_cast<const NormItem*>(m.d_norm_items));
     if (st == DPG_OK)
-        st = launch_k(k_ortho_load, unsigned(m.conv_items.size()), 256, s, who, a,
-                      static_cast<const ConvItem*>(m.d_conv_items));
-    for (int k = 0; k < hp->n_steps && st == DPG_OK; ++k) {
-        a.step = k;
-        a.st = steps[k];
-        for (int prod = 0; prod < 3 && st == DPG_OK; ++prod) st = launch_product(m, a, prod, s, who);
+        st = launch_k(a.f32 ? k_ortho_load<true> : k_ortho_load<false>, unsigned(m.conv_items.size()), 256, s,
+                      who, a, static_cast<const ConvItem*>(m.d_conv_items));
+    if (st != DPG_OK) return st;
+    CUtensorMap map[2];
+    std::memcpy(map, m.maps, sizeof map);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * m.pairs));
+    cfg.blockDim = dim3(kOrthoThreads);
+    cfg.dynamicSmemBytes = kOrthoSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;   // the pairs wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_steps, a, map[0], map[1]);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     }
-    return st;
+    return after_launch(who);
 }
 
 }  // namespace dpg

@@ -35,15 +35,17 @@ struct MatDesc {
     int64_t x[2], lo;     // first block of the two X buffers and of X's low part
     int64_t a, b;         // first block of A and of bA + cA^2 (off-diagonal parts)
     int64_t diag;         // first entry of the per-row vectors (see OrthoArgs)
-    int64_t rowsq;        // first entry of X's row sums of squares, [cbx][padded rows]
+    int64_t rowsq;        // first entry of X's row sums of squares, [cbx / 2][padded rows]
     int32_t rows_pad;     // rows of X padded to 256
     int32_t norm0, norm1; // its items in the norm table
+    int32_t tiles_sym, tiles_x;   // output tiles of A (and B), of X
 };
 
 // One 256 x 256 output tile of one product of one matrix.
 struct OrthoTile {
     int32_t mat;
     int16_t i, j;
+    int32_t prod;
 };
 
 // Items of the norm and conversion passes and of the weight update.
@@ -52,7 +54,7 @@ struct NormItem {
     int64_t start;
 };
 struct ConvItem {
-    int32_t mat, i, j, pad;   // block (i, j) of X
+    int32_t mat, i, j, pad;   // blocks (i, 2 j) and (i, 2 j + 1) of X
 };
 struct ApplyItem {
     int64_t off;          // flat offset, a multiple of 8
@@ -80,7 +82,9 @@ struct Matrices {
     int32_t n_params = 0;
     std::vector<int64_t> param_offset, numels;
     std::vector<MatDesc> mats;
-    std::vector<OrthoTile> tiles[3];
+    std::vector<OrthoTile> queue;      // tiles of a step, pair after pair (see lay_queue)
+    std::vector<int32_t> queue_first;  // pairs + 1
+    int32_t pairs = 0;
     std::vector<NormItem> norm_items;
     std::vector<ConvItem> conv_items;
     std::vector<ApplyItem> apply_items;
@@ -88,22 +92,24 @@ struct Matrices {
     int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0;
     int64_t workspace_bytes = 0;
     // byte offsets in the workspace
-    int64_t o_diag = 0, o_rowsq = 0, o_part = 0, o_scal = 0, o_count = 0, o_status = 0;
+    int64_t o_diag = 0, o_rowsq = 0, o_part = 0, o_scal = 0, o_count = 0, o_done = 0, o_status = 0;
 
     std::mutex mu;
     int device = -1;
     unsigned char* ws = nullptr;       // workspace_bytes
     unsigned char* d_tables = nullptr; // one allocation, sections below
     MatDesc* d_mats = nullptr;
-    OrthoTile* d_tiles[3] = {nullptr, nullptr, nullptr};
+    OrthoTile* d_queue = nullptr;
+    int32_t* d_queue_first = nullptr;
     NormItem* d_norm_items = nullptr;
     ConvItem* d_conv_items = nullptr;
     ApplyItem* d_apply_items = nullptr;
     double* d_scales = nullptr;
     alignas(64) unsigned char maps[2][128];   // tensor maps of the workspace: 128 and 64 rows a copy
-    int clusters = 0;                         // CTA pairs resident at once
 };
 
+// fills queue, queue_first and pairs for a device that holds `clusters` CTA pairs
+void lay_queue(Matrices& m, int clusters);
 // device side (dpg_ortho.cu)
 int upload_matrices(Matrices& m);
 void release_matrices(Matrices& m);
