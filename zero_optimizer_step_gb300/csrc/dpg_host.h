@@ -49,16 +49,16 @@ int after_launch(const char* what);
 size_t round256(size_t x);
 
 // Launches kernel k (which must begin with pdl_enter()) on `grid` CTAs of
-// `block` threads, with programmatic stream serialization unless the calling
+// `block` threads and `smem` bytes of dynamic shared memory, with programmatic stream serialization unless the calling
 // thread switched it off, then checks and counts the launch like
 // after_launch().
 template <typename... P, typename... A>
-int launch_k(void (*k)(P...), unsigned grid, unsigned block, cudaStream_t s, const char* who,
+int launch_k(void (*k)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, const char* who,
              A&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -71,6 +71,12 @@ int launch_k(void (*k)(P...), unsigned grid, unsigned block, cudaStream_t s, con
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     }
     return after_launch(who);
+}
+
+// the same without dynamic shared memory
+template <typename... P, typename... A>
+int launch_k(void (*k)(P...), unsigned grid, unsigned block, cudaStream_t s, const char* who, A&&... args) {
+    return launch_k(k, grid, block, size_t(0), s, who, std::forward<A>(args)...);
 }
 
 // Byte layout of a norm scratch with `visits` (CTA, bucket visit) slots for up

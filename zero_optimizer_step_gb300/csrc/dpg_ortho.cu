@@ -119,41 +119,55 @@ struct RoundScale {
 };
 
 // ---------------------------------------------------------------------------
-// Frobenius norms.  One CTA per item (<= 16384 elements of one matrix); sums
-// of eight squares in fp32 (in double when that leaves fp32's range), the rest
-// in double.  The CTA that finishes a matrix adds its items in item order and
-// writes the scale 2^k that puts max(norm, eps) 2^k into [2^14, 2^15) -- every
-// |u| 2^k is then below 2^15, and u 2^k is exact for bf16 u -- and
-// 1 / (max(norm, eps) 2^k).
+// Frobenius norms.  One CTA per item (<= 16384 elements of one matrix): sums
+// of squares in fp32, item sums and everything after in double.  Vectors whose
+// squares leave fp32's range (|u| beyond about 1e15, below 1e-15) are squared
+// in double: this GPU's binary64 rate is a few operations per SM and cycle, so
+// a binary64 sum per vector, with its conversions and its reduction, took four
+// times as long as the loads.  The CTA that finishes a matrix adds its items
+// in item order and writes the scale 2^k that puts max(norm, eps) 2^k into
+// [2^14, 2^15) -- every |u| 2^k is then below 2^15, and u 2^k is exact for
+// bf16 u -- and 1 / (max(norm, eps) 2^k).
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 
-__device__ __forceinline__ double block_sum(double x, double* sh) {
+// sum of f over the CTA in fp32 plus sum of w (mostly zero everywhere) in double
+__device__ __forceinline__ double block_sum(float f, double w, double* sh) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xFFFFFFFFu, f, o);
+    if (__any_sync(0xFFFFFFFFu, w != 0.0)) {     // a NaN differs from zero too
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+    }
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = double(f) + w;
     __syncthreads();
     double t = 0.0;
-    for (int w = 0; w < kNormThreads / 32; ++w) t += sh[w];
-    return t;
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kNormThreads / 32; ++k) t += sh[k];
+    return t;                                    // in thread 0
 }
 
-// the sum of eight squares
-__device__ __forceinline__ double square8(const float* x) {
+// adds eight squares to f, or to w where fp32 cannot hold them
+__device__ __forceinline__ void square8(const float* x, float& f, double& w) {
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-    if (s > 1e-30f && s < 1e30f) return double(s);
-    double t = 0.0;
+    if (s > 1e-30f && s < 1e30f) {
+        f += s;
+        return;
+    }
+    float top = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t += double(x[j]) * double(x[j]);
-    return t;
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+    if (s == 0.0f && top == 0.0f) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w += double(x[j]) * double(x[j]);
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_constant__ OrthoArgs a,
                                                             const NormItem* items) {
-    __shared__ double sh[2][kNormThreads / 32];
+    __shared__ double sh[kNormThreads / 32];
     __shared__ int last;
     pdl_enter();
     const NormItem it = items[blockIdx.x];
@@ -161,7 +175,8 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
     const int64_t base = d.off + it.start;
     constexpr int kPer = kNormChunk / (kNormThreads * 8), kFly = F32 ? 4 : 8;   // vectors per thread, in flight
     static_assert(kPer % kFly == 0, "whole batches");
-    double acc = 0.0;
+    float f = 0.0f;
+    double w = 0.0;
     if (it.count == kNormChunk && (base & 7) == 0) {
 #pragma unroll 1
         for (int k = 0; k < kPer; k += kFly) {
@@ -170,28 +185,29 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
             for (int u = 0; u < kFly; ++u)
                 load_update8<F32>(a, base + (int64_t(k + u) * kNormThreads + threadIdx.x) * 8, x[u]);
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) acc += square8(x[u]);
+            for (int u = 0; u < kFly; ++u) square8(x[u], f, w);
         }
     } else {
         for (int e = int(threadIdx.x) * 8; e < it.count; e += kNormThreads * 8) {
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = e + j < it.count ? load_update<F32>(a, base + e + j) : 0.0f;
-            acc += square8(x);
+            square8(x, f, w);
         }
     }
-    const double tot = block_sum(acc, sh[0]);
+    const double tot = block_sum(f, w, sh);
     if (threadIdx.x == 0) {
         a.part[blockIdx.x] = tot;
         __threadfence();
         last = atomicAdd(a.count + it.mat, 1) == d.norm1 - d.norm0 - 1;
     }
     __syncthreads();
-    if (!last) return;
+    if (!last || threadIdx.x >= 32) return;
     __threadfence();
-    acc = 0.0;
-    for (int k = d.norm0 + int(threadIdx.x); k < d.norm1; k += kNormThreads) acc += __ldcg(a.part + k);
-    const double sum = block_sum(acc, sh[1]);
+    double sum = 0.0;
+    for (int k = d.norm0 + int(threadIdx.x); k < d.norm1; k += 32) sum += __ldcg(a.part + k);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (threadIdx.x == 0) {
         a.count[it.mat] = 0;
         const double norm = sqrt(sum);
@@ -209,86 +225,144 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// U -> X_0 as fp16 blocks (hi and lo), zero in the padding.  One CTA per two
-// neighbouring blocks (128 x 128).  A tall matrix is transposed on the way:
-// lanes then run along X's rows, which are contiguous in U.  Moves 4 bytes per
-// element of a bf16 update (lo, all zero, is left out), 8 of an fp32 one.
+// U -> X_0 as fp16 blocks (hi and lo), zero in the padding, and the row sums
+// of squares.  One CTA per two neighbouring blocks (128 x 128).  Moves 4 bytes
+// per element of a bf16 update (lo, all zero, is left out), 8 of an fp32 one.
+// A tall matrix is transposed through shared memory: 16-byte loads along U's
+// rows; 2-byte loads along X's rows took four times as long as the copy.
 // ---------------------------------------------------------------------------
+constexpr int kLoadPitch = 136;   // fp16 values of a transposed row: 16-byte rows, banks 4 words apart
+constexpr int kLoadSmem = kBlkRows * kLoadPitch * 2;
+
+__device__ __forceinline__ void split16(float u, float rounded, uint16_t& hi, uint16_t& lo) {
+    const __half h = __float2half_rn(rounded);
+    hi = __half_as_ushort(h);
+    lo = __half_as_ushort(__float2half_rn((u - __half2float(h)) * kLoScale));
+}
+
 template <bool F32, bool TALL>
-__device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d, const ConvItem& it) {
+__device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d, const ConvItem& it,
+                                            uint16_t* sm) {
     const float sc = a.scal[it.mat].x;
     const int64_t blk = int64_t(it.i) * d.cbx + it.j * 2;
     unsigned char* hi = a.ws + (d.x[0] + blk) * kBlkBytes;
     unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
-    const bool vec = !TALL && ((d.off | d.n) & 7) == 0;
-    // by rows: sixteen lanes hold a row's sixteen chunks of 8; tall: a thread
-    // holds eight chunks of one row
-    float x[8][8];
+    const int r0 = it.i * kBlkRows, c0 = it.j * 2 * kBlkCols, m = d.m, n = d.n;
+    const int64_t off = d.off;
+    uint16_t* sm_lo = sm + kBlkRows * kLoadPitch;
+    if (TALL) {
+        // row c of U holds X's column c: X[r][c] = U[c m + r]
+        const bool vec = ((off | m) & 7) == 0;
+        if (vec) {
+            float x[8][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = TALL ? int(threadIdx.x) & 127 : 16 * i + (int(threadIdx.x) >> 4);
-        const int ch = TALL ? 8 * (int(threadIdx.x) >> 7) + i : int(threadIdx.x) & 15;
-        const int r = it.i * kBlkRows + row, c = it.j * 2 * kBlkCols + ch * 8;
-        if (vec && r < d.m && c < d.n) {
-            load_update8<F32>(a, d.off + int64_t(r) * d.n + c, x[i]);
+            for (int i = 0; i < 8; ++i) {   // 16 columns by two vectors of 8 rows per warp
+                const int q = i * 8 + int(threadIdx.x >> 5);
+                const int c = c0 + (q & 7) * 16 + (int(threadIdx.x) & 15);
+                const int r = r0 + ((q >> 3) * 2 + ((int(threadIdx.x) >> 4) & 1)) * 8;
+                if (c < n && r < m) {
+                    load_update8<F32>(a, off + int64_t(c) * m + r, x[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int q = i * 8 + int(threadIdx.x >> 5);
+                const int c = (q & 7) * 16 + (int(threadIdx.x) & 15);
+                const int r = ((q >> 3) * 2 + ((int(threadIdx.x) >> 4) & 1)) * 8;
+                const bool in = c0 + c < n && r0 + r < m;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float u = in ? x[i][j] * sc : 0.0f;
+                    uint16_t h, l;
+                    split16(u, F32 ? u * RoundScale(1.0f, r + j + c).v[0] : u, h, l);
+                    sm[(r + j) * kLoadPitch + c] = h;
+                    if (F32) sm_lo[(r + j) * kLoadPitch + c] = l;
+                }
+            }
         } else {
+            for (int e = int(threadIdx.x); e < 128 * 128; e += 256) {
+                const int c = e >> 7, r = e & 127;
+                const float u = c0 + c < n && r0 + r < m
+                                    ? load_update<F32>(a, off + int64_t(c0 + c) * m + r0 + r) * sc : 0.0f;
+                uint16_t h, l;
+                split16(u, F32 ? u * RoundScale(1.0f, r + c).v[0] : u, h, l);
+                sm[r * kLoadPitch + c] = h;
+                if (F32) sm_lo[r * kLoadPitch + c] = l;
+            }
+        }
+        __syncthreads();
+    }
+    const bool vec = !TALL && ((off | n) & 7) == 0;
+    float x[8][8];
+    if (!TALL) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[i][j] = r < d.m && c + j < d.n
-                              ? load_update<F32>(a, d.off + (TALL ? int64_t(c + j) * d.m + r
-                                                                  : int64_t(r) * d.n + c + j))
-                              : 0.0f;
+        for (int i = 0; i < 8; ++i) {   // sixteen lanes hold a row's sixteen chunks of 8
+            const int r = r0 + 16 * i + (int(threadIdx.x) >> 4), c = c0 + (int(threadIdx.x) & 15) * 8;
+            if (vec && r < m && c < n) {
+                load_update8<F32>(a, off + int64_t(r) * n + c, x[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[i][j] = r < m && c + j < n ? load_update<F32>(a, off + int64_t(r) * n + c + j) : 0.0f;
+            }
         }
     }
-    float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int row = TALL ? int(threadIdx.x) & 127 : 16 * i + (int(threadIdx.x) >> 4);
-        const int ch = TALL ? 8 * (int(threadIdx.x) >> 7) + i : int(threadIdx.x) & 15;
-        const int r = it.i * kBlkRows + row, c = it.j * 2 * kBlkCols + ch * 8;
-        const RoundScale rs(1.0f, row);
-        uint32_t h[4], l[4];
-        if (!TALL) sq = 0.0f;
+        const int row = 16 * i + (int(threadIdx.x) >> 4), ch = int(threadIdx.x) & 15;
+        uint4 h4, l4 = make_uint4(0, 0, 0, 0);
+        float sq = 0.0f;
+        if (TALL) {
+            h4 = *reinterpret_cast<const uint4*>(sm + row * kLoadPitch + ch * 8);
+            if (F32) l4 = *reinterpret_cast<const uint4*>(sm_lo + row * kLoadPitch + ch * 8);
+            const uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // (sc is a NaN for a matrix that is not finite: padding stays zero)
-            const float u = r < d.m && c + 2 * j < d.n ? x[i][2 * j] * sc : 0.0f;
-            const float v = r < d.m && c + 2 * j + 1 < d.n ? x[i][2 * j + 1] * sc : 0.0f;
-            sq = fmaf(u, u, fmaf(v, v, sq));
-            // a scaled bf16 value is an fp16 value: nothing to round, lo is 0
-            h[j] = F32 ? pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]) : pack_half2(u, v);
-            const float2 f = unpack_half2(h[j]);
-            l[j] = pack_half2((u - f.x) * kLoScale, (v - f.y) * kLoScale);
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_half2(h[j]), g = unpack_half2(l[j]);
+                const float u = fmaf(g.x, kInvLoScale, f.x), v = fmaf(g.y, kInvLoScale, f.y);
+                sq = fmaf(u, u, fmaf(v, v, sq));
+            }
+        } else {
+            const int r = r0 + row, c = c0 + ch * 8;
+            const RoundScale rs(1.0f, row);
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // (sc is a NaN for a matrix that is not finite: padding stays zero)
+                const float u = r < m && c + 2 * j < n ? x[i][2 * j] * sc : 0.0f;
+                const float v = r < m && c + 2 * j + 1 < n ? x[i][2 * j + 1] * sc : 0.0f;
+                sq = fmaf(u, u, fmaf(v, v, sq));
+                // a scaled bf16 value is an fp16 value: nothing to round, lo is 0
+                h[j] = F32 ? pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]) : pack_half2(u, v);
+                const float2 f = unpack_half2(h[j]);
+                l[j] = pack_half2((u - f.x) * kLoScale, (v - f.y) * kLoScale);
+            }
+            h4 = make_uint4(h[0], h[1], h[2], h[3]);
+            l4 = make_uint4(l[0], l[1], l[2], l[3]);
         }
         const int64_t at = (ch >> 3) * kBlkBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (F32) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-        if (!TALL) {
+        *reinterpret_cast<uint4*>(hi + at) = h4;
+        if (F32) *reinterpret_cast<uint4*>(lo + at) = l4;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-            if (ch == 0) a.rowsq[d.rowsq + int64_t(it.j) * d.rows_pad + r] = sq;
-        }
-    }
-    if (TALL) {
-        __shared__ float other[kBlkRows];
-        if (threadIdx.x >= 128) other[threadIdx.x & 127] = sq;
-        __syncthreads();
-        if (threadIdx.x < 128)
-            a.rowsq[d.rowsq + int64_t(it.j) * d.rows_pad + it.i * kBlkRows + int(threadIdx.x)] =
-                sq + other[threadIdx.x];
+        for (int o = 8; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+        if (ch == 0) a.rowsq[d.rowsq + int64_t(it.j) * d.rows_pad + r0 + row] = sq;
     }
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ OrthoArgs a, const ConvItem* items) {
+    extern __shared__ __align__(16) uint16_t load_sm[];   // kLoadSmem, twice for fp32
     pdl_enter();
     const ConvItem it = items[blockIdx.x];
     const MatDesc& d = a.mats[it.mat];
     if (it.i == 0 && it.j == 0 && threadIdx.x < 3) a.done[3 * it.mat + int(threadIdx.x)] = 0;
     if (d.tall)
-        load_blocks<F32, true>(a, d, it);
+        load_blocks<F32, true>(a, d, it, load_sm);
     else
-        load_blocks<F32, false>(a, d, it);
+        load_blocks<F32, false>(a, d, it, load_sm);
 }
 
 // ---------------------------------------------------------------------------
@@ -986,6 +1060,8 @@ int upload_matrices(Matrices& m) {
     // how many CTA pairs are resident at once decides the queues
     int clusters = 1;
     if (!m.mats.empty()) {
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_load<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          2 * kLoadSmem));
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
@@ -1104,8 +1180,8 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     st = launch_k(a.f32 ? k_ortho_norm<true> : k_ortho_norm<false>, unsigned(m.norm_items.size()), kNormThreads,
                   s, who, a, static_cast<const NormItem*>(m.d_norm_items));
     if (st == DPG_OK)
-        st = launch_k(a.f32 ? k_ortho_load<true> : k_ortho_load<false>, unsigned(m.conv_items.size()), 256, s,
-                      who, a, static_cast<const ConvItem*>(m.d_conv_items));
+        st = launch_k(a.f32 ? k_ortho_load<true> : k_ortho_load<false>, unsigned(m.conv_items.size()), 256,
+                      a.f32 ? 2 * kLoadSmem : kLoadSmem, s, who, a, static_cast<const ConvItem*>(m.d_conv_items));
     if (st != DPG_OK) return st;
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);
