@@ -495,7 +495,8 @@ typedef struct {
 /* The matrices of a plan.  rows[p], cols[p] (HOST arrays, n_params entries,
  * each >= 1): parameter p is numel_p / (rows[p] * cols[p]) row-major matrices
  * one after the other; a numel that is not a multiple of rows * cols is
- * DPG_ERR_INVALID_ARG, a zero-size parameter holds no matrix.  The object
+ * DPG_ERR_INVALID_ARG, a zero-size parameter holds no matrix; at most 2^20
+ * matrices and 2^31 128-byte rows of workspace.  The object
  * keeps what it needs of the plan (which may be destroyed before it), the
  * tile tables, and a device workspace of workspace_bytes that it allocates on
  * its first device call or in dpg_matrices_upload (call that before a stream

@@ -24,9 +24,11 @@ def _mats(shapes=((4, 6), (3, 5)), counts=(1, 2)):
 
 def test_matrices_of_a_plan():
     plan, mats = _mats()
+    assert mats.n_matrices == 3 and mats.workspace_bytes > 0
+    # 256 x 512 padded: three X arrays, and two 256 x 256 ones, of fp16 each
+    _, mats = _mats(((400, 200),), (3,))
     assert mats.n_matrices == 3
-    # 256 x 256 padded: three X arrays and two square ones of fp16 each
-    assert mats.workspace_bytes >= 3 * 5 * 256 * 256 * 2
+    assert mats.workspace_bytes >= 3 * (3 * 256 * 512 + 2 * 256 * 256) * 2
     empty = dpg.dpg_plan_buckets([0, 12, 0], 1 << 20, 1)
     assert dpg.dpg_plan_matrices(empty, [5, 3, 1], [5, 4, 1]).n_matrices == 1
     none = dpg.dpg_plan_buckets([], 1 << 20, 1)

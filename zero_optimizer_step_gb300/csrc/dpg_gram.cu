@@ -1,0 +1,525 @@
+// dpg_gram.cu -- orthogonalisation of matrices whose shorter side is at most
+// kSmallSide (see dpg_orthogonalize in include/dpg.h).
+//
+// Every Newton-Schulz step multiplies X from the left by a polynomial of its
+// Gram matrix, Q_k = aI + bA_k + cA_k^2 with A_k = X_k X_k^T, and all of these
+// are polynomials of A_0: they commute, and
+//     A_{k+1} = Q_k A_k Q_k,     X_n = (Q_{n-1} ... Q_1 Q_0) X_0.
+// So the steps run on m x m matrices alone, between one pass over U that sums
+// its Gram matrix (which also gives the norm: its trace) and one that
+// multiplies U by the product P of the Q_k: 3 m^2 n flops and a few m^3 per
+// step instead of 3 m^2 n per step, and three launches' latency instead of
+// three dependent tile products per step.
+//
+// Everything is binary32.  An error e in A_k moves the small eigenvalues l by
+// e / l relative, so the 11-bit operands of the large matrices' tensor-core
+// products would lose the directions that the steps are there to bring up;
+// with 24 bits the result is within 1e-6 (Gaussian) to 1e-3 (rank one) of the
+// exact one.  At 128 rows the plain arithmetic is no burden: 4 * 128^3
+// multiply-adds per step on eight SMs are 3 us.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "dpg_host.h"
+#include "dpg_ortho.h"
+
+namespace dpg {
+
+struct GramArgs {
+    const SmallDesc* mats;
+    const void* update;
+    uint16_t* out;           // flat bf16
+    float* copy;             // U, 32 columns at a time: [block][padded rows][32]
+    float* part;             // per Gram item: partial sum, [padded rows]^2
+    int32_t* part_exp;       // per Gram item: its values are U 2^-exp
+    float* prod;             // per matrix: the product of the Q_k, [padded rows]^2
+    int32_t* exp;            // per matrix: prod is for U 2^-exp
+    double eps;
+    int32_t n_steps;
+    float a[DPG_MAX_NS_STEPS], b[DPG_MAX_NS_STEPS], c[DPG_MAX_NS_STEPS];
+};
+
+constexpr int kGramThreads = 256;
+
+// 2^k for any k that occurs here, exactly
+__device__ __forceinline__ float pow2(int k) {
+    return k < -126 ? 0.0f : __int_as_float((k > 127 ? 127 : k) + 127 << 23);
+}
+
+// ---------------------------------------------------------------------------
+// Partial Gram matrices.  One CTA sums the outer products of up to `width`
+// columns, 32 at a time through shared memory; each thread holds a T x T block
+// of the sum (T = padded rows / 16).  U's range may exceed what fp32 squares
+// can hold, so columns are scaled by the power of two of the largest value so
+// far, and the sum with them when that grows.
+// ---------------------------------------------------------------------------
+template <int MP, bool F32>
+__device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d, const SmallItem& it, float* sm) {
+    constexpr int T = MP / 16, P = MP + 4, kPer = MP * 32 / kGramThreads;
+    float* tile = sm;                    // [32][P]
+    float* red = sm + 32 * P;            // 8 + 1
+    const int tx = int(threadIdx.x) & 15, ty = int(threadIdx.x) >> 4;
+    float acc[T][T];
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int j = 0; j < T; ++j) acc[i][j] = 0.0f;
+    int e = -1000;
+    float x[kPer];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int q = int(threadIdx.x) + i * kGramThreads;
+            const int r = d.tall ? q % MP : q >> 5, c = c0 + (d.tall ? q / MP : q & 31);
+            float v = 0.0f;
+            if (r < d.m && c < d.n) {
+                const int64_t at = d.off + (d.tall ? int64_t(c) * d.m + r : int64_t(r) * d.n + c);
+                v = F32 ? __ldg(static_cast<const float*>(a.update) + at)
+                        : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + at)) << 16);
+            }
+            x[i] = v;
+        }
+    };
+    fetch(it.c0);
+    for (int c0 = it.c0; c0 < it.c1; c0 += 32) {
+        float top = 0.0f;
+        float* copy = a.copy + d.copy + int64_t(c0 >> 5) * (MP * 32);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int q = int(threadIdx.x) + i * kGramThreads;
+            const int r = d.tall ? q % MP : q >> 5, c = d.tall ? q / MP : q & 31;
+            copy[r * 32 + c] = x[i];
+            top = fmaxf(top, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+        __syncthreads();                 // also: the tile before is used up
+#pragma unroll
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+        // |u| < 2^(te + 1); an infinity keeps its own scale and poisons the sum
+        const int te = top > 0.0f && top < 3.0e38f ? ilogbf(top) : (top > 0.0f ? 127 : -1000);
+        if (te > e) {
+            const float k = pow2(2 * (e - te));
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int j = 0; j < T; ++j) acc[i][j] *= k;
+            e = te;
+        }
+        // 2^-e in two factors: either may leave fp32's range alone
+        const float s0 = e > -1000 ? pow2(-(e >> 1)) : 0.0f, s1 = e > -1000 ? pow2(-(e - (e >> 1))) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int q = int(threadIdx.x) + i * kGramThreads;
+            const int r = d.tall ? q % MP : q >> 5, c = d.tall ? q / MP : q & 31;
+            tile[c * P + r] = x[i] * s0 * s1;
+        }
+        __syncthreads();
+        if (c0 + 32 < it.c1) fetch(c0 + 32);
+#pragma unroll 4
+        for (int k = 0; k < 32; ++k) {
+            float u[T], v[T];
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+                u[i] = tile[k * P + ty * T + i];
+                v[i] = tile[k * P + tx * T + i];
+            }
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int j = 0; j < T; ++j) acc[i][j] = fmaf(u[i], v[j], acc[i][j]);
+        }
+    }
+    float* out = a.part + it.part;
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int j = 0; j < T; ++j) out[(ty * T + i) * MP + tx * T + j] = acc[i][j];
+    if (threadIdx.x == 0) a.part_exp[it.index] = e;
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kGramThreads) k_gram_sum(const __grid_constant__ GramArgs a,
+                                                          const SmallItem* items) {
+    __shared__ __align__(16) float sm[32 * (kSmallSide + 4) + 16];
+    pdl_enter();
+    const SmallItem it = items[blockIdx.x];
+    const SmallDesc d = a.mats[it.mat];
+    switch (d.mp) {
+        case 16: return gram_item<16, F32>(a, d, it, sm);
+        case 32: return gram_item<32, F32>(a, d, it, sm);
+        case 64: return gram_item<64, F32>(a, d, it, sm);
+        default: return gram_item<128, F32>(a, d, it, sm);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The steps on the Gram matrix.  A cluster of MP / 16 CTAs per matrix; each
+// holds A and Q whole and owns 16 rows of every product, which it writes into
+// the other CTAs' copies (distributed shared memory).  Per step
+//     Q = aI + bA + cA^2,   P <- P Q,   A <- (A Q) Q
+// with two cluster barriers: after Q's rows are everywhere, and after A's.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void gram_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 rows times MP x MP, K split over the CTA's two halves: threads 0..127
+// sum the first half of K and, after adding the others' half, return the sums
+// of rows 2 ty, 2 ty + 1 and of the columns below; threads 128..255 help.
+template <int MP>
+struct RowProduct {
+    static constexpr int kCols = MP / 16;
+    float v[2][kCols];
+    // column of v[.][j] for thread tx
+    __device__ __forceinline__ static int col(int tx, int j) {
+        return kCols >= 4 ? (j >> 2) * 64 + tx * 4 + (j & 3) : tx * kCols + j;
+    }
+    __device__ __forceinline__ void run(const float* left, const float* right, float* half_sum) {
+        const int t = int(threadIdx.x) & 127, tx = t & 15, ty = t >> 4, part = int(threadIdx.x) >> 7;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) v[0][j] = v[1][j] = 0.0f;
+#pragma unroll 2
+        for (int k = part * (MP / 2); k < (part + 1) * (MP / 2); k += 4) {
+            const float4 l0 = *reinterpret_cast<const float4*>(left + (2 * ty) * MP + k);
+            const float4 l1 = *reinterpret_cast<const float4*>(left + (2 * ty + 1) * MP + k);
+            const float p0[4] = {l0.x, l0.y, l0.z, l0.w}, p1[4] = {l1.x, l1.y, l1.z, l1.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float r[kCols];
+                if constexpr (kCols >= 4) {
+#pragma unroll
+                    for (int g = 0; g < kCols / 4; ++g) {
+                        const float4 q = *reinterpret_cast<const float4*>(right + (k + u) * MP + g * 64 + tx * 4);
+                        r[4 * g] = q.x;
+                        r[4 * g + 1] = q.y;
+                        r[4 * g + 2] = q.z;
+                        r[4 * g + 3] = q.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) r[j] = right[(k + u) * MP + tx * kCols + j];
+                }
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    v[0][j] = fmaf(p0[u], r[j], v[0][j]);
+                    v[1][j] = fmaf(p1[u], r[j], v[1][j]);
+                }
+            }
+        }
+        float* h = half_sum + t;
+        if (part == 1) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+                h[(2 * j) * 128] = v[0][j];
+                h[(2 * j + 1) * 128] = v[1][j];
+            }
+        }
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+                v[0][j] += h[(2 * j) * 128];
+                v[1][j] += h[(2 * j + 1) * 128];
+            }
+        }
+    }
+};
+
+template <int MP>
+__global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_constant__ GramArgs a,
+                                                            const int32_t* which) {
+    constexpr int C = MP / 16;           // CTAs of the cluster
+    extern __shared__ __align__(16) float gram_sm[];
+    float* A = gram_sm;                  // [MP][MP]
+    float* Q = A + MP * MP;              // [MP][MP]
+    float* P = Q + MP * MP;              // [16][MP], own rows
+    float* S = P + 16 * MP;              // [16][MP], own rows: A Q
+    float* half_sum = S + 16 * MP;       // 128 x 2 MP / 16
+    __shared__ double den_sh;
+    __shared__ float scale_sh;
+    pdl_enter();
+    const int rank = int(blockIdx.x) % C, mat = which[blockIdx.x / C];
+    const SmallDesc d = a.mats[mat];
+    const int t = int(threadIdx.x), row0 = rank * 16;
+
+    // writes v to the own rows (row, col) of `dst` in every CTA of the cluster
+    auto spread = [&](float* dst, int row, int col, float v) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst + (row0 + row) * MP + col));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(c));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(to), "f"(v) : "memory");
+        }
+    };
+
+    // the partial sums under one scale, own rows
+    int e = -1000;
+    for (int k = 0; k < d.n_items; ++k) e = max(e, __ldg(a.part_exp + d.item0 + k));
+    gram_cluster_sync();                 // every CTA has started: its memory may be written
+    for (int q = t; q < 16 * MP; q += kGramThreads) {
+        const float* p = a.part + d.part + row0 * MP + q;
+        float s = 0.0f;
+        for (int k = 0; k < d.n_items; k += 8) {
+            float v[8];
+            int pe[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const bool in = k + u < d.n_items;
+                v[u] = in ? __ldg(p + int64_t(k + u) * MP * MP) : 0.0f;
+                pe[u] = in ? __ldg(a.part_exp + d.item0 + k + u) : e;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s = fmaf(v[u], pow2(2 * (pe[u] - e)), s);
+        }
+        spread(A, q / MP, q % MP, s);
+    }
+    gram_cluster_sync();
+    if (t < 32) {                        // trace: the squared norm of U 2^-e
+        double s = 0.0;
+        for (int r = t; r < MP; r += 32) s += double(A[r * MP + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (t == 0) {
+            // divisor of U 2^-e: max(norm, eps) 2^-e
+            double den = sqrt(s);
+            if (e > -1000) den = fmax(den, scalbn(a.eps, -e));
+            const bool ok = s < 3.0e38;  // a NaN or an infinity in the matrix: NaN everywhere
+            if (!(den > 0.0)) den = 1.0; // a zero matrix stays zero
+            den_sh = ok ? den : __longlong_as_double(0x7FF8000000000000ll);
+            scale_sh = float(1.0 / (den_sh * den_sh));
+        }
+    }
+    __syncthreads();
+
+    // step 0 takes A as scale * (the sum in memory)
+    float scale = scale_sh;
+    const int hx = t & 15, hy = (t & 127) >> 4;
+    RowProduct<MP> y;
+    constexpr int kCols = RowProduct<MP>::kCols;
+    for (int step = 0; step < a.n_steps; ++step) {
+        y.run(A + row0 * MP, A, half_sum);
+        const float ca = a.a[step], cb = a.b[step] * scale, cc = a.c[step] * scale * scale;
+        if (t < 128) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    const int row = 2 * hy + i, col = y.col(hx, j);
+                    float q = fmaf(cc, y.v[i][j], cb * A[(row0 + row) * MP + col]);
+                    if (col == row0 + row) q += ca;
+                    spread(Q, row, col, q);
+                }
+        }
+        gram_cluster_sync();
+        const bool last = step + 1 == a.n_steps;
+        if (step == 0) {
+            for (int q = t; q < 16 * MP; q += kGramThreads) P[q] = Q[row0 * MP + q];
+        } else {
+            y.run(P, Q, half_sum);       // (its barrier: every thread has read P)
+            if (t < 128) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) P[(2 * hy + i) * MP + y.col(hx, j)] = y.v[i][j];
+            }
+        }
+        if (last) break;
+        __syncthreads();                 // half_sum is free again
+        y.run(A + row0 * MP, Q, half_sum);
+        if (t < 128) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) S[(2 * hy + i) * MP + y.col(hx, j)] = y.v[i][j] * scale;
+        }
+        __syncthreads();
+        y.run(S, Q, half_sum);
+        if (t < 128) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) spread(A, 2 * hy + i, y.col(hx, j), y.v[i][j]);
+        }
+        scale = 1.0f;
+        gram_cluster_sync();
+    }
+    __syncthreads();
+    const float inv = float(1.0 / den_sh);
+    for (int q = t; q < 16 * MP; q += kGramThreads) a.prod[d.prod + row0 * MP + q] = P[q] * inv;
+    if (rank == 0 && t == 0) a.exp[mat] = e;
+    gram_cluster_sync();                 // no CTA leaves while others write to it
+}
+
+constexpr int gram_steps_smem(int mp) { return (2 * mp * mp + 32 * mp + 256 * (mp / 16)) * 4; }
+
+// ---------------------------------------------------------------------------
+// O = P U, 64 columns per CTA: a thread holds MP / 16 rows by 4 columns.
+// ---------------------------------------------------------------------------
+constexpr int kProdCols = 64;
+constexpr int gram_apply_smem(int mp) { return (mp * (mp + 4) + mp * kProdCols) * 4; }
+
+template <int MP>
+__device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d, const SmallItem& it, float* sm) {
+    constexpr int T = MP / 16, PP = MP + 4;
+    float* P = sm;                       // [MP][PP]
+    float* X = sm + MP * PP;             // [MP][64]
+    const int t = int(threadIdx.x), tx = t & 15, ty = t >> 4;
+    for (int q = t; q < MP * MP / 4; q += kGramThreads)
+        *reinterpret_cast<float4*>(P + (q / (MP / 4)) * PP + (q % (MP / 4)) * 4) =
+            __ldg(reinterpret_cast<const float4*>(a.prod + d.prod) + q);
+    const int e = a.exp[it.mat];
+    const float s0 = e > -1000 ? pow2(-(e >> 1)) : 0.0f, s1 = e > -1000 ? pow2(-(e - (e >> 1))) : 0.0f;
+    for (int q = t; q < MP * kProdCols; q += kGramThreads) {
+        const int blk = q / (MP * 32), r = (q / 32) % MP, c = q & 31;
+        const bool in = it.c0 + blk * 32 < d.n;   // the copy holds whole blocks of 32 columns
+        X[r * kProdCols + blk * 32 + c] =
+            in ? __ldg(a.copy + d.copy + int64_t((it.c0 >> 5) + blk) * (MP * 32) + r * 32 + c) * s0 * s1 : 0.0f;
+    }
+    __syncthreads();
+    float acc[T][4];
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    const int kend = (d.m + 3) & ~3;
+#pragma unroll 1
+    for (int k = 0; k < kend; k += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(X + (k + u) * kProdCols + tx * 4);
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            const float4 p4 = *reinterpret_cast<const float4*>(P + (ty * T + i) * PP + k);
+            const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                acc[i][0] = fmaf(p[u], x[u].x, acc[i][0]);
+                acc[i][1] = fmaf(p[u], x[u].y, acc[i][1]);
+                acc[i][2] = fmaf(p[u], x[u].z, acc[i][2]);
+                acc[i][3] = fmaf(p[u], x[u].w, acc[i][3]);
+            }
+        }
+    }
+    const bool vec = !d.tall && ((d.off | d.n) & 3) == 0;
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        const int r = ty * T + i, c = it.c0 + tx * 4;
+        if (r >= d.m) continue;
+        if (vec && c < d.n) {
+            const __nv_bfloat162 u = __floats2bfloat162_rn(acc[i][0], acc[i][1]);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i][2], acc[i][3]);
+            *reinterpret_cast<uint2*>(a.out + d.off + int64_t(r) * d.n + c) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < d.n)
+                    a.out[d.off + (d.tall ? int64_t(c + j) * d.m + r : int64_t(r) * d.n + c + j)] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][j]));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kGramThreads) k_gram_apply(const __grid_constant__ GramArgs a,
+                                                            const SmallItem* items) {
+    extern __shared__ __align__(16) float gram_sm[];
+    pdl_enter();
+    const SmallItem it = items[blockIdx.x];
+    const SmallDesc d = a.mats[it.mat];
+    switch (d.mp) {
+        case 16: return apply_item<16>(a, d, it, gram_sm);
+        case 32: return apply_item<32>(a, d, it, gram_sm);
+        case 64: return apply_item<64>(a, d, it, gram_sm);
+        default: return apply_item<128>(a, d, it, gram_sm);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+int gram_prepare() {
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_steps<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gram_steps_smem(64)));
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_steps<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gram_steps_smem(128)));
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_apply, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gram_apply_smem(kSmallSide)));
+    return DPG_OK;
+}
+
+template <int MP>
+static int launch_steps(const GramArgs& a, const int32_t* which, int n, cudaStream_t s, const char* who) {
+    if (n == 0) return DPG_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(n) * (MP / 16));
+    cfg.blockDim = dim3(kGramThreads);
+    cfg.dynamicSmemBytes = gram_steps_smem(MP);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = MP / 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = t_programmatic ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_gram_steps<MP>, a, which);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    }
+    return after_launch(who);
+}
+
+static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_hparams* hp, void* out) {
+    GramArgs a{};
+    a.mats = m.d_small;
+    a.update = update;
+    a.out = static_cast<uint16_t*>(out);
+    a.copy = reinterpret_cast<float*>(m.ws + m.o_small_copy);
+    a.part = reinterpret_cast<float*>(m.ws + m.o_small_part);
+    a.part_exp = reinterpret_cast<int32_t*>(m.ws + m.o_small_exp);
+    a.exp = a.part_exp + m.gram_items.size();
+    a.prod = reinterpret_cast<float*>(m.ws + m.o_small_prod);
+    a.eps = hp->eps;
+    a.n_steps = hp->n_steps;
+    for (int k = 0; k < hp->n_steps; ++k) {
+        a.a[k] = float(hp->coeffs[k][0]);
+        a.b[k] = float(hp->coeffs[k][1]);
+        a.c[k] = float(hp->coeffs[k][2]);
+    }
+    return a;
+}
+
+int gram_read(const Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
+              void* out, cudaStream_t s, const char* who) {
+    if (m.small.empty()) return DPG_OK;
+    return launch_k(update_dtype == DPG_F32 ? k_gram_sum<true> : k_gram_sum<false>, unsigned(m.gram_items.size()),
+                    kGramThreads, s, who, gram_args(m, update, hp, out),
+                    static_cast<const SmallItem*>(m.d_gram_items));
+}
+
+int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, void* out, cudaStream_t s,
+                const char* who) {
+    if (m.small.empty()) return DPG_OK;
+    const GramArgs a = gram_args(m, update, hp, out);
+    const int32_t* w = m.d_small_order;
+    int st = launch_steps<16>(a, w, m.small_count[0], s, who);
+    w += m.small_count[0];
+    if (st == DPG_OK) st = launch_steps<32>(a, w, m.small_count[1], s, who);
+    w += m.small_count[1];
+    if (st == DPG_OK) st = launch_steps<64>(a, w, m.small_count[2], s, who);
+    w += m.small_count[2];
+    if (st == DPG_OK) st = launch_steps<128>(a, w, m.small_count[3], s, who);
+    if (st != DPG_OK) return st;
+    const int mp = m.small_count[3] ? 128 : m.small_count[2] ? 64 : m.small_count[1] ? 32 : 16;
+    return launch_k(k_gram_apply, unsigned(m.prod_items.size()), kGramThreads, size_t(gram_apply_smem(mp)), s, who,
+                    a, static_cast<const SmallItem*>(m.d_prod_items));
+}
+
+}  // namespace dpg

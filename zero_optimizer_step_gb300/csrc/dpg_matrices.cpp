@@ -12,7 +12,40 @@
 
 namespace dpg {
 
+constexpr int64_t kMaxMatrices = 1 << 20;   // of one object
+
 static int64_t ceil_div(int64_t x, int64_t d) { return (x + d - 1) / d; }
+// Items of a small matrix: Gram sums over about 32 groups of whole 32-column
+// blocks (every further group is a partial sum to write and to read again; very
+// long matrices get one per 1024 columns, up to 128), products of 64 columns.
+static void small_items(Matrices& M, const MatDesc& d) {
+    SmallDesc s{};
+    s.off = d.off;
+    s.m = d.m;
+    s.n = d.n;
+    s.tall = d.tall;
+    s.mp = d.m <= 16 ? 16 : d.m <= 32 ? 32 : d.m <= 64 ? 64 : 128;
+    const int32_t mat = int32_t(M.small.size());
+    const int64_t blocks = ceil_div(d.n, 32);
+    s.copy = M.n_small_copy;
+    M.n_small_copy += blocks * 32 * s.mp;
+    s.prod = M.n_small_prod;
+    M.n_small_prod += int64_t(s.mp) * s.mp;
+    const int64_t groups = std::min<int64_t>(blocks, std::max<int64_t>(32, std::min<int64_t>(128, d.n / 1024)));
+    const int64_t width = ceil_div(blocks, groups) * 32;
+    s.part = M.n_small_part;
+    s.item0 = int32_t(M.gram_items.size());
+    for (int64_t c = 0; c < d.n; c += width) {
+        M.gram_items.push_back({mat, int32_t(c), int32_t(std::min<int64_t>(c + width, d.n)),
+                                int32_t(M.gram_items.size()), M.n_small_part});
+        M.n_small_part += int64_t(s.mp) * s.mp;
+    }
+    s.n_items = int32_t(M.gram_items.size()) - s.item0;
+    for (int64_t c = 0; c < d.n; c += 64)
+        M.prod_items.push_back({mat, int32_t(c), int32_t(std::min<int64_t>(c + 64, d.n)), 0, 0});
+    M.small.push_back(s);
+}
+
 static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 
 // Lays the matrices out; false when an index would leave its type.
@@ -22,6 +55,9 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
     M.param_offset = p.param_offset;
     M.numels = p.numels;
     M.scales.assign(2 * size_t(p.n_params), 1.0);
+    int64_t count = 0;
+    for (int32_t q = 0; q < p.n_params; ++q)
+        if ((count += p.numels[q] / (rows[q] * cols[q])) > kMaxMatrices) return false;
     for (int32_t q = p.n_params - 1; q >= 0; --q) {   // flat order
         const double r = double(rows[q]), c = double(cols[q]);
         M.scales[2 * size_t(q)] = std::sqrt(std::max(1.0, r / c));
@@ -39,6 +75,11 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.tall = rows[q] > cols[q];
             d.m = int32_t(std::min(rows[q], cols[q]));
             d.n = int32_t(std::max(rows[q], cols[q]));
+            ++M.n_matrices;
+            if (d.m <= kSmallSide) {
+                small_items(M, d);
+                continue;
+            }
             d.kn = int32_t(ceil_div(d.n, kBlkCols));
             d.km = int32_t(ceil_div(d.m, kBlkCols));
             const int64_t tm = ceil_div(d.m, kOrthoTile), tn = ceil_div(d.n, kOrthoTile);
@@ -89,8 +130,23 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
     o += up256(int64_t(M.mats.size()) * 3 * int64_t(sizeof(int32_t)));
     M.o_status = o;
     o += 256;
+    for (int c = 0; c < 4; ++c)
+        for (size_t k = 0; k < M.small.size(); ++k)
+            if (M.small[k].mp == 16 << c) {
+                M.small_order.push_back(int32_t(k));
+                ++M.small_count[c];
+            }
+    M.o_small_copy = o;
+    o += up256(M.n_small_copy * int64_t(sizeof(float)));
+    M.o_small_part = o;
+    o += up256(M.n_small_part * int64_t(sizeof(float)));
+    M.o_small_prod = o;
+    o += up256(M.n_small_prod * int64_t(sizeof(float)));
+    M.o_small_exp = o;   // per Gram item, then per matrix
+    o += up256(int64_t(M.gram_items.size() + M.small.size()) * int64_t(sizeof(int32_t)));
     M.workspace_bytes = o;
-    return M.norm_items.size() < 0x7FFFFFFF && M.conv_items.size() < 0x7FFFFFFF &&
+    return M.gram_items.size() < 0x7FFFFFFF && M.prod_items.size() < 0x7FFFFFFF &&
+           M.small.size() < 0x7FFFFFF && M.norm_items.size() < 0x7FFFFFFF && M.conv_items.size() < 0x7FFFFFFF &&
            M.apply_items.size() < 0x7FFFFFFF;
 }
 
@@ -276,7 +332,7 @@ void dpg_matrices_destroy(dpg_matrices_t* mats) {
 int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* workspace_bytes) {
     dpg::clear_error();
     if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_matrices_info: mats is NULL");
-    if (n_matrices) *n_matrices = int32_t(mats->m.mats.size());
+    if (n_matrices) *n_matrices = mats->m.n_matrices;
     if (workspace_bytes) *workspace_bytes = mats->m.workspace_bytes;
     return DPG_OK;
 }

@@ -234,7 +234,7 @@ int dpg_orthogonalize(dpg_matrices_t* mats, const void* update, int32_t update_d
     dpg::OrthoStep steps[DPG_MAX_NS_STEPS];
     int st = dpg::ortho_steps(hp, steps, "dpg_orthogonalize");
     if (st != DPG_OK) return st;
-    if (mats->m.mats.empty()) return DPG_OK;
+    if (mats->m.n_matrices == 0) return DPG_OK;
     st = dpg::check_flat(update, update_dtype, "update", "dpg_orthogonalize");
     if (st == DPG_OK) st = dpg::check_flat(ortho_bf16, DPG_BF16, "ortho_bf16", "dpg_orthogonalize");
     if (st == DPG_OK) st = dpg::upload_matrices(mats->m);
@@ -278,7 +278,7 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
     if (st != DPG_OK) return st;
     dpg::ApplyArgs b{};
     st = dpg::apply_args(m, update, hp, master, param_views, n_views, b, who);
-    if (st != DPG_OK || m.mats.empty()) return st;
+    if (st != DPG_OK || m.n_matrices == 0) return st;
     st = dpg::upload_matrices(m);
     if (st != DPG_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

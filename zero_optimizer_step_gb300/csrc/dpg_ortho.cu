@@ -1076,6 +1076,10 @@ int upload_matrices(Matrices& m) {
         DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps, &cfg));
         if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no CTA pair fits this device");
     }
+    if (!m.small.empty()) {
+        const int st = gram_prepare();
+        if (st != DPG_OK) return st;
+    }
     try {
         lay_queue(m, clusters);
     } catch (const std::exception&) {
@@ -1084,6 +1088,10 @@ int upload_matrices(Matrices& m) {
     const size_t bytes = round256(m.mats.size() * sizeof(MatDesc)) +
                          round256(m.queue.size() * sizeof(OrthoTile)) +
                          round256(m.queue_first.size() * sizeof(int32_t)) +
+                         round256(m.small.size() * sizeof(SmallDesc)) +
+                         round256(m.gram_items.size() * sizeof(SmallItem)) +
+                         round256(m.prod_items.size() * sizeof(SmallItem)) +
+                         round256(m.small_order.size() * sizeof(int32_t)) +
                          round256(m.norm_items.size() * sizeof(NormItem)) +
                          round256(m.conv_items.size() * sizeof(ConvItem)) +
                          round256(m.apply_items.size() * sizeof(ApplyItem)) +
@@ -1096,13 +1104,17 @@ int upload_matrices(Matrices& m) {
     if (e == cudaSuccess) e = put(t, &at, m.mats, &m.d_mats);
     if (e == cudaSuccess) e = put(t, &at, m.queue, &m.d_queue);
     if (e == cudaSuccess) e = put(t, &at, m.queue_first, &m.d_queue_first);
+    if (e == cudaSuccess) e = put(t, &at, m.small, &m.d_small);
+    if (e == cudaSuccess) e = put(t, &at, m.gram_items, &m.d_gram_items);
+    if (e == cudaSuccess) e = put(t, &at, m.prod_items, &m.d_prod_items);
+    if (e == cudaSuccess) e = put(t, &at, m.small_order, &m.d_small_order);
     if (e == cudaSuccess) e = put(t, &at, m.norm_items, &m.d_norm_items);
     if (e == cudaSuccess) e = put(t, &at, m.conv_items, &m.d_conv_items);
     if (e == cudaSuccess) e = put(t, &at, m.apply_items, &m.d_apply_items);
     if (e == cudaSuccess) e = put(t, &at, m.scales, &m.d_scales);
     // arrival counters and the status word start at zero
     if (e == cudaSuccess)
-        e = cudaMemset(static_cast<unsigned char*>(ws) + m.o_count, 0, size_t(m.workspace_bytes - m.o_count));
+        e = cudaMemset(static_cast<unsigned char*>(ws) + m.o_count, 0, size_t(m.o_status + 256 - m.o_count));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     int st = DPG_OK;
     if (e != cudaSuccess) {
@@ -1157,7 +1169,12 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
                  void* out, void* stream, const char* who) {
     OrthoArgs a{};
     int st = ortho_steps(hp, a.st, who);
-    if (st != DPG_OK || m.mats.empty()) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Everything that reads `update` comes before anything that writes `out`,
+    // which may share its memory.
+    if (st == DPG_OK) st = gram_read(m, update, update_dtype, hp, out, s, who);
+    if (st != DPG_OK) return st;
+    if (m.mats.empty()) return gram_finish(m, update, hp, out, s, who);
     a.mats = m.d_mats;
     a.ws = m.ws;
     a.diag_a = reinterpret_cast<float*>(m.ws + m.o_diag);
@@ -1176,12 +1193,12 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.n_steps = hp->n_steps;
     a.eps = hp->eps;
     a.out = static_cast<uint16_t*>(out);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_k(a.f32 ? k_ortho_norm<true> : k_ortho_norm<false>, unsigned(m.norm_items.size()), kNormThreads,
                   s, who, a, static_cast<const NormItem*>(m.d_norm_items));
     if (st == DPG_OK)
         st = launch_k(a.f32 ? k_ortho_load<true> : k_ortho_load<false>, unsigned(m.conv_items.size()), 256,
                       a.f32 ? 2 * kLoadSmem : kLoadSmem, s, who, a, static_cast<const ConvItem*>(m.d_conv_items));
+    if (st == DPG_OK) st = gram_finish(m, update, hp, out, s, who);
     if (st != DPG_OK) return st;
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);

@@ -4,6 +4,8 @@
 // (dpg_muon.cu).
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <cstdint>
 #include <mutex>
 #include <vector>
@@ -48,6 +50,22 @@ struct OrthoTile {
     int32_t prod;
 };
 
+// Matrices whose shorter side is at most kSmallSide take the steps on their
+// Gram matrices (dpg_gram.cu) and none of the tiles.
+constexpr int kSmallSide = 128;
+struct SmallDesc {
+    int64_t off;          // first element in the flat buffer
+    int32_t m, n, tall;   // as in MatDesc
+    int32_t mp;           // m padded to 16, 32, 64 or 128
+    int64_t copy, part, prod;   // first floats of its copy, partial Gram matrices, product
+    int32_t item0, n_items;     // its Gram items
+};
+// columns [c0, c1) of a small matrix
+struct SmallItem {
+    int32_t mat, c0, c1, index;
+    int64_t part;
+};
+
 // Items of the norm and conversion passes and of the weight update.
 struct NormItem {
     int32_t mat, count;   // elements [start, start + count) of the matrix
@@ -85,14 +103,21 @@ struct Matrices {
     std::vector<OrthoTile> queue;      // tiles of a step, pair after pair (see lay_queue)
     std::vector<int32_t> queue_first;  // pairs + 1
     int32_t pairs = 0;
+    std::vector<SmallDesc> small;
+    std::vector<SmallItem> gram_items, prod_items;
+    std::vector<int32_t> small_order;  // small matrices by padded side
+    int32_t small_count[4] = {0, 0, 0, 0};
+    int32_t n_matrices = 0;
     std::vector<NormItem> norm_items;
     std::vector<ConvItem> conv_items;
     std::vector<ApplyItem> apply_items;
     std::vector<double> scales;        // 2 per parameter: spectral, rms
     int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0;
+    int64_t n_small_copy = 0, n_small_part = 0, n_small_prod = 0;   // floats
     int64_t workspace_bytes = 0;
     // byte offsets in the workspace
     int64_t o_diag = 0, o_rowsq = 0, o_part = 0, o_scal = 0, o_count = 0, o_done = 0, o_status = 0;
+    int64_t o_small_copy = 0, o_small_part = 0, o_small_exp = 0, o_small_prod = 0;
 
     std::mutex mu;
     int device = -1;
@@ -101,6 +126,9 @@ struct Matrices {
     MatDesc* d_mats = nullptr;
     OrthoTile* d_queue = nullptr;
     int32_t* d_queue_first = nullptr;
+    SmallDesc* d_small = nullptr;
+    SmallItem *d_gram_items = nullptr, *d_prod_items = nullptr;
+    int32_t* d_small_order = nullptr;
     NormItem* d_norm_items = nullptr;
     ConvItem* d_conv_items = nullptr;
     ApplyItem* d_apply_items = nullptr;
@@ -118,6 +146,14 @@ int check_matrices(Matrices& m, void* stream);
 int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who);
 int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
                  void* out, void* stream, const char* who);
+
+// The small matrices' part (dpg_gram.cu): gram_read is the only one that reads
+// `update`, gram_finish the only one that writes `out`.
+int gram_prepare();
+int gram_read(const Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
+              void* out, cudaStream_t s, const char* who);
+int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, void* out, cudaStream_t s,
+                const char* who);
 
 }  // namespace dpg
 
