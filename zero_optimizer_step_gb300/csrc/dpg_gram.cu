@@ -61,6 +61,9 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
     float* tile = sm;                    // [32][P]
     float* red = sm + 32 * P;            // 8 + 1
     const int tx = int(threadIdx.x) & 15, ty = int(threadIdx.x) >> 4;
+    // a thread's columns: four neighbours in each 64, so that the lanes' reads
+    // are contiguous
+    auto col = [&](int j) { return T >= 4 ? (j >> 2) * 64 + tx * 4 + (j & 3) : tx * T + j; };
     float acc[T][T];
 #pragma unroll
     for (int i = 0; i < T; ++i)
@@ -68,18 +71,25 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
         for (int j = 0; j < T; ++j) acc[i][j] = 0.0f;
     int e = -1000;
     float x[kPer];
+    // all loads before any use (a load under its own branch would be waited
+    // for there, one memory latency per value): out of range ones read U's
+    // first element
     auto fetch = [&](int c0) {
+        uint32_t raw[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int q = int(threadIdx.x) + i * kGramThreads;
             const int r = d.tall ? q % MP : q >> 5, c = c0 + (d.tall ? q / MP : q & 31);
-            float v = 0.0f;
-            if (r < d.m && c < d.n) {
-                const int64_t at = d.off + (d.tall ? int64_t(c) * d.m + r : int64_t(r) * d.n + c);
-                v = F32 ? __ldg(static_cast<const float*>(a.update) + at)
-                        : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + at)) << 16);
-            }
-            x[i] = v;
+            const int64_t at = d.off + (r < d.m && c < d.n
+                                            ? (d.tall ? int64_t(c) * d.m + r : int64_t(r) * d.n + c) : 0);
+            raw[i] = F32 ? __ldg(static_cast<const uint32_t*>(a.update) + at)
+                         : uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + at)) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int q = int(threadIdx.x) + i * kGramThreads;
+            const int r = d.tall ? q % MP : q >> 5, c = c0 + (d.tall ? q / MP : q & 31);
+            x[i] = r < d.m && c < d.n ? __uint_as_float(raw[i]) : 0.0f;
         }
     };
     fetch(it.c0);
@@ -125,7 +135,7 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 u[i] = tile[k * P + ty * T + i];
-                v[i] = tile[k * P + tx * T + i];
+                v[i] = tile[k * P + col(i)];
             }
 #pragma unroll
             for (int i = 0; i < T; ++i)
@@ -137,7 +147,7 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
 #pragma unroll
     for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int j = 0; j < T; ++j) out[(ty * T + i) * MP + tx * T + j] = acc[i][j];
+        for (int j = 0; j < T; ++j) out[(ty * T + i) * MP + col(j)] = acc[i][j];
     if (threadIdx.x == 0) a.part_exp[it.index] = e;
 }
 
@@ -182,7 +192,7 @@ struct RowProduct {
         const int t = int(threadIdx.x) & 127, tx = t & 15, ty = t >> 4, part = int(threadIdx.x) >> 7;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) v[0][j] = v[1][j] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
         for (int k = part * (MP / 2); k < (part + 1) * (MP / 2); k += 4) {
             const float4 l0 = *reinterpret_cast<const float4*>(left + (2 * ty) * MP + k);
             const float4 l1 = *reinterpret_cast<const float4*>(left + (2 * ty + 1) * MP + k);
@@ -229,6 +239,11 @@ struct RowProduct {
     }
 };
 
+template <int W>
+struct Width {
+    static constexpr int value = W;
+};
+
 template <int MP>
 __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_constant__ GramArgs a,
                                                             const int32_t* which) {
@@ -246,14 +261,23 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
     const SmallDesc d = a.mats[mat];
     const int t = int(threadIdx.x), row0 = rank * 16;
 
-    // writes v to the own rows (row, col) of `dst` in every CTA of the cluster
-    auto spread = [&](float* dst, int row, int col, float v) {
+    // writes W neighbouring values to the own rows (row, col ..) of `dst` in
+    // every CTA of the cluster: 16 bytes at a time where there are as many (one
+    // value at a time, the writes took longer than the products)
+    auto spread = [&](float* dst, int row, int col, const float* v, auto width) {
+        constexpr int W = decltype(width)::value;
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst + (row0 + row) * MP + col));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             uint32_t to;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(c));
-            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(to), "f"(v) : "memory");
+            if constexpr (W == 4)
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};"
+                             :: "r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+            else if constexpr (W == 2)
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" :: "r"(to), "f"(v[0]), "f"(v[1]) : "memory");
+            else
+                asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(to), "f"(v[0]) : "memory");
         }
     };
 
@@ -261,22 +285,30 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
     int e = -1000;
     for (int k = 0; k < d.n_items; ++k) e = max(e, __ldg(a.part_exp + d.item0 + k));
     gram_cluster_sync();                 // every CTA has started: its memory may be written
-    for (int q = t; q < 16 * MP; q += kGramThreads) {
-        const float* p = a.part + d.part + row0 * MP + q;
-        float s = 0.0f;
-        for (int k = 0; k < d.n_items; k += 8) {
-            float v[8];
-            int pe[8];
+    for (int q = t; q < 4 * MP; q += kGramThreads) {
+        const float4* p = reinterpret_cast<const float4*>(a.part + d.part + row0 * MP) + q;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < d.n_items; k += 16) {
+            float4 v[16];
+            int pe[16];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const bool in = k + u < d.n_items;
-                v[u] = in ? __ldg(p + int64_t(k + u) * MP * MP) : 0.0f;
-                pe[u] = in ? __ldg(a.part_exp + d.item0 + k + u) : e;
+            for (int u = 0; u < 16; ++u) {
+                const int it = min(k + u, d.n_items - 1);
+                v[u] = __ldg(p + int64_t(it) * (MP * MP / 4));
+                pe[u] = __ldg(a.part_exp + d.item0 + it);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s = fmaf(v[u], pow2(2 * (pe[u] - e)), s);
+            for (int u = 0; u < 16; ++u) {
+                const float w = k + u < d.n_items ? pow2(2 * (pe[u] - e)) : 0.0f;
+                if (k + u < d.n_items) {
+                    s[0] = fmaf(v[u].x, w, s[0]);
+                    s[1] = fmaf(v[u].y, w, s[1]);
+                    s[2] = fmaf(v[u].z, w, s[2]);
+                    s[3] = fmaf(v[u].w, w, s[3]);
+                }
+            }
         }
-        spread(A, q / MP, q % MP, s);
+        spread(A, q / (MP / 4), (q % (MP / 4)) * 4, s, Width<4>());
     }
     gram_cluster_sync();
     if (t < 32) {                        // trace: the squared norm of U 2^-e
@@ -300,7 +332,7 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
     float scale = scale_sh;
     const int hx = t & 15, hy = (t & 127) >> 4;
     RowProduct<MP> y;
-    constexpr int kCols = RowProduct<MP>::kCols;
+    constexpr int kCols = RowProduct<MP>::kCols, W = kCols < 4 ? kCols : 4;
     for (int step = 0; step < a.n_steps; ++step) {
         y.run(A + row0 * MP, A, half_sum);
         const float ca = a.a[step], cb = a.b[step] * scale, cc = a.c[step] * scale * scale;
@@ -308,11 +340,15 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    const int row = 2 * hy + i, col = y.col(hx, j);
-                    float q = fmaf(cc, y.v[i][j], cb * A[(row0 + row) * MP + col]);
-                    if (col == row0 + row) q += ca;
-                    spread(Q, row, col, q);
+                for (int g = 0; g < kCols; g += W) {
+                    const int row = 2 * hy + i, col = y.col(hx, g);
+                    float q[W];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        q[j] = fmaf(cc, y.v[i][g + j], cb * A[(row0 + row) * MP + col + j]);
+                        if (col + j == row0 + row) q[j] += ca;
+                    }
+                    spread(Q, row, col, q, Width<W>());
                 }
         }
         gram_cluster_sync();
@@ -343,7 +379,8 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) spread(A, 2 * hy + i, y.col(hx, j), y.v[i][j]);
+                for (int g = 0; g < kCols; g += W)
+                    spread(A, 2 * hy + i, y.col(hx, g), &y.v[i][g], Width<W>());
         }
         scale = 1.0f;
         gram_cluster_sync();
@@ -369,16 +406,32 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
     float* P = sm;                       // [MP][PP]
     float* X = sm + MP * PP;             // [MP][64]
     const int t = int(threadIdx.x), tx = t & 15, ty = t >> 4;
-    for (int q = t; q < MP * MP / 4; q += kGramThreads)
-        *reinterpret_cast<float4*>(P + (q / (MP / 4)) * PP + (q % (MP / 4)) * 4) =
-            __ldg(reinterpret_cast<const float4*>(a.prod + d.prod) + q);
     const int e = a.exp[it.mat];
     const float s0 = e > -1000 ? pow2(-(e >> 1)) : 0.0f, s1 = e > -1000 ? pow2(-(e - (e >> 1))) : 0.0f;
-    for (int q = t; q < MP * kProdCols; q += kGramThreads) {
-        const int blk = q / (MP * 32), r = (q / 32) % MP, c = q & 31;
-        const bool in = it.c0 + blk * 32 < d.n;   // the copy holds whole blocks of 32 columns
-        X[r * kProdCols + blk * 32 + c] =
-            in ? __ldg(a.copy + d.copy + int64_t((it.c0 >> 5) + blk) * (MP * 32) + r * 32 + c) * s0 * s1 : 0.0f;
+    constexpr int kP = (MP * MP / 4 + kGramThreads - 1) / kGramThreads, kX = MP * kProdCols / 4 / kGramThreads;
+    float4 p[kP], x[kX];
+    // the copy holds whole blocks of 32 columns, and one more is never far: a
+    // second block past the end is read from the first instead
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+        const int q = t + i * kGramThreads, blk = it.c0 + q / (MP * 8) * 32 < d.n ? q / (MP * 8) : 0;
+        x[i] = __ldg(reinterpret_cast<const float4*>(a.copy + d.copy + int64_t((it.c0 >> 5) + blk) * (MP * 32)) +
+                     q % (MP * 8));
+    }
+#pragma unroll
+    for (int i = 0; i < kP; ++i)
+        p[i] = __ldg(reinterpret_cast<const float4*>(a.prod + d.prod) + min(t + i * kGramThreads, MP * MP / 4 - 1));
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+        const int q = t + i * kGramThreads, blk = q / (MP * 8), r = q / 8 % MP, c = q % 8 * 4;
+        const float k = it.c0 + blk * 32 < d.n ? 1.0f : 0.0f;
+        *reinterpret_cast<float4*>(X + r * kProdCols + blk * 32 + c) =
+            make_float4(x[i].x * s0 * s1 * k, x[i].y * s0 * s1 * k, x[i].z * s0 * s1 * k, x[i].w * s0 * s1 * k);
+    }
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+        const int q = t + i * kGramThreads;
+        if (q < MP * MP / 4) *reinterpret_cast<float4*>(P + (q / (MP / 4)) * PP + (q % (MP / 4)) * 4) = p[i];
     }
     __syncthreads();
     float acc[T][4];
