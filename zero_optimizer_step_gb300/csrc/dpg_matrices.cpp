@@ -83,7 +83,7 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.kn = int32_t(ceil_div(d.n, kBlkCols));
             d.km = int32_t(ceil_div(d.m, kBlkCols));
             const int64_t tm = ceil_div(d.m, kOrthoTile), tn = ceil_div(d.n, kOrthoTile);
-            if (tm > 0x7FFF || tn > 0x7FFF) return false;
+            if (tm > 0x3FFF || tn > 0x3FFF) return false;
             const int64_t rb = tm * (kOrthoTile / kBlkRows);
             d.cbx = int32_t(tn * (kOrthoTile / kBlkCols));
             d.cba = int32_t(tm * (kOrthoTile / kBlkCols));
@@ -100,10 +100,8 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.rows_pad = int32_t(tm * kOrthoTile);
             M.n_diag += d.rows_pad;
             d.rowsq = M.n_rowsq;
-            M.n_rowsq += int64_t(d.rows_pad) * (d.cbx / 2);
-            if (tm * tn > 0x3FFFFFF) return false;   // counts of a call stay in 32 bits
-            d.tiles_sym = int32_t(tm * (tm + 1) / 2);
-            d.tiles_x = int32_t(tm * tn);
+            M.n_rowsq += int64_t(d.rows_pad) * d.cbx;
+            if (tm * tn > 0x1FFFFFF) return false;   // counts of a call stay in 32 bits
             const int32_t mat = int32_t(M.mats.size());
             d.norm0 = int32_t(M.norm_items.size());
             for (int64_t s = 0; s < one; s += kNormChunk)
@@ -156,8 +154,11 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
 // of its sum (the tensor cores' rate) and at least 2.5 us (its finish), and
 // starts after its matrix's tiles of the product before.  It only balances the
 // queues; the kernel waits for what has really happened.
+//
+// A product whose tiles would leave most pairs idle is cut into tiles of 128
+// columns instead of 256, if these then still find a pair each: the sums take
+// as long, but the finish is half as long.
 void lay_queue(Matrices& M, int clusters) {
-    constexpr int kShare = 3;
     std::vector<int32_t> order(M.mats.size());
     for (size_t k = 0; k < order.size(); ++k) order[k] = int32_t(k);
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
@@ -165,28 +166,32 @@ void lay_queue(Matrices& M, int clusters) {
         return u.m != v.m ? u.m > v.m : u.n > v.n;
     });
     std::vector<OrthoTile> all;
-    size_t most = 0;
+    size_t most = 1;
     for (int prod = 0; prod < 3; ++prod) {
-        const size_t before = all.size();
-        for (int32_t k : order) {
-            const MatDesc& d = M.mats[size_t(k)];
-            const int tm = d.cba / 4, tn = d.cbx / 4;
-            const int rows = tm, cols = prod == kProdX ? tn : tm;
-            for (int ib = 0; ib < rows; ib += kShare)
-                for (int jb = 0; jb < cols; jb += kShare)
-                    for (int j = jb; j < cols && j < jb + kShare; ++j)
-                        for (int i = ib; i < rows && i < ib + kShare; ++i)
-                            if (prod == kProdX || j >= i) all.push_back({k, int16_t(i), int16_t(j), prod});
+        auto cut = [&](int width, std::vector<OrthoTile>& out) {
+            const int per = kOrthoTile / width;
+            for (int32_t k : order) {
+                MatDesc& d = M.mats[size_t(k)];
+                const size_t before = out.size();
+                const int tm = d.cba / 4, tn = (prod == kProdX ? d.cbx : d.cba) / 4;
+                for (int i = 0; i < tm; ++i)
+                    for (int j = prod == kProdX ? 0 : i * per; j < tn * per; ++j)
+                        out.push_back({k, int16_t(i), int16_t(j), int16_t(prod), int16_t(width)});
+                d.tiles[prod] = int32_t(out.size() - before);
+            }
+        };
+        std::vector<OrthoTile> tiles;
+        cut(128, tiles);
+        if (tiles.size() > size_t(clusters)) {
+            tiles.clear();
+            cut(256, tiles);
         }
-        most = std::max(most, all.size() - before);
+        most = std::max(most, tiles.size());
+        all.insert(all.end(), tiles.begin(), tiles.end());
     }
-    M.pairs = int32_t(std::min<size_t>(size_t(clusters), std::max<size_t>(most, 1)));
+    M.pairs = int32_t(std::min<size_t>(size_t(clusters), most));
     std::vector<std::vector<OrthoTile>> mine(size_t(M.pairs));
     std::vector<int64_t> ready(M.mats.size() * 4, 0);   // when the tiles of a product can start
-    constexpr int kGroups = 8;
-    std::vector<int32_t> turn;
-    for (int32_t g = 0; g < kGroups; ++g)
-        for (int32_t p = g; p < M.pairs; p += kGroups) turn.push_back(p);
     using Free = std::pair<int64_t, int32_t>;
     std::priority_queue<Free, std::vector<Free>, std::greater<Free>> idle;   // {time, pair}
     for (int32_t p = 0; p < M.pairs; ++p) idle.push({0, p});
@@ -198,7 +203,7 @@ void lay_queue(Matrices& M, int clusters) {
         const int64_t end = start + std::max<int64_t>(3 * (t.prod == kProdA ? d.kn : d.km), 25) + 2;
         int64_t& next = ready[size_t(t.mat) * 4 + size_t(t.prod) + 1];
         next = std::max(next, end);
-        mine[size_t(turn[size_t(f.second)])].push_back(t);
+        mine[size_t(f.second)].push_back(t);
         idle.push({end, f.second});
     }
     M.queue.clear();

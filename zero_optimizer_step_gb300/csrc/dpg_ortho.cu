@@ -61,7 +61,7 @@ struct OrthoArgs {
     float* diag_a;           // per row: A_rr
     float* diag_b;           // B_rr
     float* diag_t;           // t_r B_rr
-    float* rowsq;            // per 128 columns of X and row: sum of squares (scaled as hi)
+    float* rowsq;            // per 64 columns of X and row: sum of squares (scaled as hi)
     double* part;            // norm partials, one per norm item
     float2* scal;            // per matrix: {power-of-two scale of X_0, 1 / (norm * scale)}
     int32_t* count;          // per matrix: norm items done (zero between launches)
@@ -347,8 +347,8 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
         *reinterpret_cast<uint4*>(hi + at) = h4;
         if (F32) *reinterpret_cast<uint4*>(lo + at) = l4;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-        if (ch == 0) a.rowsq[d.rowsq + int64_t(it.j) * d.rows_pad + r0 + row] = sq;
+        for (int o = 4; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+        if ((ch & 7) == 0) a.rowsq[d.rowsq + int64_t(it.j * 2 + (ch >> 3)) * d.rows_pad + r0 + row] = sq;
     }
 }
 
@@ -384,9 +384,10 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 // Roles per CTA:
 //   warp 0       copies operands (TMA, kStages ahead)
 //   warp 1       of CTA 0: issues the products into one of two accumulators
-//   warps 2..9   finish the other accumulator: 64 columns at a time in a
-//                shared-memory slot (warp w: tensor-memory lanes 32 (w mod 4),
-//                32 of the 64 columns)
+//   warps 2..9   finish the other accumulator, 64 columns at a time in one of
+//                two shared-memory slots (warp w: tensor-memory lanes 32 (w mod
+//                4), 32 of the 64 columns; four warps to each slot side by side
+//                were a third slower, the slots then come free together)
 //   warp 10      fills the slots with what the finish needs (hi and lo of X,
 //                or the tile of A) and writes them out, as whole contiguous
 //                blocks; row-wise 16-byte accesses from the finishing warps
@@ -519,9 +520,9 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool by_column) {
     return uint64_t(addr >> 4) | (uint64_t(by_column ? 8192 >> 4 : 1) << 16) |
            (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-// fp16 operands, fp32 sums, 256 x 256; right operand by rows or by columns
-__device__ __forceinline__ uint32_t mma_shape(bool by_column) {
-    return (1u << 4) | (by_column ? 1u << 16 : 0u) | (uint32_t(kOrthoTile >> 3) << 17) |
+// fp16 operands, fp32 sums, 256 x width; right operand by rows or by columns
+__device__ __forceinline__ uint32_t mma_shape(bool by_column, int width) {
+    return (1u << 4) | (by_column ? 1u << 16 : 0u) | (uint32_t(width >> 3) << 17) |
            (uint32_t(kOrthoTile >> 4) << 24);
 }
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
@@ -593,7 +594,7 @@ __device__ __forceinline__ void put_sym(uint32_t slot, int row, int h, const flo
 // latencies add up to more than the product takes
 __device__ __forceinline__ float row_square(const OrthoArgs& a, const MatDesc& d, int r) {
     const float* p = a.rowsq + d.rowsq + r;
-    const int n = d.cbx >> 1;
+    const int n = d.cbx;
     const int64_t pitch = d.rows_pad;
     float s = 0.0f;
     for (int k = 0; k < n; k += 16) {
@@ -746,7 +747,7 @@ __device__ __forceinline__ void write_out(const OrthoArgs& a, const MatDesc& d, 
 __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& a, const MatDesc& d, int mat,
                                               int prod, int step) {
     const int before = prod == kProdA ? kProdX : prod - 1;
-    const int target = prod == kProdA ? step * 2 * d.tiles_x : (step + 1) * 2 * d.tiles_sym;
+    const int target = (prod == kProdA ? step : step + 1) * 2 * d.tiles[before];
     return wait_count(sh, a.done + 3 * mat + before, target, a.status);
 }
 
@@ -804,23 +805,25 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int64_t x = d.x[step & 1];
                 const int64_t from = prod == kProdA ? x : prod == kProdB ? d.a : d.b;
                 const int cb = prod == kProdA ? d.cbx : d.cba, kblocks = prod == kProdA ? d.kn : d.km;
+                const int half = tile.width >> 1, c0 = tile.j * tile.width + int(rank) * half;
                 const int left = int((from + int64_t(tile.i * 2 + int(rank)) * cb) * kBlkRows);
-                const int right = int((prod == kProdX ? x + tile.j * 4 + int(rank) * 2
-                                                      : from + int64_t(tile.j * 2 + int(rank)) * cb) * kBlkRows);
+                const int right = prod == kProdX ? int((x + (c0 >> 6)) * kBlkRows)
+                                                 : int((from + int64_t(c0 >> 7) * cb) * kBlkRows) + (c0 & 127);
+                const uint32_t bytes = 2 * (kHalfBytes + uint32_t(half) * 128);
                 const int pitch = d.cbx * kBlkRows;
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!(ok = wait_bounded(sh, &sh.empty[s], par, a.status))) break;
                     const uint32_t bar = full0 + uint32_t(s) * 8;
-                    if (rank == 0) mbar_expect(&sh.full[s], 2 * kStageBytes);
+                    if (rank == 0) mbar_expect(&sh.full[s], bytes);
                     const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
                     copy_box(dst, &rows128, left + kb * kBlkRows, bar);
                     if (prod == kProdX) {
                         const int row = right + (kb >> 1) * pitch + (kb & 1) * 64;
                         copy_box(dst + kHalfBytes, &rows64, row, bar);
-                        copy_box(dst + kHalfBytes + 8192, &rows64, row + kBlkRows, bar);
+                        if (half == 128) copy_box(dst + kHalfBytes + 8192, &rows64, row + kBlkRows, bar);
                     } else {
-                        copy_box(dst + kHalfBytes, &rows128, right + kb * kBlkRows, bar);
+                        copy_box(dst + kHalfBytes, half == 128 ? &rows128 : &rows64, right + kb * kBlkRows, bar);
                     }
                     if (++s == kStages) {
                         s = 0;
@@ -839,7 +842,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const bool by_column = tile.prod == kProdX;
-                const uint32_t shape = mma_shape(by_column);
+                const uint32_t shape = mma_shape(by_column, tile.width);
                 const int kblocks = tile.prod == kProdA ? d.kn : d.km;
                 const int buf = it & 1;
                 if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a.status))) break;
@@ -872,52 +875,51 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
-                const int prod = tile.prod;
-                if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
-                const bool mirror = prod != kProdX && tile.j > tile.i;
+                const int prod = tile.prod, blocks = tile.width >> 6, c0 = tile.j * blocks;
+                const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
                 const int cb = prod == kProdX ? d.cbx : d.cba;
-                // the CTA's first block within the matrix
-                const int64_t blk = int64_t(tile.i * 2 + int(rank)) * cb + tile.j * 4;
-                for (int g = 0; g <= 4 && ok; ++g) {
-                    if (g < 4) {      // fill the slot of block g
-                        const uint32_t sl = (n + g) & 1, at = slot0 + sl * kSlotBytes;
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        if (prod == kProdA) {
-                            mbar_arrive(&sh.in_full[sl]);
-                        } else if (prod == kProdB) {
-                            mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes));
-                            copy_in(at, a.ws + (d.a + blk + g) * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
-                        } else {
-                            mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (has_lo ? 2 : 1));
-                            copy_in(at, a.ws + (d.x[step & 1] + blk + g) * kBlkBytes, uint32_t(kBlkBytes),
-                                    &sh.in_full[sl]);
-                            if (has_lo)
-                                copy_in(at + uint32_t(kBlkBytes), a.ws + (d.lo + blk + g) * kBlkBytes,
-                                        uint32_t(kBlkBytes), &sh.in_full[sl]);
-                        }
+                // the CTA's first block in memory, in and out, and its mirror image's columns
+                const int64_t blk = int64_t(tile.i * 2 + int(rank)) * cb + c0;
+                const unsigned char* in = a.ws + ((prod == kProdB ? d.a : d.x[step & 1]) + blk) * kBlkBytes;
+                unsigned char* out = a.ws + ((prod == kProdA ? d.a : prod == kProdB ? d.b : d.x[(step + 1) & 1]) +
+                                             blk) * kBlkBytes;
+                unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
+                unsigned char* image = a.ws + ((prod == kProdA ? d.a : d.b) + tile.i * 4 + int(rank) * 2) * kBlkBytes;
+                auto fill = [&](int g) {
+                    const uint32_t sl = (n + uint32_t(g)) & 1, at = slot0 + sl * kSlotBytes;
+                    if (prod == kProdA) {
+                        mbar_arrive(&sh.in_full[sl]);
+                        return;
                     }
-                    if (g > 0) {      // write out block g - 1
-                        const uint32_t k = n + uint32_t(g) - 1, sl = k & 1, at = slot0 + sl * kSlotBytes;
-                        if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (k >> 1) & 1, a.status))) break;
-                        if (prod != kProdX) {
-                            const int64_t to = prod == kProdA ? d.a : d.b;
-                            copy_out(a.ws + (to + blk + g - 1) * kBlkBytes, at, uint32_t(kBlkBytes));
-                            if (mirror) {   // 64 rows from column 64 (g - 1) of the tile, 2 x 64 columns
-                                unsigned char* m = a.ws + (to + int64_t(tile.j * 2 + ((g - 1) >> 1)) * cb +
-                                                           tile.i * 4 + int(rank) * 2) * kBlkBytes +
-                                                   ((g - 1) & 1) * 8192;
-                                copy_out(m, at + uint32_t(kBlkBytes), 8192);
-                                copy_out(m + kBlkBytes, at + uint32_t(kBlkBytes) + 8192, 8192);
-                            }
-                        } else if (!last) {
-                            copy_out(a.ws + (d.x[(step + 1) & 1] + blk + g - 1) * kBlkBytes, at, uint32_t(kBlkBytes));
-                            copy_out(a.ws + (d.lo + blk + g - 1) * kBlkBytes, at + uint32_t(kBlkBytes),
-                                     uint32_t(kBlkBytes));
+                    const bool two = prod == kProdX && has_lo;
+                    mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (two ? 2 : 1));
+                    copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
+                    if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
+                };
+                if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
+                fill(0);
+                fill(1);
+                for (int g = 0; g < blocks && ok; ++g) {
+                    const uint32_t k = n + uint32_t(g), sl = k & 1, at = slot0 + sl * kSlotBytes;
+                    if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (k >> 1) & 1, a.status))) break;
+                    if (prod != kProdX) {
+                        copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
+                        if (mirror) {     // 64 rows from this block's first column, 2 x 64 columns
+                            unsigned char* m = image + int64_t((c0 + g) >> 1) * cb * kBlkBytes + ((c0 + g) & 1) * 8192;
+                            copy_out(m, at + uint32_t(kBlkBytes), 8192);
+                            copy_out(m + kBlkBytes, at + uint32_t(kBlkBytes) + 8192, 8192);
                         }
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    } else if (!last) {
+                        copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
+                        copy_out(lo + g * kBlkBytes, at + uint32_t(kBlkBytes), uint32_t(kBlkBytes));
+                    }
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    if (g + kSlots < blocks) {         // fill the slot again once it has been read
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        fill(g + kSlots);
                     }
                 }
-                n += 4;
+                n += uint32_t(blocks);
                 if (!ok) break;
                 // all of the tile is in memory before its count
                 asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -930,10 +932,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp >= 2 && warp < kSlotWarp) {
         // ---- finish ----
-        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int quad = warp & 3, half = (warp - 2) >> 2;   // the warp's rows, its 32 columns of 64
         const int row0 = quad * 32, row = row0 + lane;
+        float* cols = sh.cols[warp - 2];
         int it = 0;
-        uint32_t n = 0;
+        uint32_t n = 0;               // as above
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             const OrthoStep& s = a.st[step];
@@ -942,22 +945,22 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             for (int t = q0; t < q1 && ok; ++t, ++it) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
-                const int prod = tile.prod, buf = it & 1;
+                const int prod = tile.prod, buf = it & 1, blocks = tile.width >> 6, c0 = tile.j * tile.width;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
-                const bool mirror = prod != kProdX && tile.j > tile.i;
+                const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
                 if (lane == 0) ok = wait_operands(sh, a, d, tile.mat, prod, step);
                 if (!(ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0) != 0)) break;
                 // what the rows need, fetched while the product runs
                 const float inv_sx = step == 0 ? __ldcg(&a.scal[tile.mat].y) : s.inv_sx;
                 float p0 = 0.0f, p1 = 0.0f, dc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sq = 0.0f;
                 if (prod == kProdA) {
-                    // the two warps that hold the diagonal's 64-column block share its rows' sums
-                    if (tile.i == tile.j && half == (quad & 1)) p0 = row_square(a, d, r);
+                    // if the tile holds the diagonal of these rows, in this warp's 32 columns
+                    if (r0 >= c0 && r0 < c0 + tile.width && half == (quad & 1)) p0 = row_square(a, d, r);
                 } else if (prod == kProdB) {
                     p0 = __ldcg(a.diag_a + d.diag + r);
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        dc[g] = __ldcg(a.diag_a + d.diag + tile.j * kOrthoTile + g * 64 + half * 32 + lane);
+                        if (g < blocks) dc[g] = __ldcg(a.diag_a + d.diag + c0 + g * 64 + half * 32 + lane);
                 } else {
                     p0 = fmaf(__ldcg(a.diag_b + d.diag + r), inv_sx, s.a * inv_sx);
                     p1 = fmaf(__ldcg(a.diag_t + d.diag + r), inv_sx, s.a * inv_sx) * kInvLoScale;
@@ -966,12 +969,12 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-                for (int g = 0; g < 4; ++g, ++n) {
-                    const int col = g * 64 + half * 32;
+                for (int g = 0; g < blocks; ++g, ++n) {
+                    const int col = g * 64 + half * 32, c = c0 + col;
                     const uint32_t sl = n & 1, slot = slot0 + sl * kSlotBytes;
                     float acc[32];
                     load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(row0) << 16), acc);
-                    if (g == 3) {     // the accumulator is free for the tile after next
+                    if (g + 1 == blocks) {   // the accumulator is free for the tile after next
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                         __syncwarp();
                         if (lane == 0)
@@ -980,20 +983,21 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     }
                     ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a.status);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-                    const int c0 = tile.j * kOrthoTile + col;
                     if (prod == kProdA) {
-                        finish_a(a, s, d, inv_sx, slot, row, half, r, c0, acc, mirror, p0);
+                        finish_a(a, s, d, inv_sx, slot, row, half, r, c, acc, mirror, p0);
                     } else if (prod == kProdB) {
                         __syncwarp();
-                        sh.cols[warp - 2][lane] = g == 0 ? dc[0] : g == 1 ? dc[1] : g == 2 ? dc[2] : dc[3];
+                        cols[lane] = g == 0 ? dc[0] : g == 1 ? dc[1] : g == 2 ? dc[2] : dc[3];
                         __syncwarp();
-                        finish_b(a, s, d, slot, row, half, r, c0, acc, mirror, p0, smem_u32(sh.cols[warp - 2]));
+                        finish_b(a, s, d, slot, row, half, r, c, acc, mirror, p0, smem_u32(cols));
                     } else {
                         sq += finish_x(s, slot, row, half, r, acc, p0, p1, inv_sx * s.inv_sb, has_lo, last);
-                        if (last)
-                            write_out(a, d, slot, row0, half, r0, c0);
-                        else if (g == 3)   // of the warp's 128 columns of the tile
-                            a.rowsq[d.rowsq + int64_t(tile.j * 2 + half) * d.rows_pad + r] = sq;
+                        if (last) {
+                            write_out(a, d, slot, row0, half, r0, c);
+                        } else if (g & 1) {   // of this warp's 32 columns in two blocks
+                            a.rowsq[d.rowsq + int64_t((c0 >> 6) + (g & 2) + half) * d.rows_pad + r] = sq;
+                            sq = 0.0f;
+                        }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();

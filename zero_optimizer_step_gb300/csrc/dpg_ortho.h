@@ -37,17 +37,18 @@ struct MatDesc {
     int64_t x[2], lo;     // first block of the two X buffers and of X's low part
     int64_t a, b;         // first block of A and of bA + cA^2 (off-diagonal parts)
     int64_t diag;         // first entry of the per-row vectors (see OrthoArgs)
-    int64_t rowsq;        // first entry of X's row sums of squares, [cbx / 2][padded rows]
+    int64_t rowsq;        // first entry of X's row sums of squares, [cbx][padded rows]
     int32_t rows_pad;     // rows of X padded to 256
     int32_t norm0, norm1; // its items in the norm table
-    int32_t tiles_sym, tiles_x;   // output tiles of A (and B), of X
+    int32_t tiles[3];     // output tiles of each product (see lay_queue)
 };
 
-// One 256 x 256 output tile of one product of one matrix.
+// One output tile of one product of one matrix: 256 rows from 256 i, `width`
+// (256 or 128) columns from width j.
 struct OrthoTile {
     int32_t mat;
     int16_t i, j;
-    int32_t prod;
+    int16_t prod, width;
 };
 
 // Matrices whose shorter side is at most kSmallSide take the steps on their
