@@ -67,7 +67,7 @@ struct OrthoArgs {
     int32_t* count;          // per matrix: norm items done (zero between launches)
     int32_t* status;         // 0, or the error of the first wait that ran out
     int32_t* done;           // per matrix and product: CTA tiles finished in this call
-    const OrthoTile* queue;  // tiles of a step, pair p's at [queue_first[p], queue_first[p + 1])
+    const OrthoTile* queue;  // tiles of a step in twos, cluster c's at [queue_first[c], queue_first[c + 1])
     const int32_t* queue_first;
     const void* update;
     int32_t f32;             // update holds fp32 (else bf16)
@@ -367,23 +367,29 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 
 // ---------------------------------------------------------------------------
 // The steps.  One persistent kernel runs every product of every step.  A pair
-// of CTAs on two SMs (a cluster of 2) computes 256 x 256 tiles: CTA r holds
-// rows 128 r .. of the left operand and columns 128 r .. of the right one, 32
-// KB per 64-deep stage and SM, and the pair's tcgen05.mma (cta_group::2) reads
-// both halves.  A 128 x 256 tile on one SM would need 48 KB per stage for the
-// same arithmetic, more than L2 delivers.
+// of CTAs on two SMs computes 256 x 256 tiles: CTA r holds rows 128 r .. of the
+// left operand and columns 128 r .. of the right one, 32 KB per 64-deep stage
+// and SM, and the pair's tcgen05.mma (cta_group::2) reads both halves.  A 128 x
+// 256 tile on one SM would need 48 KB per stage for the same arithmetic.
 //
-// Every pair works through a queue of tiles that the host laid out once
+// Even 32 KB per stage are more than L2 delivers to 152 SMs at the tensor
+// cores' rate (it saturated at 15 TB/s, a third of the products' time lost), so
+// two pairs form a cluster, take two neighbours of a row of tiles, and fetch
+// the left operand once: each CTA copies half of its rows to itself and to its
+// counterpart in the other pair (multicast), 24 KB per stage and SM.
+//
+// Every cluster works through a queue of tiles that the host laid out once
 // (balanced by cost), the same in every step: A tiles, B tiles, X tiles of all
 // matrices.  A tile starts when its matrix's tiles of the product before are
 // done (a counter per matrix and product in device memory), so matrices
 // overlap at the ends of their products and a step needs no launch.  Queues
-// follow one global order and all pairs are resident (cooperative launch), so
-// the oldest unfinished tile can always run.
+// follow one global order and all clusters are resident (cooperative launch),
+// so the oldest unfinished tile can always run.
 //
 // Roles per CTA:
 //   warp 0       copies operands (TMA, kStages ahead)
-//   warp 1       of CTA 0: issues the products into one of two accumulators
+//   warp 1       of a pair's first CTA: issues the products into one of two
+//                accumulators
 //   warps 2..9   finish the other accumulator, 64 columns at a time in one of
 //                two shared-memory slots (warp w: tensor-memory lanes 32 (w mod
 //                4), 32 of the 64 columns; four warps to each slot side by side
@@ -504,6 +510,14 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
                  " [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
 }
+// the same into this CTA's and the counterparts' memory (the CTAs of `mask`);
+// each one's arrival is counted at its pair's first CTA
+__device__ __forceinline__ void copy_box_to(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar,
+                                            uint16_t mask) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;"
+                 :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar), "h"(mask) : "memory");
+}
 __device__ __forceinline__ void copy_in(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
@@ -530,10 +544,10 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
                  " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
                  :: "r"(d), "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u) : "memory");
 }
-// arrives at `bar` of both CTAs once every product issued so far is done
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// arrives at `bar` of the CTAs of `mask` once every product issued so far is done
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint32_t mask) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+                 :: "r"(smem_u32(bar)), "h"(uint16_t(mask)) : "memory");
 }
 __device__ __forceinline__ void load_acc32(uint32_t tmem, float* v) {
     uint32_t r[32];
@@ -751,7 +765,7 @@ __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& 
     return wait_count(sh, a.done + 3 * mat + before, target, a.status);
 }
 
-__global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
+__global__ void __cluster_dims__(4) __launch_bounds__(kOrthoThreads, 1)
 k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
               const __grid_constant__ CUtensorMap rows64) {
     // the kernel's only shared memory: starts on a multiple of 1 KB, as the swizzle wants it
@@ -760,12 +774,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     const uint32_t stage0 = smem_u32(dyn);
     const uint32_t slot0 = stage0 + uint32_t(kStages) * kStageBytes;
     const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
-    const uint32_t rank = cluster_rank();
-    const int pair = int(blockIdx.x >> 1);
+    // CTA 0 or 1 of its pair, pair 0 or 1 of the cluster
+    const uint32_t rank4 = cluster_rank(), rank = rank4 & 1, first = rank4 & 2, which = rank4 >> 1;
+    const int cluster = int(blockIdx.x >> 2);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.empty[s], 2);       // both pairs: a stage is filled from both
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.tfull[b], 1);
@@ -787,19 +802,21 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     pdl_enter();
     const uint32_t tmem = sh.tmem;
-    const int q0 = __ldg(a.queue_first + pair), q1 = __ldg(a.queue_first + pair + 1);
+    const int q0 = __ldg(a.queue_first + cluster), q1 = __ldg(a.queue_first + cluster + 1);
+    const OrthoTile* queue = a.queue + which;   // tile t of this pair: queue[2 t]
 
     if (warp == 0 && lane == 0) {
         // ---- operands ----
         // (what the loop over K needs is in registers: the copies' memory
         // clobbers would have a value of the descriptor loaded again for each)
-        const uint32_t full0 = map_to(smem_u32(&sh.full[0]), 0);
+        const uint32_t full0 = map_to(smem_u32(&sh.full[0]), first);
+        const uint16_t mask = uint16_t(5u << rank);   // this CTA and its counterpart
         int s = 0;
         uint32_t par = 1;             // the first pass over the ring finds it empty
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             for (int t = q0; t < q1 && ok; ++t) {
-                const OrthoTile tile = a.queue[t];
+                const OrthoTile tile = queue[2 * t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod;
                 const int64_t x = d.x[step & 1];
@@ -817,7 +834,10 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     const uint32_t bar = full0 + uint32_t(s) * 8;
                     if (rank == 0) mbar_expect(&sh.full[s], bytes);
                     const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
-                    copy_box(dst, &rows128, left + kb * kBlkRows, bar);
+                    if (tile.flags & kTileShared)
+                        copy_box_to(dst + which * 8192, &rows64, left + kb * kBlkRows + int(which) * 64, bar, mask);
+                    else
+                        copy_box(dst, &rows128, left + kb * kBlkRows, bar);
                     if (prod == kProdX) {
                         const int row = right + (kb >> 1) * pitch + (kb & 1) * 64;
                         copy_box(dst + kHalfBytes, &rows64, row, bar);
@@ -839,7 +859,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             for (int t = q0; t < q1 && ok; ++t, ++it) {
-                const OrthoTile tile = a.queue[t];
+                const OrthoTile tile = queue[2 * t];
                 const MatDesc& d = a.mats[tile.mat];
                 const bool by_column = tile.prod == kProdX;
                 const uint32_t shape = mma_shape(by_column, tile.width);
@@ -856,13 +876,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     for (int k = 0; k < 4; ++k)   // 16 deep each
                         mma_pair(tmem + uint32_t(buf) * kOrthoTile, left + 2 * k,
                                  right + (by_column ? 128 : 2) * k, shape, (kb | k) != 0);
-                    commit_pair(&sh.empty[s]);
+                    commit_to(&sh.empty[s], 15);
                     if (++s == kStages) {
                         s = 0;
                         par ^= 1;
                     }
                 }
-                if (ok) commit_pair(&sh.tfull[buf]);
+                if (ok) commit_to(&sh.tfull[buf], 3u << first);
             }
         }
     } else if (warp == kSlotWarp && lane == 0) {
@@ -873,7 +893,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
-                const OrthoTile tile = a.queue[t];
+                const OrthoTile tile = queue[2 * t];
+                if (tile.flags & kTileIdle) continue;
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, blocks = tile.width >> 6, c0 = tile.j * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
@@ -943,11 +964,24 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
-                const OrthoTile tile = a.queue[t];
+                const OrthoTile tile = queue[2 * t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, buf = it & 1, blocks = tile.width >> 6, c0 = tile.j * tile.width;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
+                auto release = [&] {     // the accumulator is free for the tile after next
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                                     :: "r"(map_to(smem_u32(&sh.tempty[buf]), first)) : "memory");
+                };
+                if (tile.flags & kTileIdle) {
+                    ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                    release();
+                    continue;
+                }
                 if (lane == 0) ok = wait_operands(sh, a, d, tile.mat, prod, step);
                 if (!(ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0) != 0)) break;
                 // what the rows need, fetched while the product runs
@@ -974,13 +1008,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     const uint32_t sl = n & 1, slot = slot0 + sl * kSlotBytes;
                     float acc[32];
                     load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(row0) << 16), acc);
-                    if (g + 1 == blocks) {   // the accumulator is free for the tile after next
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0)
-                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                                         :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
-                    }
+                    if (g + 1 == blocks) release();
                     ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a.status);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     if (prod == kProdA) {
@@ -1061,24 +1089,24 @@ int upload_matrices(Matrices& m) {
                         m.device, dev);
         return DPG_OK;
     }
-    // how many CTA pairs are resident at once decides the queues
+    // how many clusters are resident at once decides the queues
     int clusters = 1;
     if (!m.mats.empty()) {
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_load<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           2 * kLoadSmem));
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
+        cfg.gridDim = dim3(4);
         cfg.blockDim = dim3(kOrthoThreads);
         cfg.dynamicSmemBytes = kOrthoSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.x = 4;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps, &cfg));
-        if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no CTA pair fits this device");
+        if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no cluster fits this device");
     }
     if (!m.small.empty()) {
         const int st = gram_prepare();
@@ -1207,12 +1235,12 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(2 * m.pairs));
+    cfg.gridDim = dim3(unsigned(4 * m.clusters));
     cfg.blockDim = dim3(kOrthoThreads);
     cfg.dynamicSmemBytes = kOrthoSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;   // the pairs wait for one another
+    attr[0].id = cudaLaunchAttributeCooperative;   // the clusters wait for one another
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
