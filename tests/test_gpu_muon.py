@@ -81,6 +81,21 @@ def test_orthogonalize_spectra(kind, rows, cols):
     _ortho_case([(rows, cols, 1)], kind, torch.float32)
 
 
+@pytest.mark.parametrize("rows,cols", [(257, 40000), (39100, 300), (700, 26000)])
+def test_orthogonalize_many_tiles(rows, cols):
+    # enough tiles for clusters of two pairs; odd numbers of them in a row
+    _ortho_case([(rows, cols, 1)], "spiked", torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(128, 3000), (3000, 128), (65, 66), (16, 16), (17, 5000), (5000, 33),
+                                       (1, 40000), (2, 2), (128, 129)])
+def test_orthogonalize_short_side(rows, cols, dtype):
+    # the path of up to 128 rows: every padded side, partial blocks of columns
+    for kind in ("gauss", "rank1"):
+        _ortho_case([(rows, cols, 2)], kind, dtype)
+
+
 def test_orthogonalize_list_of_matrices():
     # stacks, tall and wide, odd sizes whose slices start off 16-byte boundaries
     _ortho_case([(333, 129, 2), (1, 77, 3), (64, 32, 1), (129, 333, 1), (5, 5, 5), (640, 512, 2),
@@ -113,13 +128,14 @@ def test_orthogonalize_coefficients(coeffs):
     _ortho_case([(150, 70, 1), (300, 420, 1)], "gauss", torch.bfloat16, hp=dpg.MuonHParams(coeffs=coeffs))
 
 
-def test_orthogonalize_zero_and_nonfinite_matrices():
-    shapes = [(40, 60, 6)]
+@pytest.mark.parametrize("rows,cols", [(40, 60), (150, 140)])
+def test_orthogonalize_zero_and_nonfinite_matrices(rows, cols):
+    shapes = [(rows, cols, 6)]
     rng = np.random.Generator(np.random.Philox(9))
     plan, mats = _plan(shapes)
     clean = _flat(plan, shapes, lambda p, i, r, c: make_matrix("gauss", r, c, rng))
     flat = clean.copy()
-    n = 40 * 60
+    n = rows * cols
     flat[n:2 * n] = 0.0
     flat[2 * n + 17] = np.nan
     flat[3 * n + 99] = np.inf

@@ -10,6 +10,7 @@ raises ``DpgLibraryMissing``: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence, Union
@@ -107,12 +108,16 @@ class MuonHParams:
     scale_rule: int = DPG_SCALE_SPECTRAL
 
     def c(self) -> dpg_muon_hparams:
-        h = dpg_muon_hparams(lr=self.lr, momentum=self.momentum, weight_decay=self.weight_decay,
-                             eps=self.eps, n_steps=len(self.coeffs), nesterov=int(self.nesterov),
-                             scale_rule=int(self.scale_rule))
-        for k, abc in enumerate(list(self.coeffs)[:DPG_MAX_NS_STEPS]):
-            h.coeffs[k][:] = [float(x) for x in abc]
-        return h
+        coeffs = tuple(map(tuple, self.coeffs))
+        return dpg_muon_hparams(self.lr, self.momentum, self.weight_decay, self.eps,
+                                _c_coeffs(coeffs[:DPG_MAX_NS_STEPS]), len(coeffs), int(self.nesterov),
+                                int(self.scale_rule))
+
+
+@functools.lru_cache(maxsize=64)
+def _c_coeffs(coeffs):
+    """The C array of a tuple of (a, b, c) tuples (a small call's time is mostly marshalling)."""
+    return ((ctypes.c_double * 3) * DPG_MAX_NS_STEPS)(*((float(a), float(b), float(c)) for a, b, c in coeffs))
 
 
 _lib = None
@@ -226,11 +231,13 @@ def _ptr(x: Ptr) -> Optional[int]:
     return x.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _ptr_array(n: int):
+    return ctypes.c_void_p * n
+
+
 def _ptrs(xs: Sequence[Ptr]):
-    arr = (ctypes.c_void_p * max(1, len(xs)))()
-    for k, x in enumerate(xs):
-        arr[k] = _ptr(x)
-    return arr
+    return _ptr_array(max(1, len(xs)))(*map(_ptr, xs))
 
 
 def _stream(stream) -> Optional[int]:
@@ -247,12 +254,17 @@ def _tokens(valid_tokens):
     return t, t.size
 
 
+@functools.lru_cache(maxsize=None)
+def _torch_dtypes():
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
 def _need(t, dtype_name: str, numel: int, what: str):
     """Tensors must be CUDA, contiguous, of the right dtype and large enough."""
     if t is None or isinstance(t, int):
         return
-    import torch
-    want = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype_name]
+    want = _torch_dtypes()[dtype_name]
     if t.dtype != want:
         raise TypeError(f"{what}: expected {want}, got {t.dtype}")
     if not t.is_cuda:

@@ -67,7 +67,7 @@ struct OrthoArgs {
     int32_t* count;          // per matrix: norm items done (zero between launches)
     int32_t* status;         // 0, or the error of the first wait that ran out
     int32_t* done;           // per matrix and product: CTA tiles finished in this call
-    const OrthoTile* queue;  // tiles of a step in twos, cluster c's at [queue_first[c], queue_first[c + 1])
+    const OrthoTile* queue;  // tiles of a step in groups, cluster c's at [queue_first[c], queue_first[c + 1])
     const int32_t* queue_first;
     const void* update;
     int32_t f32;             // update holds fp32 (else bf16)
@@ -373,9 +373,9 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 // 256 tile on one SM would need 48 KB per stage for the same arithmetic.
 //
 // Even 32 KB per stage are more than L2 delivers to 152 SMs at the tensor
-// cores' rate (it saturated at 15 TB/s, a third of the products' time lost), so
-// two pairs form a cluster, take two neighbours of a row of tiles, and fetch
-// the left operand once: each CTA copies half of its rows to itself and to its
+// cores' rate (15 TB/s), so where there are tiles enough (see lay_queue) two
+// pairs form a cluster, take two neighbours of a row of tiles, and fetch the
+// left operand once: each CTA copies half of its rows to itself and to its
 // counterpart in the other pair (multicast), 24 KB per stage and SM.
 //
 // Every cluster works through a queue of tiles that the host laid out once
@@ -529,9 +529,10 @@ __device__ __forceinline__ void copy_out(void* dst, uint32_t src, uint32_t bytes
 
 // Shared-memory descriptors of the 128-byte swizzle: rows of 64 K-values (8
 // rows every 1024 bytes), or 64-column groups (8 K-rows every 1024 bytes, the
-// next 64 columns 8192 bytes on).
+// next 64 columns 8192 bytes on).  The upper bits of a shared address name the
+// CTA of the cluster; in the descriptor they would reach into the next field.
 __device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool by_column) {
-    return uint64_t(addr >> 4) | (uint64_t(by_column ? 8192 >> 4 : 1) << 16) |
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(by_column ? 8192 >> 4 : 1) << 16) |
            (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 // fp16 operands, fp32 sums, 256 x width; right operand by rows or by columns
@@ -765,7 +766,8 @@ __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& 
     return wait_count(sh, a.done + 3 * mat + before, target, a.status);
 }
 
-__global__ void __cluster_dims__(4) __launch_bounds__(kOrthoThreads, 1)
+template <int PAIRS>
+__global__ void __cluster_dims__(2 * PAIRS) __launch_bounds__(kOrthoThreads, 1)
 k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
               const __grid_constant__ CUtensorMap rows64) {
     // the kernel's only shared memory: starts on a multiple of 1 KB, as the swizzle wants it
@@ -775,12 +777,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     const uint32_t slot0 = stage0 + uint32_t(kStages) * kStageBytes;
     const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
     // CTA 0 or 1 of its pair, pair 0 or 1 of the cluster
-    const uint32_t rank4 = cluster_rank(), rank = rank4 & 1, first = rank4 & 2, which = rank4 >> 1;
-    const int cluster = int(blockIdx.x >> 2);
+    const uint32_t in_cluster = cluster_rank(), rank = in_cluster & 1;
+    const uint32_t which = PAIRS == 2 ? in_cluster >> 1 : 0, first = 2 * which;
+    const int cluster = int(blockIdx.x) / (2 * PAIRS);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 2);       // both pairs: a stage is filled from both
+            mbar_init(&sh.empty[s], PAIRS);   // a stage may be filled from both pairs
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.tfull[b], 1);
@@ -803,7 +806,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     pdl_enter();
     const uint32_t tmem = sh.tmem;
     const int q0 = __ldg(a.queue_first + cluster), q1 = __ldg(a.queue_first + cluster + 1);
-    const OrthoTile* queue = a.queue + which;   // tile t of this pair: queue[2 t]
+    const OrthoTile* queue = a.queue + which;   // tile t of this pair: queue[PAIRS t]
 
     if (warp == 0 && lane == 0) {
         // ---- operands ----
@@ -816,7 +819,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             for (int t = q0; t < q1 && ok; ++t) {
-                const OrthoTile tile = queue[2 * t];
+                const OrthoTile tile = queue[PAIRS * t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod;
                 const int64_t x = d.x[step & 1];
@@ -834,7 +837,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     const uint32_t bar = full0 + uint32_t(s) * 8;
                     if (rank == 0) mbar_expect(&sh.full[s], bytes);
                     const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
-                    if (tile.flags & kTileShared)
+                    if (PAIRS == 2 && (tile.flags & kTileShared))
                         copy_box_to(dst + which * 8192, &rows64, left + kb * kBlkRows + int(which) * 64, bar, mask);
                     else
                         copy_box(dst, &rows128, left + kb * kBlkRows, bar);
@@ -859,7 +862,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             for (int t = q0; t < q1 && ok; ++t, ++it) {
-                const OrthoTile tile = queue[2 * t];
+                const OrthoTile tile = queue[PAIRS * t];
                 const MatDesc& d = a.mats[tile.mat];
                 const bool by_column = tile.prod == kProdX;
                 const uint32_t shape = mma_shape(by_column, tile.width);
@@ -876,7 +879,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     for (int k = 0; k < 4; ++k)   // 16 deep each
                         mma_pair(tmem + uint32_t(buf) * kOrthoTile, left + 2 * k,
                                  right + (by_column ? 128 : 2) * k, shape, (kb | k) != 0);
-                    commit_to(&sh.empty[s], 15);
+                    commit_to(&sh.empty[s], PAIRS == 2 ? 15u : 3u);
                     if (++s == kStages) {
                         s = 0;
                         par ^= 1;
@@ -893,8 +896,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
-                const OrthoTile tile = queue[2 * t];
-                if (tile.flags & kTileIdle) continue;
+                const OrthoTile tile = queue[PAIRS * t];
+                if (PAIRS == 2 && (tile.flags & kTileIdle)) continue;
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, blocks = tile.width >> 6, c0 = tile.j * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
@@ -964,7 +967,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
-                const OrthoTile tile = queue[2 * t];
+                const OrthoTile tile = queue[PAIRS * t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, buf = it & 1, blocks = tile.width >> 6, c0 = tile.j * tile.width;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
@@ -976,7 +979,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                                      :: "r"(map_to(smem_u32(&sh.tempty[buf]), first)) : "memory");
                 };
-                if (tile.flags & kTileIdle) {
+                if (PAIRS == 2 && (tile.flags & kTileIdle)) {
                     ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     release();
@@ -1090,30 +1093,34 @@ int upload_matrices(Matrices& m) {
         return DPG_OK;
     }
     // how many clusters are resident at once decides the queues
-    int clusters = 1;
+    int resident[2] = {1, 0};
     if (!m.mats.empty()) {
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_load<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           2 * kLoadSmem));
-        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(4);
-        cfg.blockDim = dim3(kOrthoThreads);
-        cfg.dynamicSmemBytes = kOrthoSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 4;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps, &cfg));
-        if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no cluster fits this device");
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
+        for (int pairs = 1; pairs <= 2; ++pairs) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(unsigned(2 * pairs));
+            cfg.blockDim = dim3(kOrthoThreads);
+            cfg.dynamicSmemBytes = kOrthoSmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = unsigned(2 * pairs);
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            DPG_CUDA_TRY(pairs == 1 ? cudaOccupancyMaxActiveClusters(&resident[0], k_ortho_steps<1>, &cfg)
+                                    : cudaOccupancyMaxActiveClusters(&resident[1], k_ortho_steps<2>, &cfg));
+        }
+        if (resident[0] < 1) return fail(DPG_ERR_CUDA, "matrices upload: no cluster fits this device");
     }
     if (!m.small.empty()) {
         const int st = gram_prepare();
         if (st != DPG_OK) return st;
     }
     try {
-        lay_queue(m, clusters);
+        lay_queue(m, resident);
     } catch (const std::exception&) {
         return fail(DPG_ERR_OOM, "matrices upload: out of host memory");
     }
@@ -1235,7 +1242,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(4 * m.clusters));
+    cfg.gridDim = dim3(unsigned(2 * m.cluster_pairs * m.clusters));
     cfg.blockDim = dim3(kOrthoThreads);
     cfg.dynamicSmemBytes = kOrthoSmem;
     cfg.stream = s;
@@ -1244,7 +1251,8 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_steps, a, map[0], map[1]);
+    const cudaError_t e = m.cluster_pairs == 2 ? cudaLaunchKernelEx(&cfg, k_ortho_steps<2>, a, map[0], map[1])
+                                               : cudaLaunchKernelEx(&cfg, k_ortho_steps<1>, a, map[0], map[1]);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
