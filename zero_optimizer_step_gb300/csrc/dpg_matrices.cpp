@@ -149,84 +149,53 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
 }
 
 // The tiles of one step -- A tiles, B tiles, X tiles of all matrices, larger
-// matrices first -- taken in groups of one per CTA pair of a cluster and dealt
-// out to the clusters in this order, each group to the cluster that could start
-// it first.  The model behind "first": a tile takes 0.3 us per 64 of its sum
-// (the tensor cores' rate) and at least 2.5 us (its finish), and starts after
-// its matrix's tiles of the product before.  It only balances the queues; the
-// kernel waits for what has really happened.
-//
-// Clusters of two pairs: two neighbours in a row of tiles share their left
-// operand, which the cluster then fetches once.  The tiles left over (one of an
-// odd row: the diagonal one of a symmetric product) go together without
-// sharing.  Such clusters leave 8 of 152 SMs unused and run tiles in twos, so
-// they pay only where there are many waves: with 1024 and 3328 tiles of X on 76
-// pairs they take 1923 us against 1940 and 10.84 ms against 11.38, with 256
-// (four 1024 x 4096 matrices) 511 against 516, with 144 (GPT-2-small-shaped
-// attention weights) 346 against 305.
+// matrices first -- dealt out to the pairs in this order, each to the pair that
+// could start it first.  The model behind "first": a tile takes 0.3 us per 64
+// of its sum (the tensor cores' rate) and at least 2.5 us (its finish), and
+// starts after its matrix's tiles of the product before.  It only balances the
+// queues; the kernel waits for what has really happened.
 //
 // A product whose tiles would leave most pairs idle is cut into tiles of 128
 // columns instead of 256, if these then still find a pair each: the sums take
-// as long, but the finish is half as long (one 768 x 768 matrix: 149 us against
-// 185).
-void lay_queue(Matrices& M, const int resident[2]) {
-    struct Group {
-        OrthoTile t[2];
-    };
-    int64_t x_tiles = 0;
-    for (const MatDesc& d : M.mats) x_tiles += int64_t(d.cba / 4) * (d.cbx / 4);
-    const int G = M.cluster_pairs = x_tiles >= 4 * int64_t(resident[0]) && resident[1] > 0 ? 2 : 1;
-    const size_t most_clusters = size_t(resident[G - 1]);
+// as long, but the finish is half as long.
+void lay_queue(Matrices& M, int clusters) {
     std::vector<int32_t> order(M.mats.size());
     for (size_t k = 0; k < order.size(); ++k) order[k] = int32_t(k);
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
         const MatDesc &u = M.mats[size_t(x)], &v = M.mats[size_t(y)];
         return u.m != v.m ? u.m > v.m : u.n > v.n;
     });
-    std::vector<Group> all;
+    std::vector<OrthoTile> all;
     size_t most = 1;
     for (int prod = 0; prod < 3; ++prod) {
-        auto cut = [&](int width, std::vector<Group>& out) {
+        auto cut = [&](int width, std::vector<OrthoTile>& out) {
             const int per = kOrthoTile / width;
             for (int32_t k : order) {
                 MatDesc& d = M.mats[size_t(k)];
-                const int tm = d.cba / 4, tn = (prod == kProdX ? d.cbx : d.cba) / 4 * per;
-                std::vector<OrthoTile> single;
-                d.tiles[prod] = 0;
-                for (int i = 0; i < tm; ++i) {
-                    int j = prod == kProdX ? 0 : i * per;
-                    d.tiles[prod] += tn - j;
-                    auto tile = [&](int at, int flags) {
-                        return OrthoTile{k, int16_t(i), int16_t(at), int16_t(prod), int16_t(width), flags};
-                    };
-                    for (; G == 1 && j < tn; ++j) out.push_back({{tile(j, 0), {}}});
-                    if ((tn - j) & 1) single.push_back(tile(j++, 0));
-                    for (; j < tn; j += 2) out.push_back({{tile(j, kTileShared), tile(j + 1, kTileShared)}});
-                }
-                for (size_t s = 0; s < single.size(); s += 2) {
-                    const bool odd = s + 1 == single.size();
-                    out.push_back({{single[s], single[odd ? s : s + 1]}});
-                    if (odd) out.back().t[1].flags = kTileIdle;
-                }
+                const size_t before = out.size();
+                const int tm = d.cba / 4, tn = (prod == kProdX ? d.cbx : d.cba) / 4;
+                for (int i = 0; i < tm; ++i)
+                    for (int j = prod == kProdX ? 0 : i * per; j < tn * per; ++j)
+                        out.push_back({k, int16_t(i), int16_t(j), int16_t(prod), int16_t(width)});
+                d.tiles[prod] = int32_t(out.size() - before);
             }
         };
-        std::vector<Group> groups;
-        cut(128, groups);
-        if (groups.size() > most_clusters) {
-            groups.clear();
-            cut(256, groups);
+        std::vector<OrthoTile> tiles;
+        cut(128, tiles);
+        if (tiles.size() > size_t(clusters)) {
+            tiles.clear();
+            cut(256, tiles);
         }
-        most = std::max(most, groups.size());
-        all.insert(all.end(), groups.begin(), groups.end());
+        most = std::max(most, tiles.size());
+        all.insert(all.end(), tiles.begin(), tiles.end());
     }
-    M.clusters = int32_t(std::min(most_clusters, most));
-    std::vector<std::vector<OrthoTile>> mine(size_t(M.clusters));
+    M.pairs = int32_t(std::min<size_t>(size_t(clusters), most));
+    std::vector<std::vector<OrthoTile>> mine(size_t(M.pairs));
     std::vector<int64_t> ready(M.mats.size() * 4, 0);   // when the tiles of a product can start
     using Free = std::pair<int64_t, int32_t>;
-    std::priority_queue<Free, std::vector<Free>, std::greater<Free>> idle;   // {time, cluster}
-    for (int32_t p = 0; p < M.clusters; ++p) idle.push({0, p});
-    for (const Group& g : all) {
-        const OrthoTile& t = g.t[0];
+    std::priority_queue<Free, std::vector<Free>, std::greater<Free>> idle;   // {time, pair}
+    for (int32_t p = 0; p < M.pairs; ++p) idle.push({0, p});
+    for (const OrthoTile& t : all) {
         const MatDesc& d = M.mats[size_t(t.mat)];
         const Free f = idle.top();
         idle.pop();
@@ -234,14 +203,14 @@ void lay_queue(Matrices& M, const int resident[2]) {
         const int64_t end = start + std::max<int64_t>(3 * (t.prod == kProdA ? d.kn : d.km), 25) + 2;
         int64_t& next = ready[size_t(t.mat) * 4 + size_t(t.prod) + 1];
         next = std::max(next, end);
-        mine[size_t(f.second)].insert(mine[size_t(f.second)].end(), g.t, g.t + G);
+        mine[size_t(f.second)].push_back(t);
         idle.push({end, f.second});
     }
     M.queue.clear();
     M.queue_first.assign(1, 0);
     for (const auto& q : mine) {
         M.queue.insert(M.queue.end(), q.begin(), q.end());
-        M.queue_first.push_back(int32_t(M.queue.size() / size_t(G)));
+        M.queue_first.push_back(int32_t(M.queue.size()));
     }
 }
 

@@ -67,7 +67,7 @@ struct OrthoArgs {
     int32_t* count;          // per matrix: norm items done (zero between launches)
     int32_t* status;         // 0, or the error of the first wait that ran out
     int32_t* done;           // per matrix and product: CTA tiles finished in this call
-    const OrthoTile* queue;  // tiles of a step in groups, cluster c's at [queue_first[c], queue_first[c + 1])
+    const OrthoTile* queue;  // tiles of a step, pair p's at [queue_first[p], queue_first[p + 1])
     const int32_t* queue_first;
     const void* update;
     int32_t f32;             // update holds fp32 (else bf16)
@@ -367,29 +367,27 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 
 // ---------------------------------------------------------------------------
 // The steps.  One persistent kernel runs every product of every step.  A pair
-// of CTAs on two SMs computes 256 x 256 tiles: CTA r holds rows 128 r .. of the
-// left operand and columns 128 r .. of the right one, 32 KB per 64-deep stage
-// and SM, and the pair's tcgen05.mma (cta_group::2) reads both halves.  A 128 x
-// 256 tile on one SM would need 48 KB per stage for the same arithmetic.
+// of CTAs on two SMs (a cluster of 2) computes 256 x 256 tiles: CTA r holds
+// rows 128 r .. of the left operand and columns 128 r .. of the right one, 32
+// KB per 64-deep stage and SM, and the pair's tcgen05.mma (cta_group::2) reads
+// both halves.  A 128 x 256 tile on one SM would need 48 KB per stage for the
+// same arithmetic.
 //
-// Even 32 KB per stage are more than L2 delivers to 152 SMs at the tensor
-// cores' rate (15 TB/s), so where there are tiles enough (see lay_queue) two
-// pairs form a cluster, take two neighbours of a row of tiles, and fetch the
-// left operand once: each CTA copies half of its rows to itself and to its
-// counterpart in the other pair (multicast), 24 KB per stage and SM.
+// Two pairs that share a left operand by multicast (clusters of four, 24 KB per
+// stage and SM) were 3 % slower on every list tried, 144 SMs in use instead of
+// 152: what limits large matrices is the power cap, not L2.
 //
-// Every cluster works through a queue of tiles that the host laid out once
+// Every pair works through a queue of tiles that the host laid out once
 // (balanced by cost), the same in every step: A tiles, B tiles, X tiles of all
 // matrices.  A tile starts when its matrix's tiles of the product before are
 // done (a counter per matrix and product in device memory), so matrices
 // overlap at the ends of their products and a step needs no launch.  Queues
-// follow one global order and all clusters are resident (cooperative launch),
-// so the oldest unfinished tile can always run.
+// follow one global order and all pairs are resident (cooperative launch), so
+// the oldest unfinished tile can always run.
 //
 // Roles per CTA:
 //   warp 0       copies operands (TMA, kStages ahead)
-//   warp 1       of a pair's first CTA: issues the products into one of two
-//                accumulators
+//   warp 1       of CTA 0: issues the products into one of two accumulators
 //   warps 2..9   finish the other accumulator, 64 columns at a time in one of
 //                two shared-memory slots (warp w: tensor-memory lanes 32 (w mod
 //                4), 32 of the 64 columns; four warps to each slot side by side
@@ -510,14 +508,6 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
                  " [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
 }
-// the same into this CTA's and the counterparts' memory (the CTAs of `mask`);
-// each one's arrival is counted at its pair's first CTA
-__device__ __forceinline__ void copy_box_to(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar,
-                                            uint16_t mask) {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;"
-                 :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar), "h"(mask) : "memory");
-}
 __device__ __forceinline__ void copy_in(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
@@ -530,7 +520,7 @@ __device__ __forceinline__ void copy_out(void* dst, uint32_t src, uint32_t bytes
 // Shared-memory descriptors of the 128-byte swizzle: rows of 64 K-values (8
 // rows every 1024 bytes), or 64-column groups (8 K-rows every 1024 bytes, the
 // next 64 columns 8192 bytes on).  The upper bits of a shared address name the
-// CTA of the cluster; in the descriptor they would reach into the next field.
+// CTA of the cluster and stay out of the descriptor.
 __device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool by_column) {
     return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(by_column ? 8192 >> 4 : 1) << 16) |
            (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
@@ -545,10 +535,10 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
                  " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
                  :: "r"(d), "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u) : "memory");
 }
-// arrives at `bar` of the CTAs of `mask` once every product issued so far is done
-__device__ __forceinline__ void commit_to(uint64_t* bar, uint32_t mask) {
+// arrives at `bar` of both CTAs once every product issued so far is done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(smem_u32(bar)), "h"(uint16_t(mask)) : "memory");
+                 :: "r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
 }
 __device__ __forceinline__ void load_acc32(uint32_t tmem, float* v) {
     uint32_t r[32];
@@ -766,8 +756,7 @@ __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& 
     return wait_count(sh, a.done + 3 * mat + before, target, a.status);
 }
 
-template <int PAIRS>
-__global__ void __cluster_dims__(2 * PAIRS) __launch_bounds__(kOrthoThreads, 1)
+__global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
 k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
               const __grid_constant__ CUtensorMap rows64) {
     // the kernel's only shared memory: starts on a multiple of 1 KB, as the swizzle wants it
@@ -776,14 +765,12 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     const uint32_t stage0 = smem_u32(dyn);
     const uint32_t slot0 = stage0 + uint32_t(kStages) * kStageBytes;
     const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
-    // CTA 0 or 1 of its pair, pair 0 or 1 of the cluster
-    const uint32_t in_cluster = cluster_rank(), rank = in_cluster & 1;
-    const uint32_t which = PAIRS == 2 ? in_cluster >> 1 : 0, first = 2 * which;
-    const int cluster = int(blockIdx.x) / (2 * PAIRS);
+    const uint32_t rank = cluster_rank();
+    const int pair = int(blockIdx.x >> 1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], PAIRS);   // a stage may be filled from both pairs
+            mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.tfull[b], 1);
@@ -805,21 +792,19 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     pdl_enter();
     const uint32_t tmem = sh.tmem;
-    const int q0 = __ldg(a.queue_first + cluster), q1 = __ldg(a.queue_first + cluster + 1);
-    const OrthoTile* queue = a.queue + which;   // tile t of this pair: queue[PAIRS t]
+    const int q0 = __ldg(a.queue_first + pair), q1 = __ldg(a.queue_first + pair + 1);
 
     if (warp == 0 && lane == 0) {
         // ---- operands ----
         // (what the loop over K needs is in registers: the copies' memory
         // clobbers would have a value of the descriptor loaded again for each)
-        const uint32_t full0 = map_to(smem_u32(&sh.full[0]), first);
-        const uint16_t mask = uint16_t(5u << rank);   // this CTA and its counterpart
+        const uint32_t full0 = map_to(smem_u32(&sh.full[0]), 0);
         int s = 0;
         uint32_t par = 1;             // the first pass over the ring finds it empty
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             for (int t = q0; t < q1 && ok; ++t) {
-                const OrthoTile tile = queue[PAIRS * t];
+                const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod;
                 const int64_t x = d.x[step & 1];
@@ -837,10 +822,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     const uint32_t bar = full0 + uint32_t(s) * 8;
                     if (rank == 0) mbar_expect(&sh.full[s], bytes);
                     const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
-                    if (PAIRS == 2 && (tile.flags & kTileShared))
-                        copy_box_to(dst + which * 8192, &rows64, left + kb * kBlkRows + int(which) * 64, bar, mask);
-                    else
-                        copy_box(dst, &rows128, left + kb * kBlkRows, bar);
+                    copy_box(dst, &rows128, left + kb * kBlkRows, bar);
                     if (prod == kProdX) {
                         const int row = right + (kb >> 1) * pitch + (kb & 1) * 64;
                         copy_box(dst + kHalfBytes, &rows64, row, bar);
@@ -862,7 +844,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             for (int t = q0; t < q1 && ok; ++t, ++it) {
-                const OrthoTile tile = queue[PAIRS * t];
+                const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const bool by_column = tile.prod == kProdX;
                 const uint32_t shape = mma_shape(by_column, tile.width);
@@ -879,13 +861,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     for (int k = 0; k < 4; ++k)   // 16 deep each
                         mma_pair(tmem + uint32_t(buf) * kOrthoTile, left + 2 * k,
                                  right + (by_column ? 128 : 2) * k, shape, (kb | k) != 0);
-                    commit_to(&sh.empty[s], PAIRS == 2 ? 15u : 3u);
+                    commit_pair(&sh.empty[s]);
                     if (++s == kStages) {
                         s = 0;
                         par ^= 1;
                     }
                 }
-                if (ok) commit_to(&sh.tfull[buf], 3u << first);
+                if (ok) commit_pair(&sh.tfull[buf]);
             }
         }
     } else if (warp == kSlotWarp && lane == 0) {
@@ -896,8 +878,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
-                const OrthoTile tile = queue[PAIRS * t];
-                if (PAIRS == 2 && (tile.flags & kTileIdle)) continue;
+                const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, blocks = tile.width >> 6, c0 = tile.j * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
@@ -967,24 +948,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
-                const OrthoTile tile = queue[PAIRS * t];
+                const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, buf = it & 1, blocks = tile.width >> 6, c0 = tile.j * tile.width;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
-                auto release = [&] {     // the accumulator is free for the tile after next
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                                     :: "r"(map_to(smem_u32(&sh.tempty[buf]), first)) : "memory");
-                };
-                if (PAIRS == 2 && (tile.flags & kTileIdle)) {
-                    ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
-                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-                    release();
-                    continue;
-                }
                 if (lane == 0) ok = wait_operands(sh, a, d, tile.mat, prod, step);
                 if (!(ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0) != 0)) break;
                 // what the rows need, fetched while the product runs
@@ -1011,7 +979,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     const uint32_t sl = n & 1, slot = slot0 + sl * kSlotBytes;
                     float acc[32];
                     load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(row0) << 16), acc);
-                    if (g + 1 == blocks) release();
+                    if (g + 1 == blocks) {   // the accumulator is free for the tile after next
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                                         :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
+                    }
                     ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a.status);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     if (prod == kProdA) {
@@ -1092,35 +1066,31 @@ int upload_matrices(Matrices& m) {
                         m.device, dev);
         return DPG_OK;
     }
-    // how many clusters are resident at once decides the queues
-    int resident[2] = {1, 0};
+    // how many CTA pairs are resident at once decides the queues
+    int clusters = 1;
     if (!m.mats.empty()) {
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_load<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           2 * kLoadSmem));
-        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
-        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
-        for (int pairs = 1; pairs <= 2; ++pairs) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(unsigned(2 * pairs));
-            cfg.blockDim = dim3(kOrthoThreads);
-            cfg.dynamicSmemBytes = kOrthoSmem;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = unsigned(2 * pairs);
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            DPG_CUDA_TRY(pairs == 1 ? cudaOccupancyMaxActiveClusters(&resident[0], k_ortho_steps<1>, &cfg)
-                                    : cudaOccupancyMaxActiveClusters(&resident[1], k_ortho_steps<2>, &cfg));
-        }
-        if (resident[0] < 1) return fail(DPG_ERR_CUDA, "matrices upload: no cluster fits this device");
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kOrthoThreads);
+        cfg.dynamicSmemBytes = kOrthoSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps, &cfg));
+        if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no CTA pair fits this device");
     }
     if (!m.small.empty()) {
         const int st = gram_prepare();
         if (st != DPG_OK) return st;
     }
     try {
-        lay_queue(m, resident);
+        lay_queue(m, clusters);
     } catch (const std::exception&) {
         return fail(DPG_ERR_OOM, "matrices upload: out of host memory");
     }
@@ -1242,17 +1212,16 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(2 * m.cluster_pairs * m.clusters));
+    cfg.gridDim = dim3(unsigned(2 * m.pairs));
     cfg.blockDim = dim3(kOrthoThreads);
     cfg.dynamicSmemBytes = kOrthoSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;   // the clusters wait for one another
+    attr[0].id = cudaLaunchAttributeCooperative;   // the pairs wait for one another
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = m.cluster_pairs == 2 ? cudaLaunchKernelEx(&cfg, k_ortho_steps<2>, a, map[0], map[1])
-                                               : cudaLaunchKernelEx(&cfg, k_ortho_steps<1>, a, map[0], map[1]);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_steps, a, map[0], map[1]);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));

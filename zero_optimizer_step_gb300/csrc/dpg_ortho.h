@@ -44,15 +44,11 @@ struct MatDesc {
 };
 
 // One output tile of one product of one matrix: 256 rows from 256 i, `width`
-// (256 or 128) columns from width j.  Queues hold them in groups, one tile for
-// each CTA pair of a cluster, of the same matrix, product and width.
-enum : int { kTileShared = 1,    // both tiles of the group have the same rows
-             kTileIdle = 2 };    // computed to keep step with the other, not stored
+// (256 or 128) columns from width j.
 struct OrthoTile {
     int32_t mat;
     int16_t i, j;
     int16_t prod, width;
-    int32_t flags;
 };
 
 // Matrices whose shorter side is at most kSmallSide take the steps on their
@@ -105,9 +101,9 @@ struct Matrices {
     int32_t n_params = 0;
     std::vector<int64_t> param_offset, numels;
     std::vector<MatDesc> mats;
-    std::vector<OrthoTile> queue;      // tiles of a step, cluster after cluster (see lay_queue)
-    std::vector<int32_t> queue_first;  // clusters + 1, in groups of tiles
-    int32_t clusters = 0, cluster_pairs = 1;
+    std::vector<OrthoTile> queue;      // tiles of a step, pair after pair (see lay_queue)
+    std::vector<int32_t> queue_first;  // pairs + 1
+    int32_t pairs = 0;
     std::vector<SmallDesc> small;
     std::vector<SmallItem> gram_items, prod_items;
     std::vector<int32_t> small_order;  // small matrices by padded side
@@ -141,9 +137,8 @@ struct Matrices {
     alignas(64) unsigned char maps[2][128];   // tensor maps of the workspace: 128 and 64 rows a copy
 };
 
-// fills queue, queue_first, clusters and cluster_pairs for a device that holds
-// resident[p - 1] clusters of p CTA pairs
-void lay_queue(Matrices& m, const int resident[2]);
+// fills queue, queue_first and pairs for a device that holds `clusters` CTA pairs
+void lay_queue(Matrices& m, int clusters);
 // device side (dpg_ortho.cu)
 int upload_matrices(Matrices& m);
 void release_matrices(Matrices& m);
