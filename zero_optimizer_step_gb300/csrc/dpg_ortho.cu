@@ -103,6 +103,36 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t unpack_pair(uint32_t h) {
+    const float2 f = unpack_half2(h);
+    return pair_of(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t p) {
+    const float2 f = halves_of(p);
+    return pack_half2(f.x, f.y);
+}
+
 // scale * (1 + the rounding pattern) for columns c = 0, 1, 2, 3 (mod 4) of a
 // row; a unit in the last place is 2^-11 to 2^-10 of a value, taken as 1.4 * 2^-11
 struct RoundScale {
@@ -116,6 +146,8 @@ struct RoundScale {
             v[j] = fmaf(scale * q, w, scale);
         }
     }
+    // for columns 2 j, 2 j + 1
+    __device__ __forceinline__ uint64_t pair(int j) const { return pair_of(v[2 * j & 3], v[(2 * j + 1) & 3]); }
 };
 
 // ---------------------------------------------------------------------------
@@ -392,10 +424,12 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 //                two shared-memory slots (warp w: tensor-memory lanes 32 (w mod
 //                4), 32 of the 64 columns; four warps to each slot side by side
 //                were a third slower, the slots then come free together)
-//   warp 10      fills the slots with what the finish needs (hi and lo of X,
-//                or the tile of A) and writes them out, as whole contiguous
-//                blocks; row-wise 16-byte accesses from the finishing warps
-//                themselves took 22 to 29 us per tile, four times the product
+//   warps 10, 11 fill the slots with what the finish needs (hi and lo of X, or
+//                the tile of A) and write them out, as whole contiguous blocks
+//                (two warps: the next tile's first blocks come in while this
+//                tile's last ones are on their way to memory).  Row-wise
+//                16-byte accesses from the finishing warps themselves took 22
+//                to 29 us per tile, four times the product.
 // ---------------------------------------------------------------------------
 constexpr int kStages = 5;
 constexpr int kHalfBytes = 128 * 64 * 2;              // one operand of one stage in one CTA
@@ -403,8 +437,8 @@ constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kSlots = 2;
 constexpr int kSlotBytes = 2 * int(kBlkBytes);        // hi | lo, or the tile | its transpose
 constexpr int kEpiWarps = 8;
-constexpr int kSlotWarp = 2 + kEpiWarps;
-constexpr int kOrthoThreads = 32 * (kSlotWarp + 1);
+constexpr int kFillWarp = 2 + kEpiWarps, kStoreWarp = kFillWarp + 1;
+constexpr int kOrthoThreads = 32 * (kStoreWarp + 1);
 constexpr uint64_t kWaitNs = 2000000000ull;           // bound of every wait
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -455,7 +489,8 @@ __device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
 
 // What the roles of a CTA share.
 struct OrthoShared {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], in_full[kSlots], out_ready[kSlots];
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], in_full[kSlots], out_ready[kSlots],
+        slot_free[kSlots];
     float cols[kEpiWarps][32];   // a finishing warp's 32 values of A's diagonal
     uint32_t tmem;
     volatile int abort;     // some wait of this CTA ran out, or of another one
@@ -573,14 +608,14 @@ __device__ __forceinline__ void sts16(uint32_t at, uint32_t x) {
 // ---------------------------------------------------------------------------
 // What a product does with 32 consecutive sums acc: row `row` (0..127) of the
 // CTA's rows, columns 32 h .. of the 64 in slot `slot`; r and c0 are the row
-// and first column in the matrix.
+// and first column in the matrix.  All of a slot's values are loaded before
+// the first is stored, and the arithmetic is in pairs: a warp's time here is
+// issue slots and shared-memory latency, and there are only two warps per
+// scheduler to hide it.
 // ---------------------------------------------------------------------------
 // writes 32 fp16 values into the block at `slot`, and transposed behind it:
 // two groups of 64 rows (the columns) by 64 columns (the rows)
-__device__ __forceinline__ void put_sym(uint32_t slot, int row, int h, const float* v, bool mirror) {
-    uint32_t x[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = pack_half2(v[2 * j], v[2 * j + 1]);
+__device__ __forceinline__ void put_sym(uint32_t slot, int row, int h, const uint32_t* x, bool mirror) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         sts128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4), x[4 * q], x[4 * q + 1], x[4 * q + 2],
@@ -593,6 +628,13 @@ __device__ __forceinline__ void put_sym(uint32_t slot, int row, int h, const flo
         for (int j = 0; j < 32; ++j)
             sts16(base + j * 128 + ((ch ^ (j & 7)) << 4), (j & 1) ? x[j >> 1] >> 16 : x[j >> 1] & 0xFFFFu);
     }
+}
+
+// the packed values x[16] with the one of column `lane` set to zero
+__device__ __forceinline__ void clear_diagonal(uint32_t* x, int lane) {
+    const uint32_t keep = (lane & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] &= j == (lane >> 1) ? keep : 0xFFFFFFFFu;
 }
 
 // A_rr from the row's sums of squares: sixteen loads at a time, or their
@@ -613,26 +655,32 @@ __device__ __forceinline__ float row_square(const OrthoArgs& a, const MatDesc& d
 }
 
 // diag: the row's sum of squares of X where the columns hold A's diagonal
-__device__ __forceinline__ void finish_a(const OrthoArgs& a, const OrthoStep& s, const MatDesc& d, float inv_sx,
-                                         uint32_t slot, int row, int h, int r, int c0, float* acc,
+__device__ __forceinline__ void finish_a(const OrthoArgs& a, const OrthoStep& s, int64_t diag_at, float inv_sx,
+                                         uint32_t slot, int row, int h, int r, int c0, const float* acc,
                                          bool mirror, float diag) {
     const float k = inv_sx * inv_sx;
     const RoundScale rs(s.sa * k, r);
+    const uint64_t r0 = rs.pair(0), r1 = rs.pair(1);
+    uint32_t x[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) acc[j] *= rs.v[j & 3];
+    for (int j = 0; j < 16; ++j) x[j] = pack_pair(mul2(pair_of(acc[2 * j], acc[2 * j + 1]), (j & 1) ? r1 : r0));
     const int lane = row & 31;
     if (r - lane == c0) {       // the warp's rows are these columns
-        a.diag_a[d.diag + r] = diag * k;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[j] = j == lane ? 0.0f : acc[j];
+        a.diag_a[diag_at + r] = diag * k;
+        clear_diagonal(x, lane);
     }
-    put_sym(slot, row, h, acc, mirror);
+    put_sym(slot, row, h, x, mirror);
 }
 
 // dr: A_rr; cols: A_cc of the 32 columns, in shared memory
-__device__ __forceinline__ void finish_b(const OrthoArgs& a, const OrthoStep& s, const MatDesc& d, uint32_t slot,
-                                         int row, int h, int r, int c0, float* acc, bool mirror, float dr,
+__device__ __forceinline__ void finish_b(const OrthoArgs& a, const OrthoStep& s, int64_t diag_at, uint32_t slot,
+                                         int row, int h, int r, int c0, const float* acc, bool mirror, float dr,
                                          uint32_t cols) {
+    uint4 f4[4], e4[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f4[q] = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) e4[q] = lds128(cols + 16 * q);
     // c (F F^T) + (b + c (D_r + D_c)) F, F in fp16 under the scale of A
     const float k = s.c * s.inv_sa * s.inv_sa, fb = fmaf(s.c, dr, s.b) * s.inv_sa, fc = s.c * s.inv_sa;
     const int lane = row & 31;
@@ -643,68 +691,68 @@ __device__ __forceinline__ void finish_b(const OrthoArgs& a, const OrthoStep& s,
         for (int j = 0; j < 32; ++j) ff = j == lane ? acc[j] : ff;
         const float d2 = dr * dr, aa = fmaf(ff * s.inv_sa, s.inv_sa, d2);   // (A A^T)_rr
         const float db = fmaf(fmaf(s.c, dr, s.b), dr, k * ff);
-        a.diag_b[d.diag + r] = db;
-        a.diag_t[d.diag + r] = aa > 0.0f ? db * (d2 / aa) : 0.0f;
+        a.diag_b[diag_at + r] = db;
+        a.diag_t[diag_at + r] = aa > 0.0f ? db * (d2 / aa) : 0.0f;
     }
     const RoundScale rs(s.sb, r);
+    const uint64_t r0 = rs.pair(0), r1 = rs.pair(1);
+    const uint64_t k2 = pair_of(k, k), fb2 = pair_of(fb, fb), fc2 = pair_of(fc, fc);
+    uint32_t x[16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint4 f4 = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
-        const uint4 e0 = lds128(cols + 32 * q), e1 = lds128(cols + 32 * q + 16);
-        const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
-        const uint32_t dc[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 p = unpack_half2(f[j >> 1]);
-            const float fv = (j & 1) ? p.y : p.x;
-            const float v = fmaf(k, acc[8 * q + j], fmaf(fc, __uint_as_float(dc[j]), fb) * fv);
-            acc[8 * q + j] = v * rs.v[j & 3];
-        }
+    for (int j = 0; j < 16; ++j) {
+        const uint4 f = f4[j >> 2], e = e4[j >> 1];
+        const uint32_t fw = (j & 3) == 0 ? f.x : (j & 3) == 1 ? f.y : (j & 3) == 2 ? f.z : f.w;
+        const uint64_t dc = (j & 1) ? pair_of(__uint_as_float(e.z), __uint_as_float(e.w))
+                                    : pair_of(__uint_as_float(e.x), __uint_as_float(e.y));
+        const uint64_t v = fma2(k2, pair_of(acc[2 * j], acc[2 * j + 1]), mul2(fma2(fc2, dc, fb2), unpack_pair(fw)));
+        x[j] = pack_pair(mul2(v, (j & 1) ? r1 : r0));
     }
-    if (diag) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[j] = j == lane ? 0.0f : acc[j];
-    }
-    put_sym(slot, row, h, acc, mirror);
+    if (diag) clear_diagonal(x, lane);
+    put_sym(slot, row, h, x, mirror);
 }
 
 // ah, al: factors of hi and lo; k: of the sums.  Returns the sum of squares of
-// the new (scaled) X.  The last step leaves bf16 values in the slot instead.
-__device__ __forceinline__ float finish_x(const OrthoStep& s, uint32_t slot, int row, int h, int r, float* acc,
-                                          float ah, float al, float k, bool has_lo, bool last) {
+// the new X.  The last step leaves bf16 values in the slot instead.
+__device__ __forceinline__ float finish_x(const OrthoStep& s, uint32_t slot, int row, int h, int r,
+                                          const float* acc, float ah, float al, float k, bool has_lo, bool last) {
+    uint4 h4[4], l4[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h4[q] = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        l4[q] = has_lo ? lds128(slot + uint32_t(kBlkBytes) + row * 128 + (((4 * h + q) ^ (row & 7)) << 4))
+                       : make_uint4(0, 0, 0, 0);
     const RoundScale rs(s.sx_next, r);
-    float sq = 0.0f;
+    const uint64_t r0 = rs.pair(0), r1 = rs.pair(1);
+    const uint64_t k2 = pair_of(k, k), ah2 = pair_of(ah, ah), al2 = pair_of(al, al);
+    const float up = s.sx_next * kLoScale;
+    const uint64_t up2 = pair_of(up, up), down2 = pair_of(-kLoScale, -kLoScale);
+    uint64_t sq = 0;   // two zeros
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint32_t at = slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4);
-        const uint4 h4 = lds128(at);
-        const uint4 l4 = has_lo ? lds128(at + uint32_t(kBlkBytes)) : make_uint4(0, 0, 0, 0);
-        const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w}, lo[4] = {l4.x, l4.y, l4.z, l4.w};
+        const uint32_t hi[4] = {h4[q].x, h4[q].y, h4[q].z, h4[q].w}, lo[4] = {l4[q].x, l4[q].y, l4[q].z, l4[q].w};
         uint32_t nh[4], nl[4];
-        float x[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 u = unpack_half2(hi[j]), w = unpack_half2(lo[j]);
-            x[2 * j] = fmaf(ah, u.x, fmaf(al, w.x, k * acc[8 * q + 2 * j]));
-            x[2 * j + 1] = fmaf(ah, u.y, fmaf(al, w.y, k * acc[8 * q + 2 * j + 1]));
-        }
-        if (last) {
-            const uint4 o = narrow8(x);
-            sts128(at, o.x, o.y, o.z, o.w);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u = x[2 * j] * s.sx_next, w = x[2 * j + 1] * s.sx_next;
-                sq = fmaf(u, u, fmaf(w, w, sq));
-                nh[j] = pack_half2(x[2 * j] * rs.v[2 * j & 3], x[2 * j + 1] * rs.v[(2 * j + 1) & 3]);
-                const float2 f = unpack_half2(nh[j]);
-                nl[j] = pack_half2((u - f.x) * kLoScale, (w - f.y) * kLoScale);
+            const uint64_t sum = pair_of(acc[8 * q + 2 * j], acc[8 * q + 2 * j + 1]);
+            const uint64_t x = fma2(ah2, unpack_pair(hi[j]), fma2(al2, unpack_pair(lo[j]), mul2(k2, sum)));
+            if (last) {
+                const float2 f = halves_of(x);
+                const __nv_bfloat162 o = __floats2bfloat162_rn(f.x, f.y);
+                nh[j] = *reinterpret_cast<const uint32_t*>(&o);
+            } else {
+                sq = fma2(x, x, sq);
+                nh[j] = pack_pair(mul2(x, (j & 1) ? r1 : r0));
+                // 2048 (x sx - hi), exactly as from the separate products
+                nl[j] = pack_pair(fma2(unpack_pair(nh[j]), down2, mul2(x, up2)));
             }
-            sts128(at, nh[0], nh[1], nh[2], nh[3]);
-            sts128(at + uint32_t(kBlkBytes), nl[0], nl[1], nl[2], nl[3]);
         }
+        const uint32_t at = slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4);
+        sts128(at, nh[0], nh[1], nh[2], nh[3]);
+        if (!last) sts128(at + uint32_t(kBlkBytes), nl[0], nl[1], nl[2], nl[3]);
     }
-    return sq;
+    const float2 f = halves_of(sq);
+    return f.x + f.y;
 }
 
 // A warp's 32 rows x 32 columns of bf16 results from the slot to the flat
@@ -777,6 +825,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             mbar_init(&sh.tempty[b], 2 * kEpiWarps);
             mbar_init(&sh.in_full[b], 1);
             mbar_init(&sh.out_ready[b], kEpiWarps);
+            mbar_init(&sh.slot_free[b], 1);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -870,43 +919,56 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 if (ok) commit_pair(&sh.tfull[buf]);
             }
         }
-    } else if (warp == kSlotWarp && lane == 0) {
-        // ---- slots ----
+    } else if (warp == kFillWarp && lane == 0) {
+        // ---- slots in ----
         uint32_t n = 0;               // 64-column blocks so far; block n uses slot n mod 2
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
+            for (int t = q0; t < q1 && ok; ++t) {
+                const OrthoTile tile = a.queue[t];
+                const MatDesc& d = a.mats[tile.mat];
+                const int prod = tile.prod, blocks = tile.width >> 6;
+                const int64_t blk = int64_t(tile.i * 2 + int(rank)) * (prod == kProdX ? d.cbx : d.cba) + tile.j * blocks;
+                const unsigned char* in = a.ws + ((prod == kProdB ? d.a : d.x[step & 1]) + blk) * kBlkBytes;
+                const unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
+                const bool two = prod == kProdX && has_lo;
+                if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
+                for (int g = 0; g < blocks; ++g, ++n) {
+                    const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
+                    if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a.status))) break;
+                    if (prod == kProdA) {
+                        mbar_arrive(&sh.in_full[sl]);
+                        continue;
+                    }
+                    mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (two ? 2 : 1));
+                    copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
+                    if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
+                }
+            }
+        }
+    } else if (warp == kStoreWarp && lane == 0) {
+        // ---- slots out ----
+        uint32_t n = 0;               // as above
+        bool ok = true;
+        for (int step = 0; step < a.n_steps && ok; ++step) {
+            const bool last = step + 1 == a.n_steps;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, blocks = tile.width >> 6, c0 = tile.j * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
                 const int cb = prod == kProdX ? d.cbx : d.cba;
-                // the CTA's first block in memory, in and out, and its mirror image's columns
+                // the CTA's first block in memory, and its mirror image's columns
                 const int64_t blk = int64_t(tile.i * 2 + int(rank)) * cb + c0;
-                const unsigned char* in = a.ws + ((prod == kProdB ? d.a : d.x[step & 1]) + blk) * kBlkBytes;
                 unsigned char* out = a.ws + ((prod == kProdA ? d.a : prod == kProdB ? d.b : d.x[(step + 1) & 1]) +
                                              blk) * kBlkBytes;
                 unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
                 unsigned char* image = a.ws + ((prod == kProdA ? d.a : d.b) + tile.i * 4 + int(rank) * 2) * kBlkBytes;
-                auto fill = [&](int g) {
-                    const uint32_t sl = (n + uint32_t(g)) & 1, at = slot0 + sl * kSlotBytes;
-                    if (prod == kProdA) {
-                        mbar_arrive(&sh.in_full[sl]);
-                        return;
-                    }
-                    const bool two = prod == kProdX && has_lo;
-                    mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (two ? 2 : 1));
-                    copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
-                    if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
-                };
-                if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
-                fill(0);
-                fill(1);
-                for (int g = 0; g < blocks && ok; ++g) {
-                    const uint32_t k = n + uint32_t(g), sl = k & 1, at = slot0 + sl * kSlotBytes;
-                    if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (k >> 1) & 1, a.status))) break;
+                int32_t* done = a.done + 3 * tile.mat + prod;
+                for (int g = 0; g < blocks; ++g, ++n) {
+                    const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
+                    if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (n >> 1) & 1, a.status))) break;
                     if (prod != kProdX) {
                         copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
                         if (mirror) {     // 64 rows from this block's first column, 2 x 64 columns
@@ -919,23 +981,19 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                         copy_out(lo + g * kBlkBytes, at + uint32_t(kBlkBytes), uint32_t(kBlkBytes));
                     }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    if (g + kSlots < blocks) {         // fill the slot again once it has been read
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        fill(g + kSlots);
-                    }
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    mbar_arrive(&sh.slot_free[sl]);
                 }
-                n += uint32_t(blocks);
                 if (!ok) break;
                 // all of the tile is in memory before its count
                 asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __threadfence();
-                asm volatile("red.release.gpu.global.add.s32 [%0], 1;"
-                             :: "l"(a.done + 3 * tile.mat + prod) : "memory");
+                asm volatile("red.release.gpu.global.add.s32 [%0], 1;" :: "l"(done) : "memory");
             }
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    } else if (warp >= 2 && warp < kSlotWarp) {
+    } else if (warp >= 2 && warp < kFillWarp) {
         // ---- finish ----
         const int quad = warp & 3, half = (warp - 2) >> 2;   // the warp's rows, its 32 columns of 64
         const int row0 = quad * 32, row = row0 + lane;
@@ -944,7 +1002,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t n = 0;               // as above
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const OrthoStep& s = a.st[step];
+            const OrthoStep s = a.st[step];
             const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
@@ -952,6 +1010,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, buf = it & 1, blocks = tile.width >> 6, c0 = tile.j * tile.width;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
+                const int64_t diag_at = d.diag;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
                 if (lane == 0) ok = wait_operands(sh, a, d, tile.mat, prod, step);
                 if (!(ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0) != 0)) break;
@@ -980,27 +1039,29 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     float acc[32];
                     load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(row0) << 16), acc);
                     if (g + 1 == blocks) {   // the accumulator is free for the tile after next
+                        // (its values are in registers: relaxed, a release would first wait for
+                        // this warp's stores, a microsecond)
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                         __syncwarp();
                         if (lane == 0)
-                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
                                          :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
                     }
                     ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a.status);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     if (prod == kProdA) {
-                        finish_a(a, s, d, inv_sx, slot, row, half, r, c, acc, mirror, p0);
+                        finish_a(a, s, diag_at, inv_sx, slot, row, half, r, c, acc, mirror, p0);
                     } else if (prod == kProdB) {
                         __syncwarp();
                         cols[lane] = g == 0 ? dc[0] : g == 1 ? dc[1] : g == 2 ? dc[2] : dc[3];
                         __syncwarp();
-                        finish_b(a, s, d, slot, row, half, r, c, acc, mirror, p0, smem_u32(cols));
+                        finish_b(a, s, diag_at, slot, row, half, r, c, acc, mirror, p0, smem_u32(cols));
                     } else {
                         sq += finish_x(s, slot, row, half, r, acc, p0, p1, inv_sx * s.inv_sb, has_lo, last);
                         if (last) {
                             write_out(a, d, slot, row0, half, r0, c);
                         } else if (g & 1) {   // of this warp's 32 columns in two blocks
-                            a.rowsq[d.rowsq + int64_t((c0 >> 6) + (g & 2) + half) * d.rows_pad + r] = sq;
+                            a.rowsq[d.rowsq + int64_t((c0 >> 6) + (g & 2) + half) * d.rows_pad + r] = sq * s.sx_next * s.sx_next;
                             sq = 0.0f;
                         }
                     }
