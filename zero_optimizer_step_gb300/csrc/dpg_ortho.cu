@@ -141,8 +141,10 @@ struct RoundScale {
         constexpr float q = 1.4f / 16.0f / 2048.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int k = (row + j) & 3;             // -6, 2, -2, 6 sixteenths
-            const float w = k == 0 ? -6.0f : k == 1 ? 2.0f : k == 2 ? -2.0f : 6.0f;
+            // -6, 2, -2, 6 sixteenths for (row + j) mod 4 = 0 .. 3; as a chain of selections it
+            // became a table in constant memory, 750 cycles for every use
+            const int k = row + j;
+            const float w = float((k & 1) * 8 + (k & 2) * 2 - 6);
             v[j] = fmaf(scale * q, w, scale);
         }
     }
