@@ -43,6 +43,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 #include <cstring>
 #include <exception>
@@ -492,11 +493,13 @@ __device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
 // What the roles of a CTA share.
 struct OrthoShared {
     uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], in_full[kSlots], out_ready[kSlots],
-        slot_free[kSlots];
-    float cols[kEpiWarps][32];   // a finishing warp's 32 values of A's diagonal
+        slot_free[kSlots], tile_ready;
+    alignas(16) float cols[kEpiWarps][32];   // a finishing warp's 32 values of A's diagonal (16-byte loads)
     uint32_t tmem;
     volatile int abort;     // some wait of this CTA ran out, or of another one
 };
+static_assert(offsetof(OrthoShared, cols) % 16 == 0 && (kStages * kStageBytes + kSlots * kSlotBytes) % 16 == 0,
+              "16-byte shared loads");
 constexpr int kOrthoSmem = kStages * kStageBytes + kSlots * kSlotBytes + int(sizeof(OrthoShared));
 static_assert(kOrthoSmem <= 227 * 1024, "shared memory of a CTA");
 
@@ -829,6 +832,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             mbar_init(&sh.out_ready[b], kEpiWarps);
             mbar_init(&sh.slot_free[b], 1);
         }
+        mbar_init(&sh.tile_ready, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -939,6 +943,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 for (int g = 0; g < blocks; ++g, ++n) {
                     const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
                     if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a.status))) break;
+                    // Tells the finishing warps, which so need not watch the counter in memory
+                    // themselves (ten watchers per CTA instead of two delayed it by a
+                    // microsecond).  They have all seen it for the tile before: that tile's
+                    // block in this slot is finished.
+                    if (g == 0) mbar_arrive(&sh.tile_ready);
                     if (prod == kProdA) {
                         mbar_arrive(&sh.in_full[sl]);
                         continue;
@@ -1014,8 +1023,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
                 const int64_t diag_at = d.diag;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
-                if (lane == 0) ok = wait_operands(sh, a, d, tile.mat, prod, step);
-                if (!(ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0) != 0)) break;
+                ok = wait_bounded(sh, &sh.tile_ready, uint32_t(it & 1), a.status);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 // what the rows need, fetched while the product runs
                 const float inv_sx = step == 0 ? __ldcg(&a.scal[tile.mat].y) : s.inv_sx;
                 float p0 = 0.0f, p1 = 0.0f, dc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sq = 0.0f;
