@@ -43,6 +43,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cstring>
@@ -74,6 +75,8 @@ struct OrthoArgs {
     int32_t f32;             // update holds fp32 (else bf16)
     int32_t n_steps;
     double eps;
+    float eps_frac;          // eps = eps_frac 2^eps_exp, eps_frac in [1, 2)
+    int32_t eps_exp;
     uint16_t* out;           // flat bf16
     OrthoStep st[DPG_MAX_NS_STEPS];
 };
@@ -245,15 +248,20 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (threadIdx.x == 0) {
         a.count[it.mat] = 0;
-        const double norm = sqrt(sum);
         float2 r;
-        if (!(norm <= 1.7e308)) {                       // a NaN or an infinity in the matrix
+        if (!(sum <= 1.7e308)) {                        // a NaN or an infinity in the matrix
             r.x = r.y = __int_as_float(0x7FC00000);
         } else {
-            const double den = norm > a.eps ? norm : a.eps;
-            const int k = 14 - ilogb(den);
-            r.x = float(scalbn(1.0, k));
-            r.y = float(1.0 / scalbn(den, k));
+            // sum = f 4^e, f in [1, 4): the norm is sqrt(f) 2^e (binary64 square roots and
+            // quotients cost microseconds here); below eps, eps = g 2^e instead
+            const double low = a.eps * a.eps;
+            const int e2 = int((__double_as_longlong(sum) >> 52) & 0x7FF) - 1023, e = e2 >> 1;
+            const bool small = sum < low;
+            const double unit = __longlong_as_double((long long)(1023 - 2 * e) << 52);   // 4^-e
+            const int k = 14 - (small ? a.eps_exp : e);
+            const float den = small ? a.eps_frac : sqrtf(float(sum * unit));             // in [1, 2)
+            r.x = ldexpf(1.0f, k);
+            r.y = (1.0f / 16384.0f) / den;
         }
         a.scal[it.mat] = r;
     }
@@ -1273,6 +1281,9 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.queue_first = m.d_queue_first;
     a.n_steps = hp->n_steps;
     a.eps = hp->eps;
+    int exp = 0;
+    a.eps_frac = float(2.0 * std::frexp(hp->eps, &exp));
+    a.eps_exp = exp - 1;
     a.out = static_cast<uint16_t*>(out);
     st = launch_k(a.f32 ? k_ortho_norm<true> : k_ortho_norm<false>, unsigned(m.norm_items.size()), kNormThreads,
                   s, who, a, static_cast<const NormItem*>(m.d_norm_items));
