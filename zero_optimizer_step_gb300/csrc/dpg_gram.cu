@@ -177,33 +177,48 @@ __device__ __forceinline__ void gram_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 16 rows times MP x MP, K split over the CTA's two halves: threads 0..127
-// sum the first half of K and, after adding the others' half, return the sums
-// of rows 2 ty, 2 ty + 1 and of the columns below; threads 128..255 help.
+// 16 rows times MP x MP.  The CTA's threads split K into R parts; within one, a
+// thread holds R rows by MP / 16 columns (four rows where there are columns
+// enough: half the shared-memory reads per multiply-add of two).  The parts
+// then exchange their sums, and each thread keeps one row: row() and col(j).
 template <int MP>
 struct RowProduct {
-    static constexpr int kCols = MP / 16;
-    float v[2][kCols];
-    // column of v[.][j] for thread tx
-    __device__ __forceinline__ static int col(int tx, int j) {
-        return kCols >= 4 ? (j >> 2) * 64 + tx * 4 + (j & 3) : tx * kCols + j;
+    static constexpr int kCols = MP / 16, R = MP >= 64 ? 4 : 2;
+    static constexpr int kGroup = kGramThreads / R;              // threads of a part
+    static constexpr int kExchange = R * R * kCols * kGroup;     // floats of shared memory
+    float v[kCols];
+    __device__ __forceinline__ static int tx() { return int(threadIdx.x) & 15; }
+    __device__ __forceinline__ static int ty() { return int(threadIdx.x) % kGroup >> 4; }
+    __device__ __forceinline__ static int part() { return int(threadIdx.x) / kGroup; }
+    __device__ __forceinline__ static int row() { return R * ty() + part(); }
+    __device__ __forceinline__ static int col(int j) {
+        return kCols >= 4 ? (j >> 2) * 64 + tx() * 4 + (j & 3) : tx() * kCols + j;
     }
-    __device__ __forceinline__ void run(const float* left, const float* right, float* half_sum) {
-        const int t = int(threadIdx.x) & 127, tx = t & 15, ty = t >> 4, part = int(threadIdx.x) >> 7;
+    __device__ __forceinline__ void run(const float* left, const float* right, float* exchange) {
+        float s[R][kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) v[0][j] = v[1][j] = 0.0f;
-#pragma unroll 4
-        for (int k = part * (MP / 2); k < (part + 1) * (MP / 2); k += 4) {
-            const float4 l0 = *reinterpret_cast<const float4*>(left + (2 * ty) * MP + k);
-            const float4 l1 = *reinterpret_cast<const float4*>(left + (2 * ty + 1) * MP + k);
-            const float p0[4] = {l0.x, l0.y, l0.z, l0.w}, p1[4] = {l1.x, l1.y, l1.z, l1.w};
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) s[i][j] = 0.0f;
+        left += R * ty() * MP;
+#pragma unroll 2
+        for (int k = part() * (MP / R); k < (part() + 1) * (MP / R); k += 4) {
+            float l[R][4];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float4 q = *reinterpret_cast<const float4*>(left + i * MP + k);
+                l[i][0] = q.x;
+                l[i][1] = q.y;
+                l[i][2] = q.z;
+                l[i][3] = q.w;
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 float r[kCols];
                 if constexpr (kCols >= 4) {
 #pragma unroll
                     for (int g = 0; g < kCols / 4; ++g) {
-                        const float4 q = *reinterpret_cast<const float4*>(right + (k + u) * MP + g * 64 + tx * 4);
+                        const float4 q = *reinterpret_cast<const float4*>(right + (k + u) * MP + g * 64 + tx() * 4);
                         r[4 * g] = q.x;
                         r[4 * g + 1] = q.y;
                         r[4 * g + 2] = q.z;
@@ -211,30 +226,27 @@ struct RowProduct {
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j) r[j] = right[(k + u) * MP + tx * kCols + j];
+                    for (int j = 0; j < kCols; ++j) r[j] = right[(k + u) * MP + tx() * kCols + j];
                 }
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    v[0][j] = fmaf(p0[u], r[j], v[0][j]);
-                    v[1][j] = fmaf(p1[u], r[j], v[1][j]);
-                }
-            }
-        }
-        float* h = half_sum + t;
-        if (part == 1) {
+                for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                h[(2 * j) * 128] = v[0][j];
-                h[(2 * j + 1) * 128] = v[1][j];
+                    for (int j = 0; j < kCols; ++j) s[i][j] = fmaf(l[i][u], r[j], s[i][j]);
             }
         }
+        float* e = exchange + int(threadIdx.x) % kGroup;         // [part][row][column][thread]
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i != part())
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) e[((part() * R + i) * kCols + j) * kGroup] = s[i][j];
         __syncthreads();
-        if (part == 0) {
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                v[0][j] += h[(2 * j) * 128];
-                v[1][j] += h[(2 * j + 1) * 128];
-            }
+        for (int j = 0; j < kCols; ++j) {
+            float t = 0.0f;
+#pragma unroll
+            for (int p = 0; p < R; ++p) t += p == part() ? s[p][j] : e[((p * R + part()) * kCols + j) * kGroup];
+            v[j] = t;
         }
     }
 };
@@ -245,19 +257,19 @@ struct Width {
 };
 
 template <int MP>
-__global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_constant__ GramArgs a,
-                                                            const int32_t* which) {
-    constexpr int C = MP / 16;           // CTAs of the cluster
-    extern __shared__ __align__(16) float gram_sm[];
-    float* A = gram_sm;                  // [MP][MP]
+__device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
+    constexpr int C = MP / 16;           // CTAs of the cluster that hold rows
+    if (rank >= C) {                     // the others only meet the barriers
+        for (int k = 0; k < 2 * a.n_steps + 2; ++k) gram_cluster_sync();
+        return;
+    }
+    float* A = sm;                       // [MP][MP]
     float* Q = A + MP * MP;              // [MP][MP]
     float* P = Q + MP * MP;              // [16][MP], own rows
     float* S = P + 16 * MP;              // [16][MP], own rows: A Q
-    float* half_sum = S + 16 * MP;       // 128 x 2 MP / 16
+    float* exchange = S + 16 * MP;
     __shared__ double den_sh;
     __shared__ float scale_sh;
-    pdl_enter();
-    const int rank = int(blockIdx.x) % C, mat = which[blockIdx.x / C];
     const SmallDesc d = a.mats[mat];
     const int t = int(threadIdx.x), row0 = rank * 16;
 
@@ -330,58 +342,41 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
 
     // step 0 takes A as scale * (the sum in memory)
     float scale = scale_sh;
-    const int hx = t & 15, hy = (t & 127) >> 4;
     RowProduct<MP> y;
     constexpr int kCols = RowProduct<MP>::kCols, W = kCols < 4 ? kCols : 4;
+    const int row = y.row();
     for (int step = 0; step < a.n_steps; ++step) {
-        y.run(A + row0 * MP, A, half_sum);
+        y.run(A + row0 * MP, A, exchange);
         const float ca = a.a[step], cb = a.b[step] * scale, cc = a.c[step] * scale * scale;
-        if (t < 128) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+        for (int g = 0; g < kCols; g += W) {
+            const int col = y.col(g);
+            float q[W];
 #pragma unroll
-                for (int g = 0; g < kCols; g += W) {
-                    const int row = 2 * hy + i, col = y.col(hx, g);
-                    float q[W];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        q[j] = fmaf(cc, y.v[i][g + j], cb * A[(row0 + row) * MP + col + j]);
-                        if (col + j == row0 + row) q[j] += ca;
-                    }
-                    spread(Q, row, col, q, Width<W>());
-                }
+            for (int j = 0; j < W; ++j) {
+                q[j] = fmaf(cc, y.v[g + j], cb * A[(row0 + row) * MP + col + j]);
+                if (col + j == row0 + row) q[j] += ca;
+            }
+            spread(Q, row, col, q, Width<W>());
         }
         gram_cluster_sync();
         const bool last = step + 1 == a.n_steps;
         if (step == 0) {
             for (int q = t; q < 16 * MP; q += kGramThreads) P[q] = Q[row0 * MP + q];
         } else {
-            y.run(P, Q, half_sum);       // (its barrier: every thread has read P)
-            if (t < 128) {
+            y.run(P, Q, exchange);       // (its barrier: every thread has read P)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) P[(2 * hy + i) * MP + y.col(hx, j)] = y.v[i][j];
-            }
+            for (int j = 0; j < kCols; ++j) P[row * MP + y.col(j)] = y.v[j];
         }
         if (last) break;
-        __syncthreads();                 // half_sum is free again
-        y.run(A + row0 * MP, Q, half_sum);
-        if (t < 128) {
+        __syncthreads();                 // the exchange is free again
+        y.run(A + row0 * MP, Q, exchange);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < kCols; ++j) S[(2 * hy + i) * MP + y.col(hx, j)] = y.v[i][j] * scale;
-        }
+        for (int j = 0; j < kCols; ++j) S[row * MP + y.col(j)] = y.v[j] * scale;
         __syncthreads();
-        y.run(S, Q, half_sum);
-        if (t < 128) {
+        y.run(S, Q, exchange);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int g = 0; g < kCols; g += W)
-                    spread(A, 2 * hy + i, y.col(hx, g), &y.v[i][g], Width<W>());
-        }
+        for (int g = 0; g < kCols; g += W) spread(A, row, y.col(g), &y.v[g], Width<W>());
         scale = 1.0f;
         gram_cluster_sync();
     }
@@ -392,7 +387,33 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_consta
     gram_cluster_sync();                 // no CTA leaves while others write to it
 }
 
-constexpr int gram_steps_smem(int mp) { return (2 * mp * mp + 32 * mp + 256 * (mp / 16)) * 4; }
+// All matrices of one padded side, in clusters of its size.
+template <int MP>
+__global__ void __launch_bounds__(kGramThreads) k_gram_steps(const __grid_constant__ GramArgs a,
+                                                            const int32_t* which) {
+    extern __shared__ __align__(16) float gram_sm[];
+    pdl_enter();
+    gram_steps<MP>(a, which[blockIdx.x / (MP / 16)], int(blockIdx.x) % (MP / 16), gram_sm);
+}
+
+// Matrices of any padded sides, in clusters of eight.
+__global__ void __launch_bounds__(kGramThreads) k_gram_steps_mixed(const __grid_constant__ GramArgs a) {
+    extern __shared__ __align__(16) float gram_sm[];
+    pdl_enter();
+    const int mat = int(blockIdx.x) / 8, rank = int(blockIdx.x) % 8;
+    switch (a.mats[mat].mp) {
+        case 16: return gram_steps<16>(a, mat, rank, gram_sm);
+        case 32: return gram_steps<32>(a, mat, rank, gram_sm);
+        case 64: return gram_steps<64>(a, mat, rank, gram_sm);
+        default: return gram_steps<128>(a, mat, rank, gram_sm);
+    }
+}
+
+template <int MP>
+constexpr int gram_steps_smem() {
+    return (2 * MP * MP + 32 * MP + RowProduct<MP>::kExchange) * 4;
+}
+constexpr int kMixedMost = 15;   // clusters of eight that are resident at once
 
 // ---------------------------------------------------------------------------
 // O = P U, 64 columns per CTA: a thread holds MP / 16 rows by 4 columns.
@@ -497,31 +518,34 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_apply(const __grid_consta
 // ---------------------------------------------------------------------------
 int gram_prepare() {
     DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_steps<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      gram_steps_smem(64)));
+                                      gram_steps_smem<64>()));
     DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_steps<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      gram_steps_smem(128)));
+                                      gram_steps_smem<128>()));
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_steps_mixed, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gram_steps_smem<128>()));
     DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_apply, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       gram_apply_smem(kSmallSide)));
     return DPG_OK;
 }
 
-template <int MP>
-static int launch_steps(const GramArgs& a, const int32_t* which, int n, cudaStream_t s, const char* who) {
+template <typename... P, typename... A>
+static int launch_clusters(void (*k)(P...), int n, int ctas, int smem, cudaStream_t s, const char* who,
+                           const A&... args) {
     if (n == 0) return DPG_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(n) * (MP / 16));
+    cfg.gridDim = dim3(unsigned(n) * unsigned(ctas));
     cfg.blockDim = dim3(kGramThreads);
-    cfg.dynamicSmemBytes = gram_steps_smem(MP);
+    cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = MP / 16;
+    attr[0].val.clusterDim.x = unsigned(ctas);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = t_programmatic ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_gram_steps<MP>, a, which);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
@@ -561,14 +585,24 @@ int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* h
                 const char* who) {
     if (m.small.empty()) return DPG_OK;
     const GramArgs a = gram_args(m, update, hp, out);
-    const int32_t* w = m.d_small_order;
-    int st = launch_steps<16>(a, w, m.small_count[0], s, who);
-    w += m.small_count[0];
-    if (st == DPG_OK) st = launch_steps<32>(a, w, m.small_count[1], s, who);
-    w += m.small_count[1];
-    if (st == DPG_OK) st = launch_steps<64>(a, w, m.small_count[2], s, who);
-    w += m.small_count[2];
-    if (st == DPG_OK) st = launch_steps<128>(a, w, m.small_count[3], s, who);
+    const int32_t *w = m.d_small_order, *n = m.small_count;
+    int st = DPG_OK;
+    if ((n[0] > 0) + (n[1] > 0) + (n[2] > 0) + (n[3] > 0) > 1 && int(m.small.size()) <= kMixedMost) {
+        // one launch side by side instead of one per padded side: sides of 16, 32, 64 and 128 took
+        // 11, 15, 30 and 75 us one after the other.  With more matrices than clusters of eight fit,
+        // the smaller sides would wait for places as large as the largest needs.
+        const int smem = n[3] ? gram_steps_smem<128>() : n[2] ? gram_steps_smem<64>() : gram_steps_smem<32>();
+        st = launch_clusters(k_gram_steps_mixed, int(m.small.size()), 8, smem, s, who, a);
+    } else {
+        st = launch_clusters(k_gram_steps<16>, n[0], 1, gram_steps_smem<16>(), s, who, a, w);
+        if (st == DPG_OK)
+            st = launch_clusters(k_gram_steps<32>, n[1], 2, gram_steps_smem<32>(), s, who, a, w + n[0]);
+        if (st == DPG_OK)
+            st = launch_clusters(k_gram_steps<64>, n[2], 4, gram_steps_smem<64>(), s, who, a, w + n[0] + n[1]);
+        if (st == DPG_OK)
+            st = launch_clusters(k_gram_steps<128>, n[3], 8, gram_steps_smem<128>(), s, who, a,
+                                 w + n[0] + n[1] + n[2]);
+    }
     if (st != DPG_OK) return st;
     const int mp = m.small_count[3] ? 128 : m.small_count[2] ? 64 : m.small_count[1] ? 32 : 16;
     return launch_k(k_gram_apply, unsigned(m.prod_items.size()), kGramThreads, size_t(gram_apply_smem(mp)), s, who,
