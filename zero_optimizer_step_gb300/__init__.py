@@ -243,6 +243,10 @@ def _ptrs(xs: Sequence[Ptr]):
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        # the handle alone: torch.cuda.current_stream() takes longer than a small kernel
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

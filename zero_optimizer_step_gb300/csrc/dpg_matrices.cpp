@@ -15,7 +15,7 @@ namespace dpg {
 constexpr int64_t kMaxMatrices = 1 << 20;   // of one object
 
 static int64_t ceil_div(int64_t x, int64_t d) { return (x + d - 1) / d; }
-// Items of a small matrix: Gram sums over about 32 groups of whole 32-column
+// Items of a small matrix: Gram sums over about 64 groups of whole 32-column
 // blocks (every further group is a partial sum to write and to read again; very
 // long matrices get one per 1024 columns, up to 128), products of 64 columns.
 static void small_items(Matrices& M, const MatDesc& d) {
@@ -31,7 +31,7 @@ static void small_items(Matrices& M, const MatDesc& d) {
     M.n_small_copy += blocks * 32 * s.mp;
     s.prod = M.n_small_prod;
     M.n_small_prod += int64_t(s.mp) * s.mp;
-    const int64_t groups = std::min<int64_t>(blocks, std::max<int64_t>(32, std::min<int64_t>(128, d.n / 1024)));
+    const int64_t groups = std::min<int64_t>(blocks, std::max<int64_t>(64, std::min<int64_t>(128, d.n / 1024)));
     const int64_t width = ceil_div(blocks, groups) * 32;
     s.part = M.n_small_part;
     s.item0 = int32_t(M.gram_items.size());
