@@ -499,8 +499,8 @@ typedef struct {
  * matrices and 2^31 128-byte rows of workspace.  The object
  * keeps what it needs of the plan (which may be destroyed before it), the
  * tile tables, and a device workspace of workspace_bytes that it allocates on
- * its first device call or in dpg_matrices_upload (call that before a stream
- * capture).  It serves one device; calls that use one object must not overlap
+ * its first orthogonalisation or in dpg_matrices_upload (call that before a
+ * stream capture; dpg_muon_apply needs the tables alone).  It serves one device; calls that use one object must not overlap
  * on the GPU.  Free with dpg_matrices_destroy. */
 typedef struct dpg_matrices dpg_matrices_t;
 int dpg_plan_matrices(const dpg_plan_t* plan, const int64_t* rows, const int64_t* cols,
@@ -510,8 +510,8 @@ int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* 
 int dpg_matrices_upload(dpg_matrices_t* mats);
 /* Every device-side wait of the orthogonalisation is bounded (2 s).  One that
  * runs out ends the call's kernels with incomplete results and records
- * DPG_ERR_DEVICE_TIMEOUT; this synchronises `stream` and returns the record
- * (DPG_OK if there is none), clearing it. */
+ * DPG_ERR_DEVICE_TIMEOUT, and later calls end early too; this synchronises
+ * `stream` and returns the record (DPG_OK if there is none), clearing it. */
 int dpg_matrices_status(dpg_matrices_t* mats, void* stream);
 
 /* Momentum of the reduced gradient, buckets [b0, b1), in one pass (binary32,
@@ -625,7 +625,10 @@ int dpg_debug_checks(const dpg_plan_t* plan, int32_t* built, int64_t* first_fail
  * DPG_ERR_INVALID_ARG. */
 int dpg_debug_set_limit(int64_t limit);
 
-/* Test-only fault injection for the staged step: its next launch by the
+/* Test-only fault injection for the staged step (and for the next
+ * orthogonalisation of matrices of more than 128 rows, whichever the thread
+ * calls first; there skip_unit is a 64-deep stage of the first CTA's operands
+ * and the default bound is 2 s): its next launch by the
  * calling thread never fetches unit `skip_unit` (-1: none), so the CTA
  * that owns it must run out its wait, and every wait is bounded by
  * `timeout_ns` (<= 0: the default 1 s).  Used to test the timeout path.

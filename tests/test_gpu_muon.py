@@ -175,6 +175,49 @@ def test_orthogonalize_is_deterministic_and_holds_a_shared_plan():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+def test_orthogonalize_waits_are_bounded(monkeypatch):
+    # one stage of operands is never fetched: the wait for it runs out, every
+    # other one gives up, the error is reported once, and the next call is whole
+    shapes = [(300, 700, 2), (64, 64, 1)]
+    rng = np.random.Generator(np.random.Philox(12))
+    plan, mats = _plan(shapes)
+    u = torch.from_numpy(_flat(plan, shapes, lambda p, i, r, c: make_matrix("gauss", r, c, rng))).to(DEV)
+    out = [torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), out[0])
+    dpg.dpg_matrices_status(mats)
+    monkeypatch.setenv("DPG_TEST_HOOKS", "1")
+    dpg.dpg_set_staged_fault(skip_unit=3, timeout_ns=20_000_000)
+    dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), out[1])
+    with pytest.raises(dpg.DpgError) as e:
+        dpg.dpg_matrices_status(mats)
+    assert e.value.status == dpg.DPG_ERR_DEVICE_TIMEOUT
+    dpg.dpg_matrices_status(mats)
+    dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), out[1])
+    dpg.dpg_matrices_status(mats)
+    assert torch.equal(out[0], out[1])
+
+
+def test_orthogonalize_on_two_streams_at_once():
+    # two objects whose kernels each want the whole GPU
+    shapes = [(500, 900, 2)]
+    rng = np.random.Generator(np.random.Philox(13))
+    objs = [_plan(shapes) for _ in range(2)]
+    u = torch.from_numpy(_flat(objs[0][0], shapes,
+                               lambda p, i, r, c: make_matrix("spiked", r, c, rng))).to(DEV)
+    want = torch.zeros_like(u, dtype=torch.bfloat16)
+    dpg.dpg_orthogonalize(objs[0][1], u, dpg.MuonHParams(), want)
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(want) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for (_, mats), o, s in zip(objs, outs, streams):
+            dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), o, stream=s)
+    torch.cuda.synchronize()
+    for (_, mats), o in zip(objs, outs):
+        dpg.dpg_matrices_status(mats)
+        assert torch.equal(o, want)
+
+
 @pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 8, 16])
 @pytest.mark.parametrize("mode", ["bf16", "f32", "f32_last"])
 @pytest.mark.parametrize("nesterov,out", [(True, torch.bfloat16), (False, torch.float32)])

@@ -250,7 +250,7 @@ int dpg_muon_apply(dpg_matrices_t* mats, const void* ortho_bf16, const dpg_muon_
     dpg::ApplyArgs a{};
     int st = dpg::apply_args(mats->m, ortho_bf16, hp, master, param_views, n_views, a, "dpg_muon_apply");
     if (st != DPG_OK || mats->m.apply_items.empty()) return st;
-    st = dpg::upload_matrices(mats->m);
+    st = dpg::upload_for_update(mats->m);
     if (st != DPG_OK) return st;
     return dpg::launch_apply(mats->m, a, static_cast<cudaStream_t>(stream), "dpg_muon_apply");
 }

@@ -68,6 +68,8 @@ struct OrthoArgs {
     float2* scal;            // per matrix: {power-of-two scale of X_0, 1 / (norm * scale)}
     int32_t* count;          // per matrix: norm items done (zero between launches)
     int32_t* status;         // 0, or the error of the first wait that ran out
+    uint64_t wait_ns;        // bound of every wait
+    int64_t skip;            // test only: the first CTA does not fetch this stage of its operands (-1: none)
     int32_t* done;           // per matrix and product: CTA tiles finished in this call
     const OrthoTile* queue;  // tiles of a step, pair p's at [queue_first[p], queue_first[p + 1])
     const int32_t* queue_first;
@@ -450,7 +452,7 @@ constexpr int kSlotBytes = 2 * int(kBlkBytes);        // hi | lo, or the tile | 
 constexpr int kEpiWarps = 8;
 constexpr int kFillWarp = 2 + kEpiWarps, kStoreWarp = kFillWarp + 1;
 constexpr int kOrthoThreads = 32 * (kStoreWarp + 1);
-constexpr uint64_t kWaitNs = 2000000000ull;           // bound of every wait
+constexpr uint64_t kWaitNs = 2000000000ull;           // bound of every wait, unless a test sets another
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -518,14 +520,14 @@ __device__ __forceinline__ void give_up(OrthoShared& sh, int32_t* status) {
 
 // true once the phase of `parity` completed; false when the bound ran out or
 // another role gave up (recorded in *status, the tiles after it are skipped)
-__device__ __forceinline__ bool wait_bounded(OrthoShared& sh, uint64_t* bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool wait_bounded(OrthoShared& sh, uint64_t* bar, uint32_t parity, const OrthoArgs& a) {
     const uint32_t at = smem_u32(bar);
     if (try_wait(at, parity)) return true;
-    const uint64_t until = global_ns() + kWaitNs;
+    const uint64_t until = global_ns() + a.wait_ns;
     while (!try_wait(at, parity)) {
         if (sh.abort) return false;
         if (global_ns() > until) {
-            give_up(sh, status);
+            give_up(sh, a.status);
             return false;
         }
     }
@@ -534,13 +536,14 @@ __device__ __forceinline__ bool wait_bounded(OrthoShared& sh, uint64_t* bar, uin
 
 // The same for a counter in device memory that other CTAs raise to `target`.
 // What they wrote before is visible afterwards, to copies too.
-__device__ __forceinline__ bool wait_count(OrthoShared& sh, const int32_t* count, int32_t target, int32_t* status) {
+__device__ __forceinline__ bool wait_count(OrthoShared& sh, const int32_t* count, int32_t target,
+                                           const OrthoArgs& a) {
     if (target > 0 && load_acquire(count) < target) {
-        const uint64_t until = global_ns() + kWaitNs;
+        const uint64_t until = global_ns() + a.wait_ns;
         while (load_acquire(count) < target) {
             if (sh.abort) return false;
-            if (load_acquire(status) != 0 || global_ns() > until) {
-                give_up(sh, status);
+            if (load_acquire(a.status) != 0 || global_ns() > until) {
+                give_up(sh, a.status);
                 return false;
             }
         }
@@ -814,7 +817,7 @@ __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& 
                                               int prod, int step) {
     const int before = prod == kProdA ? kProdX : prod - 1;
     const int target = (prod == kProdA ? step : step + 1) * 2 * d.tiles[before];
-    return wait_count(sh, a.done + 3 * mat + before, target, a.status);
+    return wait_count(sh, a.done + 3 * mat + before, target, a);
 }
 
 __global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
@@ -863,6 +866,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         // clobbers would have a value of the descriptor loaded again for each)
         const uint32_t full0 = map_to(smem_u32(&sh.full[0]), 0);
         int s = 0;
+        int64_t skip = blockIdx.x == 0 ? a.skip : -1;   // stages until the one left out
         uint32_t par = 1;             // the first pass over the ring finds it empty
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
@@ -881,11 +885,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int pitch = d.cbx * kBlkRows;
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!(ok = wait_bounded(sh, &sh.empty[s], par, a.status))) break;
+                    if (!(ok = wait_bounded(sh, &sh.empty[s], par, a))) break;
                     const uint32_t bar = full0 + uint32_t(s) * 8;
                     if (rank == 0) mbar_expect(&sh.full[s], bytes);
                     const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
-                    copy_box(dst, &rows128, left + kb * kBlkRows, bar);
+                    if (skip-- != 0) copy_box(dst, &rows128, left + kb * kBlkRows, bar);
                     if (prod == kProdX) {
                         const int row = right + (kb >> 1) * pitch + (kb & 1) * 64;
                         copy_box(dst + kHalfBytes, &rows64, row, bar);
@@ -913,10 +917,10 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const uint32_t shape = mma_shape(by_column, tile.width);
                 const int kblocks = tile.prod == kProdA ? d.kn : d.km;
                 const int buf = it & 1;
-                if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a.status))) break;
+                if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!(ok = wait_bounded(sh, &sh.full[s], par, a.status))) break;
+                    if (!(ok = wait_bounded(sh, &sh.full[s], par, a))) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t at = stage0 + uint32_t(s) * kStageBytes;
                     const uint64_t left = desc_of(at, false), right = desc_of(at + kHalfBytes, by_column);
@@ -950,7 +954,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
                 for (int g = 0; g < blocks; ++g, ++n) {
                     const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
-                    if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a.status))) break;
+                    if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a))) break;
                     // Tells the finishing warps, which so need not watch the counter in memory
                     // themselves (ten watchers per CTA instead of two delayed it by a
                     // microsecond).  They have all seen it for the tile before: that tile's
@@ -987,7 +991,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 int32_t* done = a.done + 3 * tile.mat + prod;
                 for (int g = 0; g < blocks; ++g, ++n) {
                     const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
-                    if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (n >> 1) & 1, a.status))) break;
+                    if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (n >> 1) & 1, a))) break;
                     if (prod != kProdX) {
                         copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
                         if (mirror) {     // 64 rows from this block's first column, 2 x 64 columns
@@ -1031,7 +1035,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
                 const int64_t diag_at = d.diag;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
-                ok = wait_bounded(sh, &sh.tile_ready, uint32_t(it & 1), a.status);
+                ok = wait_bounded(sh, &sh.tile_ready, uint32_t(it & 1), a);
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 // what the rows need, fetched while the product runs
                 const float inv_sx = step == 0 ? __ldcg(&a.scal[tile.mat].y) : s.inv_sx;
@@ -1048,7 +1052,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     p0 = fmaf(__ldcg(a.diag_b + d.diag + r), inv_sx, s.a * inv_sx);
                     p1 = fmaf(__ldcg(a.diag_t + d.diag + r), inv_sx, s.a * inv_sx) * kInvLoScale;
                 }
-                ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a.status);
+                ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a);
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
@@ -1066,7 +1070,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                             asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
                                          :: "r"(map_to(smem_u32(&sh.tempty[buf]), 0)) : "memory");
                     }
-                    ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a.status);
+                    ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     if (prod == kProdA) {
                         finish_a(a, s, diag_at, inv_sx, slot, row, half, r, c, acc, mirror, p0);
@@ -1136,8 +1140,8 @@ static int encode_map(CUtensorMap* map, void* base, int64_t rows, uint32_t box_r
     return e == CUDA_SUCCESS ? DPG_OK : fail(DPG_ERR_CUDA, "matrices upload: tensor map error %d", int(e));
 }
 
-int upload_matrices(Matrices& m) {
-    std::lock_guard<std::mutex> g(m.mu);
+// The tables of the weight update, which needs nothing else; m.mu is held.
+static int upload_update_tables(Matrices& m) {
     int dev = 0;
     DPG_CUDA_TRY(cudaGetDevice(&dev));
     if (m.device >= 0) {
@@ -1146,6 +1150,33 @@ int upload_matrices(Matrices& m) {
                         m.device, dev);
         return DPG_OK;
     }
+    const size_t bytes = round256(m.apply_items.size() * sizeof(ApplyItem)) +
+                         round256(m.scales.size() * sizeof(double));
+    void* tables = nullptr;
+    cudaError_t e = cudaMalloc(&tables, bytes ? bytes : 256);
+    size_t at = 0;
+    if (e == cudaSuccess) e = put(static_cast<unsigned char*>(tables), &at, m.apply_items, &m.d_apply_items);
+    if (e == cudaSuccess) e = put(static_cast<unsigned char*>(tables), &at, m.scales, &m.d_scales);
+    if (e != cudaSuccess) {
+        cudaFree(tables);
+        cudaGetLastError();
+        return fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA, "matrices upload: %s",
+                    cudaGetErrorString(e));
+    }
+    m.d_update_tables = static_cast<unsigned char*>(tables);
+    m.device = dev;
+    return DPG_OK;
+}
+
+int upload_for_update(Matrices& m) {
+    std::lock_guard<std::mutex> g(m.mu);
+    return upload_update_tables(m);
+}
+
+int upload_matrices(Matrices& m) {
+    std::lock_guard<std::mutex> g(m.mu);
+    int st = upload_update_tables(m);
+    if (st != DPG_OK || m.ws) return st;
     // how many CTA pairs are resident at once decides the queues
     int clusters = 1;
     if (!m.mats.empty()) {
@@ -1166,7 +1197,7 @@ int upload_matrices(Matrices& m) {
         if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no CTA pair fits this device");
     }
     if (!m.small.empty()) {
-        const int st = gram_prepare();
+        st = gram_prepare();
         if (st != DPG_OK) return st;
     }
     try {
@@ -1182,9 +1213,7 @@ int upload_matrices(Matrices& m) {
                          round256(m.prod_items.size() * sizeof(SmallItem)) +
                          round256(m.small_order.size() * sizeof(int32_t)) +
                          round256(m.norm_items.size() * sizeof(NormItem)) +
-                         round256(m.conv_items.size() * sizeof(ConvItem)) +
-                         round256(m.apply_items.size() * sizeof(ApplyItem)) +
-                         round256(m.scales.size() * sizeof(double));
+                         round256(m.conv_items.size() * sizeof(ConvItem));
     void *ws = nullptr, *tables = nullptr;
     cudaError_t e = cudaMalloc(&tables, bytes ? bytes : 256);
     if (e == cudaSuccess) e = cudaMalloc(&ws, size_t(m.workspace_bytes));
@@ -1199,13 +1228,10 @@ int upload_matrices(Matrices& m) {
     if (e == cudaSuccess) e = put(t, &at, m.small_order, &m.d_small_order);
     if (e == cudaSuccess) e = put(t, &at, m.norm_items, &m.d_norm_items);
     if (e == cudaSuccess) e = put(t, &at, m.conv_items, &m.d_conv_items);
-    if (e == cudaSuccess) e = put(t, &at, m.apply_items, &m.d_apply_items);
-    if (e == cudaSuccess) e = put(t, &at, m.scales, &m.d_scales);
     // arrival counters and the status word start at zero
     if (e == cudaSuccess)
         e = cudaMemset(static_cast<unsigned char*>(ws) + m.o_count, 0, size_t(m.o_status + 256 - m.o_count));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
-    int st = DPG_OK;
     if (e != cudaSuccess) {
         cudaGetLastError();
         st = fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA, "matrices upload: %s",
@@ -1224,12 +1250,11 @@ int upload_matrices(Matrices& m) {
     }
     m.d_tables = t;
     m.ws = static_cast<unsigned char*>(ws);
-    m.device = dev;
     return DPG_OK;
 }
 
 int check_matrices(Matrices& m, void* stream) {
-    if (m.device < 0) return DPG_OK;   // nothing has run
+    if (!m.ws) return DPG_OK;          // nothing has run
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int32_t word = 0;
     DPG_CUDA_TRY(cudaMemcpyAsync(&word, m.ws + m.o_status, sizeof word, cudaMemcpyDeviceToHost, s));
@@ -1246,11 +1271,13 @@ void release_matrices(Matrices& m) {
     int cur = -1;
     const bool have_cur = cudaGetDevice(&cur) == cudaSuccess;
     if (cudaSetDevice(m.device) == cudaSuccess) {
+        cudaFree(m.d_update_tables);
         cudaFree(m.d_tables);
         cudaFree(m.ws);
     }
     if (have_cur) cudaSetDevice(cur);
     cudaGetLastError();
+    m.ws = nullptr;
     m.device = -1;
 }
 
@@ -1277,6 +1304,10 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.update = update;
     a.f32 = update_dtype == DPG_F32;
     a.done = reinterpret_cast<int32_t*>(m.ws + m.o_done);
+    a.skip = t_staged_skip;
+    a.wait_ns = t_staged_timeout_ns > 0 ? uint64_t(t_staged_timeout_ns) : kWaitNs;
+    t_staged_skip = -1;
+    t_staged_timeout_ns = 0;
     a.queue = m.d_queue;
     a.queue_first = m.d_queue_first;
     a.n_steps = hp->n_steps;

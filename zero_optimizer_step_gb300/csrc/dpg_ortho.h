@@ -124,6 +124,7 @@ struct Matrices {
     int device = -1;
     unsigned char* ws = nullptr;       // workspace_bytes
     unsigned char* d_tables = nullptr; // one allocation, sections below
+    unsigned char* d_update_tables = nullptr;   // apply_items and scales
     MatDesc* d_mats = nullptr;
     OrthoTile* d_queue = nullptr;
     int32_t* d_queue_first = nullptr;
@@ -141,6 +142,7 @@ struct Matrices {
 void lay_queue(Matrices& m, int clusters);
 // device side (dpg_ortho.cu)
 int upload_matrices(Matrices& m);
+int upload_for_update(Matrices& m);   // only what dpg_muon_apply needs
 void release_matrices(Matrices& m);
 int check_matrices(Matrices& m, void* stream);
 // validates hp for the orthogonalisation and fills steps[0 .. hp->n_steps)
