@@ -195,11 +195,12 @@ struct RowProduct {
         return kCols >= 4 ? (j >> 2) * 64 + tx() * 4 + (j & 3) : tx() * kCols + j;
     }
     __device__ __forceinline__ void run(const float* left, const float* right, float* exchange) {
-        float s[R][kCols];
+        constexpr int kTwo = (kCols + 1) / 2;                    // columns in pairs (at 16: one and a zero)
+        uint64_t two[R][kTwo];
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) s[i][j] = 0.0f;
+            for (int j = 0; j < kTwo; ++j) two[i][j] = 0;
         left += R * ty() * MP;
 #pragma unroll 2
         for (int k = part() * (MP / R); k < (part() + 1) * (MP / R); k += 4) {
@@ -214,26 +215,33 @@ struct RowProduct {
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                float r[kCols];
+                uint64_t r[kTwo];
+                const float* from = right + (k + u) * MP;
                 if constexpr (kCols >= 4) {
 #pragma unroll
                     for (int g = 0; g < kCols / 4; ++g) {
-                        const float4 q = *reinterpret_cast<const float4*>(right + (k + u) * MP + g * 64 + tx() * 4);
-                        r[4 * g] = q.x;
-                        r[4 * g + 1] = q.y;
-                        r[4 * g + 2] = q.z;
-                        r[4 * g + 3] = q.w;
+                        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(from + g * 64 + tx() * 4);
+                        r[2 * g] = q.x;
+                        r[2 * g + 1] = q.y;
                     }
+                } else if constexpr (kCols == 2) {
+                    r[0] = *reinterpret_cast<const uint64_t*>(from + tx() * 2);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) r[j] = right[(k + u) * MP + tx() * kCols + j];
+                    r[0] = pair_of(from[tx()], 0.0f);
                 }
 #pragma unroll
-                for (int i = 0; i < R; ++i)
+                for (int i = 0; i < R; ++i) {
+                    const uint64_t l2 = pair_of(l[i][u], l[i][u]);
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j) s[i][j] = fmaf(l[i][u], r[j], s[i][j]);
+                    for (int j = 0; j < kTwo; ++j) two[i][j] = fma2(l2, r[j], two[i][j]);
+                }
             }
         }
+        float s[R][kCols];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) s[i][j] = j % 2 ? halves_of(two[i][j / 2]).y : halves_of(two[i][j / 2]).x;
         float* e = exchange + int(threadIdx.x) % kGroup;         // [part][row][column][thread]
 #pragma unroll
         for (int i = 0; i < R; ++i)
