@@ -64,11 +64,12 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
     // a thread's columns: four neighbours in each 64, so that the lanes' reads
     // are contiguous
     auto col = [&](int j) { return T >= 4 ? (j >> 2) * 64 + tx * 4 + (j & 3) : tx * T + j; };
-    float acc[T][T];
+    constexpr int kTwo = (T + 1) / 2;    // a thread's columns in pairs (at 16: one and a zero)
+    uint64_t acc[T][kTwo];
 #pragma unroll
     for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int j = 0; j < T; ++j) acc[i][j] = 0.0f;
+        for (int j = 0; j < kTwo; ++j) acc[i][j] = 0;
     int e = -1000;
     float x[kPer];
     // all loads before any use (a load under its own branch would be waited
@@ -116,7 +117,7 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
 #pragma unroll
             for (int i = 0; i < T; ++i)
 #pragma unroll
-                for (int j = 0; j < T; ++j) acc[i][j] *= k;
+                for (int j = 0; j < kTwo; ++j) acc[i][j] = mul2(acc[i][j], pair_of(k, k));
             e = te;
         }
         // 2^-e in two factors: either may leave fp32's range alone
@@ -131,7 +132,7 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
         if (c0 + 32 < it.c1) fetch(c0 + 32);
 #pragma unroll 4
         for (int k = 0; k < 32; ++k) {
-            float u[T], v[T];
+            float u[T], v[2 * kTwo] = {};
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 u[i] = tile[k * P + ty * T + i];
@@ -140,14 +141,16 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
 #pragma unroll
             for (int i = 0; i < T; ++i)
 #pragma unroll
-                for (int j = 0; j < T; ++j) acc[i][j] = fmaf(u[i], v[j], acc[i][j]);
+                for (int j = 0; j < kTwo; ++j)
+                    acc[i][j] = fma2(pair_of(u[i], u[i]), pair_of(v[2 * j], v[2 * j + 1]), acc[i][j]);
         }
     }
     float* out = a.part + it.part;
 #pragma unroll
     for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int j = 0; j < T; ++j) out[(ty * T + i) * MP + col(j)] = acc[i][j];
+        for (int j = 0; j < T; ++j)
+            out[(ty * T + i) * MP + col(j)] = j % 2 ? halves_of(acc[i][j / 2]).y : halves_of(acc[i][j / 2]).x;
     if (threadIdx.x == 0) a.part_exp[it.index] = e;
 }
 
@@ -463,27 +466,23 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
         if (q < MP * MP / 4) *reinterpret_cast<float4*>(P + (q / (MP / 4)) * PP + (q % (MP / 4)) * 4) = p[i];
     }
     __syncthreads();
-    float acc[T][4];
+    uint64_t acc[T][2];
 #pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    for (int i = 0; i < T; ++i) acc[i][0] = acc[i][1] = 0;
     const int kend = (d.m + 3) & ~3;
 #pragma unroll 1
     for (int k = 0; k < kend; k += 4) {
-        float4 x[4];
+        ulonglong2 x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(X + (k + u) * kProdCols + tx * 4);
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const ulonglong2*>(X + (k + u) * kProdCols + tx * 4);
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             const float4 p4 = *reinterpret_cast<const float4*>(P + (ty * T + i) * PP + k);
             const float p[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                acc[i][0] = fmaf(p[u], x[u].x, acc[i][0]);
-                acc[i][1] = fmaf(p[u], x[u].y, acc[i][1]);
-                acc[i][2] = fmaf(p[u], x[u].z, acc[i][2]);
-                acc[i][3] = fmaf(p[u], x[u].w, acc[i][3]);
+                acc[i][0] = fma2(pair_of(p[u], p[u]), x[u].x, acc[i][0]);
+                acc[i][1] = fma2(pair_of(p[u], p[u]), x[u].y, acc[i][1]);
             }
         }
     }
@@ -492,9 +491,11 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
     for (int i = 0; i < T; ++i) {
         const int r = ty * T + i, c = it.c0 + tx * 4;
         if (r >= d.m) continue;
+        const float2 o01 = halves_of(acc[i][0]), o23 = halves_of(acc[i][1]);
+        const float o[4] = {o01.x, o01.y, o23.x, o23.y};
         if (vec && c < d.n) {
-            const __nv_bfloat162 u = __floats2bfloat162_rn(acc[i][0], acc[i][1]);
-            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i][2], acc[i][3]);
+            const __nv_bfloat162 u = __floats2bfloat162_rn(o[0], o[1]);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[2], o[3]);
             *reinterpret_cast<uint2*>(a.out + d.off + int64_t(r) * d.n + c) =
                 make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
         } else {
@@ -502,7 +503,7 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
             for (int j = 0; j < 4; ++j)
                 if (c + j < d.n)
                     a.out[d.off + (d.tall ? int64_t(c + j) * d.m + r : int64_t(r) * d.n + c + j)] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][j]));
+                        __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
         }
     }
 }
