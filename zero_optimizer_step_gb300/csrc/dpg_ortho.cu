@@ -89,17 +89,45 @@ __device__ __forceinline__ float load_update(const OrthoArgs& a, int64_t i) {
     return __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + i)) << 16);
 }
 
-// eight consecutive elements from i, a multiple of 8
+// Eight consecutive elements as they are in memory (loads in flight hold four
+// registers for bf16 so, not eight).
 template <bool F32>
-__device__ __forceinline__ void load_update8(const OrthoArgs& a, int64_t i, float* x) {
-    if (F32) {
-        const F8 v = ld_grad_f8(static_cast<const float*>(a.update) + i);
+struct Raw8;
+template <>
+struct Raw8<true> {
+    F8 v;
+    __device__ __forceinline__ void load(const OrthoArgs& a, int64_t i) {
+        v = ld_grad_f8(static_cast<const float*>(a.update) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] = 0.0f;
+    }
+    // the first `n` elements from i on, singly; zeros after them
+    __device__ __forceinline__ void load_some(const OrthoArgs& a, int64_t i, int n) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] = j < n ? __ldg(static_cast<const float*>(a.update) + i + j) : 0.0f;
+    }
+    __device__ __forceinline__ void widen(float* x) const {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = v.v[j];
-    } else {
-        widen8(ld_grad_u4(static_cast<const uint16_t*>(a.update) + i), x);
     }
-}
+};
+template <>
+struct Raw8<false> {
+    uint4 v;
+    __device__ __forceinline__ void load(const OrthoArgs& a, int64_t i) {
+        v = ld_grad_u4(static_cast<const uint16_t*>(a.update) + i);
+    }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load_some(const OrthoArgs& a, int64_t i, int n) {
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = j < n ? __ldg(static_cast<const uint16_t*>(a.update) + i + j) : 0;
+        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+    __device__ __forceinline__ void widen(float* x) const { widen8(v, x); }
+};
 
 __device__ __forceinline__ uint32_t pack_half2(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -199,12 +227,16 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
     if (it.count == kNormChunk && (base & 7) == 0) {
 #pragma unroll 1
         for (int k = 0; k < kPer; k += kFly) {
-            float x[kFly][8];
+            Raw8<F32> raw[kFly];
 #pragma unroll
             for (int u = 0; u < kFly; ++u)
-                load_update8<F32>(a, base + (int64_t(k + u) * kNormThreads + threadIdx.x) * 8, x[u]);
+                raw[u].load(a, base + (int64_t(k + u) * kNormThreads + threadIdx.x) * 8);
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) square8(x[u], f, w);
+            for (int u = 0; u < kFly; ++u) {
+                float x[8];
+                raw[u].widen(x);
+                square8(x, f, w);
+            }
         }
     } else {
         for (int e = int(threadIdx.x) * 8; e < it.count; e += kNormThreads * 8) {
@@ -278,18 +310,16 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
         // row c of U holds X's column c: X[r][c] = U[c m + r]
         const bool vec = ((off | m) & 7) == 0;
         if (vec) {
-            float x[8][8];
+            Raw8<F32> raw[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {   // 16 columns by two vectors of 8 rows per warp
                 const int q = i * 8 + int(threadIdx.x >> 5);
                 const int c = c0 + (q & 7) * 16 + (int(threadIdx.x) & 15);
                 const int r = r0 + ((q >> 3) * 2 + ((int(threadIdx.x) >> 4) & 1)) * 8;
-                if (c < n && r < m) {
-                    load_update8<F32>(a, off + int64_t(c) * m + r, x[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
-                }
+                if (c < n && r < m)
+                    raw[i].load(a, off + int64_t(c) * m + r);
+                else
+                    raw[i].zero();
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -297,9 +327,11 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 const int c = (q & 7) * 16 + (int(threadIdx.x) & 15);
                 const int r = ((q >> 3) * 2 + ((int(threadIdx.x) >> 4) & 1)) * 8;
                 const bool in = c0 + c < n && r0 + r < m;
+                float x[8];
+                raw[i].widen(x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float u = in ? x[i][j] * sc : 0.0f;
+                    const float u = in ? x[j] * sc : 0.0f;
                     uint16_t h, l;
                     split16(u, F32 ? u * RoundScale(1.0f, r + j + c).v[0] : u, h, l);
                     sm[(r + j) * kLoadPitch + c] = h;
@@ -320,18 +352,15 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
         __syncthreads();
     }
     const bool vec = !TALL && ((off | n) & 7) == 0;
-    float x[8][8];
+    Raw8<F32> raw[8];
     if (!TALL) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {   // sixteen lanes hold a row's sixteen chunks of 8
             const int r = r0 + 16 * i + (int(threadIdx.x) >> 4), c = c0 + (int(threadIdx.x) & 15) * 8;
-            if (vec && r < m && c < n) {
-                load_update8<F32>(a, off + int64_t(r) * n + c, x[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[i][j] = r < m && c + j < n ? load_update<F32>(a, off + int64_t(r) * n + c + j) : 0.0f;
-            }
+            if (vec && r < m && c < n)
+                raw[i].load(a, off + int64_t(r) * n + c);
+            else
+                raw[i].load_some(a, off + int64_t(r) * n + c, r < m ? n - c : 0);
         }
     }
 #pragma unroll
@@ -352,12 +381,14 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
         } else {
             const int r = r0 + row, c = c0 + ch * 8;
             const RoundScale rs(1.0f, row);
+            float x[8];
+            raw[i].widen(x);
             uint32_t h[4], l[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // (sc is a NaN for a matrix that is not finite: padding stays zero)
-                const float u = r < m && c + 2 * j < n ? x[i][2 * j] * sc : 0.0f;
-                const float v = r < m && c + 2 * j + 1 < n ? x[i][2 * j + 1] * sc : 0.0f;
+                const float u = r < m && c + 2 * j < n ? x[2 * j] * sc : 0.0f;
+                const float v = r < m && c + 2 * j + 1 < n ? x[2 * j + 1] * sc : 0.0f;
                 sq = fmaf(u, u, fmaf(v, v, sq));
                 // a scaled bf16 value is an fp16 value: nothing to round, lo is 0
                 h[j] = F32 ? pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]) : pack_half2(u, v);
