@@ -58,6 +58,12 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
     int64_t count = 0;
     for (int32_t q = 0; q < p.n_params; ++q)
         if ((count += p.numels[q] / (rows[q] * cols[q])) > kMaxMatrices) return false;
+    // Items of the norm pass: as long as leaves about four per SM (each costs a fence and an
+    // atomic besides its loads)
+    int64_t tiled = 0;
+    for (int32_t q = 0; q < p.n_params; ++q)
+        if (std::min(rows[q], cols[q]) > kSmallSide) tiled += p.numels[q];
+    const int64_t norm_chunk = kNormChunk * std::clamp<int64_t>(ceil_div(tiled, 608 * int64_t(kNormChunk)), 1, 8);
     for (int32_t q = p.n_params - 1; q >= 0; --q) {   // flat order
         const double r = double(rows[q]), c = double(cols[q]);
         M.scales[2 * size_t(q)] = std::sqrt(std::max(1.0, r / c));
@@ -104,8 +110,8 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             if (tm * tn > 0x1FFFFFF) return false;   // counts of a call stay in 32 bits
             const int32_t mat = int32_t(M.mats.size());
             d.norm0 = int32_t(M.norm_items.size());
-            for (int64_t s = 0; s < one; s += kNormChunk)
-                M.norm_items.push_back({mat, int32_t(std::min<int64_t>(kNormChunk, one - s)), s});
+            for (int64_t s = 0; s < one; s += norm_chunk)
+                M.norm_items.push_back({mat, int32_t(std::min(norm_chunk, one - s)), s});
             d.norm1 = int32_t(M.norm_items.size());
             for (int64_t i = 0; i < rb; ++i)
                 for (int64_t j = 0; j < d.cbx / 2; ++j)

@@ -220,13 +220,14 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
     const NormItem it = items[blockIdx.x];
     const MatDesc& d = a.mats[it.mat];
     const int64_t base = d.off + it.start;
-    constexpr int kPer = kNormChunk / (kNormThreads * 8), kFly = F32 ? 4 : 8;   // vectors per thread, in flight
-    static_assert(kPer % kFly == 0, "whole batches");
+    constexpr int kFly = F32 ? 4 : 8;   // vectors in flight per thread
+    static_assert(kNormChunk % (kFly * kNormThreads * 8) == 0, "whole batches");
     float f = 0.0f;
     double w = 0.0;
-    if (it.count == kNormChunk && (base & 7) == 0) {
+    if (it.count % kNormChunk == 0 && (base & 7) == 0) {
+        const int per = it.count / (kNormThreads * 8);
 #pragma unroll 1
-        for (int k = 0; k < kPer; k += kFly) {
+        for (int k = 0; k < per; k += kFly) {
             Raw8<F32> raw[kFly];
 #pragma unroll
             for (int u = 0; u < kFly; ++u)
