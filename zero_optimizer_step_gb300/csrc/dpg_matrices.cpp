@@ -154,16 +154,63 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
            M.apply_items.size() < 0x7FFFFFFF;
 }
 
+// A deal of one step's tiles to the pairs.
+struct Deal {
+    std::vector<std::vector<OrthoTile>> mine;   // pair by pair
+    int64_t end = 0;                            // modelled time of the step
+};
+
 // The tiles of one step -- A tiles, B tiles, X tiles of all matrices, larger
-// matrices first -- dealt out to the pairs in this order, each to the pair that
-// could start it first.  The model behind "first": a tile takes 0.3 us per 64
-// of its sum (the tensor cores' rate) and at least 2.5 us (its finish), and
-// starts after its matrix's tiles of the product before.  It only balances the
-// queues; the kernel waits for what has really happened.
-//
-// A product whose tiles would leave most pairs idle is cut into tiles of 128
-// columns instead of 256, if these then still find a pair each: the sums take
-// as long, but the finish is half as long.
+// matrices first, `width[prod]` columns each -- dealt out to the pairs in this
+// order, each to the pair that could start it first.  The model behind "first"
+// (units of 25 ns): a tile holds its pair for 0.3 us per 64 of its sum, or for
+// its finish (3 us) where that is longer, and starts 1.5 us after the last of
+// its matrix's tiles of the product before.  At 128 columns the finish is 1.75
+// us and the sum of A and B 0.225 us per 64; that of X is no shorter than at
+// 256, as its stored rows of X are read and written beside it.  It only
+// balances the queues; the kernel waits for what has really happened.
+static Deal deal(const Matrices& M, const std::vector<int32_t>& order, const int* width, int pairs) {
+    Deal out;
+    out.mine.resize(size_t(pairs));
+    using Free = std::pair<int64_t, int32_t>;
+    std::priority_queue<Free, std::vector<Free>, std::greater<Free>> idle;   // {time, pair}
+    for (int32_t p = 0; p < pairs; ++p) idle.push({0, p});
+    std::vector<int64_t> ready(M.mats.size(), 0), next(M.mats.size(), 0);
+    for (int prod = 0; prod < 3; ++prod) {
+        const int per = kOrthoTile / width[prod];
+        const int64_t stage = per == 1 || prod == kProdX ? 12 : 9, finish = per == 1 ? 120 : 70, signal = 60;
+        for (int32_t k : order) {
+            const MatDesc& d = M.mats[size_t(k)];
+            const int64_t sum = stage * (prod == kProdA ? d.kn : d.km);
+            const int tm = d.cba / 4, tn = (prod == kProdX ? d.cbx : d.cba) / 4;
+            for (int i = 0; i < tm; ++i)
+                for (int j = prod == kProdX ? 0 : i * per; j < tn * per; ++j) {
+                    const Free f = idle.top();
+                    idle.pop();
+                    const int64_t start = std::max(f.first, ready[size_t(k)]);
+                    const int64_t done = start + sum + finish + signal;
+                    next[size_t(k)] = std::max(next[size_t(k)], done);
+                    out.end = std::max(out.end, done);
+                    out.mine[size_t(f.second)].push_back(
+                        {k, int16_t(i), int16_t(j), int16_t(prod), int16_t(width[prod])});
+                    idle.push({start + std::max(sum, finish), f.second});
+                }
+        }
+        ready = next;
+    }
+    return out;
+}
+
+// Tiles of a product are 256 columns wide or, where that lets the step end
+// earlier in the model, 128: with few tiles, more pairs work at a product and
+// each has half the finish.  Measured with all three products at 256, with A
+// and B at 128, with all at 128 (us, 76 pairs):
+//     4 of 768 x 2304, 4 of 768 x 768   254   243   261
+//     4 of 768 x 768                    186   168   156
+//     4 of 1024 x 4096                  393   368   456
+//     4 of 2048 x 2048                  591   673   816
+// The model picks the fastest of the eight mixtures for these and for the six
+// other sets that it was compared with.
 void lay_queue(Matrices& M, int clusters) {
     std::vector<int32_t> order(M.mats.size());
     for (size_t k = 0; k < order.size(); ++k) order[k] = int32_t(k);
@@ -171,50 +218,29 @@ void lay_queue(Matrices& M, int clusters) {
         const MatDesc &u = M.mats[size_t(x)], &v = M.mats[size_t(y)];
         return u.m != v.m ? u.m > v.m : u.n > v.n;
     });
-    std::vector<OrthoTile> all;
-    size_t most = 1;
-    for (int prod = 0; prod < 3; ++prod) {
-        auto cut = [&](int width, std::vector<OrthoTile>& out) {
-            const int per = kOrthoTile / width;
-            for (int32_t k : order) {
-                MatDesc& d = M.mats[size_t(k)];
-                const size_t before = out.size();
-                const int tm = d.cba / 4, tn = (prod == kProdX ? d.cbx : d.cba) / 4;
-                for (int i = 0; i < tm; ++i)
-                    for (int j = prod == kProdX ? 0 : i * per; j < tn * per; ++j)
-                        out.push_back({k, int16_t(i), int16_t(j), int16_t(prod), int16_t(width)});
-                d.tiles[prod] = int32_t(out.size() - before);
-            }
-        };
-        std::vector<OrthoTile> tiles;
-        cut(128, tiles);
-        if (tiles.size() > size_t(clusters)) {
-            tiles.clear();
-            cut(256, tiles);
+    Deal best;
+    int cut = 0;
+    for (int c = 0; c < 8; ++c) {
+        const int width[3] = {c & 1 ? 128 : 256, c & 2 ? 128 : 256, c & 4 ? 128 : 256};
+        Deal d = deal(M, order, width, clusters);
+        if (c == 0 || d.end < best.end) {
+            best = std::move(d);
+            cut = c;
         }
-        most = std::max(most, tiles.size());
-        all.insert(all.end(), tiles.begin(), tiles.end());
     }
-    M.pairs = int32_t(std::min<size_t>(size_t(clusters), most));
-    std::vector<std::vector<OrthoTile>> mine(size_t(M.pairs));
-    std::vector<int64_t> ready(M.mats.size() * 4, 0);   // when the tiles of a product can start
-    using Free = std::pair<int64_t, int32_t>;
-    std::priority_queue<Free, std::vector<Free>, std::greater<Free>> idle;   // {time, pair}
-    for (int32_t p = 0; p < M.pairs; ++p) idle.push({0, p});
-    for (const OrthoTile& t : all) {
-        const MatDesc& d = M.mats[size_t(t.mat)];
-        const Free f = idle.top();
-        idle.pop();
-        const int64_t start = std::max(f.first, ready[size_t(t.mat) * 4 + size_t(t.prod)]);
-        const int64_t end = start + std::max<int64_t>(3 * (t.prod == kProdA ? d.kn : d.km), 25) + 2;
-        int64_t& next = ready[size_t(t.mat) * 4 + size_t(t.prod) + 1];
-        next = std::max(next, end);
-        mine[size_t(f.second)].push_back(t);
-        idle.push({end, f.second});
+    for (MatDesc& d : M.mats) {
+        const int64_t tm = d.cba / 4, tn = d.cbx / 4;
+        for (int prod = 0; prod < 3; ++prod) {
+            const int64_t per = cut >> prod & 1 ? 2 : 1;
+            d.tiles[prod] = int32_t((prod == kProdX ? tm * tn : tm * (tm + 1) / 2) * per);
+        }
     }
+    // pairs without a tile come last: none is given one before an idle pair
+    while (!best.mine.empty() && best.mine.back().empty()) best.mine.pop_back();
+    M.pairs = int32_t(best.mine.size());
     M.queue.clear();
     M.queue_first.assign(1, 0);
-    for (const auto& q : mine) {
+    for (const auto& q : best.mine) {
         M.queue.insert(M.queue.end(), q.begin(), q.end());
         M.queue_first.push_back(int32_t(M.queue.size()));
     }
