@@ -88,6 +88,23 @@ def test_orthogonalize_many_tiles(rows, cols):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shapes", [[(200, 9000, 1)], [(9001, 300, 2)], [(150, 1030, 3)], [(700, 4300, 1)],
+                                    [(513, 2305, 4), (300, 256, 4)], [(129, 2000, 40), (400, 400, 1)]])
+def test_orthogonalize_long_matrices(shapes, dtype):
+    # sums over the long side in parts, beside matrices that have none, and the
+    # same bits every time
+    _ortho_case(shapes, "spiked", dtype)
+    rng = np.random.Generator(np.random.Philox(14))
+    plan, mats = _plan(shapes)
+    u = torch.from_numpy(_flat(plan, shapes, lambda p, i, r, c: make_matrix("gauss", r, c, rng))).to(DEV).to(dtype)
+    outs = [torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    for o in outs:
+        dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), o)
+    dpg.dpg_matrices_status(mats)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,cols", [(128, 3000), (3000, 128), (65, 66), (16, 16), (17, 5000), (5000, 33),
                                        (1, 40000), (2, 2), (128, 129)])
 def test_orthogonalize_short_side(rows, cols, dtype):

@@ -46,6 +46,13 @@ static void small_items(Matrices& M, const MatDesc& d) {
     M.small.push_back(s);
 }
 
+// How many parts an A tile's sum may have: the parts' sums (256 KB each) are
+// left in the buffer of the next X, which is free while A is built.
+static int most_parts(const MatDesc& d) {
+    const int tm = d.cba / 4, tn = d.cbx / 4;
+    return tn >= 4 * (tm + 1) ? 4 : tn >= 2 * (tm + 1) ? 2 : 1;
+}
+
 static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 
 // Lays the matrices out; false when an index would leave its type.
@@ -108,6 +115,11 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.rowsq = M.n_rowsq;
             M.n_rowsq += int64_t(d.rows_pad) * d.cbx;
             if (tm * tn > 0x1FFFFFF) return false;   // counts of a call stay in 32 bits
+            if (most_parts(d) > 1) {
+                d.group0 = int32_t(M.n_groups);
+                M.n_groups += tm * (tm + 1);         // A tiles of 128 columns
+                if (M.n_groups > 0x3FFFFFF) return false;
+            }
             const int32_t mat = int32_t(M.mats.size());
             d.norm0 = int32_t(M.norm_items.size());
             for (int64_t s = 0; s < one; s += norm_chunk)
@@ -132,6 +144,8 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
     o += up256(int64_t(M.mats.size()) * int64_t(sizeof(int32_t)));
     M.o_done = o;   // per matrix and product: tiles finished in this call
     o += up256(int64_t(M.mats.size()) * 3 * int64_t(sizeof(int32_t)));
+    M.o_join = o;   // per group of parts, CTA and warp: parts left in this call
+    o += up256(M.n_groups * 16 * int64_t(sizeof(int32_t)));
     M.o_status = o;
     o += 256;
     for (int c = 0; c < 4; ++c)
@@ -154,22 +168,31 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
            M.apply_items.size() < 0x7FFFFFFF;
 }
 
+// How the products of a step are cut: blocks of 64 columns in a tile of each,
+// and the most parts of an A tile.
+struct Cut {
+    int blocks[3], parts;
+};
 // A deal of one step's tiles to the pairs.
 struct Deal {
     std::vector<std::vector<OrthoTile>> mine;   // pair by pair
     int64_t end = 0;                            // modelled time of the step
 };
 
+static int parts_of(const MatDesc& d, const Cut& c) { return std::min(c.parts, most_parts(d)); }
+
 // The tiles of one step -- A tiles, B tiles, X tiles of all matrices, larger
-// matrices first, `width[prod]` columns each -- dealt out to the pairs in this
-// order, each to the pair that could start it first.  The model behind "first"
-// (units of 25 ns): a tile holds its pair for 0.3 us per 64 of its sum, or for
-// its finish (3 us) where that is longer, and starts 1.5 us after the last of
-// its matrix's tiles of the product before.  At 128 columns the finish is 1.75
-// us and the sum of A and B 0.225 us per 64; that of X is no shorter than at
-// 256, as its stored rows of X are read and written beside it.  It only
-// balances the queues; the kernel waits for what has really happened.
-static Deal deal(const Matrices& M, const std::vector<int32_t>& order, const int* width, int pairs) {
+// matrices first -- dealt out to the pairs in this order, each to the pair that
+// could start it first.  The parts of a tile wait for one another, so they go
+// to different pairs and stand next to one another in the order.  The model
+// behind "first" (units of 25 ns): a tile holds its pair for 0.3 us per 64 of
+// its sum, or for its finish (3 us) where that is longer, and starts 1.5 us
+// after the last of its matrix's tiles of the product before.  At 128 columns
+// the finish is 1.75 us and the sum of A and B 0.225 us per 64; that of X is no
+// shorter than at 256, as its stored rows of X are read and written beside it.
+// Parts take 3 us to join.  It only balances the queues; the kernel waits for
+// what has really happened.
+static Deal deal(const Matrices& M, const std::vector<int32_t>& order, const Cut& cut, int pairs) {
     Deal out;
     out.mine.resize(size_t(pairs));
     using Free = std::pair<int64_t, int32_t>;
@@ -177,23 +200,33 @@ static Deal deal(const Matrices& M, const std::vector<int32_t>& order, const int
     for (int32_t p = 0; p < pairs; ++p) idle.push({0, p});
     std::vector<int64_t> ready(M.mats.size(), 0), next(M.mats.size(), 0);
     for (int prod = 0; prod < 3; ++prod) {
-        const int per = kOrthoTile / width[prod];
+        const int blocks = cut.blocks[prod], per = 4 / blocks;
         const int64_t stage = per == 1 || prod == kProdX ? 12 : 9, finish = per == 1 ? 120 : 70, signal = 60;
         for (int32_t k : order) {
             const MatDesc& d = M.mats[size_t(k)];
-            const int64_t sum = stage * (prod == kProdA ? d.kn : d.km);
+            const int parts = prod == kProdA ? parts_of(d, cut) : 1;
+            const int64_t sum = stage * ((prod == kProdA ? d.kn : d.km) + parts - 1) / parts;
+            const int64_t join = parts > 1 ? 120 : 0;
             const int tm = d.cba / 4, tn = (prod == kProdX ? d.cbx : d.cba) / 4;
+            int32_t group = d.group0;
             for (int i = 0; i < tm; ++i)
-                for (int j = prod == kProdX ? 0 : i * per; j < tn * per; ++j) {
-                    const Free f = idle.top();
-                    idle.pop();
-                    const int64_t start = std::max(f.first, ready[size_t(k)]);
-                    const int64_t done = start + sum + finish + signal;
-                    next[size_t(k)] = std::max(next[size_t(k)], done);
-                    out.end = std::max(out.end, done);
-                    out.mine[size_t(f.second)].push_back(
-                        {k, int16_t(i), int16_t(j), int16_t(prod), int16_t(width[prod])});
-                    idle.push({start + std::max(sum, finish), f.second});
+                for (int j = prod == kProdX ? 0 : i * per; j < tn * per; ++j, ++group) {
+                    Free f[4];
+                    for (int s = 0; s < parts; ++s) {
+                        f[s] = idle.top();
+                        idle.pop();
+                    }
+                    for (int s = 0; s < parts; ++s) {
+                        const int64_t start = std::max(f[s].first, ready[size_t(k)]);
+                        // (a part holds its pair until the last one is there)
+                        const int64_t held = std::max(f[parts - 1].first, start) + std::max(sum, finish) + join;
+                        const int64_t done = held - std::max(sum, finish) + sum + finish + signal;
+                        next[size_t(k)] = std::max(next[size_t(k)], done);
+                        out.end = std::max(out.end, done);
+                        out.mine[size_t(f[s].second)].push_back({k, group, int16_t(i), int16_t(j), uint8_t(prod),
+                                                                 uint8_t(blocks), uint8_t(s), uint8_t(parts >> 1)});
+                        idle.push({held, f[s].second});
+                    }
                 }
         }
         ready = next;
@@ -218,22 +251,29 @@ void lay_queue(Matrices& M, int clusters) {
         const MatDesc &u = M.mats[size_t(x)], &v = M.mats[size_t(y)];
         return u.m != v.m ? u.m > v.m : u.n > v.n;
     });
+    int64_t wide = 0;   // X tiles of 256 columns
+    for (const MatDesc& d : M.mats) wide += int64_t(d.cba / 4) * (d.cbx / 4);
     Deal best;
-    int cut = 0;
-    for (int c = 0; c < 8; ++c) {
-        const int width[3] = {c & 1 ? 128 : 256, c & 2 ? 128 : 256, c & 4 ? 128 : 256};
-        Deal d = deal(M, order, width, clusters);
+    Cut cut{};
+    for (int c = 0; c < 20; ++c) {
+        // A: whole at 256, whole at 128, in two or four parts at 256, in two at 128
+        static const int a_blocks[5] = {4, 2, 4, 4, 2}, a_parts[5] = {1, 1, 2, 4, 2};
+        const Cut u{{a_blocks[c >> 2], c & 1 ? 2 : 4, c & 2 ? 2 : 4}, a_parts[c >> 2]};
+        if (u.parts > clusters) continue;
+        Deal d = deal(M, order, u, clusters);
         if (c == 0 || d.end < best.end) {
             best = std::move(d);
-            cut = c;
+            cut = u;
         }
+        if (wide > 16 * int64_t(clusters)) break;   // enough tiles for every pair as they are
     }
     for (MatDesc& d : M.mats) {
         const int64_t tm = d.cba / 4, tn = d.cbx / 4;
-        for (int prod = 0; prod < 3; ++prod) {
-            const int64_t per = cut >> prod & 1 ? 2 : 1;
-            d.tiles[prod] = int32_t((prod == kProdX ? tm * tn : tm * (tm + 1) / 2) * per);
-        }
+        const int parts = parts_of(d, cut);
+        for (int prod = 0; prod < 3; ++prod)
+            d.tiles[prod] = int32_t((prod == kProdX ? tm * tn : tm * (tm + 1) / 2) * (4 / cut.blocks[prod]) *
+                                    (prod == kProdA ? parts : 1));
+        d.groups = parts > 1 ? d.tiles[kProdA] / parts : 0;
     }
     // pairs without a tile come last: none is given one before an idle pair
     while (!best.mine.empty() && best.mine.back().empty()) best.mine.pop_back();

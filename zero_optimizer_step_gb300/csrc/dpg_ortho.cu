@@ -71,6 +71,7 @@ struct OrthoArgs {
     uint64_t wait_ns;        // bound of every wait
     int64_t skip;            // test only: the first CTA does not fetch this stage of its operands (-1: none)
     int32_t* done;           // per matrix and product: CTA tiles finished in this call
+    int32_t* join;           // per group of parts, CTA and finishing warp: parts left in this call
     const OrthoTile* queue;  // tiles of a step, pair p's at [queue_first[p], queue_first[p + 1])
     const int32_t* queue_first;
     const void* update;
@@ -414,7 +415,10 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
     pdl_enter();
     const ConvItem it = items[blockIdx.x];
     const MatDesc& d = a.mats[it.mat];
-    if (it.i == 0 && it.j == 0 && threadIdx.x < 3) a.done[3 * it.mat + int(threadIdx.x)] = 0;
+    if (it.i == 0 && it.j == 0) {
+        if (threadIdx.x < 3) a.done[3 * it.mat + int(threadIdx.x)] = 0;
+        for (int k = int(threadIdx.x); k < 16 * d.groups; k += 256) a.join[int64_t(d.group0) * 16 + k] = 0;
+    }
     if (d.tall)
         load_blocks<F32, true>(a, d, it, load_sm);
     else
@@ -617,6 +621,23 @@ __device__ __forceinline__ void load_acc32(uint32_t tmem, float* v) {
                  : "r"(tmem) : "memory");
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+__device__ __forceinline__ void store_acc32(uint32_t tmem, const float* v) {
+    uint32_t r[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[j]);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
+                 " tcgen05.wait::st.sync.aligned;"
+                 :: "r"(tmem), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                    "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                    "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+                    "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                    "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+                    "r"(r[31])
+                 : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
@@ -831,6 +852,73 @@ __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& 
     return wait_count(sh, a.done + 3 * mat + before, target, a);
 }
 
+// First 64-deep block and number of blocks of a part of a tile's sum.
+__device__ __forceinline__ int2 part_of_sum(const MatDesc& d, const OrthoTile& t, int part) {
+    const int all = t.prod == kProdA ? d.kn : d.km;
+    const int k0 = all * part >> t.split;
+    return make_int2(k0, (all * (part + 1) >> t.split) - k0);
+}
+
+// A tile of A in parts.  Every part holds sums for the whole tile, over its
+// share of the columns of X; it finishes one part's share of the 64-column
+// blocks and leaves the others' sums for the pairs that finish those.  Per
+// group: [part][CTA][warp][block][four columns][lane], 16 bytes each, in the
+// buffer of the next X: a warp writes and reads 512 contiguous bytes at once,
+// and needs only what the same warp of the other pairs left.  Adds the others'
+// sums, in their order, to this part's in tensor memory.  (Not inlined: beside
+// the other code of the finish it made every product 0.3 us longer.)
+constexpr int kSumsOfWarp = 8 * 32;   // float4 per block
+__device__ __noinline__ bool join_parts(OrthoShared& sh, const OrthoArgs& a, const MatDesc& d, OrthoTile t,
+                                        uint32_t sums, int step, int warp) {   // warp: 0 .. 15 of the pair's
+    const int own = t.blocks >> t.split, lane = int(threadIdx.x & 31);
+    const int64_t per_part = int64_t(2 * kEpiWarps) * t.blocks * kSumsOfWarp;
+    float4* left = reinterpret_cast<float4*>(a.ws + d.x[(step + 1) & 1] * kBlkBytes) +
+                   (int64_t(t.group - d.group0) << t.split) * per_part +
+                   int64_t(warp) * t.blocks * kSumsOfWarp + lane;
+#pragma unroll 1
+    for (int b = 0; b < t.blocks; ++b) {
+        if (b >= t.part * own && b < (t.part + 1) * own) continue;
+        float v[32];
+        load_acc32(sums + uint32_t(b) * 64, v);
+        float4* out = left + t.part * per_part + b * kSumsOfWarp;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            __stcg(out + q * 32, make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+    }
+    __syncwarp();
+    bool ok = true;
+    if (lane == 0) {
+        int32_t* join = a.join + int64_t(t.group) * (2 * kEpiWarps) + warp;
+        __threadfence();
+        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" :: "l"(join) : "memory");
+        ok = wait_count(sh, join, (step + 1) << t.split, a);
+    }
+    if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+    __syncwarp();
+#pragma unroll 1
+    for (int b = t.part * own; b < (t.part + 1) * own; ++b) {
+        float acc[32];
+        load_acc32(sums + uint32_t(b) * 64, acc);
+#pragma unroll 1
+        for (int p = 0; p < 1 << t.split; ++p) {
+            if (p == t.part) continue;
+            const float4* in = left + p * per_part + b * kSumsOfWarp;
+            float4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __ldcg(in + q * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                acc[4 * q] += v[q].x;
+                acc[4 * q + 1] += v[q].y;
+                acc[4 * q + 2] += v[q].z;
+                acc[4 * q + 3] += v[q].w;
+            }
+        }
+        store_acc32(sums + uint32_t(b) * 64, acc);
+    }
+    return true;
+}
+
 __global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
 k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
               const __grid_constant__ CUtensorMap rows64) {
@@ -887,11 +975,12 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int prod = tile.prod;
                 const int64_t x = d.x[step & 1];
                 const int64_t from = prod == kProdA ? x : prod == kProdB ? d.a : d.b;
-                const int cb = prod == kProdA ? d.cbx : d.cba, kblocks = prod == kProdA ? d.kn : d.km;
-                const int half = tile.width >> 1, c0 = tile.j * tile.width + int(rank) * half;
-                const int left = int((from + int64_t(tile.i * 2 + int(rank)) * cb) * kBlkRows);
+                const int cb = prod == kProdA ? d.cbx : d.cba, kblocks = part_of_sum(d, tile, tile.part).y;
+                const int half = tile.blocks * 32, c0 = tile.j * tile.blocks * 64 + int(rank) * half;
+                const int k0 = part_of_sum(d, tile, tile.part).x * kBlkRows;
+                const int left = int((from + int64_t(tile.i * 2 + int(rank)) * cb) * kBlkRows) + k0;
                 const int right = prod == kProdX ? int((x + (c0 >> 6)) * kBlkRows)
-                                                 : int((from + int64_t(c0 >> 7) * cb) * kBlkRows) + (c0 & 127);
+                                                 : int((from + int64_t(c0 >> 7) * cb) * kBlkRows) + (c0 & 127) + k0;
                 const uint32_t bytes = 2 * (kHalfBytes + uint32_t(half) * 128);
                 const int pitch = d.cbx * kBlkRows;
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
@@ -925,8 +1014,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const bool by_column = tile.prod == kProdX;
-                const uint32_t shape = mma_shape(by_column, tile.width);
-                const int kblocks = tile.prod == kProdA ? d.kn : d.km;
+                const uint32_t shape = mma_shape(by_column, tile.blocks * 64);
+                const int kblocks = part_of_sum(d, tile, tile.part).y;
                 const int buf = it & 1;
                 if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -951,13 +1040,14 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
     } else if (warp == kFillWarp && lane == 0) {
         // ---- slots in ----
         uint32_t n = 0;               // 64-column blocks so far; block n uses slot n mod 2
+        int before = 2;               // blocks of the tile before
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
-                const int prod = tile.prod, blocks = tile.width >> 6;
+                const int prod = tile.prod, blocks = tile.blocks >> tile.split;   // (parts: of A, which reads no blocks)
                 const int64_t blk = int64_t(tile.i * 2 + int(rank)) * (prod == kProdX ? d.cbx : d.cba) + tile.j * blocks;
                 const unsigned char* in = a.ws + ((prod == kProdB ? d.a : d.x[step & 1]) + blk) * kBlkBytes;
                 const unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
@@ -968,9 +1058,15 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a))) break;
                     // Tells the finishing warps, which so need not watch the counter in memory
                     // themselves (ten watchers per CTA instead of two delayed it by a
-                    // microsecond).  They have all seen it for the tile before: that tile's
-                    // block in this slot is finished.
-                    if (g == 0) mbar_arrive(&sh.tile_ready);
+                    // microsecond).  They have all seen it for the tile before, or they could
+                    // miss a phase: a block of that tile is finished, the one in this slot or,
+                    // if it had one only, the one in the other slot.
+                    if (g == 0) {
+                        if (before == 1 &&
+                            !(ok = wait_bounded(sh, &sh.slot_free[sl ^ 1], ((n - 1) >> 1) & 1, a)))
+                            break;
+                        mbar_arrive(&sh.tile_ready);
+                    }
                     if (prod == kProdA) {
                         mbar_arrive(&sh.in_full[sl]);
                         continue;
@@ -979,6 +1075,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
                     if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
                 }
+                before = blocks;
             }
         }
     } else if (warp == kStoreWarp && lane == 0) {
@@ -990,7 +1087,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
-                const int prod = tile.prod, blocks = tile.width >> 6, c0 = tile.j * blocks;
+                const int prod = tile.prod, blocks = tile.blocks >> tile.split;
+                const int c0 = tile.j * tile.blocks + tile.part * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
                 const int cb = prod == kProdX ? d.cbx : d.cba;
                 // the CTA's first block in memory, and its mirror image's columns
@@ -1042,7 +1140,9 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
             for (int t = q0; t < q1 && ok; ++t, ++it) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
-                const int prod = tile.prod, buf = it & 1, blocks = tile.width >> 6, c0 = tile.j * tile.width;
+                const int prod = tile.prod, buf = it & 1, blocks = tile.blocks >> tile.split;
+                const int first = tile.part * blocks;        // of the tile's blocks, the first to finish here
+                const int c0 = (tile.j * tile.blocks + first) * 64;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
                 const int64_t diag_at = d.diag;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
@@ -1053,7 +1153,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 float p0 = 0.0f, p1 = 0.0f, dc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sq = 0.0f;
                 if (prod == kProdA) {
                     // if the tile holds the diagonal of these rows, in this warp's 32 columns
-                    if (r0 >= c0 && r0 < c0 + tile.width && half == (quad & 1)) p0 = row_square(a, d, r);
+                    if (r0 >= c0 && r0 < c0 + blocks * 64 && half == (quad & 1)) p0 = row_square(a, d, r);
                 } else if (prod == kProdB) {
                     p0 = __ldcg(a.diag_a + d.diag + r);
 #pragma unroll
@@ -1066,12 +1166,15 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a);
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t sums = tmem + uint32_t(buf) * kOrthoTile + uint32_t(half) * 32 + (uint32_t(row0) << 16);
+                if (tile.split && !(ok = join_parts(sh, a, d, tile, sums, step, int(rank) * kEpiWarps + warp - 2)))
+                    break;
 #pragma unroll 1
                 for (int g = 0; g < blocks; ++g, ++n) {
-                    const int col = g * 64 + half * 32, c = c0 + col;
+                    const int c = c0 + g * 64 + half * 32;
                     const uint32_t sl = n & 1, slot = slot0 + sl * kSlotBytes;
                     float acc[32];
-                    load_acc32(tmem + uint32_t(buf) * kOrthoTile + uint32_t(col) + (uint32_t(row0) << 16), acc);
+                    load_acc32(sums + uint32_t(first + g) * 64, acc);
                     if (g + 1 == blocks) {   // the accumulator is free for the tile after next
                         // (its values are in registers: relaxed, a release would first wait for
                         // this warp's stores, a microsecond)
@@ -1315,6 +1418,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.update = update;
     a.f32 = update_dtype == DPG_F32;
     a.done = reinterpret_cast<int32_t*>(m.ws + m.o_done);
+    a.join = reinterpret_cast<int32_t*>(m.ws + m.o_join);
     a.skip = t_staged_skip;
     a.wait_ns = t_staged_timeout_ns > 0 ? uint64_t(t_staged_timeout_ns) : kWaitNs;
     t_staged_skip = -1;

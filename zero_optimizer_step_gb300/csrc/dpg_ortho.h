@@ -40,16 +40,23 @@ struct MatDesc {
     int64_t rowsq;        // first entry of X's row sums of squares, [cbx][padded rows]
     int32_t rows_pad;     // rows of X padded to 256
     int32_t norm0, norm1; // its items in the norm table
-    int32_t tiles[3];     // output tiles of each product (see lay_queue)
+    int32_t tiles[3];     // output tiles of each product (see lay_queue), each part counted
+    int32_t group0;       // its first group of parts
+    int32_t groups;       // A tiles that are summed in parts (0: none)
 };
 
-// One output tile of one product of one matrix: 256 rows from 256 i, `width`
-// (256 or 128) columns from width j.
-struct OrthoTile {
+// One output tile of one product of one matrix: 256 rows from 256 i, 64 blocks
+// columns from 64 blocks j.  A tile of A may be summed in parts: the pairs of
+// the parts each take a share of the sum's length, leave one another their
+// sums, and each finishes its share of the columns.
+struct alignas(16) OrthoTile {
     int32_t mat;
+    int32_t group;        // which tile in parts, of all
     int16_t i, j;
-    int16_t prod, width;
+    uint8_t prod, blocks; // blocks: 4 or 2
+    uint8_t part, split;  // split: log2 of the number of parts
 };
+static_assert(sizeof(OrthoTile) == 16, "one load");
 
 // Matrices whose shorter side is at most kSmallSide take the steps on their
 // Gram matrices (dpg_gram.cu) and none of the tiles.
@@ -113,11 +120,11 @@ struct Matrices {
     std::vector<ConvItem> conv_items;
     std::vector<ApplyItem> apply_items;
     std::vector<double> scales;        // 2 per parameter: spectral, rms
-    int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0;
+    int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0, n_groups = 0;
     int64_t n_small_copy = 0, n_small_part = 0, n_small_prod = 0;   // floats
     int64_t workspace_bytes = 0;
     // byte offsets in the workspace
-    int64_t o_diag = 0, o_rowsq = 0, o_part = 0, o_scal = 0, o_count = 0, o_done = 0, o_status = 0;
+    int64_t o_diag = 0, o_rowsq = 0, o_part = 0, o_scal = 0, o_count = 0, o_done = 0, o_join = 0, o_status = 0;
     int64_t o_small_copy = 0, o_small_part = 0, o_small_exp = 0, o_small_prod = 0;
 
     std::mutex mu;
