@@ -113,6 +113,13 @@ def test_orthogonalize_short_side(rows, cols, dtype):
         _ortho_case([(rows, cols, 2)], kind, dtype)
 
 
+@pytest.mark.parametrize("shapes", [[(100, 100, 30)], [(128, 600, 70), (20, 20, 5)],
+                                    [(1, 777, 1), (50, 40, 3), (200, 300, 1)], [(7, 64, 900), (260, 260, 1)]])
+def test_orthogonalize_short_sides_among_others(shapes):
+    # too many for the small launches at once, or beside larger ones
+    _ortho_case(shapes, "spiked", torch.bfloat16)
+
+
 def test_orthogonalize_list_of_matrices():
     # stacks, tall and wide, odd sizes whose slices start off 16-byte boundaries
     _ortho_case([(333, 129, 2), (1, 77, 3), (64, 32, 1), (129, 333, 1), (5, 5, 5), (640, 512, 2),

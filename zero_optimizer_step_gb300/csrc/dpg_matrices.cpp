@@ -15,6 +15,8 @@ namespace dpg {
 constexpr int64_t kMaxMatrices = 1 << 20;   // of one object
 
 static int64_t ceil_div(int64_t x, int64_t d) { return (x + d - 1) / d; }
+static int padded_side(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+
 // Items of a small matrix: Gram sums over about 64 groups of whole 32-column
 // blocks (every further group is a partial sum to write and to read again; very
 // long matrices get one per 1024 columns, up to 128), products of 64 columns.
@@ -24,7 +26,7 @@ static void small_items(Matrices& M, const MatDesc& d) {
     s.m = d.m;
     s.n = d.n;
     s.tall = d.tall;
-    s.mp = d.m <= 16 ? 16 : d.m <= 32 ? 32 : d.m <= 64 ? 64 : 128;
+    s.mp = padded_side(d.m);
     const int32_t mat = int32_t(M.small.size());
     const int64_t blocks = ceil_div(d.n, 32);
     s.copy = M.n_small_copy;
@@ -55,6 +57,47 @@ static int most_parts(const MatDesc& d) {
 
 static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 
+// Which matrices of at most kSmallSide rows take the Gram path, by padded side
+// (16, 32, 64, 128): true where five steps of all of them are estimated to take
+// longer as tiles.  The Gram path is three launches of its own: its steps take
+// 12, 17, 30 or 62 us for as many matrices as have their clusters resident, its
+// two passes over the columns up to 2 ns per column, nothing else runs beside
+// it.  Tiles are padded to 256 and their fifteen products follow one another,
+// but as many as there are pairs run at once, and beside larger matrices they
+// only fill gaps.  Measured, Gram path and tiles (us):
+//     1 of 128 x 1000     82   117      1 of 128 x 6000     94   151
+//     15 of 128 x 1000   113   141      16 of 128 x 6000   319   368
+//     16 of 128 x 1000   169   142      64 of 128 x 600    409   201
+//     30 of 100 x 100    147   113      64 of 64 x 2000    170   415
+//     64 x 32 and 32 x 10 23    96      4 of 128 x 50000   438   862
+static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols, bool* gram) {
+    static const double steps[4] = {12, 17, 30, 62}, pass[4] = {0.3e-3, 0.5e-3, 1e-3, 2e-3};
+    static const int64_t resident[4] = {1000, 300, 70, 15};
+    int64_t count[4] = {}, columns[4] = {}, longest[4] = {};
+    double tiles[4] = {};
+    bool larger = false;
+    for (int32_t q = 0; q < p.n_params; ++q) {
+        const int64_t m = std::min(rows[q], cols[q]), n = std::max(rows[q], cols[q]);
+        const int64_t k = p.numels[q] / (rows[q] * cols[q]);
+        if (m > kSmallSide) {
+            larger = larger || k > 0;
+            continue;
+        }
+        const int s = padded_side(m), c = s == 16 ? 0 : s == 32 ? 1 : s == 64 ? 2 : 3;
+        const double deep = double(ceil_div(n, kBlkCols)), wide = double(ceil_div(n, kOrthoTile));
+        count[c] += k;
+        columns[c] += k * n;
+        longest[c] = std::max(longest[c], n);
+        tiles[c] += double(k) * 5.0 * (std::max(0.3 * deep, 3.0) + 3.0 + 3.0 * wide) / 76.0;
+    }
+    for (int c = 3; c >= 0; --c) {
+        const double one = larger ? 0.0 : 90.0 + 1.5 * double(ceil_div(longest[c], kBlkCols));
+        gram[c] = steps[c] * double(ceil_div(count[c], resident[c])) + 10.0 + pass[c] * double(columns[c]) <=
+                  one + tiles[c];
+        larger = larger || (count[c] > 0 && !gram[c]);
+    }
+}
+
 // Lays the matrices out; false when an index would leave its type.
 static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Matrices& M) {
     M.total_padded = p.total_padded;
@@ -67,9 +110,15 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
         if ((count += p.numels[q] / (rows[q] * cols[q])) > kMaxMatrices) return false;
     // Items of the norm pass: as long as leaves about four per SM (each costs a fence and an
     // atomic besides its loads)
+    bool gram[4];
+    choose_gram(p, rows, cols, gram);
+    auto by_gram = [&](int64_t m) {
+        const int s = m <= kSmallSide ? padded_side(m) : 0;
+        return s && gram[s == 16 ? 0 : s == 32 ? 1 : s == 64 ? 2 : 3];
+    };
     int64_t tiled = 0;
     for (int32_t q = 0; q < p.n_params; ++q)
-        if (std::min(rows[q], cols[q]) > kSmallSide) tiled += p.numels[q];
+        if (!by_gram(std::min(rows[q], cols[q]))) tiled += p.numels[q];
     const int64_t norm_chunk = kNormChunk * std::clamp<int64_t>(ceil_div(tiled, 608 * int64_t(kNormChunk)), 1, 8);
     for (int32_t q = p.n_params - 1; q >= 0; --q) {   // flat order
         const double r = double(rows[q]), c = double(cols[q]);
@@ -89,7 +138,7 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.m = int32_t(std::min(rows[q], cols[q]));
             d.n = int32_t(std::max(rows[q], cols[q]));
             ++M.n_matrices;
-            if (d.m <= kSmallSide) {
+            if (by_gram(d.m)) {
                 small_items(M, d);
                 continue;
             }
@@ -236,14 +285,18 @@ static Deal deal(const Matrices& M, const std::vector<int32_t>& order, const Cut
 
 // Tiles of a product are 256 columns wide or, where that lets the step end
 // earlier in the model, 128: with few tiles, more pairs work at a product and
-// each has half the finish.  Measured with all three products at 256, with A
-// and B at 128, with all at 128 (us, 76 pairs):
-//     4 of 768 x 2304, 4 of 768 x 768   254   243   261
-//     4 of 768 x 768                    186   168   156
-//     4 of 1024 x 4096                  393   368   456
-//     4 of 2048 x 2048                  591   673   816
-// The model picks the fastest of the eight mixtures for these and for the six
-// other sets that it was compared with.
+// each has half the finish.  Where rows are long, A's sums are also cut into
+// two or four parts.  Measured with all three products at 256; A and B at 128;
+// all at 128; A at 256 in four parts (two where the rows allow no more) and B
+// at 128 (us, 76 pairs):
+//     4 of 768 x 2304, 4 of 768 x 768   257   246   263   250
+//     4 of 768 x 768                    186   168   156     -
+//     4 of 2048 x 2048                  591   673   816     -
+//     4 of 1024 x 4096                  395   369   454   355
+//     6 of 300 x 5000                   345   323   334   286
+//     200 x 10000                       343   328   335   198
+// For these, and for ten of twelve other sets, the model picks the fastest of
+// the mixtures; for the two (512 x 2048, 768 x 3000) one that is 2 % behind.
 void lay_queue(Matrices& M, int clusters) {
     std::vector<int32_t> order(M.mats.size());
     for (size_t k = 0; k < order.size(); ++k) order[k] = int32_t(k);

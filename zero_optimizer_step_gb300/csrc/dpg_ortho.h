@@ -58,8 +58,8 @@ struct alignas(16) OrthoTile {
 };
 static_assert(sizeof(OrthoTile) == 16, "one load");
 
-// Matrices whose shorter side is at most kSmallSide take the steps on their
-// Gram matrices (dpg_gram.cu) and none of the tiles.
+// Matrices whose shorter side is at most kSmallSide may take the steps on their
+// Gram matrices (dpg_gram.cu) and none of the tiles (see choose_gram).
 constexpr int kSmallSide = 128;
 struct SmallDesc {
     int64_t off;          // first element in the flat buffer
