@@ -1,6 +1,10 @@
 """The matrix-orthogonalising (Muon) operators on the GPU against plain forms:
 dpg_muon_momentum and dpg_muon_apply bit for bit against the same binary32
 operations in numpy, dpg_orthogonalize against the steps in 64 bits."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -404,3 +408,12 @@ def test_step_minimises_a_matrix_least_squares():
         dpg.dpg_muon_step(plan, mats, gs, [n // 2, n // 2], dpg.MuonHParams(lr=0.1, momentum=0.8), w, m,
                           upd, [p])
     assert losses[-1] < 0.05 * losses[0]
+
+
+def test_example_trains_a_small_network():
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(here, "examples", "muon_adam.py")], cwd=here,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    losses = [float(line.split()[-1]) for line in r.stdout.splitlines() if line.startswith("step")]
+    assert len(losses) == 4 and losses[-1] < 0.5 * losses[0], r.stdout
