@@ -500,8 +500,9 @@ typedef struct {
  * keeps what it needs of the plan (which may be destroyed before it), the
  * tile tables, and a device workspace of workspace_bytes that it allocates on
  * its first orthogonalisation or in dpg_matrices_upload (call that before a
- * stream capture; dpg_muon_apply needs the tables alone).  It serves one device; calls that use one object must not overlap
- * on the GPU.  Free with dpg_matrices_destroy. */
+ * stream capture; dpg_muon_apply needs the tables alone).  It serves one
+ * device; calls that use one object must not overlap on the GPU.  Free with
+ * dpg_matrices_destroy. */
 typedef struct dpg_matrices dpg_matrices_t;
 int dpg_plan_matrices(const dpg_plan_t* plan, const int64_t* rows, const int64_t* cols,
                       dpg_matrices_t** out);
@@ -536,11 +537,16 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * ortho_bf16 (flat bf16; may be `update` itself when that is bf16, and may be
  * the start of `update`'s memory when that is fp32).  Padding slots are
  * neither read nor written.
- * Arithmetic: X is held as a pair of fp16 numbers under a power-of-two scale
- * (22 bits), the off-diagonal parts of A and bA + cA^2 in one fp16 number,
+ * Arithmetic, shorter side above 128: X is held as a pair of fp16 numbers
+ * under a power-of-two scale (22 bits), the off-diagonal parts of A and bA + cA^2 in one fp16 number,
  * their diagonals and every sum in fp32.  The result is within about 1e-3
- * (relative Frobenius norm) of the exact one, also for matrices of low rank;
- * see the tests for the bound.  A matrix that holds a NaN or an infinity
+ * (relative Frobenius norm) of the exact one, also for matrices of low rank.
+ * Shorter side up to 128: either this, or the same steps on the Gram matrix
+ * (A_k+1 = Q_k A_k Q_k, Q_k = aI + b A_k + c A_k^2, X = Q_n-1 .. Q_0 U / norm)
+ * in fp32, within 1e-6 to 1e-3, whichever is faster for the matrices of the
+ * object; the choice depends on their shapes and numbers alone, and results
+ * are the same bits on every call.  Results are rounded to bf16 (1.7e-3).
+ * A matrix that holds a NaN or an infinity
  * gives NaN everywhere, a zero matrix zeros; other matrices are not affected.
  * Coefficients under which the iteration could leave fp16's range (singular
  * values above 32 starting from [0, 1]) are DPG_ERR_INVALID_ARG. */

@@ -167,7 +167,8 @@ struct RoundScale {
 };
 
 // ---------------------------------------------------------------------------
-// Frobenius norms.  One CTA per item (<= 16384 elements of one matrix): sums
+// Frobenius norms.  One CTA per item (16384 elements of one matrix or up to
+// eight times as many, see lay_out): sums
 // of squares in fp32, item sums and everything after in double.  Vectors whose
 // squares leave fp32's range (|u| beyond about 1e15, below 1e-15) are squared
 // in double: this GPU's binary64 rate is a few operations per SM and cycle, so
@@ -175,7 +176,9 @@ struct RoundScale {
 // times as long as the loads.  The CTA that finishes a matrix adds its items
 // in item order and writes the scale 2^k that puts max(norm, eps) 2^k into
 // [2^14, 2^15) -- every |u| 2^k is then below 2^15, and u 2^k is exact for
-// bf16 u -- and 1 / (max(norm, eps) 2^k).
+// bf16 u -- and 1 / (max(norm, eps) 2^k).  Reads each element once: 134 MB
+// (a 1B model's layer) in 26 us, 5.2 TB/s; 19 MB in 10.5 us, where the launch,
+// one memory latency and the last CTA's sum are half.
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
 // per element of a bf16 update (lo, all zero, is left out), 8 of an fp32 one.
 // A tall matrix is transposed through shared memory: 16-byte loads along U's
 // rows; 2-byte loads along X's rows took four times as long as the copy.
+// 134 MB read and 134 MB written in 57 us (4.7 TB/s), 34 + 34 MB in 14 us.
 // ---------------------------------------------------------------------------
 constexpr int kLoadPitch = 136;   // fp16 values of a transposed row: 16-byte rows, banks 4 words apart
 constexpr int kLoadSmem = kBlkRows * kLoadPitch * 2;
@@ -436,6 +440,15 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 // Two pairs that share a left operand by multicast (clusters of four, 24 KB per
 // stage and SM) were 3 % slower on every list tried, 144 SMs in use instead of
 // 152: what limits large matrices is the power cap, not L2.
+//
+// Measured, whole calls: 218M elements of an 8B model's layer 11.33 ms, 1.30
+// PFLOP/s of m^2 n + m^3 + 2 m^2 n flops per step (the 1.37 kW cap holds the
+// clock near 1.45 GHz, where a plain fp16 library product of 8192^3 runs at
+// 1.55 to 1.65); a 1B model's layer 1.92 ms, 1.23 PFLOP/s, of which norm and
+// load are 0.08; eight GPT-2-small attention matrices 0.243 ms, 0.52 PFLOP/s.
+// There, as for every list whose products last one or two rounds of tiles, the
+// way from product to product bounds it: finish 2 to 3 us, stores and their
+// count 1.4 us, operands 1 us, fifteen times.
 //
 // Every pair works through a queue of tiles that the host laid out once
 // (balanced by cost), the same in every step: A tiles, B tiles, X tiles of all
