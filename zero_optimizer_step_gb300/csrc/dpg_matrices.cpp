@@ -64,7 +64,8 @@ static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 // two passes over the columns up to 2 ns per column, nothing else runs beside
 // it.  Tiles are padded to 256 and their fifteen products follow one another,
 // but as many as there are pairs run at once, and beside larger matrices they
-// only fill gaps.  Measured, Gram path and tiles (us):
+// only fill gaps.  Lists whose padded tiles would take more than 16 GB stay on
+// the Gram path, which needs a third of that.  Measured, Gram path and tiles (us):
 //     1 of 128 x 1000     82   117      1 of 128 x 6000     94   151
 //     15 of 128 x 1000   113   141      16 of 128 x 6000   319   368
 //     16 of 128 x 1000   169   142      64 of 128 x 600    409   201
@@ -73,7 +74,7 @@ static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols, bool* gram) {
     static const double steps[4] = {12, 17, 30, 62}, pass[4] = {0.3e-3, 0.5e-3, 1e-3, 2e-3};
     static const int64_t resident[4] = {1000, 300, 70, 15};
-    int64_t count[4] = {}, columns[4] = {}, longest[4] = {};
+    int64_t count[4] = {}, columns[4] = {}, longest[4] = {}, blocks[4] = {};
     double tiles[4] = {};
     bool larger = false;
     for (int32_t q = 0; q < p.n_params; ++q) {
@@ -88,12 +89,14 @@ static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols,
         count[c] += k;
         columns[c] += k * n;
         longest[c] = std::max(longest[c], n);
+        blocks[c] += k * 8 * (3 * ceil_div(n, kOrthoTile) + 2);   // as lay_out counts them
         tiles[c] += double(k) * 5.0 * (std::max(0.3 * deep, 3.0) + 3.0 + 3.0 * wide) / 76.0;
     }
     for (int c = 3; c >= 0; --c) {
         const double one = larger ? 0.0 : 90.0 + 1.5 * double(ceil_div(longest[c], kBlkCols));
-        gram[c] = steps[c] * double(ceil_div(count[c], resident[c])) + 10.0 + pass[c] * double(columns[c]) <=
-                  one + tiles[c];
+        gram[c] = blocks[c] * kBlkBytes > (int64_t(16) << 30) ||
+                  steps[c] * double(ceil_div(count[c], resident[c])) + 10.0 + pass[c] * double(columns[c]) <=
+                      one + tiles[c];
         larger = larger || (count[c] > 0 && !gram[c]);
     }
 }
