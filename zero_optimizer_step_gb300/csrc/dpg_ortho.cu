@@ -904,7 +904,6 @@ __device__ __noinline__ bool join_parts(OrthoShared& sh, const OrthoArgs& a, con
     bool ok = true;
     if (lane == 0) {
         int32_t* join = a.join + int64_t(t.group) * (2 * kEpiWarps) + warp;
-        __threadfence();
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" :: "l"(join) : "memory");
         ok = wait_count(sh, join, (step + 1) << t.split, a);
     }
@@ -1132,10 +1131,10 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     mbar_arrive(&sh.slot_free[sl]);
                 }
                 if (!ok) break;
-                // all of the tile is in memory before its count
+                // all of the tile is in memory before its count (the release covers what the
+                // finishing warps wrote, too: they arrived at out_ready after it)
                 asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                 asm volatile("fence.proxy.async;" ::: "memory");
-                __threadfence();
                 asm volatile("red.release.gpu.global.add.s32 [%0], 1;" :: "l"(done) : "memory");
             }
         }
