@@ -71,6 +71,7 @@ static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 //     16 of 128 x 1000   169   142      64 of 128 x 600    409   201
 //     30 of 100 x 100    147   113      64 of 64 x 2000    170   415
 //     64 x 32 and 32 x 10 23    96      4 of 128 x 50000   438   862
+// (Later steps made the Gram times 1 to 5 %, the tiles' 2 to 4 % shorter.)
 static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols, bool* gram) {
     static const double steps[4] = {12, 17, 30, 62}, pass[4] = {0.3e-3, 0.5e-3, 1e-3, 2e-3};
     static const int64_t resident[4] = {1000, 300, 70, 15};
@@ -298,7 +299,8 @@ static Deal deal(const Matrices& M, const std::vector<int32_t>& order, const Cut
 //     4 of 1024 x 4096                  395   369   454   355
 //     6 of 300 x 5000                   345   323   334   286
 //     200 x 10000                       343   328   335   198
-// For these, and for ten of twelve other sets, the model picks the fastest of
+// (Later steps made all of them 2 to 4 % faster.)  For these, and for ten of
+// twelve other sets, the model picks the fastest of
 // the mixtures; for the two (512 x 2048, 768 x 3000) one that is 2 % behind.
 void lay_queue(Matrices& M, int clusters) {
     std::vector<int32_t> order(M.mats.size());

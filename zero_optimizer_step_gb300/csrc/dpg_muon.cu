@@ -9,8 +9,8 @@
 // different points of their loads and stores keep DRAM busy.
 //
 // Measured (one GB300, whole calls): momentum of 28.3M elements, R = 8, bf16,
-// 736 MB in 104.8 us (7.0 TB/s); 134M elements, fp32 update, 3758 MB in 527 us
-// (7.1 TB/s); 42M elements, R = 4, fp32 gradients, 1090 MB in 148 us (7.4 TB/s).
+// 736 MB in 105 us (7.0 TB/s); 134M elements, fp32 update, 3758 MB in 529 us
+// (7.1 TB/s); 42M elements, R = 4, fp32 gradients, 1090 MB in 149 us (7.3 TB/s).
 // Update of 28.3M elements with four views, 510 MB in 76 us (6.7 TB/s); of 134M
 // with one, 1610 MB in 230 us (7.0 TB/s).  A plain copy reaches 6.8.  Tiny calls are the host's 10 to 20 us.
 #include <cuda_bf16.h>

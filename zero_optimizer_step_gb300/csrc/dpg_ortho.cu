@@ -441,14 +441,14 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 // stage and SM) were 3 % slower on every list tried, 144 SMs in use instead of
 // 152: what limits large matrices is the power cap, not L2.
 //
-// Measured, whole calls: 218M elements of an 8B model's layer 11.33 ms, 1.30
+// Measured, whole calls: 218M elements of an 8B model's layer 11.4 ms, 1.29
 // PFLOP/s of m^2 n + m^3 + 2 m^2 n flops per step (the 1.37 kW cap holds the
 // clock near 1.45 GHz, where a plain fp16 library product of 8192^3 runs at
-// 1.55 to 1.65); a 1B model's layer 1.92 ms, 1.23 PFLOP/s, of which norm and
-// load are 0.08; eight GPT-2-small attention matrices 0.243 ms, 0.52 PFLOP/s.
+// 1.55 to 1.65); a 1B model's layer 1.91 to 1.98 ms, 1.2 PFLOP/s, of which norm
+// and load are 0.08; eight GPT-2-small attention matrices 0.233 ms, 0.54 PFLOP/s.
 // There, as for every list whose products last one or two rounds of tiles, the
 // way from product to product bounds it: finish 2 to 3 us, stores and their
-// count 1.4 us, operands 1 us, fifteen times.
+// count 1 us, operands 1 us, fifteen times.
 //
 // Every pair works through a queue of tiles that the host laid out once
 // (balanced by cost), the same in every step: A tiles, B tiles, X tiles of all
