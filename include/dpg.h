@@ -543,9 +543,13 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * (relative Frobenius norm) of the exact one, also for matrices of low rank.
  * Shorter side up to 128: either this, or the same steps on the Gram matrix
  * (A_k+1 = Q_k A_k Q_k, Q_k = aI + b A_k + c A_k^2, X = Q_n-1 .. Q_0 U / norm)
- * in fp32, within 1e-6 to 1e-3, whichever is faster for the matrices of the
- * object; the choice depends on their shapes and numbers alone, and results
- * are the same bits on every call.  Results are rounded to bf16 (1.7e-3).
+ * in fp32, whichever is faster for the matrices of the object; the choice
+ * depends on their shapes and numbers alone, and results are the same bits on
+ * every call.  Five default steps are within 1e-6 to 1e-3; steps whose a_k^2
+ * multiply to more (2.4e5) start from the new X every few steps and are as near
+ * as those on X in fp32 (2e-4, and what 2^-21 of U's norm in U would change: the
+ * product of the a_k times as much in directions that U lacks).  Results are
+ * rounded to bf16 (1.7e-3).
  * A matrix that holds a NaN or an infinity
  * gives NaN everywhere, a zero matrix zeros; other matrices are not affected.
  * Coefficients under which the iteration could leave fp16's range (singular

@@ -1,0 +1,112 @@
+"""dpg_orthogonalize beyond five default steps, and on matrices whose rows
+depend on one another, against the steps in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import zero_optimizer_step_gb300 as dpg
+from muon_schedules import LONG_REL, SCHEDULES, STEPS_REL, allowed, condition, make_low_rank, to_dtype
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+LONG = [k for k in SCHEDULES if k != "5"]
+KINDS = ["rank1", "rank4", "half", "tail", "repeated", "equal", "gauss", "spiked"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from zero_optimizer_step_gb300 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def _takes_tiles(mats, upd, out):
+    """Whether all of the object's matrices take the tiles: three launches
+    (norms, load, steps), where the Gram path takes three for each of its
+    phases and six default steps are two of them."""
+    before = dpg.dpg_launch_count()
+    dpg.dpg_orthogonalize(mats, upd, dpg.MuonHParams(coeffs=SCHEDULES["6"]), out)
+    return dpg.dpg_launch_count() - before == 3
+
+
+def _check(shapes, kinds, name, dtype, steps_rel, tiles, seed=31):
+    """One object over `shapes`; the matrices take `kinds` in turn.  tiles: the
+    path its matrices must have been given."""
+    rng = np.random.Generator(np.random.Philox(seed))
+    plan = dpg.dpg_plan_buckets([r * c * k for r, c, k in shapes], 1 << 40, 1)
+    mats = dpg.dpg_plan_matrices(plan, [s[0] for s in shapes], [s[1] for s in shapes])
+    hp = dpg.MuonHParams(coeffs=SCHEDULES[name], eps=1e-20)
+    flat = np.zeros(plan.total_padded, np.float64)
+    items = []
+    for p, (r, c, k) in enumerate(shapes):
+        for i in range(k):
+            at = slice(int(plan.param_offset[p]) + i * r * c, int(plan.param_offset[p]) + (i + 1) * r * c)
+            kind = kinds[len(items) % len(kinds)]
+            u = to_dtype(make_low_rank(kind, r, c, rng), dtype == torch.bfloat16)
+            flat[at] = u.reshape(-1)
+            items.append((kind, r, c, at, u))
+    upd = torch.from_numpy(flat.astype(np.float32)).to(dtype).to(DEV)
+    out = torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV)
+    assert _takes_tiles(mats, upd, out) == tiles
+    dpg.dpg_orthogonalize(mats, upd, hp, out)
+    dpg.dpg_matrices_status(mats)
+    got = out.double().cpu().numpy()
+    for kind, r, c, at, u in items:
+        want, moved = condition(u, hp.coeffs, hp.eps, rng)
+        y = got[at].reshape(r, c)
+        assert np.all(np.isfinite(y)), f"{kind} {r}x{c}"
+        rel = np.linalg.norm(y - want) / np.linalg.norm(want)
+        assert rel <= allowed(steps_rel, moved), f"{kind} {r}x{c}: {rel:.3e}, moved {moved:.1e}"
+        # no direction grows past what the steps can make of a singular value
+        assert np.linalg.norm(y, 2) <= 2.2, f"{kind} {r}x{c}"
+
+
+@pytest.mark.parametrize("name", LONG)
+@pytest.mark.parametrize("rows,cols", [(16, 40), (40, 16), (32, 64), (64, 300), (128, 600), (600, 100), (5, 7)])
+def test_long_schedules_short_side(rows, cols, name):
+    _check([(rows, cols, len(KINDS))], KINDS, name, torch.bfloat16, LONG_REL, tiles=False)
+    _check([(rows, cols, len(KINDS))], KINDS, name, torch.float32, LONG_REL, tiles=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shapes,tiles", [([(100, 200, 8)], False), ([(200, 100, 8)], False), ([(31, 90, 8)], False),
+                                          ([(256, 512, 8)], True), ([(700, 300, 8)], True)])
+def test_five_steps_on_dependent_rows(shapes, tiles, dtype):
+    _check(shapes, KINDS, "5", dtype, STEPS_REL, tiles)
+
+
+def test_long_schedules_are_deterministic_and_leave_no_trace():
+    # the same bits every time, also for a default call before and after
+    rng = np.random.Generator(np.random.Philox(32))
+    shapes = [(300, 500, 2), (64, 90, 2)]
+    plan = dpg.dpg_plan_buckets([r * c * k for r, c, k in shapes], 1 << 40, 1)
+    mats = dpg.dpg_plan_matrices(plan, [s[0] for s in shapes], [s[1] for s in shapes])
+    u = torch.from_numpy(rng.standard_normal(plan.total_padded).astype(np.float32)).to(DEV)
+    outs = [torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV) for _ in range(5)]
+    for o, name in zip(outs, ("5", "16", "5", "16", "5")):
+        dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(coeffs=SCHEDULES[name]), o)
+    dpg.dpg_matrices_status(mats)
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[0], outs[4]) and torch.equal(outs[1], outs[3])
+
+
+def test_step_with_a_long_schedule_in_a_cuda_graph():
+    shapes = [(300, 120, 1), (64, 32, 1)]
+    plan = dpg.dpg_plan_buckets([r * c * k for r, c, k in shapes], 1 << 18, 1)
+    mats = dpg.dpg_plan_matrices(plan, [s[0] for s in shapes], [s[1] for s in shapes])
+    g = torch.Generator().manual_seed(4)
+    n = plan.total_padded
+    grads = [(torch.randn(n, generator=g) * 1e-3).to(torch.bfloat16).to(DEV)]
+    w, m = (torch.randn(n, generator=g) * 0.02).to(DEV), torch.zeros(n, device=DEV)
+    upd = torch.zeros(n, device=DEV)
+    hp = dpg.MuonHParams(eps=1e-12, coeffs=SCHEDULES["8"])
+    w2, m2 = w.clone(), m.clone()
+    for _ in range(2):      # (the first call of a schedule allocates what it needs)
+        dpg.dpg_muon_step(plan, mats, grads, [7], hp, w2, m2, upd, [])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        dpg.dpg_muon_step(plan, mats, grads, [7], hp, w, m, upd, [])
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(w, w2) and torch.equal(m, m2)

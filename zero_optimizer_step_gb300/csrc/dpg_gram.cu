@@ -15,8 +15,12 @@
 // Everything is binary32.  An error e in A_k moves the small eigenvalues l by
 // e / l relative, so the 11-bit operands of the large matrices' tensor-core
 // products would lose the directions that the steps are there to bring up;
-// with 24 bits the result is within 1e-6 (Gaussian) to 1e-3 (rank one) of the
-// exact one.
+// with 24 bits the result of five default steps is within 1e-6 (Gaussian) to
+// 7e-4 (rank one) of the exact one.  A step multiplies e by up to a^2, and what
+// e made negative is never brought back: twelve steps on one A_0 ended in NaN
+// for low ranks.  Longer schedules are therefore cut into phases (gram_phases):
+// P is applied to the copy of X, and the Gram matrix is summed anew, which is
+// as good as the iteration on X itself.
 //
 // Times (128 x 6000, five steps): sum 18 us, steps 67 us, application 12 us;
 // the steps alone 12, 17, 30, 62 us at 16, 32, 64, 128 rows.  A step of 128
@@ -39,14 +43,15 @@ struct GramArgs {
     const SmallDesc* mats;
     const void* update;
     uint16_t* out;           // flat bf16
-    float* copy;             // U, 32 columns at a time: [block][padded rows][32]
+    float* copy;             // U, or X after a phase, 32 columns at a time: [block][padded rows][32]
     float* part;             // per Gram item: partial sum, [padded rows]^2
     int32_t* part_exp;       // per Gram item: its values are U 2^-exp
     float* prod;             // per matrix: the product of the Q_k, [padded rows]^2
     int32_t* exp;            // per matrix: prod is for U 2^-exp
     int32_t* status;         // 0, or the error of the first wait that ran out
     double eps;
-    int32_t n_steps;
+    int32_t first;           // the copy holds U, to be divided by its norm; else X as it is
+    int32_t n_steps;         // of this phase
     float a[DPG_MAX_NS_STEPS], b[DPG_MAX_NS_STEPS], c[DPG_MAX_NS_STEPS];
 };
 
@@ -64,7 +69,9 @@ __device__ __forceinline__ float pow2(int k) {
 // can hold, so columns are scaled by the power of two of the largest value so
 // far, and the sum with them when that grows.
 // ---------------------------------------------------------------------------
-template <int MP, bool F32>
+enum : int { kFromBf16 = 0, kFromF32 = 1, kFromCopy = 2 };   // what is summed
+
+template <int MP, int FROM>
 __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d, const SmallItem& it, float* sm) {
     constexpr int T = MP / 16, P = MP + 4, kPer = MP * 32 / kGramThreads;
     float* tile = sm;                    // [32][P]
@@ -81,24 +88,31 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
         for (int j = 0; j < kTwo; ++j) acc[i][j] = 0;
     int e = -1000;
     float x[kPer];
+    const bool tall = FROM != kFromCopy && d.tall;   // (the copy holds X's rows)
     // all loads before any use (a load under its own branch would be waited
     // for there, one memory latency per value): out of range ones read U's
     // first element
     auto fetch = [&](int c0) {
+        if (FROM == kFromCopy) {           // whole blocks, zeros past the matrix
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                x[i] = __ldg(a.copy + d.copy + int64_t(c0 >> 5) * (MP * 32) + int(threadIdx.x) + i * kGramThreads);
+            return;
+        }
         uint32_t raw[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int q = int(threadIdx.x) + i * kGramThreads;
-            const int r = d.tall ? q % MP : q >> 5, c = c0 + (d.tall ? q / MP : q & 31);
+            const int r = tall ? q % MP : q >> 5, c = c0 + (tall ? q / MP : q & 31);
             const int64_t at = d.off + (r < d.m && c < d.n
-                                            ? (d.tall ? int64_t(c) * d.m + r : int64_t(r) * d.n + c) : 0);
-            raw[i] = F32 ? __ldg(static_cast<const uint32_t*>(a.update) + at)
-                         : uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + at)) << 16;
+                                            ? (tall ? int64_t(c) * d.m + r : int64_t(r) * d.n + c) : 0);
+            raw[i] = FROM == kFromF32 ? __ldg(static_cast<const uint32_t*>(a.update) + at)
+                                      : uint32_t(__ldg(static_cast<const uint16_t*>(a.update) + at)) << 16;
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int q = int(threadIdx.x) + i * kGramThreads;
-            const int r = d.tall ? q % MP : q >> 5, c = c0 + (d.tall ? q / MP : q & 31);
+            const int r = tall ? q % MP : q >> 5, c = c0 + (tall ? q / MP : q & 31);
             x[i] = r < d.m && c < d.n ? __uint_as_float(raw[i]) : 0.0f;
         }
     };
@@ -109,8 +123,8 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int q = int(threadIdx.x) + i * kGramThreads;
-            const int r = d.tall ? q % MP : q >> 5, c = d.tall ? q / MP : q & 31;
-            copy[r * 32 + c] = x[i];
+            const int r = tall ? q % MP : q >> 5, c = tall ? q / MP : q & 31;
+            if (FROM != kFromCopy) copy[r * 32 + c] = x[i];
             top = fmaxf(top, fabsf(x[i]));
         }
 #pragma unroll
@@ -134,7 +148,7 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int q = int(threadIdx.x) + i * kGramThreads;
-            const int r = d.tall ? q % MP : q >> 5, c = d.tall ? q / MP : q & 31;
+            const int r = tall ? q % MP : q >> 5, c = tall ? q / MP : q & 31;
             tile[c * P + r] = x[i] * s0 * s1;
         }
         __syncthreads();
@@ -163,7 +177,7 @@ __device__ __forceinline__ void gram_item(const GramArgs& a, const SmallDesc& d,
     if (threadIdx.x == 0) a.part_exp[it.index] = e;
 }
 
-template <bool F32>
+template <int FROM>
 __global__ void __launch_bounds__(kGramThreads) k_gram_sum(const __grid_constant__ GramArgs a,
                                                           const SmallItem* items) {
     __shared__ __align__(16) float sm[32 * (kSmallSide + 4) + 16];
@@ -171,10 +185,10 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_sum(const __grid_constant
     const SmallItem it = items[blockIdx.x];
     const SmallDesc d = a.mats[it.mat];
     switch (d.mp) {
-        case 16: return gram_item<16, F32>(a, d, it, sm);
-        case 32: return gram_item<32, F32>(a, d, it, sm);
-        case 64: return gram_item<64, F32>(a, d, it, sm);
-        default: return gram_item<128, F32>(a, d, it, sm);
+        case 16: return gram_item<16, FROM>(a, d, it, sm);
+        case 32: return gram_item<32, FROM>(a, d, it, sm);
+        case 64: return gram_item<64, FROM>(a, d, it, sm);
+        default: return gram_item<128, FROM>(a, d, it, sm);
     }
 }
 
@@ -398,9 +412,9 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (t == 0) {
-            // divisor of U 2^-e: max(norm, eps) 2^-e
-            double den = sqrt(s);
-            if (e > -1000) den = fmax(den, scalbn(a.eps, -e));
+            // divisor of U 2^-e: max(norm, eps) 2^-e; of X 2^-e: 2^-e
+            double den = a.first ? sqrt(s) : 1.0;
+            if (e > -1000) den = a.first ? fmax(den, scalbn(a.eps, -e)) : scalbn(1.0, -e);
             const bool ok = s < 3.0e38;  // a NaN or an infinity in the matrix: NaN everywhere
             if (!(den > 0.0)) den = 1.0; // a zero matrix stays zero
             den_sh = ok ? den : __longlong_as_double(0x7FF8000000000000ll);
@@ -488,11 +502,13 @@ constexpr int kMixedMost = 15;   // clusters of eight that are resident at once
 
 // ---------------------------------------------------------------------------
 // O = P U, 64 columns per CTA: a thread holds MP / 16 rows by 4 columns.
+// BACK: not the end, the new X goes back into the copy (a CTA has all of its
+// columns in shared memory by then, and no other one reads them).
 // ---------------------------------------------------------------------------
 constexpr int kProdCols = 64;
 constexpr int gram_apply_smem(int mp) { return (mp * (mp + 4) + mp * kProdCols) * 4; }
 
-template <int MP>
+template <int MP, bool BACK>
 __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d, const SmallItem& it, float* sm) {
     constexpr int T = MP / 16, PP = MP + 4;
     float* P = sm;                       // [MP][PP]
@@ -507,8 +523,9 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
 #pragma unroll
     for (int i = 0; i < kX; ++i) {
         const int q = t + i * kGramThreads, blk = it.c0 + q / (MP * 8) * 32 < d.n ? q / (MP * 8) : 0;
-        x[i] = __ldg(reinterpret_cast<const float4*>(a.copy + d.copy + int64_t((it.c0 >> 5) + blk) * (MP * 32)) +
-                     q % (MP * 8));
+        const float4* from =
+            reinterpret_cast<const float4*>(a.copy + d.copy + int64_t((it.c0 >> 5) + blk) * (MP * 32)) + q % (MP * 8);
+        x[i] = BACK ? *from : __ldg(from);
     }
 #pragma unroll
     for (int i = 0; i < kP; ++i)
@@ -553,7 +570,11 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
         if (r >= d.m) continue;
         const float2 o01 = halves_of(acc[i][0]), o23 = halves_of(acc[i][1]);
         const float o[4] = {o01.x, o01.y, o23.x, o23.y};
-        if (vec && c < d.n) {
+        if (BACK) {
+            if (c < d.n)                 // (a started block is whole in the copy)
+                *reinterpret_cast<float4*>(a.copy + d.copy + int64_t(c >> 5) * (MP * 32) + r * 32 + (c & 31)) =
+                    make_float4(o[0], c + 1 < d.n ? o[1] : 0.0f, c + 2 < d.n ? o[2] : 0.0f, c + 3 < d.n ? o[3] : 0.0f);
+        } else if (vec && c < d.n) {
             const __nv_bfloat162 u = __floats2bfloat162_rn(o[0], o[1]);
             const __nv_bfloat162 v = __floats2bfloat162_rn(o[2], o[3]);
             *reinterpret_cast<uint2*>(a.out + d.off + int64_t(r) * d.n + c) =
@@ -568,6 +589,7 @@ __device__ __forceinline__ void apply_item(const GramArgs& a, const SmallDesc& d
     }
 }
 
+template <bool BACK>
 __global__ void __launch_bounds__(kGramThreads) k_gram_apply(const __grid_constant__ GramArgs a,
                                                             const SmallItem* items) {
     extern __shared__ __align__(16) float gram_sm[];
@@ -575,10 +597,10 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_apply(const __grid_consta
     const SmallItem it = items[blockIdx.x];
     const SmallDesc d = a.mats[it.mat];
     switch (d.mp) {
-        case 16: return apply_item<16>(a, d, it, gram_sm);
-        case 32: return apply_item<32>(a, d, it, gram_sm);
-        case 64: return apply_item<64>(a, d, it, gram_sm);
-        default: return apply_item<128>(a, d, it, gram_sm);
+        case 16: return apply_item<16, BACK>(a, d, it, gram_sm);
+        case 32: return apply_item<32, BACK>(a, d, it, gram_sm);
+        case 64: return apply_item<64, BACK>(a, d, it, gram_sm);
+        default: return apply_item<128, BACK>(a, d, it, gram_sm);
     }
 }
 
@@ -592,7 +614,9 @@ int gram_prepare() {
                                       gram_steps_smem<128>()));
     DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_steps_mixed, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       gram_steps_smem<128>()));
-    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_apply, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_apply<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gram_apply_smem(kSmallSide)));
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_gram_apply<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       gram_apply_smem(kSmallSide)));
     return DPG_OK;
 }
@@ -622,7 +646,9 @@ static int launch_clusters(void (*k)(P...), int n, int ctas, int smem, cudaStrea
     return after_launch(who);
 }
 
-static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_hparams* hp, void* out) {
+// arguments of steps [k0, k1) of hp
+static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_hparams* hp, int k0, int k1,
+                          void* out) {
     GramArgs a{};
     a.mats = m.d_small;
     a.update = update;
@@ -634,11 +660,12 @@ static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_
     a.prod = reinterpret_cast<float*>(m.ws + m.o_small_prod);
     a.status = reinterpret_cast<int32_t*>(m.ws + m.o_status);
     a.eps = hp->eps;
-    a.n_steps = hp->n_steps;
-    for (int k = 0; k < hp->n_steps; ++k) {
-        a.a[k] = float(hp->coeffs[k][0]);
-        a.b[k] = float(hp->coeffs[k][1]);
-        a.c[k] = float(hp->coeffs[k][2]);
+    a.first = k0 == 0;
+    a.n_steps = k1 - k0;
+    for (int k = k0; k < k1; ++k) {
+        a.a[k - k0] = float(hp->coeffs[k][0]);
+        a.b[k - k0] = float(hp->coeffs[k][1]);
+        a.c[k - k0] = float(hp->coeffs[k][2]);
     }
     return a;
 }
@@ -646,15 +673,12 @@ static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_
 int gram_read(const Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
               void* out, cudaStream_t s, const char* who) {
     if (m.small.empty()) return DPG_OK;
-    return launch_k(update_dtype == DPG_F32 ? k_gram_sum<true> : k_gram_sum<false>, unsigned(m.gram_items.size()),
-                    kGramThreads, s, who, gram_args(m, update, hp, out),
+    return launch_k(update_dtype == DPG_F32 ? k_gram_sum<kFromF32> : k_gram_sum<kFromBf16>,
+                    unsigned(m.gram_items.size()), kGramThreads, s, who, gram_args(m, update, hp, 0, 0, out),
                     static_cast<const SmallItem*>(m.d_gram_items));
 }
 
-int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, void* out, cudaStream_t s,
-                const char* who) {
-    if (m.small.empty()) return DPG_OK;
-    const GramArgs a = gram_args(m, update, hp, out);
+static int launch_gram_steps(const Matrices& m, const GramArgs& a, cudaStream_t s, const char* who) {
     const int32_t *w = m.d_small_order, *n = m.small_count;
     int st = DPG_OK;
     if ((n[0] > 0) + (n[1] > 0) + (n[2] > 0) + (n[3] > 0) > 1 && int(m.small.size()) <= kMixedMost) {
@@ -673,10 +697,26 @@ int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* h
             st = launch_clusters(k_gram_steps<128>, n[3], 8, gram_steps_smem<128>(), s, who, a,
                                  w + n[0] + n[1] + n[2]);
     }
-    if (st != DPG_OK) return st;
+    return st;
+}
+
+int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, const OrthoSchedule& sch,
+                void* out, cudaStream_t s, const char* who) {
+    if (m.small.empty()) return DPG_OK;
     const int mp = m.small_count[3] ? 128 : m.small_count[2] ? 64 : m.small_count[1] ? 32 : 16;
-    return launch_k(k_gram_apply, unsigned(m.prod_items.size()), kGramThreads, size_t(gram_apply_smem(mp)), s, who,
-                    a, static_cast<const SmallItem*>(m.d_prod_items));
+    int st = DPG_OK;
+    for (int p = 0; p < sch.n_phases && st == DPG_OK; ++p) {
+        const bool last = p + 1 == sch.n_phases;
+        const GramArgs a = gram_args(m, update, hp, p ? sch.phase_end[p - 1] : 0, sch.phase_end[p], out);
+        st = launch_gram_steps(m, a, s, who);
+        if (st == DPG_OK)
+            st = launch_k(last ? k_gram_apply<false> : k_gram_apply<true>, unsigned(m.prod_items.size()), kGramThreads,
+                          size_t(gram_apply_smem(mp)), s, who, a, static_cast<const SmallItem*>(m.d_prod_items));
+        if (st == DPG_OK && !last)
+            st = launch_k(k_gram_sum<kFromCopy>, unsigned(m.gram_items.size()), kGramThreads, s, who, a,
+                          static_cast<const SmallItem*>(m.d_gram_items));
+    }
+    return st;
 }
 
 }  // namespace dpg

@@ -384,7 +384,43 @@ static float scale_for(double most) {
     return float(std::ldexp(1.0, 14 - e));
 }
 
-int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who) {
+// How much a step may enlarge an error in an eigenvalue l of the Gram matrix:
+// the largest slope of l (a + b l + c l^2)^2 over [0, hi], at least 1.  It is
+// a^2 at 0, and there it counts: an eigenvalue that rounding made negative
+// meets a factor that grows with its size, so nothing brings it back.
+static double gram_growth(double a, double b, double c, double hi) {
+    double most = 1.0;
+    for (int i = 0; i <= 16; ++i) {
+        const double l = hi * i / 16.0, q = a + l * (b + l * c);
+        most = std::max(most, std::fabs(q * (q + 2.0 * l * (b + 2.0 * c * l))));
+    }
+    return most;
+}
+
+// Cuts the steps into phases; the Gram path applies a phase's product to X and
+// sums the Gram matrix of the new X before the next one.  growth: of each step.
+// The sum's rounding (1e-8 to 1e-7 of the largest eigenvalue) times the growth
+// of a phase is what a phase adds to the result.  Five default steps (2.4e5) as
+// one phase: up to 7e-4 for a matrix of rank one, three launches.  Whatever
+// grows by more is cut at 2000 (three default steps), where the phases together
+// leave no more than the iteration on X in binary32 does (1e-5 to 2e-4): each
+// phase is three launches more, and cut at 2.4e5 too they left up to 2e-3.
+static void gram_phases(const double* growth, int n_steps, OrthoSchedule* sch) {
+    constexpr double kOnePhase = 2.4e5, kEach = 2000.0;
+    double all = 1.0, phase = 1.0;
+    for (int k = 0; k < n_steps; ++k) all *= growth[k];
+    sch->n_phases = 0;
+    for (int k = 0; k < n_steps; ++k) {
+        if (k > 0 && phase * growth[k] > kEach && all > kOnePhase) {
+            sch->phase_end[sch->n_phases++] = k;
+            phase = 1.0;
+        }
+        phase *= growth[k];
+    }
+    sch->phase_end[sch->n_phases++] = n_steps;
+}
+
+int ortho_steps(const dpg_muon_hparams* hp, OrthoSchedule* sch, const char* who) {
     if (!hp) return fail(DPG_ERR_INVALID_ARG, "%s: hparams is NULL", who);
     if (hp->n_steps < 1 || hp->n_steps > DPG_MAX_NS_STEPS)
         return fail(DPG_ERR_INVALID_ARG, "%s: n_steps %d outside [1, %d]", who, hp->n_steps,
@@ -395,13 +431,14 @@ int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who) {
     // at most 1 for X_0 and at most largest_odd() of the previous bound after
     // a step; the entries of A and of bA + cA^2 follow.  The 1% covers what
     // the roundings of a step can add.
-    double top = 1.0;
+    double top = 1.0, growth[DPG_MAX_NS_STEPS];
     float sx = 0.0f;
     for (int k = 0; k < hp->n_steps; ++k) {
         const double a = hp->coeffs[k][0], b = hp->coeffs[k][1], c = hp->coeffs[k][2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
             return fail(DPG_ERR_INVALID_ARG, "%s: coeffs[%d] not finite", who, k);
-        OrthoStep& s = steps[k];
+        growth[k] = gram_growth(a, b, c, top * top);
+        OrthoStep& s = sch->st[k];
         s.a = float(a);
         s.b = float(b);
         s.c = float(c);
@@ -415,6 +452,7 @@ int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who) {
             return fail(DPG_ERR_INVALID_ARG, "%s: after step %d singular values may reach %g", who, k, top);
         s.sx_next = sx = scale_for(top);
     }
+    gram_phases(growth, hp->n_steps, sch);
     return DPG_OK;
 }
 

@@ -237,15 +237,15 @@ int dpg_orthogonalize(dpg_matrices_t* mats, const void* update, int32_t update_d
     dpg::clear_error();
     const dpg::Trace trace("dpg_orthogonalize");
     if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_orthogonalize: mats is NULL");
-    dpg::OrthoStep steps[DPG_MAX_NS_STEPS];
-    int st = dpg::ortho_steps(hp, steps, "dpg_orthogonalize");
+    dpg::OrthoSchedule sch;
+    int st = dpg::ortho_steps(hp, &sch, "dpg_orthogonalize");
     if (st != DPG_OK) return st;
     if (mats->m.n_matrices == 0) return DPG_OK;
     st = dpg::check_flat(update, update_dtype, "update", "dpg_orthogonalize");
     if (st == DPG_OK) st = dpg::check_flat(ortho_bf16, DPG_BF16, "ortho_bf16", "dpg_orthogonalize");
     if (st == DPG_OK) st = dpg::upload_matrices(mats->m);
     if (st != DPG_OK) return st;
-    return dpg::ortho_launch(mats->m, update, update_dtype, hp, ortho_bf16, stream, "dpg_orthogonalize");
+    return dpg::ortho_launch(mats->m, update, update_dtype, hp, sch, ortho_bf16, stream, "dpg_orthogonalize");
 }
 
 int dpg_muon_apply(dpg_matrices_t* mats, const void* ortho_bf16, const dpg_muon_hparams* hp,
@@ -274,8 +274,8 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
     dpg::Matrices& m = mats->m;
     if (m.total_padded != p.total_padded || m.param_offset != p.param_offset || m.numels != p.numels)
         return fail(DPG_ERR_INVALID_ARG, "%s: mats were made from another plan", who);
-    dpg::OrthoStep steps[DPG_MAX_NS_STEPS];
-    int st = dpg::ortho_steps(hp, steps, who);
+    dpg::OrthoSchedule sch;
+    int st = dpg::ortho_steps(hp, &sch, who);
     if (st != DPG_OK) return st;
     dpg::MomentumArgs a{};
     int grid = 0;
@@ -289,7 +289,7 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
     if (st != DPG_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = dpg::launch_momentum(a, grid, grads_dtype, last_micro_bf16 != nullptr, s, who);
-    if (st == DPG_OK) st = dpg::ortho_launch(m, update, update_dtype, hp, update, stream, who);
+    if (st == DPG_OK) st = dpg::ortho_launch(m, update, update_dtype, hp, sch, update, stream, who);
     if (st == DPG_OK) st = dpg::launch_apply(m, b, s, who);
     return st;
 }

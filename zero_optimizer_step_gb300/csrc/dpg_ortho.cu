@@ -1410,15 +1410,15 @@ void release_matrices(Matrices& m) {
 }
 
 int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
-                 void* out, void* stream, const char* who) {
+                 const OrthoSchedule& sch, void* out, void* stream, const char* who) {
     OrthoArgs a{};
-    int st = ortho_steps(hp, a.st, who);
+    std::memcpy(a.st, sch.st, sizeof a.st);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Everything that reads `update` comes before anything that writes `out`,
     // which may share its memory.
-    if (st == DPG_OK) st = gram_read(m, update, update_dtype, hp, out, s, who);
+    int st = gram_read(m, update, update_dtype, hp, out, s, who);
     if (st != DPG_OK) return st;
-    if (m.mats.empty()) return gram_finish(m, update, hp, out, s, who);
+    if (m.mats.empty()) return gram_finish(m, update, hp, sch, out, s, who);
     a.mats = m.d_mats;
     a.ws = m.ws;
     a.diag_a = reinterpret_cast<float*>(m.ws + m.o_diag);
@@ -1450,7 +1450,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     if (st == DPG_OK)
         st = launch_k(a.f32 ? k_ortho_load<true> : k_ortho_load<false>, unsigned(m.conv_items.size()), 256,
                       a.f32 ? 2 * kLoadSmem : kLoadSmem, s, who, a, static_cast<const ConvItem*>(m.d_conv_items));
-    if (st == DPG_OK) st = gram_finish(m, update, hp, out, s, who);
+    if (st == DPG_OK) st = gram_finish(m, update, hp, sch, out, s, who);
     if (st != DPG_OK) return st;
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);

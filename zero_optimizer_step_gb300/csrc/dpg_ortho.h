@@ -103,6 +103,13 @@ struct OrthoStep {
     float sb, inv_sb;  // scale of bA + cA^2
 };
 
+// The steps of a call, and where the Gram path sums its matrices anew.
+struct OrthoSchedule {
+    OrthoStep st[DPG_MAX_NS_STEPS];
+    int32_t n_phases;                      // of the Gram path (see gram_phases)
+    int32_t phase_end[DPG_MAX_NS_STEPS];   // the step after each
+};
+
 struct Matrices {
     int64_t total_padded = 0;
     int32_t n_params = 0;
@@ -152,18 +159,18 @@ int upload_matrices(Matrices& m);
 int upload_for_update(Matrices& m);   // only what dpg_muon_apply needs
 void release_matrices(Matrices& m);
 int check_matrices(Matrices& m, void* stream);
-// validates hp for the orthogonalisation and fills steps[0 .. hp->n_steps)
-int ortho_steps(const dpg_muon_hparams* hp, OrthoStep* steps, const char* who);
+// validates hp for the orthogonalisation and fills the schedule
+int ortho_steps(const dpg_muon_hparams* hp, OrthoSchedule* sch, const char* who);
 int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
-                 void* out, void* stream, const char* who);
+                 const OrthoSchedule& sch, void* out, void* stream, const char* who);
 
 // The small matrices' part (dpg_gram.cu): gram_read is the only one that reads
 // `update`, gram_finish the only one that writes `out`.
 int gram_prepare();
 int gram_read(const Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
               void* out, cudaStream_t s, const char* who);
-int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, void* out, cudaStream_t s,
-                const char* who);
+int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, const OrthoSchedule& sch,
+                void* out, cudaStream_t s, const char* who);
 
 }  // namespace dpg
 
