@@ -538,9 +538,17 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * the start of `update`'s memory when that is fp32).  Padding slots are
  * neither read nor written.
  * Arithmetic, shorter side above 128: X is held as a pair of fp16 numbers
- * under a power-of-two scale (22 bits), the off-diagonal parts of A and bA + cA^2 in one fp16 number,
- * their diagonals and every sum in fp32.  The result is within about 1e-3
- * (relative Frobenius norm) of the exact one, also for matrices of low rank.
+ * under a power-of-two scale (22 bits), the off-diagonal parts of A and bA + cA^2
+ * in one fp16 number, their diagonals and every sum in fp32.  While the a_k
+ * (those above 1) multiply to at most 490, as five default ones do, the result is
+ * within about 1e-3 (relative Frobenius norm) of the exact one, 3e-3 for
+ * matrices of half rank or with repeated rows.  What the roundings leave in
+ * directions that U lacks grows by a_k in every step, so in schedules that
+ * multiply to more, all steps but the last few hold those parts as pairs too:
+ * within 1.5e-3, and what 2^-21 of U's norm in U would change (the product of
+ * the a_k times as much in those directions, as in any binary32 iteration).
+ * Such steps take two to three times as long, and the first call that has them
+ * allocates up to 4/5 of workspace_bytes more (make it before a capture).
  * Shorter side up to 128: either this, or the same steps on the Gram matrix
  * (A_k+1 = Q_k A_k Q_k, Q_k = aI + b A_k + c A_k^2, X = Q_n-1 .. Q_0 U / norm)
  * in fp32, whichever is faster for the matrices of the object; the choice

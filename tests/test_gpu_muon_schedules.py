@@ -68,11 +68,27 @@ def test_long_schedules_short_side(rows, cols, name):
     _check([(rows, cols, len(KINDS))], KINDS, name, torch.float32, LONG_REL, tiles=False)
 
 
+@pytest.mark.parametrize("name", LONG)
+@pytest.mark.parametrize("rows,cols", [(150, 260), (260, 150), (256, 512), (520, 300)])
+def test_long_schedules_tiles(rows, cols, name):
+    _check([(rows, cols, len(KINDS))], KINDS, name, torch.bfloat16, LONG_REL, tiles=True)
+    _check([(rows, cols, len(KINDS))], KINDS, name, torch.float32, LONG_REL, tiles=True)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("shapes,tiles", [([(100, 200, 8)], False), ([(200, 100, 8)], False), ([(31, 90, 8)], False),
                                           ([(256, 512, 8)], True), ([(700, 300, 8)], True)])
 def test_five_steps_on_dependent_rows(shapes, tiles, dtype):
     _check(shapes, KINDS, "5", dtype, STEPS_REL, tiles)
+
+
+@pytest.mark.parametrize("name", ["8", "minimax8"])
+def test_long_schedules_long_matrices(name):
+    # sums in parts, tiles of several widths, many columns
+    _check([(200, 9000, 2)], ["spiked", "repeated"], name, torch.bfloat16, LONG_REL, tiles=True)
+    _check([(5000, 300, 1), (700, 900, 2)], ["gauss", "rank4", "half"], name, torch.float32, LONG_REL, tiles=True)
+    _check([(128, 6000, 2), (3000, 64, 2)], ["rank4", "repeated", "spiked"], name, torch.bfloat16, LONG_REL,
+           tiles=False)
 
 
 def test_long_schedules_are_deterministic_and_leave_no_trace():

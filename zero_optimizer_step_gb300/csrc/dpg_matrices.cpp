@@ -160,6 +160,9 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.a = d.lo + xb;
             d.b = d.a + ab;
             M.n_blocks = d.b + ab;
+            d.lo2 = M.n_low_blocks;
+            d.blo = d.lo2 + xb;
+            M.n_low_blocks = d.blo + ab;   // (fewer than n_blocks)
             // a block's first 128-byte row is a 32-bit coordinate of the copies
             if (M.n_blocks * kBlkRows > 0x7FFFFFFFll) return false;
             d.diag = M.n_diag;
@@ -420,6 +423,34 @@ static void gram_phases(const double* growth, int n_steps, OrthoSchedule* sch) {
     sch->phase_end[sch->n_phases++] = n_steps;
 }
 
+// Which steps of the tiles take both halves of their operands.  In directions
+// that X lacks, what a step's roundings leave there is multiplied by the a_k of
+// the steps after it.  With fp16 halves alone (3e-4 a step) five default steps
+// end within 2.7e-3 whatever the matrix, six at 6e-3 and eight at 7e-2 (every
+// row twice, or rank m / 2).  Where the a_k multiply to more than those five
+// (485), the steps with more than 4 still to come -- all but the last two of
+// default ones -- take both: the end is within 1.3e-3 again.  Such a step takes
+// two to three times as long (eight GPT-2-small attention matrices 88 us
+// against 41, a 1B model's layer 1.1 ms against 0.34).
+static void both_halves(const dpg_muon_hparams* hp, OrthoSchedule* sch) {
+    double all = 1.0, to_come = 1.0;
+    for (int k = 0; k < hp->n_steps; ++k) all *= std::max(1.0, std::fabs(hp->coeffs[k][0]));
+    sch->both_steps = 0;
+    for (int k = hp->n_steps - 1; k >= 0 && all > 490.0; --k) {
+        if (to_come > 4.0) {
+            sch->both_steps = k + 1;
+            break;
+        }
+        to_come *= std::max(1.0, std::fabs(hp->coeffs[k][0]));
+    }
+    // The low half is kept times 2048 where only the steps' own sums read it,
+    // and as it is where products read it beside the high half.
+    for (int k = 0; k < hp->n_steps; ++k) {
+        sch->st[k].inv_lo = k < sch->both_steps ? 1.0f : 1.0f / kLoScale;
+        sch->st[k].lo_next = k + 1 < sch->both_steps ? 1.0f : kLoScale;
+    }
+}
+
 int ortho_steps(const dpg_muon_hparams* hp, OrthoSchedule* sch, const char* who) {
     if (!hp) return fail(DPG_ERR_INVALID_ARG, "%s: hparams is NULL", who);
     if (hp->n_steps < 1 || hp->n_steps > DPG_MAX_NS_STEPS)
@@ -453,6 +484,7 @@ int ortho_steps(const dpg_muon_hparams* hp, OrthoSchedule* sch, const char* who)
         s.sx_next = sx = scale_for(top);
     }
     gram_phases(growth, hp->n_steps, sch);
+    both_halves(hp, sch);
     return DPG_OK;
 }
 
@@ -519,7 +551,7 @@ int dpg_matrices_status(dpg_matrices_t* mats, void* stream) {
 int dpg_matrices_upload(dpg_matrices_t* mats) {
     dpg::clear_error();
     if (!mats) return fail(DPG_ERR_INVALID_ARG, "dpg_matrices_upload: mats is NULL");
-    return dpg::upload_matrices(mats->m);
+    return dpg::upload_matrices(mats->m, false);
 }
 
 }  // extern "C"

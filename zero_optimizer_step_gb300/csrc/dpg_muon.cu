@@ -243,7 +243,7 @@ int dpg_orthogonalize(dpg_matrices_t* mats, const void* update, int32_t update_d
     if (mats->m.n_matrices == 0) return DPG_OK;
     st = dpg::check_flat(update, update_dtype, "update", "dpg_orthogonalize");
     if (st == DPG_OK) st = dpg::check_flat(ortho_bf16, DPG_BF16, "ortho_bf16", "dpg_orthogonalize");
-    if (st == DPG_OK) st = dpg::upload_matrices(mats->m);
+    if (st == DPG_OK) st = dpg::upload_matrices(mats->m, sch.both_steps > 0);
     if (st != DPG_OK) return st;
     return dpg::ortho_launch(mats->m, update, update_dtype, hp, sch, ortho_bf16, stream, "dpg_orthogonalize");
 }
@@ -285,7 +285,7 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
     dpg::ApplyArgs b{};
     st = dpg::apply_args(m, update, hp, master, param_views, n_views, b, who);
     if (st != DPG_OK || m.n_matrices == 0) return st;
-    st = dpg::upload_matrices(m);
+    st = dpg::upload_matrices(m, sch.both_steps > 0);
     if (st != DPG_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = dpg::launch_momentum(a, grid, grads_dtype, last_micro_bf16 != nullptr, s, who);

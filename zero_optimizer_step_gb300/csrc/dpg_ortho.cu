@@ -15,7 +15,7 @@
 // multiplied by a (3.4) in every step.  Here
 //   * X is a pair hi + lo / 2048 of fp16 numbers (22 bits).  The products use
 //     hi; the term a X, the one that carries the amplified directions, uses
-//     both, so no rounding of X is amplified.
+//     both, so the rounding of X itself is not amplified.
 //   * the diagonals of A and B, which are large where the matrices are close
 //     to multiples of the identity, are kept in fp32 apart from the fp16
 //     off-diagonal parts F: with A = D + F,
@@ -35,9 +35,16 @@
 //   * every stored fp16 matrix carries a power-of-two scale that the host
 //     derives from the largest value the step can produce, so nothing
 //     overflows and small entries stay normal numbers.
-// Together 3e-4 to 1.3e-3 of relative Frobenius error over Gaussian, spiked,
-// constant and low-rank matrices, below the rounding of the bf16 result itself
-// (1.7e-3).
+// Together 3e-4 to 1.3e-3 of relative Frobenius error after five default steps
+// over Gaussian, spiked, constant and low-rank matrices, below the rounding of
+// the bf16 result itself (1.7e-3); 1.9e-3 for rank m / 2 and 2.7e-3 where every
+// row stands twice, whose diagonals in fp32 and off-diagonal parts in fp16 do
+// not cancel exactly.
+//
+// What they leave grows with the a of every step to come.  In the early steps
+// of schedules that multiply it by more (both_halves), A and B are pairs of
+// fp16 numbers too and the products take hi hi + lo hi + hi lo, as three sums
+// in one accumulator; t is 1.  That is 1e-6 a step, the roundings of fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,12 +61,14 @@
 
 namespace dpg {
 
-constexpr float kLoScale = 2048.0f;
-constexpr float kInvLoScale = 1.0f / 2048.0f;
+constexpr float kInvLoScale = 1.0f / kLoScale;
 
 struct OrthoArgs {
     const MatDesc* mats;
     unsigned char* ws;       // blocks
+    unsigned char* ws_low;   // blocks of the second workspace
+    int32_t both_steps;      // the first so many steps take both halves
+    float lo_scale, inv_lo_scale;   // of X_0's low half
     float* diag_a;           // per row: A_rr
     float* diag_b;           // B_rr
     float* diag_t;           // t_r B_rr
@@ -296,10 +305,10 @@ __global__ void __launch_bounds__(kNormThreads) k_ortho_norm(const __grid_consta
 constexpr int kLoadPitch = 136;   // fp16 values of a transposed row: 16-byte rows, banks 4 words apart
 constexpr int kLoadSmem = kBlkRows * kLoadPitch * 2;
 
-__device__ __forceinline__ void split16(float u, float rounded, uint16_t& hi, uint16_t& lo) {
+__device__ __forceinline__ void split16(float u, float rounded, float scale, uint16_t& hi, uint16_t& lo) {
     const __half h = __float2half_rn(rounded);
     hi = __half_as_ushort(h);
-    lo = __half_as_ushort(__float2half_rn((u - __half2float(h)) * kLoScale));
+    lo = __half_as_ushort(__float2half_rn((u - __half2float(h)) * scale));
 }
 
 template <bool F32, bool TALL>
@@ -339,7 +348,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 for (int j = 0; j < 8; ++j) {
                     const float u = in ? x[j] * sc : 0.0f;
                     uint16_t h, l;
-                    split16(u, F32 ? u * RoundScale(1.0f, r + j + c).v[0] : u, h, l);
+                    split16(u, F32 ? u * RoundScale(1.0f, r + j + c).v[0] : u, a.lo_scale, h, l);
                     sm[(r + j) * kLoadPitch + c] = h;
                     if (F32) sm_lo[(r + j) * kLoadPitch + c] = l;
                 }
@@ -350,7 +359,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 const float u = c0 + c < n && r0 + r < m
                                     ? load_update<F32>(a, off + int64_t(c0 + c) * m + r0 + r) * sc : 0.0f;
                 uint16_t h, l;
-                split16(u, F32 ? u * RoundScale(1.0f, r + c).v[0] : u, h, l);
+                split16(u, F32 ? u * RoundScale(1.0f, r + c).v[0] : u, a.lo_scale, h, l);
                 sm[r * kLoadPitch + c] = h;
                 if (F32) sm_lo[r * kLoadPitch + c] = l;
             }
@@ -381,7 +390,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 f = unpack_half2(h[j]), g = unpack_half2(l[j]);
-                const float u = fmaf(g.x, kInvLoScale, f.x), v = fmaf(g.y, kInvLoScale, f.y);
+                const float u = fmaf(g.x, a.inv_lo_scale, f.x), v = fmaf(g.y, a.inv_lo_scale, f.y);
                 sq = fmaf(u, u, fmaf(v, v, sq));
             }
         } else {
@@ -399,7 +408,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 // a scaled bf16 value is an fp16 value: nothing to round, lo is 0
                 h[j] = F32 ? pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]) : pack_half2(u, v);
                 const float2 f = unpack_half2(h[j]);
-                l[j] = pack_half2((u - f.x) * kLoScale, (v - f.y) * kLoScale);
+                l[j] = pack_half2((u - f.x) * a.lo_scale, (v - f.y) * a.lo_scale);
             }
             h4 = make_uint4(h[0], h[1], h[2], h[3]);
             l4 = make_uint4(l[0], l[1], l[2], l[3]);
@@ -774,10 +783,69 @@ __device__ __forceinline__ void finish_b(const OrthoArgs& a, const OrthoStep& s,
     put_sym(slot, row, h, x, mirror);
 }
 
-// ah, al: factors of hi and lo; k: of the sums.  Returns the sum of squares of
-// the new X.  The last step leaves bf16 values in the slot instead.
+// What a step that takes both halves does with a tile of A or B.  The values
+// as they are to be stored, in fp32 in place of the sums:
+__device__ __forceinline__ void values_a(const OrthoArgs& a, const OrthoStep& s, int64_t diag_at, float inv_sx, int row,
+                                         int r, int c0, float* acc, float diag) {
+    const float k = inv_sx * inv_sx;
+    const int lane = row & 31;
+    const bool on = r - lane == c0;
+    if (on) a.diag_a[diag_at + r] = diag * k;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = on && j == lane ? 0.0f : acc[j] * (s.sa * k);
+}
+// (as finish_b, with F the sum of both halves, in the slot one behind the other)
+__device__ __forceinline__ void values_b(const OrthoArgs& a, const OrthoStep& s, int64_t diag_at, uint32_t slot,
+                                         int row, int h, int r, int c0, float* acc, float dr, const float* cols) {
+    const float k = s.c * s.inv_sa * s.inv_sa, fb = fmaf(s.c, dr, s.b) * s.inv_sa, fc = s.c * s.inv_sa;
+    const int lane = row & 31;
+    const bool on = r - lane == c0;
+    if (on) {
+        float ff = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) ff = j == lane ? acc[j] : ff;
+        const float db = fmaf(fmaf(s.c, dr, s.b), dr, k * ff);
+        a.diag_b[diag_at + r] = db;
+        a.diag_t[diag_at + r] = db;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t at = slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4);
+        const uint4 f4 = lds128(at), l4 = lds128(at + uint32_t(kBlkBytes));
+        const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 u = unpack_half2(f[j]), v = unpack_half2(l[j]);
+            const int e = 8 * q + 2 * j;
+            acc[e] = fmaf(k, acc[e], fmaf(fc, cols[e], fb) * (u.x + v.x)) * s.sb;
+            acc[e + 1] = fmaf(k, acc[e + 1], fmaf(fc, cols[e + 1], fb) * (u.y + v.y)) * s.sb;
+        }
+    }
+    if (on)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[j] = j == lane ? 0.0f : acc[j];
+}
+// one half of 32 values into the slot
+__device__ __forceinline__ void put_half(uint32_t slot, int row, int h, int r, const float* v, bool mirror, bool low) {
+    const RoundScale rs(1.0f, r);
+    uint32_t x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        x[j] = pack_half2(v[2 * j] * rs.v[2 * j & 3], v[2 * j + 1] * rs.v[(2 * j + 1) & 3]);
+        if (low) {
+            const float2 f = unpack_half2(x[j]);
+            x[j] = pack_half2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+        }
+    }
+    put_sym(slot, row, h, x, mirror);
+}
+
+// ah, al: factors of hi and lo; k: of the sums; lo_scale: of the new lo.
+// Returns the sum of squares of the new X.  The last step leaves bf16 values in
+// the slot instead.
 __device__ __forceinline__ float finish_x(const OrthoStep& s, uint32_t slot, int row, int h, int r,
-                                          const float* acc, float ah, float al, float k, bool has_lo, bool last) {
+                                          const float* acc, float ah, float al, float k, float lo_scale, bool has_lo,
+                                          bool last) {
     uint4 h4[4], l4[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) h4[q] = lds128(slot + row * 128 + (((4 * h + q) ^ (row & 7)) << 4));
@@ -788,8 +856,8 @@ __device__ __forceinline__ float finish_x(const OrthoStep& s, uint32_t slot, int
     const RoundScale rs(s.sx_next, r);
     const uint64_t r0 = rs.pair(0), r1 = rs.pair(1);
     const uint64_t k2 = pair_of(k, k), ah2 = pair_of(ah, ah), al2 = pair_of(al, al);
-    const float up = s.sx_next * kLoScale;
-    const uint64_t up2 = pair_of(up, up), down2 = pair_of(-kLoScale, -kLoScale);
+    const float up = s.sx_next * lo_scale;
+    const uint64_t up2 = pair_of(up, up), down2 = pair_of(-lo_scale, -lo_scale);
     uint64_t sq = 0;   // two zeros
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -806,7 +874,7 @@ __device__ __forceinline__ float finish_x(const OrthoStep& s, uint32_t slot, int
             } else {
                 sq = fma2(x, x, sq);
                 nh[j] = pack_pair(mul2(x, (j & 1) ? r1 : r0));
-                // 2048 (x sx - hi), exactly as from the separate products
+                // lo_scale (x sx - hi), exactly as from the separate products
                 nl[j] = pack_pair(fma2(unpack_pair(nh[j]), down2, mul2(x, up2)));
             }
         }
@@ -859,12 +927,30 @@ __device__ __forceinline__ void write_out(const OrthoArgs& a, const MatDesc& d, 
     }
 }
 
+// X's low part as step `step` reads it (and step - 1 writes it): in place, or
+// from buffer to buffer through the steps that take both halves.
+template <bool BOTH>
+__device__ __forceinline__ unsigned char* low_half(const OrthoArgs& a, const MatDesc& d, int step) {
+    return BOTH && (min(step, a.both_steps) & 1) ? a.ws_low + d.lo2 * kBlkBytes : a.ws + d.lo * kBlkBytes;
+}
+
 // The count that must have been reached before a tile of (prod, step) starts.
 __device__ __forceinline__ bool wait_operands(OrthoShared& sh, const OrthoArgs& a, const MatDesc& d, int mat,
                                               int prod, int step) {
     const int before = prod == kProdA ? kProdX : prod - 1;
     const int target = (prod == kProdA ? step : step + 1) * 2 * d.tiles[before];
     return wait_count(sh, a.done + 3 * mat + before, target, a);
+}
+
+// How many sums a product is: hi hi, lo hi, hi lo.  X_0 of a bf16 update has no lo.
+__device__ __forceinline__ int sums_of(int prod, bool both, bool has_lo) {
+    return !both ? 1 : prod == kProdB || has_lo ? 3 : prod == kProdX ? 2 : 1;
+}
+// How often a 64-column block of a tile goes through a slot.  With both halves,
+// a block of A leaves as hi and as lo, one of B comes in (both halves of A's)
+// before it does: their mirror images need the room of the second half.
+__device__ __forceinline__ int visits_of(int prod, bool both) {
+    return !both || prod == kProdX ? 1 : prod == kProdA ? 2 : 3;
 }
 
 // First 64-deep block and number of blocks of a part of a tile's sum.
@@ -933,9 +1019,15 @@ __device__ __noinline__ bool join_parts(OrthoShared& sh, const OrthoArgs& a, con
     return true;
 }
 
+// BOTH: some steps take both halves of their operands (their code beside the
+// other made that slower).  X's low part is then an operand that other tiles
+// read, so it alternates between two buffers as X does; the free one holds A's
+// low part while that is needed.
+template <bool BOTH>
 __global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
 k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
-              const __grid_constant__ CUtensorMap rows64) {
+              const __grid_constant__ CUtensorMap rows64, const __grid_constant__ CUtensorMap low128,
+              const __grid_constant__ CUtensorMap low64) {
     // the kernel's only shared memory: starts on a multiple of 1 KB, as the swizzle wants it
     extern __shared__ __align__(1024) unsigned char dyn[];
     OrthoShared& sh = *reinterpret_cast<OrthoShared*>(dyn + kStages * kStageBytes + kSlots * kSlotBytes);
@@ -983,6 +1075,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t par = 1;             // the first pass over the ring finds it empty
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
+            const bool both = BOTH && step < a.both_steps, has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
@@ -992,24 +1085,43 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int cb = prod == kProdA ? d.cbx : d.cba, kblocks = part_of_sum(d, tile, tile.part).y;
                 const int half = tile.blocks * 32, c0 = tile.j * tile.blocks * 64 + int(rank) * half;
                 const int k0 = part_of_sum(d, tile, tile.part).x * kBlkRows;
-                const int left = int((from + int64_t(tile.i * 2 + int(rank)) * cb) * kBlkRows) + k0;
-                const int right = prod == kProdX ? int((x + (c0 >> 6)) * kBlkRows)
-                                                 : int((from + int64_t(c0 >> 7) * cb) * kBlkRows) + (c0 & 127) + k0;
+                int left = int((from + int64_t(tile.i * 2 + int(rank)) * cb) * kBlkRows) + k0;
+                int right = prod == kProdX ? int((x + (c0 >> 6)) * kBlkRows)
+                                           : int((from + int64_t(c0 >> 7) * cb) * kBlkRows) + (c0 & 127) + k0;
                 const uint32_t bytes = 2 * (kHalfBytes + uint32_t(half) * 128);
                 const int pitch = d.cbx * kBlkRows;
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
-                for (int kb = 0; kb < kblocks; ++kb) {
+                const CUtensorMap *left_map = &rows128, *right128 = &rows128, *right64 = &rows64;
+                const int left_hi = left, right_hi = right, sums = sums_of(prod, both, has_lo);
+                for (int k = 0, kb = 0, sum = 0; k < kblocks * sums; ++k, ++kb) {
+                    if (BOTH && kb == kblocks) {   // the next sum
+                        kb = 0;
+                        // from the blocks of the high half to those of the low one: X's (or, where
+                        // A is the operand, A's) in the first or the second workspace, or B's
+                        const bool second = ((prod == kProdB ? step + 1 : step) & 1) != 0;
+                        const int64_t low = second ? d.lo2 : d.lo;
+                        if (++sum == 1) {
+                            left = left_hi + int(((prod == kProdX ? d.blo : low) - from) * kBlkRows);
+                            left_map = prod == kProdX || second ? &low128 : &rows128;
+                        } else {
+                            left = left_hi;
+                            left_map = &rows128;
+                            right = right_hi + int((low - (prod == kProdX ? x : from)) * kBlkRows);
+                            right128 = second ? &low128 : &rows128;
+                            right64 = second ? &low64 : &rows64;
+                        }
+                    }
                     if (!(ok = wait_bounded(sh, &sh.empty[s], par, a))) break;
                     const uint32_t bar = full0 + uint32_t(s) * 8;
                     if (rank == 0) mbar_expect(&sh.full[s], bytes);
                     const uint32_t dst = stage0 + uint32_t(s) * kStageBytes;
-                    if (skip-- != 0) copy_box(dst, &rows128, left + kb * kBlkRows, bar);
+                    if (skip-- != 0) copy_box(dst, left_map, left + kb * kBlkRows, bar);
                     if (prod == kProdX) {
                         const int row = right + (kb >> 1) * pitch + (kb & 1) * 64;
-                        copy_box(dst + kHalfBytes, &rows64, row, bar);
-                        if (half == 128) copy_box(dst + kHalfBytes + 8192, &rows64, row + kBlkRows, bar);
+                        copy_box(dst + kHalfBytes, right64, row, bar);
+                        if (half == 128) copy_box(dst + kHalfBytes + 8192, right64, row + kBlkRows, bar);
                     } else {
-                        copy_box(dst + kHalfBytes, half == 128 ? &rows128 : &rows64, right + kb * kBlkRows, bar);
+                        copy_box(dst + kHalfBytes, half == 128 ? right128 : right64, right + kb * kBlkRows, bar);
                     }
                     if (++s == kStages) {
                         s = 0;
@@ -1024,12 +1136,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t par = 0;
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
+            const bool both = BOTH && step < a.both_steps, has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const bool by_column = tile.prod == kProdX;
                 const uint32_t shape = mma_shape(by_column, tile.blocks * 64);
-                const int kblocks = part_of_sum(d, tile, tile.part).y;
+                const int kblocks = part_of_sum(d, tile, tile.part).y * sums_of(tile.prod, both, has_lo);
                 const int buf = it & 1;
                 if (!(ok = wait_bounded(sh, &sh.tempty[buf], uint32_t((it >> 1) & 1) ^ 1u, a))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -1057,17 +1170,19 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         int before = 2;               // blocks of the tile before
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool has_lo = step > 0 || a.f32;
+            const bool has_lo = step > 0 || a.f32, both = BOTH && step < a.both_steps;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod, blocks = tile.blocks >> tile.split;   // (parts: of A, which reads no blocks)
                 const int64_t blk = int64_t(tile.i * 2 + int(rank)) * (prod == kProdX ? d.cbx : d.cba) + tile.j * blocks;
                 const unsigned char* in = a.ws + ((prod == kProdB ? d.a : d.x[step & 1]) + blk) * kBlkBytes;
-                const unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
-                const bool two = prod == kProdX && has_lo;
+                // (of X, or A's in the buffer that X's goes to next)
+                const unsigned char* lo = low_half<BOTH>(a, d, prod == kProdB ? step + 1 : step) + blk * kBlkBytes;
+                const bool two = prod == kProdX ? has_lo : both;
+                const int visits = visits_of(prod, both);
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
-                for (int g = 0; g < blocks; ++g, ++n) {
+                for (int g = 0, v = 0; g < blocks; g += ++v == visits, v = v == visits ? 0 : v, ++n) {
                     const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
                     if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a))) break;
                     // Tells the finishing warps, which so need not watch the counter in memory
@@ -1075,13 +1190,13 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     // microsecond).  They have all seen it for the tile before, or they could
                     // miss a phase: a block of that tile is finished, the one in this slot or,
                     // if it had one only, the one in the other slot.
-                    if (g == 0) {
+                    if (g == 0 && v == 0) {
                         if (before == 1 &&
                             !(ok = wait_bounded(sh, &sh.slot_free[sl ^ 1], ((n - 1) >> 1) & 1, a)))
                             break;
                         mbar_arrive(&sh.tile_ready);
                     }
-                    if (prod == kProdA) {
+                    if (prod == kProdA || v > 0) {
                         mbar_arrive(&sh.in_full[sl]);
                         continue;
                     }
@@ -1089,7 +1204,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
                     if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
                 }
-                before = blocks;
+                before = blocks * visits;
             }
         }
     } else if (warp == kStoreWarp && lane == 0) {
@@ -1097,11 +1212,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t n = 0;               // as above
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool last = step + 1 == a.n_steps;
+            const bool last = step + 1 == a.n_steps, both = BOTH && step < a.both_steps;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
-                const int prod = tile.prod, blocks = tile.blocks >> tile.split;
+                const int prod = tile.prod, blocks = tile.blocks >> tile.split, visits = visits_of(prod, both);
                 const int c0 = tile.j * tile.blocks + tile.part * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
                 const int cb = prod == kProdX ? d.cbx : d.cba;
@@ -1109,16 +1224,27 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int64_t blk = int64_t(tile.i * 2 + int(rank)) * cb + c0;
                 unsigned char* out = a.ws + ((prod == kProdA ? d.a : prod == kProdB ? d.b : d.x[(step + 1) & 1]) +
                                              blk) * kBlkBytes;
-                unsigned char* lo = a.ws + (d.lo + blk) * kBlkBytes;
-                unsigned char* image = a.ws + ((prod == kProdA ? d.a : d.b) + tile.i * 4 + int(rank) * 2) * kBlkBytes;
+                // where the low half goes: X's, or A's beside it, or B's
+                unsigned char* low = BOTH && both && prod == kProdB ? a.ws_low + d.blo * kBlkBytes
+                                                                    : low_half<BOTH>(a, d, step + 1);
+                unsigned char* lo = low + blk * kBlkBytes;
+                const int64_t image_at = int64_t(tile.i * 4 + int(rank) * 2) * kBlkBytes;
+                unsigned char* image = a.ws + (prod == kProdA ? d.a : d.b) * kBlkBytes + image_at;
                 int32_t* done = a.done + 3 * tile.mat + prod;
-                for (int g = 0; g < blocks; ++g, ++n) {
+                for (int g = 0, v = 0; g < blocks; g += ++v == visits, v = v == visits ? 0 : v, ++n) {
                     const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
                     if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (n >> 1) & 1, a))) break;
                     if (prod != kProdX) {
-                        copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
+                        // with both halves the last two of a block's visits leave hi and lo
+                        const bool is_low = both && v + 1 == visits;
+                        if (both && v + 2 < visits) {
+                            mbar_arrive(&sh.slot_free[sl]);
+                            continue;
+                        }
+                        copy_out((is_low ? lo : out) + g * kBlkBytes, at, uint32_t(kBlkBytes));
                         if (mirror) {     // 64 rows from this block's first column, 2 x 64 columns
-                            unsigned char* m = image + int64_t((c0 + g) >> 1) * cb * kBlkBytes + ((c0 + g) & 1) * 8192;
+                            unsigned char* m = (is_low ? low + image_at : image) +
+                                               int64_t((c0 + g) >> 1) * cb * kBlkBytes + ((c0 + g) & 1) * 8192;
                             copy_out(m, at + uint32_t(kBlkBytes), 8192);
                             copy_out(m + kBlkBytes, at + uint32_t(kBlkBytes) + 8192, 8192);
                         }
@@ -1149,8 +1275,9 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             const OrthoStep s = a.st[step];
-            const bool last = step + 1 == a.n_steps;
+            const bool last = step + 1 == a.n_steps, both = BOTH && step < a.both_steps;
             const bool has_lo = step > 0 || a.f32;
+            const float inv_lo = BOTH ? s.inv_lo : kInvLoScale, lo_next = BOTH ? s.lo_next : kLoScale;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
@@ -1175,7 +1302,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                         if (g < blocks) dc[g] = __ldcg(a.diag_a + d.diag + c0 + g * 64 + half * 32 + lane);
                 } else {
                     p0 = fmaf(__ldcg(a.diag_b + d.diag + r), inv_sx, s.a * inv_sx);
-                    p1 = fmaf(__ldcg(a.diag_t + d.diag + r), inv_sx, s.a * inv_sx) * kInvLoScale;
+                    p1 = fmaf(__ldcg(a.diag_t + d.diag + r), inv_sx, s.a * inv_sx) * inv_lo;
                 }
                 ok = wait_bounded(sh, &sh.tfull[buf], uint32_t((it >> 1) & 1), a);
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
@@ -1200,6 +1327,33 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                     }
                     ok = wait_bounded(sh, &sh.in_full[sl], (n >> 1) & 1, a);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                    if (BOTH && both && prod != kProdX) {
+                        const int visits = visits_of(prod, both);
+                        if (prod == kProdA) {
+                            values_a(a, s, diag_at, inv_sx, row, r, c, acc, p0);
+                        } else {
+                            __syncwarp();
+                            cols[lane] = g == 0 ? dc[0] : g == 1 ? dc[1] : g == 2 ? dc[2] : dc[3];
+                            __syncwarp();
+                            values_b(a, s, diag_at, slot, row, half, r, c, acc, p0, cols);
+                        }
+#pragma unroll 1
+                        for (int v = 0; v < visits; ++v) {
+                            const uint32_t sv = n & 1;
+                            if (v > 0) {
+                                ok = wait_bounded(sh, &sh.in_full[sv], (n >> 1) & 1, a);
+                                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                            }
+                            if (v + 2 >= visits)
+                                put_half(slot0 + sv * kSlotBytes, row, half, r, acc, mirror, v + 1 == visits);
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh.out_ready[sv]);
+                            if (v + 1 < visits) ++n;      // (the loop counts the last)
+                        }
+                        if (!ok) break;
+                        continue;
+                    }
                     if (prod == kProdA) {
                         finish_a(a, s, diag_at, inv_sx, slot, row, half, r, c, acc, mirror, p0);
                     } else if (prod == kProdB) {
@@ -1208,7 +1362,7 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                         __syncwarp();
                         finish_b(a, s, diag_at, slot, row, half, r, c, acc, mirror, p0, smem_u32(cols));
                     } else {
-                        sq += finish_x(s, slot, row, half, r, acc, p0, p1, inv_sx * s.inv_sb, has_lo, last);
+                        sq += finish_x(s, slot, row, half, r, acc, p0, p1, inv_sx * s.inv_sb, lo_next, has_lo, last);
                         if (last) {
                             write_out(a, d, slot, row0, half, r0, c);
                         } else if (g & 1) {   // of this warp's 32 columns in two blocks
@@ -1301,16 +1455,42 @@ int upload_for_update(Matrices& m) {
     return upload_update_tables(m);
 }
 
-int upload_matrices(Matrices& m) {
+// The second workspace, which only steps that take both halves need; m.mu is
+// held, the tables are there.
+static int upload_low(Matrices& m) {
+    if (m.ws_low || m.n_low_blocks == 0) return DPG_OK;
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
+    void* low = nullptr;
+    const cudaError_t e = cudaMalloc(&low, size_t(m.n_low_blocks * kBlkBytes));
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA, "matrices upload: %s",
+                    cudaGetErrorString(e));
+    }
+    for (int k = 0; k < 2; ++k) {
+        CUtensorMap map;
+        const int st = encode_map(&map, low, m.n_low_blocks * kBlkRows, k ? 64 : 128);
+        if (st != DPG_OK) {
+            cudaFree(low);
+            return st;
+        }
+        std::memcpy(m.maps[2 + k], &map, sizeof map);
+    }
+    m.ws_low = static_cast<unsigned char*>(low);
+    return DPG_OK;
+}
+
+int upload_matrices(Matrices& m, bool both) {
     std::lock_guard<std::mutex> g(m.mu);
     int st = upload_update_tables(m);
-    if (st != DPG_OK || m.ws) return st;
+    if (st != DPG_OK) return st;
+    if (m.ws) return both ? upload_low(m) : DPG_OK;
     // how many CTA pairs are resident at once decides the queues
     int clusters = 1;
     if (!m.mats.empty()) {
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_load<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           2 * kLoadSmem));
-        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kOrthoThreads);
@@ -1321,7 +1501,7 @@ int upload_matrices(Matrices& m) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps, &cfg));
+        DPG_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, k_ortho_steps<false>, &cfg));
         if (clusters < 1) return fail(DPG_ERR_CUDA, "matrices upload: no CTA pair fits this device");
     }
     if (!m.small.empty()) {
@@ -1378,7 +1558,7 @@ int upload_matrices(Matrices& m) {
     }
     m.d_tables = t;
     m.ws = static_cast<unsigned char*>(ws);
-    return DPG_OK;
+    return both ? upload_low(m) : DPG_OK;
 }
 
 int check_matrices(Matrices& m, void* stream) {
@@ -1402,6 +1582,7 @@ void release_matrices(Matrices& m) {
         cudaFree(m.d_update_tables);
         cudaFree(m.d_tables);
         cudaFree(m.ws);
+        cudaFree(m.ws_low);
     }
     if (have_cur) cudaSetDevice(cur);
     cudaGetLastError();
@@ -1439,6 +1620,10 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     t_staged_timeout_ns = 0;
     a.queue = m.d_queue;
     a.queue_first = m.d_queue_first;
+    a.ws_low = m.ws_low;
+    a.both_steps = sch.both_steps;
+    a.inv_lo_scale = sch.st[0].inv_lo;
+    a.lo_scale = 1.0f / a.inv_lo_scale;
     a.n_steps = hp->n_steps;
     a.eps = hp->eps;
     int exp = 0;
@@ -1452,8 +1637,9 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
                       a.f32 ? 2 * kLoadSmem : kLoadSmem, s, who, a, static_cast<const ConvItem*>(m.d_conv_items));
     if (st == DPG_OK) st = gram_finish(m, update, hp, sch, out, s, who);
     if (st != DPG_OK) return st;
-    CUtensorMap map[2];
-    std::memcpy(map, m.maps, sizeof map);
+    const bool both = sch.both_steps > 0;
+    CUtensorMap map[4] = {};
+    std::memcpy(map, m.maps, both ? sizeof map : 2 * sizeof map[0]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(2 * m.pairs));
     cfg.blockDim = dim3(kOrthoThreads);
@@ -1464,7 +1650,8 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_steps, a, map[0], map[1]);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, both ? k_ortho_steps<true> : k_ortho_steps<false>, a, map[0],
+                                             map[1], map[2], map[3]);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));

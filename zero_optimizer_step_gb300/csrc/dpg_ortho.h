@@ -36,6 +36,7 @@ struct MatDesc {
     int32_t cbx, cba;     // 64-column blocks in a row of X, of A
     int64_t x[2], lo;     // first block of the two X buffers and of X's low part
     int64_t a, b;         // first block of A and of bA + cA^2 (off-diagonal parts)
+    int64_t lo2, blo;     // in the second workspace: first block of X's other low part, of B's low part
     int64_t diag;         // first entry of the per-row vectors (see OrthoArgs)
     int64_t rowsq;        // first entry of X's row sums of squares, [cbx][padded rows]
     int32_t rows_pad;     // rows of X padded to 256
@@ -93,6 +94,8 @@ constexpr int kApplyChunk = 1024;
 // Products of a step, in order: A = X X^T, B = bA + cA^2, X' = aX + BX.
 enum : int { kProdA = 0, kProdB = 1, kProdX = 2 };
 
+constexpr float kLoScale = 2048.0f;   // of X's low half
+
 // Constants of one Newton-Schulz step.  Stored fp16 values are the true ones
 // times a power of two that keeps the largest the step can produce below 2^15.
 struct OrthoStep {
@@ -101,11 +104,14 @@ struct OrthoStep {
     float sx_next;     // scale of the new X
     float sa, inv_sa;  // scale of A
     float sb, inv_sb;  // scale of bA + cA^2
+    float inv_lo;      // 1 / what X's low part is multiplied by as it is read
+    float lo_next;     // and what as it is written
 };
 
 // The steps of a call, and where the Gram path sums its matrices anew.
 struct OrthoSchedule {
     OrthoStep st[DPG_MAX_NS_STEPS];
+    int32_t both_steps;                    // the first so many take both halves (see both_halves)
     int32_t n_phases;                      // of the Gram path (see gram_phases)
     int32_t phase_end[DPG_MAX_NS_STEPS];   // the step after each
 };
@@ -127,6 +133,7 @@ struct Matrices {
     std::vector<ConvItem> conv_items;
     std::vector<ApplyItem> apply_items;
     std::vector<double> scales;        // 2 per parameter: spectral, rms
+    int64_t n_low_blocks = 0;          // of the second workspace
     int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0, n_groups = 0;
     int64_t n_small_copy = 0, n_small_part = 0, n_small_prod = 0;   // floats
     int64_t workspace_bytes = 0;
@@ -137,6 +144,7 @@ struct Matrices {
     std::mutex mu;
     int device = -1;
     unsigned char* ws = nullptr;       // workspace_bytes
+    unsigned char* ws_low = nullptr;   // n_low_blocks blocks, from the first call that needs them on
     unsigned char* d_tables = nullptr; // one allocation, sections below
     unsigned char* d_update_tables = nullptr;   // apply_items and scales
     MatDesc* d_mats = nullptr;
@@ -149,13 +157,14 @@ struct Matrices {
     ConvItem* d_conv_items = nullptr;
     ApplyItem* d_apply_items = nullptr;
     double* d_scales = nullptr;
-    alignas(64) unsigned char maps[2][128];   // tensor maps of the workspace: 128 and 64 rows a copy
+    // tensor maps of the workspace (128 and 64 rows a copy) and of the second one
+    alignas(64) unsigned char maps[4][128];
 };
 
 // fills queue, queue_first and pairs for a device that holds `clusters` CTA pairs
 void lay_queue(Matrices& m, int clusters);
 // device side (dpg_ortho.cu)
-int upload_matrices(Matrices& m);
+int upload_matrices(Matrices& m, bool both);   // both: steps that take both halves follow
 int upload_for_update(Matrices& m);   // only what dpg_muon_apply needs
 void release_matrices(Matrices& m);
 int check_matrices(Matrices& m, void* stream);
