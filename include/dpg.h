@@ -511,8 +511,11 @@ int dpg_matrices_info(const dpg_matrices_t* mats, int32_t* n_matrices, int64_t* 
 int dpg_matrices_upload(dpg_matrices_t* mats);
 /* Every device-side wait of the orthogonalisation is bounded (2 s).  One that
  * runs out ends the call's kernels with incomplete results and records
- * DPG_ERR_DEVICE_TIMEOUT, and later calls end early too; this synchronises
- * `stream` and returns the record (DPG_OK if there is none), clearing it. */
+ * DPG_ERR_DEVICE_TIMEOUT.  While the record stands, later orthogonalisations may
+ * end early too, and dpg_muon_apply and dpg_muon_step leave master weights and
+ * views as they are (the step's momentum has taken its gradient by then).  This
+ * synchronises `stream` and returns the record (DPG_OK if there is none),
+ * clearing it. */
 int dpg_matrices_status(dpg_matrices_t* mats, void* stream);
 
 /* Momentum of the reduced gradient, buckets [b0, b1), in one pass (binary32,

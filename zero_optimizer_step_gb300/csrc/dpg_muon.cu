@@ -62,6 +62,7 @@ struct ApplyArgs {
     const ApplyItem* items;
     const double* scales;   // 2 per parameter
     const uint16_t* ortho;
+    const int32_t* status;  // of the orthogonalisation; NULL: none has run
     float* master;
     void* views[DPG_MAX_VIEWS];
     int32_t n_views, rule, decay;
@@ -73,6 +74,8 @@ __global__ void __launch_bounds__(kChunkThreads) k_muon_apply(const __grid_const
     static_assert(kApplyChunk == kChunkThreads * kVec, "one vector per thread");
     pdl_enter();
     const ApplyItem it = a.items[blockIdx.x];
+    // o is incomplete: weights and views stay as they are
+    if (a.status && __ldcg(a.status) != 0) return;
     const int e = int(threadIdx.x) * kVec;
     if (e >= it.count) return;
     const int64_t i = it.off + e;
@@ -206,6 +209,7 @@ static int launch_apply(const Matrices& m, ApplyArgs& a, cudaStream_t s, const c
     if (m.apply_items.empty()) return DPG_OK;
     a.items = m.d_apply_items;
     a.scales = m.d_scales;
+    a.status = m.ws ? reinterpret_cast<const int32_t*>(m.ws + m.o_status) : nullptr;
     return launch_k(k_muon_apply, unsigned(m.apply_items.size()), kChunkThreads, s, who, a);
 }
 
