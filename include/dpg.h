@@ -647,9 +647,10 @@ int dpg_debug_checks(const dpg_plan_t* plan, int32_t* built, int64_t* first_fail
 int dpg_debug_set_limit(int64_t limit);
 
 /* Test-only fault injection for the staged step (and for the next
- * orthogonalisation of matrices of more than 128 rows, whichever the thread
- * calls first; there skip_unit is a 64-deep stage of the first CTA's operands
- * and the default bound is 2 s): its next launch by the
+ * orthogonalisation, whichever the thread calls first; there skip_unit is a
+ * 64-deep stage of the first CTA's operands, or, whatever it is from 0 on, a
+ * matrix on the Gram path lacks one exchanged value; the default bound is
+ * 2 s): its next launch by the
  * calling thread never fetches unit `skip_unit` (-1: none), so the CTA
  * that owns it must run out its wait, and every wait is bounded by
  * `timeout_ns` (<= 0: the default 1 s).  Used to test the timeout path.

@@ -28,7 +28,7 @@ def _timed_out(mats):
     dpg.dpg_matrices_status(mats)      # reported once
 
 
-STEP_SHAPES = [[(300, 700, 2)]]
+STEP_SHAPES = [[(300, 700, 2)], [(60, 90, 1), (20, 20, 3)]]
 
 
 @pytest.mark.parametrize("shapes", STEP_SHAPES)
@@ -73,3 +73,40 @@ def test_step_whose_wait_ran_out_leaves_the_weights(monkeypatch, shapes, upd_dty
     for p, (r, c, k) in enumerate(shapes):
         at = slice(int(plan.param_offset[p]), int(plan.param_offset[p]) + r * c * k)
         assert torch.equal(w[at], want_w[at]) and torch.equal(view[at], want_view[at])
+
+
+@pytest.mark.parametrize("shapes", [[(16, 40, 2)], [(30, 50, 1)], [(64, 200, 1)], [(100, 128, 1)],
+                                    [(5, 7, 1), (128, 90, 1), (40, 41, 1)]])
+def test_short_side_waits_are_bounded(monkeypatch, shapes):
+    # one value of an exchange is never sent: the waits for it run out, the
+    # error is reported once, and the next call is whole
+    rng = np.random.Generator(np.random.Philox(41))
+    plan, mats = _object(shapes)
+    u = torch.from_numpy(rng.standard_normal(plan.total_padded).astype(np.float32)).to(DEV)
+    outs = [torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), outs[0])
+    dpg.dpg_matrices_status(mats)
+    monkeypatch.setenv("DPG_TEST_HOOKS", "1")
+    dpg.dpg_set_staged_fault(skip_unit=0, timeout_ns=20_000_000)
+    dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), outs[1])
+    _timed_out(mats)
+    for o in outs[1:]:                 # (the fault is used up)
+        dpg.dpg_orthogonalize(mats, u, dpg.MuonHParams(), o)
+        dpg.dpg_matrices_status(mats)
+        assert torch.equal(o, outs[0])
+
+
+def test_fault_is_used_up_by_matrices_of_any_size(monkeypatch):
+    _, small = _object([(20, 30, 1)])
+    plan, large = _object([(300, 400, 1)])
+    u = torch.randn(plan.total_padded, device=DEV)
+    o = torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV)
+    monkeypatch.setenv("DPG_TEST_HOOKS", "1")
+    dpg.dpg_set_staged_fault(skip_unit=-1, timeout_ns=20_000_000)
+    dpg.dpg_orthogonalize(small, u, dpg.MuonHParams(), o)
+    dpg.dpg_matrices_status(small)
+    dpg.dpg_set_staged_fault(skip_unit=0, timeout_ns=20_000_000)
+    dpg.dpg_orthogonalize(small, u, dpg.MuonHParams(), o)
+    dpg.dpg_orthogonalize(large, u, dpg.MuonHParams(), o)
+    dpg.dpg_matrices_status(large)
+    _timed_out(small)

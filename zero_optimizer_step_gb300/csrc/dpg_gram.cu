@@ -49,6 +49,8 @@ struct GramArgs {
     float* prod;             // per matrix: the product of the Q_k, [padded rows]^2
     int32_t* exp;            // per matrix: prod is for U 2^-exp
     int32_t* status;         // 0, or the error of the first wait that ran out
+    uint64_t wait_ns;        // bound of every wait
+    int32_t leave_out;       // test only: the first CTA does not send its first values
     double eps;
     int32_t first;           // the copy holds U, to be divided by its norm; else X as it is
     int32_t n_steps;         // of this phase
@@ -206,7 +208,6 @@ __global__ void __launch_bounds__(kGramThreads) k_gram_sum(const __grid_constant
 // against 66 for 1000 of 16 x 64, and as long at 64 and 128 rows, where the
 // bytes are the exchange.
 // ---------------------------------------------------------------------------
-constexpr uint64_t kGramWaitNs = 2000000000ull;   // bound of an exchange
 __device__ __forceinline__ void gram_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -320,8 +321,10 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
     // writes W neighbouring values to the own rows (row, col ..) of `dst` in
     // every CTA of the cluster: 16 bytes at a time where there are as many (one
     // value at a time, the writes took longer than the products)
+    bool ok = true;                      // after a wait ran out: waits and sends no more, the result is worthless
     auto spread = [&](float* dst, uint64_t* bar, int row, int col, const float* v, auto width) {
         constexpr int W = decltype(width)::value;
+        if (!ok) return;
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst + (row0 + row) * MP + col));
         const uint32_t bar_at = static_cast<uint32_t>(__cvta_generic_to_shared(bar));
 #pragma unroll
@@ -340,13 +343,13 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
                              :: "r"(to), "f"(v[0]), "r"(bar_to) : "memory");
         }
     };
-    // expects one exchange (thread 0, before any wait for it), and waits for the n-th
+    // expects one exchange (thread 0, before any wait for it; not on top of one that never
+    // ended), and waits for the n-th
     auto expect_all = [&](uint64_t* bar) {
-        if (t == 0)
+        if (t == 0 && ok)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                          :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar))), "r"(MP * MP * 4) : "memory");
     };
-    bool ok = true;                      // after a wait ran out: waits no more, the result is worthless
     auto wait_all = [&](uint64_t* bar, int n) {
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(bar));
         uint64_t since = 0;
@@ -361,7 +364,7 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
                 uint64_t now;
                 asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
                 if (polls == 0) since = now;
-                if (now - since > kGramWaitNs) {
+                if (now - since > a.wait_ns) {
                     ok = false;
                     atomicCAS(a.status, 0, DPG_ERR_DEVICE_TIMEOUT);
                 }
@@ -403,7 +406,8 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
                 }
             }
         }
-        spread(A, all_of, q / (MP / 4), (q % (MP / 4)) * 4, s, Width<4>());
+        if (!(a.leave_out && blockIdx.x == 0 && q == 0))
+            spread(A, all_of, q / (MP / 4), (q % (MP / 4)) * 4, s, Width<4>());
     }
     wait_all(all_of, 0);
     if (t < 32) {                        // trace: the squared norm of U 2^-e
@@ -469,6 +473,13 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
     const float inv = float(1.0 / den_sh);
     for (int q = t; q < 16 * MP; q += kGramThreads) a.prod[d.prod + row0 * MP + q] = P[q] * inv;
     if (rank == 0 && t == 0) a.exp[mat] = e;
+    if (!ok) {                           // what others sent without being waited for lands within this time
+        uint64_t since, now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(since));
+        do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        while (now - since < 2000000ull);
+    }
+    __syncwarp();
     gram_cluster_sync();                 // no CTA leaves while others write to it
 }
 
@@ -650,6 +661,7 @@ static int launch_clusters(void (*k)(P...), int n, int ctas, int smem, cudaStrea
 static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_hparams* hp, int k0, int k1,
                           void* out) {
     GramArgs a{};
+    a.wait_ns = kOrthoWaitNs;
     a.mats = m.d_small;
     a.update = update;
     a.out = static_cast<uint16_t*>(out);
@@ -701,13 +713,15 @@ static int launch_gram_steps(const Matrices& m, const GramArgs& a, cudaStream_t 
 }
 
 int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, const OrthoSchedule& sch,
-                void* out, cudaStream_t s, const char* who) {
+                const WaitFault& fault, void* out, cudaStream_t s, const char* who) {
     if (m.small.empty()) return DPG_OK;
     const int mp = m.small_count[3] ? 128 : m.small_count[2] ? 64 : m.small_count[1] ? 32 : 16;
     int st = DPG_OK;
     for (int p = 0; p < sch.n_phases && st == DPG_OK; ++p) {
         const bool last = p + 1 == sch.n_phases;
-        const GramArgs a = gram_args(m, update, hp, p ? sch.phase_end[p - 1] : 0, sch.phase_end[p], out);
+        GramArgs a = gram_args(m, update, hp, p ? sch.phase_end[p - 1] : 0, sch.phase_end[p], out);
+        a.wait_ns = fault.wait_ns;
+        a.leave_out = fault.skip >= 0;
         st = launch_gram_steps(m, a, s, who);
         if (st == DPG_OK)
             st = launch_k(last ? k_gram_apply<false> : k_gram_apply<true>, unsigned(m.prod_items.size()), kGramThreads,

@@ -489,7 +489,6 @@ constexpr int kSlotBytes = 2 * int(kBlkBytes);        // hi | lo, or the tile | 
 constexpr int kEpiWarps = 8;
 constexpr int kFillWarp = 2 + kEpiWarps, kStoreWarp = kFillWarp + 1;
 constexpr int kOrthoThreads = 32 * (kStoreWarp + 1);
-constexpr uint64_t kWaitNs = 2000000000ull;           // bound of every wait, unless a test sets another
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -1594,12 +1593,15 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
                  const OrthoSchedule& sch, void* out, void* stream, const char* who) {
     OrthoArgs a{};
     std::memcpy(a.st, sch.st, sizeof a.st);
+    const WaitFault fault{t_staged_skip, t_staged_timeout_ns > 0 ? uint64_t(t_staged_timeout_ns) : kOrthoWaitNs};
+    t_staged_skip = -1;
+    t_staged_timeout_ns = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Everything that reads `update` comes before anything that writes `out`,
     // which may share its memory.
     int st = gram_read(m, update, update_dtype, hp, out, s, who);
     if (st != DPG_OK) return st;
-    if (m.mats.empty()) return gram_finish(m, update, hp, sch, out, s, who);
+    if (m.mats.empty()) return gram_finish(m, update, hp, sch, fault, out, s, who);
     a.mats = m.d_mats;
     a.ws = m.ws;
     a.diag_a = reinterpret_cast<float*>(m.ws + m.o_diag);
@@ -1614,10 +1616,8 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.f32 = update_dtype == DPG_F32;
     a.done = reinterpret_cast<int32_t*>(m.ws + m.o_done);
     a.join = reinterpret_cast<int32_t*>(m.ws + m.o_join);
-    a.skip = t_staged_skip;
-    a.wait_ns = t_staged_timeout_ns > 0 ? uint64_t(t_staged_timeout_ns) : kWaitNs;
-    t_staged_skip = -1;
-    t_staged_timeout_ns = 0;
+    a.skip = fault.skip;
+    a.wait_ns = fault.wait_ns;
     a.queue = m.d_queue;
     a.queue_first = m.d_queue_first;
     a.ws_low = m.ws_low;
@@ -1635,7 +1635,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     if (st == DPG_OK)
         st = launch_k(a.f32 ? k_ortho_load<true> : k_ortho_load<false>, unsigned(m.conv_items.size()), 256,
                       a.f32 ? 2 * kLoadSmem : kLoadSmem, s, who, a, static_cast<const ConvItem*>(m.d_conv_items));
-    if (st == DPG_OK) st = gram_finish(m, update, hp, sch, out, s, who);
+    if (st == DPG_OK) st = gram_finish(m, update, hp, sch, fault, out, s, who);
     if (st != DPG_OK) return st;
     const bool both = sch.both_steps > 0;
     CUtensorMap map[4] = {};

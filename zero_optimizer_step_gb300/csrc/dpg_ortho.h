@@ -94,6 +94,13 @@ constexpr int kApplyChunk = 1024;
 // Products of a step, in order: A = X X^T, B = bA + cA^2, X' = aX + BX.
 enum : int { kProdA = 0, kProdB = 1, kProdX = 2 };
 
+constexpr uint64_t kOrthoWaitNs = 2000000000ull;   // bound of every wait, unless a test sets another
+// what a test does to one call
+struct WaitFault {
+    int64_t skip;         // >= 0: one copy or exchange is left out
+    uint64_t wait_ns;
+};
+
 constexpr float kLoScale = 2048.0f;   // of X's low half
 
 // Constants of one Newton-Schulz step.  Stored fp16 values are the true ones
@@ -179,7 +186,7 @@ int gram_prepare();
 int gram_read(const Matrices& m, const void* update, int32_t update_dtype, const dpg_muon_hparams* hp,
               void* out, cudaStream_t s, const char* who);
 int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* hp, const OrthoSchedule& sch,
-                void* out, cudaStream_t s, const char* who);
+                const WaitFault& fault, void* out, cudaStream_t s, const char* who);
 
 }  // namespace dpg
 
