@@ -47,6 +47,10 @@ bool aligned(const void* p, uintptr_t a);
 // checks the launch just issued and counts it
 int after_launch(const char* what);
 size_t round256(size_t x);
+// Waits for the copies and fills of an upload.  A copy from pageable memory may
+// return once its bytes are staged, and a fill at once; a kernel on a stream that
+// does not wait for the default one could read before they have arrived.
+cudaError_t upload_done();
 
 // Launches kernel k (which must begin with pdl_enter()) on `grid` CTAs of
 // `block` threads and `smem` bytes of dynamic shared memory, with programmatic stream serialization unless the calling

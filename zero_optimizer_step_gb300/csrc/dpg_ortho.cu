@@ -1438,6 +1438,7 @@ static int upload_update_tables(Matrices& m) {
     size_t at = 0;
     if (e == cudaSuccess) e = put(static_cast<unsigned char*>(tables), &at, m.apply_items, &m.d_apply_items);
     if (e == cudaSuccess) e = put(static_cast<unsigned char*>(tables), &at, m.scales, &m.d_scales);
+    if (e == cudaSuccess) e = upload_done();
     if (e != cudaSuccess) {
         cudaFree(tables);
         cudaGetLastError();
@@ -1538,7 +1539,7 @@ int upload_matrices(Matrices& m, bool both) {
     // arrival counters and the status word start at zero
     if (e == cudaSuccess)
         e = cudaMemset(static_cast<unsigned char*>(ws) + m.o_count, 0, size_t(m.o_status + 256 - m.o_count));
-    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = upload_done();
     if (e != cudaSuccess) {
         cudaGetLastError();
         st = fail(e == cudaErrorMemoryAllocation ? DPG_ERR_OOM : DPG_ERR_CUDA, "matrices upload: %s",

@@ -88,6 +88,8 @@ int after_launch(const char* what) {
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
+cudaError_t upload_done() { return cudaStreamSynchronize(cudaStreamLegacy); }
+
 
 VisLayout vis_layout(int64_t visits, int64_t ctas) {
     VisLayout L;
@@ -199,6 +201,7 @@ int upload(Plan& p) {
 #ifdef DPG_DEBUG
     if (e == cudaSuccess) e = cudaMemset(static_cast<unsigned char*>(clip) + clip_sq_bytes + 192, 0, 8);
 #endif
+    if (e == cudaSuccess) e = upload_done();
     if (e != cudaSuccess) {
         cudaFree(bo); cudaFree(tb); cudaFree(it); cudaFree(vis); cudaFree(clip); cudaFree(chunk);
         cudaFree(seg);
