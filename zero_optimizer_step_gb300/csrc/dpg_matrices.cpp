@@ -348,25 +348,24 @@ void lay_queue(Matrices& M, int clusters) {
 }
 
 // Largest |a s + b s^3 + c s^5| for s in [0, hi]: at an end or where the
-// derivative a + 3 b s^2 + 5 c s^4 vanishes.
+// derivative a + 3 b l + 5 c l^2, l = s^2, vanishes.  Coefficients are divided
+// by the largest, and each root is a quotient that does not cancel (for a tiny
+// c the textbook formula gives 0 in place of the root -a / 3 b).
 static double largest_odd(double a, double b, double c, double hi) {
+    const double size = std::max(std::fabs(a), std::max(std::fabs(b), std::fabs(c)));
+    if (size == 0.0) return 0.0;
+    a /= size;
+    b /= size;
+    c /= size;
     auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
     double best = p(hi);
-    const double A = 5.0 * c, B = 3.0 * b;
-    double root[2];
-    int n = 0;
-    if (A != 0.0) {
-        const double disc = B * B - 4.0 * A * a;
-        if (disc >= 0.0) {
-            root[n++] = (-B + std::sqrt(disc)) / (2.0 * A);
-            root[n++] = (-B - std::sqrt(disc)) / (2.0 * A);
-        }
-    } else if (B != 0.0) {
-        root[n++] = -a / B;
+    const double A = 5.0 * c, B = 3.0 * b, disc = B * B - 4.0 * A * a;
+    if (disc >= 0.0) {
+        const double q = -0.5 * (B + std::copysign(std::sqrt(disc), B));   // roots q / A and a / q
+        for (const double l : {A != 0.0 ? q / A : 0.0, q != 0.0 ? a / q : 0.0})
+            if (l > 0.0 && l < hi * hi) best = std::max(best, p(std::sqrt(l)));
     }
-    for (int k = 0; k < n; ++k)
-        if (root[k] > 0.0 && root[k] < hi * hi) best = std::max(best, p(std::sqrt(root[k])));
-    return best;
+    return best * size;
 }
 
 // Largest |b l + c l^2| for l in [0, hi].
