@@ -45,3 +45,30 @@ def test_quintic_extrema_inside():
     # s (1 - s^2)^2 k = k s - 2 k s^3 + k s^5: largest at s = 1 / sqrt(5), 0.286 k
     assert "update is NULL" in _refusal([(110.0, -220.0, 110.0)])
     assert "after step 0" in _refusal([(113.0, -226.0, 113.0)])
+
+
+def _values(hp):
+    c = hp.c()
+    return [list(c.coeffs[k]) for k in range(c.n_steps)]
+
+
+def test_coefficients_are_read_at_every_call():
+    # values held in objects that are changed in place: not those of an earlier call
+    a, row = torch.tensor(3.0), [torch.tensor(2.0), torch.tensor(-1.5), torch.tensor(0.5)]
+    hp = dpg.MuonHParams(coeffs=[(a, -1.0, 0.25), row])
+    assert _values(hp) == [[3.0, -1.0, 0.25], [2.0, -1.5, 0.5]]
+    a.fill_(1.0)
+    row[1].fill_(-2.0)
+    assert _values(hp) == [[1.0, -1.0, 0.25], [2.0, -2.0, 0.5]]
+    table = torch.tensor([[3.0, -1.0, 0.25]], dtype=torch.float64)
+    hp = dpg.MuonHParams(coeffs=table)
+    assert _values(hp) == [[3.0, -1.0, 0.25]]
+    table[0, 0] = 2.0
+    assert _values(hp) == [[2.0, -1.0, 0.25]]
+    assert ctypes.sizeof(hp.c()) == 16 * 24 + 32 + 16
+
+
+def test_coefficients_need_three_values_a_step():
+    for bad in ([(1.0, 2.0)], [(1.0, 2.0, 3.0, 4.0)]):
+        with pytest.raises(ValueError):
+            dpg.MuonHParams(coeffs=bad).c()

@@ -108,7 +108,8 @@ class MuonHParams:
     scale_rule: int = DPG_SCALE_SPECTRAL
 
     def c(self) -> dpg_muon_hparams:
-        coeffs = tuple(map(tuple, self.coeffs))
+        # (values: the cache must not go by objects that may be changed in place)
+        coeffs = tuple([(float(a), float(b), float(c)) for a, b, c in self.coeffs])
         return dpg_muon_hparams(self.lr, self.momentum, self.weight_decay, self.eps,
                                 _c_coeffs(coeffs[:DPG_MAX_NS_STEPS]), len(coeffs), int(self.nesterov),
                                 int(self.scale_rule))
@@ -117,7 +118,7 @@ class MuonHParams:
 @functools.lru_cache(maxsize=64)
 def _c_coeffs(coeffs):
     """The C array of a tuple of (a, b, c) tuples (a small call's time is mostly marshalling)."""
-    return ((ctypes.c_double * 3) * DPG_MAX_NS_STEPS)(*((float(a), float(b), float(c)) for a, b, c in coeffs))
+    return ((ctypes.c_double * 3) * DPG_MAX_NS_STEPS)(*coeffs)
 
 
 _lib = None
