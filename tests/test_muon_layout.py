@@ -1,0 +1,38 @@
+"""How the matrices of an object are laid out, and the limits of one object, on
+the host (no GPU)."""
+import pytest
+
+import zero_optimizer_step_gb300 as dpg
+
+GIB = 1 << 30
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from zero_optimizer_step_gb300 import build
+    build.build()
+
+
+def _mats(rows, cols, count):
+    plan = dpg.dpg_plan_buckets([rows * cols * count], 1 << 50, 1)
+    return dpg.dpg_plan_matrices(plan, [rows], [cols])
+
+
+def _tile_bytes(rows, cols, count):
+    """The tiles' blocks: three X and two Gram matrices of fp16, padded to 256."""
+    m, n = -(-min(rows, cols) // 256) * 256, -(-max(rows, cols) // 256) * 256
+    return count * 2 * (3 * m * n + 2 * m * m)
+
+
+@pytest.mark.parametrize("rows,cols,count", [(128, 2048, 6000), (2048, 128, 6000), (128, 4096, 3000), (100, 6000, 3000),
+                                             (128, 1024, 20000)])
+def test_large_lists_take_the_path_of_less_memory(rows, cols, count):
+    # (a tenth more for counters, items and row sums)
+    tiles = _tile_bytes(rows, cols, count)
+    assert tiles > 16 * GIB and _mats(rows, cols, count).workspace_bytes <= 1.1 * tiles
+
+
+@pytest.mark.parametrize("rows,cols,count", [(16, 64, 1 << 16), (10, 100, 1 << 17), (32, 256, 1 << 15)])
+def test_large_lists_of_narrow_matrices_are_not_padded_to_tiles(rows, cols, count):
+    tiles = _tile_bytes(rows, cols, count)
+    assert tiles > 16 * GIB and _mats(rows, cols, count).workspace_bytes < tiles / 8

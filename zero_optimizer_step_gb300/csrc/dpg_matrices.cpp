@@ -17,9 +17,16 @@ constexpr int64_t kMaxMatrices = 1 << 20;   // of one object
 static int64_t ceil_div(int64_t x, int64_t d) { return (x + d - 1) / d; }
 static int padded_side(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 
-// Items of a small matrix: Gram sums over about 64 groups of whole 32-column
+// Columns of a small matrix's Gram items: about 64 groups of whole 32-column
 // blocks (every further group is a partial sum to write and to read again; very
-// long matrices get one per 1024 columns, up to 128), products of 64 columns.
+// long matrices get one per 1024 columns, up to 128).
+static int64_t gram_width(int64_t n) {
+    const int64_t blocks = ceil_div(n, 32);
+    const int64_t groups = std::min<int64_t>(blocks, std::max<int64_t>(64, std::min<int64_t>(128, n / 1024)));
+    return ceil_div(blocks, groups) * 32;
+}
+
+// Items of a small matrix: Gram sums, products of 64 columns.
 static void small_items(Matrices& M, const MatDesc& d) {
     SmallDesc s{};
     s.off = d.off;
@@ -33,8 +40,7 @@ static void small_items(Matrices& M, const MatDesc& d) {
     M.n_small_copy += blocks * 32 * s.mp;
     s.prod = M.n_small_prod;
     M.n_small_prod += int64_t(s.mp) * s.mp;
-    const int64_t groups = std::min<int64_t>(blocks, std::max<int64_t>(64, std::min<int64_t>(128, d.n / 1024)));
-    const int64_t width = ceil_div(blocks, groups) * 32;
+    const int64_t width = gram_width(d.n);
     s.part = M.n_small_part;
     s.item0 = int32_t(M.gram_items.size());
     for (int64_t c = 0; c < d.n; c += width) {
@@ -64,8 +70,10 @@ static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 // two passes over the columns up to 2 ns per column, nothing else runs beside
 // it.  Tiles are padded to 256 and their fifteen products follow one another,
 // but as many as there are pairs run at once, and beside larger matrices they
-// only fill gaps.  Lists whose padded tiles would take more than 16 GB stay on
-// the Gram path, which needs a third of that.  Measured, Gram path and tiles (us):
+// only fill gaps.  Where the padded tiles would take more than 16 GB, the path
+// that needs less memory is taken: the copy and one sum per 32 columns or more of
+// the Gram path are a fraction of the tiles for narrow matrices, but up to half
+// as much again for 128 rows.  Measured, Gram path and tiles (us):
 //     1 of 128 x 1000     82   117      1 of 128 x 6000     94   151
 //     15 of 128 x 1000   113   141      16 of 128 x 6000   319   368
 //     16 of 128 x 1000   169   142      64 of 128 x 600    409   201
@@ -75,7 +83,7 @@ static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols, bool* gram) {
     static const double steps[4] = {12, 17, 30, 62}, pass[4] = {0.3e-3, 0.5e-3, 1e-3, 2e-3};
     static const int64_t resident[4] = {1000, 300, 70, 15};
-    int64_t count[4] = {}, columns[4] = {}, longest[4] = {}, blocks[4] = {};
+    int64_t count[4] = {}, columns[4] = {}, longest[4] = {}, blocks[4] = {}, floats[4] = {};
     double tiles[4] = {};
     bool larger = false;
     for (int32_t q = 0; q < p.n_params; ++q) {
@@ -91,13 +99,15 @@ static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols,
         columns[c] += k * n;
         longest[c] = std::max(longest[c], n);
         blocks[c] += k * 8 * (3 * ceil_div(n, kOrthoTile) + 2);   // as lay_out counts them
+        floats[c] += k * (ceil_div(n, 32) * 32 * s + (ceil_div(n, gram_width(n)) + 1) * s * s);   // and small_items
         tiles[c] += double(k) * 5.0 * (std::max(0.3 * deep, 3.0) + 3.0 + 3.0 * wide) / 76.0;
     }
     for (int c = 3; c >= 0; --c) {
         const double one = larger ? 0.0 : 90.0 + 1.5 * double(ceil_div(longest[c], kBlkCols));
-        gram[c] = blocks[c] * kBlkBytes > (int64_t(16) << 30) ||
-                  steps[c] * double(ceil_div(count[c], resident[c])) + 10.0 + pass[c] * double(columns[c]) <=
-                      one + tiles[c];
+        gram[c] = blocks[c] * kBlkBytes > (int64_t(16) << 30)
+                      ? floats[c] * int64_t(sizeof(float)) < blocks[c] * kBlkBytes
+                      : steps[c] * double(ceil_div(count[c], resident[c])) + 10.0 + pass[c] * double(columns[c]) <=
+                            one + tiles[c];
         larger = larger || (count[c] > 0 && !gram[c]);
     }
 }
