@@ -36,3 +36,21 @@ def test_large_lists_take_the_path_of_less_memory(rows, cols, count):
 def test_large_lists_of_narrow_matrices_are_not_padded_to_tiles(rows, cols, count):
     tiles = _tile_bytes(rows, cols, count)
     assert tiles > 16 * GIB and _mats(rows, cols, count).workspace_bytes < tiles / 8
+
+
+def test_rows_of_the_workspace_stay_within_a_copys_coordinate():
+    # 129 x 129 is padded to 256 x 256: 5 x 8 blocks of 128 rows each, and a
+    # block's first row has to stay below 2^31
+    most = ((1 << 31) - 1) // 128 // 40
+    assert _mats(129, 129, most).n_matrices == most
+    with pytest.raises(dpg.DpgError) as e:
+        _mats(129, 129, most + 1)
+    assert e.value.status == dpg.DPG_ERR_INVALID_ARG and "large" in str(e.value)
+
+
+def test_matrices_of_one_object_are_counted():
+    most = 1 << 20
+    assert _mats(1, 1, most).n_matrices == most
+    with pytest.raises(dpg.DpgError) as e:
+        _mats(1, 1, most + 1)
+    assert e.value.status == dpg.DPG_ERR_INVALID_ARG and "large" in str(e.value)
