@@ -482,6 +482,8 @@ int dpg_step_noalloc(const dpg_plan_t* plan, const void* const* grads, int32_t g
  *              quintic coefficients coeffs[k] = {a, b, c}
  *   eps        >= 1e-30: floor of the Frobenius norm a matrix is divided by
  *   lr, weight_decay, scale_rule: see dpg_muon_apply
+ *   precise    != 0: all steps as precise as long schedules' early ones (see
+ *              dpg_orthogonalize)
  * ------------------------------------------------------------------------- */
 #define DPG_MAX_NS_STEPS 16
 #define DPG_SCALE_SPECTRAL 0 /* sqrt(max(1, rows / cols))   */
@@ -489,7 +491,7 @@ int dpg_step_noalloc(const dpg_plan_t* plan, const void* const* grads, int32_t g
 typedef struct {
     double lr, momentum, weight_decay, eps;
     double coeffs[DPG_MAX_NS_STEPS][3];
-    int32_t n_steps, nesterov, scale_rule, reserved;
+    int32_t n_steps, nesterov, scale_rule, precise;
 } dpg_muon_hparams;
 
 /* The matrices of a plan.  rows[p], cols[p] (HOST arrays, n_params entries,
@@ -551,7 +553,8 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * within 1.5e-3, and what 2^-21 of U's norm in U would change (the product of
  * the a_k times as much in those directions, as in any binary32 iteration).
  * Such steps take two to three times as long, and the first call that has them
- * allocates up to 4/5 of workspace_bytes more (make it before a capture).
+ * allocates 1/3 to 2/5 of workspace_bytes more (make it before a capture).  With
+ * `precise` every step is one of them: within 1e-4, 1e-6 for full rank.
  * Shorter side up to 128: either this, or the same steps on the Gram matrix
  * (A_k+1 = Q_k A_k Q_k, Q_k = aI + b A_k + c A_k^2, X = Q_n-1 .. Q_0 U / norm)
  * in fp32, whichever is faster for the matrices of the object; the choice

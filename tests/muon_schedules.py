@@ -67,8 +67,9 @@ def condition(u, coeffs, eps, rng):
 
 def allowed(steps_rel, moved):
     """The steps' own error and the rounding of the result to bf16 (at most
-    2^-9 of every value), which are independent, and the conditioning: the
-    sampled movements stand for others of their size up to a factor of two."""
+    2^-8 of a value, under 2^-9 in the root mean square over values of all
+    mantissas), which are independent, and the conditioning: the sampled
+    movements stand for others of their size up to a factor of two."""
     return 1.05 * math.hypot(2.0 ** -9, steps_rel) + 2.0 * moved
 
 

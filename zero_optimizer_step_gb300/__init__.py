@@ -92,13 +92,15 @@ class dpg_muon_hparams(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("eps", ctypes.c_double),
                 ("coeffs", (ctypes.c_double * 3) * DPG_MAX_NS_STEPS),
                 ("n_steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
-                ("scale_rule", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("scale_rule", ctypes.c_int32), ("precise", ctypes.c_int32)]
 
 
 @dataclass
 class MuonHParams:
     """Hyper-parameters of the matrix-orthogonalising step; ``coeffs`` holds one
-    (a, b, c) per Newton-Schulz step (default: five steps of Jordan et al.)."""
+    (a, b, c) per Newton-Schulz step (default: five steps of Jordan et al.).
+    ``precise``: products of both fp16 halves in all steps, at two to three times
+    the time."""
     lr: float = 0.02
     momentum: float = 0.95
     weight_decay: float = 0.0
@@ -106,13 +108,14 @@ class MuonHParams:
     nesterov: bool = True
     coeffs: Sequence[Sequence[float]] = ((3.4445, -4.7750, 2.0315),) * 5
     scale_rule: int = DPG_SCALE_SPECTRAL
+    precise: bool = False
 
     def c(self) -> dpg_muon_hparams:
         # (values: the cache must not go by objects that may be changed in place)
         coeffs = tuple([(float(a), float(b), float(c)) for a, b, c in self.coeffs])
         return dpg_muon_hparams(self.lr, self.momentum, self.weight_decay, self.eps,
                                 _c_coeffs(coeffs[:DPG_MAX_NS_STEPS]), len(coeffs), int(self.nesterov),
-                                int(self.scale_rule))
+                                int(self.scale_rule), int(bool(self.precise)))
 
 
 @functools.lru_cache(maxsize=64)

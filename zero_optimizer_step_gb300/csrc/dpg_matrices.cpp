@@ -417,13 +417,13 @@ static double gram_growth(double a, double b, double c, double hi) {
 // grows by more is cut at 2000 (three default steps), where the phases together
 // leave no more than the iteration on X in binary32 does (1e-5 to 2e-4): each
 // phase is three launches more, and cut at 2.4e5 too they left up to 2e-3.
-static void gram_phases(const double* growth, int n_steps, OrthoSchedule* sch) {
+static void gram_phases(const double* growth, int n_steps, bool precise, OrthoSchedule* sch) {
     constexpr double kOnePhase = 2.4e5, kEach = 2000.0;
     double all = 1.0, phase = 1.0;
     for (int k = 0; k < n_steps; ++k) all *= growth[k];
     sch->n_phases = 0;
     for (int k = 0; k < n_steps; ++k) {
-        if (k > 0 && phase * growth[k] > kEach && all > kOnePhase) {
+        if (k > 0 && phase * growth[k] > kEach && (all > kOnePhase || precise)) {
             sch->phase_end[sch->n_phases++] = k;
             phase = 1.0;
         }
@@ -444,8 +444,8 @@ static void gram_phases(const double* growth, int n_steps, OrthoSchedule* sch) {
 static void both_halves(const dpg_muon_hparams* hp, OrthoSchedule* sch) {
     double all = 1.0, to_come = 1.0;
     for (int k = 0; k < hp->n_steps; ++k) all *= std::max(1.0, std::fabs(hp->coeffs[k][0]));
-    sch->both_steps = 0;
-    for (int k = hp->n_steps - 1; k >= 0 && all > 490.0; --k) {
+    sch->both_steps = hp->precise ? hp->n_steps : 0;
+    for (int k = hp->n_steps - 1; k >= 0 && all > 490.0 && !hp->precise; --k) {
         if (to_come > 4.0) {
             sch->both_steps = k + 1;
             break;
@@ -492,7 +492,7 @@ int ortho_steps(const dpg_muon_hparams* hp, OrthoSchedule* sch, const char* who)
             return fail(DPG_ERR_INVALID_ARG, "%s: after step %d singular values may reach %g", who, k, top);
         s.sx_next = sx = scale_for(top);
     }
-    gram_phases(growth, hp->n_steps, sch);
+    gram_phases(growth, hp->n_steps, hp->precise != 0, sch);
     both_halves(hp, sch);
     return DPG_OK;
 }
