@@ -54,3 +54,12 @@ def test_matrices_of_one_object_are_counted():
     with pytest.raises(dpg.DpgError) as e:
         _mats(1, 1, most + 1)
     assert e.value.status == dpg.DPG_ERR_INVALID_ARG and "large" in str(e.value)
+
+
+def test_a_parameter_without_elements_changes_nothing():
+    def workspace(numels, rows, cols):
+        plan = dpg.dpg_plan_buckets(numels, 1 << 50, 1)
+        return dpg.dpg_plan_matrices(plan, rows, cols).workspace_bytes
+    alone = workspace([100 * 100 * 30], [100], [100])
+    assert workspace([100 * 100 * 30, 0], [100, 100], [100, 1 << 23]) == alone
+    assert workspace([0, 100 * 100 * 30], [1 << 23, 100], [1 << 23, 100]) == alone

@@ -89,8 +89,9 @@ static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols,
     for (int32_t q = 0; q < p.n_params; ++q) {
         const int64_t m = std::min(rows[q], cols[q]), n = std::max(rows[q], cols[q]);
         const int64_t k = p.numels[q] / (rows[q] * cols[q]);
+        if (k == 0) continue;
         if (m > kSmallSide) {
-            larger = larger || k > 0;
+            larger = true;
             continue;
         }
         const int s = padded_side(m), c = s == 16 ? 0 : s == 32 ? 1 : s == 64 ? 2 : 3;
