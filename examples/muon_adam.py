@@ -49,6 +49,7 @@ def main():
 
     matrices, vectors = Group([w1, w2]), Group([bias, gain])
     shapes = dpg.dpg_plan_matrices(matrices.plan, [h, d], [d, h])
+    dpg.dpg_matrices_upload(shapes)                     # tables and workspace now, not in the first step
     momentum = torch.zeros_like(matrices.master)
     update = torch.zeros_like(matrices.view)
     exp_avg, exp_avg_sq = torch.zeros_like(vectors.master), torch.zeros_like(vectors.master)

@@ -554,7 +554,7 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * the a_k times as much in those directions, as in any binary32 iteration).
  * Such steps take two to three times as long, and the first call that has them
  * allocates 1/3 to 2/5 of workspace_bytes more (make it before a capture).  With
- * `precise` every step is one of them: within 1e-4, 1e-6 for full rank.
+ * `precise` every step is one of them: within 2e-4, 2e-5 at full rank.
  * Shorter side up to 128: either this, or the same steps on the Gram matrix
  * (A_k+1 = Q_k A_k Q_k, Q_k = aI + b A_k + c A_k^2, X = Q_n-1 .. Q_0 U / norm)
  * in fp32, whichever is faster for the matrices of the object; the choice
@@ -572,7 +572,8 @@ int dpg_orthogonalize(dpg_matrices_t* mats, const void* update, int32_t update_d
                       const dpg_muon_hparams* hp, void* ortho_bf16, void* stream);
 
 /* Weight update from the orthogonalised update o (flat bf16), every element
- * of every matrix, binary32, no FMA:
+ * of every matrix, binary32, no FMA (in the up to seven padding slots after a
+ * parameter, master keeps its value and views get that, rounded):
  *   w <- w - fp32(lr * weight_decay) * w     (if weight_decay != 0)
  *   w <- w - fp32(lr * scale) * o            scale by scale_rule and shape
  *   param_views[k] = bf16_rne(w)             (k < n_views <= DPG_MAX_VIEWS) */

@@ -74,12 +74,15 @@ static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 // that needs less memory is taken: the copy and one sum per 32 columns or more of
 // the Gram path are a fraction of the tiles for narrow matrices, but up to half
 // as much again for 128 rows.  Measured, Gram path and tiles (us):
-//     1 of 128 x 1000     82   117      1 of 128 x 6000     94   151
-//     15 of 128 x 1000   113   141      16 of 128 x 6000   319   368
-//     16 of 128 x 1000   169   142      64 of 128 x 600    409   201
-//     30 of 100 x 100    147   113      64 of 64 x 2000    170   415
-//     64 x 32 and 32 x 10 23    96      4 of 128 x 50000   438   862
-// (Later steps made the Gram times 1 to 5 %, the tiles' 2 to 4 % shorter.)
+//     1 of 128 x 1000     79   110      1 of 128 x 6000     90   147
+//     15 of 128 x 1000   109   131      16 of 128 x 6000   315   353
+//     16 of 128 x 1000   165   132      64 of 128 x 600    402   191
+//     30 of 100 x 100    142   104      64 of 64 x 2000    166   398
+//     64 x 32 and 32 x 10 20    89      4 of 128 x 50000   434   837
+//     1000 of 16 x 64     65  1254
+// The numbers in the rule (76 pairs, clusters resident at once, times) are those
+// of this GPU, fitted to sets like these; with long schedules each path's share
+// grows alike, so it goes by five steps.
 static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols, bool* gram) {
     static const double steps[4] = {12, 17, 30, 62}, pass[4] = {0.3e-3, 0.5e-3, 1e-3, 2e-3};
     static const int64_t resident[4] = {1000, 300, 70, 15};

@@ -44,7 +44,9 @@
 // What they leave grows with the a of every step to come.  In the early steps
 // of schedules that multiply it by more (both_halves), A and B are pairs of
 // fp16 numbers too and the products take hi hi + lo hi + hi lo, as three sums
-// in one accumulator; t is 1.  That is 1e-6 a step, the roundings of fp32.
+// in one accumulator; t is 1.  That leaves 5e-6 (256 x 512) to 2e-5 (512 x 1024)
+// at full rank, 1e-4 at low rank, as binary32 does, for two to three times the
+// time.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -450,10 +452,10 @@ __global__ void __launch_bounds__(256) k_ortho_load(const __grid_constant__ Orth
 // stage and SM) were 3 % slower on every list tried, 144 SMs in use instead of
 // 152: what limits large matrices is the power cap, not L2.
 //
-// Measured, whole calls: 218M elements of an 8B model's layer 11.4 ms, 1.29
+// Measured, whole calls: 218M elements of an 8B model's layer 11.2 to 11.6 ms, 1.29
 // PFLOP/s of m^2 n + m^3 + 2 m^2 n flops per step (the 1.37 kW cap holds the
 // clock near 1.45 GHz, where a plain fp16 library product of 8192^3 runs at
-// 1.55 to 1.65); a 1B model's layer 1.91 to 1.98 ms, 1.2 PFLOP/s, of which norm
+// 1.55 to 1.65); a 1B model's layer 1.79 to 1.99 ms, 1.2 PFLOP/s, of which norm
 // and load are 0.08; eight GPT-2-small attention matrices 0.233 ms, 0.54 PFLOP/s.
 // There, as for every list whose products last one or two rounds of tiles, the
 // way from product to product bounds it: finish 2 to 3 us, stores and their
