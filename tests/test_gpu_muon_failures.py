@@ -110,3 +110,21 @@ def test_fault_is_used_up_by_matrices_of_any_size(monkeypatch):
     dpg.dpg_orthogonalize(large, u, dpg.MuonHParams(), o)
     dpg.dpg_matrices_status(large)
     _timed_out(small)
+
+
+@pytest.mark.parametrize("skip", [0, 3, 40])
+def test_waits_of_steps_with_both_halves_are_bounded(monkeypatch, skip):
+    rng = np.random.Generator(np.random.Philox(42))
+    plan, mats = _object([(300, 700, 2)])
+    u = torch.from_numpy(rng.standard_normal(plan.total_padded).astype(np.float32)).to(DEV)
+    hp = dpg.MuonHParams(precise=True)
+    outs = [torch.zeros(plan.total_padded, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    dpg.dpg_orthogonalize(mats, u, hp, outs[0])
+    dpg.dpg_matrices_status(mats)
+    monkeypatch.setenv("DPG_TEST_HOOKS", "1")
+    dpg.dpg_set_staged_fault(skip_unit=skip, timeout_ns=20_000_000)
+    dpg.dpg_orthogonalize(mats, u, hp, outs[1])
+    _timed_out(mats)
+    dpg.dpg_orthogonalize(mats, u, hp, outs[1])
+    dpg.dpg_matrices_status(mats)
+    assert torch.equal(outs[0], outs[1])

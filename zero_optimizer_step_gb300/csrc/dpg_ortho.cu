@@ -1183,28 +1183,29 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const bool two = prod == kProdX ? has_lo : both;
                 const int visits = visits_of(prod, both);
                 if (!(ok = wait_operands(sh, a, d, tile.mat, prod, step))) break;
-                for (int g = 0, v = 0; g < blocks; g += ++v == visits, v = v == visits ? 0 : v, ++n) {
-                    const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
-                    if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a))) break;
-                    // Tells the finishing warps, which so need not watch the counter in memory
-                    // themselves (ten watchers per CTA instead of two delayed it by a
-                    // microsecond).  They have all seen it for the tile before, or they could
-                    // miss a phase: a block of that tile is finished, the one in this slot or,
-                    // if it had one only, the one in the other slot.
-                    if (g == 0 && v == 0) {
-                        if (before == 1 &&
-                            !(ok = wait_bounded(sh, &sh.slot_free[sl ^ 1], ((n - 1) >> 1) & 1, a)))
-                            break;
-                        mbar_arrive(&sh.tile_ready);
+                for (int g = 0; g < blocks && ok; ++g)
+                    for (int v = 0; v < visits; ++v, ++n) {
+                        const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
+                        if (!(ok = wait_bounded(sh, &sh.slot_free[sl], ((n >> 1) & 1) ^ 1u, a))) break;
+                        // Tells the finishing warps, which so need not watch the counter in memory
+                        // themselves (ten watchers per CTA instead of two delayed it by a
+                        // microsecond).  They have all seen it for the tile before, or they could
+                        // miss a phase: a block of that tile is finished, the one in this slot or,
+                        // if it had one only, the one in the other slot.
+                        if (g == 0 && v == 0) {
+                            if (before == 1 &&
+                                !(ok = wait_bounded(sh, &sh.slot_free[sl ^ 1], ((n - 1) >> 1) & 1, a)))
+                                break;
+                            mbar_arrive(&sh.tile_ready);
+                        }
+                        if (prod == kProdA || v > 0) {
+                            mbar_arrive(&sh.in_full[sl]);
+                            continue;
+                        }
+                        mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (two ? 2 : 1));
+                        copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
+                        if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
                     }
-                    if (prod == kProdA || v > 0) {
-                        mbar_arrive(&sh.in_full[sl]);
-                        continue;
-                    }
-                    mbar_expect(&sh.in_full[sl], uint32_t(kBlkBytes) * (two ? 2 : 1));
-                    copy_in(at, in + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
-                    if (two) copy_in(at + uint32_t(kBlkBytes), lo + g * kBlkBytes, uint32_t(kBlkBytes), &sh.in_full[sl]);
-                }
                 before = blocks * visits;
             }
         }
@@ -1232,31 +1233,32 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int64_t image_at = int64_t(tile.i * 4 + int(rank) * 2) * kBlkBytes;
                 unsigned char* image = a.ws + (prod == kProdA ? d.a : d.b) * kBlkBytes + image_at;
                 int32_t* done = a.done + 3 * tile.mat + prod;
-                for (int g = 0, v = 0; g < blocks; g += ++v == visits, v = v == visits ? 0 : v, ++n) {
-                    const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
-                    if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (n >> 1) & 1, a))) break;
-                    if (prod != kProdX) {
-                        // with both halves the last two of a block's visits leave hi and lo
-                        const bool is_low = both && v + 1 == visits;
-                        if (both && v + 2 < visits) {
-                            mbar_arrive(&sh.slot_free[sl]);
-                            continue;
+                for (int g = 0; g < blocks && ok; ++g)
+                    for (int v = 0; v < visits; ++v, ++n) {
+                        const uint32_t sl = n & 1, at = slot0 + sl * kSlotBytes;
+                        if (!(ok = wait_bounded(sh, &sh.out_ready[sl], (n >> 1) & 1, a))) break;
+                        if (prod != kProdX) {
+                            // with both halves the last two of a block's visits leave hi and lo
+                            const bool is_low = both && v + 1 == visits;
+                            if (both && v + 2 < visits) {
+                                mbar_arrive(&sh.slot_free[sl]);
+                                continue;
+                            }
+                            copy_out((is_low ? lo : out) + g * kBlkBytes, at, uint32_t(kBlkBytes));
+                            if (mirror) {     // 64 rows from this block's first column, 2 x 64 columns
+                                unsigned char* m = (is_low ? low + image_at : image) +
+                                                   int64_t((c0 + g) >> 1) * cb * kBlkBytes + ((c0 + g) & 1) * 8192;
+                                copy_out(m, at + uint32_t(kBlkBytes), 8192);
+                                copy_out(m + kBlkBytes, at + uint32_t(kBlkBytes) + 8192, 8192);
+                            }
+                        } else if (!last) {
+                            copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
+                            copy_out(lo + g * kBlkBytes, at + uint32_t(kBlkBytes), uint32_t(kBlkBytes));
                         }
-                        copy_out((is_low ? lo : out) + g * kBlkBytes, at, uint32_t(kBlkBytes));
-                        if (mirror) {     // 64 rows from this block's first column, 2 x 64 columns
-                            unsigned char* m = (is_low ? low + image_at : image) +
-                                               int64_t((c0 + g) >> 1) * cb * kBlkBytes + ((c0 + g) & 1) * 8192;
-                            copy_out(m, at + uint32_t(kBlkBytes), 8192);
-                            copy_out(m + kBlkBytes, at + uint32_t(kBlkBytes) + 8192, 8192);
-                        }
-                    } else if (!last) {
-                        copy_out(out + g * kBlkBytes, at, uint32_t(kBlkBytes));
-                        copy_out(lo + g * kBlkBytes, at + uint32_t(kBlkBytes), uint32_t(kBlkBytes));
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        mbar_arrive(&sh.slot_free[sl]);
                     }
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    mbar_arrive(&sh.slot_free[sl]);
-                }
                 if (!ok) break;
                 // all of the tile is in memory before its count (the release covers what the
                 // finishing warps wrote, too: they arrived at out_ready after it)
