@@ -111,17 +111,30 @@ class MuonHParams:
     precise: bool = False
 
     def c(self) -> dpg_muon_hparams:
-        # (values: the cache must not go by objects that may be changed in place)
-        coeffs = tuple([(float(a), float(b), float(c)) for a, b, c in self.coeffs])
-        return dpg_muon_hparams(self.lr, self.momentum, self.weight_decay, self.eps,
-                                _c_coeffs(coeffs[:DPG_MAX_NS_STEPS]), len(coeffs), int(self.nesterov),
-                                int(self.scale_rule), int(bool(self.precise)))
+        coeffs = tuple(map(tuple, self.coeffs))
+        return dpg_muon_hparams(self.lr, self.momentum, self.weight_decay, self.eps, _c_coeffs(coeffs),
+                                len(coeffs), int(self.nesterov), int(self.scale_rule), bool(self.precise))
 
 
-@functools.lru_cache(maxsize=64)
+_coeff_arrays = {}
+
+
 def _c_coeffs(coeffs):
-    """The C array of a tuple of (a, b, c) tuples (a small call's time is mostly marshalling)."""
-    return ((ctypes.c_double * 3) * DPG_MAX_NS_STEPS)(*coeffs)
+    """The C array of a tuple of (a, b, c) tuples.  Those of plain numbers are kept
+    (a small call's time is mostly marshalling); other objects may be changed in
+    place, so theirs are read at every call."""
+    try:
+        array = _coeff_arrays.get(coeffs)
+    except TypeError:                    # not hashable
+        array = None
+    if array is None:
+        array = ((ctypes.c_double * 3) * DPG_MAX_NS_STEPS)(
+            *((float(a), float(b), float(c)) for a, b, c in coeffs[:DPG_MAX_NS_STEPS]))
+        if all(type(x) in (float, int) for row in coeffs for x in row):
+            if len(_coeff_arrays) >= 64:
+                _coeff_arrays.clear()
+            _coeff_arrays[coeffs] = array
+    return array
 
 
 _lib = None

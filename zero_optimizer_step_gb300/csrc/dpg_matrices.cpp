@@ -406,8 +406,8 @@ static float scale_for(double most) {
 // meets a factor that grows with its size, so nothing brings it back.
 static double gram_growth(double a, double b, double c, double hi) {
     double most = 1.0;
-    for (int i = 0; i <= 16; ++i) {
-        const double l = hi * i / 16.0, q = a + l * (b + l * c);
+    for (int i = 0; i <= 4; ++i) {
+        const double l = hi * i / 4.0, q = a + l * (b + l * c);
         most = std::max(most, std::fabs(q * (q + 2.0 * l * (b + 2.0 * c * l))));
     }
     return most;
