@@ -50,7 +50,7 @@ struct GramArgs {
     int32_t* exp;            // per matrix: prod is for U 2^-exp
     int32_t* status;         // 0, or the error of the first wait that ran out
     uint64_t wait_ns;        // bound of every wait
-    int32_t leave_out;       // test only: the first CTA does not send its first values
+    int32_t leave_out;       // test only: 0: the first CTA does not send its first values (-1: none)
     double eps;
     int32_t first;           // the copy holds U, to be divided by its norm; else X as it is
     int32_t n_steps;         // of this phase
@@ -212,6 +212,15 @@ __device__ __forceinline__ void gram_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// After a wait that ran out: what others sent without being waited for lands
+// within this time.  (Not inlined: the code would be fetched in every call.)
+__device__ __noinline__ void linger() {
+    uint64_t since, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(since));
+    do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    while (now - since < 2000000ull);
+}
+
 // 16 rows times MP x MP.  The CTA's threads split K into R parts; within one, a
 // thread holds R rows by MP / 16 columns (four rows where there are columns
 // enough: half the shared-memory reads per multiply-add of two).  The parts
@@ -321,10 +330,9 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
     // writes W neighbouring values to the own rows (row, col ..) of `dst` in
     // every CTA of the cluster: 16 bytes at a time where there are as many (one
     // value at a time, the writes took longer than the products)
-    bool ok = true;                      // after a wait ran out: waits and sends no more, the result is worthless
+    bool ok = true;                      // after a wait ran out: waits no more, the result is worthless
     auto spread = [&](float* dst, uint64_t* bar, int row, int col, const float* v, auto width) {
         constexpr int W = decltype(width)::value;
-        if (!ok) return;
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst + (row0 + row) * MP + col));
         const uint32_t bar_at = static_cast<uint32_t>(__cvta_generic_to_shared(bar));
 #pragma unroll
@@ -343,10 +351,10 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
                              :: "r"(to), "f"(v[0]), "r"(bar_to) : "memory");
         }
     };
-    // expects one exchange (thread 0, before any wait for it; not on top of one that never
-    // ended), and waits for the n-th
+    // expects one exchange (thread 0, before any wait for it, after the last one ended), and
+    // waits for the n-th
     auto expect_all = [&](uint64_t* bar) {
-        if (t == 0 && ok)
+        if (t == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                          :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar))), "r"(MP * MP * 4) : "memory");
     };
@@ -383,6 +391,7 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
     int e = -1000;
     for (int k = 0; k < d.n_items; ++k) e = max(e, __ldg(a.part_exp + d.item0 + k));
     gram_cluster_sync();                 // every CTA has started: its memory may be written
+    const int leave_out = blockIdx.x == 0 ? a.leave_out : -1;
     for (int q = t; q < 4 * MP; q += kGramThreads) {
         const float4* p = reinterpret_cast<const float4*>(a.part + d.part + row0 * MP) + q;
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -406,7 +415,7 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
                 }
             }
         }
-        if (!(a.leave_out && blockIdx.x == 0 && q == 0))
+        if (q != leave_out)
             spread(A, all_of, q / (MP / 4), (q % (MP / 4)) * 4, s, Width<4>());
     }
     wait_all(all_of, 0);
@@ -416,9 +425,9 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (t == 0) {
-            // divisor of U 2^-e: max(norm, eps) 2^-e; of X 2^-e: 2^-e
-            double den = a.first ? sqrt(s) : 1.0;
-            if (e > -1000) den = a.first ? fmax(den, scalbn(a.eps, -e)) : scalbn(1.0, -e);
+            // divisor of U 2^-e: max(norm, eps) 2^-e; of X 2^-e: 2^-e (a.eps is 1)
+            double den = sqrt(a.first ? s : 0.0);
+            if (e > -1000) den = fmax(den, scalbn(a.eps, -e));
             const bool ok = s < 3.0e38;  // a NaN or an infinity in the matrix: NaN everywhere
             if (!(den > 0.0)) den = 1.0; // a zero matrix stays zero
             den_sh = ok ? den : __longlong_as_double(0x7FF8000000000000ll);
@@ -457,8 +466,11 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
             for (int j = 0; j < kCols; ++j) P[row * MP + y.col(j)] = y.v[j];
         }
         if (last) break;
+        // the exchange is free again; and a CTA that waited in vain ends here: it expects nothing
+        // on top of what never came, and sends at most the rows of one more exchange, whose bytes
+        // a barrier can count unexpected
+        if (__syncthreads_or(!ok)) break;
         expect_all(all_of);
-        __syncthreads();                 // the exchange is free again
         y.run(A + row0 * MP, Q, exchange);
 #pragma unroll
         for (int j = 0; j < kCols; ++j) S[row * MP + y.col(j)] = y.v[j] * scale;
@@ -473,12 +485,7 @@ __device__ void gram_steps(const GramArgs& a, int mat, int rank, float* sm) {
     const float inv = float(1.0 / den_sh);
     for (int q = t; q < 16 * MP; q += kGramThreads) a.prod[d.prod + row0 * MP + q] = P[q] * inv;
     if (rank == 0 && t == 0) a.exp[mat] = e;
-    if (!ok) {                           // what others sent without being waited for lands within this time
-        uint64_t since, now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(since));
-        do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        while (now - since < 2000000ull);
-    }
+    if (!ok) linger();
     __syncwarp();
     gram_cluster_sync();                 // no CTA leaves while others write to it
 }
@@ -671,7 +678,7 @@ static GramArgs gram_args(const Matrices& m, const void* update, const dpg_muon_
     a.exp = a.part_exp + m.gram_items.size();
     a.prod = reinterpret_cast<float*>(m.ws + m.o_small_prod);
     a.status = reinterpret_cast<int32_t*>(m.ws + m.o_status);
-    a.eps = hp->eps;
+    a.eps = k0 == 0 ? hp->eps : 1.0;
     a.first = k0 == 0;
     a.n_steps = k1 - k0;
     for (int k = k0; k < k1; ++k) {
@@ -721,7 +728,7 @@ int gram_finish(const Matrices& m, const void* update, const dpg_muon_hparams* h
         const bool last = p + 1 == sch.n_phases;
         GramArgs a = gram_args(m, update, hp, p ? sch.phase_end[p - 1] : 0, sch.phase_end[p], out);
         a.wait_ns = fault.wait_ns;
-        a.leave_out = fault.skip >= 0;
+        a.leave_out = fault.skip >= 0 ? 0 : -1;
         st = launch_gram_steps(m, a, s, who);
         if (st == DPG_OK)
             st = launch_k(last ? k_gram_apply<false> : k_gram_apply<true>, unsigned(m.prod_items.size()), kGramThreads,

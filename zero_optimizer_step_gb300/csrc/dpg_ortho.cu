@@ -1025,10 +1025,15 @@ __device__ __noinline__ bool join_parts(OrthoShared& sh, const OrthoArgs& a, con
 // read, so it alternates between two buffers as X does; the free one holds A's
 // low part while that is needed.
 template <bool BOTH>
+struct LowMaps {};
+template <>
+struct LowMaps<true> {
+    CUtensorMap rows128, rows64;     // of the second workspace
+};
+template <bool BOTH>
 __global__ void __cluster_dims__(2) __launch_bounds__(kOrthoThreads, 1)
 k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUtensorMap rows128,
-              const __grid_constant__ CUtensorMap rows64, const __grid_constant__ CUtensorMap low128,
-              const __grid_constant__ CUtensorMap low64) {
+              const __grid_constant__ CUtensorMap rows64, const __grid_constant__ LowMaps<BOTH> low_maps) {
     // the kernel's only shared memory: starts on a multiple of 1 KB, as the swizzle wants it
     extern __shared__ __align__(1024) unsigned char dyn[];
     OrthoShared& sh = *reinterpret_cast<OrthoShared*>(dyn + kStages * kStageBytes + kSlots * kSlotBytes);
@@ -1095,21 +1100,23 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const CUtensorMap *left_map = &rows128, *right128 = &rows128, *right64 = &rows64;
                 const int left_hi = left, right_hi = right, sums = sums_of(prod, both, has_lo);
                 for (int k = 0, kb = 0, sum = 0; k < kblocks * sums; ++k, ++kb) {
-                    if (BOTH && kb == kblocks) {   // the next sum
-                        kb = 0;
-                        // from the blocks of the high half to those of the low one: X's (or, where
-                        // A is the operand, A's) in the first or the second workspace, or B's
-                        const bool second = ((prod == kProdB ? step + 1 : step) & 1) != 0;
-                        const int64_t low = second ? d.lo2 : d.lo;
-                        if (++sum == 1) {
-                            left = left_hi + int(((prod == kProdX ? d.blo : low) - from) * kBlkRows);
-                            left_map = prod == kProdX || second ? &low128 : &rows128;
-                        } else {
-                            left = left_hi;
-                            left_map = &rows128;
-                            right = right_hi + int((low - (prod == kProdX ? x : from)) * kBlkRows);
-                            right128 = second ? &low128 : &rows128;
-                            right64 = second ? &low64 : &rows64;
+                    if constexpr (BOTH) {
+                        if (kb == kblocks) {   // the next sum
+                            kb = 0;
+                            // from the blocks of the high half to those of the low one: X's (or, where
+                            // A is the operand, A's) in the first or the second workspace, or B's
+                            const bool second = ((prod == kProdB ? step + 1 : step) & 1) != 0;
+                            const int64_t low = second ? d.lo2 : d.lo;
+                            if (++sum == 1) {
+                                left = left_hi + int(((prod == kProdX ? d.blo : low) - from) * kBlkRows);
+                                left_map = prod == kProdX || second ? &low_maps.rows128 : &rows128;
+                            } else {
+                                left = left_hi;
+                                left_map = &rows128;
+                                right = right_hi + int((low - (prod == kProdX ? x : from)) * kBlkRows);
+                                right128 = second ? &low_maps.rows128 : &rows128;
+                                right64 = second ? &low_maps.rows64 : &rows64;
+                            }
                         }
                     }
                     if (!(ok = wait_bounded(sh, &sh.empty[s], par, a))) break;
@@ -1642,9 +1649,13 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
                       a.f32 ? 2 * kLoadSmem : kLoadSmem, s, who, a, static_cast<const ConvItem*>(m.d_conv_items));
     if (st == DPG_OK) st = gram_finish(m, update, hp, sch, fault, out, s, who);
     if (st != DPG_OK) return st;
-    const bool both = sch.both_steps > 0;
-    CUtensorMap map[4] = {};
-    std::memcpy(map, m.maps, both ? sizeof map : 2 * sizeof map[0]);
+    CUtensorMap map[2];
+    std::memcpy(map, m.maps, sizeof map);
+    LowMaps<true> low_maps = {};
+    if (sch.both_steps > 0) {
+        std::memcpy(&low_maps.rows128, m.maps[2], sizeof map[0]);
+        std::memcpy(&low_maps.rows64, m.maps[3], sizeof map[0]);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(2 * m.pairs));
     cfg.blockDim = dim3(kOrthoThreads);
@@ -1655,8 +1666,9 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, both ? k_ortho_steps<true> : k_ortho_steps<false>, a, map[0],
-                                             map[1], map[2], map[3]);
+    const cudaError_t e = sch.both_steps > 0
+                              ? cudaLaunchKernelEx(&cfg, k_ortho_steps<true>, a, map[0], map[1], low_maps)
+                              : cudaLaunchKernelEx(&cfg, k_ortho_steps<false>, a, map[0], map[1], LowMaps<false>{});
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
