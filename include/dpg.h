@@ -546,24 +546,25 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * under a power-of-two scale (22 bits), the off-diagonal parts of A and bA + cA^2
  * in one fp16 number, their diagonals and every sum in fp32.  While the a_k
  * (those above 1) multiply to at most 490, as five default ones do, the result is
- * within about 1e-3 (relative Frobenius norm) of the exact one, 3e-3 for
- * matrices of half rank or with repeated rows.  What the roundings leave in
- * directions that U lacks grows by a_k in every step, so in schedules that
- * multiply to more, all steps but the last few hold those parts as pairs too:
- * within 1.5e-3, and what 2^-21 of U's norm in U would change (the product of
- * the a_k times as much in those directions, as in any binary32 iteration).
- * Such steps take two to three times as long, and the first call that has them
- * allocates 1/3 to 2/5 of workspace_bytes more (make it before a capture).  With
- * `precise` every step is one of them: within 2e-4, 2e-5 at full rank.
- * Shorter side up to 128: either this, or the same steps on the Gram matrix
+ * within about 1e-3 (relative Frobenius norm) of the exact one, 2e-3 for matrices
+ * of half rank or with repeated rows (4e-3 if they have hardly more than 128).
+ * What the roundings leave in directions that U lacks grows by a_k in every step,
+ * so in schedules that multiply to more, all steps but the last few hold those
+ * parts as pairs too: within 1.5e-3, and what 2^-20 of U's norm in U would change
+ * (the product of the a_k times as much in those directions, as in any binary32
+ * iteration).  Such steps take two to three times as long, and the first call that
+ * has them allocates 1/3 to 2/5 of workspace_bytes more (make it before a
+ * capture).  With `precise` every step is one of them: within 2e-4 (5e-4 after
+ * sixteen steps), 2e-5 at full rank and five steps.
+ * Shorter side 2 to 64: the same steps on the Gram matrix
  * (A_k+1 = Q_k A_k Q_k, Q_k = aI + b A_k + c A_k^2, X = Q_n-1 .. Q_0 U / norm)
- * in fp32, whichever is faster for the matrices of the object; the choice
- * depends on their shapes and numbers alone, and results are the same bits on
- * every call.  Five default steps are within 1e-6 to 1e-3; steps whose a_k^2
- * multiply to more (2.4e5) start from the new X every few steps and are as near
- * as those on X in fp32 (2e-4, and what 2^-21 of U's norm in U would change: the
- * product of the a_k times as much in directions that U lacks).  Results are
- * rounded to bf16 (1.7e-3).
+ * in fp32; five default steps are within 1e-6 to 1e-3.  Steps whose a_k^2 multiply
+ * to more than 2.4e5 start from the new X every few steps, within 2e-4 and what the
+ * same 2^-20 would change.  Shorter side 65 to 128: this, or pairs in all steps as
+ * above, whichever is faster for the matrices of the object (so for single rows,
+ * which are within 1e-3 either way); the choice depends on their shapes and numbers
+ * alone.
+ * Results are the same bits on every call; they are rounded to bf16 (1.7e-3).
  * A matrix that holds a NaN or an infinity
  * gives NaN everywhere, a zero matrix zeros; other matrices are not affected.
  * Coefficients under which the iteration could leave fp16's range (singular

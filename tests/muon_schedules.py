@@ -38,6 +38,10 @@ def make_low_rank(kind, rows, cols, rng):
     m = min(rows, cols)
     if kind == "rank4":
         u = n((rows, 4)) @ n((4, cols))
+    elif kind == "rank2":
+        u = n((rows, 2)) @ n((2, cols))
+    elif kind == "near1":     # rank one and a hundredth of noise
+        u = n((rows, 1)) @ n((1, cols)) + 0.01 * n((rows, cols))
     elif kind == "half":
         u = n((rows, max(1, m // 2))) @ n((max(1, m // 2), cols))
     elif kind == "tail":      # one singular value 1, the others 1e-4
@@ -65,11 +69,14 @@ def condition(u, coeffs, eps, rng):
     return want, moved / np.linalg.norm(want)
 
 
-def allowed(steps_rel, moved):
+def allowed(steps_rel, moved, elements=1 << 20):
     """The steps' own error and the rounding of the result to bf16 (at most
     2^-8 of a value, under 2^-9 in the root mean square over values of all
     mantissas), which are independent, and the conditioning: the sampled
-    movements stand for others of their size up to a factor of two."""
+    movements stand for others of their size up to a factor of two.  A handful
+    of elements has no mean to speak of: the largest rounding counts."""
+    if elements < 16:
+        return 2.0 ** -8 + steps_rel + 2.0 * moved
     return 1.05 * math.hypot(2.0 ** -9, steps_rel) + 2.0 * moved
 
 

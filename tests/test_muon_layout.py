@@ -19,9 +19,10 @@ def _mats(rows, cols, count):
 
 
 def _tile_bytes(rows, cols, count):
-    """The tiles' blocks: three X and two Gram matrices of fp16, padded to 256."""
+    """The tiles' blocks for a short side of up to 128: four parts of X and three
+    of Gram matrices, of fp16, padded to 256."""
     m, n = -(-min(rows, cols) // 256) * 256, -(-max(rows, cols) // 256) * 256
-    return count * 2 * (3 * m * n + 2 * m * m)
+    return count * 2 * (4 * m * n + 3 * m * m)
 
 
 @pytest.mark.parametrize("rows,cols,count", [(128, 2048, 6000), (2048, 128, 6000), (128, 4096, 3000), (100, 6000, 3000),

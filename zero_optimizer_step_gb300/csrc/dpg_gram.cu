@@ -1,5 +1,5 @@
 // dpg_gram.cu -- orthogonalisation of matrices whose shorter side is at most
-// kSmallSide, unless choose_gram sends them to the tiles (see
+// kGramSide, or kSmallSide where choose_paths sends them here (see
 // dpg_orthogonalize in include/dpg.h).
 //
 // Every Newton-Schulz step multiplies X from the left by a polynomial of its

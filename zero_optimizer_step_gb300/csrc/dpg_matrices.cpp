@@ -63,57 +63,76 @@ static int most_parts(const MatDesc& d) {
 
 static int64_t up256(int64_t x) { return ceil_div(x, 256) * 256; }
 
-// Which matrices of at most kSmallSide rows take the Gram path, by padded side
-// (16, 32, 64, 128): true where five steps of all of them are estimated to take
-// longer as tiles.  The Gram path is three launches of its own: its steps take
-// 12, 17, 30 or 62 us for as many matrices as have their clusters resident, its
-// two passes over the columns up to 2 ns per column, nothing else runs beside
-// it.  Tiles are padded to 256 and their fifteen products follow one another,
-// but as many as there are pairs run at once, and beside larger matrices they
-// only fill gaps.  Where the padded tiles would take more than 16 GB, the path
-// that needs less memory is taken: the copy and one sum per 32 columns or more of
-// the Gram path are a fraction of the tiles for narrow matrices, but up to half
-// as much again for 128 rows.  Measured, Gram path and tiles (us):
-//     1 of 128 x 1000     79   110      1 of 128 x 6000     90   147
-//     15 of 128 x 1000   109   131      16 of 128 x 6000   315   353
-//     16 of 128 x 1000   165   132      64 of 128 x 600    402   191
-//     30 of 100 x 100    142   104      64 of 64 x 2000    166   398
-//     64 x 32 and 32 x 10 20    89      4 of 128 x 50000   434   837
-//     1000 of 16 x 64     65  1254
-// The numbers in the rule (76 pairs, clusters resident at once, times) are those
-// of this GPU, fitted to sets like these; with long schedules each path's share
-// grows alike, so it goes by five steps.
-static void choose_gram(const Plan& p, const int64_t* rows, const int64_t* cols, bool* gram) {
-    static const double steps[4] = {12, 17, 30, 62}, pass[4] = {0.3e-3, 0.5e-3, 1e-3, 2e-3};
-    static const int64_t resident[4] = {1000, 300, 70, 15};
-    int64_t count[4] = {}, columns[4] = {}, longest[4] = {}, blocks[4] = {}, floats[4] = {};
-    double tiles[4] = {};
+// Which matrices of at most kSmallSide rows take the Gram path.  From 2 to 64 rows
+// all do: the tiles, padded to 256, were 10 to 900 us slower, except for one to four
+// short ones of 32 and 64 rows beside larger matrices, 10 to 25 us faster, and use
+// up to eight times the memory.
+//
+// Those of 65 to 128 rows: where five default steps of all of them are estimated to
+// take no longer so.  The Gram path is three launches of its own: its
+// steps take 62 us for as many matrices as have their clusters resident, its two
+// passes over the columns 2 ns per column, and nothing else runs beside it.  The
+// tiles' fifteen products follow one another and take both halves of their operands
+// (see lay_out), but as many tiles as there are pairs run at once, and beside larger
+// matrices they mostly fill gaps.  Measured, Gram path and tiles (us):
+//     1 of 128 x 128      74   127      beside 4 of 768 x 768 (146)   223   152
+//     1 of 128 x 1000     79   181                                   227   213
+//     16 of 128 x 1000   166   204                                   316   231
+//     16 of 128 x 600    152   181                                   299   203
+//     64 of 128 x 600    405   274                                   557   358
+//     30 of 100 x 100    144   145                                   292   261
+//     4 of 128 x 6000    121   268                                   270   280
+// (In 48 such sets, alone and beside five lists, the rule picks the slower path
+// twice, by 15 and 26 us of 700 and 2080.)  The numbers in the rule (76 pairs, 15
+// clusters, times) are this GPU's; with long schedules both paths' times grow alike.
+// Where the tiles would take more than 16 GB, the path of less memory is taken.
+//
+// Single rows have no off-diagonal parts that would need both halves.  A few beside
+// matrices on the tiles stay there and save the Gram path's launches (1 x 777 beside
+// four of 517 to 1031 rows: 175 against 185 us).
+struct Paths {
+    bool gram_rows;    // single rows take the Gram path
+    bool gram_large;   // 65 to 128 rows do
+    bool gram(int64_t m) const {
+        return m == 1 ? gram_rows : m <= kGramSide || (m <= kSmallSide && gram_large);
+    }
+};
+static Paths choose_paths(const Plan& p, const int64_t* rows, const int64_t* cols) {
+    int64_t count = 0, columns = 0, longest = 0, blocks = 0, floats = 0;
+    double tiles = 0, single = 0, single_sum = 0;
     bool larger = false;
     for (int32_t q = 0; q < p.n_params; ++q) {
         const int64_t m = std::min(rows[q], cols[q]), n = std::max(rows[q], cols[q]);
         const int64_t k = p.numels[q] / (rows[q] * cols[q]);
         if (k == 0) continue;
-        if (m > kSmallSide) {
-            larger = true;
-            continue;
-        }
-        const int s = padded_side(m), c = s == 16 ? 0 : s == 32 ? 1 : s == 64 ? 2 : 3;
+        larger = larger || m > kSmallSide;
         const double deep = double(ceil_div(n, kBlkCols)), wide = double(ceil_div(n, kOrthoTile));
-        count[c] += k;
-        columns[c] += k * n;
-        longest[c] = std::max(longest[c], n);
-        blocks[c] += k * 8 * (3 * ceil_div(n, kOrthoTile) + 2);   // as lay_out counts them
-        floats[c] += k * (ceil_div(n, 32) * 32 * s + (ceil_div(n, gram_width(n)) + 1) * s * s);   // and small_items
-        tiles[c] += double(k) * 5.0 * (std::max(0.3 * deep, 3.0) + 3.0 + 3.0 * wide) / 76.0;
+        if (m == 1) {
+            single += double(k) * 5.0 * (std::max(0.3 * deep, 3.0) + 3.0 + 3.0 * wide) / 76.0;
+            single_sum = std::max(single_sum, 0.3 * deep);
+        }
+        if (m <= kGramSide || m > kSmallSide) continue;
+        count += k;
+        columns += k * n;
+        longest = std::max(longest, n);
+        blocks += k * 8 * (4 * ceil_div(n, kOrthoTile) + 3);   // as lay_out counts them
+        floats += k * (ceil_div(n, 32) * 32 * kSmallSide +     // as small_items
+                       (ceil_div(n, gram_width(n)) + 1) * kSmallSide * kSmallSide);
+        // in units of a pair's time: three sums each, or the finish of a block in 1, 2 or 3 visits
+        tiles += double(k) * 5.0 * (std::max(0.9 * deep, 5.0) + 9.0 + 6.0 * wide) / 76.0;
     }
-    for (int c = 3; c >= 0; --c) {
-        const double one = larger ? 0.0 : 90.0 + 1.5 * double(ceil_div(longest[c], kBlkCols));
-        gram[c] = blocks[c] * kBlkBytes > (int64_t(16) << 30)
-                      ? floats[c] * int64_t(sizeof(float)) < blocks[c] * kBlkBytes
-                      : steps[c] * double(ceil_div(count[c], resident[c])) + 10.0 + pass[c] * double(columns[c]) <=
-                            one + tiles[c];
-        larger = larger || (count[c] > 0 && !gram[c]);
+    Paths out;
+    if (blocks * kBlkBytes > (int64_t(16) << 30)) {
+        out.gram_large = floats * int64_t(sizeof(float)) < blocks * kBlkBytes;
+    } else {
+        const double deep = double(ceil_div(longest, kBlkCols));
+        out.gram_large = 62.0 * double(ceil_div(count, 15)) + 10.0 + 2e-3 * double(columns) <=
+                         (larger ? 10.0 + deep : 120.0 + 2.0 * deep) + tiles;
     }
+    const bool on_tiles = larger || (count > 0 && !out.gram_large);
+    // (the Gram path's launches take about 13 us; a tile's sum may take as long as others' do)
+    out.gram_rows = !on_tiles || single > 10.0 || single_sum > 10.0;
+    return out;
 }
 
 // Lays the matrices out; false when an index would leave its type.
@@ -128,15 +147,10 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
         if ((count += p.numels[q] / (rows[q] * cols[q])) > kMaxMatrices) return false;
     // Items of the norm pass: as long as leaves about four per SM (each costs a fence and an
     // atomic besides its loads)
-    bool gram[4];
-    choose_gram(p, rows, cols, gram);
-    auto by_gram = [&](int64_t m) {
-        const int s = m <= kSmallSide ? padded_side(m) : 0;
-        return s && gram[s == 16 ? 0 : s == 32 ? 1 : s == 64 ? 2 : 3];
-    };
+    const Paths paths = choose_paths(p, rows, cols);
     int64_t tiled = 0;
     for (int32_t q = 0; q < p.n_params; ++q)
-        if (!by_gram(std::min(rows[q], cols[q]))) tiled += p.numels[q];
+        if (!paths.gram(std::min(rows[q], cols[q]))) tiled += p.numels[q];
     const int64_t norm_chunk = kNormChunk * std::clamp<int64_t>(ceil_div(tiled, 608 * int64_t(kNormChunk)), 1, 8);
     for (int32_t q = p.n_params - 1; q >= 0; --q) {   // flat order
         const double r = double(rows[q]), c = double(cols[q]);
@@ -156,7 +170,7 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.m = int32_t(std::min(rows[q], cols[q]));
             d.n = int32_t(std::max(rows[q], cols[q]));
             ++M.n_matrices;
-            if (by_gram(d.m)) {
+            if (paths.gram(d.m)) {
                 small_items(M, d);
                 continue;
             }
@@ -174,9 +188,16 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
             d.a = d.lo + xb;
             d.b = d.a + ab;
             M.n_blocks = d.b + ab;
-            d.lo2 = M.n_low_blocks;
+            // Few rows average little of the rounding that fp16 off-diagonal parts
+            // leave: five default steps on rank one end 5 % off at 2 to 4 rows, 1 % at
+            // 16, 5e-3 at 32, and every row twice 4e-3 at 128.  Both halves in all
+            // steps leave 1e-4; their blocks are few.
+            d.both = d.m > 1 && d.m <= kSmallSide;
+            M.any_both = M.any_both || d.both;
+            int64_t& low = d.both ? M.n_blocks : M.n_low_blocks;
+            d.lo2 = low;
             d.blo = d.lo2 + xb;
-            M.n_low_blocks = d.blo + ab;   // (fewer than n_blocks)
+            low = d.blo + ab;              // (n_low_blocks stays below n_blocks)
             // a block's first 128-byte row is a 32-bit coordinate of the copies
             if (M.n_blocks * kBlkRows > 0x7FFFFFFFll) return false;
             d.diag = M.n_diag;
@@ -439,8 +460,8 @@ static void gram_phases(const double* growth, int n_steps, bool precise, OrthoSc
 // Which steps of the tiles take both halves of their operands.  In directions
 // that X lacks, what a step's roundings leave there is multiplied by the a_k of
 // the steps after it.  With fp16 halves alone (3e-4 a step) five default steps
-// end within 2.7e-3 whatever the matrix, six at 6e-3 and eight at 7e-2 (every
-// row twice, or rank m / 2).  Where the a_k multiply to more than those five
+// end within 2.7e-3 for 256 rows and more whatever the matrix (4e-3 for 129), six
+// at 6e-3 and eight at 7e-2 (every row twice, or rank m / 2).  Where the a_k multiply to more than those five
 // (485), the steps with more than 4 still to come -- all but the last two of
 // default ones -- take both: the end is within 1.3e-3 again.  Such a step takes
 // two to three times as long (eight GPT-2-small attention matrices 88 us
@@ -455,12 +476,6 @@ static void both_halves(const dpg_muon_hparams* hp, OrthoSchedule* sch) {
             break;
         }
         to_come *= std::max(1.0, std::fabs(hp->coeffs[k][0]));
-    }
-    // The low half is kept times 2048 where only the steps' own sums read it,
-    // and as it is where products read it beside the high half.
-    for (int k = 0; k < hp->n_steps; ++k) {
-        sch->st[k].inv_lo = k < sch->both_steps ? 1.0f : 1.0f / kLoScale;
-        sch->st[k].lo_next = k + 1 < sch->both_steps ? 1.0f : kLoScale;
     }
 }
 

@@ -41,9 +41,9 @@
 // row stands twice, whose diagonals in fp32 and off-diagonal parts in fp16 do
 // not cancel exactly.
 //
-// What they leave grows with the a of every step to come.  In the early steps
-// of schedules that multiply it by more (both_halves), A and B are pairs of
-// fp16 numbers too and the products take hi hi + lo hi + hi lo, as three sums
+// What they leave grows with the a of every step to come, and is more where few
+// rows average it.  In the early steps of schedules that multiply it by more
+// (both_halves), and in all steps for up to 128 rows, A and B are pairs of fp16 numbers too and the products take hi hi + lo hi + hi lo, as three sums
 // in one accumulator; t is 1.  That leaves 5e-6 (256 x 512) to 2e-5 (512 x 1024)
 // at full rank, 1e-4 at low rank, as binary32 does, for two to three times the
 // time.
@@ -70,7 +70,6 @@ struct OrthoArgs {
     unsigned char* ws;       // blocks
     unsigned char* ws_low;   // blocks of the second workspace
     int32_t both_steps;      // the first so many steps take both halves
-    float lo_scale, inv_lo_scale;   // of X_0's low half
     float* diag_a;           // per row: A_rr
     float* diag_b;           // B_rr
     float* diag_t;           // t_r B_rr
@@ -313,9 +312,20 @@ __device__ __forceinline__ void split16(float u, float rounded, float scale, uin
     lo = __half_as_ushort(__float2half_rn((u - __half2float(h)) * scale));
 }
 
+// How many of the call's steps take both halves of a matrix's operands.
+__device__ __forceinline__ int both_steps_of(const OrthoArgs& a, const MatDesc& d) {
+    return d.both ? a.n_steps : a.both_steps;
+}
+// What X's low half is multiplied by as step `step` reads it: 2048 where only
+// its own sums do, 1 where products read it beside the high half.
+__device__ __forceinline__ float lo_scale_of(const OrthoArgs& a, const MatDesc& d, int step) {
+    return step < both_steps_of(a, d) ? 1.0f : kLoScale;
+}
+
 template <bool F32, bool TALL>
 __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d, const ConvItem& it,
                                             uint16_t* sm) {
+    const float lo_scale = lo_scale_of(a, d, 0), inv_lo_scale = 1.0f / lo_scale;
     const float sc = a.scal[it.mat].x;
     const int64_t blk = int64_t(it.i) * d.cbx + it.j * 2;
     unsigned char* hi = a.ws + (d.x[0] + blk) * kBlkBytes;
@@ -350,7 +360,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 for (int j = 0; j < 8; ++j) {
                     const float u = in ? x[j] * sc : 0.0f;
                     uint16_t h, l;
-                    split16(u, F32 ? u * RoundScale(1.0f, r + j + c).v[0] : u, a.lo_scale, h, l);
+                    split16(u, F32 ? u * RoundScale(1.0f, r + j + c).v[0] : u, lo_scale, h, l);
                     sm[(r + j) * kLoadPitch + c] = h;
                     if (F32) sm_lo[(r + j) * kLoadPitch + c] = l;
                 }
@@ -361,7 +371,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 const float u = c0 + c < n && r0 + r < m
                                     ? load_update<F32>(a, off + int64_t(c0 + c) * m + r0 + r) * sc : 0.0f;
                 uint16_t h, l;
-                split16(u, F32 ? u * RoundScale(1.0f, r + c).v[0] : u, a.lo_scale, h, l);
+                split16(u, F32 ? u * RoundScale(1.0f, r + c).v[0] : u, lo_scale, h, l);
                 sm[r * kLoadPitch + c] = h;
                 if (F32) sm_lo[r * kLoadPitch + c] = l;
             }
@@ -392,7 +402,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 f = unpack_half2(h[j]), g = unpack_half2(l[j]);
-                const float u = fmaf(g.x, a.inv_lo_scale, f.x), v = fmaf(g.y, a.inv_lo_scale, f.y);
+                const float u = fmaf(g.x, inv_lo_scale, f.x), v = fmaf(g.y, inv_lo_scale, f.y);
                 sq = fmaf(u, u, fmaf(v, v, sq));
             }
         } else {
@@ -410,7 +420,7 @@ __device__ __forceinline__ void load_blocks(const OrthoArgs& a, const MatDesc& d
                 // a scaled bf16 value is an fp16 value: nothing to round, lo is 0
                 h[j] = F32 ? pack_half2(u * rs.v[2 * j & 3], v * rs.v[(2 * j + 1) & 3]) : pack_half2(u, v);
                 const float2 f = unpack_half2(h[j]);
-                l[j] = pack_half2((u - f.x) * a.lo_scale, (v - f.y) * a.lo_scale);
+                l[j] = pack_half2((u - f.x) * lo_scale, (v - f.y) * lo_scale);
             }
             h4 = make_uint4(h[0], h[1], h[2], h[3]);
             l4 = make_uint4(l[0], l[1], l[2], l[3]);
@@ -932,7 +942,8 @@ __device__ __forceinline__ void write_out(const OrthoArgs& a, const MatDesc& d, 
 // from buffer to buffer through the steps that take both halves.
 template <bool BOTH>
 __device__ __forceinline__ unsigned char* low_half(const OrthoArgs& a, const MatDesc& d, int step) {
-    return BOTH && (min(step, a.both_steps) & 1) ? a.ws_low + d.lo2 * kBlkBytes : a.ws + d.lo * kBlkBytes;
+    return BOTH && (min(step, both_steps_of(a, d)) & 1) ? (d.both ? a.ws : a.ws_low) + d.lo2 * kBlkBytes
+                                                        : a.ws + d.lo * kBlkBytes;
 }
 
 // The count that must have been reached before a tile of (prod, step) starts.
@@ -1020,8 +1031,7 @@ __device__ __noinline__ bool join_parts(OrthoShared& sh, const OrthoArgs& a, con
     return true;
 }
 
-// BOTH: some steps take both halves of their operands (their code beside the
-// other made that slower).  X's low part is then an operand that other tiles
+// BOTH: some steps of some matrices take both halves of their operands.  X's low part is then an operand that other tiles
 // read, so it alternates between two buffers as X does; the free one holds A's
 // low part while that is needed.
 template <bool BOTH>
@@ -1081,11 +1091,12 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t par = 1;             // the first pass over the ring finds it empty
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool both = BOTH && step < a.both_steps, has_lo = step > 0 || a.f32;
+            const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
                 const int prod = tile.prod;
+                const bool both = BOTH && step < both_steps_of(a, d);
                 const int64_t x = d.x[step & 1];
                 const int64_t from = prod == kProdA ? x : prod == kProdB ? d.a : d.b;
                 const int cb = prod == kProdA ? d.cbx : d.cba, kblocks = part_of_sum(d, tile, tile.part).y;
@@ -1107,15 +1118,16 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                             // A is the operand, A's) in the first or the second workspace, or B's
                             const bool second = ((prod == kProdB ? step + 1 : step) & 1) != 0;
                             const int64_t low = second ? d.lo2 : d.lo;
+                            const CUtensorMap* low128 = d.both ? &rows128 : &low_maps.rows128;
                             if (++sum == 1) {
                                 left = left_hi + int(((prod == kProdX ? d.blo : low) - from) * kBlkRows);
-                                left_map = prod == kProdX || second ? &low_maps.rows128 : &rows128;
+                                left_map = prod == kProdX || second ? low128 : &rows128;
                             } else {
                                 left = left_hi;
                                 left_map = &rows128;
                                 right = right_hi + int((low - (prod == kProdX ? x : from)) * kBlkRows);
-                                right128 = second ? &low_maps.rows128 : &rows128;
-                                right64 = second ? &low_maps.rows64 : &rows64;
+                                right128 = second ? low128 : &rows128;
+                                right64 = second && !d.both ? &low_maps.rows64 : &rows64;
                             }
                         }
                     }
@@ -1144,10 +1156,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t par = 0;
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool both = BOTH && step < a.both_steps, has_lo = step > 0 || a.f32;
+            const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
+                const bool both = BOTH && step < both_steps_of(a, d);
                 const bool by_column = tile.prod == kProdX;
                 const uint32_t shape = mma_shape(by_column, tile.blocks * 64);
                 const int kblocks = part_of_sum(d, tile, tile.part).y * sums_of(tile.prod, both, has_lo);
@@ -1178,10 +1191,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         int before = 2;               // blocks of the tile before
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool has_lo = step > 0 || a.f32, both = BOTH && step < a.both_steps;
+            const bool has_lo = step > 0 || a.f32;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
+                const bool both = BOTH && step < both_steps_of(a, d);
                 const int prod = tile.prod, blocks = tile.blocks >> tile.split;   // (parts: of A, which reads no blocks)
                 const int64_t blk = int64_t(tile.i * 2 + int(rank)) * (prod == kProdX ? d.cbx : d.cba) + tile.j * blocks;
                 const unsigned char* in = a.ws + ((prod == kProdB ? d.a : d.x[step & 1]) + blk) * kBlkBytes;
@@ -1221,10 +1235,11 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         uint32_t n = 0;               // as above
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
-            const bool last = step + 1 == a.n_steps, both = BOTH && step < a.both_steps;
+            const bool last = step + 1 == a.n_steps;
             for (int t = q0; t < q1 && ok; ++t) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
+                const bool both = BOTH && step < both_steps_of(a, d);
                 const int prod = tile.prod, blocks = tile.blocks >> tile.split, visits = visits_of(prod, both);
                 const int c0 = tile.j * tile.blocks + tile.part * blocks;
                 const bool mirror = prod != kProdX && (c0 >> 2) > tile.i;
@@ -1234,8 +1249,9 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 unsigned char* out = a.ws + ((prod == kProdA ? d.a : prod == kProdB ? d.b : d.x[(step + 1) & 1]) +
                                              blk) * kBlkBytes;
                 // where the low half goes: X's, or A's beside it, or B's
-                unsigned char* low = BOTH && both && prod == kProdB ? a.ws_low + d.blo * kBlkBytes
-                                                                    : low_half<BOTH>(a, d, step + 1);
+                unsigned char* low = BOTH && both && prod == kProdB
+                                         ? (d.both ? a.ws : a.ws_low) + d.blo * kBlkBytes
+                                         : low_half<BOTH>(a, d, step + 1);
                 unsigned char* lo = low + blk * kBlkBytes;
                 const int64_t image_at = int64_t(tile.i * 4 + int(rank) * 2) * kBlkBytes;
                 unsigned char* image = a.ws + (prod == kProdA ? d.a : d.b) * kBlkBytes + image_at;
@@ -1285,9 +1301,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
         bool ok = true;
         for (int step = 0; step < a.n_steps && ok; ++step) {
             const OrthoStep s = a.st[step];
-            const bool last = step + 1 == a.n_steps, both = BOTH && step < a.both_steps;
+            const bool last = step + 1 == a.n_steps;
             const bool has_lo = step > 0 || a.f32;
-            const float inv_lo = BOTH ? s.inv_lo : kInvLoScale, lo_next = BOTH ? s.lo_next : kLoScale;
             for (int t = q0; t < q1 && ok; ++t, ++it) {
                 const OrthoTile tile = a.queue[t];
                 const MatDesc& d = a.mats[tile.mat];
@@ -1296,6 +1311,8 @@ k_ortho_steps(const __grid_constant__ OrthoArgs a, const __grid_constant__ CUten
                 const int c0 = (tile.j * tile.blocks + first) * 64;
                 const int r0 = tile.i * kOrthoTile + int(rank) * 128 + row0, r = r0 + lane;
                 const int64_t diag_at = d.diag;
+                const bool both = BOTH && step < both_steps_of(a, d);
+                const float inv_lo = both ? 1.0f : kInvLoScale, lo_next = BOTH ? lo_scale_of(a, d, step + 1) : kLoScale;
                 const bool mirror = prod != kProdX && (c0 >> 8) > tile.i;
                 ok = wait_bounded(sh, &sh.tile_ready, uint32_t(it & 1), a);
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
@@ -1470,7 +1487,6 @@ int upload_for_update(Matrices& m) {
 // held, the tables are there.
 static int upload_low(Matrices& m) {
     if (m.ws_low || m.n_low_blocks == 0) return DPG_OK;
-    DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
     void* low = nullptr;
     const cudaError_t e = cudaMalloc(&low, size_t(m.n_low_blocks * kBlkBytes));
     if (e != cudaSuccess) {
@@ -1501,6 +1517,7 @@ int upload_matrices(Matrices& m, bool both) {
     if (!m.mats.empty()) {
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_load<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           2 * kLoadSmem));
+        DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
         DPG_CUDA_TRY(cudaFuncSetAttribute(k_ortho_steps<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthoSmem));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
@@ -1634,8 +1651,6 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     a.queue_first = m.d_queue_first;
     a.ws_low = m.ws_low;
     a.both_steps = sch.both_steps;
-    a.inv_lo_scale = sch.st[0].inv_lo;
-    a.lo_scale = 1.0f / a.inv_lo_scale;
     a.n_steps = hp->n_steps;
     a.eps = hp->eps;
     int exp = 0;
@@ -1652,7 +1667,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     CUtensorMap map[2];
     std::memcpy(map, m.maps, sizeof map);
     LowMaps<true> low_maps = {};
-    if (sch.both_steps > 0) {
+    if (m.ws_low) {
         std::memcpy(&low_maps.rows128, m.maps[2], sizeof map[0]);
         std::memcpy(&low_maps.rows64, m.maps[3], sizeof map[0]);
     }
@@ -1666,7 +1681,7 @@ int ortho_launch(Matrices& m, const void* update, int32_t update_dtype, const dp
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = sch.both_steps > 0
+    const cudaError_t e = sch.both_steps > 0 || m.any_both
                               ? cudaLaunchKernelEx(&cfg, k_ortho_steps<true>, a, map[0], map[1], low_maps)
                               : cudaLaunchKernelEx(&cfg, k_ortho_steps<false>, a, map[0], map[1], LowMaps<false>{});
     if (e != cudaSuccess) {

@@ -36,7 +36,9 @@ struct MatDesc {
     int32_t cbx, cba;     // 64-column blocks in a row of X, of A
     int64_t x[2], lo;     // first block of the two X buffers and of X's low part
     int64_t a, b;         // first block of A and of bA + cA^2 (off-diagonal parts)
-    int64_t lo2, blo;     // in the second workspace: first block of X's other low part, of B's low part
+    int64_t lo2, blo;     // first block of X's other low part, of B's low part: in the second
+                          // workspace, or in the first if `both`
+    int32_t both;         // all steps take both halves (see lay_out)
     int64_t diag;         // first entry of the per-row vectors (see OrthoArgs)
     int64_t rowsq;        // first entry of X's row sums of squares, [cbx][padded rows]
     int32_t rows_pad;     // rows of X padded to 256
@@ -59,8 +61,10 @@ struct alignas(16) OrthoTile {
 };
 static_assert(sizeof(OrthoTile) == 16, "one load");
 
-// Matrices whose shorter side is at most kSmallSide may take the steps on their
-// Gram matrices (dpg_gram.cu) and none of the tiles (see choose_gram).
+// Matrices whose shorter side is at most kGramSide take the steps on their Gram
+// matrices (dpg_gram.cu) and none of the tiles, those of up to kSmallSide where that
+// is faster (see choose_paths).
+constexpr int kGramSide = 64;
 constexpr int kSmallSide = 128;
 struct SmallDesc {
     int64_t off;          // first element in the flat buffer
@@ -111,8 +115,6 @@ struct OrthoStep {
     float sx_next;     // scale of the new X
     float sa, inv_sa;  // scale of A
     float sb, inv_sb;  // scale of bA + cA^2
-    float inv_lo;      // 1 / what X's low part is multiplied by as it is read
-    float lo_next;     // and what as it is written
 };
 
 // The steps of a call, and where the Gram path sums its matrices anew.
@@ -140,6 +142,7 @@ struct Matrices {
     std::vector<ConvItem> conv_items;
     std::vector<ApplyItem> apply_items;
     std::vector<double> scales;        // 2 per parameter: spectral, rms
+    bool any_both = false;             // one of mats is `both`
     int64_t n_low_blocks = 0;          // of the second workspace
     int64_t n_blocks = 0, n_diag = 0, n_rowsq = 0, n_groups = 0;
     int64_t n_small_copy = 0, n_small_part = 0, n_small_prod = 0;   // floats
