@@ -547,7 +547,9 @@ int dpg_muon_momentum(const dpg_plan_t* plan, const void* const* grads, int32_t 
  * in one fp16 number, their diagonals and every sum in fp32.  While the a_k
  * (those above 1) multiply to at most 490, as five default ones do, the result is
  * within about 1e-3 (relative Frobenius norm) of the exact one, 2e-3 for matrices
- * of half rank or with repeated rows (4e-3 if they have hardly more than 128).
+ * of half rank or with repeated rows (4e-3 if they have hardly more than 128), and
+ * within 5e-3 to 1e-2 (fp32 updates: 5e-2) for one that is zero but for 64 to 2 rows
+ * (of the shorter side) that depend on one another: take `precise` for such.
  * What the roundings leave in directions that U lacks grows by a_k in every step,
  * so in schedules that multiply to more, all steps but the last few hold those
  * parts as pairs too: within 1.5e-3, and what 2^-20 of U's norm in U would change

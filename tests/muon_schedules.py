@@ -27,6 +27,9 @@ SCHEDULES = {
 # Relative Frobenius error of the steps alone: any matrix at up to five default
 # steps; longer schedules.
 STEPS_REL = 3e-3
+# five default steps where all but a few rows are zero and those depend on one
+# another: bf16 updates, fp32 ones
+FEW_ROWS_REL = {True: 1.2e-2, False: 6e-2}
 LONG_REL = 1.5e-3
 # The steps are those of a matrix this close to the given one (relative): what
 # the fp32 sums and the 22 bits of X can move.
@@ -40,6 +43,11 @@ def make_low_rank(kind, rows, cols, rng):
         u = n((rows, 4)) @ n((4, cols))
     elif kind == "rank2":
         u = n((rows, 2)) @ n((2, cols))
+    elif kind.startswith("rows"):   # rank two in the first rows of the shorter side, zero elsewhere
+        h = int(kind[4:])
+        u = np.zeros((m, max(rows, cols)))
+        u[:h] = n((h, 2)) @ n((2, max(rows, cols)))
+        u = u if rows <= cols else u.T
     elif kind == "near1":     # rank one and a hundredth of noise
         u = n((rows, 1)) @ n((1, cols)) + 0.01 * n((rows, cols))
     elif kind == "half":

@@ -25,7 +25,7 @@ def built():
 @pytest.mark.parametrize("rows,cols", [(256, 512), (700, 300), (151, 333), (100, 300), (40, 16), (200, 9000)])
 def test_precise(rows, cols, dtype, name):
     kinds = [("gauss", FULL_RANK), ("spiked", FULL_RANK), ("half", LOW_RANK), ("rank4", LOW_RANK),
-             ("repeated", LOW_RANK)]
+             ("repeated", LOW_RANK), ("rows4", LOW_RANK), ("rows16", LOW_RANK)]
     rng = np.random.Generator(np.random.Philox(61))
     n = rows * cols
     plan = dpg.dpg_plan_buckets([n * len(kinds)], 1 << 40, 1)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import zero_optimizer_step_gb300 as dpg
-from muon_schedules import LONG_REL, SCHEDULES, STEPS_REL, allowed, condition, make_low_rank, to_dtype
+from muon_schedules import FEW_ROWS_REL, LONG_REL, SCHEDULES, STEPS_REL, allowed, condition, make_low_rank, to_dtype
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -146,3 +146,14 @@ def test_single_rows_on_both_paths(n, name):
     for dtype in (torch.bfloat16, torch.float32):
         _check([(1, n, 2), (n, 1, 1)], ["gauss"], name, dtype, LONG_REL, tiles=False)
         _check([(300, 400, 1), (1, n, 2), (n, 1, 1)], ["gauss"], name, dtype, LONG_REL, tiles=n < 4000)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_few_dependent_rows(dtype):
+    # what five default steps leave in the largest case known (see dpg.h); long
+    # schedules' early steps, and short sides, have both halves
+    kinds = ["rows3", "rows4", "rows8", "rows16"]
+    _check([(256, 512, 4)], kinds, "5", dtype, FEW_ROWS_REL[dtype == torch.bfloat16], tiles=True)
+    _check([(700, 300, 4)], kinds, "8", dtype, LONG_REL, tiles=True)
+    _check([(100, 300, 4)], kinds, "5", dtype, LONG_REL, tiles=False)
+    _check([(300, 400, 1), (100, 622, 4)], ["gauss"] + kinds, "5", dtype, LONG_REL, tiles=True)
