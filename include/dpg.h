@@ -593,6 +593,132 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
                   float* master, float* momentum, void* update, int32_t update_dtype,
                   void* const* param_views, int32_t n_views, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit floating point: quantised matrices and their products (no counterpart
+ * on the pages: a narrower form of the parameters than bf16 for the layers
+ * that read what the step writes, and of the activations and gradients beside
+ * them; OCP Microscaling Formats 1.0 defines E2M1 and E8M0)
+ *
+ * A quantised matrix holds rows x cols elements in blocks along its rows:
+ *   DPG_NVFP4  16 elements to an E4M3 scale, and one power of two 2^e for the
+ *              whole matrix: value = 2^e * scale * code
+ *   DPG_MXFP4  32 elements to an E8M0 scale: value = scale * code
+ * with codes E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign).  Values are exact in
+ * bf16 and fp32 down to their subnormal numbers.
+ * A block's scale is the least of its type with max|x| <= 6 * scale * 2^e, so
+ * no element saturates; e is the least with amax <= 6 * 448 * 2^e and e >=
+ * -126, amax the largest finite |x| of the matrix.  A block that holds a NaN
+ * or an infinity has a NaN for its scale, and so NaN for its values; other
+ * blocks are not affected.
+ *
+ * dpg_fp4: the caller's buffers of one quantised matrix.
+ *   codes   code_bytes, 16-byte aligned: row r at r * 16 * ceil(cols / 32),
+ *           element 2 j in the low half of byte j; zeros behind the last
+ *   scales  scale_bytes, 16-byte aligned: tiles of 128 rows x 4 blocks, 512
+ *           bytes each, tile (i, j) at (i * ceil(blocks / 4) + j) * 512, in it
+ *           row r, block b at (r % 32) * 16 + (r / 32) * 4 + b; zeros behind
+ *           the last row and block (the layout that the tensor cores copy)
+ *   amax    one float, DPG_NVFP4 only (the largest finite |x|, from which a
+ *           reader derives e); may be NULL for DPG_MXFP4
+ * 0 <= rows, cols <= 2^30.
+ * dpg_fp4_sizes: bytes of its codes and scales (either pointer may be NULL).
+ * ------------------------------------------------------------------------- */
+#define DPG_NVFP4 0
+#define DPG_MXFP4 1
+typedef struct {
+    void* codes;
+    void* scales;
+    float* amax;
+    int64_t rows, cols;
+    int32_t format;
+} dpg_fp4;
+int dpg_fp4_sizes(int64_t rows, int64_t cols, int32_t format, int64_t* code_bytes,
+                  int64_t* scale_bytes);
+
+/* Quantises x (rows x cols of DPG_BF16 or DPG_F32, row i at x + i * row_stride
+ * elements, aligned to its element; row_stride >= cols, or any for one row)
+ * into by_row, a rows x cols matrix, and by_col, its transpose (cols x rows,
+ * in blocks of their own along x's columns).  Either may be NULL, not both;
+ * where both are given they have one format and buffers of their own.
+ * seed == NULL: codes are the nearest, ties to the even one.
+ * seed: DEVICE pointer to one int64, read when the kernels run (so that a
+ *   replayed graph takes the seed of the day).  |x| between neighbouring
+ *   values lo and hi = lo + gap becomes hi if
+ *     |x| - lo > (2 u + 1) 2^-17 gap,
+ *   u the 16 random bits of the element: of Philox4x32-10 (Salmon et al. 2011)
+ *   with the seed as key and counter {n mod 2^32, n / 2^32, side, 0}, n = r *
+ *   ceil(cols / 8) + c / 8 in the quantised matrix's own rows and columns, half
+ *   word c mod 8 (low halves first), side 0 for by_row and 1 for by_col.
+ * Results are the same bits on every call. */
+int dpg_fp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
+                     int64_t row_stride, const int64_t* seed, const dpg_fp4* by_row,
+                     const dpg_fp4* by_col, void* stream);
+
+/* out (rows x cols of DPG_BF16 or DPG_F32, row i at out + i * row_stride
+ * elements, aligned to its element) = the values of q. */
+int dpg_fp4_dequantize(const dpg_fp4* q, void* out, int32_t out_dtype, int64_t row_stride,
+                       void* stream);
+
+/* The 4-bit form of every matrix of a plan (beside dpg_allgather_params, which
+ * writes bf16 views): matrix k, in the order of the parameters and of the
+ * matrices of a stack, from its place in the flat fp32 masters.  by_row and
+ * by_col: HOST arrays of n = the object's number of matrices, either may be
+ * NULL, not both; entry k must have matrix k's rows and cols (by_col: cols and
+ * rows).  seed as in dpg_fp4_quantize; matrix k takes the seed plus k.  All
+ * arguments are checked before anything is launched. */
+int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, const int64_t* seed,
+                             const dpg_fp4* by_row, const dpg_fp4* by_col, int32_t n, void* stream);
+
+/* c = a b^T, or c + a b^T with accumulate != 0 (DPG_F32 only): a is m x k, b
+ * n x k, of one format; c m x n of c_dtype (DPG_BF16, rounded to nearest even,
+ * or DPG_F32), row i at c + i * row_stride elements, aligned to its element;
+ * row_stride >= n (any for one row).  Of one layer with weight W (out x in):
+ *   y  = x W^T      a = x by row,        b = W by row
+ *   dx = dy W       a = dy by row,       b = W by column
+ *   dW = dy^T x     a = dy by column,    b = x by column
+ * with c a slice of a flat gradient buffer or of an fp32 accumulator.
+ * Products and sums on the tensor cores in fp32; k = 0 gives zeros (or c).
+ * Results are the same bits on every call.  c may not overlap a or b.
+ * Every device-side wait is bounded (2 s); one that runs out leaves c
+ * incomplete and records DPG_ERR_DEVICE_TIMEOUT for the device. */
+int dpg_fp4_product(const dpg_fp4* a, const dpg_fp4* b, void* c, int32_t c_dtype,
+                    int64_t row_stride, int32_t accumulate, void* stream);
+/* Synchronises `stream` and returns the current device's record of such a wait
+ * (DPG_OK if there is none), clearing it. */
+int dpg_fp4_status(void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm (Ba et al. 2016) and its gradients (no counterpart on the pages:
+ * the small parameters of a plan are its gains and biases, and this leaves
+ * their gradients where the step reads them)
+ * x, y, dy, dx: rows x cols of `dtype` (DPG_BF16 or DPG_F32), rows back to
+ * back, aligned to their element.  gain, bias: cols elements of param_dtype.
+ *   mean_r = sum_c x / cols,  rstd_r = 1 / sqrt(sum_c (x - mean_r)^2 / cols + eps)
+ *   n = (x - mean_r) * rstd_r,  y = n * gain + bias
+ * in fp32, y rounded once.  gain may be NULL (ones), bias may be NULL (zeros).
+ * mean, rstd: `rows` floats, written for the backward pass; both NULL: not kept.
+ * y may be x.  eps: finite, >= 0.
+ * ------------------------------------------------------------------------- */
+int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, const void* gain,
+                   const void* bias, int32_t param_dtype, double eps, void* y, float* mean,
+                   float* rstd, void* stream);
+/* With g = dy * gain:
+ *   dx = rstd_r * (g - sum_c g / cols - n * sum_c (g * n) / cols)
+ *   dgain_c = sum_r dy * n,  dbias_c = sum_r dy
+ * each of dx, dgain, dbias may be NULL (not computed); dx may be dy or x.
+ * dgain, dbias: cols elements of grad_dtype (DPG_BF16: rounded once; DPG_F32),
+ * aligned to their element, so they may be slices of a replica's flat gradient
+ * buffer; accumulate != 0 (DPG_F32 only) adds to what they hold.  The sums over
+ * the rows are in fp32, in an order fixed by the sizes: the same bits on every
+ * call.  workspace: DEVICE memory of dpg_layer_norm_workspace(rows, cols) bytes,
+ * 16-byte aligned (may be NULL if dgain and dbias are), used by one call at a time; it
+ * need not be initialised.  rows = 0 gives zero sums. */
+int64_t dpg_layer_norm_workspace(int64_t rows, int64_t cols);
+int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t rows,
+                            int64_t cols, const void* gain, int32_t param_dtype, const float* mean,
+                            const float* rstd, void* dx, void* dgain, void* dbias,
+                            int32_t grad_dtype, int32_t accumulate, void* workspace, void* stream);
+
 /* Launch shape -------------------------------------------------------------- */
 /* By default the fused passes (dpg_step, dpg_reduce_scatter_adam,
  * dpg_step_fold2, dpg_adam_from_reduced, dpg_allreduce_grads and

@@ -36,6 +36,8 @@ DPG_MAX_VIEWS = 64
 DPG_MAX_NS_STEPS = 16
 DPG_SCALE_SPECTRAL = 0
 DPG_SCALE_RMS = 1
+DPG_NVFP4 = 0
+DPG_MXFP4 = 1
 
 # symbols declared in include/dpg.h
 EXPORTED = (
@@ -51,6 +53,9 @@ EXPORTED = (
     "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit",
     "dpg_plan_matrices", "dpg_matrices_destroy", "dpg_matrices_info", "dpg_matrices_upload",
     "dpg_matrices_status", "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply", "dpg_muon_step",
+    "dpg_fp4_sizes", "dpg_fp4_quantize", "dpg_fp4_dequantize", "dpg_allgather_params_fp4",
+    "dpg_fp4_product", "dpg_fp4_status", "dpg_layer_norm", "dpg_layer_norm_workspace",
+    "dpg_layer_norm_backward",
 )
 DPG_MAX_STATE_ARRAYS = 8
 DPG_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -203,6 +208,16 @@ def lib() -> ctypes.CDLL:
         L.dpg_orthogonalize.argtypes = [P, P, i32, P, P, P]
         L.dpg_muon_apply.argtypes = [P, P, P, P, P, i32, P]
         L.dpg_muon_step.argtypes = [P, P, P, i32, P, P, i32, P, P, P, P, i32, P, i32, P]
+        L.dpg_fp4_sizes.argtypes = [i64, i64, i32, P, P]
+        L.dpg_fp4_quantize.argtypes = [P, i32, i64, i64, i64, P, P, P, P]
+        L.dpg_fp4_dequantize.argtypes = [P, P, i32, i64, P]
+        L.dpg_allgather_params_fp4.argtypes = [P, P, P, P, P, i32, P]
+        L.dpg_fp4_product.argtypes = [P, P, P, i32, i64, i32, P]
+        L.dpg_fp4_status.argtypes = [P]
+        L.dpg_layer_norm.argtypes = [P, i32, i64, i64, P, P, i32, ctypes.c_double, P, P, P, P]
+        L.dpg_layer_norm_workspace.argtypes = [i64, i64]
+        L.dpg_layer_norm_workspace.restype = i64
+        L.dpg_layer_norm_backward.argtypes = [P, P, i32, i64, i64, P, i32, P, P, P, P, P, i32, i32, P, P]
         L.dpg_time_next_fused_launch.restype = c_int
         for name in ("dpg_plan_buckets", "dpg_plan_info", "dpg_plan_bucket", "dpg_plan_param",
                      "dpg_plan_export", "dpg_plan_upload", "dpg_pack", "dpg_unpack",
@@ -216,7 +231,9 @@ def lib() -> ctypes.CDLL:
                      "dpg_plan_shards", "dpg_debug_checks", "dpg_debug_set_limit",
                      "dpg_plan_matrices", "dpg_matrices_info", "dpg_matrices_upload",
                      "dpg_matrices_status", "dpg_muon_momentum", "dpg_orthogonalize", "dpg_muon_apply",
-                     "dpg_muon_step"):
+                     "dpg_muon_step", "dpg_fp4_sizes", "dpg_fp4_quantize", "dpg_fp4_dequantize",
+                     "dpg_allgather_params_fp4", "dpg_fp4_product", "dpg_fp4_status", "dpg_layer_norm",
+                     "dpg_layer_norm_backward"):
             getattr(L, name).restype = c_int
         _lib = L
     return _lib
@@ -911,6 +928,204 @@ def dpg_muon_step(plan: Plan, mats: Matrices, grads: Sequence[Ptr], valid_tokens
         None if last_micro is None else _ptrs(last_micro), tok.ctypes.data, n_tok,
         ctypes.byref(hpc), _ptr(master), _ptr(momentum), _ptr(update), ud, _ptrs(param_views),
         len(param_views), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# 4-bit matrices and their products
+# --------------------------------------------------------------------------
+class dpg_fp4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("format", ctypes.c_int32)]
+
+
+class Fp4:
+    """A rows x cols matrix of 4-bit codes with a scale to every 16 (DPG_NVFP4) or
+    32 (DPG_MXFP4) of a row: its device buffers and their C description."""
+
+    def __init__(self, rows: int, cols: int, format: int = DPG_NVFP4, device="cuda"):
+        import torch
+        codes, scales = ctypes.c_int64(), ctypes.c_int64()
+        _check(lib().dpg_fp4_sizes(rows, cols, format, ctypes.byref(codes), ctypes.byref(scales)))
+        self.rows, self.cols, self.format = int(rows), int(cols), int(format)
+        self.codes = torch.empty(codes.value, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(scales.value, dtype=torch.uint8, device=device)
+        self.amax = torch.zeros(1, dtype=torch.float32, device=device)
+        self.c = dpg_fp4(self.codes.data_ptr(), self.scales.data_ptr(), self.amax.data_ptr(), self.rows,
+                         self.cols, self.format)
+        self._ref = ctypes.byref(self.c)
+
+
+def _fp4(q: Optional[Fp4], what: str):
+    if q is None:
+        return None
+    if not isinstance(q, Fp4):
+        raise TypeError(f"{what}: expected an Fp4")
+    _here(q.codes, what)
+    return q._ref
+
+
+def _here(t, what: str):
+    """Kernels are launched on the current device: its tensors only."""
+    import torch
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, but device {torch.cuda.current_device()} is current")
+
+
+def _matrix(t, what: str):
+    """(pointer, dtype, row stride) of a two-dimensional tensor with neighbouring
+    columns."""
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: columns must be neighbours in memory")
+    _here(t, what)
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), DPG_BF16 if t.dtype == torch.bfloat16 else DPG_F32, stride
+
+
+def _seed(seed):
+    """A one-element int64 CUDA tensor, read when the kernels run."""
+    if seed is None:
+        return None
+    import torch
+    if not isinstance(seed, torch.Tensor) or seed.dtype != torch.int64 or seed.numel() != 1:
+        raise TypeError("seed: expected a CUDA tensor of one int64")
+    _here(seed, "seed")
+    return seed.data_ptr()
+
+
+def dpg_fp4_quantize(x, by_row: Optional[Fp4] = None, by_col: Optional[Fp4] = None, *, seed=None,
+                     stream=None):
+    """by_row <- x (bf16 or fp32 matrix), by_col <- its transpose, each in blocks
+    along its own rows; nearest values, or stochastic ones with a seed."""
+    p, dt, stride = _matrix(x, "x")
+    _check(lib().dpg_fp4_quantize(p, dt, x.shape[0], x.shape[1], stride, _seed(seed), _fp4(by_row, "by_row"),
+                                  _fp4(by_col, "by_col"), _stream(stream)))
+
+
+def dpg_fp4_dequantize(q: Fp4, out, stream=None):
+    """out (bf16 or fp32 matrix) <- the values of q."""
+    if tuple(out.shape) != (q.rows, q.cols):
+        raise ValueError(f"out: expected {q.rows} x {q.cols}, got {tuple(out.shape)}")
+    p, dt, stride = _matrix(out, "out")
+    _check(lib().dpg_fp4_dequantize(_fp4(q, "q"), p, dt, stride, _stream(stream)))
+
+
+def dpg_allgather_params_fp4(mats: Matrices, master: Ptr, by_row: Optional[Sequence[Fp4]] = None,
+                             by_col: Optional[Sequence[Fp4]] = None, *, seed=None, stream=None):
+    """The 4-bit form of every matrix of a plan, in the order of its parameters,
+    from the flat fp32 masters; by_col holds the transposes."""
+    _need(master, "f32", mats.total_padded, "master")
+    arrays = []
+    for name, qs in (("by_row", by_row), ("by_col", by_col)):
+        if qs is not None:
+            if len(qs) != mats.n_matrices:
+                raise ValueError(f"{name}: need {mats.n_matrices} matrices, got {len(qs)}")
+            for q in qs:
+                _fp4(q, name)
+            qs = (dpg_fp4 * max(1, len(qs)))(*(q.c for q in qs))
+        arrays.append(qs)
+    _check(lib().dpg_allgather_params_fp4(mats.handle, _ptr(master), _seed(seed), arrays[0], arrays[1],
+                                          mats.n_matrices, _stream(stream)))
+
+
+def dpg_fp4_product(a: Fp4, b: Fp4, out, *, accumulate: bool = False, stream=None):
+    """out (a.rows x b.rows, bf16 or fp32) <- a b^T, or out + a b^T."""
+    if tuple(out.shape) != (a.rows, b.rows):
+        raise ValueError(f"out: expected {a.rows} x {b.rows}, got {tuple(out.shape)}")
+    p, dt, stride = _matrix(out, "out")
+    _check(lib().dpg_fp4_product(_fp4(a, "a"), _fp4(b, "b"), p, dt, stride, 1 if accumulate else 0,
+                                 _stream(stream)))
+
+
+def dpg_fp4_status(stream=None):
+    """Synchronise the stream; raise DpgError if a product timed out."""
+    _check(lib().dpg_fp4_status(_stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# layer norm
+# --------------------------------------------------------------------------
+def _vector(t, n: int, what: str):
+    """(pointer, dtype) of a contiguous tensor of n elements, or (None, None)."""
+    if t is None:
+        return None, None
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements")
+    _here(t, what)
+    return t.data_ptr(), DPG_BF16 if t.dtype == torch.bfloat16 else DPG_F32
+
+
+def _pair_dtype(a, b, what: str) -> int:
+    if a is not None and b is not None and a != b:
+        raise TypeError(f"{what}: expected one dtype")
+    return a if a is not None else b if b is not None else DPG_F32
+
+
+def _rows_of(x):
+    if x.dim() < 1:
+        raise ValueError("x: expected rows")
+    cols = x.shape[-1]
+    return x.numel() // cols if cols else 0, cols
+
+
+def _stat(t, rows: int, what: str):
+    if t is None:
+        return None
+    p, dt = _vector(t, rows, what)
+    if dt != DPG_F32:
+        raise TypeError(f"{what}: expected float32, got {t.dtype}")
+    return p
+
+
+def dpg_layer_norm(x, gain, bias, eps: float, y, mean=None, rstd=None, stream=None):
+    """y <- (x - mean) * rstd * gain + bias over the last dimension; mean and rstd
+    (fp32, one a row) are kept for the backward pass."""
+    rows, cols = _rows_of(x)
+    px, dt = _vector(x, x.numel(), "x")
+    py, dy = _vector(y, x.numel(), "y")
+    if dy != dt:
+        raise TypeError("y: expected the dtype of x")
+    (pg, dg), (pb, db) = _vector(gain, cols, "gain"), _vector(bias, cols, "bias")
+    _check(lib().dpg_layer_norm(px, dt, rows, cols, pg, pb, _pair_dtype(dg, db, "gain and bias"), float(eps), py,
+                                _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd"), _stream(stream)))
+
+
+def dpg_layer_norm_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace of a backward pass that sums gain's or bias's gradients."""
+    return int(lib().dpg_layer_norm_workspace(rows, cols))
+
+
+def dpg_layer_norm_backward(dy, x, gain, mean, rstd, dx=None, dgain=None, dbias=None, workspace=None, *,
+                            accumulate: bool = False, stream=None):
+    """dx, and the gradients of gain and bias summed over the rows (bf16 or fp32;
+    accumulate: added to what fp32 ones hold).  Each may be None."""
+    rows, cols = _rows_of(x)
+    px, dt = _vector(x, x.numel(), "x")
+    pdy, ddy = _vector(dy, x.numel(), "dy")
+    pdx, ddx = _vector(dx, x.numel(), "dx")
+    if ddy != dt or ddx not in (None, dt):
+        raise TypeError("dy, dx: expected the dtype of x")
+    pg, dg = _vector(gain, cols, "gain")
+    (pdg, ddg), (pdb, ddb) = _vector(dgain, cols, "dgain"), _vector(dbias, cols, "dbias")
+    if workspace is not None:
+        _here(workspace, "workspace")
+        need = dpg_layer_norm_workspace(rows, cols)
+        if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace: needs {need} contiguous bytes")
+        workspace = workspace.data_ptr()
+    _check(lib().dpg_layer_norm_backward(
+        pdy, px, dt, rows, cols, pg, _pair_dtype(dg, None, "gain"), _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), pdx, pdg, pdb, _pair_dtype(ddg, ddb, "dgain and dbias"),
+        1 if accumulate else 0, workspace, _stream(stream)))
 
 
 def dpg_set_fused_max_ctas(max_ctas: int = 0):

@@ -1,0 +1,786 @@
+// dpg_fp4_product.cu -- products of 4-bit quantised matrices on the tensor cores
+// (see dpg_fp4_product in include/dpg.h).
+//
+// C = A B^T, both operands stored along the sum.  A tcgen05.mma of 4-bit kind
+// takes 64 elements of each row (32 bytes) and their scales: 4 for blocks of 16,
+// 2 for blocks of 32; codes come from shared memory (rows of 256 elements, 128
+// bytes, 128-byte swizzle), scales from tensor memory, where tcgen05.cp brings
+// a tile of 128 rows x 4 scales as it is stored (32 lanes x 16 bytes, copied to
+// the four quarters of the lanes).  Sums are fp32 in tensor memory; the matrices'
+// powers of two are applied to them at the end.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "dpg_async.cuh"
+#include "dpg_fp4.h"
+#include "dpg_host.h"
+
+namespace dpg {
+
+constexpr int kProdDepth = 256;                  // elements of the sum in a stage
+constexpr int kCodeRow = kProdDepth / 2;         // bytes of a row in a stage
+constexpr int kRowTile = 128;                    // rows of an operand in a CTA
+constexpr int kScaleBytes = 2048;                // room for the scales of 128 rows in a stage
+constexpr uint64_t kProdWaitNs = 2000000000ull;  // bound of every wait, unless a test sets another
+
+// 0, or the error of the first wait that ran out on this device
+__device__ int32_t g_fp4_status;
+
+struct ProductArgs {
+    void* c;
+    int64_t stride;
+    const float* amax_a;         // DPG_NVFP4: of the operands
+    const float* amax_b;
+    int32_t m, n, k;
+    int32_t c_f32, add;
+    int32_t vec;                 // 16-byte accesses of C's rows are allowed
+    int32_t rows, cols;          // of the product as it is computed (its transpose if `swap`)
+    int32_t tiles_r, tiles_c;
+    int32_t swap;                // rows are C's columns
+    int32_t split;               // CTAs (of one cluster) that share a sum
+    uint64_t wait_ns;
+    int64_t skip;                // test only: the first CTA leaves out this stage's first copy (-1: none)
+};
+
+struct ProductMaps {
+    CUtensorMap codes_r, codes_c, scales_r, scales_c;
+};
+
+// ---------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void give_up(volatile int* abort) {
+    *abort = 1;
+    atomicCAS(&g_fp4_status, 0, DPG_ERR_DEVICE_TIMEOUT);
+}
+// true once the phase of `parity` completed; false when the bound ran out or
+// another role of the CTA gave up
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t ns) {
+    const uint32_t at = smem_u32(bar);
+    if (try_wait(at, parity)) return true;
+    const uint64_t until = global_ns() + ns;
+    while (!try_wait(at, parity)) {
+        if (*abort) return false;
+        if (global_ns() > until) {
+            give_up(abort);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void copy_tile(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// `bar` may be the other CTA's of the pair
+__device__ __forceinline__ void copy_tile_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// rows of 128 bytes with a 128-byte swizzle, 8 rows every 1024 bytes
+__device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// 32 rows of 16 bytes, 8 rows every 128 bytes
+__device__ __forceinline__ uint64_t scales_desc(uint32_t addr) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+// E2M1 operands by rows, rows x cols sums, E8M0 (MX) or E4M3 scales; `id`: which
+// two of the four scales (E8M0)
+template <bool MX>
+__device__ __forceinline__ uint32_t product_shape(int rows, int cols, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | (uint32_t(cols >> 3) << 17) | (MX ? 1u << 23 : 0u) |
+           (uint32_t(rows >> 7) << 27) | (id << 29);
+}
+template <bool MX, bool PAIR>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t sa, uint32_t sb,
+                                         bool add) {
+#define DPG_MMA(group, kind)                                                                       \
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n tcgen05.mma.cta_group::" group      \
+                 ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n}"                             \
+                 :: "r"(d), "l"(a), "l"(b), "r"(shape), "r"(sa), "r"(sb), "r"(add ? 1u : 0u) : "memory")
+    if (MX) {
+        if (PAIR) DPG_MMA("2", "mxf4.block_scale.scale_vec::2X");
+        else DPG_MMA("1", "mxf4.block_scale.scale_vec::2X");
+    } else {
+        if (PAIR) DPG_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+        else DPG_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    }
+#undef DPG_MMA
+}
+// 512 bytes of scales to four columns of tensor memory
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(scales_desc(smem)) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(scales_desc(smem)) : "memory");
+}
+// arrives at `bar` once everything issued so far is done (PAIR: in both CTAs)
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     :: "r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     :: "r"(smem_u32(bar)) : "memory");
+}
+
+// One stage's products: up to 4 of 64 elements, scales first.  `at`: the stage
+// (codes of the rows, of the columns, scales of the rows, of the columns), COLS:
+// columns of the instruction, CODES: bytes of the columns' codes in this CTA.
+template <bool MX, bool PAIR, int COLS, int CODES>
+__device__ __forceinline__ void multiply_stage(uint32_t at, uint32_t d, uint32_t sf, int steps, bool fresh) {
+    constexpr int kColTiles = COLS > 128 ? 2 : 1;
+    const uint32_t sr = at + kRowTile * kCodeRow + CODES, sc = sr + kScaleBytes;
+    const uint32_t tr = sf, tc = sf + 16;            // columns: 4 a tile of the rows, 4 or 8 of the columns
+    const int tiles = MX ? (steps + 1) >> 1 : steps;
+    for (int t = 0; t < tiles; ++t) {
+        copy_scales<PAIR>(tr + 4 * t, sr + t * kFp4TileBytes);
+#pragma unroll
+        for (int q = 0; q < kColTiles; ++q)
+            copy_scales<PAIR>(tc + 4 * (kColTiles * t + q), sc + (q * (MX ? 2 : 4) + t) * kFp4TileBytes);
+    }
+    const uint64_t a = codes_desc(at), b = codes_desc(at + kRowTile * kCodeRow);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < steps) {
+            const int t = MX ? k >> 1 : k;
+            const uint32_t id = MX ? 2u * uint32_t(k & 1) : 0u;
+            multiply<MX, PAIR>(d, a + 2 * k, b + 2 * k, product_shape<MX>(PAIR ? 256 : 128, COLS, id), tr + 4 * t,
+                               tc + 4 * kColTiles * t, !fresh || k > 0);
+        }
+}
+
+// ---------------------------------------------------------------------------
+// results
+// ---------------------------------------------------------------------------
+// the operands' powers of two, as two factors (their product may leave fp32's range)
+struct ProductScale {
+    float f[2];
+};
+template <bool MX>
+__device__ __forceinline__ ProductScale product_scale(const ProductArgs& a) {
+    ProductScale s;
+    s.f[0] = s.f[1] = 1.0f;
+    if (!MX) {
+        const int e = fp4_exponent(__float_as_uint(__ldg(a.amax_a))) + fp4_exponent(__float_as_uint(__ldg(a.amax_b)));
+        const int h = e >> 1;      // -126 .. 117
+        s.f[0] = __uint_as_float(uint32_t(127 + h) << 23);
+        s.f[1] = __uint_as_float(uint32_t(127 + e - h) << 23);
+    }
+    return s;
+}
+
+// N (a multiple of 8) neighbouring sums of row `r`, columns from c on, into C
+template <int N>
+__device__ __forceinline__ void store_along(const ProductArgs& a, const ProductScale& s, int r, int c, const float* v) {
+    if (r >= a.m || c >= a.n) return;
+    const int64_t at = int64_t(r) * a.stride + c;
+    float x[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = v[j] * s.f[0] * s.f[1];
+    if (a.vec && c + N <= a.n) {
+        if (a.c_f32) {
+            float* p = static_cast<float*>(a.c) + at;
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                float4 y = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                if (a.add) {
+                    const float4 o = *reinterpret_cast<const float4*>(p + j);
+                    y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+                }
+                *reinterpret_cast<float4*>(p + j) = y;
+            }
+        } else {
+            uint16_t* p = static_cast<uint16_t*>(a.c) + at;
+#pragma unroll
+            for (int j = 0; j < N; j += 8) *reinterpret_cast<uint4*>(p + j) = narrow8(x + j);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (c + j < a.n) {
+            if (a.c_f32) {
+                float* p = static_cast<float*>(a.c) + at + j;
+                *p = a.add ? *p + x[j] : x[j];
+            } else {
+                static_cast<__nv_bfloat16*>(a.c)[at + j] = __float2bfloat16_rn(x[j]);
+            }
+        }
+}
+
+// one sum, element (r, c) of C
+__device__ __forceinline__ void store_one(const ProductArgs& a, const ProductScale& s, int r, int c, float v) {
+    if (r >= a.m || c >= a.n) return;
+    const int64_t at = int64_t(r) * a.stride + c;
+    const float x = v * s.f[0] * s.f[1];
+    if (a.c_f32) {
+        float* p = static_cast<float*>(a.c) + at;
+        *p = a.add ? *p + x : x;
+    } else {
+        static_cast<__nv_bfloat16*>(a.c)[at] = __float2bfloat16_rn(x);
+    }
+}
+
+// N sums of row r of the product as it is computed, from column c on
+template <int N>
+__device__ __forceinline__ void store_sums(const ProductArgs& a, const ProductScale& s, int r, int c, const float* v) {
+    if (a.swap) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) store_one(a, s, c + j, r, v[j]);
+    } else {
+        store_along<N>(a, s, r, c, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Small products: 128 x COLS sums to a CTA.  Where there are few tiles, the CTAs
+// of a cluster share the sum, leave their parts in shared memory and add them in
+// the order of their ranks, each a share of the columns.
+//
+// Two CTAs fit an SM and hold at most 256 of its 512 columns of tensor memory
+// each; beside the CTAs of the large product and of the orthogonalisation
+// no other fits.  So no CTA of a cluster ever waits for tensor memory that a CTA
+// which waits for another cluster's holds.
+//
+//   warp 0  copies operands     warp 1  issues the products     warps 2..5  store
+// ---------------------------------------------------------------------------
+constexpr int kSmallThreads = 192;
+template <int COLS>
+struct SmallShape {
+    static constexpr int kCodes = COLS * kCodeRow;
+    static constexpr int kStage = kRowTile * kCodeRow + kCodes + 2 * kScaleBytes;
+    static constexpr int kStages = COLS <= 32 ? 4 : COLS == 64 ? 4 : 3;
+    static constexpr int kScaleColumn = COLS < 32 ? 32 : COLS;             // of tensor memory
+    static constexpr int kColumns = kScaleColumn + 64 <= 128 ? 128 : 256;
+    static constexpr int kSmem = kStages * kStage + 256;
+    static_assert(kStage % 1024 == 0, "the swizzle's boundary");
+    static_assert(kSmem > 77 * 1024 && 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM, not three");
+    static_assert(COLS * kRowTile * 4 <= kStages * kStage, "room for the sums");
+};
+struct SmallShared {
+    uint64_t full[4], empty[4], done;
+    uint32_t tmem;
+    volatile int abort;
+};
+
+template <bool MX, int COLS>
+__global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_constant__ ProductArgs a,
+                                                             const __grid_constant__ ProductMaps maps) {
+    using S = SmallShape<COLS>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    SmallShared& sh = *reinterpret_cast<SmallShared*>(dyn + kStages * S::kStage);
+    const uint32_t stage0 = smem_u32(dyn);
+    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        mbar_init(&sh.done, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(&sh.tmem)), "n"(S::kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    pdl_enter();
+    const uint32_t tmem = sh.tmem;
+    const int rank = a.split > 1 ? int(cluster_rank()) : 0;
+    const int tile = int(blockIdx.x) / a.split;
+    const int r0 = tile % a.tiles_r * kRowTile, c0 = tile / a.tiles_r * COLS;
+    // this CTA's stages of the sum
+    const int all = (a.k + kProdDepth - 1) / kProdDepth;
+    const int first = int(int64_t(all) * rank / a.split), last = int(int64_t(all) * (rank + 1) / a.split);
+
+    if (warp == 0 && lane == 0) {
+        int s = 0;
+        uint32_t par = 1;
+        for (int k = first; k < last; ++k) {
+            if (!wait_phase(&sh.empty[s], par, &sh.abort, a.wait_ns)) break;
+            const uint32_t at = stage0 + uint32_t(s) * S::kStage, bar = smem_u32(&sh.full[s]);
+            mbar_expect(&sh.full[s], kRowTile * kCodeRow + S::kCodes + 2 * (MX ? 1024 : 2048));
+            if (blockIdx.x != 0 || k - first != a.skip) copy_tile(at, &maps.codes_r, k * kCodeRow, r0, bar);
+            copy_tile(at + kRowTile * kCodeRow, &maps.codes_c, k * kCodeRow, c0, bar);
+            const uint32_t sf = at + kRowTile * kCodeRow + S::kCodes;
+            copy_tile(sf, &maps.scales_r, k * (MX ? 128 : 256), r0 / kFp4TileRows, bar);
+            copy_tile(sf + kScaleBytes, &maps.scales_c, k * (MX ? 128 : 256), c0 / kFp4TileRows, bar);
+            if (++s == kStages) {
+                s = 0;
+                par ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        int s = 0;
+        uint32_t par = 0;
+        bool ok = true;
+        for (int k = first; k < last; ++k) {
+            if (!(ok = wait_phase(&sh.full[s], par, &sh.abort, a.wait_ns))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int left = a.k - k * kProdDepth, steps = left >= kProdDepth ? 4 : (left + 63) >> 6;
+            multiply_stage<MX, false, COLS, S::kCodes>(stage0 + uint32_t(s) * S::kStage, tmem,
+                                                       tmem + S::kScaleColumn + 32 * (k & 1), steps, k == first);
+            commit<false>(&sh.empty[s]);
+            if (++s == kStages) {
+                s = 0;
+                par ^= 1;
+            }
+        }
+        if (ok) commit<false>(&sh.done);
+    }
+    __syncwarp();
+    if (warp >= 2) {
+        const int row = (warp & 3) * 32 + lane;
+        const ProductScale scale = product_scale<MX>(a);
+        const bool ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.done, 0, &sh.abort, a.wait_ns));
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t sums = tmem + (uint32_t((warp & 3) * 32) << 16);
+        constexpr int kGroup = COLS < 32 ? COLS : 32;
+        if (ok)
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 32) {
+                float v[32];
+                load_acc32(sums + c, v);                    // (COLS = 16: with 16 unused columns)
+                if (a.split == 1) {
+                    store_sums<kGroup>(a, scale, r0 + row, c0 + c, v);
+                } else {
+                    // the stages are free: every product of this CTA is done
+                    float* part = reinterpret_cast<float*>(dyn) + row;
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j) part[(c + j) * kRowTile] = v[j];
+                }
+            }
+    }
+    if (sh.abort) {   // the copies this CTA has in flight land within this time
+        const uint64_t until = global_ns() + 2000000ull;
+        while (global_ns() < until) {}
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (a.split > 1) {
+        cluster_sync();
+        if (warp >= 2 && !sh.abort) {
+            const int row = (warp & 3) * 32 + lane, share = COLS / a.split, from = rank * share;
+            const ProductScale scale = product_scale<MX>(a);
+            for (int c = from; c < from + share; c += 8) {
+                const int some = share < 8 ? share : 8;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                for (int q = 0; q < a.split; ++q) {
+                    const uint32_t part = map_to(stage0 + uint32_t(c * kRowTile + row) * 4, uint32_t(q));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < some) {
+                            float x;
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(part + j * kRowTile * 4) : "memory");
+                            v[j] += x;
+                        }
+                }
+                if (some == 8) {
+                    store_sums<8>(a, scale, r0 + row, c0 + c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < some) {
+                            if (a.swap) store_one(a, scale, c0 + c + j, r0 + row, v[j]);
+                            else store_one(a, scale, r0 + row, c0 + c + j, v[j]);
+                        }
+                }
+            }
+        }
+        cluster_sync();                                     // the others have read this CTA's part
+    }
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(S::kColumns) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Large products: 256 x 256 sums to a pair of CTAs on two SMs, pairs that stay
+// and take tile after tile.  CTA r holds rows 128 r .. of both operands; the
+// pair's products read both halves, and each CTA's tensor memory holds the scales
+// of its own rows and of all columns.
+//
+// Tensor memory: sums of even tiles in columns 0 .. 255, of odd ones in 160 ..
+// 415, two sets of a stage's scales in 416 .. 511.  The next tile's products
+// start when the 96 columns that both sums have are stored, which is done first.
+//
+//   warp 0  copies operands     warp 1  of CTA 0: issues the products
+//   warps 2..9  store (warp w: lanes 32 (w mod 4) .., every other 32 columns)
+// ---------------------------------------------------------------------------
+constexpr int kLargeStages = 5;
+constexpr int kLargeCodes = kRowTile * kCodeRow;
+constexpr int kLargeStage = 2 * kLargeCodes + 3 * kScaleBytes;
+constexpr int kLargeEpiWarps = 8;
+constexpr int kLargeThreads = 32 * (2 + kLargeEpiWarps);
+constexpr int kLargeTile = 256;
+constexpr int kOverlap = 96;
+struct LargeShared {
+    uint64_t full[kLargeStages], empty[kLargeStages], done[2], clear;
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr int kLargeSmem = kLargeStages * kLargeStage + int(sizeof(LargeShared));
+static_assert(kLargeStage % 1024 == 0, "the swizzle's boundary");
+static_assert(kLargeSmem <= 227 * 1024 && kLargeSmem + 78 * 1024 > 228 * 1024, "alone on its SM");
+
+// tile t of the queue: 8 rows of tiles at a time, column after column, so that
+// the tiles in work at one time share operands
+__device__ __forceinline__ void large_tile(const ProductArgs& a, int t, int& r0, int& c0) {
+    const int per = 8 * a.tiles_c, g = t / per, in = t - g * per;
+    const int high = min(8, a.tiles_r - 8 * g);
+    r0 = (8 * g + in % high) * kLargeTile;
+    c0 = in / high * kLargeTile;
+}
+
+template <bool MX>
+__global__ void __cluster_dims__(2) __launch_bounds__(kLargeThreads, 1)
+k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ ProductMaps maps) {
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    LargeShared& sh = *reinterpret_cast<LargeShared*>(dyn + kLargeStages * kLargeStage);
+    const uint32_t stage0 = smem_u32(dyn);
+    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const uint32_t rank = cluster_rank();
+    const int pair = int(blockIdx.x >> 1), pairs = int(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kLargeStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        mbar_init(&sh.done[0], 1);
+        mbar_init(&sh.done[1], 1);
+        mbar_init(&sh.clear, 2 * kLargeEpiWarps);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    pdl_enter();
+    const uint32_t tmem = sh.tmem;
+    const int tiles = a.tiles_r * a.tiles_c, stages = (a.k + kProdDepth - 1) / kProdDepth;
+
+    if (warp == 0 && lane == 0) {
+        const uint32_t full0 = map_to(smem_u32(&sh.full[0]), 0);
+        constexpr int kScales = MX ? 1024 : 2048;
+        int s = 0;
+        int64_t skip = blockIdx.x == 0 ? a.skip : -1;
+        uint32_t par = 1;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int r0, c0;
+            large_tile(a, t, r0, c0);
+            for (int k = 0; k < stages; ++k) {
+                if (!(ok = wait_phase(&sh.empty[s], par, &sh.abort, a.wait_ns))) break;
+                const uint32_t at = stage0 + uint32_t(s) * kLargeStage, bar = full0 + uint32_t(s) * 8;
+                if (rank == 0) mbar_expect(&sh.full[s], 2 * (2 * kLargeCodes + 3 * kScales));
+                if (skip-- != 0) copy_tile_pair(at, &maps.codes_r, k * kCodeRow, r0 + int(rank) * kRowTile, bar);
+                copy_tile_pair(at + kLargeCodes, &maps.codes_c, k * kCodeRow, c0 + int(rank) * kRowTile, bar);
+                const uint32_t sf = at + 2 * kLargeCodes;
+                copy_tile_pair(sf, &maps.scales_r, k * (MX ? 128 : 256), r0 / kFp4TileRows + int(rank), bar);
+                copy_tile_pair(sf + kScaleBytes, &maps.scales_c, k * (MX ? 128 : 256), c0 / kFp4TileRows, bar);
+                if (++s == kLargeStages) {
+                    s = 0;
+                    par ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        int s = 0, it = 0;
+        uint32_t par = 0, set = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs, ++it) {
+            if (it > 0 && !(ok = wait_phase(&sh.clear, uint32_t(it - 1) & 1u, &sh.abort, a.wait_ns))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + uint32_t(it & 1) * (kLargeTile - kOverlap);
+            for (int k = 0; k < stages; ++k, set ^= 1) {
+                if (!(ok = wait_phase(&sh.full[s], par, &sh.abort, a.wait_ns))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const int left = a.k - k * kProdDepth, steps = left >= kProdDepth ? 4 : (left + 63) >> 6;
+                multiply_stage<MX, true, kLargeTile, kLargeCodes>(stage0 + uint32_t(s) * kLargeStage, d,
+                                                                  tmem + 2 * kLargeTile - kOverlap + 48 * set, steps,
+                                                                  k == 0);
+                commit<true>(&sh.empty[s]);
+                if (++s == kLargeStages) {
+                    s = 0;
+                    par ^= 1;
+                }
+            }
+            if (ok) commit<true>(&sh.done[it & 1]);
+        }
+    } else if (warp >= 2) {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const ProductScale scale = product_scale<MX>(a);
+        const uint32_t clear = map_to(smem_u32(&sh.clear), 0);
+        int it = 0;
+        for (int t = pair; t < tiles; t += pairs, ++it) {
+            int r0, c0;
+            large_tile(a, t, r0, c0);
+            const int r = r0 + int(rank) * kRowTile + quad * 32 + lane;
+            const bool ok = wait_phase(&sh.done[it & 1], uint32_t(it >> 1) & 1u, &sh.abort, a.wait_ns);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t sums = tmem + uint32_t(it & 1) * (kLargeTile - kOverlap) + (uint32_t(quad * 32) << 16);
+            // in groups of 32 columns: the three that the next tile's sums take first
+            const int before = (it & 1) ? 0 : kLargeTile - kOverlap;
+#pragma unroll 1
+            for (int g = half; g < kLargeTile / 32; g += 2) {
+                const int c = (before + g * 32) & (kLargeTile - 1);
+                float v[32];
+                load_acc32(sums + uint32_t(c), v);
+                if (g + 2 >= kOverlap / 32 && g < kOverlap / 32) {    // this warp's last of the three
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(clear) : "memory");
+                }
+                store_along<32>(a, scale, r, c0 + c, v);
+            }
+        }
+    }
+    __syncwarp();
+    if (sh.abort) {   // the copies this CTA has in flight land within this time
+        const uint64_t until = global_ns() + 2000000ull;
+        while (global_ns() < until) {}
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+}
+
+// k = 0: zeros, or what C held
+__global__ void __launch_bounds__(256) k_fp4_zero(const __grid_constant__ ProductArgs a) {
+    pdl_enter();
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= int64_t(a.m) * a.n) return;
+    const int64_t at = i / a.n * a.stride + i % a.n;
+    if (a.c_f32) static_cast<float*>(a.c)[at] = 0.0f;
+    else static_cast<uint16_t*>(a.c)[at] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static int encoder(EncodeTiled* out, const char* who) {
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled fn = known.load(std::memory_order_acquire);
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        DPG_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found));
+        if (found != cudaDriverEntryPointSuccess || !p)
+            return fail(DPG_ERR_CUDA, "%s: the driver has no tensor maps", who);
+        fn = reinterpret_cast<EncodeTiled>(p);
+        known.store(fn, std::memory_order_release);
+    }
+    *out = fn;
+    return DPG_OK;
+}
+
+// codes: boxes of 256 elements x box_rows; scales: boxes of a stage's tiles x
+// box_tiles rows of tiles.  What lies outside is zero.
+static int encode_operand(const dpg_fp4* q, int box_rows, int box_tiles, CUtensorMap* codes, CUtensorMap* scales,
+                          const char* who) {
+    EncodeTiled fn = nullptr;
+    const int st = encoder(&fn, who);
+    if (st != DPG_OK) return st;
+    const cuuint32_t step[2] = {1, 1};
+    const cuuint64_t dims[2] = {cuuint64_t(q->cols + 1) / 2, cuuint64_t(q->rows)};
+    const cuuint64_t pitch[1] = {cuuint64_t(fp4_pitch(q->cols))};
+    const cuuint32_t box[2] = {kCodeRow, cuuint32_t(box_rows)};
+    CUresult e = fn(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q->codes, dims, pitch, box, step,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e == CUDA_SUCCESS) {
+        const int64_t tiles = fp4_tiles(q->cols, q->format);
+        const cuuint64_t sdims[2] = {cuuint64_t(tiles) * (kFp4TileBytes / 8),
+                                     cuuint64_t((q->rows + kFp4TileRows - 1) / kFp4TileRows)};
+        const cuuint64_t spitch[1] = {cuuint64_t(tiles) * kFp4TileBytes};
+        const cuuint32_t sbox[2] = {q->format == DPG_MXFP4 ? 128u : 256u, cuuint32_t(box_tiles)};
+        e = fn(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, q->scales, sdims, spitch, sbox, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    return e == CUDA_SUCCESS ? DPG_OK : fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
+}
+
+template <bool MX, int COLS>
+static int launch_small(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int sms, cudaStream_t s, const char* who) {
+    using S = SmallShape<COLS>;
+    a.tiles_r = (a.rows + kRowTile - 1) / kRowTile;
+    a.tiles_c = (a.cols + COLS - 1) / COLS;
+    const int64_t tiles = int64_t(a.tiles_r) * a.tiles_c;
+    const int stages = (a.k + kProdDepth - 1) / kProdDepth;
+    // more CTAs share a sum while that leaves them at most two to an SM and two stages each
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= 2 * sms && stages >= 4 * a.split) a.split *= 2;
+    if (tiles * a.split > 0x7FFFFFFF) return fail(DPG_ERR_INVALID_ARG, "%s: %lld tiles", who, (long long)tiles);
+    ProductMaps maps;
+    int st = encode_operand(r, kRowTile, 1, &maps.codes_r, &maps.scales_r, who);
+    if (st == DPG_OK) st = encode_operand(c, COLS, 1, &maps.codes_c, &maps.scales_c, who);
+    if (st != DPG_OK) return st;
+    auto k = k_fp4_small<MX, COLS>;
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles * a.split));
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (a.split > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(a.split);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (t_programmatic) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = unsigned(n);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a, maps);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    }
+    return after_launch(who);
+}
+
+template <bool MX>
+static int launch_large(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int sms, cudaStream_t s, const char* who) {
+    a.tiles_r = (a.rows + kLargeTile - 1) / kLargeTile;
+    a.tiles_c = (a.cols + kLargeTile - 1) / kLargeTile;
+    a.split = 1;
+    const int64_t tiles = int64_t(a.tiles_r) * a.tiles_c;
+    if (tiles > 0x3FFFFFFF) return fail(DPG_ERR_INVALID_ARG, "%s: %lld tiles", who, (long long)tiles);
+    ProductMaps maps;
+    int st = encode_operand(r, kRowTile, 1, &maps.codes_r, &maps.scales_r, who);
+    if (st == DPG_OK) st = encode_operand(c, kRowTile, 2, &maps.codes_c, &maps.scales_c, who);
+    if (st != DPG_OK) return st;
+    const int pairs = int(tiles < sms / 2 ? tiles : sms / 2);
+    DPG_CUDA_TRY(cudaFuncSetAttribute(k_fp4_large<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLargeSmem));
+    return launch_k(k_fp4_large<MX>, unsigned(2 * pairs), kLargeThreads, size_t(kLargeSmem), s, who, a, maps);
+}
+
+template <bool MX>
+static int product(const dpg_fp4* x, const dpg_fp4* w, ProductArgs a, cudaStream_t s, const char* who) {
+    int dev = 0, sms = 0;
+    DPG_CUDA_TRY(cudaGetDevice(&dev));
+    int st = sm_count(dev, &sms);
+    if (st != DPG_OK) return st;
+    const int64_t large = (int64_t(a.m) + kLargeTile - 1) / kLargeTile * ((int64_t(a.n) + kLargeTile - 1) / kLargeTile);
+    a.rows = a.m;
+    a.cols = a.n;
+    if (large >= sms / 2) return launch_large<MX>(a, x, w, sms, s, who);
+    const int few = a.m < a.n ? a.m : a.n;
+    if (few > 64) return launch_small<MX, 128>(a, x, w, sms, s, who);
+    // the shorter side in the columns of the sums
+    a.swap = a.m < a.n;
+    if (a.swap) {
+        a.rows = a.n;
+        a.cols = a.m;
+    }
+    const dpg_fp4 *r = a.swap ? w : x, *c = a.swap ? x : w;
+    if (few <= 16) return launch_small<MX, 16>(a, r, c, sms, s, who);
+    if (few <= 32) return launch_small<MX, 32>(a, r, c, sms, s, who);
+    return launch_small<MX, 64>(a, r, c, sms, s, who);
+}
+
+}  // namespace dpg
+
+using dpg::fail;
+
+extern "C" {
+
+int dpg_fp4_product(const dpg_fp4* x, const dpg_fp4* w, void* c, int32_t c_dtype, int64_t row_stride,
+                    int32_t accumulate, void* stream) {
+    dpg::clear_error();
+    const char* who = "dpg_fp4_product";
+    const dpg::Trace trace(who);
+    if (!x) return fail(DPG_ERR_INVALID_ARG, "%s: a is NULL", who);
+    if (!w) return fail(DPG_ERR_INVALID_ARG, "%s: b is NULL", who);
+    int st = dpg::fp4_check(x, "a", who);
+    if (st == DPG_OK) st = dpg::fp4_check(w, "b", who);
+    if (st != DPG_OK) return st;
+    if (x->format != w->format) return fail(DPG_ERR_INVALID_ARG, "%s: a and b have different formats", who);
+    if (x->cols != w->cols)
+        return fail(DPG_ERR_INVALID_ARG, "%s: sums over %lld and %lld elements", who, (long long)x->cols,
+                    (long long)w->cols);
+    if (c_dtype != DPG_BF16 && c_dtype != DPG_F32)
+        return fail(DPG_ERR_INVALID_ARG, "%s: dtype %d of c unknown", who, c_dtype);
+    if (accumulate && c_dtype != DPG_F32) return fail(DPG_ERR_INVALID_ARG, "%s: only an fp32 c is added to", who);
+    dpg::ProductArgs a{};
+    if (x->rows == 0 || w->rows == 0) return DPG_OK;
+    if (!c) return fail(DPG_ERR_INVALID_ARG, "%s: c is NULL", who);
+    if (!dpg::aligned(c, c_dtype == DPG_BF16 ? 2 : 4)) return fail(DPG_ERR_MISALIGNED, "%s: c misaligned", who);
+    if (x->rows > 1 && (row_stride < w->rows || row_stride > (int64_t(1) << 40)))
+        return fail(DPG_ERR_INVALID_ARG, "%s: row stride %lld of c, which has %lld columns", who, (long long)row_stride,
+                    (long long)w->rows);
+    a.c = c;
+    a.stride = x->rows > 1 ? row_stride : w->rows;
+    a.amax_a = x->amax;
+    a.amax_b = w->amax;
+    a.m = int32_t(x->rows);
+    a.n = int32_t(w->rows);
+    a.k = int32_t(x->cols);
+    a.c_f32 = c_dtype == DPG_F32;
+    a.add = accumulate != 0;
+    a.vec = dpg::aligned(c, 16) && (x->rows <= 1 || row_stride % (a.c_f32 ? 4 : 8) == 0);
+    a.wait_ns = dpg::t_staged_timeout_ns > 0 ? uint64_t(dpg::t_staged_timeout_ns) : dpg::kProdWaitNs;
+    a.skip = dpg::t_staged_skip;
+    dpg::t_staged_skip = -1;
+    dpg::t_staged_timeout_ns = 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.k == 0) {
+        if (a.add) return DPG_OK;
+        int grid = 0;
+        st = dpg::grid_cover((int64_t(a.m) * a.n + 255) / 256, &grid, who);
+        return st != DPG_OK ? st : dpg::launch_k(dpg::k_fp4_zero, unsigned(grid), 256, s, who, a);
+    }
+    return x->format == DPG_MXFP4 ? dpg::product<true>(x, w, a, s, who) : dpg::product<false>(x, w, a, s, who);
+}
+
+int dpg_fp4_status(void* stream) {
+    dpg::clear_error();
+    using dpg::fail;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* word = nullptr;
+    int32_t got = 0;
+    DPG_CUDA_TRY(cudaGetSymbolAddress(&word, dpg::g_fp4_status));
+    DPG_CUDA_TRY(cudaMemcpyAsync(&got, word, sizeof got, cudaMemcpyDeviceToHost, s));
+    DPG_CUDA_TRY(cudaMemsetAsync(word, 0, sizeof got, s));
+    DPG_CUDA_TRY(cudaStreamSynchronize(s));
+    if (got != 0) return fail(got, "dpg_fp4_product: a wait on the device ran out; its results are incomplete");
+    return DPG_OK;
+}
+
+}  // extern "C"

@@ -141,6 +141,8 @@ static bool lay_out(const Plan& p, const int64_t* rows, const int64_t* cols, Mat
     M.n_params = p.n_params;
     M.param_offset = p.param_offset;
     M.numels = p.numels;
+    M.rows.assign(rows, rows + p.n_params);
+    M.cols.assign(cols, cols + p.n_params);
     M.scales.assign(2 * size_t(p.n_params), 1.0);
     int64_t count = 0;
     for (int32_t q = 0; q < p.n_params; ++q)

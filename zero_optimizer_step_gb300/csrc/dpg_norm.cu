@@ -1,0 +1,633 @@
+// dpg_norm.cu -- layer norm, its gradients, and the sums of the gain's and the
+// bias's gradients over the rows (see dpg_layer_norm and
+// dpg_layer_norm_backward in include/dpg.h).
+//
+// Both passes are streams of HBM traffic: forward 2 + 2 bytes per bf16 element,
+// backward 4 + 2.  A row is held in the registers of a warp (up to 1024
+// columns) or of a CTA (up to 32768 forward, 16384 backward), so that it is read
+// once: the mean, then the squares about it, then the result.  Longer rows are
+// read again from L2.
+//
+// Backward, a warp or a CTA keeps to the same columns over many rows, and adds
+// what each row gives to the gain's and the bias's gradients in registers; at
+// the end it leaves its sums in the workspace, and a second kernel adds those in
+// order.  The number of parts goes by the sizes alone, so the sums are the same
+// bits on every call.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "dpg_device.cuh"
+#include "dpg_host.h"
+
+namespace dpg {
+
+constexpr int64_t kNormMaxSide = int64_t(1) << 30;
+constexpr int kNormParts = 304;      // most CTAs of a backward pass: two per SM
+
+struct NormArgs {
+    const void* x;
+    const void* gain;                // nullable
+    const void* bias;                // nullable
+    void* y;
+    float* mean;                     // nullable with rstd
+    float* rstd;
+    int64_t rows;
+    int32_t cols;
+    int32_t params_f32;
+    float eps;
+};
+
+struct NormBackArgs {
+    const void* dy;
+    const void* x;
+    const void* gain;                // nullable
+    const float* mean;
+    const float* rstd;
+    void* dx;                        // nullable
+    float* part;                     // [parts][2][cols]; NULL: no sums
+    int64_t rows;
+    int32_t cols;
+    int32_t params_f32;
+    int32_t parts;
+};
+
+// ---------------------------------------------------------------------------
+// A row in registers: T threads hold V groups of 8 elements each.  VEC: groups
+// are 8 neighbours, loaded 16 bytes at a time; else the T threads hold
+// neighbouring elements, loaded singly (odd widths, unaligned buffers).
+// ---------------------------------------------------------------------------
+template <bool VEC, int T>
+__device__ __forceinline__ int column_of(int lane, int v, int j) {
+    return VEC ? (lane + v * T) * 8 + j : (v * 8 + j) * T + lane;
+}
+
+template <bool F32>
+struct NormRaw {
+    uint4 q[F32 ? 2 : 1];
+};
+
+// group v of the row at p (NULL: zeros): columns from `cols` on are zeros
+template <bool F32, bool VEC, int T>
+__device__ __forceinline__ NormRaw<F32> load_group(const void* p, int64_t row_at, int cols, int lane, int v) {
+    NormRaw<F32> r;
+    if (VEC) {
+        const int c = column_of<true, T>(lane, v, 0);
+        if (c < cols) {
+            const unsigned char* at = static_cast<const unsigned char*>(p) + (row_at + c) * (F32 ? 4 : 2);
+            // (plain loads: the output may be the input)
+#pragma unroll
+            for (int k = 0; k < (F32 ? 2 : 1); ++k)
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(r.q[k].x), "=r"(r.q[k].y), "=r"(r.q[k].z), "=r"(r.q[k].w)
+                             : "l"(at + 16 * k));
+        } else {
+#pragma unroll
+            for (int k = 0; k < (F32 ? 2 : 1); ++k) r.q[k] = make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = column_of<false, T>(lane, v, j);
+            e[j] = c >= cols ? 0u
+                   : F32     ? *(static_cast<const volatile uint32_t*>(p) + row_at + c)
+                             : uint32_t(*(static_cast<const volatile uint16_t*>(p) + row_at + c));
+        }
+        if (F32) {
+            r.q[0] = make_uint4(e[0], e[1], e[2], e[3]);
+            r.q[F32 ? 1 : 0] = make_uint4(e[4], e[5], e[6], e[7]);
+        } else {
+            r.q[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
+    }
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void widen_group(const NormRaw<F32>& r, float* f) {
+    if (F32) {
+        const uint4 a = r.q[0], b = r.q[F32 ? 1 : 0];
+        f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
+        f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+    } else {
+        widen8(r.q[0], f);
+    }
+}
+
+template <bool F32, bool VEC, int T>
+__device__ __forceinline__ void store_group(void* p, int64_t row_at, int cols, int lane, int v, const float* f) {
+    if (VEC) {
+        const int c = column_of<true, T>(lane, v, 0);
+        if (c >= cols) return;
+        unsigned char* at = static_cast<unsigned char*>(p) + (row_at + c) * (F32 ? 4 : 2);
+        if (F32) {
+            st_u4(at, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+            st_u4(at + 16, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+        } else {
+            st_u4(at, narrow8(f));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = column_of<false, T>(lane, v, j);
+            if (c >= cols) continue;
+            if (F32) static_cast<float*>(p)[row_at + c] = f[j];
+            else static_cast<__nv_bfloat16*>(p)[row_at + c] = __float2bfloat16_rn(f[j]);
+        }
+    }
+}
+
+// group v of a gain or bias
+template <bool VEC, int T>
+__device__ __forceinline__ void load_params(const void* p, int32_t f32, int cols, int lane, int v, float* f) {
+    if (f32) widen_group<true>(load_group<true, VEC, T>(p, 0, cols, lane, v), f);
+    else widen_group<false>(load_group<false, VEC, T>(p, 0, cols, lane, v), f);
+}
+
+// sums of a and b over the T threads of a row, the same in all of them; `sh`
+// holds two values per warp and is free again after the next call's barrier
+// (calls alternate between two halves of it)
+template <int T>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2* sh) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if (T == 32) return make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.0f;
+    const float2 w = (threadIdx.x & 31) < T / 32 ? sh[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+    a = w.x;
+    b = w.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    return make_float2(a, b);
+}
+
+template <int T>
+constexpr int norm_threads() { return T == 32 ? 256 : T; }
+
+template <bool F32, bool VEC, int T, int V>
+__global__ void __launch_bounds__(norm_threads<T>()) k_layer_norm(const __grid_constant__ NormArgs a) {
+    __shared__ float2 sh[2][32];
+    pdl_enter();
+    const int lane = int(threadIdx.x) % T;
+    const int64_t r = int64_t(blockIdx.x) * (norm_threads<T>() / T) + int(threadIdx.x) / T;
+    if (r >= a.rows) return;                       // a whole warp or CTA
+    const int64_t at = r * a.cols;
+    NormRaw<F32> raw[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, at, a.cols, lane, v);
+    float x[V][8], s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        widen_group<F32>(raw[v], x[v]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += x[v][j];
+    }
+    const float n = float(a.cols);
+    const float mean = row_sum<T>(s, 0.0f, sh[0]).x / n;
+    s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[v][j] = column_of<VEC, T>(lane, v, j) < a.cols ? x[v][j] - mean : 0.0f;
+            s = fmaf(x[v][j], x[v][j], s);
+        }
+    const float rstd = 1.0f / sqrtf(row_sum<T>(s, 0.0f, sh[1]).x / n + a.eps);
+    if (lane == 0 && a.mean) {
+        a.mean[r] = mean;
+        a.rstd[r] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float g[8], b[8];
+        if (a.gain) load_params<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
+        if (a.bias) load_params<VEC, T>(a.bias, a.params_f32, a.cols, lane, v, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[v][j] *= rstd;
+            if (a.gain) x[v][j] *= g[j];
+            if (a.bias) x[v][j] += b[j];
+        }
+        store_group<F32, VEC, T>(a.y, at, a.cols, lane, v, x[v]);
+    }
+}
+
+// The same for rows of any length, read three times.
+constexpr int kLongThreads = 1024;
+__device__ __forceinline__ float load_one(const void* p, int32_t f32, int64_t i) {
+    return f32 ? *(static_cast<const volatile float*>(p) + i)
+               : __uint_as_float(uint32_t(*(static_cast<const volatile uint16_t*>(p) + i)) << 16);
+}
+__device__ __forceinline__ void store_one(void* p, int32_t f32, int64_t i, float v) {
+    if (f32) static_cast<float*>(p)[i] = v;
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_constant__ NormArgs a, int32_t f32) {
+    __shared__ float2 sh[2][32];
+    pdl_enter();
+    const int64_t at = int64_t(blockIdx.x) * a.cols;
+    float s = 0.0f;
+    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) s += load_one(a.x, f32, at + c);
+    const float mean = row_sum<kLongThreads>(s, 0.0f, sh[0]).x / float(a.cols);
+    s = 0.0f;
+    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
+        const float d = load_one(a.x, f32, at + c) - mean;
+        s = fmaf(d, d, s);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<kLongThreads>(s, 0.0f, sh[1]).x / float(a.cols) + a.eps);
+    if (threadIdx.x == 0 && a.mean) {
+        a.mean[blockIdx.x] = mean;
+        a.rstd[blockIdx.x] = rstd;
+    }
+    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
+        float v = (load_one(a.x, f32, at + c) - mean) * rstd;
+        if (a.gain) v *= load_one(a.gain, a.params_f32, c);
+        if (a.bias) v += load_one(a.bias, a.params_f32, c);
+        store_one(a.y, f32, at + c, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  CTA p takes rows p, p + parts, ... (T = 32: its eight warps take
+// eight rows at a time); the next row is on its way while one is worked on.
+// ---------------------------------------------------------------------------
+template <bool F32, bool VEC, int T, int V>
+__global__ void __launch_bounds__(norm_threads<T>()) k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
+    constexpr int kRows = norm_threads<T>() / T;   // rows of a CTA at a time
+    __shared__ float2 sh[2][32];
+    __shared__ float sums[T == 32 ? 2 * T * V * 8 : 1];
+    pdl_enter();
+    const int lane = int(threadIdx.x) % T, group = int(threadIdx.x) / T;
+    const int64_t first = int64_t(blockIdx.x) * kRows + group, step = int64_t(gridDim.x) * kRows;
+    float dg[V][8], db[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[v][j] = db[v][j] = 0.0f;
+    NormRaw<F32> nx[V], ny[V];
+    float nmean = 0.0f, nrstd = 0.0f;
+    if (first < a.rows) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            nx[v] = load_group<F32, VEC, T>(a.x, first * a.cols, a.cols, lane, v);
+            ny[v] = load_group<F32, VEC, T>(a.dy, first * a.cols, a.cols, lane, v);
+        }
+        nmean = __ldg(a.mean + first);
+        nrstd = __ldg(a.rstd + first);
+    }
+    int half = 0;
+    for (int64_t r = first; r < a.rows; r += step, half ^= 1) {
+        float x[V][8], y[V][8];
+        const float mean = nmean, rstd = nrstd;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            widen_group<F32>(nx[v], x[v]);
+            widen_group<F32>(ny[v], y[v]);
+        }
+        if (r + step < a.rows) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                nx[v] = load_group<F32, VEC, T>(a.x, (r + step) * a.cols, a.cols, lane, v);
+                ny[v] = load_group<F32, VEC, T>(a.dy, (r + step) * a.cols, a.cols, lane, v);
+            }
+            nmean = __ldg(a.mean + r + step);
+            nrstd = __ldg(a.rstd + r + step);
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float g[8];
+            if (a.gain) load_params<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[v][j] = column_of<VEC, T>(lane, v, j) < a.cols ? (x[v][j] - mean) * rstd : 0.0f;
+                dg[v][j] = fmaf(y[v][j], x[v][j], dg[v][j]);
+                db[v][j] += y[v][j];
+                if (a.gain) y[v][j] *= g[j];
+                s1 += y[v][j];
+                s2 = fmaf(y[v][j], x[v][j], s2);
+            }
+        }
+        if (a.dx) {
+            const float2 t = row_sum<T>(s1, s2, sh[half]);
+            const float c1 = t.x / float(a.cols), c2 = t.y / float(a.cols);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[v][j] = rstd * (y[v][j] - c1 - x[v][j] * c2);
+                store_group<F32, VEC, T>(a.dx, r * a.cols, a.cols, lane, v, y[v]);
+            }
+        }
+    }
+    if (!a.part) return;
+    float* out = a.part + int64_t(blockIdx.x) * 2 * a.cols;
+    if (T == 32) {                                 // the warps' sums, in order
+        for (int w = 0; w < kRows; ++w) {
+            if (group == w) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float* p = sums + (v * 8 + j) * 32 + lane;
+                        float* q = p + T * V * 8;
+                        *p = w == 0 ? dg[v][j] : *p + dg[v][j];
+                        *q = w == 0 ? db[v][j] : *q + db[v][j];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int k = int(threadIdx.x); k < T * V * 8; k += norm_threads<T>()) {
+            const int c = column_of<VEC, T>(k & 31, k >> 8, (k >> 5) & 7);
+            if (c < a.cols) {
+                out[c] = sums[k];
+                out[a.cols + c] = sums[T * V * 8 + k];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = column_of<VEC, T>(lane, v, j);
+                if (c < a.cols) {
+                    out[c] = dg[v][j];
+                    out[a.cols + c] = db[v][j];
+                }
+            }
+    }
+}
+
+// Rows of any length: first the sums, CTA (columns, part) over rows part,
+// part + parts, ...; then dx, which may take the place of dy or x.
+__global__ void __launch_bounds__(256) k_layer_norm_columns(const __grid_constant__ NormBackArgs a, int32_t f32) {
+    pdl_enter();
+    const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (c >= a.cols) return;
+    float dg = 0.0f, db = 0.0f;
+    for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+        const float y = load_one(a.dy, f32, r * a.cols + c);
+        const float n = (load_one(a.x, f32, r * a.cols + c) - __ldg(a.mean + r)) * __ldg(a.rstd + r);
+        dg = fmaf(y, n, dg);
+        db += y;
+    }
+    float* out = a.part + int64_t(blockIdx.y) * 2 * a.cols;
+    out[c] = dg;
+    out[a.cols + c] = db;
+}
+
+__global__ void __launch_bounds__(kLongThreads) k_layer_norm_dx_long(const __grid_constant__ NormBackArgs a, int32_t f32) {
+    __shared__ float2 sh[32];
+    pdl_enter();
+    const int64_t r = blockIdx.x, at = r * a.cols;
+    const float mean = __ldg(a.mean + r), rstd = __ldg(a.rstd + r);
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
+        float g = load_one(a.dy, f32, at + c);
+        if (a.gain) g *= load_one(a.gain, a.params_f32, c);
+        s1 += g;
+        s2 = fmaf(g, (load_one(a.x, f32, at + c) - mean) * rstd, s2);
+    }
+    const float2 t = row_sum<kLongThreads>(s1, s2, sh);
+    const float c1 = t.x / float(a.cols), c2 = t.y / float(a.cols);
+    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
+        float g = load_one(a.dy, f32, at + c);
+        if (a.gain) g *= load_one(a.gain, a.params_f32, c);
+        const float n = (load_one(a.x, f32, at + c) - mean) * rstd;
+        store_one(a.dx, f32, at + c, rstd * (g - c1 - n * c2));
+    }
+}
+
+// Adds the parts in order: 32 columns to a CTA, 32 threads to a column, then
+// their sums along a fixed tree.
+struct NormSumArgs {
+    const float* part;
+    void* out[2];                  // dgain, dbias (either may be NULL)
+    int32_t parts, cols, f32, add;
+};
+__global__ void __launch_bounds__(1024) k_layer_norm_sums(const __grid_constant__ NormSumArgs a) {
+    __shared__ float sh[32][33];
+    pdl_enter();
+    const int64_t c = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31);
+    const int which = blockIdx.y, row = int(threadIdx.x >> 5);
+    if (!a.out[which]) return;
+    float s = 0.0f;
+    if (c < a.cols)
+#pragma unroll 4
+        for (int p = row; p < a.parts; p += 32) s += __ldcg(a.part + (int64_t(p) * 2 + which) * a.cols + c);
+    sh[row][threadIdx.x & 31] = s;
+    __syncthreads();
+    s = sh[threadIdx.x & 31][row];                 // warp `row` adds column `row`
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int64_t mine = int64_t(blockIdx.x) * 32 + row;
+    if ((threadIdx.x & 31) != 0 || mine >= a.cols) return;
+    if (a.f32) {
+        float* p = static_cast<float*>(a.out[which]) + mine;
+        *p = a.add ? *p + s : s;
+    } else {
+        static_cast<__nv_bfloat16*>(a.out[which])[mine] = __float2bfloat16_rn(s);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+static int norm_shape(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype, const char* who) {
+    if (rows < 0 || cols < 0 || rows > kNormMaxSide || cols > kNormMaxSide)
+        return fail(DPG_ERR_INVALID_ARG, "%s: %lld x %lld outside [0, 2^30]", who, (long long)rows, (long long)cols);
+    if (dtype != DPG_BF16 && dtype != DPG_F32) return fail(DPG_ERR_INVALID_ARG, "%s: dtype %d unknown", who, dtype);
+    if (param_dtype != DPG_BF16 && param_dtype != DPG_F32)
+        return fail(DPG_ERR_INVALID_ARG, "%s: param_dtype %d unknown", who, param_dtype);
+    return DPG_OK;
+}
+
+static int norm_pointer(const void* p, int32_t dtype, bool may_be_null, const char* name, const char* who) {
+    if (!p && !may_be_null) return fail(DPG_ERR_INVALID_ARG, "%s: %s is NULL", who, name);
+    if (!aligned(p, dtype == DPG_BF16 ? 2 : 4)) return fail(DPG_ERR_MISALIGNED, "%s: %s misaligned", who, name);
+    return DPG_OK;
+}
+
+// CTAs of a backward pass, which leave as many parts: one for 1, 8, ... rows
+static int norm_parts(int64_t rows, int64_t cols) {
+    const int64_t groups = cols <= 1024 ? (rows + 7) / 8 : rows;
+    return int(groups < 1 ? 1 : groups < kNormParts ? groups : kNormParts);
+}
+
+template <int T, int V>
+static int launch_norm(const NormArgs& a, bool f32, bool vec, cudaStream_t s, const char* who) {
+    constexpr int per = norm_threads<T>() / T;
+    auto k = f32 ? (vec ? k_layer_norm<true, true, T, V> : k_layer_norm<true, false, T, V>)
+                 : (vec ? k_layer_norm<false, true, T, V> : k_layer_norm<false, false, T, V>);
+    return launch_k(k, unsigned((a.rows + per - 1) / per), norm_threads<T>(), s, who, a);
+}
+
+template <int T, int V>
+static int launch_back(const NormBackArgs& a, bool f32, bool vec, cudaStream_t s, const char* who) {
+    auto k = f32 ? (vec ? k_layer_norm_back<true, true, T, V> : k_layer_norm_back<true, false, T, V>)
+                 : (vec ? k_layer_norm_back<false, true, T, V> : k_layer_norm_back<false, false, T, V>);
+    return launch_k(k, unsigned(a.parts), norm_threads<T>(), s, who, a);
+}
+
+}  // namespace dpg
+
+using dpg::fail;
+
+extern "C" {
+
+int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, const void* gain, const void* bias,
+                   int32_t param_dtype, double eps, void* y, float* mean, float* rstd, void* stream) {
+    dpg::clear_error();
+    const char* who = "dpg_layer_norm";
+    const dpg::Trace trace(who);
+    int st = dpg::norm_shape(rows, cols, dtype, param_dtype, who);
+    if (st != DPG_OK) return st;
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(DPG_ERR_INVALID_ARG, "%s: eps %g", who, eps);
+    if ((mean == nullptr) != (rstd == nullptr))
+        return fail(DPG_ERR_INVALID_ARG, "%s: mean and rstd are kept together", who);
+    if (rows == 0 || cols == 0) return DPG_OK;
+    st = dpg::norm_pointer(x, dtype, false, "x", who);
+    if (st == DPG_OK) st = dpg::norm_pointer(y, dtype, false, "y", who);
+    if (st == DPG_OK) st = dpg::norm_pointer(gain, param_dtype, true, "gain", who);
+    if (st == DPG_OK) st = dpg::norm_pointer(bias, param_dtype, true, "bias", who);
+    if (st == DPG_OK) st = dpg::norm_pointer(mean, DPG_F32, true, "mean", who);
+    if (st == DPG_OK) st = dpg::norm_pointer(rstd, DPG_F32, true, "rstd", who);
+    if (st != DPG_OK) return st;
+    dpg::NormArgs a{};
+    a.x = x;
+    a.gain = gain;
+    a.bias = bias;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.cols = int32_t(cols);
+    a.params_f32 = param_dtype == DPG_F32;
+    a.eps = float(eps);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f32 = dtype == DPG_F32;
+    const bool vec = cols % 8 == 0 && dpg::aligned(x, 16) && dpg::aligned(y, 16) && dpg::aligned(gain, 16) &&
+                     dpg::aligned(bias, 16);
+    if (cols <= 256) return dpg::launch_norm<32, 1>(a, f32, vec, s, who);
+    if (cols <= 512) return dpg::launch_norm<32, 2>(a, f32, vec, s, who);
+    if (cols <= 1024) return dpg::launch_norm<32, 4>(a, f32, vec, s, who);
+    if (cols <= 2048) return dpg::launch_norm<128, 2>(a, f32, vec, s, who);
+    if (cols <= 4096) return dpg::launch_norm<256, 2>(a, f32, vec, s, who);
+    if (cols <= 8192) return dpg::launch_norm<512, 2>(a, f32, vec, s, who);
+    if (cols <= 16384) return dpg::launch_norm<1024, 2>(a, f32, vec, s, who);
+    if (cols <= 32768) return dpg::launch_norm<1024, 4>(a, f32, vec, s, who);
+    return dpg::launch_k(dpg::k_layer_norm_long, unsigned(rows), dpg::kLongThreads, s, who, a, int32_t(f32));
+}
+
+int64_t dpg_layer_norm_workspace(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0 || rows > dpg::kNormMaxSide || cols > dpg::kNormMaxSide) return 0;
+    return int64_t(dpg::norm_parts(rows, cols)) * 2 * cols * int64_t(sizeof(float));
+}
+
+int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t rows, int64_t cols,
+                            const void* gain, int32_t param_dtype, const float* mean, const float* rstd, void* dx,
+                            void* dgain, void* dbias, int32_t grad_dtype, int32_t accumulate, void* workspace,
+                            void* stream) {
+    dpg::clear_error();
+    const char* who = "dpg_layer_norm_backward";
+    const dpg::Trace trace(who);
+    int st = dpg::norm_shape(rows, cols, dtype, param_dtype, who);
+    if (st != DPG_OK) return st;
+    if (grad_dtype != DPG_BF16 && grad_dtype != DPG_F32)
+        return fail(DPG_ERR_INVALID_ARG, "%s: grad_dtype %d unknown", who, grad_dtype);
+    if (accumulate && grad_dtype != DPG_F32)
+        return fail(DPG_ERR_INVALID_ARG, "%s: only fp32 gradients are added to", who);
+    const bool sums = dgain || dbias;
+    if (cols == 0 || (rows == 0 && (!sums || accumulate))) return DPG_OK;
+    if (rows > 0) {
+        st = dpg::norm_pointer(dy, dtype, false, "dy", who);
+        if (st == DPG_OK) st = dpg::norm_pointer(x, dtype, false, "x", who);
+        if (st == DPG_OK) st = dpg::norm_pointer(gain, param_dtype, true, "gain", who);
+        if (st == DPG_OK) st = dpg::norm_pointer(mean, DPG_F32, false, "mean", who);
+        if (st == DPG_OK) st = dpg::norm_pointer(rstd, DPG_F32, false, "rstd", who);
+        if (st == DPG_OK) st = dpg::norm_pointer(dx, dtype, true, "dx", who);
+    }
+    if (st == DPG_OK) st = dpg::norm_pointer(dgain, grad_dtype, true, "dgain", who);
+    if (st == DPG_OK) st = dpg::norm_pointer(dbias, grad_dtype, true, "dbias", who);
+    if (st != DPG_OK) return st;
+    if (sums && !workspace) return fail(DPG_ERR_INVALID_ARG, "%s: workspace is NULL", who);
+    if (sums && !dpg::aligned(workspace, 16)) return fail(DPG_ERR_MISALIGNED, "%s: workspace misaligned", who);
+    if (!sums && !dx) return DPG_OK;
+    dpg::NormBackArgs a{};
+    a.dy = dy;
+    a.x = x;
+    a.gain = gain;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.dx = dx;
+    a.part = sums ? static_cast<float*>(workspace) : nullptr;
+    a.rows = rows;
+    a.cols = int32_t(cols);
+    a.params_f32 = param_dtype == DPG_F32;
+    a.parts = dpg::norm_parts(rows, cols);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f32 = dtype == DPG_F32;
+    const bool vec = cols % 8 == 0 && dpg::aligned(x, 16) && dpg::aligned(dy, 16) && dpg::aligned(dx, 16) &&
+                     dpg::aligned(gain, 16);
+    if (cols <= 256) st = dpg::launch_back<32, 1>(a, f32, vec, s, who);
+    else if (cols <= 512) st = dpg::launch_back<32, 2>(a, f32, vec, s, who);
+    else if (cols <= 768) st = dpg::launch_back<32, 3>(a, f32, vec, s, who);
+    else if (cols <= 1024) st = dpg::launch_back<32, 4>(a, f32, vec, s, who);
+    else if (cols <= 2048) st = dpg::launch_back<256, 1>(a, f32, vec, s, who);
+    else if (cols <= 4096) st = dpg::launch_back<512, 1>(a, f32, vec, s, who);
+    else if (cols <= 8192) st = dpg::launch_back<512, 2>(a, f32, vec, s, who);
+    else if (cols <= 16384) st = dpg::launch_back<1024, 2>(a, f32, vec, s, who);
+    else {
+        if (sums) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(unsigned((cols + 255) / 256), unsigned(a.parts));
+            cfg.blockDim = dim3(256);
+            cfg.stream = s;
+            const cudaError_t e = cudaLaunchKernelEx(&cfg, dpg::k_layer_norm_columns, a, int32_t(f32));
+            if (e != cudaSuccess) {
+                (void)cudaGetLastError();
+                return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+            }
+            st = dpg::after_launch(who);
+        }
+        if (st == DPG_OK && dx && rows > 0)
+            st = dpg::launch_k(dpg::k_layer_norm_dx_long, unsigned(rows), dpg::kLongThreads, s, who, a, int32_t(f32));
+    }
+    if (st != DPG_OK || !sums) return st;
+    dpg::NormSumArgs t{};
+    t.part = a.part;
+    t.out[0] = dgain;
+    t.out[1] = dbias;
+    t.parts = a.parts;
+    t.cols = a.cols;
+    t.f32 = grad_dtype == DPG_F32;
+    t.add = accumulate != 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((cols + 31) / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dpg::t_programmatic ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, dpg::k_layer_norm_sums, t);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    }
+    return dpg::after_launch(who);
+}
+
+}  // extern "C"

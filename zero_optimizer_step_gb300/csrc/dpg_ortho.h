@@ -129,6 +129,7 @@ struct Matrices {
     int64_t total_padded = 0;
     int32_t n_params = 0;
     std::vector<int64_t> param_offset, numels;
+    std::vector<int32_t> rows, cols;   // of each parameter's matrices
     std::vector<MatDesc> mats;
     std::vector<OrthoTile> queue;      // tiles of a step, pair after pair (see lay_queue)
     std::vector<int32_t> queue_first;  // pairs + 1
