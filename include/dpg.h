@@ -603,7 +603,8 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
  *   DPG_NVFP4  16 elements to an E4M3 scale, and one power of two 2^e for the
  *              whole matrix: value = 2^e * scale * code
  *   DPG_MXFP4  32 elements to an E8M0 scale: value = scale * code
- * with codes E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign).  Values are exact in
+ * with codes E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign; an element that is -0
+ * may have either zero's code).  Values are exact in
  * bf16 and fp32 down to their subnormal numbers.
  * A block's scale is the least of its type with max|x| <= 6 * scale * 2^e, so
  * no element saturates; e is the least with amax <= 6 * 448 * 2^e and e >=

@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
         if (r < a.rows && c < a.cols) {
             unsigned char* p = a.row.codes + r * a.row.pitch + (c >> 1);
             if (MX) *reinterpret_cast<uint4*>(p) = make_uint4(codes[0], codes[1], codes[B / 8 - 2], codes[B / 8 - 1]);
+            else if ((blk & 1) == 0 && c + B >= a.cols) *reinterpret_cast<uint4*>(p) = make_uint4(codes[0], codes[1], 0, 0);
             else *reinterpret_cast<uint2*>(p) = make_uint2(codes[0], codes[1]);
         }
         sc[0][(blk >> 2) * kFp4TileBytes + (row & 31) * 16 + (row >> 5) * 4 + (blk & 3)] =
