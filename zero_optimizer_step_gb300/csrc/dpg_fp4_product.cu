@@ -48,6 +48,7 @@ struct ProductArgs {
 
 struct ProductMaps {
     CUtensorMap codes_r, codes_c, scales_r, scales_c;
+    CUtensorMap result;          // C, where its rows start on 16-byte boundaries (large products)
 };
 
 // ---------------------------------------------------------------------------
@@ -71,6 +72,14 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
         }
     }
     return true;
+}
+// One lane of a warp.  What the warp computes before it stays in uniform
+// registers, where the instructions want their operands: under `lane == 0` each
+// was moved there on its own, 74 cycles to a copy of scales.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void copy_tile(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -117,9 +126,9 @@ __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uin
 }
 // 512 bytes of scales to four columns of tensor memory
 template <bool PAIR>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
-    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(scales_desc(smem)) : "memory");
-    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(scales_desc(smem)) : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t smem) {
+    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(smem) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(smem) : "memory");
 }
 // arrives at `bar` once everything issued so far is done (PAIR: in both CTAs)
 template <bool PAIR>
@@ -132,30 +141,36 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                      :: "r"(smem_u32(bar)) : "memory");
 }
 
-// One stage's products: up to 4 of 64 elements, scales first.  `at`: the stage
+// One stage's products: `steps` of 64 elements, scales first.  `at`: the stage
 // (codes of the rows, of the columns, scales of the rows, of the columns), COLS:
 // columns of the instruction, CODES: bytes of the columns' codes in this CTA.
-template <bool MX, bool PAIR, int COLS, int CODES>
-__device__ __forceinline__ void multiply_stage(uint32_t at, uint32_t d, uint32_t sf, int steps, bool fresh) {
-    constexpr int kColTiles = COLS > 128 ? 2 : 1;
-    const uint32_t sr = at + kRowTile * kCodeRow + CODES, sc = sr + kScaleBytes;
+template <bool MX, bool PAIR, int COLS, int CODES, int STEPS>
+__device__ __forceinline__ void multiply_steps(uint32_t at, uint32_t d, uint32_t sf, bool fresh) {
+    constexpr int kColTiles = COLS > 128 ? 2 : 1, kTiles = MX ? (STEPS + 1) / 2 : STEPS;
+    constexpr int kSr = kRowTile * kCodeRow + CODES, kSc = kSr + kScaleBytes;
     const uint32_t tr = sf, tc = sf + 16;            // columns: 4 a tile of the rows, 4 or 8 of the columns
-    const int tiles = MX ? (steps + 1) >> 1 : steps;
-    for (int t = 0; t < tiles; ++t) {
-        copy_scales<PAIR>(tr + 4 * t, sr + t * kFp4TileBytes);
+    const uint64_t scales = scales_desc(at), a = codes_desc(at);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        copy_scales<PAIR>(tr + 4 * t, scales + (kSr + t * kFp4TileBytes) / 16);
 #pragma unroll
         for (int q = 0; q < kColTiles; ++q)
-            copy_scales<PAIR>(tc + 4 * (kColTiles * t + q), sc + (q * (MX ? 2 : 4) + t) * kFp4TileBytes);
+            copy_scales<PAIR>(tc + 4 * (kColTiles * t + q), scales + (kSc + (q * (MX ? 2 : 4) + t) * kFp4TileBytes) / 16);
     }
-    const uint64_t a = codes_desc(at), b = codes_desc(at + kRowTile * kCodeRow);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < steps) {
-            const int t = MX ? k >> 1 : k;
-            const uint32_t id = MX ? 2u * uint32_t(k & 1) : 0u;
-            multiply<MX, PAIR>(d, a + 2 * k, b + 2 * k, product_shape<MX>(PAIR ? 256 : 128, COLS, id), tr + 4 * t,
-                               tc + 4 * kColTiles * t, !fresh || k > 0);
-        }
+    for (int k = 0; k < STEPS; ++k) {
+        const int t = MX ? k >> 1 : k;
+        multiply<MX, PAIR>(d, a + 2 * k, a + kRowTile * kCodeRow / 16 + 2 * k,
+                           product_shape<MX>(PAIR ? 256 : 128, COLS, MX ? 2u * uint32_t(k & 1) : 0u), tr + 4 * t,
+                           tc + 4 * kColTiles * t, !fresh || k > 0);
+    }
+}
+template <bool MX, bool PAIR, int COLS, int CODES>
+__device__ __forceinline__ void multiply_stage(uint32_t at, uint32_t d, uint32_t sf, int steps, bool fresh) {
+    if (steps >= 4) multiply_steps<MX, PAIR, COLS, CODES, 4>(at, d, sf, fresh);
+    else if (steps == 3) multiply_steps<MX, PAIR, COLS, CODES, 3>(at, d, sf, fresh);
+    else if (steps == 2) multiply_steps<MX, PAIR, COLS, CODES, 2>(at, d, sf, fresh);
+    else multiply_steps<MX, PAIR, COLS, CODES, 1>(at, d, sf, fresh);
 }
 
 // ---------------------------------------------------------------------------
@@ -178,35 +193,28 @@ __device__ __forceinline__ ProductScale product_scale(const ProductArgs& a) {
     return s;
 }
 
-// N (a multiple of 8) neighbouring sums of row `r`, columns from c on, into C
-template <int N>
-__device__ __forceinline__ void store_along(const ProductArgs& a, const ProductScale& s, int r, int c, const float* v) {
+// four neighbouring results of C's row r, from column c on (a multiple of 4)
+__device__ __forceinline__ void store_four(const ProductArgs& a, int r, int c, const float* x) {
     if (r >= a.m || c >= a.n) return;
     const int64_t at = int64_t(r) * a.stride + c;
-    float x[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = v[j] * s.f[0] * s.f[1];
-    if (a.vec && c + N <= a.n) {
+    if (a.vec && c + 4 <= a.n) {
         if (a.c_f32) {
-            float* p = static_cast<float*>(a.c) + at;
-#pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                float4 y = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                if (a.add) {
-                    const float4 o = *reinterpret_cast<const float4*>(p + j);
-                    y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
-                }
-                *reinterpret_cast<float4*>(p + j) = y;
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.c) + at);
+            float4 y = make_float4(x[0], x[1], x[2], x[3]);
+            if (a.add) {
+                const float4 o = *p;
+                y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
             }
+            *p = y;
         } else {
-            uint16_t* p = static_cast<uint16_t*>(a.c) + at;
-#pragma unroll
-            for (int j = 0; j < N; j += 8) *reinterpret_cast<uint4*>(p + j) = narrow8(x + j);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.c) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
         }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < 4; ++j)
         if (c + j < a.n) {
             if (a.c_f32) {
                 float* p = static_cast<float*>(a.c) + at + j;
@@ -217,11 +225,10 @@ __device__ __forceinline__ void store_along(const ProductArgs& a, const ProductS
         }
 }
 
-// one sum, element (r, c) of C
-__device__ __forceinline__ void store_one(const ProductArgs& a, const ProductScale& s, int r, int c, float v) {
+// one result
+__device__ __forceinline__ void store_one(const ProductArgs& a, int r, int c, float x) {
     if (r >= a.m || c >= a.n) return;
     const int64_t at = int64_t(r) * a.stride + c;
-    const float x = v * s.f[0] * s.f[1];
     if (a.c_f32) {
         float* p = static_cast<float*>(a.c) + at;
         *p = a.add ? *p + x : x;
@@ -230,21 +237,22 @@ __device__ __forceinline__ void store_one(const ProductArgs& a, const ProductSca
     }
 }
 
-// N sums of row r of the product as it is computed, from column c on
-template <int N>
-__device__ __forceinline__ void store_sums(const ProductArgs& a, const ProductScale& s, int r, int c, const float* v) {
-    if (a.swap) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) store_one(a, s, c + j, r, v[j]);
-    } else {
-        store_along<N>(a, s, r, c, v);
-    }
+// Sums leave tensor memory a row to a lane; stored so, each access of a warp is
+// 32 lines of memory (4 us for a tile of 128 x 256 where its products take 4 at
+// k = 4096).  They go through shared memory, rows of COLS values in 16-byte
+// pieces whose order within the row goes by the row, so that both a column of
+// pieces and a row of them lie in different banks.
+template <int COLS>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    constexpr int kMask = COLS >= 32 ? 7 : 3;
+    return row * COLS + ((piece ^ ((COLS >= 32 ? row : row >> 1) & kMask)) << 2);
 }
 
 // ---------------------------------------------------------------------------
 // Small products: 128 x COLS sums to a CTA.  Where there are few tiles, the CTAs
 // of a cluster share the sum, leave their parts in shared memory and add them in
-// the order of their ranks, each a share of the columns.
+// the order of their ranks, each a share of the rows (or, where C's rows run along
+// the tile's columns, of the columns).
 //
 // Two CTAs fit an SM and hold at most 256 of its 512 columns of tensor memory
 // each; beside the CTAs of the large product and of the orthogonalisation
@@ -272,6 +280,23 @@ struct SmallShared {
     volatile int abort;
 };
 
+// of CTA q's shared memory (`split` == 1: this CTA's)
+__device__ __forceinline__ float load_part(uint32_t at, int q, int split) {
+    float x;
+    if (split == 1) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    else asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to(at, uint32_t(q))) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 load_part4(uint32_t at, int q, int split) {
+    float4 x;
+    if (split == 1)
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(map_to(at, uint32_t(q))) : "memory");
+    return x;
+}
+
 template <bool MX, int COLS>
 __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_constant__ ProductArgs a,
                                                              const __grid_constant__ ProductMaps maps) {
@@ -280,7 +305,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
     extern __shared__ __align__(1024) unsigned char dyn[];
     SmallShared& sh = *reinterpret_cast<SmallShared*>(dyn + kStages * S::kStage);
     const uint32_t stage0 = smem_u32(dyn);
-    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = int(threadIdx.x & 31);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -324,44 +349,50 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
                 par ^= 1;
             }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
+        const bool mine = elect_one();
         int s = 0;
         uint32_t par = 0;
         bool ok = true;
         for (int k = first; k < last; ++k) {
-            if (!(ok = wait_phase(&sh.full[s], par, &sh.abort, a.wait_ns))) break;
+            ok = wait_phase(&sh.full[s], par, &sh.abort, a.wait_ns);
+            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const int left = a.k - k * kProdDepth, steps = left >= kProdDepth ? 4 : (left + 63) >> 6;
-            multiply_stage<MX, false, COLS, S::kCodes>(stage0 + uint32_t(s) * S::kStage, tmem,
-                                                       tmem + S::kScaleColumn + 32 * (k & 1), steps, k == first);
-            commit<false>(&sh.empty[s]);
+            if (mine) {
+                multiply_stage<MX, false, COLS, S::kCodes>(stage0 + uint32_t(s) * S::kStage, tmem,
+                                                           tmem + S::kScaleColumn + 32 * (k & 1), steps, k == first);
+                commit<false>(&sh.empty[s]);
+            }
+            __syncwarp();
             if (++s == kStages) {
                 s = 0;
                 par ^= 1;
             }
         }
-        if (ok) commit<false>(&sh.done);
+        if (ok && mine) commit<false>(&sh.done);
     }
     __syncwarp();
+    float* const part = reinterpret_cast<float*>(dyn);
     if (warp >= 2) {
         const int row = (warp & 3) * 32 + lane;
-        const ProductScale scale = product_scale<MX>(a);
         const bool ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.done, 0, &sh.abort, a.wait_ns));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t sums = tmem + (uint32_t((warp & 3) * 32) << 16);
         constexpr int kGroup = COLS < 32 ? COLS : 32;
-        if (ok)
+        if (ok)                                             // the stages are free: every product is done
 #pragma unroll 1
             for (int c = 0; c < COLS; c += 32) {
                 float v[32];
                 load_acc32(sums + c, v);                    // (COLS = 16: with 16 unused columns)
-                if (a.split == 1) {
-                    store_sums<kGroup>(a, scale, r0 + row, c0 + c, v);
-                } else {
-                    // the stages are free: every product of this CTA is done
-                    float* part = reinterpret_cast<float*>(dyn) + row;
+                if (a.swap) {
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j) part[(c + j) * kRowTile] = v[j];
+                    for (int j = 0; j < kGroup; ++j) part[(c + j) * kRowTile + row] = v[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kGroup; j += 4)
+                        *reinterpret_cast<float4*>(part + piece_at<COLS>(row, (c + j) >> 2)) =
+                            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
             }
     }
@@ -371,40 +402,33 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (a.split > 1) {
-        cluster_sync();
-        if (warp >= 2 && !sh.abort) {
-            const int row = (warp & 3) * 32 + lane, share = COLS / a.split, from = rank * share;
-            const ProductScale scale = product_scale<MX>(a);
-            for (int c = from; c < from + share; c += 8) {
-                const int some = share < 8 ? share : 8;
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (a.split > 1) cluster_sync();
+    if (!sh.abort) {
+        const ProductScale scale = product_scale<MX>(a);
+        const uint32_t part0 = smem_u32(part);
+        if (a.swap) {                                       // columns of sums: neighbours in C's rows
+            const int share = COLS / a.split, from = rank * share * kRowTile;
+            for (int e = int(threadIdx.x); e < share * kRowTile; e += kSmallThreads) {
+                float x = 0.0f;
+                for (int q = 0; q < a.split; ++q) x += load_part(part0 + uint32_t(from + e) * 4, q, a.split);
+                store_one(a, c0 + (from + e) / kRowTile, r0 + (from + e) % kRowTile, x * scale.f[0] * scale.f[1]);
+            }
+        } else {
+            const int share = kRowTile / a.split, from = rank * share;
+            for (int e = int(threadIdx.x); e < share * (COLS / 4); e += kSmallThreads) {
+                const int row = from + e / (COLS / 4), piece = e % (COLS / 4);
+                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int q = 0; q < a.split; ++q) {
-                    const uint32_t part = map_to(stage0 + uint32_t(c * kRowTile + row) * 4, uint32_t(q));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < some) {
-                            float x;
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(part + j * kRowTile * 4) : "memory");
-                            v[j] += x;
-                        }
+                    const float4 y = load_part4(part0 + uint32_t(piece_at<COLS>(row, piece)) * 4, q, a.split);
+                    x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
                 }
-                if (some == 8) {
-                    store_sums<8>(a, scale, r0 + row, c0 + c, v);
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < some) {
-                            if (a.swap) store_one(a, scale, c0 + c + j, r0 + row, v[j]);
-                            else store_one(a, scale, r0 + row, c0 + c + j, v[j]);
-                        }
-                }
+                for (int j = 0; j < 4; ++j) x[j] = x[j] * scale.f[0] * scale.f[1];
+                store_four(a, r0 + row, c0 + 4 * piece, x);
             }
         }
-        cluster_sync();                                     // the others have read this CTA's part
     }
+    if (a.split > 1) cluster_sync();                        // the others have read this CTA's part
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(S::kColumns) : "memory");
 }
@@ -420,7 +444,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
 // start when the 96 columns that both sums have are stored, which is done first.
 //
 //   warp 0  copies operands     warp 1  of CTA 0: issues the products
-//   warps 2..9  store (warp w: lanes 32 (w mod 4) .., every other 32 columns)
+//   warps 2..9  store (warp w: lanes 32 (w mod 4) .., every other 32 columns):
+//               32 x 32 sums to 4 KB of shared memory and from there by bulk
+//               copies of 32 rows x 64 bytes, added to C where they are to be, or
+//               singly where C's rows do not start on 16-byte boundaries
 // ---------------------------------------------------------------------------
 constexpr int kLargeStages = 5;
 constexpr int kLargeCodes = kRowTile * kCodeRow;
@@ -434,7 +461,8 @@ struct LargeShared {
     uint32_t tmem;
     volatile int abort;
 };
-constexpr int kLargeSmem = kLargeStages * kLargeStage + int(sizeof(LargeShared));
+constexpr int kStoreBytes = 4096;                // of a storing warp: two boxes, or 32 x 32 sums
+constexpr int kLargeSmem = kLargeStages * kLargeStage + kLargeEpiWarps * kStoreBytes + int(sizeof(LargeShared));
 static_assert(kLargeStage % 1024 == 0, "the swizzle's boundary");
 static_assert(kLargeSmem <= 227 * 1024 && kLargeSmem + 78 * 1024 > 228 * 1024, "alone on its SM");
 
@@ -447,13 +475,66 @@ __device__ __forceinline__ void large_tile(const ProductArgs& a, int t, int& r0,
     c0 = in / high * kLargeTile;
 }
 
+// A warp's 32 x 32 results (lane: row) by bulk copies: boxes of 32 rows x 64
+// bytes with a 64-byte swizzle, in two halves of the warp's shared memory in turn.
+__device__ __forceinline__ void store_boxes(const ProductArgs& a, const CUtensorMap* map, uint32_t smem, int lane, int r,
+                                            int c, const float* v, uint32_t& boxes) {
+    const int n = a.c_f32 ? 2 : 1, width = a.c_f32 ? 16 : 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h >= n || c + h * width >= a.n) break;
+        const uint32_t at = smem + (boxes++ & 1) * (kStoreBytes / 2), row = at + uint32_t(lane) * 64;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // what it held is on its way
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t to = row + (uint32_t(j) ^ (uint32_t(lane) >> 1 & 3u)) * 16;
+            uint4 w;
+            if (a.c_f32) {
+                w = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
+                               __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
+            } else {
+                w = narrow8(v + 8 * j);
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(to), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (a.add)
+                asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
+                             :: "l"(map), "r"(c + h * width), "r"(r), "r"(at) : "memory");
+            else
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                             :: "l"(map), "r"(c + h * width), "r"(r), "r"(at) : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+// the same, four columns of four rows to a lane group, any alignment
+__device__ __forceinline__ void store_singly(const ProductArgs& a, float* box, int lane, int r, int c, const float* v) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(box + piece_at<32>(lane, j >> 2)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3), piece = lane & 7;
+        const float4 y = *reinterpret_cast<const float4*>(box + piece_at<32>(row, piece));
+        const float x[4] = {y.x, y.y, y.z, y.w};
+        store_four(a, r + row, c + 4 * piece, x);
+    }
+}
+
 template <bool MX>
 __global__ void __cluster_dims__(2) __launch_bounds__(kLargeThreads, 1)
 k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ ProductMaps maps) {
     extern __shared__ __align__(1024) unsigned char dyn[];
-    LargeShared& sh = *reinterpret_cast<LargeShared*>(dyn + kLargeStages * kLargeStage);
+    LargeShared& sh =
+        *reinterpret_cast<LargeShared*>(dyn + kLargeStages * kLargeStage + kLargeEpiWarps * kStoreBytes);
     const uint32_t stage0 = smem_u32(dyn);
-    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = int(threadIdx.x & 31);
     const uint32_t rank = cluster_rank();
     const int pair = int(blockIdx.x >> 1), pairs = int(gridDim.x >> 1);
     if (threadIdx.x == 0) {
@@ -505,38 +586,46 @@ k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ Produ
                 }
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        const bool mine = elect_one();
         int s = 0, it = 0;
         uint32_t par = 0, set = 0;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, ++it) {
-            if (it > 0 && !(ok = wait_phase(&sh.clear, uint32_t(it - 1) & 1u, &sh.abort, a.wait_ns))) break;
+            if (it > 0) ok = wait_phase(&sh.clear, uint32_t(it - 1) & 1u, &sh.abort, a.wait_ns);
+            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + uint32_t(it & 1) * (kLargeTile - kOverlap);
             for (int k = 0; k < stages; ++k, set ^= 1) {
-                if (!(ok = wait_phase(&sh.full[s], par, &sh.abort, a.wait_ns))) break;
+                ok = wait_phase(&sh.full[s], par, &sh.abort, a.wait_ns);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const int left = a.k - k * kProdDepth, steps = left >= kProdDepth ? 4 : (left + 63) >> 6;
-                multiply_stage<MX, true, kLargeTile, kLargeCodes>(stage0 + uint32_t(s) * kLargeStage, d,
-                                                                  tmem + 2 * kLargeTile - kOverlap + 48 * set, steps,
-                                                                  k == 0);
-                commit<true>(&sh.empty[s]);
+                if (mine) {
+                    multiply_stage<MX, true, kLargeTile, kLargeCodes>(stage0 + uint32_t(s) * kLargeStage, d,
+                                                                      tmem + 2 * kLargeTile - kOverlap + 48 * set,
+                                                                      steps, k == 0);
+                    commit<true>(&sh.empty[s]);
+                }
+                __syncwarp();
                 if (++s == kLargeStages) {
                     s = 0;
                     par ^= 1;
                 }
             }
-            if (ok) commit<true>(&sh.done[it & 1]);
+            if (ok && mine) commit<true>(&sh.done[it & 1]);
         }
     } else if (warp >= 2) {
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const ProductScale scale = product_scale<MX>(a);
         const uint32_t clear = map_to(smem_u32(&sh.clear), 0);
+        float* const box = reinterpret_cast<float*>(dyn + kLargeStages * kLargeStage + (warp - 2) * kStoreBytes);
+        uint32_t boxes = 0;                          // stored so far
         int it = 0;
         for (int t = pair; t < tiles; t += pairs, ++it) {
             int r0, c0;
             large_tile(a, t, r0, c0);
-            const int r = r0 + int(rank) * kRowTile + quad * 32 + lane;
+            const int r = r0 + int(rank) * kRowTile + quad * 32;
             const bool ok = wait_phase(&sh.done[it & 1], uint32_t(it >> 1) & 1u, &sh.abort, a.wait_ns);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -554,9 +643,15 @@ k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ Produ
                     if (lane == 0)
                         asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(clear) : "memory");
                 }
-                store_along<32>(a, scale, r, c0 + c, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = v[j] * scale.f[0] * scale.f[1];
+                if (r < a.m && c0 + c < a.n) {       // the warp's first row
+                    if (a.vec) store_boxes(a, &maps.result, smem_u32(box), lane, r, c0 + c, v, boxes);
+                    else store_singly(a, box, lane, r, c0 + c, v);
+                }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     if (sh.abort) {   // the copies this CTA has in flight land within this time
@@ -686,6 +781,19 @@ static int launch_large(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     int st = encode_operand(r, kRowTile, 1, &maps.codes_r, &maps.scales_r, who);
     if (st == DPG_OK) st = encode_operand(c, kRowTile, 2, &maps.codes_c, &maps.scales_c, who);
     if (st != DPG_OK) return st;
+    if (a.vec) {
+        EncodeTiled fn = nullptr;
+        st = encoder(&fn, who);
+        if (st != DPG_OK) return st;
+        const int size = a.c_f32 ? 4 : 2;
+        const cuuint64_t dims[2] = {cuuint64_t(a.n), cuuint64_t(a.m)};
+        const cuuint64_t pitch[1] = {cuuint64_t(a.stride) * size};
+        const cuuint32_t box[2] = {cuuint32_t(64 / size), 32}, step[2] = {1, 1};
+        const CUresult e = fn(&maps.result, a.c_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              2, a.c, dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (e != CUDA_SUCCESS) return fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
+    }
     const int pairs = int(tiles < sms / 2 ? tiles : sms / 2);
     DPG_CUDA_TRY(cudaFuncSetAttribute(k_fp4_large<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLargeSmem));
     return launch_k(k_fp4_large<MX>, unsigned(2 * pairs), kLargeThreads, size_t(kLargeSmem), s, who, a, maps);
@@ -700,8 +808,8 @@ static int product(const dpg_fp4* x, const dpg_fp4* w, ProductArgs a, cudaStream
     const int64_t large = (int64_t(a.m) + kLargeTile - 1) / kLargeTile * ((int64_t(a.n) + kLargeTile - 1) / kLargeTile);
     a.rows = a.m;
     a.cols = a.n;
-    if (large >= sms / 2) return launch_large<MX>(a, x, w, sms, s, who);
     const int few = a.m < a.n ? a.m : a.n;
+    if (few > kRowTile && large >= sms / 2) return launch_large<MX>(a, x, w, sms, s, who);
     if (few > 64) return launch_small<MX, 128>(a, x, w, sms, s, who);
     // the shorter side in the columns of the sums
     a.swap = a.m < a.n;
