@@ -619,13 +619,15 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
  *           bytes each, tile (i, j) at (i * ceil(blocks / 4) + j) * 512, in it
  *           row r, block b at (r % 32) * 16 + (r / 32) * 4 + b; zeros behind
  *           the last row and block (the layout that the tensor cores copy)
- *   amax    one float, DPG_NVFP4 only (the largest finite |x|, from which a
- *           reader derives e); may be NULL for DPG_MXFP4
+ *   amax    DPG_FP4_AMAX_FLOATS floats, DPG_NVFP4 only: the first is the largest
+ *           finite |x|, from which a reader derives e, the others are room that
+ *           the quantisation works in; may be NULL for DPG_MXFP4
  * 0 <= rows, cols <= 2^30.
  * dpg_fp4_sizes: bytes of its codes and scales (either pointer may be NULL).
  * ------------------------------------------------------------------------- */
 #define DPG_NVFP4 0
 #define DPG_MXFP4 1
+#define DPG_FP4_AMAX_FLOATS 256
 typedef struct {
     void* codes;
     void* scales;

@@ -103,7 +103,7 @@ def values_of(q):
     scale = np.append(E8M0, np.nan)[s] if q.format == MX else np.append(E4M3, np.nan)[np.minimum(s, 0x7F)]
     unit = 1.0
     if q.format == NV:
-        unit = 2.0 ** exponent(q.amax.cpu().double().numpy().reshape(1, 1), NV)
+        unit = 2.0 ** exponent(q.amax[:1].cpu().double().numpy().reshape(1, 1), NV)
     v = np.where(c & 8, -1.0, 1.0) * LEVELS[c & 7]
     return v * np.repeat(scale, block_of(q.format), 1)[:, :q.cols] * unit
 

@@ -249,4 +249,4 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             for p, q in zip(a, b):
-                assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales) and torch.equal(p.amax, q.amax)
+                assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales) and torch.equal(p.amax[0], q.amax[0])

@@ -38,6 +38,7 @@ DPG_SCALE_SPECTRAL = 0
 DPG_SCALE_RMS = 1
 DPG_NVFP4 = 0
 DPG_MXFP4 = 1
+DPG_FP4_AMAX_FLOATS = 256
 
 # symbols declared in include/dpg.h
 EXPORTED = (
@@ -949,10 +950,25 @@ class Fp4:
         self.rows, self.cols, self.format = int(rows), int(cols), int(format)
         self.codes = torch.empty(codes.value, dtype=torch.uint8, device=device)
         self.scales = torch.empty(scales.value, dtype=torch.uint8, device=device)
-        self.amax = torch.zeros(1, dtype=torch.float32, device=device)
+        self.amax = torch.zeros(DPG_FP4_AMAX_FLOATS, dtype=torch.float32, device=device)
         self.c = dpg_fp4(self.codes.data_ptr(), self.scales.data_ptr(), self.amax.data_ptr(), self.rows,
                          self.cols, self.format)
         self._ref = ctypes.byref(self.c)
+        self._device = self.codes.device.index if self.codes.is_cuda else None
+
+
+def _current_device() -> int:
+    import torch
+    # torch.cuda.current_device() takes longer than a small kernel's checks
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return get() if get is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _elsewhere(index, what: str):
+    """Kernels are launched on the current device: its tensors only."""
+    if index is None:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    raise ValueError(f"{what}: on device {index}, but device {_current_device()} is current")
 
 
 def _fp4(q: Optional[Fp4], what: str):
@@ -960,32 +976,36 @@ def _fp4(q: Optional[Fp4], what: str):
         return None
     if not isinstance(q, Fp4):
         raise TypeError(f"{what}: expected an Fp4")
-    _here(q.codes, what)
+    if q._device is None or q._device != _current_device():
+        _elsewhere(q._device, what)
     return q._ref
 
 
 def _here(t, what: str):
-    """Kernels are launched on the current device: its tensors only."""
+    if not t.is_cuda or t.get_device() != _current_device():
+        _elsewhere(t.get_device() if t.is_cuda else None, what)
+
+
+@functools.lru_cache(maxsize=None)
+def _dtype_codes():
     import torch
-    if not t.is_cuda:
-        raise TypeError(f"{what}: expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}, but device {torch.cuda.current_device()} is current")
+    return {torch.bfloat16: DPG_BF16, torch.float32: DPG_F32}
 
 
 def _matrix(t, what: str):
     """(pointer, dtype, row stride) of a two-dimensional tensor with neighbouring
     columns."""
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    dt = _dtype_codes().get(t.dtype)
+    if dt is None:
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{what}: columns must be neighbours in memory")
     _here(t, what)
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return t.data_ptr(), DPG_BF16 if t.dtype == torch.bfloat16 else DPG_F32, stride
+    return t.data_ptr(), dt, stride if rows > 1 else cols
 
 
 def _seed(seed):
@@ -1055,13 +1075,14 @@ def _vector(t, n: int, what: str):
     """(pointer, dtype) of a contiguous tensor of n elements, or (None, None)."""
     if t is None:
         return None, None
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    dt = _dtype_codes().get(t.dtype)
+    if dt is None:
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous elements")
-    _here(t, what)
-    return t.data_ptr(), DPG_BF16 if t.dtype == torch.bfloat16 else DPG_F32
+    if not t.is_cuda or t.get_device() != _current_device():
+        _elsewhere(t.get_device() if t.is_cuda else None, what)
+    return t.data_ptr(), dt
 
 
 def _pair_dtype(a, b, what: str) -> int:

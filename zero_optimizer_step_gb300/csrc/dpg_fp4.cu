@@ -20,6 +20,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "dpg_async.cuh"
 #include "dpg_fp4.h"
 #include "dpg_host.h"
 #include "dpg_ortho.h"
@@ -43,15 +44,20 @@ struct QuantArgs {
     int32_t vec;                        // 16-byte loads are allowed
     const int64_t* seed;                // NULL: nearest
     int64_t seed_plus;
-    const float* amax;                  // where k_fp4_amax left it
+    float* amax;                        // E4M3: the largest magnitude, and behind it its parts
     float* amax_copy;                   // the other side's (NULL: none)
+    int32_t parts;                      // that k_fp4_amax left (0: this launch, one cluster, finds it)
     QuantSide row, col;
 };
 
 // ---------------------------------------------------------------------------
 // Largest finite magnitude, as the bits of an fp32 number: these order like the
-// numbers, and a maximum is the same in any order.
+// numbers.  Every CTA leaves the one of its share behind the result's place, and
+// the CTAs of the quantisation take the largest of them: nothing to set to zero
+// before, and no atomics (9700 on one address took 12 us).
 // ---------------------------------------------------------------------------
+constexpr int kAmaxParts = DPG_FP4_AMAX_FLOATS - 1;
+
 template <bool F32>
 __device__ __forceinline__ uint32_t magnitude_bits(uint32_t w) {      // of one fp32 or two bf16 values
     if (F32) {
@@ -63,43 +69,54 @@ __device__ __forceinline__ uint32_t magnitude_bits(uint32_t w) {      // of one 
     hi = hi < 0x7F800000u ? hi : 0u;
     return lo > hi ? lo : hi;
 }
+template <bool F32>
+__device__ __forceinline__ uint32_t magnitude_bits4(uint4 v) {
+    return max(max(magnitude_bits<F32>(v.x), magnitude_bits<F32>(v.y)),
+               max(magnitude_bits<F32>(v.z), magnitude_bits<F32>(v.w)));
+}
+// largest over 256 threads, in all of them
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* sh) {
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+    __syncthreads();
+    return __reduce_max_sync(0xFFFFFFFFu, sh[threadIdx.x & 7]);
+}
 
 template <bool F32>
 __global__ void __launch_bounds__(256) k_fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t stride,
-                                                  int32_t flat16, uint32_t* amax) {
+                                                  int32_t flat, uint32_t* parts) {
+    __shared__ uint32_t sh[8];
     pdl_enter();
     uint32_t m = 0;
-    const int64_t step = int64_t(gridDim.x) * 256, t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    constexpr int kPer = F32 ? 4 : 8;   // elements of 16 bytes
-    if (flat16) {                       // rows back to back, from a 16-byte boundary
-        const int64_t n = rows * cols, vecs = n / kPer;
-        const unsigned char* p = static_cast<const unsigned char*>(x);
+    constexpr int kPer = F32 ? 4 : 8, kFly = 8;      // elements of 16 bytes, loads in flight
+    if (flat) {                                      // rows back to back
+        const int64_t n = rows * cols, t = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+        // up to the first 16-byte boundary, and behind the last one, singly
+        const int64_t head = min(n, int64_t((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (F32 ? 4 : 2));
+        const int64_t vecs = (n - head) / kPer, tail = head + vecs * kPer;
+        const unsigned char* p = static_cast<const unsigned char*>(x) + head * (F32 ? 4 : 2);
         int64_t i = t;
-        for (; i + 3 * step < vecs; i += 4 * step) {
-            uint4 v[4];
+        for (; i + (kFly - 1) * step < vecs; i += kFly * step) {
+            uint4 v[kFly];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const uint4*>(p + (i + u * step) * 16);
+            for (int u = 0; u < kFly; ++u) v[u] = *reinterpret_cast<const uint4*>(p + (i + u * step) * 16);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                m = max(max(m, max(magnitude_bits<F32>(v[u].x), magnitude_bits<F32>(v[u].y))),
-                        max(magnitude_bits<F32>(v[u].z), magnitude_bits<F32>(v[u].w)));
+            for (int u = 0; u < kFly; ++u) m = max(m, magnitude_bits4<F32>(v[u]));
         }
-        for (; i < vecs; i += step) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p + i * 16);
-            m = max(max(m, max(magnitude_bits<F32>(v.x), magnitude_bits<F32>(v.y))),
-                    max(magnitude_bits<F32>(v.z), magnitude_bits<F32>(v.w)));
-        }
-        for (int64_t j = vecs * kPer + t; j < n; j += step)
+        for (; i < vecs; i += step) m = max(m, magnitude_bits4<F32>(*reinterpret_cast<const uint4*>(p + i * 16)));
+        if (t < head + n - tail) {
+            const int64_t j = t < head ? t : tail + t - head;
             m = max(m, F32 ? magnitude_bits<true>(static_cast<const uint32_t*>(x)[j])
                            : magnitude_bits<false>(static_cast<const uint16_t*>(x)[j]));
+        }
     } else {
         for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
             for (int64_t c = threadIdx.x; c < cols; c += 256)
                 m = max(m, F32 ? magnitude_bits<true>(static_cast<const uint32_t*>(x)[r * stride + c])
                                : magnitude_bits<false>(static_cast<const uint16_t*>(x)[r * stride + c]));
     }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if ((threadIdx.x & 31) == 0 && m) atomicMax(amax, m);
+    m = block_max(m, sh);
+    if (threadIdx.x == 0) parts[blockIdx.x] = m;
 }
 
 // ---------------------------------------------------------------------------
@@ -233,6 +250,62 @@ constexpr int kColPitch = 80;                              // bytes of a column'
 template <bool F32, bool MX>
 constexpr int quant_smem() { return TileOf<F32>::kBytes + kQuantTile * kColPitch; }
 
+// The B elements of row r from column c on, zeros behind the last.  Where rows do
+// not start on 16-byte boundaries, the 16-byte pieces that hold the block are
+// loaded (those that lie in the matrix) and shifted into place.
+template <bool F32, int B>
+__device__ __forceinline__ void load_block(const QuantArgs& a, int64_t r, int64_t c, uint32_t* w) {
+    constexpr int kWords = B * (F32 ? 4 : 2) / 4, kSize = F32 ? 4 : 2;
+    const int64_t at = r * a.stride + c;
+    const unsigned char* p = static_cast<const unsigned char*>(a.x) + at * kSize;
+    const bool whole = r < a.rows && c + B <= a.cols;
+    if (a.vec) {
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < kWords / 4; ++j) {
+                const uint4 v = ld_grad_u4(p + 16 * j);
+                w[4 * j] = v.x;
+                w[4 * j + 1] = v.y;
+                w[4 * j + 2] = v.z;
+                w[4 * j + 3] = v.w;
+            }
+            return;
+        }
+    } else if (whole && at >= 16 / kSize && r + 1 < a.rows) {        // (not the first and the last few)
+        const int off = int(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
+        const unsigned char* q = p - off * kSize;
+        uint32_t v[kWords + 4];
+#pragma unroll
+        for (int j = 0; j < kWords / 4 + 1; ++j) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + (j < kWords / 4 || off ? j : 0));
+            v[4 * j] = u.x;
+            v[4 * j + 1] = u.y;
+            v[4 * j + 2] = u.z;
+            v[4 * j + 3] = u.w;
+        }
+        const int words = F32 ? off : off >> 1;
+#pragma unroll
+        for (int j = 0; j < kWords + 2; ++j) v[j] = (words & 2) ? v[j + 2] : v[j];
+#pragma unroll
+        for (int j = 0; j < kWords + 1; ++j) v[j] = (words & 1) ? v[j + 1] : v[j];
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+            w[j] = F32 ? v[j] : __funnelshift_r(v[j], v[j + 1], (off & 1) * 16);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+        if (F32) {
+            w[j] = r < a.rows && c + j < a.cols ? __ldg(static_cast<const uint32_t*>(a.x) + at + j) : 0u;
+        } else {
+            const uint16_t* h = static_cast<const uint16_t*>(a.x) + at + 2 * j;
+            const uint32_t lo = r < a.rows && c + 2 * j < a.cols ? __ldg(h) : 0u;
+            const uint32_t hi = r < a.rows && c + 2 * j + 1 < a.cols ? __ldg(h + 1) : 0u;
+            w[j] = lo | hi << 16;
+        }
+    }
+}
+
 template <bool F32, bool MX, bool SR>
 __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
     constexpr int B = MX ? 32 : 16;                        // elements of a block
@@ -248,42 +321,41 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
     const int64_t r0 = ti * kQuantTile, c0 = tj * kQuantTile;
     const int tid = int(threadIdx.x);
     const bool by_row = a.row.codes != nullptr, by_col = a.col.codes != nullptr;
-    float unit = 1.0f;
-    if (!MX) {
-        const float amax = __ldcg(a.amax);
-        unit = __uint_as_float(uint32_t(127 - fp4_exponent(__float_as_uint(amax))) << 23);
-        if (a.amax_copy && blockIdx.x == 0 && tid == 0) *a.amax_copy = amax;
-    }
     const uint64_t key = SR ? uint64_t(__ldg(a.seed) + a.seed_plus) : 0;
 
     uint32_t raw[kTasks][kWords];
 #pragma unroll
     for (int k = 0; k < kTasks; ++k) {
         const int task = k * kQuantThreads + tid, row = task / kBlocks, blk = task % kBlocks;
-        const int64_t r = r0 + row, c = c0 + blk * B;
-        const int64_t at = r * a.stride + c;
-        if (r < a.rows && c + B <= a.cols && a.vec) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.x) + at * (F32 ? 4 : 2));
-#pragma unroll
-            for (int j = 0; j < kWords / 4; ++j) {
-                const uint4 v = ld_grad_u4(p + j);
-                raw[k][4 * j] = v.x;
-                raw[k][4 * j + 1] = v.y;
-                raw[k][4 * j + 2] = v.z;
-                raw[k][4 * j + 3] = v.w;
-            }
+        load_block<F32, B>(a, r0 + row, c0 + blk * B, raw[k]);
+    }
+    float unit = 1.0f;
+    if (!MX) {
+        __shared__ uint32_t sh[8];
+        uint32_t m = 0;
+        if (a.parts) {
+            if (tid < a.parts) m = __ldcg(reinterpret_cast<const uint32_t*>(a.amax) + 1 + tid);
         } else {
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                if (F32) {
-                    raw[k][j] = r < a.rows && c + j < a.cols ? __ldg(static_cast<const uint32_t*>(a.x) + at + j) : 0u;
-                } else {
-                    const uint16_t* p = static_cast<const uint16_t*>(a.x) + at + 2 * j;
-                    const uint32_t lo = r < a.rows && c + 2 * j < a.cols ? __ldg(p) : 0u;
-                    const uint32_t hi = r < a.rows && c + 2 * j + 1 < a.cols ? __ldg(p + 1) : 0u;
-                    raw[k][j] = lo | hi << 16;
-                }
+            for (int k = 0; k < kTasks; ++k)
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) m = max(m, magnitude_bits<F32>(raw[k][j]));
+        }
+        m = block_max(m, sh);
+        if (!a.parts && gridDim.x > 1) {
+            __shared__ uint32_t mine;
+            if (tid == 0) mine = m;
+            cluster_sync();
+            for (uint32_t q = 0; q < gridDim.x; ++q) {
+                uint32_t other;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(map_to(smem_u32(&mine), q)) : "memory");
+                m = max(m, other);
             }
+        }
+        unit = __uint_as_float(uint32_t(127 - fp4_exponent(m)) << 23);
+        if (blockIdx.x == 0 && tid == 0) {
+            *a.amax = __uint_as_float(m);
+            if (a.amax_copy) *a.amax_copy = __uint_as_float(m);
         }
     }
 #pragma unroll
@@ -378,78 +450,78 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
             *reinterpret_cast<uint4*>(q.scales + (i * q.tiles + j) * kFp4TileBytes + part * 16) =
                 *reinterpret_cast<const uint4*>(sc[side] + t * kFp4TileBytes + part * 16);
     }
+    if (!MX && !a.parts && gridDim.x > 1) cluster_sync();   // the others have read this CTA's maximum
 }
 
 // ---------------------------------------------------------------------------
-// Values of a quantised matrix: a thread takes 32 elements of a row.
+// Values of a quantised matrix.  A thread writes one aligned piece of a row: 16
+// bytes of bf16, 32 of fp32, the 8 elements that lie there (fewer at a row's
+// ends); their codes, and their scales where a block ends among them, are
+// shifted into place, so rows may start anywhere.
 // ---------------------------------------------------------------------------
 struct DequantArgs {
     const unsigned char* codes;
     const unsigned char* scales;
     const float* amax;
-    int64_t rows, cols, pitch, tiles, stride, chunks;   // chunks: of 32 elements in a row
+    int64_t rows, cols, pitch, tiles, stride;
+    int64_t pieces;                                     // of a row
     void* out;
-    int32_t vec;                                        // 16-byte stores are allowed
 };
+
+template <bool MX>
+__device__ __forceinline__ float scale_value(int byte, float unit) {
+    if (MX) return byte == 0xFF ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte == 0 ? 0x00400000u : uint32_t(byte) << 23);
+    return byte == 0x7F ? __uint_as_float(0x7FC00000u) : e4m3_value(byte) * unit;
+}
 
 template <bool F32, bool MX>
 __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ DequantArgs a) {
+    constexpr int kSize = F32 ? 4 : 2, kShift = MX ? 5 : 4;   // log2 of a block
     pdl_enter();
     const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t r = t / a.chunks, ch = t % a.chunks;
+    const int64_t r = a.pieces > 0x7FFFFFFF || t > 0x7FFFFFFF ? t / a.pieces : int64_t(uint32_t(t) / uint32_t(a.pieces));
     if (r >= a.rows) return;
-    const uint4 q = ld_grad_u4(a.codes + r * a.pitch + ch * 16);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    unsigned char* row = static_cast<unsigned char*>(a.out) + r * a.stride * kSize;
+    const int skew = int(reinterpret_cast<uintptr_t>(row) & (8 * kSize - 1)) / kSize;   // elements before the row in its first piece
+    const int64_t e0 = (t - r * a.pieces) * 8 - skew;                                   // may be negative
+    if (e0 >= a.cols) return;
+    const int64_t first = max(e0, int64_t(0)), last = min(e0 + 8, a.cols) - 1;
+    // codes: 8 from e0 on, of two neighbouring words (those that the row has)
+    const int64_t word = e0 >> 3, words = a.pitch >> 2;
+    const uint32_t* cp = reinterpret_cast<const uint32_t*>(a.codes + r * a.pitch);
+    const uint32_t w0 = __ldg(cp + max(word, int64_t(0))), w1 = __ldg(cp + min(word + 1, words - 1));
+    const uint32_t w = __funnelshift_r(w0, w1, 4 * int(e0 & 7));
     const unsigned char* sp = a.scales + (r >> 7) * a.tiles * kFp4TileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-    float s[2];
-    if (MX) {
-        const int byte = __ldg(sp + (ch >> 2) * kFp4TileBytes + (ch & 3));
-        s[0] = s[1] = byte == 0xFF ? __uint_as_float(0x7FC00000u)
-                                   : __uint_as_float(byte == 0 ? 0x00400000u : uint32_t(byte) << 23);
-    } else {
-        const float unit = __uint_as_float(0x3F800000u + uint32_t(fp4_exponent(__float_as_uint(__ldg(a.amax)))) * 0x800000u);
-        const uint32_t two = __ldg(reinterpret_cast<const unsigned short*>(sp + (ch >> 1) * kFp4TileBytes + (ch & 1) * 2));
+    const int64_t b0 = first >> kShift, b1 = last >> kShift;
+    const float unit = MX ? 1.0f : __uint_as_float(0x3F800000u + uint32_t(fp4_exponent(__float_as_uint(__ldg(a.amax)))) * 0x800000u);
+    const float s0 = scale_value<MX>(__ldg(sp + (b0 >> 2) * kFp4TileBytes + (b0 & 3)), unit);
+    const float s1 = b1 == b0 ? s0 : scale_value<MX>(__ldg(sp + (b1 >> 2) * kFp4TileBytes + (b1 & 3)), unit);
+    const int change = int((b1 << kShift) - e0);            // first element of the second block
+    float v[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int byte = int(two >> (8 * h)) & 0xFF;
-            s[h] = byte == 0x7F ? __uint_as_float(0x7FC00000u) : e4m3_value(byte) * unit;
-        }
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = w >> (4 * j), m = c & 7u;
+        // .5 m below 2 (0, .5, 1, 1.5), else (2 + low bit) 2^(m / 2 - 2)
+        const float f = m < 2 ? 0.5f * float(m) : __uint_as_float((252u + m) << 22);
+        v[j] = ((c & 8u) ? -f : f) * (j < change ? s0 : s1);
     }
-    const int n = int(min(int64_t(32), a.cols - ch * 32));
-    const int64_t at = r * a.stride + ch * 32;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t c = w[g] >> (4 * j), m = c & 7u;
-            // .5 m below 2 (0, .5, 1, 1.5), else (2 + low bit) 2^(m / 2 - 2)
-            const float f = m < 2 ? 0.5f * float(m) : __uint_as_float((252u + m) << 22);
-            v[j] = ((c & 8u) ? -f : f) * s[g >> 1];
-        }
+    if (e0 >= 0 && e0 + 8 <= a.cols) {
         if (F32) {
-            float* p = static_cast<float*>(a.out) + at + 8 * g;
-            if (a.vec && 8 * g + 8 <= n) {
-                *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
+            F8 f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * g + j < n) p[j] = v[j];
-            }
+            for (int j = 0; j < 8; ++j) f.v[j] = v[j];
+            st_f8(reinterpret_cast<float*>(row) + e0, f);
         } else {
-            uint16_t* p = static_cast<uint16_t*>(a.out) + at + 8 * g;
-            const uint4 h = narrow8(v);
-            if (a.vec && 8 * g + 8 <= n) {
-                st_u4(p, h);
-            } else {
-                const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * g + j < n) p[j] = uint16_t(hw[j >> 1] >> (16 * (j & 1)));
-            }
+            st_u4(row + e0 * 2, narrow8(v));
         }
+        return;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (e0 + j >= 0 && e0 + j < a.cols) {
+            if (F32) reinterpret_cast<float*>(row)[e0 + j] = v[j];
+            else reinterpret_cast<__nv_bfloat16*>(row)[e0 + j] = __float2bfloat16_rn(v[j]);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -534,35 +606,67 @@ static int quant_args(const void* x, int32_t dtype, int64_t rows, int64_t cols, 
     return DPG_OK;
 }
 
-template <bool F32, bool MX>
-static int launch_quant(const QuantArgs& a, cudaStream_t s, const char* who) {
-    auto k = a.seed ? k_fp4_quantize<F32, MX, true> : k_fp4_quantize<F32, MX, false>;
+template <bool F32, bool MX, bool SR>
+static int launch_quant(const QuantArgs& a, int64_t tiles, cudaStream_t s, const char* who) {
+    auto k = k_fp4_quantize<F32, MX, SR>;
     const int smem = a.col.codes ? quant_smem<F32, MX>() : 0;
-    if (smem > 48 * 1024) DPG_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    const int64_t tiles = (a.rows + kQuantTile - 1) / kQuantTile * a.tiles_c;
-    return launch_k(k, unsigned(tiles), kQuantThreads, size_t(smem), s, who, a);
-}
-
-static int quantize(const QuantArgs& a, int32_t dtype, int32_t format, cudaStream_t s, const char* who) {
-    if (a.rows == 0 || a.cols == 0) return DPG_OK;
-    if (format == DPG_NVFP4) {
-        uint32_t* amax = reinterpret_cast<uint32_t*>(const_cast<float*>(a.amax));
-        DPG_CUDA_TRY(cudaMemsetAsync(amax, 0, sizeof(uint32_t), s));
-        int dev = 0, sms = 0;
-        DPG_CUDA_TRY(cudaGetDevice(&dev));
-        int st = sm_count(dev, &sms);
-        if (st != DPG_OK) return st;
-        const int64_t n = a.rows * a.cols;
-        const int flat16 = a.stride == a.cols && aligned(a.x, 16);
-        const int64_t want = flat16 ? (n + 8191) / 8192 : a.rows;
-        const unsigned grid = unsigned(want < 1 ? 1 : want < 8 * sms ? want : 8 * sms);
-        st = launch_k(dtype == DPG_F32 ? k_fp4_amax<true> : k_fp4_amax<false>, grid, 256, s, who, a.x, a.rows, a.cols,
-                      a.stride, int32_t(flat16), amax);
+    if (smem > 48 * 1024) {
+        static std::atomic<uint64_t> once{0};
+        const int st = allow_smem(reinterpret_cast<const void*>(k), smem, once, who);
         if (st != DPG_OK) return st;
     }
-    if (dtype == DPG_F32)
-        return format == DPG_MXFP4 ? launch_quant<true, true>(a, s, who) : launch_quant<true, false>(a, s, who);
-    return format == DPG_MXFP4 ? launch_quant<false, true>(a, s, who) : launch_quant<false, false>(a, s, who);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles));
+    cfg.blockDim = dim3(kQuantThreads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (t_programmatic) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (!MX && !a.parts && tiles > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(tiles);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    }
+    return after_launch(who);
+}
+
+static int quantize(QuantArgs& a, int32_t dtype, int32_t format, cudaStream_t s, const char* who) {
+    if (a.rows == 0 || a.cols == 0) return DPG_OK;
+    const bool f32 = dtype == DPG_F32, mx = format == DPG_MXFP4;
+    const int64_t tiles = (a.rows + kQuantTile - 1) / kQuantTile * a.tiles_c;
+    // up to 8 tiles are one cluster, whose CTAs find the largest magnitude among themselves
+    if (!mx && tiles > 8) {
+        const int64_t n = a.rows * a.cols;
+        const bool flat = a.stride == a.cols;
+        const int64_t want = flat ? (n + 16383) / 16384 : a.rows;
+        a.parts = int32_t(want < kAmaxParts ? want : kAmaxParts);
+        const int st = launch_k(f32 ? k_fp4_amax<true> : k_fp4_amax<false>, unsigned(a.parts), 256, s, who, a.x, a.rows,
+                                a.cols, a.stride, int32_t(flat), reinterpret_cast<uint32_t*>(a.amax) + 1);
+        if (st != DPG_OK) return st;
+    }
+    const int which = (f32 ? 4 : 0) + (mx ? 2 : 0) + (a.seed ? 1 : 0);
+    switch (which) {
+        case 0: return launch_quant<false, false, false>(a, tiles, s, who);
+        case 1: return launch_quant<false, false, true>(a, tiles, s, who);
+        case 2: return launch_quant<false, true, false>(a, tiles, s, who);
+        case 3: return launch_quant<false, true, true>(a, tiles, s, who);
+        case 4: return launch_quant<true, false, false>(a, tiles, s, who);
+        case 5: return launch_quant<true, false, true>(a, tiles, s, who);
+        case 6: return launch_quant<true, true, false>(a, tiles, s, who);
+        default: return launch_quant<true, true, true>(a, tiles, s, who);
+    }
 }
 
 }  // namespace dpg
@@ -612,12 +716,13 @@ int dpg_fp4_dequantize(const dpg_fp4* q, void* out, int32_t out_dtype, int64_t r
     a.cols = q->cols;
     a.pitch = dpg::fp4_pitch(q->cols);
     a.tiles = dpg::fp4_tiles(q->cols, q->format);
-    a.chunks = (q->cols + 31) / 32;
     a.stride = q->rows > 1 ? row_stride : q->cols;
     a.out = out;
-    a.vec = dpg::aligned(out, 16) && (q->rows <= 1 || row_stride % (out_dtype == DPG_F32 ? 4 : 8) == 0);
+    // one more where a row may start inside a piece
+    const bool whole = dpg::aligned(out, out_dtype == DPG_F32 ? 32 : 16) && (q->rows <= 1 || row_stride % 8 == 0);
+    a.pieces = (q->cols + 7) / 8 + (whole ? 0 : 1);
     int grid = 0;
-    st = dpg::grid_cover((a.rows * a.chunks + 255) / 256, &grid, "dpg_fp4_dequantize");
+    st = dpg::grid_cover((a.rows * a.pieces + 255) / 256, &grid, "dpg_fp4_dequantize");
     if (st != DPG_OK) return st;
     const bool mx = q->format == DPG_MXFP4;
     auto k = out_dtype == DPG_F32 ? (mx ? dpg::k_fp4_dequantize<true, true> : dpg::k_fp4_dequantize<true, false>)

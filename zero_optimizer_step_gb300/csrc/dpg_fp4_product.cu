@@ -741,7 +741,9 @@ static int launch_small(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     if (st == DPG_OK) st = encode_operand(c, COLS, 1, &maps.codes_c, &maps.scales_c, who);
     if (st != DPG_OK) return st;
     auto k = k_fp4_small<MX, COLS>;
-    DPG_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+    static std::atomic<uint64_t> once{0};
+    st = allow_smem(reinterpret_cast<const void*>(k), S::kSmem, once, who);
+    if (st != DPG_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(tiles * a.split));
     cfg.blockDim = dim3(kSmallThreads);
@@ -795,7 +797,9 @@ static int launch_large(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
         if (e != CUDA_SUCCESS) return fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
     }
     const int pairs = int(tiles < sms / 2 ? tiles : sms / 2);
-    DPG_CUDA_TRY(cudaFuncSetAttribute(k_fp4_large<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLargeSmem));
+    static std::atomic<uint64_t> once{0};
+    st = allow_smem(reinterpret_cast<const void*>(k_fp4_large<MX>), kLargeSmem, once, who);
+    if (st != DPG_OK) return st;
     return launch_k(k_fp4_large<MX>, unsigned(2 * pairs), kLargeThreads, size_t(kLargeSmem), s, who, a, maps);
 }
 

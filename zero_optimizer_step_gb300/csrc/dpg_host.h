@@ -52,6 +52,22 @@ size_t round256(size_t x);
 // does not wait for the default one could read before they have arrived.
 cudaError_t upload_done();
 
+// Lets `fn` use `bytes` of dynamic shared memory on the current device; `once`
+// (of one kernel) remembers the devices that know.
+inline int allow_smem(const void* fn, int bytes, std::atomic<uint64_t>& once, const char* who) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (e == cudaSuccess && (once.load(std::memory_order_acquire) & bit)) return DPG_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(DPG_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    }
+    once.fetch_or(bit, std::memory_order_release);
+    return DPG_OK;
+}
+
 // Launches kernel k (which must begin with pdl_enter()) on `grid` CTAs of
 // `block` threads and `smem` bytes of dynamic shared memory, with programmatic stream serialization unless the calling
 // thread switched it off, then checks and counts the launch like
