@@ -7,18 +7,22 @@
 // Every decision is exact:
 //   * s by a product with 1/6 rounded up, then compared with its neighbours
 //     through 6 s, which is exact;
-//   * x / s for an E8M0 scale is a product with a power of two; for an E4M3 one
-//     it is the correctly rounded quotient, from the reciprocal and one residual
-//     (Markstein 1990).  A borderline m s has at most 7 bits, so a quotient whose
-//     x is not on it rounds to something else than m, and ties stay ties.  The
-//     product with the reciprocal alone is off by one unit for 11 of the 56
-//     borderlines, and would round those ties up.
-//   * stochastic: |x| - lo s and (2 u + 1) 2^-17 gap s are exact in fp32.
-#include <cuda_fp4.h>
+//   * y = x / s for an E8M0 scale is a product with a power of two; for an E4M3
+//     one it is the correctly rounded quotient, from the reciprocal and one
+//     residual (Markstein 1990).  A borderline m s has at most 7 bits, so a
+//     quotient whose x is not on it rounds to something else than m, and ties stay
+//     ties.  The product with the reciprocal alone is off by one unit for 11 of the
+//     56 borderlines, and would round those ties up.
+//   * stochastic: the threshold lo + (2 u + 1) 2^-17 gap is an fp32 number, so y
+//     is above it exactly where y rounded up is.  With one bit of y's significand
+//     kept, the 22 bits below it are its distance from lo in units of 2^-22 gap: a
+//     sum with 2^22 - 1 - 32 (2 u + 1) carries where it is above the threshold.
+//     Below 1 the steps stay .5: there the same is done with y + 1, rounded up.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
-#include <cstring>
 
 #include "dpg_async.cuh"
 #include "dpg_fp4.h"
@@ -74,36 +78,38 @@ __device__ __forceinline__ uint32_t magnitude_bits4(uint4 v) {
     return max(max(magnitude_bits<F32>(v.x), magnitude_bits<F32>(v.y)),
                max(magnitude_bits<F32>(v.z), magnitude_bits<F32>(v.w)));
 }
-// largest over 256 threads, in all of them
+// largest over 32 W threads, in all of them
+template <int W>
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* sh) {
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
     __syncthreads();
-    return __reduce_max_sync(0xFFFFFFFFu, sh[threadIdx.x & 7]);
+    return __reduce_max_sync(0xFFFFFFFFu, sh[threadIdx.x & (W - 1)]);
 }
+constexpr int kAmaxThreads = 512;
 
 template <bool F32>
-__global__ void __launch_bounds__(256) k_fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t stride,
+__global__ void __launch_bounds__(kAmaxThreads) k_fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t stride,
                                                   int32_t flat, uint32_t* parts) {
-    __shared__ uint32_t sh[8];
+    __shared__ uint32_t sh[kAmaxThreads / 32];
     pdl_enter();
     uint32_t m = 0;
     constexpr int kPer = F32 ? 4 : 8, kFly = 8;      // elements of 16 bytes, loads in flight
     if (flat) {                                      // rows back to back
-        const int64_t n = rows * cols, t = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+        const int64_t n = rows * cols, t = int64_t(blockIdx.x) * kAmaxThreads + threadIdx.x,
+                      step = int64_t(gridDim.x) * kAmaxThreads;
         // up to the first 16-byte boundary, and behind the last one, singly
         const int64_t head = min(n, int64_t((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (F32 ? 4 : 2));
         const int64_t vecs = (n - head) / kPer, tail = head + vecs * kPer;
         const unsigned char* p = static_cast<const unsigned char*>(x) + head * (F32 ? 4 : 2);
-        int64_t i = t;
-        for (; i + (kFly - 1) * step < vecs; i += kFly * step) {
+        for (int64_t i = t; i < vecs; i += kFly * step) {
             uint4 v[kFly];
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) v[u] = *reinterpret_cast<const uint4*>(p + (i + u * step) * 16);
+            for (int u = 0; u < kFly; ++u)
+                v[u] = i + u * step < vecs ? *reinterpret_cast<const uint4*>(p + (i + u * step) * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int u = 0; u < kFly; ++u) m = max(m, magnitude_bits4<F32>(v[u]));
         }
-        for (; i < vecs; i += step) m = max(m, magnitude_bits4<F32>(*reinterpret_cast<const uint4*>(p + i * 16)));
         if (t < head + n - tail) {
             const int64_t j = t < head ? t : tail + t - head;
             m = max(m, F32 ? magnitude_bits<true>(static_cast<const uint32_t*>(x)[j])
@@ -111,11 +117,11 @@ __global__ void __launch_bounds__(256) k_fp4_amax(const void* x, int64_t rows, i
         }
     } else {
         for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-            for (int64_t c = threadIdx.x; c < cols; c += 256)
+            for (int64_t c = threadIdx.x; c < cols; c += kAmaxThreads)
                 m = max(m, F32 ? magnitude_bits<true>(static_cast<const uint32_t*>(x)[r * stride + c])
                                : magnitude_bits<false>(static_cast<const uint16_t*>(x)[r * stride + c]));
     }
-    m = block_max(m, sh);
+    m = block_max<kAmaxThreads / 32>(m, sh);
     if (threadIdx.x == 0) parts[blockIdx.x] = m;
 }
 
@@ -145,94 +151,138 @@ __device__ __forceinline__ float e4m3_value(int byte) {
     return byte < 8 ? float(byte) * 0.001953125f : __uint_as_float(uint32_t(byte + 960) << 20);
 }
 
+constexpr int kInverses = 128;     // of every E4M3 value, in shared memory
+
 struct BlockScale {
     int byte;          // as stored
-    float s, inv;      // its value, and about 1 / s (0 for s = 0); inv alone for E8M0
+    float s, inv;      // E4M3: scale * 2^e; about 1 / (scale * 2^e), 0 for 0 or where `bad`
     bool bad;          // a NaN or an infinity in the block
 };
 
-// of a block whose largest magnitude has the bits `top`; `unit` = 2^-e (E4M3)
-template <bool MX>
-__device__ __forceinline__ BlockScale block_scale(uint32_t top, float unit) {
+// of a block whose largest magnitude has the bits `top`; E4M3: unit = 2^-e, whole =
+// 2^e, inverses[byte] = 1 / its value, rounded to nearest
+template <bool F32, bool MX>
+__device__ __forceinline__ BlockScale block_scale(uint32_t top, float unit, float whole, const float* inverses) {
     BlockScale b;
     b.bad = top >= 0x7F800000u;
     if (MX) {
         const int e = int(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-        b.byte = b.bad ? 0xFF : e < 0 ? 0 : e;
-        b.inv = b.bad ? 0.0f : __uint_as_float(uint32_t(254 - b.byte) << 23);
-        b.s = __uint_as_float(b.byte == 0 ? 0x00400000u : uint32_t(b.byte) << 23);
+        const int k = e < 0 ? 0 : e;
+        b.byte = b.bad ? 0xFF : k;
+        b.inv = b.bad ? 0.0f : __uint_as_float(uint32_t(254 - k) << 23);
+        b.s = 0.0f;                                     // (not used)
         return b;
     }
     const float u = __uint_as_float(top) * unit;
-    const float q = u * 0.166666672f;                   // 1/6 rounded up
+    const float q = u * 0.166666672f;                   // 1/6 rounded up: at most two units above u / 6
+    // E4M3 values are the fp32 numbers with three bits, down to 2^-6, and multiples of 2^-9 below
     int k;
-    if (q < 0.015625f)
-        k = int(ceilf(q * 512.0f));
-    else
-        k = int((__float_as_uint(q) + 0xFFFFFu) >> 20) - 960;
-    k = k > 0x7E ? 0x7E : k;
-    if (k > 0 && 6.0f * e4m3_value(k - 1) >= u) --k;
-    else if (k < 0x7E && 6.0f * e4m3_value(k) < u) ++k;
-    b.s = e4m3_value(k);
-    b.inv = b.bad || k == 0 ? 0.0f : 1.0f / b.s;
+    if (F32) {
+        k = q < 0.015625f ? int(ceilf(q * 512.0f)) : int((__float_as_uint(q) + 0xFFFFFu) >> 20) - 960;
+        k = k > 0x7E ? 0x7E : k;
+        if (k > 0 && 6.0f * e4m3_value(k - 1) >= u) --k;
+        else if (k < 0x7E && 6.0f * e4m3_value(k) < u) ++k;
+    } else {
+        // u has 8 bits: u / 6 is on a value, or 2^-9 of itself from it
+        const float r = __uint_as_float(__float_as_uint(q) - (q > 0.0f ? 16u : 0u));
+        k = q < 0.015625f ? int(ceilf(r * 512.0f)) : int((__float_as_uint(r) + 0xFFFFFu) >> 20) - 960;
+        k = k > 0x7E ? 0x7E : k;
+    }
+    b.s = e4m3_value(k) * whole;
+    b.inv = b.bad ? 0.0f : inverses[k] * unit;
     b.byte = b.bad ? 0x7F : k;
     return b;
 }
 
-// two codes, x in the low half
-__device__ __forceinline__ uint32_t nearest2(float x, float y) {
-    return __nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
+// eight values to nearest codes, the first in the lowest four bits
+__device__ __forceinline__ uint32_t nearest8(const uint64_t* y) {
+    uint32_t r;
+    const float2 a = halves_of(y[0]), b = halves_of(y[1]), c = halves_of(y[2]), d = halves_of(y[3]);
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+    return r;
 }
 
-// code of v >= 0 (already times 2^-e), to the value above where the 16 bits u say so
-template <bool MX>
-__device__ __forceinline__ uint32_t stochastic(float v, const BlockScale& b, uint32_t u) {
-    const float y = v * b.inv;
-    // lo = y with one bit behind the point of its binade, in halves below 1
-    const uint32_t bits = __float_as_uint(y);
+// Code of y >= 0, rounded up where it is not exact, to the value above where the
+// 16 bits u say so.
+__device__ __forceinline__ uint32_t stochastic(float y, uint32_t u) {
     const bool small = y < 1.0f;
-    const bool half = y >= 0.5f;
-    const float lo = small ? (half ? 0.5f : 0.0f) : __uint_as_float(bits & 0xFFC00000u);
-    const uint32_t code = small ? (half ? 1u : 0u) : (bits >> 22) - 252u;
-    const float gap = y < 2.0f ? 0.5f : y < 4.0f ? 1.0f : 2.0f;
-    const float t = (2.0f * float(u) + 1.0f) * 7.62939453125e-6f * gap;
-    // an E8M0 scale: in units of s, exactly; else v - lo s and t s are exact.  (Where the rounding
-    // of y took it to a neighbour of the right lo, the comparison still ends at the right code:
-    // the distance to it is below or above every threshold.)
-    return code + (MX ? y - lo > t : fmaf(-lo, b.s, v) > t * b.s ? 1u : 0u);
+    const uint32_t z = __float_as_uint(small ? __fadd_ru(y, 1.0f) : y);
+    return ((z + (0x400000u - 1u - 32u) - 64u * u) >> 22) - (small ? 254u : 252u);
 }
 
-// N consecutive elements of a block (N a multiple of 8) to codes, 8 to a word.
-// n0: number of the first group of 8 (random bits); x: values times 2^-e where
-// E4M3.
-template <bool MX, bool SR, int N>
-__device__ __forceinline__ void encode(const float* x, const BlockScale& b, uint64_t n0, uint32_t side,
-                                       uint64_t key, uint32_t* out) {
+// B elements of a block to codes, 8 to a word.  w: the elements as they are in
+// memory (bf16: two to a word); n0: number of their first group of 8 (random bits).
+template <bool F32, bool MX, bool SR, int B>
+__device__ __forceinline__ void encode(const uint32_t* w, const BlockScale& b, uint64_t n0, uint32_t side, uint64_t key,
+                                       uint32_t* out) {
+    const uint64_t inv = pair_of(b.inv, b.inv), s = pair_of(-b.s, -b.s);
 #pragma unroll
-    for (int w = 0; w < N / 8; ++w) {
-        const float* v = x + 8 * w;
-        uint32_t word = 0;
-        if (SR) {
-            const uint4 r = philox(n0 + w, side, key);
-            const uint32_t h[4] = {r.x, r.y, r.z, r.w};
+    for (int g = 0; g < B / 8; ++g) {
+        uint64_t y[4];
+        uint32_t up = 0;           // which quotients are rounded down
+        uint32_t signs = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t u = (j & 1) ? h[j >> 1] >> 16 : h[j >> 1] & 0xFFFFu;
-                const uint32_t c = stochastic<MX>(fabsf(v[j]), b, u);
-                word |= (c | (__float_as_uint(v[j]) >> 28 & 8u)) << (4 * j);
+        for (int j = 0; j < 4; ++j) {
+            const int at = 4 * g + j;                       // of a pair
+            float lo, hi;
+            if (F32) {
+                lo = __uint_as_float(w[2 * at]);
+                hi = __uint_as_float(w[2 * at + 1]);
+            } else {
+                widen2(w[at], lo, hi);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float y0 = v[2 * j] * b.inv, y1 = v[2 * j + 1] * b.inv;
-                if (!MX) {
-                    y0 = fmaf(fmaf(-y0, b.s, v[2 * j]), b.inv, y0);
-                    y1 = fmaf(fmaf(-y1, b.s, v[2 * j + 1]), b.inv, y1);
+            if (SR) {
+                signs |= (__float_as_uint(lo) >> 31) << (8 * j + 3) | (__float_as_uint(hi) >> 31) << (8 * j + 7);
+                lo = fabsf(lo);
+                hi = fabsf(hi);
+            }
+            const uint64_t x = pair_of(lo, hi);
+            y[j] = mul2(x, inv);
+            if (!MX) {
+                y[j] = fma2(fma2(y[j], s, x), inv, y[j]);
+                if (SR) {
+                    const float2 rest = halves_of(fma2(y[j], s, x));
+                    up |= (rest.x > 0.0f ? 1u : 0u) << (2 * j) | (rest.y > 0.0f ? 2u : 0u) << (2 * j);
                 }
-                word |= nearest2(y0, y1) << (8 * j);
             }
         }
-        out[w] = b.bad ? 0u : word;
+        uint32_t word;
+        if (SR) {
+            const uint4 r = philox(n0 + g, side, key);
+            const uint32_t h[4] = {r.x, r.y, r.z, r.w};
+            word = signs;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 f = halves_of(y[j]);
+                if (!MX) {
+                    f.x = __uint_as_float(__float_as_uint(f.x) + (up >> (2 * j) & 1u));
+                    f.y = __uint_as_float(__float_as_uint(f.y) + (up >> (2 * j + 1) & 1u));
+                }
+                word |= stochastic(f.x, h[j] & 0xFFFFu) << (8 * j) | stochastic(f.y, h[j] >> 16) << (8 * j + 4);
+            }
+        } else {
+            word = nearest8(y);
+        }
+        out[g] = b.bad ? 0u : word;
+    }
+}
+
+// bits of the largest magnitude of a block (of a NaN, or of the infinity, where it has one)
+template <bool F32, int B>
+__device__ __forceinline__ uint32_t block_top(const uint32_t* w) {
+    uint32_t top = 0;
+    if constexpr (F32) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) top = max(top, w[j] & 0x7FFFFFFFu);
+        return top;
+    } else {
+#pragma unroll
+        for (int j = 0; j < B / 2; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+        return max(top << 16, top & 0xFFFF0000u);
     }
 }
 
@@ -306,6 +356,16 @@ __device__ __forceinline__ void load_block(const QuantArgs& a, int64_t r, int64_
     }
 }
 
+// an element, or two, times 2^100 (which are below 2^-88, NaN or infinite)
+template <bool F32>
+__device__ __forceinline__ uint32_t larger(uint32_t w) {
+    constexpr float k = 1.2676506002282294e30f;
+    if (F32) return __float_as_uint(__uint_as_float(w) * k);
+    float lo, hi;
+    widen2(w, lo, hi);
+    return __byte_perm(__float_as_uint(lo * k), __float_as_uint(hi * k), 0x7632);
+}
+
 template <bool F32, bool MX, bool SR>
 __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
     constexpr int B = MX ? 32 : 16;                        // elements of a block
@@ -329,10 +389,13 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
         const int task = k * kQuantThreads + tid, row = task / kBlocks, blk = task % kBlocks;
         load_block<F32, B>(a, r0 + row, c0 + blk * B, raw[k]);
     }
-    float unit = 1.0f;
+    float unit = 1.0f, whole = 1.0f;
+    bool tiny = false;
+    __shared__ float inverses[MX ? 1 : kInverses];
     if (!MX) {
         __shared__ uint32_t sh[8];
         uint32_t m = 0;
+        if (tid < kInverses) inverses[tid] = tid == 0 || tid == 0x7F ? 0.0f : 1.0f / e4m3_value(tid);   // (block_max waits)
         if (a.parts) {
             if (tid < a.parts) m = __ldcg(reinterpret_cast<const uint32_t*>(a.amax) + 1 + tid);
         } else {
@@ -341,7 +404,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) m = max(m, magnitude_bits<F32>(raw[k][j]));
         }
-        m = block_max(m, sh);
+        m = block_max<kQuantThreads / 32>(m, sh);
         if (!a.parts && gridDim.x > 1) {
             __shared__ uint32_t mine;
             if (tid == 0) mine = m;
@@ -352,7 +415,11 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
                 m = max(m, other);
             }
         }
-        unit = __uint_as_float(uint32_t(127 - fp4_exponent(m)) << 23);
+        // Where 2^-e times the inverse of a scale would leave fp32, elements are made larger first.
+        const int e = fp4_exponent(m);
+        tiny = e < -100;
+        unit = __uint_as_float(uint32_t(127 - (tiny ? e + 100 : e)) << 23);
+        whole = __uint_as_float(uint32_t(127 + (tiny ? e + 100 : e)) << 23);
         if (blockIdx.x == 0 && tid == 0) {
             *a.amax = __uint_as_float(m);
             if (a.amax_copy) *a.amax_copy = __uint_as_float(m);
@@ -361,6 +428,10 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
 #pragma unroll
     for (int k = 0; k < kTasks; ++k) {
         const int task = k * kQuantThreads + tid, row = task / kBlocks, blk = task % kBlocks;
+        if (tiny) {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) raw[k][j] = larger<F32>(raw[k][j]);
+        }
         if (by_col) {
             uint4* p = reinterpret_cast<uint4*>(tile + row * TileOf<F32>::kPitch + blk * kWords);
 #pragma unroll
@@ -369,21 +440,9 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
         }
         if (!by_row) continue;
         const int64_t r = r0 + row, c = c0 + blk * B;
-        float x[B];
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-            x[j] = F32 ? __uint_as_float(raw[k][j])
-                       : __uint_as_float((j & 1) ? raw[k][j >> 1] & 0xFFFF0000u : raw[k][j >> 1] << 16);
-            top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-        }
-        const BlockScale b = block_scale<MX>(top, unit);
-        if (!MX) {
-#pragma unroll
-            for (int j = 0; j < B; ++j) x[j] *= unit;
-        }
+        const BlockScale b = block_scale<F32, MX>(block_top<F32, B>(raw[k]), unit, whole, inverses);
         uint32_t codes[B / 8];
-        encode<MX, SR, B>(x, b, uint64_t(r) * a.row.vectors + uint64_t(c >> 3), 0, key, codes);
+        encode<F32, MX, SR, B>(raw[k], b, uint64_t(r) * a.row.vectors + uint64_t(c >> 3), 0, key, codes);
         if (r < a.rows && c < a.cols) {
             unsigned char* p = a.row.codes + r * a.row.pitch + (c >> 1);
             if (MX) *reinterpret_cast<uint4*>(p) = make_uint4(codes[0], codes[1], codes[B / 8 - 2], codes[B / 8 - 1]);
@@ -401,35 +460,30 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
         for (int k = 0; k < kColTasks; ++k) {
             const int task = k * kQuantThreads + tid, pair = task % (kQuantTile / 2), blk = task / (kQuantTile / 2);
             const int64_t r = r0 + blk * B;
-            float x[2][B];
-            uint32_t top[2] = {0, 0};
+            uint32_t w[2][kWords];
+            const uint32_t* p = tile + blk * B * TileOf<F32>::kPitch + (F32 ? 2 * pair : pair);
 #pragma unroll
-            for (int j = 0; j < B; ++j) {
-                const uint32_t* p = tile + (blk * B + j) * TileOf<F32>::kPitch;
+            for (int j = 0; j < kWords; ++j) {
                 if (F32) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p + 2 * pair);
-                    x[0][j] = __uint_as_float(v.x);
-                    x[1][j] = __uint_as_float(v.y);
+                    const uint2 v = *reinterpret_cast<const uint2*>(p + j * TileOf<F32>::kPitch);
+                    w[0][j] = v.x;
+                    w[1][j] = v.y;
                 } else {
-                    widen2(p[pair], x[0][j], x[1][j]);
+                    const uint32_t v = p[2 * j * TileOf<F32>::kPitch], u = p[(2 * j + 1) * TileOf<F32>::kPitch];
+                    w[0][j] = __byte_perm(v, u, 0x5410);
+                    w[1][j] = __byte_perm(v, u, 0x7632);
                 }
-                top[0] = max(top[0], __float_as_uint(x[0][j]) & 0x7FFFFFFFu);
-                top[1] = max(top[1], __float_as_uint(x[1][j]) & 0x7FFFFFFFu);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int col = 2 * pair + h;
                 const int64_t c = c0 + col;
-                const BlockScale b = block_scale<MX>(top[h], unit);
-                if (!MX) {
-#pragma unroll
-                    for (int j = 0; j < B; ++j) x[h][j] *= unit;
-                }
+                const BlockScale b = block_scale<F32, MX>(block_top<F32, B>(w[h]), unit, whole, inverses);
                 uint32_t codes[B / 8];
-                encode<MX, SR, B>(x[h], b, uint64_t(c) * a.col.vectors + uint64_t(r >> 3), 1, key, codes);
-                uint32_t* p = reinterpret_cast<uint32_t*>(out + col * kColPitch + blk * (B / 2));
+                encode<F32, MX, SR, B>(w[h], b, uint64_t(c) * a.col.vectors + uint64_t(r >> 3), 1, key, codes);
+                uint32_t* q = reinterpret_cast<uint32_t*>(out + col * kColPitch + blk * (B / 2));
 #pragma unroll
-                for (int j = 0; j < B / 8; ++j) p[j] = codes[j];
+                for (int j = 0; j < B / 8; ++j) q[j] = codes[j];
                 sc[1][(blk >> 2) * kFp4TileBytes + (col & 31) * 16 + (col >> 5) * 4 + (blk & 3)] =
                     static_cast<unsigned char>(c < a.cols && r < a.rows ? b.byte : 0);
             }
@@ -454,11 +508,14 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
 }
 
 // ---------------------------------------------------------------------------
-// Values of a quantised matrix.  A thread writes one aligned piece of a row: 16
-// bytes of bf16, 32 of fp32, the 8 elements that lie there (fewer at a row's
+// Values of a quantised matrix.  A thread writes one aligned piece of a row: 32
+// bytes of bf16, 64 of fp32, the 16 elements that lie there (fewer at a row's
 // ends); their codes, and their scales where a block ends among them, are
-// shifted into place, so rows may start anywhere.
+// shifted into place, so rows may start anywhere.  Pieces of 8 elements took 33
+// instructions an element, twice the time.
 // ---------------------------------------------------------------------------
+constexpr int kPiece = 16;
+
 struct DequantArgs {
     const unsigned char* codes;
     const unsigned char* scales;
@@ -474,54 +531,73 @@ __device__ __forceinline__ float scale_value(int byte, float unit) {
     return byte == 0x7F ? __uint_as_float(0x7FC00000u) : e4m3_value(byte) * unit;
 }
 
+// the values of eight codes
+__device__ __forceinline__ void widen_codes(uint32_t w, float* f) {
+    uint32_t h[4];
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+    }
+}
+
 template <bool F32, bool MX>
 __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ DequantArgs a) {
     constexpr int kSize = F32 ? 4 : 2, kShift = MX ? 5 : 4;   // log2 of a block
     pdl_enter();
     const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t r = a.pieces > 0x7FFFFFFF || t > 0x7FFFFFFF ? t / a.pieces : int64_t(uint32_t(t) / uint32_t(a.pieces));
+    const int64_t r = (a.pieces | t) > 0x7FFFFFFF ? t / a.pieces : int64_t(uint32_t(t) / uint32_t(a.pieces));
     if (r >= a.rows) return;
     unsigned char* row = static_cast<unsigned char*>(a.out) + r * a.stride * kSize;
-    const int skew = int(reinterpret_cast<uintptr_t>(row) & (8 * kSize - 1)) / kSize;   // elements before the row in its first piece
-    const int64_t e0 = (t - r * a.pieces) * 8 - skew;                                   // may be negative
-    if (e0 >= a.cols) return;
-    const int64_t first = max(e0, int64_t(0)), last = min(e0 + 8, a.cols) - 1;
-    // codes: 8 from e0 on, of two neighbouring words (those that the row has)
-    const int64_t word = e0 >> 3, words = a.pitch >> 2;
+    // elements before the row in its first piece
+    const int skew = int(reinterpret_cast<uintptr_t>(row) & (kPiece * kSize - 1)) / kSize;
+    const int cols = int(a.cols);
+    const int e0 = int(t - r * a.pieces) * kPiece - skew;     // may be negative
+    if (e0 >= cols) return;
+    const int first = max(e0, 0), last = min(e0 + kPiece, cols) - 1;
+    // codes: 16 from e0 on, of three neighbouring words (those that the row has)
+    const int word = e0 >> 3, most = int(a.pitch >> 2) - 1;
     const uint32_t* cp = reinterpret_cast<const uint32_t*>(a.codes + r * a.pitch);
-    const uint32_t w0 = __ldg(cp + max(word, int64_t(0))), w1 = __ldg(cp + min(word + 1, words - 1));
-    const uint32_t w = __funnelshift_r(w0, w1, 4 * int(e0 & 7));
+    uint32_t w[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) w[j] = __ldg(cp + min(max(word + j, 0), most));
     const unsigned char* sp = a.scales + (r >> 7) * a.tiles * kFp4TileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-    const int64_t b0 = first >> kShift, b1 = last >> kShift;
+    const int b0 = first >> kShift, b1 = last >> kShift;
     const float unit = MX ? 1.0f : __uint_as_float(0x3F800000u + uint32_t(fp4_exponent(__float_as_uint(__ldg(a.amax)))) * 0x800000u);
-    const float s0 = scale_value<MX>(__ldg(sp + (b0 >> 2) * kFp4TileBytes + (b0 & 3)), unit);
-    const float s1 = b1 == b0 ? s0 : scale_value<MX>(__ldg(sp + (b1 >> 2) * kFp4TileBytes + (b1 & 3)), unit);
-    const int change = int((b1 << kShift) - e0);            // first element of the second block
-    float v[8];
+    const float s0 = scale_value<MX>(__ldg(sp + int64_t(b0 >> 2) * kFp4TileBytes + (b0 & 3)), unit);
+    const float s1 = b1 == b0 ? s0 : scale_value<MX>(__ldg(sp + int64_t(b1 >> 2) * kFp4TileBytes + (b1 & 3)), unit);
+    const int change = (b1 << kShift) - e0;                   // first element of the second block
+    const bool whole = e0 >= 0 && e0 + kPiece <= cols;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t c = w >> (4 * j), m = c & 7u;
-        // .5 m below 2 (0, .5, 1, 1.5), else (2 + low bit) 2^(m / 2 - 2)
-        const float f = m < 2 ? 0.5f * float(m) : __uint_as_float((252u + m) << 22);
-        v[j] = ((c & 8u) ? -f : f) * (j < change ? s0 : s1);
-    }
-    if (e0 >= 0 && e0 + 8 <= a.cols) {
-        if (F32) {
-            F8 f;
+    for (int g = 0; g < 2; ++g) {
+        float v[8];
+        widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f.v[j] = v[j];
-            st_f8(reinterpret_cast<float*>(row) + e0, f);
+        for (int j = 0; j < 8; ++j) v[j] *= 8 * g + j < change ? s0 : s1;
+        if (whole) {
+            if (F32) {
+                F8 f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f.v[j] = v[j];
+                st_f8(reinterpret_cast<float*>(row) + e0 + 8 * g, f);
+            } else {
+                st_u4(row + (int64_t(e0) + 8 * g) * 2, narrow8(v));
+            }
         } else {
-            st_u4(row + e0 * 2, narrow8(v));
-        }
-        return;
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (e0 + j >= 0 && e0 + j < a.cols) {
-            if (F32) reinterpret_cast<float*>(row)[e0 + j] = v[j];
-            else reinterpret_cast<__nv_bfloat16*>(row)[e0 + j] = __float2bfloat16_rn(v[j]);
+            for (int j = 0; j < 8; ++j) {
+                const int e = e0 + 8 * g + j;
+                if (e < 0 || e >= cols) continue;
+                if (F32) reinterpret_cast<float*>(row)[e] = v[j];
+                else reinterpret_cast<__nv_bfloat16*>(row)[e] = __float2bfloat16_rn(v[j]);
+            }
         }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -652,7 +728,7 @@ static int quantize(QuantArgs& a, int32_t dtype, int32_t format, cudaStream_t s,
         const bool flat = a.stride == a.cols;
         const int64_t want = flat ? (n + 16383) / 16384 : a.rows;
         a.parts = int32_t(want < kAmaxParts ? want : kAmaxParts);
-        const int st = launch_k(f32 ? k_fp4_amax<true> : k_fp4_amax<false>, unsigned(a.parts), 256, s, who, a.x, a.rows,
+        const int st = launch_k(f32 ? k_fp4_amax<true> : k_fp4_amax<false>, unsigned(a.parts), kAmaxThreads, s, who, a.x, a.rows,
                                 a.cols, a.stride, int32_t(flat), reinterpret_cast<uint32_t*>(a.amax) + 1);
         if (st != DPG_OK) return st;
     }
@@ -719,8 +795,8 @@ int dpg_fp4_dequantize(const dpg_fp4* q, void* out, int32_t out_dtype, int64_t r
     a.stride = q->rows > 1 ? row_stride : q->cols;
     a.out = out;
     // one more where a row may start inside a piece
-    const bool whole = dpg::aligned(out, out_dtype == DPG_F32 ? 32 : 16) && (q->rows <= 1 || row_stride % 8 == 0);
-    a.pieces = (q->cols + 7) / 8 + (whole ? 0 : 1);
+    const bool whole = dpg::aligned(out, out_dtype == DPG_F32 ? 64 : 32) && (q->rows <= 1 || row_stride % dpg::kPiece == 0);
+    a.pieces = (q->cols + dpg::kPiece - 1) / dpg::kPiece + (whole ? 0 : 1);
     int grid = 0;
     st = dpg::grid_cover((a.rows * a.pieces + 255) / 256, &grid, "dpg_fp4_dequantize");
     if (st != DPG_OK) return st;
