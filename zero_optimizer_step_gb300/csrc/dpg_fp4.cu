@@ -18,7 +18,7 @@
 //     kept, the 22 bits below it are its distance from lo in units of 2^-22 gap: a
 //     sum with 2^22 - 1 - 32 (2 u + 1) carries where it is above the threshold.
 //     Below 1 the steps stay .5: there the same is done with y + 1, rounded up.
-#include <cuda_fp16.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -31,7 +31,7 @@
 
 namespace dpg {
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 512;
 constexpr int kQuantTile = 128;         // rows and columns of a CTA's tile
 
 struct QuantSide {
@@ -188,6 +188,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top, float unit, floa
         k = q < 0.015625f ? int(ceilf(r * 512.0f)) : int((__float_as_uint(r) + 0xFFFFFu) >> 20) - 960;
         k = k > 0x7E ? 0x7E : k;
     }
+    k = k == 0 && top != 0 ? 1 : k;                     // (u may have been too small for fp32)
     b.s = e4m3_value(k) * whole;
     b.inv = b.bad ? 0.0f : inverses[k] * unit;
     b.byte = b.bad ? 0x7F : k;
@@ -287,71 +288,90 @@ __device__ __forceinline__ uint32_t block_top(const uint32_t* w) {
 }
 
 // ---------------------------------------------------------------------------
-// Both orientations from one read.  A CTA takes 128 x 128 elements: rows from
-// registers as they were loaded, columns from shared memory.
+// Both orientations from one read.  A CTA takes 128 x 128 elements into shared
+// memory by asynchronous copies, with a thread to each block of a row and of a
+// column after that; codes leave through shared memory too, 64 bytes of a row at
+// a time.  (Blocks loaded to registers by the thread that takes them: lanes 32 to
+// 128 bytes apart, 16 warps to an SM, 68 us for 8192 x 4096 fp32 masters.)  Rows of
+// the tile are 16 bytes longer than a multiple of 128, so that neighbouring rows'
+// pieces lie in different banks.
 // ---------------------------------------------------------------------------
 template <bool F32>
 struct TileOf {
     static constexpr int kPitch = F32 ? 132 : 68;          // words of a row in shared memory
     static constexpr int kBytes = kQuantTile * kPitch * 4;
+    static constexpr int kPieces = F32 ? 32 : 16;          // 16-byte pieces of a row
+    static constexpr int kPer = F32 ? 4 : 8;               // elements of a piece
+    static constexpr int kLoads = kQuantTile * kPieces / kQuantThreads;
 };
-constexpr int kColPitch = 80;                              // bytes of a column's codes in shared memory
+constexpr int kCodesPitch = 72;                            // bytes of a row's codes in shared memory
 
-template <bool F32, bool MX>
-constexpr int quant_smem() { return TileOf<F32>::kBytes + kQuantTile * kColPitch; }
+template <bool F32>
+constexpr int quant_smem() { return TileOf<F32>::kBytes + 2 * kQuantTile * kCodesPitch; }
 
-// The B elements of row r from column c on, zeros behind the last.  Where rows do
-// not start on 16-byte boundaries, the 16-byte pieces that hold the block are
-// loaded (those that lie in the matrix) and shifted into place.
-template <bool F32, int B>
-__device__ __forceinline__ void load_block(const QuantArgs& a, int64_t r, int64_t c, uint32_t* w) {
-    constexpr int kWords = B * (F32 ? 4 : 2) / 4, kSize = F32 ? 4 : 2;
-    const int64_t at = r * a.stride + c;
+// `bytes` (0 .. 16) of a 16-byte piece, zeros behind them
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// One piece from element `at` on, `n` of its elements in the matrix.  Where rows
+// do not start on 16-byte boundaries, the two aligned pieces that hold it are
+// loaded (if both lie in the matrix) and shifted into place.
+template <bool F32>
+__device__ __forceinline__ uint4 load_piece(const QuantArgs& a, int64_t at, int64_t n, int64_t end) {
+    constexpr int kSize = F32 ? 4 : 2, kPer = TileOf<F32>::kPer;
     const unsigned char* p = static_cast<const unsigned char*>(a.x) + at * kSize;
-    const bool whole = r < a.rows && c + B <= a.cols;
-    if (a.vec) {
-        if (whole) {
-#pragma unroll
-            for (int j = 0; j < kWords / 4; ++j) {
-                const uint4 v = ld_grad_u4(p + 16 * j);
-                w[4 * j] = v.x;
-                w[4 * j + 1] = v.y;
-                w[4 * j + 2] = v.z;
-                w[4 * j + 3] = v.w;
-            }
-            return;
-        }
-    } else if (whole && at >= 16 / kSize && r + 1 < a.rows) {        // (not the first and the last few)
+    uint32_t w[4];
+    if (n >= kPer && at >= kPer && at + 2 * kPer <= end) {
         const int off = int(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
-        const unsigned char* q = p - off * kSize;
-        uint32_t v[kWords + 4];
-#pragma unroll
-        for (int j = 0; j < kWords / 4 + 1; ++j) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + (j < kWords / 4 || off ? j : 0));
-            v[4 * j] = u.x;
-            v[4 * j + 1] = u.y;
-            v[4 * j + 2] = u.z;
-            v[4 * j + 3] = u.w;
-        }
+        const uint4* q = reinterpret_cast<const uint4*>(p - off * kSize);
+        const uint4 lo = __ldg(q), hi = __ldg(q + 1);
+        uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
         const int words = F32 ? off : off >> 1;
 #pragma unroll
-        for (int j = 0; j < kWords + 2; ++j) v[j] = (words & 2) ? v[j + 2] : v[j];
+        for (int j = 0; j < 6; ++j) v[j] = (words & 2) ? v[j + 2] : v[j];
 #pragma unroll
-        for (int j = 0; j < kWords + 1; ++j) v[j] = (words & 1) ? v[j + 1] : v[j];
+        for (int j = 0; j < 5; ++j) v[j] = (words & 1) ? v[j + 1] : v[j];
 #pragma unroll
-        for (int j = 0; j < kWords; ++j)
-            w[j] = F32 ? v[j] : __funnelshift_r(v[j], v[j + 1], (off & 1) * 16);
-        return;
+        for (int j = 0; j < 4; ++j) w[j] = F32 ? v[j] : __funnelshift_r(v[j], v[j + 1], (off & 1) * 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) {
+    for (int j = 0; j < 4; ++j) {
         if (F32) {
-            w[j] = r < a.rows && c + j < a.cols ? __ldg(static_cast<const uint32_t*>(a.x) + at + j) : 0u;
+            w[j] = j < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + j) : 0u;
         } else {
-            const uint16_t* h = static_cast<const uint16_t*>(a.x) + at + 2 * j;
-            const uint32_t lo = r < a.rows && c + 2 * j < a.cols ? __ldg(h) : 0u;
-            const uint32_t hi = r < a.rows && c + 2 * j + 1 < a.cols ? __ldg(h + 1) : 0u;
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + 2 * j;
+            const uint32_t lo = 2 * j < n ? __ldg(h) : 0u, hi = 2 * j + 1 < n ? __ldg(h + 1) : 0u;
             w[j] = lo | hi << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t r0, int64_t c0, uint32_t* tile) {
+    using T = TileOf<F32>;
+    if (a.vec) {
+#pragma unroll
+        for (int k = 0; k < T::kLoads; ++k) {
+            const int id = k * kQuantThreads + int(threadIdx.x), row = id / T::kPieces, piece = id % T::kPieces;
+            const int64_t r = r0 + row, c = c0 + piece * T::kPer;
+            const int64_t n = r < a.rows ? min(a.cols - c, int64_t(T::kPer)) : 0;
+            const bool some = n > 0;
+            copy_piece(smem_u32(tile + row * T::kPitch + piece * 4),
+                       static_cast<const unsigned char*>(a.x) + (some ? r * a.stride + c : 0) * (F32 ? 4 : 2),
+                       some ? int(n) * (F32 ? 4 : 2) : 0);
+        }
+    } else {
+        const int64_t end = (a.rows - 1) * a.stride + a.cols;
+#pragma unroll 4
+        for (int k = 0; k < T::kLoads; ++k) {
+            const int id = k * kQuantThreads + int(threadIdx.x), row = id / T::kPieces, piece = id % T::kPieces;
+            const int64_t r = r0 + row, c = c0 + piece * T::kPer;
+            const int64_t n = r < a.rows ? a.cols - c : 0;
+            *reinterpret_cast<uint4*>(tile + row * T::kPitch + piece * 4) =
+                n > 0 ? load_piece<F32>(a, r * a.stride + c, n, end) : make_uint4(0, 0, 0, 0);
         }
     }
 }
@@ -367,7 +387,8 @@ __device__ __forceinline__ uint32_t larger(uint32_t w) {
 }
 
 template <bool F32, bool MX, bool SR>
-__global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
+    using T = TileOf<F32>;
     constexpr int B = MX ? 32 : 16;                        // elements of a block
     constexpr int kBlocks = kQuantTile / B;                // blocks of a tile's row
     constexpr int kTasks = kQuantTile * kBlocks / kQuantThreads;
@@ -375,34 +396,32 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
     constexpr int kTiles = kBlocks / 4;                    // scale tiles of a tile
     extern __shared__ __align__(16) uint32_t tile[];
     __shared__ __align__(16) unsigned char sc[2][kTiles * kFp4TileBytes];
-    unsigned char* const out = reinterpret_cast<unsigned char*>(tile) + TileOf<F32>::kBytes;
-    pdl_enter();
+    unsigned char* const out = reinterpret_cast<unsigned char*>(tile) + T::kBytes;
     const int64_t ti = blockIdx.x / a.tiles_c, tj = blockIdx.x % a.tiles_c;
     const int64_t r0 = ti * kQuantTile, c0 = tj * kQuantTile;
     const int tid = int(threadIdx.x);
-    const bool by_row = a.row.codes != nullptr, by_col = a.col.codes != nullptr;
+    // After k_fp4_amax, which has itself waited for what came before it, x may be read at once.
+    if (!a.parts) pdl_enter();
+    load_tile<F32>(a, r0, c0, tile);
+    if (a.parts) pdl_enter();
     const uint64_t key = SR ? uint64_t(__ldg(a.seed) + a.seed_plus) : 0;
-
-    uint32_t raw[kTasks][kWords];
-#pragma unroll
-    for (int k = 0; k < kTasks; ++k) {
-        const int task = k * kQuantThreads + tid, row = task / kBlocks, blk = task % kBlocks;
-        load_block<F32, B>(a, r0 + row, c0 + blk * B, raw[k]);
-    }
     float unit = 1.0f, whole = 1.0f;
     bool tiny = false;
     __shared__ float inverses[MX ? 1 : kInverses];
     if (!MX) {
-        __shared__ uint32_t sh[8];
+        __shared__ uint32_t sh[kQuantThreads / 32];
         uint32_t m = 0;
         if (tid < kInverses) inverses[tid] = tid == 0 || tid == 0x7F ? 0.0f : 1.0f / e4m3_value(tid);   // (block_max waits)
         if (a.parts) {
             if (tid < a.parts) m = __ldcg(reinterpret_cast<const uint32_t*>(a.amax) + 1 + tid);
         } else {
+            asm volatile("cp.async.wait_all;" ::: "memory");       // (this thread's own pieces)
 #pragma unroll
-            for (int k = 0; k < kTasks; ++k)
-#pragma unroll
-                for (int j = 0; j < kWords; ++j) m = max(m, magnitude_bits<F32>(raw[k][j]));
+            for (int k = 0; k < T::kLoads; ++k) {
+                const int id = k * kQuantThreads + tid;
+                m = max(m, magnitude_bits4<F32>(
+                               *reinterpret_cast<const uint4*>(tile + id / T::kPieces * T::kPitch + id % T::kPieces * 4)));
+            }
         }
         m = block_max<kQuantThreads / 32>(m, sh);
         if (!a.parts && gridDim.x > 1) {
@@ -425,84 +444,68 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
             if (a.amax_copy) *a.amax_copy = __uint_as_float(m);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kTasks; ++k) {
-        const int task = k * kQuantThreads + tid, row = task / kBlocks, blk = task % kBlocks;
-        if (tiny) {
+    for (int side = 0; side < 2; ++side) {
+        const QuantSide& q = side ? a.col : a.row;
+        if (!q.codes) continue;
+        const int64_t major = side ? c0 : r0, minor = side ? r0 : c0;          // of the quantised matrix's rows, columns
+        const int64_t n_major = side ? a.cols : a.rows, n_minor = side ? a.rows : a.cols;
+#pragma unroll 1
+        for (int k = 0; k < kTasks; ++k) {
+            const int task = k * kQuantThreads + tid, line = task % kQuantTile, blk = task / kQuantTile;
+            uint32_t w[kWords];
+            if (side == 0) {
+                const uint4* p = reinterpret_cast<const uint4*>(tile + line * T::kPitch + blk * kWords);
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) raw[k][j] = larger<F32>(raw[k][j]);
-        }
-        if (by_col) {
-            uint4* p = reinterpret_cast<uint4*>(tile + row * TileOf<F32>::kPitch + blk * kWords);
+                for (int j = 0; j < kWords / 4; ++j) {
+                    const uint4 v = p[j];
+                    w[4 * j] = v.x;
+                    w[4 * j + 1] = v.y;
+                    w[4 * j + 2] = v.z;
+                    w[4 * j + 3] = v.w;
+                }
+            } else {
+                const uint32_t* p = tile + blk * B * T::kPitch + (F32 ? line : line >> 1);
+                const uint32_t half = line & 1 ? 0x7632u : 0x5410u;
 #pragma unroll
-            for (int j = 0; j < kWords / 4; ++j)
-                p[j] = make_uint4(raw[k][4 * j], raw[k][4 * j + 1], raw[k][4 * j + 2], raw[k][4 * j + 3]);
+                for (int j = 0; j < kWords; ++j)
+                    w[j] = F32 ? p[j * T::kPitch] : __byte_perm(p[2 * j * T::kPitch], p[(2 * j + 1) * T::kPitch], half);
+            }
+            if (tiny) {
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) w[j] = larger<F32>(w[j]);
+            }
+            const int64_t i = major + line, j0 = minor + blk * B;
+            const BlockScale b = block_scale<F32, MX>(block_top<F32, B>(w), unit, whole, inverses);
+            uint32_t codes[B / 8];
+            encode<F32, MX, SR, B>(w, b, uint64_t(i) * q.vectors + uint64_t(j0 >> 3), side, key, codes);
+            uint2* p = reinterpret_cast<uint2*>(out + (side * kQuantTile + line) * kCodesPitch + blk * (B / 2));
+#pragma unroll
+            for (int j = 0; j < B / 16; ++j) p[j] = make_uint2(codes[2 * j], codes[2 * j + 1]);
+            sc[side][(blk >> 2) * kFp4TileBytes + (line & 31) * 16 + (line >> 5) * 4 + (blk & 3)] =
+                static_cast<unsigned char>(i < n_major && j0 < n_minor ? b.byte : 0);
         }
-        if (!by_row) continue;
-        const int64_t r = r0 + row, c = c0 + blk * B;
-        const BlockScale b = block_scale<F32, MX>(block_top<F32, B>(raw[k]), unit, whole, inverses);
-        uint32_t codes[B / 8];
-        encode<F32, MX, SR, B>(raw[k], b, uint64_t(r) * a.row.vectors + uint64_t(c >> 3), 0, key, codes);
-        if (r < a.rows && c < a.cols) {
-            unsigned char* p = a.row.codes + r * a.row.pitch + (c >> 1);
-            if (MX) *reinterpret_cast<uint4*>(p) = make_uint4(codes[0], codes[1], codes[B / 8 - 2], codes[B / 8 - 1]);
-            else if ((blk & 1) == 0 && c + B >= a.cols) *reinterpret_cast<uint4*>(p) = make_uint4(codes[0], codes[1], 0, 0);
-            else *reinterpret_cast<uint2*>(p) = make_uint2(codes[0], codes[1]);
-        }
-        sc[0][(blk >> 2) * kFp4TileBytes + (row & 31) * 16 + (row >> 5) * 4 + (blk & 3)] =
-            static_cast<unsigned char>(r < a.rows && c < a.cols ? b.byte : 0);
     }
     __syncthreads();
-    if (by_col) {
-        // two neighbouring columns and one block of rows to a task
-        constexpr int kColTasks = kQuantTile / 2 * kBlocks / kQuantThreads;
-#pragma unroll 1
-        for (int k = 0; k < kColTasks; ++k) {
-            const int task = k * kQuantThreads + tid, pair = task % (kQuantTile / 2), blk = task / (kQuantTile / 2);
-            const int64_t r = r0 + blk * B;
-            uint32_t w[2][kWords];
-            const uint32_t* p = tile + blk * B * TileOf<F32>::kPitch + (F32 ? 2 * pair : pair);
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                if (F32) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p + j * TileOf<F32>::kPitch);
-                    w[0][j] = v.x;
-                    w[1][j] = v.y;
-                } else {
-                    const uint32_t v = p[2 * j * TileOf<F32>::kPitch], u = p[(2 * j + 1) * TileOf<F32>::kPitch];
-                    w[0][j] = __byte_perm(v, u, 0x5410);
-                    w[1][j] = __byte_perm(v, u, 0x7632);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int col = 2 * pair + h;
-                const int64_t c = c0 + col;
-                const BlockScale b = block_scale<F32, MX>(block_top<F32, B>(w[h]), unit, whole, inverses);
-                uint32_t codes[B / 8];
-                encode<F32, MX, SR, B>(w[h], b, uint64_t(c) * a.col.vectors + uint64_t(r >> 3), 1, key, codes);
-                uint32_t* q = reinterpret_cast<uint32_t*>(out + col * kColPitch + blk * (B / 2));
-#pragma unroll
-                for (int j = 0; j < B / 8; ++j) q[j] = codes[j];
-                sc[1][(blk >> 2) * kFp4TileBytes + (col & 31) * 16 + (col >> 5) * 4 + (blk & 3)] =
-                    static_cast<unsigned char>(c < a.cols && r < a.rows ? b.byte : 0);
-            }
-        }
-        __syncthreads();
-        for (int k = tid; k < kQuantTile * 4; k += kQuantThreads) {      // 16 bytes: 32 rows of a column
-            const int col = k >> 2, part = k & 3;
-            if (c0 + col < a.cols && r0 + part * 32 < a.rows)
-                *reinterpret_cast<uint4*>(a.col.codes + (c0 + col) * a.col.pitch + (r0 >> 1) + part * 16) =
-                    *reinterpret_cast<const uint4*>(out + col * kColPitch + part * 16);
-        }
-    }
-    for (int k = tid; k < 2 * kTiles * 32; k += kQuantThreads) {
-        const int side = k / (kTiles * 32), t = k / 32 % kTiles, part = k % 32;
+    for (int side = 0; side < 2; ++side) {
         const QuantSide& q = side ? a.col : a.row;
-        const int64_t i = side ? tj : ti, j = (side ? ti : tj) * kTiles + t;
-        if (q.codes && j < q.tiles)
-            *reinterpret_cast<uint4*>(q.scales + (i * q.tiles + j) * kFp4TileBytes + part * 16) =
-                *reinterpret_cast<const uint4*>(sc[side] + t * kFp4TileBytes + part * 16);
+        if (!q.codes) continue;
+        const int64_t major = side ? c0 : r0, minor = side ? r0 : c0, n_major = side ? a.cols : a.rows;
+#pragma unroll
+        for (int k = 0; k < kQuantTile * 8 / kQuantThreads; ++k) {             // 8 bytes: 16 codes of a row
+            const int id = k * kQuantThreads + tid, line = id >> 3, part = id & 7;
+            const int64_t at = (minor >> 1) + part * 8;
+            if (major + line < n_major && at < q.pitch)
+                *reinterpret_cast<uint2*>(q.codes + (major + line) * q.pitch + at) =
+                    *reinterpret_cast<const uint2*>(out + (side * kQuantTile + line) * kCodesPitch + part * 8);
+        }
+        const int64_t i = side ? tj : ti, j0 = (side ? ti : tj) * kTiles;
+        if (tid < kTiles * 32 && j0 + tid / 32 < q.tiles)
+            *reinterpret_cast<uint4*>(q.scales + (i * q.tiles + j0) * kFp4TileBytes + tid * 16) =
+                *reinterpret_cast<const uint4*>(sc[side] + tid * 16);
     }
     if (!MX && !a.parts && gridDim.x > 1) cluster_sync();   // the others have read this CTA's maximum
 }
@@ -511,8 +514,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize(const __grid_con
 // Values of a quantised matrix.  A thread writes one aligned piece of a row: 32
 // bytes of bf16, 64 of fp32, the 16 elements that lie there (fewer at a row's
 // ends); their codes, and their scales where a block ends among them, are
-// shifted into place, so rows may start anywhere.  Pieces of 8 elements took 33
-// instructions an element, twice the time.
+// shifted into place, so rows may start anywhere.  (Pieces of 8 elements and
+// conversions one by one took 33 instructions an element.)
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 16;
 
@@ -531,19 +534,22 @@ __device__ __forceinline__ float scale_value(int byte, float unit) {
     return byte == 0x7F ? __uint_as_float(0x7FC00000u) : e4m3_value(byte) * unit;
 }
 
-// the values of eight codes
-__device__ __forceinline__ void widen_codes(uint32_t w, float* f) {
-    uint32_t h[4];
-    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
-        " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
-        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+// Eight codes as four pairs of bf16.  The two bytes of a magnitude are picked from
+// tables in registers by the code's low three bits, four codes at a time.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t* h) {
+    // 0 .5 1 1.5 2 3 4 6 = 0000 3F00 3F80 3FC0 4000 4040 4080 40C0
+    constexpr uint32_t hi0 = 0x3F3F3F00u, hi1 = 0x40404040u, lo0 = 0xC0800000u, lo1 = 0xC0804000u;
+    const uint32_t m = w & 0x77777777u, w4 = w << 4;
+    uint32_t hi = __byte_perm(hi0, hi1, m), lo = __byte_perm(lo0, lo1, m);
+    h[0] = __byte_perm(lo, hi, 0x5140);
+    h[1] = __byte_perm(lo, hi, 0x7362);
+    hi = __byte_perm(hi0, hi1, m >> 16);
+    lo = __byte_perm(lo0, lo1, m >> 16);
+    h[2] = __byte_perm(lo, hi, 0x5140);
+    h[3] = __byte_perm(lo, hi, 0x7362);
+    // signs: bit 7 of byte j of w << 4, and of w
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-        f[2 * j] = v.x;
-        f[2 * j + 1] = v.y;
-    }
+    for (int j = 0; j < 4; ++j) h[j] |= __byte_perm(w4, w, uint32_t(j) << 4 | uint32_t(4 + j) << 12) & 0x80008000u;
 }
 
 template <bool F32, bool MX>
@@ -564,8 +570,15 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
     const int word = e0 >> 3, most = int(a.pitch >> 2) - 1;
     const uint32_t* cp = reinterpret_cast<const uint32_t*>(a.codes + r * a.pitch);
     uint32_t w[3];
+    if ((e0 & 15) == 0) {
+        const uint2 two = __ldg(reinterpret_cast<const uint2*>(cp + word));
+        w[0] = two.x;
+        w[1] = two.y;
+        w[2] = 0;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 3; ++j) w[j] = __ldg(cp + min(max(word + j, 0), most));
+        for (int j = 0; j < 3; ++j) w[j] = __ldg(cp + min(max(word + j, 0), most));
+    }
     const unsigned char* sp = a.scales + (r >> 7) * a.tiles * kFp4TileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
     const int b0 = first >> kShift, b1 = last >> kShift;
     const float unit = MX ? 1.0f : __uint_as_float(0x3F800000u + uint32_t(fp4_exponent(__float_as_uint(__ldg(a.amax)))) * 0x800000u);
@@ -573,12 +586,37 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
     const float s1 = b1 == b0 ? s0 : scale_value<MX>(__ldg(sp + int64_t(b1 >> 2) * kFp4TileBytes + (b1 & 3)), unit);
     const int change = (b1 << kShift) - e0;                   // first element of the second block
     const bool whole = e0 >= 0 && e0 + kPiece <= cols;
+    // Products in bf16 are exact (2 and 4 bits) unless a scale or a result is below its normal numbers.
+    const bool normal = !F32 && !(s0 != 0.0f && s0 < 7.5e-37f) && !(s1 != 0.0f && s1 < 7.5e-37f);
+    const __nv_bfloat162 t0 = __float2bfloat162_rn(s0), t1 = __float2bfloat162_rn(s1),
+                         both = __halves2bfloat162(t0.x, t1.x);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
+        uint32_t h[4];
+        widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), h);
         float v[8];
-        widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), v);
+        if (F32 || !normal) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= 8 * g + j < change ? s0 : s1;
+            for (int j = 0; j < 4; ++j) {
+                widen2(h[j], v[2 * j], v[2 * j + 1]);
+                v[2 * j] *= 8 * g + 2 * j < change ? s0 : s1;
+                v[2 * j + 1] *= 8 * g + 2 * j + 1 < change ? s0 : s1;
+            }
+        }
+        if (!F32) {
+            if (normal) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int e = 8 * g + 2 * j;
+                    const __nv_bfloat162 p =
+                        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h[j]), e + 1 < change ? t0 : e < change ? both : t1);
+                    h[j] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+            } else {
+                const uint4 n = narrow8(v);
+                h[0] = n.x, h[1] = n.y, h[2] = n.z, h[3] = n.w;
+            }
+        }
         if (whole) {
             if (F32) {
                 F8 f;
@@ -586,7 +624,7 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
                 for (int j = 0; j < 8; ++j) f.v[j] = v[j];
                 st_f8(reinterpret_cast<float*>(row) + e0 + 8 * g, f);
             } else {
-                st_u4(row + (int64_t(e0) + 8 * g) * 2, narrow8(v));
+                st_u4(row + (int64_t(e0) + 8 * g) * 2, make_uint4(h[0], h[1], h[2], h[3]));
             }
         } else {
 #pragma unroll
@@ -594,7 +632,7 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
                 const int e = e0 + 8 * g + j;
                 if (e < 0 || e >= cols) continue;
                 if (F32) reinterpret_cast<float*>(row)[e] = v[j];
-                else reinterpret_cast<__nv_bfloat16*>(row)[e] = __float2bfloat16_rn(v[j]);
+                else reinterpret_cast<uint16_t*>(row)[e] = uint16_t(h[j >> 1] >> (16 * (j & 1)));
             }
         }
     }
@@ -685,12 +723,10 @@ static int quant_args(const void* x, int32_t dtype, int64_t rows, int64_t cols, 
 template <bool F32, bool MX, bool SR>
 static int launch_quant(const QuantArgs& a, int64_t tiles, cudaStream_t s, const char* who) {
     auto k = k_fp4_quantize<F32, MX, SR>;
-    const int smem = a.col.codes ? quant_smem<F32, MX>() : 0;
-    if (smem > 48 * 1024) {
-        static std::atomic<uint64_t> once{0};
-        const int st = allow_smem(reinterpret_cast<const void*>(k), smem, once, who);
-        if (st != DPG_OK) return st;
-    }
+    const int smem = quant_smem<F32>();
+    static std::atomic<uint64_t> once{0};
+    const int st = allow_smem(reinterpret_cast<const void*>(k), smem, once, who);
+    if (st != DPG_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(tiles));
     cfg.blockDim = dim3(kQuantThreads);
