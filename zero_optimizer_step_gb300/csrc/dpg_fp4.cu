@@ -13,11 +13,11 @@
 //     quotient whose x is not on it rounds to something else than m, and ties stay
 //     ties.  The product with the reciprocal alone is off by one unit for 11 of the
 //     56 borderlines, and would round those ties up.
-//   * stochastic: the threshold lo + (2 u + 1) 2^-17 gap is an fp32 number, so y
-//     is above it exactly where y rounded up is.  With one bit of y's significand
-//     kept, the 22 bits below it are its distance from lo in units of 2^-22 gap: a
-//     sum with 2^22 - 1 - 32 (2 u + 1) carries where it is above the threshold.
-//     Below 1 the steps stay .5: there the same is done with y + 1, rounded up.
+//   * stochastic: the place of y between the values, in codes, is min(2 y, y + 2,
+//     y / 2 + 4), and y goes up where the fraction of that place is above (2 u + 1)
+//     2^-17.  The threshold is an fp32 number, so y, the lines and a sum with 32,
+//     whose last place is 2^-18, may all be rounded up; then the place is an
+//     integer in units of 2^-18, and one less 4 u carries where it is above.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -129,9 +129,8 @@ __global__ void __launch_bounds__(kAmaxThreads) k_fp4_amax(const void* x, int64_
 // One block
 // ---------------------------------------------------------------------------
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011)
-__device__ __forceinline__ uint4 philox(uint64_t n, uint32_t side, uint64_t key) {
-    uint32_t x0 = uint32_t(n), x1 = uint32_t(n >> 32), x2 = side, x3 = 0, k0 = uint32_t(key),
-             k1 = uint32_t(key >> 32);
+__device__ __forceinline__ uint4 philox(uint64_t n, uint32_t side, uint2 key) {
+    uint32_t x0 = uint32_t(n), x1 = uint32_t(n >> 32), x2 = side, x3 = 0, k0 = key.x, k1 = key.y;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
         const uint32_t a = __umulhi(0xD2511F53u, x0), b = 0xD2511F53u * x0;
@@ -207,68 +206,75 @@ __device__ __forceinline__ uint32_t nearest8(const uint64_t* y) {
     return r;
 }
 
-// Code of y >= 0, rounded up where it is not exact, to the value above where the
-// 16 bits u say so.
-__device__ __forceinline__ uint32_t stochastic(float y, uint32_t u) {
-    const bool small = y < 1.0f;
-    const uint32_t z = __float_as_uint(small ? __fadd_ru(y, 1.0f) : y);
-    return ((z + (0x400000u - 1u - 32u) - 64u * u) >> 22) - (small ? 254u : 252u);
+__device__ __forceinline__ uint64_t fma2_up(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rp.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 32 + the place of y >= 0 between the values + 1 - 3 * 2^-18, rounded up to 2^-18
+__device__ __forceinline__ void places(uint64_t y, uint32_t* p) {
+    constexpr float one = 1.0f - 3.0f / 262144.0f;
+    const float2 a = halves_of(fma2_up(y, pair_of(2.0f, 2.0f), pair_of(32.0f + one, 32.0f + one)));
+    const float2 b = halves_of(fma2_up(y, pair_of(1.0f, 1.0f), pair_of(34.0f + one, 34.0f + one)));
+    const float2 c = halves_of(fma2_up(y, pair_of(0.5f, 0.5f), pair_of(36.0f + one, 36.0f + one)));
+    p[0] = __float_as_uint(fminf(fminf(a.x, b.x), c.x));
+    p[1] = __float_as_uint(fminf(fminf(a.y, b.y), c.y));
 }
 
 // B elements of a block to codes, 8 to a word.  w: the elements as they are in
 // memory (bf16: two to a word); n0: number of their first group of 8 (random bits).
 template <bool F32, bool MX, bool SR, int B>
-__device__ __forceinline__ void encode(const uint32_t* w, const BlockScale& b, uint64_t n0, uint32_t side, uint64_t key,
+__device__ __forceinline__ void encode(const uint32_t* w, const BlockScale& b, uint64_t n0, uint32_t side, uint2 key,
                                        uint32_t* out) {
     const uint64_t inv = pair_of(b.inv, b.inv), s = pair_of(-b.s, -b.s);
 #pragma unroll
     for (int g = 0; g < B / 8; ++g) {
         uint64_t y[4];
-        uint32_t up = 0;           // which quotients are rounded down
-        uint32_t signs = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int at = 4 * g + j;                       // of a pair
             float lo, hi;
             if (F32) {
-                lo = __uint_as_float(w[2 * at]);
-                hi = __uint_as_float(w[2 * at + 1]);
+                lo = __uint_as_float(SR ? w[2 * at] & 0x7FFFFFFFu : w[2 * at]);
+                hi = __uint_as_float(SR ? w[2 * at + 1] & 0x7FFFFFFFu : w[2 * at + 1]);
             } else {
-                widen2(w[at], lo, hi);
-            }
-            if (SR) {
-                signs |= (__float_as_uint(lo) >> 31) << (8 * j + 3) | (__float_as_uint(hi) >> 31) << (8 * j + 7);
-                lo = fabsf(lo);
-                hi = fabsf(hi);
+                widen2(SR ? w[at] & 0x7FFF7FFFu : w[at], lo, hi);
             }
             const uint64_t x = pair_of(lo, hi);
             y[j] = mul2(x, inv);
             if (!MX) {
                 y[j] = fma2(fma2(y[j], s, x), inv, y[j]);
-                if (SR) {
-                    const float2 rest = halves_of(fma2(y[j], s, x));
-                    up |= (rest.x > 0.0f ? 1u : 0u) << (2 * j) | (rest.y > 0.0f ? 2u : 0u) << (2 * j);
-                }
+                // up, where it is not exact (what is left of x tells which)
+                if (SR) y[j] = fma2_up(fma2(y[j], s, x), inv, y[j]);
             }
         }
-        uint32_t word;
         if (SR) {
             const uint4 r = philox(n0 + g, side, key);
             const uint32_t h[4] = {r.x, r.y, r.z, r.w};
-            word = signs;
+            uint32_t lo, hi;                                // bytes that hold the signs in bit 7
+            if (F32) {
+                const uint32_t* v = w + 8 * g;
+                lo = __byte_perm(__byte_perm(v[0], v[2], 0x0073), __byte_perm(v[4], v[6], 0x0073), 0x5410);
+                hi = __byte_perm(__byte_perm(v[1], v[3], 0x0073), __byte_perm(v[5], v[7], 0x0073), 0x5410);
+            } else {
+                const uint32_t* v = w + 4 * g;
+                lo = __byte_perm(__byte_perm(v[0], v[1], 0x0051), __byte_perm(v[2], v[3], 0x0051), 0x5410);
+                hi = __byte_perm(__byte_perm(v[0], v[1], 0x0073), __byte_perm(v[2], v[3], 0x0073), 0x5410);
+            }
+            uint32_t word = (hi & 0x80808080u) | ((lo & 0x80808080u) >> 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 f = halves_of(y[j]);
-                if (!MX) {
-                    f.x = __uint_as_float(__float_as_uint(f.x) + (up >> (2 * j) & 1u));
-                    f.y = __uint_as_float(__float_as_uint(f.y) + (up >> (2 * j + 1) & 1u));
-                }
-                word |= stochastic(f.x, h[j] & 0xFFFFu) << (8 * j) | stochastic(f.y, h[j] >> 16) << (8 * j + 4);
+                uint32_t p[2];
+                places(y[j], p);
+                const uint32_t t = p[0] - 4u * (h[j] & 0xFFFFu), v = p[1] - 4u * (h[j] >> 16);
+                // codes in bits 18 .. 20, nothing set above them up to bit 24
+                word |= (8 * j < 18 ? t >> (18 - 8 * j) : t << (8 * j - 18)) & (7u << (8 * j));
+                word |= (8 * j + 4 < 18 ? v >> (14 - 8 * j) : v << (8 * j - 14)) & (7u << (8 * j + 4));
             }
+            out[g] = b.bad ? 0u : word;
         } else {
-            word = nearest8(y);
+            out[g] = b.bad ? 0u : nearest8(y);
         }
-        out[g] = b.bad ? 0u : word;
     }
 }
 
@@ -283,7 +289,7 @@ __device__ __forceinline__ uint32_t block_top(const uint32_t* w) {
     } else {
 #pragma unroll
         for (int j = 0; j < B / 2; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
-        return max(top << 16, top & 0xFFFF0000u);
+        return max(top << 16, top) & 0xFFFF0000u;
     }
 }
 
@@ -318,7 +324,7 @@ __device__ __forceinline__ void copy_piece(uint32_t dst, const void* src, int by
 // do not start on 16-byte boundaries, the two aligned pieces that hold it are
 // loaded (if both lie in the matrix) and shifted into place.
 template <bool F32>
-__device__ __forceinline__ uint4 load_piece(const QuantArgs& a, int64_t at, int64_t n, int64_t end) {
+__device__ __forceinline__ uint4 load_piece(const QuantArgs& a, int64_t at, int n, int64_t end) {
     constexpr int kSize = F32 ? 4 : 2, kPer = TileOf<F32>::kPer;
     const unsigned char* p = static_cast<const unsigned char*>(a.x) + at * kSize;
     uint32_t w[4];
@@ -349,29 +355,33 @@ __device__ __forceinline__ uint4 load_piece(const QuantArgs& a, int64_t at, int6
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// rows, cols: of the tile that the matrix has
 template <bool F32>
-__device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t r0, int64_t c0, uint32_t* tile) {
+__device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t r0, int64_t c0, int rows, int cols, uint32_t* tile) {
     using T = TileOf<F32>;
+    constexpr int kSize = F32 ? 4 : 2, kStep = kQuantThreads / T::kPieces;     // rows from one load to the next
+    const int row0 = int(threadIdx.x) / T::kPieces, piece = int(threadIdx.x) % T::kPieces;
+    const int n = cols - piece * T::kPer;                                      // elements from the piece's first on
+    int64_t at = (r0 + row0) * a.stride + c0 + piece * T::kPer;
     if (a.vec) {
+        const int bytes = n >= T::kPer ? 16 : n > 0 ? n * kSize : 0;
+        const unsigned char* p = static_cast<const unsigned char*>(a.x) + at * kSize;
+        const int64_t step = kStep * a.stride * kSize;
+        uint32_t dst = smem_u32(tile + row0 * T::kPitch + piece * 4);
 #pragma unroll
         for (int k = 0; k < T::kLoads; ++k) {
-            const int id = k * kQuantThreads + int(threadIdx.x), row = id / T::kPieces, piece = id % T::kPieces;
-            const int64_t r = r0 + row, c = c0 + piece * T::kPer;
-            const int64_t n = r < a.rows ? min(a.cols - c, int64_t(T::kPer)) : 0;
-            const bool some = n > 0;
-            copy_piece(smem_u32(tile + row * T::kPitch + piece * 4),
-                       static_cast<const unsigned char*>(a.x) + (some ? r * a.stride + c : 0) * (F32 ? 4 : 2),
-                       some ? int(n) * (F32 ? 4 : 2) : 0);
+            const int some = row0 + k * kStep < rows ? bytes : 0;
+            copy_piece(dst, some ? p : a.x, some);
+            p += step;
+            dst += kStep * T::kPitch * 4;
         }
     } else {
         const int64_t end = (a.rows - 1) * a.stride + a.cols;
 #pragma unroll 4
         for (int k = 0; k < T::kLoads; ++k) {
-            const int id = k * kQuantThreads + int(threadIdx.x), row = id / T::kPieces, piece = id % T::kPieces;
-            const int64_t r = r0 + row, c = c0 + piece * T::kPer;
-            const int64_t n = r < a.rows ? a.cols - c : 0;
-            *reinterpret_cast<uint4*>(tile + row * T::kPitch + piece * 4) =
-                n > 0 ? load_piece<F32>(a, r * a.stride + c, n, end) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(tile + (row0 + k * kStep) * T::kPitch + piece * 4) =
+                n > 0 && row0 + k * kStep < rows ? load_piece<F32>(a, at, n, end) : make_uint4(0, 0, 0, 0);
+            at += kStep * a.stride;
         }
     }
 }
@@ -400,11 +410,17 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
     const int64_t ti = blockIdx.x / a.tiles_c, tj = blockIdx.x % a.tiles_c;
     const int64_t r0 = ti * kQuantTile, c0 = tj * kQuantTile;
     const int tid = int(threadIdx.x);
+    const int rows = int(min(a.rows - r0, int64_t(kQuantTile))), cols = int(min(a.cols - c0, int64_t(kQuantTile)));
     // After k_fp4_amax, which has itself waited for what came before it, x may be read at once.
     if (!a.parts) pdl_enter();
-    load_tile<F32>(a, r0, c0, tile);
+    load_tile<F32>(a, r0, c0, rows, cols, tile);
     if (a.parts) pdl_enter();
-    const uint64_t key = SR ? uint64_t(__ldg(a.seed) + a.seed_plus) : 0;
+    uint2 key = make_uint2(0, 0);
+    if (SR) {                                              // (the same in the warp: its schedule stays in uniform registers)
+        const uint64_t k = uint64_t(__ldg(a.seed) + a.seed_plus);
+        key.x = __shfl_sync(0xFFFFFFFFu, uint32_t(k), 0);
+        key.y = __shfl_sync(0xFFFFFFFFu, uint32_t(k >> 32), 0);
+    }
     float unit = 1.0f, whole = 1.0f;
     bool tiny = false;
     __shared__ float inverses[MX ? 1 : kInverses];
@@ -450,11 +466,14 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
     for (int side = 0; side < 2; ++side) {
         const QuantSide& q = side ? a.col : a.row;
         if (!q.codes) continue;
-        const int64_t major = side ? c0 : r0, minor = side ? r0 : c0;          // of the quantised matrix's rows, columns
-        const int64_t n_major = side ? a.cols : a.rows, n_minor = side ? a.rows : a.cols;
+        const int lines = side ? cols : rows, length = side ? rows : cols;     // of the quantised matrix that the tile has
+        const int line = tid % kQuantTile;
+        unsigned char* const place = out + (side * kQuantTile + line) * kCodesPitch;
+        unsigned char* const scale = sc[side] + (line & 31) * 16 + (line >> 5) * 4;
+        const uint64_t group = SR ? uint64_t((side ? c0 : r0) + line) * q.vectors + uint64_t((side ? r0 : c0) >> 3) : 0;
 #pragma unroll 1
         for (int k = 0; k < kTasks; ++k) {
-            const int task = k * kQuantThreads + tid, line = task % kQuantTile, blk = task / kQuantTile;
+            const int blk = k * (kQuantThreads / kQuantTile) + tid / kQuantTile;
             uint32_t w[kWords];
             if (side == 0) {
                 const uint4* p = reinterpret_cast<const uint4*>(tile + line * T::kPitch + blk * kWords);
@@ -477,15 +496,14 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) w[j] = larger<F32>(w[j]);
             }
-            const int64_t i = major + line, j0 = minor + blk * B;
             const BlockScale b = block_scale<F32, MX>(block_top<F32, B>(w), unit, whole, inverses);
             uint32_t codes[B / 8];
-            encode<F32, MX, SR, B>(w, b, uint64_t(i) * q.vectors + uint64_t(j0 >> 3), side, key, codes);
-            uint2* p = reinterpret_cast<uint2*>(out + (side * kQuantTile + line) * kCodesPitch + blk * (B / 2));
+            encode<F32, MX, SR, B>(w, b, group + blk * (B / 8), side, key, codes);
+            uint2* p = reinterpret_cast<uint2*>(place + blk * (B / 2));
 #pragma unroll
             for (int j = 0; j < B / 16; ++j) p[j] = make_uint2(codes[2 * j], codes[2 * j + 1]);
-            sc[side][(blk >> 2) * kFp4TileBytes + (line & 31) * 16 + (line >> 5) * 4 + (blk & 3)] =
-                static_cast<unsigned char>(i < n_major && j0 < n_minor ? b.byte : 0);
+            scale[(blk >> 2) * kFp4TileBytes + (blk & 3)] =
+                static_cast<unsigned char>(line < lines && blk * B < length ? b.byte : 0);
         }
     }
     __syncthreads();
@@ -493,15 +511,16 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
     for (int side = 0; side < 2; ++side) {
         const QuantSide& q = side ? a.col : a.row;
         if (!q.codes) continue;
-        const int64_t major = side ? c0 : r0, minor = side ? r0 : c0, n_major = side ? a.cols : a.rows;
+        const int lines = side ? cols : rows, first = tid >> 3, part = tid & 7;
+        const int64_t at = ((side ? r0 : c0) >> 1) + part * 8;
+        unsigned char* p = q.codes + ((side ? c0 : r0) + first) * q.pitch + at;
+        if (at < q.pitch)
 #pragma unroll
-        for (int k = 0; k < kQuantTile * 8 / kQuantThreads; ++k) {             // 8 bytes: 16 codes of a row
-            const int id = k * kQuantThreads + tid, line = id >> 3, part = id & 7;
-            const int64_t at = (minor >> 1) + part * 8;
-            if (major + line < n_major && at < q.pitch)
-                *reinterpret_cast<uint2*>(q.codes + (major + line) * q.pitch + at) =
-                    *reinterpret_cast<const uint2*>(out + (side * kQuantTile + line) * kCodesPitch + part * 8);
-        }
+            for (int k = 0; k < kQuantTile; k += kQuantThreads / 8) {          // 8 bytes: 16 codes of a row
+                if (first + k < lines)
+                    *reinterpret_cast<uint2*>(p + k * q.pitch) =
+                        *reinterpret_cast<const uint2*>(out + (side * kQuantTile + first + k) * kCodesPitch + part * 8);
+            }
         const int64_t i = side ? tj : ti, j0 = (side ? ti : tj) * kTiles;
         if (tid < kTiles * 32 && j0 + tid / 32 < q.tiles)
             *reinterpret_cast<uint4*>(q.scales + (i * q.tiles + j0) * kFp4TileBytes + tid * 16) =
@@ -586,36 +605,33 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
     const float s1 = b1 == b0 ? s0 : scale_value<MX>(__ldg(sp + int64_t(b1 >> 2) * kFp4TileBytes + (b1 & 3)), unit);
     const int change = (b1 << kShift) - e0;                   // first element of the second block
     const bool whole = e0 >= 0 && e0 + kPiece <= cols;
-    // Products in bf16 are exact (2 and 4 bits) unless a scale or a result is below its normal numbers.
-    const bool normal = !F32 && !(s0 != 0.0f && s0 < 7.5e-37f) && !(s1 != 0.0f && s1 < 7.5e-37f);
-    const __nv_bfloat162 t0 = __float2bfloat162_rn(s0), t1 = __float2bfloat162_rn(s1),
-                         both = __halves2bfloat162(t0.x, t1.x);
+    // One scale and bf16: products in bf16 are exact (2 and 4 bits) unless the scale or a result is
+    // below its normal numbers.
+    if (!F32 && whole && b0 == b1 && !(s0 != 0.0f && s0 < 7.5e-37f)) {
+        const __nv_bfloat162 s = __float2bfloat162_rn(s0);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t h[4];
+            widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h[j]), s);
+                h[j] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            st_u4(row + (int64_t(e0) + 8 * g) * 2, make_uint4(h[0], h[1], h[2], h[3]));
+        }
+        return;
+    }
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         uint32_t h[4];
         widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), h);
         float v[8];
-        if (F32 || !normal) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                widen2(h[j], v[2 * j], v[2 * j + 1]);
-                v[2 * j] *= 8 * g + 2 * j < change ? s0 : s1;
-                v[2 * j + 1] *= 8 * g + 2 * j + 1 < change ? s0 : s1;
-            }
-        }
-        if (!F32) {
-            if (normal) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int e = 8 * g + 2 * j;
-                    const __nv_bfloat162 p =
-                        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h[j]), e + 1 < change ? t0 : e < change ? both : t1);
-                    h[j] = *reinterpret_cast<const uint32_t*>(&p);
-                }
-            } else {
-                const uint4 n = narrow8(v);
-                h[0] = n.x, h[1] = n.y, h[2] = n.z, h[3] = n.w;
-            }
+        for (int j = 0; j < 4; ++j) {
+            widen2(h[j], v[2 * j], v[2 * j + 1]);
+            v[2 * j] *= 8 * g + 2 * j < change ? s0 : s1;
+            v[2 * j + 1] *= 8 * g + 2 * j + 1 < change ? s0 : s1;
         }
         if (whole) {
             if (F32) {
@@ -624,7 +640,7 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
                 for (int j = 0; j < 8; ++j) f.v[j] = v[j];
                 st_f8(reinterpret_cast<float*>(row) + e0 + 8 * g, f);
             } else {
-                st_u4(row + (int64_t(e0) + 8 * g) * 2, make_uint4(h[0], h[1], h[2], h[3]));
+                st_u4(row + (int64_t(e0) + 8 * g) * 2, narrow8(v));
             }
         } else {
 #pragma unroll
@@ -632,7 +648,7 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
                 const int e = e0 + 8 * g + j;
                 if (e < 0 || e >= cols) continue;
                 if (F32) reinterpret_cast<float*>(row)[e] = v[j];
-                else reinterpret_cast<uint16_t*>(row)[e] = uint16_t(h[j >> 1] >> (16 * (j & 1)));
+                else reinterpret_cast<__nv_bfloat16*>(row)[e] = __float2bfloat16_rn(v[j]);
             }
         }
     }
