@@ -31,7 +31,6 @@
 
 namespace dpg {
 
-constexpr int kQuantThreads = 512;
 constexpr int kQuantTile = 128;         // rows and columns of a CTA's tile
 
 struct QuantSide {
@@ -78,6 +77,16 @@ __device__ __forceinline__ uint32_t magnitude_bits4(uint4 v) {
     return max(max(magnitude_bits<F32>(v.x), magnitude_bits<F32>(v.y)),
                max(magnitude_bits<F32>(v.z), magnitude_bits<F32>(v.w)));
 }
+// the same with NaNs and infinities among them; bf16: of the two halves each
+template <bool F32>
+__device__ __forceinline__ uint32_t any_magnitude(uint32_t m, uint4 v) {
+    if constexpr (F32) {
+        return max(max(max(m, v.x & 0x7FFFFFFFu), max(v.y & 0x7FFFFFFFu, v.z & 0x7FFFFFFFu)), v.w & 0x7FFFFFFFu);
+    } else {
+        m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+        return __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+    }
+}
 // largest over 32 W threads, in all of them
 template <int W>
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* sh) {
@@ -108,7 +117,12 @@ __global__ void __launch_bounds__(kAmaxThreads) k_fp4_amax(const void* x, int64_
             for (int u = 0; u < kFly; ++u)
                 v[u] = i + u * step < vecs ? *reinterpret_cast<const uint4*>(p + (i + u * step) * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) m = max(m, magnitude_bits4<F32>(v[u]));
+            for (int u = 0; u < kFly; ++u) m = any_magnitude<F32>(m, v[u]);
+        }
+        if (!F32) m = max(m << 16, m) & 0xFFFF0000u;
+        if (m >= 0x7F800000u) {                      // not all are finite: the largest of those that are
+            m = 0;
+            for (int64_t i = t; i < vecs; i += step) m = max(m, magnitude_bits4<F32>(*reinterpret_cast<const uint4*>(p + i * 16)));
         }
         if (t < head + n - tail) {
             const int64_t j = t < head ? t : tail + t - head;
@@ -183,9 +197,8 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top, float unit, floa
         else if (k < 0x7E && 6.0f * e4m3_value(k) < u) ++k;
     } else {
         // u has 8 bits: u / 6 is on a value, or 2^-9 of itself from it
-        const float r = __uint_as_float(__float_as_uint(q) - (q > 0.0f ? 16u : 0u));
-        k = q < 0.015625f ? int(ceilf(r * 512.0f)) : int((__float_as_uint(r) + 0xFFFFFu) >> 20) - 960;
-        k = k > 0x7E ? 0x7E : k;
+        k = int((__float_as_uint(q) + (0xFFFFFu - 16u)) >> 20) - 960;
+        if (q < 0.0156f) k = int(ceilf(__uint_as_float(__float_as_uint(q) - (q > 1e-30f ? 16u : 0u)) * 512.0f));
     }
     k = k == 0 && top != 0 ? 1 : k;                     // (u may have been too small for fp32)
     b.s = e4m3_value(k) * whole;
@@ -302,18 +315,21 @@ __device__ __forceinline__ uint32_t block_top(const uint32_t* w) {
 // the tile are 16 bytes longer than a multiple of 128, so that neighbouring rows'
 // pieces lie in different banks.
 // ---------------------------------------------------------------------------
-template <bool F32>
+template <bool F32, bool SR>
 struct TileOf {
     static constexpr int kPitch = F32 ? 132 : 68;          // words of a row in shared memory
     static constexpr int kBytes = kQuantTile * kPitch * 4;
     static constexpr int kPieces = F32 ? 32 : 16;          // 16-byte pieces of a row
     static constexpr int kPer = F32 ? 4 : 8;               // elements of a piece
-    static constexpr int kLoads = kQuantTile * kPieces / kQuantThreads;
+    // two CTAs of fp32 tiles fit an SM, four of bf16 ones (16384 x 4096 both sides 114 -> 92 us);
+    // random bits take long enough for few tiles to want the threads
+    static constexpr int kThreads = F32 || SR ? 512 : 256;
+    static constexpr int kLoads = kQuantTile * kPieces / kThreads;
 };
 constexpr int kCodesPitch = 72;                            // bytes of a row's codes in shared memory
 
 template <bool F32>
-constexpr int quant_smem() { return TileOf<F32>::kBytes + 2 * kQuantTile * kCodesPitch; }
+constexpr int quant_smem() { return TileOf<F32, false>::kBytes + 2 * kQuantTile * kCodesPitch; }
 
 // `bytes` (0 .. 16) of a 16-byte piece, zeros behind them
 __device__ __forceinline__ void copy_piece(uint32_t dst, const void* src, int bytes) {
@@ -325,7 +341,7 @@ __device__ __forceinline__ void copy_piece(uint32_t dst, const void* src, int by
 // loaded (if both lie in the matrix) and shifted into place.
 template <bool F32>
 __device__ __forceinline__ uint4 load_piece(const QuantArgs& a, int64_t at, int n, int64_t end) {
-    constexpr int kSize = F32 ? 4 : 2, kPer = TileOf<F32>::kPer;
+    constexpr int kSize = F32 ? 4 : 2, kPer = TileOf<F32, false>::kPer;
     const unsigned char* p = static_cast<const unsigned char*>(a.x) + at * kSize;
     uint32_t w[4];
     if (n >= kPer && at >= kPer && at + 2 * kPer <= end) {
@@ -356,10 +372,10 @@ __device__ __forceinline__ uint4 load_piece(const QuantArgs& a, int64_t at, int 
 }
 
 // rows, cols: of the tile that the matrix has
-template <bool F32>
+template <bool F32, bool SR>
 __device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t r0, int64_t c0, int rows, int cols, uint32_t* tile) {
-    using T = TileOf<F32>;
-    constexpr int kSize = F32 ? 4 : 2, kStep = kQuantThreads / T::kPieces;     // rows from one load to the next
+    using T = TileOf<F32, SR>;
+    constexpr int kSize = F32 ? 4 : 2, kStep = T::kThreads / T::kPieces;     // rows from one load to the next
     const int row0 = int(threadIdx.x) / T::kPieces, piece = int(threadIdx.x) % T::kPieces;
     const int n = cols - piece * T::kPer;                                      // elements from the piece's first on
     int64_t at = (r0 + row0) * a.stride + c0 + piece * T::kPer;
@@ -397,11 +413,11 @@ __device__ __forceinline__ uint32_t larger(uint32_t w) {
 }
 
 template <bool F32, bool MX, bool SR>
-__global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
-    using T = TileOf<F32>;
+__global__ void __launch_bounds__(TileOf<F32, SR>::kThreads, F32 || SR ? 2 : 4) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
+    using T = TileOf<F32, SR>;
     constexpr int B = MX ? 32 : 16;                        // elements of a block
     constexpr int kBlocks = kQuantTile / B;                // blocks of a tile's row
-    constexpr int kTasks = kQuantTile * kBlocks / kQuantThreads;
+    constexpr int kTasks = kQuantTile * kBlocks / T::kThreads;
     constexpr int kWords = B * (F32 ? 4 : 2) / 4;          // 32-bit words of a block
     constexpr int kTiles = kBlocks / 4;                    // scale tiles of a tile
     extern __shared__ __align__(16) uint32_t tile[];
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
     const int rows = int(min(a.rows - r0, int64_t(kQuantTile))), cols = int(min(a.cols - c0, int64_t(kQuantTile)));
     // After k_fp4_amax, which has itself waited for what came before it, x may be read at once.
     if (!a.parts) pdl_enter();
-    load_tile<F32>(a, r0, c0, rows, cols, tile);
+    load_tile<F32, SR>(a, r0, c0, rows, cols, tile);
     if (a.parts) pdl_enter();
     uint2 key = make_uint2(0, 0);
     if (SR) {                                              // (the same in the warp: its schedule stays in uniform registers)
@@ -425,7 +441,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
     bool tiny = false;
     __shared__ float inverses[MX ? 1 : kInverses];
     if (!MX) {
-        __shared__ uint32_t sh[kQuantThreads / 32];
+        __shared__ uint32_t sh[T::kThreads / 32];
         uint32_t m = 0;
         if (tid < kInverses) inverses[tid] = tid == 0 || tid == 0x7F ? 0.0f : 1.0f / e4m3_value(tid);   // (block_max waits)
         if (a.parts) {
@@ -434,12 +450,12 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
             asm volatile("cp.async.wait_all;" ::: "memory");       // (this thread's own pieces)
 #pragma unroll
             for (int k = 0; k < T::kLoads; ++k) {
-                const int id = k * kQuantThreads + tid;
+                const int id = k * T::kThreads + tid;
                 m = max(m, magnitude_bits4<F32>(
                                *reinterpret_cast<const uint4*>(tile + id / T::kPieces * T::kPitch + id % T::kPieces * 4)));
             }
         }
-        m = block_max<kQuantThreads / 32>(m, sh);
+        m = block_max<T::kThreads / 32>(m, sh);
         if (!a.parts && gridDim.x > 1) {
             __shared__ uint32_t mine;
             if (tid == 0) mine = m;
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
         const uint64_t group = SR ? uint64_t((side ? c0 : r0) + line) * q.vectors + uint64_t((side ? r0 : c0) >> 3) : 0;
 #pragma unroll 1
         for (int k = 0; k < kTasks; ++k) {
-            const int blk = k * (kQuantThreads / kQuantTile) + tid / kQuantTile;
+            const int blk = k * (T::kThreads / kQuantTile) + tid / kQuantTile;
             uint32_t w[kWords];
             if (side == 0) {
                 const uint4* p = reinterpret_cast<const uint4*>(tile + line * T::kPitch + blk * kWords);
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_fp4_quantize(const __grid_
         unsigned char* p = q.codes + ((side ? c0 : r0) + first) * q.pitch + at;
         if (at < q.pitch)
 #pragma unroll
-            for (int k = 0; k < kQuantTile; k += kQuantThreads / 8) {          // 8 bytes: 16 codes of a row
+            for (int k = 0; k < kQuantTile; k += T::kThreads / 8) {          // 8 bytes: 16 codes of a row
                 if (first + k < lines)
                     *reinterpret_cast<uint2*>(p + k * q.pitch) =
                         *reinterpret_cast<const uint2*>(out + (side * kQuantTile + first + k) * kCodesPitch + part * 8);
@@ -745,7 +761,7 @@ static int launch_quant(const QuantArgs& a, int64_t tiles, cudaStream_t s, const
     if (st != DPG_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(tiles));
-    cfg.blockDim = dim3(kQuantThreads);
+    cfg.blockDim = dim3(TileOf<F32, SR>::kThreads);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -25,7 +26,8 @@
 namespace dpg {
 
 constexpr int64_t kNormMaxSide = int64_t(1) << 30;
-constexpr int kNormParts = 304;      // most CTAs of a backward pass: two per SM
+constexpr int kNormParts = 304;      // CTAs of a backward pass, at most: two per SM, of 128
+                                     // or 256 threads (768 to 2048 columns) twice as many
 
 struct NormArgs {
     const void* x;
@@ -106,6 +108,37 @@ __device__ __forceinline__ NormRaw<F32> load_group(const void* p, int64_t row_at
     return r;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t twice(float x) { return pair_of(x, x); }
+__device__ __forceinline__ float sum_of(uint64_t p) {
+    const float2 f = halves_of(p);
+    return f.x + f.y;
+}
+__device__ __forceinline__ void unpair(const uint64_t* p, float* f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 t = halves_of(p[j]);
+        f[2 * j] = t.x;
+        f[2 * j + 1] = t.y;
+    }
+}
+// s / n, rounded to nearest: a product with inv = 1 / n and one residual (Markstein 1990)
+__device__ __forceinline__ float over(float s, float n, float inv) {
+    const float q = s * inv;
+    const float r = fmaf(fmaf(-q, n, s), inv, q);
+    return fabsf(q) < 3.4e38f ? r : q;            // (not of an infinity)
+}
+// 1 / sqrt(v) within an ulp: the approximation and one of Newton's steps
+__device__ __forceinline__ float inverse_root(float v) {
+    const float r = rsqrtf(v);
+    const float e = fmaf(-v * r, r, 1.0f);
+    return r > 0.0f && r < 3.4e38f ? fmaf(0.5f * r, e, r) : r;
+}
+
 template <bool F32>
 __device__ __forceinline__ void widen_group(const NormRaw<F32>& r, float* f) {
     if (F32) {
@@ -114,6 +147,29 @@ __device__ __forceinline__ void widen_group(const NormRaw<F32>& r, float* f) {
         f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
     } else {
         widen8(r.q[0], f);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void widen_pairs(const NormRaw<F32>& r, uint64_t* p) {
+    float f[8];
+    widen_group<F32>(r, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = pair_of(f[2 * j], f[2 * j + 1]);
+}
+
+// Zeroes what lies behind the last column: the whole group, or single elements.
+template <bool VEC, int T>
+__device__ __forceinline__ void mask_group(int cols, int lane, int v, uint64_t* p) {
+    if (VEC) {
+        if (column_of<true, T>(lane, v, 0) >= cols) p[0] = p[1] = p[2] = p[3] = 0;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = halves_of(p[j]);
+            p[j] = pair_of(column_of<false, T>(lane, v, 2 * j) < cols ? t.x : 0.0f,
+                           column_of<false, T>(lane, v, 2 * j + 1) < cols ? t.y : 0.0f);
+        }
     }
 }
 
@@ -140,11 +196,38 @@ __device__ __forceinline__ void store_group(void* p, int64_t row_at, int cols, i
     }
 }
 
-// group v of a gain or bias
+// group v of a gain or bias, which stays in L1 from row to row
 template <bool VEC, int T>
 __device__ __forceinline__ void load_params(const void* p, int32_t f32, int cols, int lane, int v, float* f) {
-    if (f32) widen_group<true>(load_group<true, VEC, T>(p, 0, cols, lane, v), f);
-    else widen_group<false>(load_group<false, VEC, T>(p, 0, cols, lane, v), f);
+    if (VEC) {
+        const int c = column_of<true, T>(lane, v, 0);
+        if (c >= cols) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+        } else if (f32) {
+            const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+            const float4 a = __ldg(at), b = __ldg(at + 1);
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+            widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c)), f);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = column_of<false, T>(lane, v, j);
+            f[j] = c >= cols ? 0.0f
+                   : f32     ? __ldg(static_cast<const float*>(p) + c)
+                             : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + c)) << 16);
+        }
+    }
+}
+
+template <bool VEC, int T>
+__device__ __forceinline__ void load_param_pairs(const void* p, int32_t f32, int cols, int lane, int v, uint64_t* out) {
+    float f[8];
+    load_params<VEC, T>(p, f32, cols, lane, v, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = pair_of(f[2 * j], f[2 * j + 1]);
 }
 
 // sums of a and b over the T threads of a row, the same in all of them; `sh`
@@ -175,51 +258,68 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2* sh) {
 template <int T>
 constexpr int norm_threads() { return T == 32 ? 256 : T; }
 
+// CTAs to an SM: as many as leave the row's registers, and 1024 threads at least
+template <int T, int V>
+constexpr int norm_ctas() { return T == 32 ? (V == 1 ? 4 : 3) : T == 128 ? 8 : T == 256 ? 4 : T == 512 ? 2 : 1; }
+
+// Warps (T = 32) or CTAs stay and take row after row; the next is on its way while
+// one is worked on.  (A CTA to every row or eight spent half its time on its start
+// and on loads of the parameters behind the statistics.)
 template <bool F32, bool VEC, int T, int V>
-__global__ void __launch_bounds__(norm_threads<T>()) k_layer_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_norm(const __grid_constant__ NormArgs a) {
     __shared__ float2 sh[2][32];
     pdl_enter();
     const int lane = int(threadIdx.x) % T;
-    const int64_t r = int64_t(blockIdx.x) * (norm_threads<T>() / T) + int(threadIdx.x) / T;
-    if (r >= a.rows) return;                       // a whole warp or CTA
-    const int64_t at = r * a.cols;
+    const int64_t first = int64_t(blockIdx.x) * (norm_threads<T>() / T) + int(threadIdx.x) / T;
+    const int64_t step = int64_t(gridDim.x) * (norm_threads<T>() / T);
     NormRaw<F32> raw[V];
+    if (first < a.rows) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, at, a.cols, lane, v);
-    float x[V][8], s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        widen_group<F32>(raw[v], x[v]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += x[v][j];
+        for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, first * a.cols, a.cols, lane, v);
     }
-    const float n = float(a.cols);
-    const float mean = row_sum<T>(s, 0.0f, sh[0]).x / n;
-    s = 0.0f;
+    const float n = float(a.cols), inv = 1.0f / n;
+    for (int64_t r = first; r < a.rows; r += step) {
+        uint64_t x[V][4], s = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            widen_pairs<F32>(raw[v], x[v]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[v][j] = column_of<VEC, T>(lane, v, j) < a.cols ? x[v][j] - mean : 0.0f;
-            s = fmaf(x[v][j], x[v][j], s);
+            for (int j = 0; j < 4; ++j) s = add2(s, x[v][j]);
         }
-    const float rstd = 1.0f / sqrtf(row_sum<T>(s, 0.0f, sh[1]).x / n + a.eps);
-    if (lane == 0 && a.mean) {
-        a.mean[r] = mean;
-        a.rstd[r] = rstd;
-    }
+        if (r + step < a.rows) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float g[8], b[8];
-        if (a.gain) load_params<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
-        if (a.bias) load_params<VEC, T>(a.bias, a.params_f32, a.cols, lane, v, b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[v][j] *= rstd;
-            if (a.gain) x[v][j] *= g[j];
-            if (a.bias) x[v][j] += b[j];
+            for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, (r + step) * a.cols, a.cols, lane, v);
         }
-        store_group<F32, VEC, T>(a.y, at, a.cols, lane, v, x[v]);
+        const float mean = over(row_sum<T>(sum_of(s), 0.0f, sh[0]).x, n, inv);
+        s = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[v][j] = add2(x[v][j], twice(-mean));
+            mask_group<VEC, T>(a.cols, lane, v, x[v]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s = fma2(x[v][j], x[v][j], s);
+        }
+        const float rstd = inverse_root(over(row_sum<T>(sum_of(s), 0.0f, sh[1]).x, n, inv) + a.eps);
+        if (lane == 0 && a.mean) {
+            a.mean[r] = mean;
+            a.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            uint64_t g[4], b[4] = {0, 0, 0, 0};
+            if (a.bias) load_param_pairs<VEC, T>(a.bias, a.params_f32, a.cols, lane, v, b);
+            if (a.gain) load_param_pairs<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[v][j] = mul2(x[v][j], twice(rstd));
+                if (a.gain) x[v][j] = fma2(x[v][j], g[j], b[j]);
+                else if (a.bias) x[v][j] = add2(x[v][j], b[j]);
+            }
+            float y[8];
+            unpair(x[v], y);
+            store_group<F32, VEC, T>(a.y, r * a.cols, a.cols, lane, v, y);
+        }
     }
 }
 
@@ -261,98 +361,192 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_c
 
 // ---------------------------------------------------------------------------
 // Backward.  CTA p takes rows p, p + parts, ... (T = 32: its eight warps take
-// eight rows at a time); the next row is on its way while one is worked on.
+// eight rows at a time).  A thread's groups of x and dy come through shared memory,
+// three rows ahead (asynchronous copies, which only the thread itself waits for):
+// a second set of registers for the next row left one CTA to an SM.
 // ---------------------------------------------------------------------------
+// rows ahead: 128 KB to a row of 16384 fp32 columns leave one
+template <bool F32, int T, int V>
+constexpr int rows_ahead() { return F32 && T * V == 2048 ? 1 : 3; }
+
+template <bool F32, int T, int V>
+constexpr int back_smem() { return rows_ahead<F32, T, V>() * norm_threads<T>() * V * 2 * (F32 ? 32 : 16); }
+
 template <bool F32, bool VEC, int T, int V>
-__global__ void __launch_bounds__(norm_threads<T>()) k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
+struct BackRows {
+    uint4* own;                                    // this thread's first piece in shared memory
+    NormRaw<F32> direct[VEC ? 1 : 2 * V];          // odd widths and unaligned rows: loaded as they are needed
+    static constexpr int kPieces = F32 ? 2 : 1, kThreads = norm_threads<T>(), kAhead = rows_ahead<F32, T, V>();
+
+    // piece k of group v of x (0) or dy (1) in slot s; neighbouring threads' pieces are neighbours
+    __device__ __forceinline__ uint4* piece(int s, int which, int v, int k) const {
+        return own + (((s * 2 + which) * V + v) * kPieces + k) * kThreads;
+    }
+    __device__ __forceinline__ void fetch(const NormBackArgs& a, int64_t r, int s, int lane) {
+        if (!VEC) return;
+        if (r < a.rows) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int c = column_of<true, T>(lane, v, 0);
+                    if (c >= a.cols) continue;
+                    const unsigned char* p = static_cast<const unsigned char*>(which ? a.dy : a.x) + (r * a.cols + c) * (F32 ? 4 : 2);
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                     :: "r"(uint32_t(__cvta_generic_to_shared(piece(s, which, v, k)))), "l"(p + 16 * k) : "memory");
+                }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void arrive(const NormBackArgs& a, int64_t r, int lane) {
+        if (VEC) {
+            asm volatile("cp.async.wait_group %0;" :: "n"(kAhead - 1) : "memory");
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                direct[2 * v] = load_group<F32, false, T>(a.x, r * a.cols, a.cols, lane, v);
+                direct[2 * v + 1] = load_group<F32, false, T>(a.dy, r * a.cols, a.cols, lane, v);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const NormBackArgs& a, int s, int which, int lane, int v, uint64_t* f) const {
+        NormRaw<F32> raw;
+        if (VEC) {
+            const bool in = column_of<true, T>(lane, v, 0) < a.cols;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) raw.q[k] = in ? *piece(s, which, v, k) : make_uint4(0, 0, 0, 0);
+        } else {
+            raw = direct[VEC ? 0 : 2 * v + which];
+        }
+        widen_pairs<F32>(raw, f);
+    }
+};
+
+// group v of n = (x - mean) rstd and of dy
+template <bool F32, bool VEC, int T, int V>
+__device__ __forceinline__ void normalised(const NormBackArgs& a, const BackRows<F32, VEC, T, V>& rows, int s, int lane, int v,
+                                           float mean, float rstd, uint64_t* n, uint64_t* dy) {
+    rows.get(a, s, 0, lane, v, n);
+    rows.get(a, s, 1, lane, v, dy);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) n[j] = mul2(add2(n[j], twice(-mean)), twice(rstd));
+    mask_group<VEC, T>(a.cols, lane, v, n);
+}
+
+template <bool F32, bool VEC, int T, int V>
+__global__ void __launch_bounds__(norm_threads<T>(), T == 32 ? 2 : T <= 256 ? 4 : V == 1 ? 2 : 1)
+k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
     constexpr int kRows = norm_threads<T>() / T;   // rows of a CTA at a time
+    constexpr int kAhead = rows_ahead<F32, T, V>();
+    extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float2 sh[2][32];
-    __shared__ float sums[T == 32 ? 2 * T * V * 8 : 1];
     pdl_enter();
     const int lane = int(threadIdx.x) % T, group = int(threadIdx.x) / T;
     const int64_t first = int64_t(blockIdx.x) * kRows + group, step = int64_t(gridDim.x) * kRows;
-    float dg[V][8], db[V][8];
+    BackRows<F32, VEC, T, V> rows;
+    rows.own = reinterpret_cast<uint4*>(dyn) + threadIdx.x;
+    for (int s = 0; s < kAhead; ++s) rows.fetch(a, first + s * step, s, lane);
+    uint64_t dg[V][4], db[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dg[v][j] = db[v][j] = 0.0f;
-    NormRaw<F32> nx[V], ny[V];
-    float nmean = 0.0f, nrstd = 0.0f;
+        for (int j = 0; j < 4; ++j) dg[v][j] = db[v][j] = 0;
+    const float n = float(a.cols), inv = 1.0f / n;
+    float next_mean = 0.0f, next_rstd = 0.0f;
     if (first < a.rows) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            nx[v] = load_group<F32, VEC, T>(a.x, first * a.cols, a.cols, lane, v);
-            ny[v] = load_group<F32, VEC, T>(a.dy, first * a.cols, a.cols, lane, v);
-        }
-        nmean = __ldg(a.mean + first);
-        nrstd = __ldg(a.rstd + first);
+        next_mean = __ldg(a.mean + first);
+        next_rstd = __ldg(a.rstd + first);
     }
-    int half = 0;
+    int half = 0, s = 0;
     for (int64_t r = first; r < a.rows; r += step, half ^= 1) {
-        float x[V][8], y[V][8];
-        const float mean = nmean, rstd = nrstd;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            widen_group<F32>(nx[v], x[v]);
-            widen_group<F32>(ny[v], y[v]);
-        }
+        const float mean = next_mean, rstd = next_rstd;
         if (r + step < a.rows) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                nx[v] = load_group<F32, VEC, T>(a.x, (r + step) * a.cols, a.cols, lane, v);
-                ny[v] = load_group<F32, VEC, T>(a.dy, (r + step) * a.cols, a.cols, lane, v);
-            }
-            nmean = __ldg(a.mean + r + step);
-            nrstd = __ldg(a.rstd + r + step);
+            next_mean = __ldg(a.mean + r + step);
+            next_rstd = __ldg(a.rstd + r + step);
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        rows.arrive(a, r, lane);
+        uint64_t s1 = 0, s2 = 0;
+        // n and g of the row; up to two groups keep them, more would not fit beside the sums
+        constexpr bool kKeep = V <= 2;
+        uint64_t x[kKeep ? V : 1][4], y[kKeep ? V : 1][4];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float g[8];
-            if (a.gain) load_params<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
+            uint64_t *xv = x[kKeep ? v : 0], *yv = y[kKeep ? v : 0];
+            normalised(a, rows, s, lane, v, mean, rstd, xv, yv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[v][j] = column_of<VEC, T>(lane, v, j) < a.cols ? (x[v][j] - mean) * rstd : 0.0f;
-                dg[v][j] = fmaf(y[v][j], x[v][j], dg[v][j]);
-                db[v][j] += y[v][j];
-                if (a.gain) y[v][j] *= g[j];
-                s1 += y[v][j];
-                s2 = fmaf(y[v][j], x[v][j], s2);
+            for (int j = 0; j < 4; ++j) {
+                dg[v][j] = fma2(yv[j], xv[j], dg[v][j]);
+                db[v][j] = add2(db[v][j], yv[j]);
+            }
+            if (a.gain) {
+                uint64_t g[4];
+                load_param_pairs<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) yv[j] = mul2(yv[j], g[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s1 = add2(s1, yv[j]);
+                s2 = fma2(yv[j], xv[j], s2);
             }
         }
         if (a.dx) {
-            const float2 t = row_sum<T>(s1, s2, sh[half]);
-            const float c1 = t.x / float(a.cols), c2 = t.y / float(a.cols);
+            const float2 t = row_sum<T>(sum_of(s1), sum_of(s2), sh[half]);
+            const uint64_t c1 = twice(-over(t.x, n, inv)), c2 = twice(-over(t.y, n, inv));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                uint64_t *xv = x[kKeep ? v : 0], *yv = y[kKeep ? v : 0];
+                if (!kKeep) {
+                    normalised(a, rows, s, lane, v, mean, rstd, xv, yv);
+                    if (a.gain) {
+                        uint64_t g[4];
+                        load_param_pairs<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[v][j] = rstd * (y[v][j] - c1 - x[v][j] * c2);
-                store_group<F32, VEC, T>(a.dx, r * a.cols, a.cols, lane, v, y[v]);
+                        for (int j = 0; j < 4; ++j) yv[j] = mul2(yv[j], g[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) yv[j] = mul2(fma2(xv[j], c2, add2(yv[j], c1)), twice(rstd));
+                float out[8];
+                unpair(yv, out);
+                store_group<F32, VEC, T>(a.dx, r * a.cols, a.cols, lane, v, out);
             }
         }
+        rows.fetch(a, r + kAhead * step, s, lane);
+        s = s + 1 == kAhead ? 0 : s + 1;
     }
     if (!a.part) return;
+    float dgf[V][8], dbf[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        unpair(dg[v], dgf[v]);
+        unpair(db[v], dbf[v]);
+    }
     float* out = a.part + int64_t(blockIdx.x) * 2 * a.cols;
     if (T == 32) {                                 // the warps' sums, in order
-        for (int w = 0; w < kRows; ++w) {
-            if (group == w) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        constexpr int kSums = T * V * 8;
+        float* sums = reinterpret_cast<float*>(dyn);
+        static_assert(back_smem<F32, T, V>() >= 2 * kRows * kSums * 4, "room for the warps' sums");
+        {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float* p = sums + (v * 8 + j) * 32 + lane;
-                        float* q = p + T * V * 8;
-                        *p = w == 0 ? dg[v][j] : *p + dg[v][j];
-                        *q = w == 0 ? db[v][j] : *q + db[v][j];
-                    }
-            }
+                for (int j = 0; j < 8; ++j) {
+                    sums[(group * 2) * kSums + (v * 8 + j) * 32 + lane] = dgf[v][j];
+                    sums[(group * 2 + 1) * kSums + (v * 8 + j) * 32 + lane] = dbf[v][j];
+                }
             __syncthreads();
-        }
-        for (int k = int(threadIdx.x); k < T * V * 8; k += norm_threads<T>()) {
-            const int c = column_of<VEC, T>(k & 31, k >> 8, (k >> 5) & 7);
-            if (c < a.cols) {
-                out[c] = sums[k];
-                out[a.cols + c] = sums[T * V * 8 + k];
+            for (int k = int(threadIdx.x); k < 2 * kSums; k += norm_threads<T>()) {
+                const int at = k % kSums, c = column_of<VEC, T>(at & 31, at >> 8, (at >> 5) & 7);
+                if (c >= a.cols) continue;
+                float t = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kRows; ++w) t += sums[w * 2 * kSums + k];
+                out[(k / kSums) * int64_t(a.cols) + c] = t;
             }
         }
     } else {
@@ -362,8 +556,8 @@ __global__ void __launch_bounds__(norm_threads<T>()) k_layer_norm_back(const __g
             for (int j = 0; j < 8; ++j) {
                 const int c = column_of<VEC, T>(lane, v, j);
                 if (c < a.cols) {
-                    out[c] = dg[v][j];
-                    out[a.cols + c] = db[v][j];
+                    out[c] = dgf[v][j];
+                    out[a.cols + c] = dbf[v][j];
                 }
             }
     }
@@ -461,8 +655,9 @@ static int norm_pointer(const void* p, int32_t dtype, bool may_be_null, const ch
 
 // CTAs of a backward pass, which leave as many parts: one for 1, 8, ... rows
 static int norm_parts(int64_t rows, int64_t cols) {
-    const int64_t groups = cols <= 1024 ? (rows + 7) / 8 : rows;
-    return int(groups < 1 ? 1 : groups < kNormParts ? groups : kNormParts);
+    const int64_t groups = cols <= 768 ? (rows + 7) / 8 : rows;
+    const int64_t most = cols > 768 && cols <= 2048 ? 2 * kNormParts : kNormParts;
+    return int(groups < 1 ? 1 : groups < most ? groups : most);
 }
 
 template <int T, int V>
@@ -470,14 +665,24 @@ static int launch_norm(const NormArgs& a, bool f32, bool vec, cudaStream_t s, co
     constexpr int per = norm_threads<T>() / T;
     auto k = f32 ? (vec ? k_layer_norm<true, true, T, V> : k_layer_norm<true, false, T, V>)
                  : (vec ? k_layer_norm<false, true, T, V> : k_layer_norm<false, false, T, V>);
-    return launch_k(k, unsigned((a.rows + per - 1) / per), norm_threads<T>(), s, who, a);
+    int dev = 0, grid = 0;
+    DPG_CUDA_TRY(cudaGetDevice(&dev));
+    const int st = grid_for(reinterpret_cast<const void*>(k), norm_threads<T>(), dev, (a.rows + per - 1) / per, &grid);
+    return st != DPG_OK ? st : launch_k(k, unsigned(grid), norm_threads<T>(), s, who, a);
 }
 
+template <bool F32, bool VEC, int T, int V>
+static int launch_back_as(const NormBackArgs& a, cudaStream_t s, const char* who) {
+    auto k = k_layer_norm_back<F32, VEC, T, V>;
+    constexpr int smem = VEC || T == 32 ? back_smem<F32, T, V>() : 0;
+    static std::atomic<uint64_t> once{0};
+    const int st = smem > 0 ? allow_smem(reinterpret_cast<const void*>(k), smem, once, who) : DPG_OK;
+    return st != DPG_OK ? st : launch_k(k, unsigned(a.parts), norm_threads<T>(), size_t(smem), s, who, a);
+}
 template <int T, int V>
 static int launch_back(const NormBackArgs& a, bool f32, bool vec, cudaStream_t s, const char* who) {
-    auto k = f32 ? (vec ? k_layer_norm_back<true, true, T, V> : k_layer_norm_back<true, false, T, V>)
-                 : (vec ? k_layer_norm_back<false, true, T, V> : k_layer_norm_back<false, false, T, V>);
-    return launch_k(k, unsigned(a.parts), norm_threads<T>(), s, who, a);
+    if (f32) return vec ? launch_back_as<true, true, T, V>(a, s, who) : launch_back_as<true, false, T, V>(a, s, who);
+    return vec ? launch_back_as<false, true, T, V>(a, s, who) : launch_back_as<false, false, T, V>(a, s, who);
 }
 
 }  // namespace dpg
@@ -521,6 +726,7 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
                      dpg::aligned(bias, 16);
     if (cols <= 256) return dpg::launch_norm<32, 1>(a, f32, vec, s, who);
     if (cols <= 512) return dpg::launch_norm<32, 2>(a, f32, vec, s, who);
+    if (cols <= 768) return dpg::launch_norm<32, 3>(a, f32, vec, s, who);
     if (cols <= 1024) return dpg::launch_norm<32, 4>(a, f32, vec, s, who);
     if (cols <= 2048) return dpg::launch_norm<128, 2>(a, f32, vec, s, who);
     if (cols <= 4096) return dpg::launch_norm<256, 2>(a, f32, vec, s, who);
@@ -583,11 +789,11 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     if (cols <= 256) st = dpg::launch_back<32, 1>(a, f32, vec, s, who);
     else if (cols <= 512) st = dpg::launch_back<32, 2>(a, f32, vec, s, who);
     else if (cols <= 768) st = dpg::launch_back<32, 3>(a, f32, vec, s, who);
-    else if (cols <= 1024) st = dpg::launch_back<32, 4>(a, f32, vec, s, who);
+    else if (cols <= 1024) st = dpg::launch_back<128, 1>(a, f32, vec, s, who);
     else if (cols <= 2048) st = dpg::launch_back<256, 1>(a, f32, vec, s, who);
     else if (cols <= 4096) st = dpg::launch_back<512, 1>(a, f32, vec, s, who);
     else if (cols <= 8192) st = dpg::launch_back<512, 2>(a, f32, vec, s, who);
-    else if (cols <= 16384) st = dpg::launch_back<1024, 2>(a, f32, vec, s, who);
+    else if (cols <= 16384) st = dpg::launch_back<512, 4>(a, f32, vec, s, who);
     else {
         if (sums) {
             cudaLaunchConfig_t cfg = {};
