@@ -26,8 +26,7 @@
 namespace dpg {
 
 constexpr int64_t kNormMaxSide = int64_t(1) << 30;
-constexpr int kNormParts = 304;      // CTAs of a backward pass, at most: two per SM, of 128
-                                     // or 256 threads (768 to 2048 columns) twice as many
+constexpr int kNormSms = 152;        // CTAs of a backward pass go by a GB300's SMs (see norm_parts)
 
 struct NormArgs {
     const void* x;
@@ -230,29 +229,42 @@ __device__ __forceinline__ void load_param_pairs(const void* p, int32_t f32, int
     for (int j = 0; j < 4; ++j) out[j] = pair_of(f[2 * j], f[2 * j + 1]);
 }
 
-// sums of a and b over the T threads of a row, the same in all of them; `sh`
-// holds two values per warp and is free again after the next call's barrier
-// (calls alternate between two halves of it)
+// Sum over the T threads of a row, the same in all of them.  `sh` holds a value
+// per warp and is free again after the next call's barrier (calls alternate
+// between two).
 template <int T>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* sh) {
+__device__ __forceinline__ float row_sum(float a, float* sh) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    }
-    if (T == 32) return make_float2(a, b);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    if (T == 32) return a;
+    constexpr int kWarps = T / 32;
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
     __syncthreads();
-    a = b = 0.0f;
-    const float2 w = (threadIdx.x & 31) < T / 32 ? sh[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
-    a = w.x;
-    b = w.y;
+    a = sh[threadIdx.x & (kWarps - 1)];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    for (int o = kWarps / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    return a;
+}
+// The same for two sums (2 values per warp in `sh`): lanes 0 .. 15 add up a, the
+// others b, at half the exchanges.
+template <int T>
+__device__ __forceinline__ float2 row_sums(float a, float b, float* sh) {
+    const bool low = (threadIdx.x & 16) == 0;
+    float t = (low ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if (T > 32) {
+        constexpr int kWarps = T / 32, kLanes = kWarps < 16 ? kWarps : 16;
+        if ((threadIdx.x & 15) == 0) sh[(threadIdx.x >> 5) + (low ? 0 : kWarps)] = t;
+        __syncthreads();
+        const float* from = sh + (low ? 0 : kWarps);
+        t = from[threadIdx.x & (kLanes - 1)];
+        if (kWarps > 16) t += from[16 + (threadIdx.x & 15)];
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
-    return make_float2(a, b);
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, t, 16);
+    return low ? make_float2(t, other) : make_float2(other, t);
 }
 
 template <int T>
@@ -260,14 +272,14 @@ constexpr int norm_threads() { return T == 32 ? 256 : T; }
 
 // CTAs to an SM: as many as leave the row's registers, and 1024 threads at least
 template <int T, int V>
-constexpr int norm_ctas() { return T == 32 ? (V == 1 ? 4 : 3) : T == 128 ? 8 : T == 256 ? 4 : T == 512 ? 2 : 1; }
+constexpr int norm_ctas() { return T == 32 ? (V == 1 ? 4 : 3) : T == 1024 ? 1 : (V <= 2 ? 1024 : 768) / T; }
 
 // Warps (T = 32) or CTAs stay and take row after row; the next is on its way while
 // one is worked on.  (A CTA to every row or eight spent half its time on its start
 // and on loads of the parameters behind the statistics.)
 template <bool F32, bool VEC, int T, int V>
 __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_norm(const __grid_constant__ NormArgs a) {
-    __shared__ float2 sh[2][32];
+    __shared__ float sh[2][64];
     pdl_enter();
     const int lane = int(threadIdx.x) % T;
     const int64_t first = int64_t(blockIdx.x) * (norm_threads<T>() / T) + int(threadIdx.x) / T;
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_
 #pragma unroll
             for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, (r + step) * a.cols, a.cols, lane, v);
         }
-        const float mean = over(row_sum<T>(sum_of(s), 0.0f, sh[0]).x, n, inv);
+        const float mean = over(row_sum<T>(sum_of(s), sh[0]), n, inv);
         s = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -300,7 +312,7 @@ __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_
 #pragma unroll
             for (int j = 0; j < 4; ++j) s = fma2(x[v][j], x[v][j], s);
         }
-        const float rstd = inverse_root(over(row_sum<T>(sum_of(s), 0.0f, sh[1]).x, n, inv) + a.eps);
+        const float rstd = inverse_root(over(row_sum<T>(sum_of(s), sh[1]), n, inv) + a.eps);
         if (lane == 0 && a.mean) {
             a.mean[r] = mean;
             a.rstd[r] = rstd;
@@ -335,18 +347,18 @@ __device__ __forceinline__ void store_one(void* p, int32_t f32, int64_t i, float
 }
 
 __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_constant__ NormArgs a, int32_t f32) {
-    __shared__ float2 sh[2][32];
+    __shared__ float sh[2][64];
     pdl_enter();
     const int64_t at = int64_t(blockIdx.x) * a.cols;
     float s = 0.0f;
     for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) s += load_one(a.x, f32, at + c);
-    const float mean = row_sum<kLongThreads>(s, 0.0f, sh[0]).x / float(a.cols);
+    const float mean = row_sum<kLongThreads>(s, sh[0]) / float(a.cols);
     s = 0.0f;
     for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
         const float d = load_one(a.x, f32, at + c) - mean;
         s = fmaf(d, d, s);
     }
-    const float rstd = 1.0f / sqrtf(row_sum<kLongThreads>(s, 0.0f, sh[1]).x / float(a.cols) + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<kLongThreads>(s, sh[1]) / float(a.cols) + a.eps);
     if (threadIdx.x == 0 && a.mean) {
         a.mean[blockIdx.x] = mean;
         a.rstd[blockIdx.x] = rstd;
@@ -436,12 +448,12 @@ __device__ __forceinline__ void normalised(const NormBackArgs& a, const BackRows
 }
 
 template <bool F32, bool VEC, int T, int V>
-__global__ void __launch_bounds__(norm_threads<T>(), T == 32 ? 2 : T <= 256 ? 4 : V == 1 ? 2 : 1)
+__global__ void __launch_bounds__(norm_threads<T>(), T == 32 ? 2 : T <= 256 ? (V == 1 ? 4 : 3) : 1)
 k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
     constexpr int kRows = norm_threads<T>() / T;   // rows of a CTA at a time
     constexpr int kAhead = rows_ahead<F32, T, V>();
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ float2 sh[2][32];
+    __shared__ float sh[2][64];
     pdl_enter();
     const int lane = int(threadIdx.x) % T, group = int(threadIdx.x) / T;
     const int64_t first = int64_t(blockIdx.x) * kRows + group, step = int64_t(gridDim.x) * kRows;
@@ -468,8 +480,8 @@ k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
         }
         rows.arrive(a, r, lane);
         uint64_t s1 = 0, s2 = 0;
-        // n and g of the row; up to two groups keep them, more would not fit beside the sums
-        constexpr bool kKeep = V <= 2;
+        // n and g of the row; one group keeps them, more would not fit beside the sums
+        constexpr bool kKeep = V == 1;
         uint64_t x[kKeep ? V : 1][4], y[kKeep ? V : 1][4];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -493,7 +505,7 @@ k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
             }
         }
         if (a.dx) {
-            const float2 t = row_sum<T>(sum_of(s1), sum_of(s2), sh[half]);
+            const float2 t = row_sums<T>(sum_of(s1), sum_of(s2), sh[half]);
             const uint64_t c1 = twice(-over(t.x, n, inv)), c2 = twice(-over(t.y, n, inv));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(256) k_layer_norm_columns(const __grid_constan
 }
 
 __global__ void __launch_bounds__(kLongThreads) k_layer_norm_dx_long(const __grid_constant__ NormBackArgs a, int32_t f32) {
-    __shared__ float2 sh[32];
+    __shared__ float sh[64];
     pdl_enter();
     const int64_t r = blockIdx.x, at = r * a.cols;
     const float mean = __ldg(a.mean + r), rstd = __ldg(a.rstd + r);
@@ -593,7 +605,7 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_dx_long(const __gri
         s1 += g;
         s2 = fmaf(g, (load_one(a.x, f32, at + c) - mean) * rstd, s2);
     }
-    const float2 t = row_sum<kLongThreads>(s1, s2, sh);
+    const float2 t = row_sums<kLongThreads>(s1, s2, sh);
     const float c1 = t.x / float(a.cols), c2 = t.y / float(a.cols);
     for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
         float g = load_one(a.dy, f32, at + c);
@@ -656,7 +668,7 @@ static int norm_pointer(const void* p, int32_t dtype, bool may_be_null, const ch
 // CTAs of a backward pass, which leave as many parts: one for 1, 8, ... rows
 static int norm_parts(int64_t rows, int64_t cols) {
     const int64_t groups = cols <= 768 ? (rows + 7) / 8 : rows;
-    const int64_t most = cols > 768 && cols <= 2048 ? 2 * kNormParts : kNormParts;
+    const int64_t most = cols > 768 && cols <= 2048 ? 4 * kNormSms : cols > 2048 && cols <= 4096 ? 3 * kNormSms : 2 * kNormSms;
     return int(groups < 1 ? 1 : groups < most ? groups : most);
 }
 
@@ -729,9 +741,9 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
     if (cols <= 768) return dpg::launch_norm<32, 3>(a, f32, vec, s, who);
     if (cols <= 1024) return dpg::launch_norm<32, 4>(a, f32, vec, s, who);
     if (cols <= 2048) return dpg::launch_norm<128, 2>(a, f32, vec, s, who);
-    if (cols <= 4096) return dpg::launch_norm<256, 2>(a, f32, vec, s, who);
-    if (cols <= 8192) return dpg::launch_norm<512, 2>(a, f32, vec, s, who);
-    if (cols <= 16384) return dpg::launch_norm<1024, 2>(a, f32, vec, s, who);
+    if (cols <= 4096) return dpg::launch_norm<128, 4>(a, f32, vec, s, who);
+    if (cols <= 8192) return dpg::launch_norm<256, 4>(a, f32, vec, s, who);
+    if (cols <= 16384) return dpg::launch_norm<512, 4>(a, f32, vec, s, who);
     if (cols <= 32768) return dpg::launch_norm<1024, 4>(a, f32, vec, s, who);
     return dpg::launch_k(dpg::k_layer_norm_long, unsigned(rows), dpg::kLongThreads, s, who, a, int32_t(f32));
 }
@@ -791,7 +803,7 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     else if (cols <= 768) st = dpg::launch_back<32, 3>(a, f32, vec, s, who);
     else if (cols <= 1024) st = dpg::launch_back<128, 1>(a, f32, vec, s, who);
     else if (cols <= 2048) st = dpg::launch_back<256, 1>(a, f32, vec, s, who);
-    else if (cols <= 4096) st = dpg::launch_back<512, 1>(a, f32, vec, s, who);
+    else if (cols <= 4096) st = dpg::launch_back<256, 2>(a, f32, vec, s, who);
     else if (cols <= 8192) st = dpg::launch_back<512, 2>(a, f32, vec, s, who);
     else if (cols <= 16384) st = dpg::launch_back<512, 4>(a, f32, vec, s, who);
     else {
