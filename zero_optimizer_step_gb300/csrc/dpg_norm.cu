@@ -56,55 +56,27 @@ struct NormBackArgs {
 };
 
 // ---------------------------------------------------------------------------
-// A row in registers: T threads hold V groups of 8 elements each.  VEC: groups
-// are 8 neighbours, loaded 16 bytes at a time; else the T threads hold
-// neighbouring elements, loaded singly (odd widths, unaligned buffers).
+// A row in registers: T threads hold V groups of 8 elements each.
+//   kRowFull  groups are 8 neighbours, loaded 16 bytes at a time, and fill the row:
+//          no bounds to check (a third of the instructions at 4096 columns)
+//   kRowVec   the same, the last groups may lie behind the row
+//   kRowOdd   the T threads hold neighbouring elements, loaded singly (widths that
+//          are no multiple of 8, unaligned buffers)
 // ---------------------------------------------------------------------------
-template <bool VEC, int T>
+enum NormMode : int { kRowOdd = 0, kRowVec = 1, kRowFull = 2 };
+
+template <int MODE, int T>
 __device__ __forceinline__ int column_of(int lane, int v, int j) {
-    return VEC ? (lane + v * T) * 8 + j : (v * 8 + j) * T + lane;
+    return MODE == kRowOdd ? (v * 8 + j) * T + lane : (lane + v * T) * 8 + j;
 }
-
-template <bool F32>
-struct NormRaw {
-    uint4 q[F32 ? 2 : 1];
-};
-
-// group v of the row at p (NULL: zeros): columns from `cols` on are zeros
-template <bool F32, bool VEC, int T>
-__device__ __forceinline__ NormRaw<F32> load_group(const void* p, int64_t row_at, int cols, int lane, int v) {
-    NormRaw<F32> r;
-    if (VEC) {
-        const int c = column_of<true, T>(lane, v, 0);
-        if (c < cols) {
-            const unsigned char* at = static_cast<const unsigned char*>(p) + (row_at + c) * (F32 ? 4 : 2);
-            // (plain loads: the output may be the input)
-#pragma unroll
-            for (int k = 0; k < (F32 ? 2 : 1); ++k)
-                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(r.q[k].x), "=r"(r.q[k].y), "=r"(r.q[k].z), "=r"(r.q[k].w)
-                             : "l"(at + 16 * k));
-        } else {
-#pragma unroll
-            for (int k = 0; k < (F32 ? 2 : 1); ++k) r.q[k] = make_uint4(0, 0, 0, 0);
-        }
-    } else {
-        uint32_t e[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = column_of<false, T>(lane, v, j);
-            e[j] = c >= cols ? 0u
-                   : F32     ? *(static_cast<const volatile uint32_t*>(p) + row_at + c)
-                             : uint32_t(*(static_cast<const volatile uint16_t*>(p) + row_at + c));
-        }
-        if (F32) {
-            r.q[0] = make_uint4(e[0], e[1], e[2], e[3]);
-            r.q[F32 ? 1 : 0] = make_uint4(e[4], e[5], e[6], e[7]);
-        } else {
-            r.q[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-        }
-    }
-    return r;
+template <int MODE, int T>
+__device__ __forceinline__ bool group_in(int cols, int lane, int v) {
+    return MODE == kRowFull || column_of<MODE, T>(lane, v, 0) < cols;
+}
+// where a thread's columns of a row start
+template <bool F32, int MODE>
+__device__ __forceinline__ const unsigned char* start_of(const void* p, int64_t row_at, int lane) {
+    return static_cast<const unsigned char*>(p) + (row_at + (MODE == kRowOdd ? lane : lane * 8)) * (F32 ? 4 : 2);
 }
 
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -139,45 +111,81 @@ __device__ __forceinline__ float inverse_root(float v) {
 }
 
 template <bool F32>
-__device__ __forceinline__ void widen_group(const NormRaw<F32>& r, float* f) {
+struct NormRaw {
+    uint4 q[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ void widen_pairs(const NormRaw<F32>& r, uint64_t* p) {
     if (F32) {
         const uint4 a = r.q[0], b = r.q[F32 ? 1 : 0];
-        f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
-        f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+        p[0] = pair_of(__uint_as_float(a.x), __uint_as_float(a.y));
+        p[1] = pair_of(__uint_as_float(a.z), __uint_as_float(a.w));
+        p[2] = pair_of(__uint_as_float(b.x), __uint_as_float(b.y));
+        p[3] = pair_of(__uint_as_float(b.z), __uint_as_float(b.w));
     } else {
+        float f[8];
         widen8(r.q[0], f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = pair_of(f[2 * j], f[2 * j + 1]);
     }
 }
 
-template <bool F32>
-__device__ __forceinline__ void widen_pairs(const NormRaw<F32>& r, uint64_t* p) {
-    float f[8];
-    widen_group<F32>(r, f);
+// Group v of a row whose columns of this thread start at p; zeros behind the last.
+// (Plain loads: the output may be the input.)
+template <bool F32, int MODE, int T>
+__device__ __forceinline__ NormRaw<F32> load_group(const unsigned char* p, int cols, int lane, int v) {
+    NormRaw<F32> r;
+    if (MODE != kRowOdd) {
+        const unsigned char* at = p + v * T * 8 * (F32 ? 4 : 2);
+        const bool in = group_in<MODE, T>(cols, lane, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = pair_of(f[2 * j], f[2 * j + 1]);
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) {
+            r.q[k] = make_uint4(0, 0, 0, 0);
+            if (in)
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(r.q[k].x), "=r"(r.q[k].y), "=r"(r.q[k].z), "=r"(r.q[k].w)
+                             : "l"(at + 16 * k));
+        }
+    } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            e[j] = column_of<kRowOdd, T>(lane, v, j) >= cols ? 0u
+                   : F32 ? *(reinterpret_cast<const volatile uint32_t*>(p) + (v * 8 + j) * T)
+                         : uint32_t(*(reinterpret_cast<const volatile uint16_t*>(p) + (v * 8 + j) * T));
+        }
+        if (F32) {
+            r.q[0] = make_uint4(e[0], e[1], e[2], e[3]);
+            r.q[F32 ? 1 : 0] = make_uint4(e[4], e[5], e[6], e[7]);
+        } else {
+            r.q[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
+    }
+    return r;
 }
 
 // Zeroes what lies behind the last column: the whole group, or single elements.
-template <bool VEC, int T>
+template <int MODE, int T>
 __device__ __forceinline__ void mask_group(int cols, int lane, int v, uint64_t* p) {
-    if (VEC) {
-        if (column_of<true, T>(lane, v, 0) >= cols) p[0] = p[1] = p[2] = p[3] = 0;
-    } else {
+    if (MODE == kRowVec) {
+        if (!group_in<kRowVec, T>(cols, lane, v)) p[0] = p[1] = p[2] = p[3] = 0;
+    } else if (MODE == kRowOdd) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 t = halves_of(p[j]);
-            p[j] = pair_of(column_of<false, T>(lane, v, 2 * j) < cols ? t.x : 0.0f,
-                           column_of<false, T>(lane, v, 2 * j + 1) < cols ? t.y : 0.0f);
+            p[j] = pair_of(column_of<kRowOdd, T>(lane, v, 2 * j) < cols ? t.x : 0.0f,
+                           column_of<kRowOdd, T>(lane, v, 2 * j + 1) < cols ? t.y : 0.0f);
         }
     }
 }
 
-template <bool F32, bool VEC, int T>
-__device__ __forceinline__ void store_group(void* p, int64_t row_at, int cols, int lane, int v, const float* f) {
-    if (VEC) {
-        const int c = column_of<true, T>(lane, v, 0);
-        if (c >= cols) return;
-        unsigned char* at = static_cast<unsigned char*>(p) + (row_at + c) * (F32 ? 4 : 2);
+template <bool F32, int MODE, int T>
+__device__ __forceinline__ void store_group(unsigned char* p, int cols, int lane, int v, const uint64_t* pairs) {
+    float f[8];
+    unpair(pairs, f);
+    if (MODE != kRowOdd) {
+        if (!group_in<MODE, T>(cols, lane, v)) return;
+        unsigned char* at = p + v * T * 8 * (F32 ? 4 : 2);
         if (F32) {
             st_u4(at, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
             st_u4(at + 16, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
@@ -187,46 +195,35 @@ __device__ __forceinline__ void store_group(void* p, int64_t row_at, int cols, i
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = column_of<false, T>(lane, v, j);
-            if (c >= cols) continue;
-            if (F32) static_cast<float*>(p)[row_at + c] = f[j];
-            else static_cast<__nv_bfloat16*>(p)[row_at + c] = __float2bfloat16_rn(f[j]);
+            if (column_of<kRowOdd, T>(lane, v, j) >= cols) continue;
+            if (F32) reinterpret_cast<float*>(p)[(v * 8 + j) * T] = f[j];
+            else reinterpret_cast<__nv_bfloat16*>(p)[(v * 8 + j) * T] = __float2bfloat16_rn(f[j]);
         }
     }
 }
 
-// group v of a gain or bias, which stays in L1 from row to row
-template <bool VEC, int T>
-__device__ __forceinline__ void load_params(const void* p, int32_t f32, int cols, int lane, int v, float* f) {
-    if (VEC) {
-        const int c = column_of<true, T>(lane, v, 0);
-        if (c >= cols) {
+// Group v of a gain or bias of bf16 or fp32 (PF32); these stay in L1 from row to row.
+template <bool PF32, int MODE, int T>
+__device__ __forceinline__ void load_params(const void* p, int cols, int lane, int v, uint64_t* out) {
+    NormRaw<PF32> r;
+    if (MODE != kRowOdd) {
+        const bool in = group_in<MODE, T>(cols, lane, v);
+        const uint4* at = reinterpret_cast<const uint4*>(start_of<PF32, MODE>(p, 0, lane) + v * T * 8 * (PF32 ? 4 : 2));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-        } else if (f32) {
-            const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
-            const float4 a = __ldg(at), b = __ldg(at + 1);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
-            widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c)), f);
-        }
+        for (int k = 0; k < (PF32 ? 2 : 1); ++k) r.q[k] = in ? __ldg(at + k) : make_uint4(0, 0, 0, 0);
+        widen_pairs<PF32>(r, out);
     } else {
+        float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = column_of<false, T>(lane, v, j);
+            const int c = column_of<kRowOdd, T>(lane, v, j);
             f[j] = c >= cols ? 0.0f
-                   : f32     ? __ldg(static_cast<const float*>(p) + c)
+                   : PF32    ? __ldg(static_cast<const float*>(p) + c)
                              : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + c)) << 16);
         }
-    }
-}
-
-template <bool VEC, int T>
-__device__ __forceinline__ void load_param_pairs(const void* p, int32_t f32, int cols, int lane, int v, uint64_t* out) {
-    float f[8];
-    load_params<VEC, T>(p, f32, cols, lane, v, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = pair_of(f[2 * j], f[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) out[j] = pair_of(f[2 * j], f[2 * j + 1]);
+    }
 }
 
 // Sum over the T threads of a row, the same in all of them.  `sh` holds a value
@@ -270,26 +267,52 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float* sh) {
 template <int T>
 constexpr int norm_threads() { return T == 32 ? 256 : T; }
 
-// CTAs to an SM: as many as leave the row's registers, and 1024 threads at least
-template <int T, int V>
-constexpr int norm_ctas() { return T == 32 ? (V == 1 ? 4 : 3) : T == 1024 ? 1 : (V <= 2 ? 1024 : 768) / T; }
+// CTAs to an SM: as many as leave the registers of a row and of the next
+template <bool F32, int T, int V>
+constexpr int norm_ctas() {
+    return T == 32 ? (V == 1 ? 4 : F32 && V > 2 ? 2 : 3) : T == 1024 ? 1 : (V <= 2 ? 1024 : F32 ? 512 : 768) / T;
+}
+
+// y = x * rstd, times the gain, plus the bias; which of them there are, and their
+// type, is known to the instance (a branch to every group cost an instruction an
+// element)
+template <bool F32, int MODE, int T, int V, bool GAIN, bool BIAS, bool PF32>
+__device__ __forceinline__ void finish_row(const NormArgs& a, int lane, uint64_t (*x)[4], float rstd, unsigned char* y) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        uint64_t g[4], b[4] = {0, 0, 0, 0};
+        if (GAIN) load_params<PF32, MODE, T>(a.gain, a.cols, lane, v, g);
+        if (BIAS) load_params<PF32, MODE, T>(a.bias, a.cols, lane, v, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[v][j] = mul2(x[v][j], twice(rstd));
+            if (GAIN) x[v][j] = BIAS ? fma2(x[v][j], g[j], b[j]) : mul2(x[v][j], g[j]);
+            else if (BIAS) x[v][j] = add2(x[v][j], b[j]);
+        }
+        store_group<F32, MODE, T>(y, a.cols, lane, v, x[v]);
+    }
+}
 
 // Warps (T = 32) or CTAs stay and take row after row; the next is on its way while
 // one is worked on.  (A CTA to every row or eight spent half its time on its start
 // and on loads of the parameters behind the statistics.)
-template <bool F32, bool VEC, int T, int V>
-__global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_norm(const __grid_constant__ NormArgs a) {
+template <bool F32, int MODE, int T, int V>
+__global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<F32, T, V>()) k_layer_norm(const __grid_constant__ NormArgs a) {
     __shared__ float sh[2][64];
     pdl_enter();
+    constexpr int kSize = F32 ? 4 : 2;
     const int lane = int(threadIdx.x) % T;
     const int64_t first = int64_t(blockIdx.x) * (norm_threads<T>() / T) + int(threadIdx.x) / T;
-    const int64_t step = int64_t(gridDim.x) * (norm_threads<T>() / T);
+    const int64_t step = int64_t(gridDim.x) * (norm_threads<T>() / T), skip = step * a.cols * kSize;
+    const unsigned char* from = start_of<F32, MODE>(a.x, first * a.cols, lane);
+    unsigned char* to = const_cast<unsigned char*>(start_of<F32, MODE>(a.y, first * a.cols, lane));
+    const int kind = (a.gain ? 1 : 0) + (a.bias ? 2 : 0) + (a.params_f32 ? 4 : 0);
+    const float n = float(a.cols), inv = 1.0f / n;
     NormRaw<F32> raw[V];
     if (first < a.rows) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, first * a.cols, a.cols, lane, v);
+        for (int v = 0; v < V; ++v) raw[v] = load_group<F32, MODE, T>(from, a.cols, lane, v);
     }
-    const float n = float(a.cols), inv = 1.0f / n;
     for (int64_t r = first; r < a.rows; r += step) {
         uint64_t x[V][4], s = 0;
 #pragma unroll
@@ -298,9 +321,10 @@ __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_
 #pragma unroll
             for (int j = 0; j < 4; ++j) s = add2(s, x[v][j]);
         }
+        from += skip;
         if (r + step < a.rows) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) raw[v] = load_group<F32, VEC, T>(a.x, (r + step) * a.cols, a.cols, lane, v);
+            for (int v = 0; v < V; ++v) raw[v] = load_group<F32, MODE, T>(from, a.cols, lane, v);
         }
         const float mean = over(row_sum<T>(sum_of(s), sh[0]), n, inv);
         s = 0;
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_
         for (int v = 0; v < V; ++v) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[v][j] = add2(x[v][j], twice(-mean));
-            mask_group<VEC, T>(a.cols, lane, v, x[v]);
+            mask_group<MODE, T>(a.cols, lane, v, x[v]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s = fma2(x[v][j], x[v][j], s);
         }
@@ -317,21 +341,16 @@ __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<T, V>()) k_layer_
             a.mean[r] = mean;
             a.rstd[r] = rstd;
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            uint64_t g[4], b[4] = {0, 0, 0, 0};
-            if (a.bias) load_param_pairs<VEC, T>(a.bias, a.params_f32, a.cols, lane, v, b);
-            if (a.gain) load_param_pairs<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[v][j] = mul2(x[v][j], twice(rstd));
-                if (a.gain) x[v][j] = fma2(x[v][j], g[j], b[j]);
-                else if (a.bias) x[v][j] = add2(x[v][j], b[j]);
-            }
-            float y[8];
-            unpair(x[v], y);
-            store_group<F32, VEC, T>(a.y, r * a.cols, a.cols, lane, v, y);
+        switch (kind) {
+            case 1: finish_row<F32, MODE, T, V, true, false, false>(a, lane, x, rstd, to); break;
+            case 2: finish_row<F32, MODE, T, V, false, true, false>(a, lane, x, rstd, to); break;
+            case 3: finish_row<F32, MODE, T, V, true, true, false>(a, lane, x, rstd, to); break;
+            case 5: finish_row<F32, MODE, T, V, true, false, true>(a, lane, x, rstd, to); break;
+            case 6: finish_row<F32, MODE, T, V, false, true, true>(a, lane, x, rstd, to); break;
+            case 7: finish_row<F32, MODE, T, V, true, true, true>(a, lane, x, rstd, to); break;
+            default: finish_row<F32, MODE, T, V, false, false, false>(a, lane, x, rstd, to); break;
         }
+        to += skip;
     }
 }
 
@@ -384,82 +403,135 @@ constexpr int rows_ahead() { return F32 && T * V == 2048 ? 1 : 3; }
 template <bool F32, int T, int V>
 constexpr int back_smem() { return rows_ahead<F32, T, V>() * norm_threads<T>() * V * 2 * (F32 ? 32 : 16); }
 
-template <bool F32, bool VEC, int T, int V>
+template <bool F32, int MODE, int T, int V>
 struct BackRows {
     uint4* own;                                    // this thread's first piece in shared memory
-    NormRaw<F32> direct[VEC ? 1 : 2 * V];          // odd widths and unaligned rows: loaded as they are needed
+    const unsigned char *x, *dy;                   // its columns of the row to fetch next (kRowOdd: of the row at hand)
+    NormRaw<F32> direct[MODE == kRowOdd ? 2 * V : 1]; // odd widths and unaligned rows: loaded as they are needed
     static constexpr int kPieces = F32 ? 2 : 1, kThreads = norm_threads<T>(), kAhead = rows_ahead<F32, T, V>();
+    static constexpr int kSlot = 2 * V * kPieces * kThreads;
 
-    // piece k of group v of x (0) or dy (1) in slot s; neighbouring threads' pieces are neighbours
+    // piece k of group v of x (0) or dy (1) of slot s; neighbouring threads' pieces are neighbours
     __device__ __forceinline__ uint4* piece(int s, int which, int v, int k) const {
-        return own + (((s * 2 + which) * V + v) * kPieces + k) * kThreads;
+        return own + s * kSlot + ((which * V + v) * kPieces + k) * kThreads;
     }
-    __device__ __forceinline__ void fetch(const NormBackArgs& a, int64_t r, int s, int lane) {
-        if (!VEC) return;
-        if (r < a.rows) {
+    __device__ __forceinline__ void fetch(const NormBackArgs& a, bool more, int s, int lane, int64_t skip) {
+        if (MODE == kRowOdd) return;
+        if (more) {
+            const uint32_t to = uint32_t(__cvta_generic_to_shared(piece(s, 0, 0, 0)));
 #pragma unroll
             for (int which = 0; which < 2; ++which)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int c = column_of<true, T>(lane, v, 0);
-                    if (c >= a.cols) continue;
-                    const unsigned char* p = static_cast<const unsigned char*>(which ? a.dy : a.x) + (r * a.cols + c) * (F32 ? 4 : 2);
+                for (int v = 0; v < V; ++v)
+                    if (group_in<MODE, T>(a.cols, lane, v))
 #pragma unroll
-                    for (int k = 0; k < kPieces; ++k)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                     :: "r"(uint32_t(__cvta_generic_to_shared(piece(s, which, v, k)))), "l"(p + 16 * k) : "memory");
-                }
+                        for (int k = 0; k < kPieces; ++k)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                         :: "r"(to + ((which * V + v) * kPieces + k) * kThreads * 16),
+                                            "l"((which ? dy : x) + v * T * 8 * (F32 ? 4 : 2) + 16 * k) : "memory");
+            x += skip;
+            dy += skip;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    __device__ __forceinline__ void arrive(const NormBackArgs& a, int64_t r, int lane) {
-        if (VEC) {
+    __device__ __forceinline__ void arrive(const NormBackArgs& a, int lane, int64_t skip) {
+        if (MODE != kRowOdd) {
             asm volatile("cp.async.wait_group %0;" :: "n"(kAhead - 1) : "memory");
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                direct[2 * v] = load_group<F32, false, T>(a.x, r * a.cols, a.cols, lane, v);
-                direct[2 * v + 1] = load_group<F32, false, T>(a.dy, r * a.cols, a.cols, lane, v);
+                direct[2 * v] = load_group<F32, kRowOdd, T>(x, a.cols, lane, v);
+                direct[2 * v + 1] = load_group<F32, kRowOdd, T>(dy, a.cols, lane, v);
             }
+            x += skip;
+            dy += skip;
         }
     }
     __device__ __forceinline__ void get(const NormBackArgs& a, int s, int which, int lane, int v, uint64_t* f) const {
         NormRaw<F32> raw;
-        if (VEC) {
-            const bool in = column_of<true, T>(lane, v, 0) < a.cols;
+        if (MODE != kRowOdd) {
+            const bool in = group_in<MODE, T>(a.cols, lane, v);
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) raw.q[k] = in ? *piece(s, which, v, k) : make_uint4(0, 0, 0, 0);
         } else {
-            raw = direct[VEC ? 0 : 2 * v + which];
+            raw = direct[MODE == kRowOdd ? 2 * v + which : 0];
         }
         widen_pairs<F32>(raw, f);
     }
 };
 
-// group v of n = (x - mean) rstd and of dy
-template <bool F32, bool VEC, int T, int V>
-__device__ __forceinline__ void normalised(const NormBackArgs& a, const BackRows<F32, VEC, T, V>& rows, int s, int lane, int v,
-                                           float mean, float rstd, uint64_t* n, uint64_t* dy) {
-    rows.get(a, s, 0, lane, v, n);
-    rows.get(a, s, 1, lane, v, dy);
+// A row's sums: what it adds to the gradients, and (in pairs) the sums of g and g n.
+// With `keep`, x - mean and g stay in d and g.
+template <bool F32, int MODE, int T, int V, int GAIN>
+__device__ __forceinline__ void back_sums(const NormBackArgs& a, const BackRows<F32, MODE, T, V>& rows, int s, int lane,
+                                          float mean, float rstd, uint64_t (*dg)[4], uint64_t (*db)[4], uint64_t* d,
+                                          uint64_t* g, uint64_t& s1, uint64_t& s2) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) n[j] = mul2(add2(n[j], twice(-mean)), twice(rstd));
-    mask_group<VEC, T>(a.cols, lane, v, n);
+    for (int v = 0; v < V; ++v) {
+        uint64_t gain[4];
+        rows.get(a, s, 0, lane, v, d);
+        rows.get(a, s, 1, lane, v, g);
+        if (GAIN) load_params<GAIN == 2, MODE, T>(a.gain, a.cols, lane, v, gain);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = add2(d[j], twice(-mean));
+        mask_group<MODE, T>(a.cols, lane, v, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint64_t n = mul2(d[j], twice(rstd));
+            dg[v][j] = fma2(g[j], n, dg[v][j]);
+            db[v][j] = add2(db[v][j], g[j]);
+            if (GAIN) g[j] = mul2(g[j], gain[j]);
+            s1 = add2(s1, g[j]);
+            s2 = fma2(g[j], n, s2);
+        }
+    }
 }
 
-template <bool F32, bool VEC, int T, int V>
+// dx = rstd g - rstd c1 - (x - mean) rstd^2 c2; `kept`: d and g hold x - mean and g
+template <bool F32, int MODE, int T, int V, int GAIN, bool KEPT>
+__device__ __forceinline__ void back_row(const NormBackArgs& a, const BackRows<F32, MODE, T, V>& rows, int s, int lane,
+                                         float mean, float rstd, float c1, float c2, uint64_t* d, uint64_t* g,
+                                         unsigned char* dx) {
+    const uint64_t k1 = twice(-rstd * c1), k2 = twice(-rstd * rstd * c2), k = twice(rstd);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (!KEPT) {                               // (from shared memory again: registers hold the sums)
+            uint64_t gain[4];
+            rows.get(a, s, 0, lane, v, d);
+            rows.get(a, s, 1, lane, v, g);
+            if (GAIN) load_params<GAIN == 2, MODE, T>(a.gain, a.cols, lane, v, gain);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d[j] = add2(d[j], twice(-mean));
+                if (GAIN) g[j] = mul2(g[j], gain[j]);
+            }
+        }
+        uint64_t out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[j] = fma2(g[j], k, fma2(d[j], k2, k1));
+        store_group<F32, MODE, T>(dx, a.cols, lane, v, out);
+    }
+}
+
+template <bool F32, int MODE, int T, int V>
 __global__ void __launch_bounds__(norm_threads<T>(), T == 32 ? 2 : T <= 256 ? (V == 1 ? 4 : 3) : 1)
 k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
     constexpr int kRows = norm_threads<T>() / T;   // rows of a CTA at a time
-    constexpr int kAhead = rows_ahead<F32, T, V>();
+    constexpr int kAhead = rows_ahead<F32, T, V>(), kSize = F32 ? 4 : 2;
+    constexpr bool kKeep = V == 1;                 // more would not fit beside the sums
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float sh[2][64];
     pdl_enter();
     const int lane = int(threadIdx.x) % T, group = int(threadIdx.x) / T;
     const int64_t first = int64_t(blockIdx.x) * kRows + group, step = int64_t(gridDim.x) * kRows;
-    BackRows<F32, VEC, T, V> rows;
+    const int64_t skip = step * a.cols * kSize;
+    const int gain = a.gain ? a.params_f32 ? 2 : 1 : 0;
+    BackRows<F32, MODE, T, V> rows;
     rows.own = reinterpret_cast<uint4*>(dyn) + threadIdx.x;
-    for (int s = 0; s < kAhead; ++s) rows.fetch(a, first + s * step, s, lane);
+    rows.x = start_of<F32, MODE>(a.x, first * a.cols, lane);
+    rows.dy = start_of<F32, MODE>(a.dy, first * a.cols, lane);
+    unsigned char* to = const_cast<unsigned char*>(start_of<F32, MODE>(a.dx, first * a.cols, lane));
+    for (int s = 0; s < kAhead; ++s) rows.fetch(a, first + s * step < a.rows, s, lane, skip);
     uint64_t dg[V][4], db[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -478,55 +550,20 @@ k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
             next_mean = __ldg(a.mean + r + step);
             next_rstd = __ldg(a.rstd + r + step);
         }
-        rows.arrive(a, r, lane);
-        uint64_t s1 = 0, s2 = 0;
-        // n and g of the row; one group keeps them, more would not fit beside the sums
-        constexpr bool kKeep = V == 1;
-        uint64_t x[kKeep ? V : 1][4], y[kKeep ? V : 1][4];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            uint64_t *xv = x[kKeep ? v : 0], *yv = y[kKeep ? v : 0];
-            normalised(a, rows, s, lane, v, mean, rstd, xv, yv);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                dg[v][j] = fma2(yv[j], xv[j], dg[v][j]);
-                db[v][j] = add2(db[v][j], yv[j]);
-            }
-            if (a.gain) {
-                uint64_t g[4];
-                load_param_pairs<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) yv[j] = mul2(yv[j], g[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s1 = add2(s1, yv[j]);
-                s2 = fma2(yv[j], xv[j], s2);
-            }
-        }
+        rows.arrive(a, lane, skip);
+        uint64_t s1 = 0, s2 = 0, d[4], g[4];
+        if (gain == 1) back_sums<F32, MODE, T, V, 1>(a, rows, s, lane, mean, rstd, dg, db, d, g, s1, s2);
+        else if (gain == 2) back_sums<F32, MODE, T, V, 2>(a, rows, s, lane, mean, rstd, dg, db, d, g, s1, s2);
+        else back_sums<F32, MODE, T, V, 0>(a, rows, s, lane, mean, rstd, dg, db, d, g, s1, s2);
         if (a.dx) {
             const float2 t = row_sums<T>(sum_of(s1), sum_of(s2), sh[half]);
-            const uint64_t c1 = twice(-over(t.x, n, inv)), c2 = twice(-over(t.y, n, inv));
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                uint64_t *xv = x[kKeep ? v : 0], *yv = y[kKeep ? v : 0];
-                if (!kKeep) {
-                    normalised(a, rows, s, lane, v, mean, rstd, xv, yv);
-                    if (a.gain) {
-                        uint64_t g[4];
-                        load_param_pairs<VEC, T>(a.gain, a.params_f32, a.cols, lane, v, g);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) yv[j] = mul2(yv[j], g[j]);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) yv[j] = mul2(fma2(xv[j], c2, add2(yv[j], c1)), twice(rstd));
-                float out[8];
-                unpair(yv, out);
-                store_group<F32, VEC, T>(a.dx, r * a.cols, a.cols, lane, v, out);
-            }
+            const float c1 = over(t.x, n, inv), c2 = over(t.y, n, inv);
+            if (kKeep || gain == 0) back_row<F32, MODE, T, V, 0, kKeep>(a, rows, s, lane, mean, rstd, c1, c2, d, g, to);
+            else if (gain == 1) back_row<F32, MODE, T, V, 1, false>(a, rows, s, lane, mean, rstd, c1, c2, d, g, to);
+            else back_row<F32, MODE, T, V, 2, false>(a, rows, s, lane, mean, rstd, c1, c2, d, g, to);
+            to += skip;
         }
-        rows.fetch(a, r + kAhead * step, s, lane);
+        rows.fetch(a, r + kAhead * step < a.rows, s, lane, skip);
         s = s + 1 == kAhead ? 0 : s + 1;
     }
     if (!a.part) return;
@@ -538,35 +575,33 @@ k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
     }
     float* out = a.part + int64_t(blockIdx.x) * 2 * a.cols;
     if (T == 32) {                                 // the warps' sums, in order
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (MODE != kRowOdd) asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         constexpr int kSums = T * V * 8;
+        static_assert(T > 32 || back_smem<F32, T, V>() >= 2 * kRows * kSums * 4, "room for the warps' sums");
         float* sums = reinterpret_cast<float*>(dyn);
-        static_assert(back_smem<F32, T, V>() >= 2 * kRows * kSums * 4, "room for the warps' sums");
-        {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sums[(group * 2) * kSums + (v * 8 + j) * 32 + lane] = dgf[v][j];
-                    sums[(group * 2 + 1) * kSums + (v * 8 + j) * 32 + lane] = dbf[v][j];
-                }
-            __syncthreads();
-            for (int k = int(threadIdx.x); k < 2 * kSums; k += norm_threads<T>()) {
-                const int at = k % kSums, c = column_of<VEC, T>(at & 31, at >> 8, (at >> 5) & 7);
-                if (c >= a.cols) continue;
-                float t = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kRows; ++w) t += sums[w * 2 * kSums + k];
-                out[(k / kSums) * int64_t(a.cols) + c] = t;
+            for (int j = 0; j < 8; ++j) {
+                sums[(group * 2) * kSums + (v * 8 + j) * 32 + lane] = dgf[v][j];
+                sums[(group * 2 + 1) * kSums + (v * 8 + j) * 32 + lane] = dbf[v][j];
             }
+        __syncthreads();
+        for (int k = int(threadIdx.x); k < 2 * kSums; k += norm_threads<T>()) {
+            const int at = k % kSums, c = column_of<MODE, T>(at & 31, at >> 8, (at >> 5) & 7);
+            if (c >= a.cols) continue;
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kRows; ++w) t += sums[w * 2 * kSums + k];
+            out[(k / kSums) * int64_t(a.cols) + c] = t;
         }
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int c = column_of<VEC, T>(lane, v, j);
+                const int c = column_of<MODE, T>(lane, v, j);
                 if (c < a.cols) {
                     out[c] = dgf[v][j];
                     out[a.cols + c] = dbf[v][j];
@@ -672,29 +707,41 @@ static int norm_parts(int64_t rows, int64_t cols) {
     return int(groups < 1 ? 1 : groups < most ? groups : most);
 }
 
-template <int T, int V>
-static int launch_norm(const NormArgs& a, bool f32, bool vec, cudaStream_t s, const char* who) {
+template <bool F32, int MODE, int T, int V>
+static int launch_norm_as(const NormArgs& a, cudaStream_t s, const char* who) {
     constexpr int per = norm_threads<T>() / T;
-    auto k = f32 ? (vec ? k_layer_norm<true, true, T, V> : k_layer_norm<true, false, T, V>)
-                 : (vec ? k_layer_norm<false, true, T, V> : k_layer_norm<false, false, T, V>);
+    auto k = k_layer_norm<F32, MODE, T, V>;
     int dev = 0, grid = 0;
     DPG_CUDA_TRY(cudaGetDevice(&dev));
     const int st = grid_for(reinterpret_cast<const void*>(k), norm_threads<T>(), dev, (a.rows + per - 1) / per, &grid);
     return st != DPG_OK ? st : launch_k(k, unsigned(grid), norm_threads<T>(), s, who, a);
 }
+template <int T, int V>
+static int launch_norm(const NormArgs& a, bool f32, bool vec, cudaStream_t s, const char* who) {
+    const int mode = !vec ? kRowOdd : a.cols == T * V * 8 ? kRowFull : kRowVec;
+    if (f32)
+        return mode == kRowFull ? launch_norm_as<true, kRowFull, T, V>(a, s, who)
+               : mode == kRowVec ? launch_norm_as<true, kRowVec, T, V>(a, s, who) : launch_norm_as<true, kRowOdd, T, V>(a, s, who);
+    return mode == kRowFull ? launch_norm_as<false, kRowFull, T, V>(a, s, who)
+           : mode == kRowVec ? launch_norm_as<false, kRowVec, T, V>(a, s, who) : launch_norm_as<false, kRowOdd, T, V>(a, s, who);
+}
 
-template <bool F32, bool VEC, int T, int V>
+template <bool F32, int MODE, int T, int V>
 static int launch_back_as(const NormBackArgs& a, cudaStream_t s, const char* who) {
-    auto k = k_layer_norm_back<F32, VEC, T, V>;
-    constexpr int smem = VEC || T == 32 ? back_smem<F32, T, V>() : 0;
+    auto k = k_layer_norm_back<F32, MODE, T, V>;
+    constexpr int smem = MODE != kRowOdd || T == 32 ? back_smem<F32, T, V>() : 0;
     static std::atomic<uint64_t> once{0};
     const int st = smem > 0 ? allow_smem(reinterpret_cast<const void*>(k), smem, once, who) : DPG_OK;
     return st != DPG_OK ? st : launch_k(k, unsigned(a.parts), norm_threads<T>(), size_t(smem), s, who, a);
 }
 template <int T, int V>
 static int launch_back(const NormBackArgs& a, bool f32, bool vec, cudaStream_t s, const char* who) {
-    if (f32) return vec ? launch_back_as<true, true, T, V>(a, s, who) : launch_back_as<true, false, T, V>(a, s, who);
-    return vec ? launch_back_as<false, true, T, V>(a, s, who) : launch_back_as<false, false, T, V>(a, s, who);
+    const int mode = !vec ? kRowOdd : a.cols == T * V * 8 ? kRowFull : kRowVec;
+    if (f32)
+        return mode == kRowFull ? launch_back_as<true, kRowFull, T, V>(a, s, who)
+               : mode == kRowVec ? launch_back_as<true, kRowVec, T, V>(a, s, who) : launch_back_as<true, kRowOdd, T, V>(a, s, who);
+    return mode == kRowFull ? launch_back_as<false, kRowFull, T, V>(a, s, who)
+           : mode == kRowVec ? launch_back_as<false, kRowVec, T, V>(a, s, who) : launch_back_as<false, kRowOdd, T, V>(a, s, who);
 }
 
 }  // namespace dpg
