@@ -275,17 +275,32 @@ def _ptrs(xs: Sequence[Ptr]):
     return _ptr_array(max(1, len(xs)))(*map(_ptr, xs))
 
 
+_raw_stream = _get_device = None     # torch's own getters, once CUDA is initialised
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         # the handle alone: torch.cuda.current_stream() takes longer than a small kernel
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
+        if _raw_stream is not None:
+            return _raw_stream(_get_device())
+        import torch
+        _current_device()
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_device() -> int:
+    """The current device; like the stream's handle without torch's own detours."""
+    global _raw_stream, _get_device
+    if _get_device is not None:
+        return _get_device()
+    import torch
+    raw, get = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is not None and get is not None and torch.cuda.is_initialized():
+        _raw_stream, _get_device = raw, get
+    return torch.cuda.current_device()
 
 
 def _tokens(valid_tokens):
@@ -957,33 +972,32 @@ class Fp4:
         self._device = self.codes.device.index if self.codes.is_cuda else None
 
 
-def _current_device() -> int:
-    import torch
-    # torch.cuda.current_device() takes longer than a small kernel's checks
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return get() if get is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
-
-
 def _elsewhere(index, what: str):
     """Kernels are launched on the current device: its tensors only."""
-    if index is None:
+    if index is None or index < 0:
         raise TypeError(f"{what}: expected a CUDA tensor")
     raise ValueError(f"{what}: on device {index}, but device {_current_device()} is current")
 
 
-def _fp4(q: Optional[Fp4], what: str):
+def _device_of(t, what: str) -> int:
+    """The current device, on which `t` has to be."""
+    index = t.get_device()
+    if index < 0:
+        _elsewhere(index, what)
+    here = _current_device()
+    if index != here:
+        _elsewhere(index, what)
+    return here
+
+
+def _fp4(q: Optional[Fp4], here: int, what: str):
     if q is None:
         return None
     if not isinstance(q, Fp4):
         raise TypeError(f"{what}: expected an Fp4")
-    if q._device is None or q._device != _current_device():
+    if q._device != here:
         _elsewhere(q._device, what)
     return q._ref
-
-
-def _here(t, what: str):
-    if not t.is_cuda or t.get_device() != _current_device():
-        _elsewhere(t.get_device() if t.is_cuda else None, what)
 
 
 @functools.lru_cache(maxsize=None)
@@ -993,8 +1007,8 @@ def _dtype_codes():
 
 
 def _matrix(t, what: str):
-    """(pointer, dtype, row stride) of a two-dimensional tensor with neighbouring
-    columns."""
+    """(pointer, dtype, rows, columns, row stride, device) of a two-dimensional
+    tensor with neighbouring columns on the current device."""
     dt = _dtype_codes().get(t.dtype)
     if dt is None:
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
@@ -1004,18 +1018,18 @@ def _matrix(t, what: str):
     stride, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{what}: columns must be neighbours in memory")
-    _here(t, what)
-    return t.data_ptr(), dt, stride if rows > 1 else cols
+    return t.data_ptr(), dt, rows, cols, stride if rows > 1 else cols, _device_of(t, what)
 
 
-def _seed(seed):
+def _seed(seed, here: int):
     """A one-element int64 CUDA tensor, read when the kernels run."""
     if seed is None:
         return None
     import torch
     if not isinstance(seed, torch.Tensor) or seed.dtype != torch.int64 or seed.numel() != 1:
         raise TypeError("seed: expected a CUDA tensor of one int64")
-    _here(seed, "seed")
+    if seed.get_device() != here:
+        _elsewhere(seed.get_device(), "seed")
     return seed.data_ptr()
 
 
@@ -1023,17 +1037,17 @@ def dpg_fp4_quantize(x, by_row: Optional[Fp4] = None, by_col: Optional[Fp4] = No
                      stream=None):
     """by_row <- x (bf16 or fp32 matrix), by_col <- its transpose, each in blocks
     along its own rows; nearest values, or stochastic ones with a seed."""
-    p, dt, stride = _matrix(x, "x")
-    _check(lib().dpg_fp4_quantize(p, dt, x.shape[0], x.shape[1], stride, _seed(seed), _fp4(by_row, "by_row"),
-                                  _fp4(by_col, "by_col"), _stream(stream)))
+    p, dt, rows, cols, stride, here = _matrix(x, "x")
+    _check(lib().dpg_fp4_quantize(p, dt, rows, cols, stride, _seed(seed, here), _fp4(by_row, here, "by_row"),
+                                  _fp4(by_col, here, "by_col"), _stream(stream)))
 
 
 def dpg_fp4_dequantize(q: Fp4, out, stream=None):
     """out (bf16 or fp32 matrix) <- the values of q."""
-    if tuple(out.shape) != (q.rows, q.cols):
+    if out.shape != (q.rows, q.cols):
         raise ValueError(f"out: expected {q.rows} x {q.cols}, got {tuple(out.shape)}")
-    p, dt, stride = _matrix(out, "out")
-    _check(lib().dpg_fp4_dequantize(_fp4(q, "q"), p, dt, stride, _stream(stream)))
+    p, dt, _, _, stride, here = _matrix(out, "out")
+    _check(lib().dpg_fp4_dequantize(_fp4(q, here, "q"), p, dt, stride, _stream(stream)))
 
 
 def dpg_allgather_params_fp4(mats: Matrices, master: Ptr, by_row: Optional[Sequence[Fp4]] = None,
@@ -1041,25 +1055,26 @@ def dpg_allgather_params_fp4(mats: Matrices, master: Ptr, by_row: Optional[Seque
     """The 4-bit form of every matrix of a plan, in the order of its parameters,
     from the flat fp32 masters; by_col holds the transposes."""
     _need(master, "f32", mats.total_padded, "master")
+    here = _current_device() if master is None or isinstance(master, int) else _device_of(master, "master")
     arrays = []
     for name, qs in (("by_row", by_row), ("by_col", by_col)):
         if qs is not None:
             if len(qs) != mats.n_matrices:
                 raise ValueError(f"{name}: need {mats.n_matrices} matrices, got {len(qs)}")
             for q in qs:
-                _fp4(q, name)
+                _fp4(q, here, name)
             qs = (dpg_fp4 * max(1, len(qs)))(*(q.c for q in qs))
         arrays.append(qs)
-    _check(lib().dpg_allgather_params_fp4(mats.handle, _ptr(master), _seed(seed), arrays[0], arrays[1],
+    _check(lib().dpg_allgather_params_fp4(mats.handle, _ptr(master), _seed(seed, here), arrays[0], arrays[1],
                                           mats.n_matrices, _stream(stream)))
 
 
 def dpg_fp4_product(a: Fp4, b: Fp4, out, *, accumulate: bool = False, stream=None):
     """out (a.rows x b.rows, bf16 or fp32) <- a b^T, or out + a b^T."""
-    if tuple(out.shape) != (a.rows, b.rows):
+    if out.shape != (a.rows, b.rows):
         raise ValueError(f"out: expected {a.rows} x {b.rows}, got {tuple(out.shape)}")
-    p, dt, stride = _matrix(out, "out")
-    _check(lib().dpg_fp4_product(_fp4(a, "a"), _fp4(b, "b"), p, dt, stride, 1 if accumulate else 0,
+    p, dt, _, _, stride, here = _matrix(out, "out")
+    _check(lib().dpg_fp4_product(_fp4(a, here, "a"), _fp4(b, here, "b"), p, dt, stride, 1 if accumulate else 0,
                                  _stream(stream)))
 
 
@@ -1071,7 +1086,7 @@ def dpg_fp4_status(stream=None):
 # --------------------------------------------------------------------------
 # layer norm
 # --------------------------------------------------------------------------
-def _vector(t, n: int, what: str):
+def _vector(t, n: int, what: str, here: int):
     """(pointer, dtype) of a contiguous tensor of n elements, or (None, None)."""
     if t is None:
         return None, None
@@ -1080,73 +1095,75 @@ def _vector(t, n: int, what: str):
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous elements")
-    if not t.is_cuda or t.get_device() != _current_device():
-        _elsewhere(t.get_device() if t.is_cuda else None, what)
+    if t.get_device() != here:
+        _elsewhere(t.get_device(), what)
     return t.data_ptr(), dt
 
 
-def _pair_dtype(a, b, what: str) -> int:
-    if a is not None and b is not None and a != b:
-        raise TypeError(f"{what}: expected one dtype")
-    return a if a is not None else b if b is not None else DPG_F32
-
-
 def _rows_of(x):
+    """(pointer, dtype, rows, columns, device) of contiguous rows on the current device."""
     if x.dim() < 1:
         raise ValueError("x: expected rows")
-    cols = x.shape[-1]
-    return x.numel() // cols if cols else 0, cols
+    cols, n, index = x.shape[-1], x.numel(), x.get_device()
+    p, dt = _vector(x, n, "x", index)
+    if index < 0 or index != _current_device():
+        _elsewhere(index, "x")
+    return p, dt, n // cols if cols else 0, cols, index
 
 
-def _stat(t, rows: int, what: str):
+def _same(t, n: int, dtype: int, what: str, here: int):
+    """The pointer of a tensor (or None) of the dtype given."""
     if t is None:
         return None
-    p, dt = _vector(t, rows, what)
-    if dt != DPG_F32:
-        raise TypeError(f"{what}: expected float32, got {t.dtype}")
+    p, dt = _vector(t, n, what, here)
+    if dt != dtype:
+        raise TypeError(f"{what}: expected {'float32' if dtype == DPG_F32 else 'bfloat16'}, got {t.dtype}")
     return p
 
 
 def dpg_layer_norm(x, gain, bias, eps: float, y, mean=None, rstd=None, stream=None):
     """y <- (x - mean) * rstd * gain + bias over the last dimension; mean and rstd
     (fp32, one a row) are kept for the backward pass."""
-    rows, cols = _rows_of(x)
-    px, dt = _vector(x, x.numel(), "x")
-    py, dy = _vector(y, x.numel(), "y")
-    if dy != dt:
-        raise TypeError("y: expected the dtype of x")
-    (pg, dg), (pb, db) = _vector(gain, cols, "gain"), _vector(bias, cols, "bias")
-    _check(lib().dpg_layer_norm(px, dt, rows, cols, pg, pb, _pair_dtype(dg, db, "gain and bias"), float(eps), py,
-                                _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd"), _stream(stream)))
+    px, dt, rows, cols, here = _rows_of(x)
+    pg, pd = _vector(gain, cols, "gain", here)
+    if pd is None:
+        pb, pd = _vector(bias, cols, "bias", here)
+    else:
+        pb = _same(bias, cols, pd, "bias", here)
+    _check(lib().dpg_layer_norm(px, dt, rows, cols, pg, pb, DPG_F32 if pd is None else pd, eps,
+                                _same(y, rows * cols, dt, "y", here), _same(mean, rows, DPG_F32, "mean", here),
+                                _same(rstd, rows, DPG_F32, "rstd", here), _stream(stream)))
 
 
 def dpg_layer_norm_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace of a backward pass that sums gain's or bias's gradients."""
-    return int(lib().dpg_layer_norm_workspace(rows, cols))
+    return lib().dpg_layer_norm_workspace(rows, cols)
 
 
 def dpg_layer_norm_backward(dy, x, gain, mean, rstd, dx=None, dgain=None, dbias=None, workspace=None, *,
                             accumulate: bool = False, stream=None):
     """dx, and the gradients of gain and bias summed over the rows (bf16 or fp32;
     accumulate: added to what fp32 ones hold).  Each may be None."""
-    rows, cols = _rows_of(x)
-    px, dt = _vector(x, x.numel(), "x")
-    pdy, ddy = _vector(dy, x.numel(), "dy")
-    pdx, ddx = _vector(dx, x.numel(), "dx")
-    if ddy != dt or ddx not in (None, dt):
-        raise TypeError("dy, dx: expected the dtype of x")
-    pg, dg = _vector(gain, cols, "gain")
-    (pdg, ddg), (pdb, ddb) = _vector(dgain, cols, "dgain"), _vector(dbias, cols, "dbias")
+    px, dt, rows, cols, here = _rows_of(x)
+    n = rows * cols
+    pg, pd = _vector(gain, cols, "gain", here)
+    pdg, gd = _vector(dgain, cols, "dgain", here)
+    if gd is None:
+        pdb, gd = _vector(dbias, cols, "dbias", here)
+    else:
+        pdb = _same(dbias, cols, gd, "dbias", here)
     if workspace is not None:
-        _here(workspace, "workspace")
         need = dpg_layer_norm_workspace(rows, cols)
-        if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        if workspace.get_device() != here:
+            _elsewhere(workspace.get_device(), "workspace")
+        if workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
             raise ValueError(f"workspace: needs {need} contiguous bytes")
         workspace = workspace.data_ptr()
     _check(lib().dpg_layer_norm_backward(
-        pdy, px, dt, rows, cols, pg, _pair_dtype(dg, None, "gain"), _stat(mean, rows, "mean"),
-        _stat(rstd, rows, "rstd"), pdx, pdg, pdb, _pair_dtype(ddg, ddb, "dgain and dbias"),
-        1 if accumulate else 0, workspace, _stream(stream)))
+        _same(dy, n, dt, "dy", here), px, dt, rows, cols, pg, DPG_F32 if pd is None else pd,
+        _same(mean, rows, DPG_F32, "mean", here), _same(rstd, rows, DPG_F32, "rstd", here),
+        _same(dx, n, dt, "dx", here), pdg, pdb, DPG_F32 if gd is None else gd, 1 if accumulate else 0, workspace,
+        _stream(stream)))
 
 
 def dpg_set_fused_max_ctas(max_ctas: int = 0):
