@@ -230,8 +230,23 @@ __device__ __forceinline__ void places(uint64_t y, uint32_t* p) {
     const float2 a = halves_of(fma2_up(y, pair_of(2.0f, 2.0f), pair_of(32.0f + one, 32.0f + one)));
     const float2 b = halves_of(fma2_up(y, pair_of(1.0f, 1.0f), pair_of(34.0f + one, 34.0f + one)));
     const float2 c = halves_of(fma2_up(y, pair_of(0.5f, 0.5f), pair_of(36.0f + one, 36.0f + one)));
-    p[0] = __float_as_uint(fminf(fminf(a.x, b.x), c.x));
-    p[1] = __float_as_uint(fminf(fminf(a.y, b.y), c.y));
+    float x, y1;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a.x), "f"(b.x), "f"(c.x));
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y1) : "f"(a.y), "f"(b.y), "f"(c.y));
+    p[0] = __float_as_uint(x);
+    p[1] = __float_as_uint(y1);
+}
+
+// p - 4 times the lower, the upper half of h
+__device__ __forceinline__ uint32_t less_low(uint32_t p, uint32_t h) {
+    uint32_t r;
+    asm("dp2a.lo.u32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(0x000000FC), "r"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t less_high(uint32_t p, uint32_t h) {
+    uint32_t r;
+    asm("dp2a.lo.u32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(0x0000FC00), "r"(p));
+    return r;
 }
 
 // B elements of a block to codes, 8 to a word.  w: the elements as they are in
@@ -274,16 +289,18 @@ __device__ __forceinline__ void encode(const uint32_t* w, const BlockScale& b, u
                 lo = __byte_perm(__byte_perm(v[0], v[1], 0x0051), __byte_perm(v[2], v[3], 0x0051), 0x5410);
                 hi = __byte_perm(__byte_perm(v[0], v[1], 0x0073), __byte_perm(v[2], v[3], 0x0073), 0x5410);
             }
-            uint32_t word = (hi & 0x80808080u) | ((lo & 0x80808080u) >> 4);
+            uint32_t t[8];                                  // codes in bits 18 .. 20
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t p[2];
                 places(y[j], p);
-                const uint32_t t = p[0] - 4u * (h[j] & 0xFFFFu), v = p[1] - 4u * (h[j] >> 16);
-                // codes in bits 18 .. 20, nothing set above them up to bit 24
-                word |= (8 * j < 18 ? t >> (18 - 8 * j) : t << (8 * j - 18)) & (7u << (8 * j));
-                word |= (8 * j + 4 < 18 ? v >> (14 - 8 * j) : v << (8 * j - 14)) & (7u << (8 * j + 4));
+                t[2 * j] = less_low(p[0], h[j]);
+                t[2 * j + 1] = less_high(p[1], h[j]);
             }
+            const uint32_t even = __byte_perm(__byte_perm(t[0], t[2], 0x0062), __byte_perm(t[4], t[6], 0x0062), 0x5410);
+            const uint32_t odd = __byte_perm(__byte_perm(t[1], t[3], 0x0062), __byte_perm(t[5], t[7], 0x0062), 0x5410);
+            uint32_t word = (hi & 0x80808080u) | ((lo & 0x80808080u) >> 4);
+            word |= ((even >> 2) & 0x07070707u) | ((odd << 2) & 0x70707070u);
             out[g] = b.bad ? 0u : word;
         } else {
             out[g] = b.bad ? 0u : nearest8(y);
