@@ -24,6 +24,7 @@ namespace dpg {
 constexpr int kProdDepth = 256;                  // elements of the sum in a stage
 constexpr int kCodeRow = kProdDepth / 2;         // bytes of a row in a stage
 constexpr int kRowTile = 128;                    // rows of an operand in a CTA
+constexpr int kStoreBytes = 4096;                // of a storing warp: two boxes, or 32 x 32 sums
 constexpr int kScaleBytes = 2048;                // room for the scales of 128 rows in a stage
 constexpr uint64_t kProdWaitNs = 2000000000ull;  // bound of every wait, unless a test sets another
 
@@ -85,6 +86,17 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, const CUtensorMap* map, 
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// 128-byte rows y .. of row of tiles z
+__device__ __forceinline__ void copy_scale_rows(uint32_t dst, const CUtensorMap* map, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_scale_rows_pair(uint32_t dst, const CUtensorMap* map, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 // `bar` may be the other CTA's of the pair
 __device__ __forceinline__ void copy_tile_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -193,47 +205,40 @@ __device__ __forceinline__ ProductScale product_scale(const ProductArgs& a) {
     return s;
 }
 
-// four neighbouring results of C's row r, from column c on (a multiple of 4)
-__device__ __forceinline__ void store_four(const ProductArgs& a, int r, int c, const float* x) {
-    if (r >= a.m || c >= a.n) return;
-    const int64_t at = int64_t(r) * a.stride + c;
-    if (a.vec && c + 4 <= a.n) {
-        if (a.c_f32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.c) + at);
-            float4 y = make_float4(x[0], x[1], x[2], x[3]);
-            if (a.add) {
-                const float4 o = *p;
-                y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
-            }
-            *p = y;
+// Four neighbouring results at `at` (elements of C), `n` of them inside C.
+__device__ __forceinline__ float4 held_four(const ProductArgs& a, int64_t at, int n) {
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float* p = static_cast<const float*>(a.c) + at;
+    if (a.vec && n >= 4) return *reinterpret_cast<const float4*>(p);
+    if (n > 0) o.x = p[0];
+    if (n > 1) o.y = p[1];
+    if (n > 2) o.z = p[2];
+    if (n > 3) o.w = p[3];
+    return o;
+}
+__device__ __forceinline__ void store_four(const ProductArgs& a, int64_t at, int n, float4 y) {
+    if (a.c_f32) {
+        float* p = static_cast<float*>(a.c) + at;
+        if (a.vec && n >= 4) {
+            *reinterpret_cast<float4*>(p) = y;
         } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.c) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (n > 0) p[0] = y.x;
+            if (n > 1) p[1] = y.y;
+            if (n > 2) p[2] = y.z;
+            if (n > 3) p[3] = y.w;
         }
         return;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (c + j < a.n) {
-            if (a.c_f32) {
-                float* p = static_cast<float*>(a.c) + at + j;
-                *p = a.add ? *p + x[j] : x[j];
-            } else {
-                static_cast<__nv_bfloat16*>(a.c)[at + j] = __float2bfloat16_rn(x[j]);
-            }
-        }
-}
-
-// one result
-__device__ __forceinline__ void store_one(const ProductArgs& a, int r, int c, float x) {
-    if (r >= a.m || c >= a.n) return;
-    const int64_t at = int64_t(r) * a.stride + c;
-    if (a.c_f32) {
-        float* p = static_cast<float*>(a.c) + at;
-        *p = a.add ? *p + x : x;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.c) + at;
+    if (a.vec && n >= 4) {
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     } else {
-        static_cast<__nv_bfloat16*>(a.c)[at] = __float2bfloat16_rn(x);
+        if (n > 0) p[0] = lo.x;
+        if (n > 1) p[1] = lo.y;
+        if (n > 2) p[2] = hi.x;
+        if (n > 3) p[3] = hi.y;
     }
 }
 
@@ -246,6 +251,76 @@ template <int COLS>
 __device__ __forceinline__ int piece_at(int row, int piece) {
     constexpr int kMask = COLS >= 32 ? 7 : 3;
     return row * COLS + ((piece ^ ((COLS >= 32 ? row : row >> 1) & kMask)) << 2);
+}
+
+// A warp's 32 x 32 results (lane: row) by bulk copies: boxes of 32 rows x 64
+// bytes with a 64-byte swizzle, in two halves of the warp's 4 KB in turn.  (One box
+// of 128 bytes at a time: 4096 x 2304 x 768 9.3 us instead of 7.3.)
+__device__ __forceinline__ void store_boxes(const ProductArgs& a, const CUtensorMap* map, uint32_t smem, int lane, int r,
+                                            int c, const float* v, uint32_t& boxes) {
+    const int n = a.c_f32 ? 2 : 1, width = a.c_f32 ? 16 : 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h >= n || c + h * width >= a.n) break;
+        const uint32_t at = smem + (boxes++ & 1) * (kStoreBytes / 2), row = at + uint32_t(lane) * 64;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // what it held is on its way
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t to = row + (uint32_t(j) ^ (uint32_t(lane) >> 1 & 3u)) * 16;
+            const uint4 w = a.c_f32 ? make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
+                                                 __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]))
+                                    : narrow8(v + 8 * j);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(to), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (a.add)
+                asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
+                             :: "l"(map), "r"(c + h * width), "r"(r), "r"(at) : "memory");
+            else
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                             :: "l"(map), "r"(c + h * width), "r"(r), "r"(at) : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+// 32 x 32 results singly, four columns of four rows to a lane group, any alignment
+__device__ __forceinline__ void store_singly(const ProductArgs& a, float* box, int lane, int r, int c, const float* v) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(box + piece_at<32>(lane, j >> 2)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    __syncwarp();
+    const int row0 = lane >> 3, piece = lane & 7, n = a.n - c - 4 * piece, rows = a.m - r - row0;
+    const int64_t at = int64_t(r + row0) * a.stride + c + 4 * piece, step = 4 * a.stride;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {           // four rows' old values at a time
+        float4 o[4];
+        if (a.add) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (16 * half + 4 * i < rows) o[i] = held_four(a, at + (4 * half + i) * step, n);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (16 * half + 4 * i < rows) {
+                float4 y = *reinterpret_cast<const float4*>(box + piece_at<32>(16 * half + i * 4 + row0, piece));
+                if (a.add) y.x += o[i].x, y.y += o[i].y, y.z += o[i].z, y.w += o[i].w;
+                store_four(a, at + (4 * half + i) * step, n, y);
+            }
+    }
+}
+
+// 32 columns of a warp's 32 rows from row r, column c on, scaled, into C
+__device__ __forceinline__ void store_columns(const ProductArgs& a, const CUtensorMap* map, const ProductScale& scale, float* box,
+                                              int lane, int r, int c, float* v, uint32_t& boxes) {
+    if (r >= a.m || c >= a.n) return;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = v[j] * scale.f[0] * scale.f[1];
+    if (a.vec) store_boxes(a, map, smem_u32(box), lane, r, c, v, boxes);
+    else store_singly(a, box, lane, r, c, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -280,25 +355,88 @@ struct SmallShared {
     volatile int abort;
 };
 
-// of CTA q's shared memory (`split` == 1: this CTA's)
-__device__ __forceinline__ float load_part(uint32_t at, int q, int split) {
-    float x;
-    if (split == 1) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
-    else asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to(at, uint32_t(q))) : "memory");
-    return x;
+// The cluster's parts of a tile added up, this CTA's share of its rows: a thread
+// keeps to four columns.  What C holds and the parts of kBatch rows are on their way
+// at a time.
+template <int COLS, int SPLIT>
+__device__ __forceinline__ void join_rows(const ProductArgs& a, const ProductScale& scale, uint32_t part, int rank, int r0, int c0) {
+    constexpr int kPer = COLS / 4, kStep = kSmallThreads / kPer, kBatch = SPLIT == 8 ? 2 : 4;
+    constexpr int kShare = kRowTile / SPLIT;
+    const int piece = int(threadIdx.x) % kPer, row0 = int(threadIdx.x) / kPer;
+    const int n = a.n - c0 - 4 * piece, rows = min(kShare, a.m - r0 - rank * kShare);
+    uint32_t from[SPLIT];
+#pragma unroll
+    for (int q = 0; q < SPLIT; ++q) from[q] = map_to(part, uint32_t(q));
+    for (int i = row0; i < rows; i += kBatch * kStep) {
+        const int64_t at = int64_t(r0 + rank * kShare + i) * a.stride + c0 + 4 * piece;
+        float4 o[kBatch], y[kBatch][SPLIT];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (i + u * kStep >= rows) continue;
+            if (a.add) o[u] = held_four(a, at + u * kStep * a.stride, n);
+            const uint32_t off = uint32_t(piece_at<COLS>(rank * kShare + i + u * kStep, piece)) * 4;
+#pragma unroll
+            for (int q = 0; q < SPLIT; ++q)
+                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(y[u][q].x), "=f"(y[u][q].y), "=f"(y[u][q].z), "=f"(y[u][q].w)
+                             : "r"(from[q] + off) : "memory");
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (i + u * kStep >= rows) continue;
+            float4 x = y[u][0];
+#pragma unroll
+            for (int q = 1; q < SPLIT; ++q) x.x += y[u][q].x, x.y += y[u][q].y, x.z += y[u][q].z, x.w += y[u][q].w;
+            x = make_float4(x.x * scale.f[0] * scale.f[1], x.y * scale.f[0] * scale.f[1], x.z * scale.f[0] * scale.f[1],
+                            x.w * scale.f[0] * scale.f[1]);
+            if (a.add) x.x += o[u].x, x.y += o[u].y, x.z += o[u].z, x.w += o[u].w;
+            store_four(a, at + u * kStep * a.stride, n, x);
+        }
+    }
 }
-__device__ __forceinline__ float4 load_part4(uint32_t at, int q, int split) {
-    float4 x;
-    if (split == 1)
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
-    else
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(map_to(at, uint32_t(q))) : "memory");
-    return x;
+// The same where C's rows run along the tile's columns: this CTA's share of those,
+// a thread to a row of the tile.
+template <int COLS, int SPLIT>
+__device__ __forceinline__ void join_columns(const ProductArgs& a, const ProductScale& scale, uint32_t part, int rank, int r0,
+                                             int c0) {
+    constexpr int kShare = COLS / SPLIT, kBatch = kShare < 4 ? kShare : 4;
+    const int row = int(threadIdx.x), c = c0 + rank * kShare;
+    if (row >= kRowTile || r0 + row >= a.n) return;
+    uint32_t from[SPLIT];
+#pragma unroll
+    for (int q = 0; q < SPLIT; ++q) from[q] = map_to(part, uint32_t(q)) + uint32_t(rank * kShare * kRowTile + row) * 4;
+#pragma unroll 1
+    for (int j = 0; j < kShare && c + j < a.m; j += kBatch) {
+        float x[kBatch], y[kBatch][SPLIT];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t at = int64_t(c + j + u) * a.stride + r0 + row;
+            x[u] = a.add && c + j + u < a.m ? static_cast<const float*>(a.c)[at] : 0.0f;
+#pragma unroll
+            for (int q = 0; q < SPLIT; ++q)
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y[u][q]) : "r"(from[q] + uint32_t(j + u) * kRowTile * 4) : "memory");
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (c + j + u >= a.m) continue;
+            const int64_t at = int64_t(c + j + u) * a.stride + r0 + row;
+            float t = y[u][0];
+#pragma unroll
+            for (int q = 1; q < SPLIT; ++q) t += y[u][q];
+            t = x[u] + t * scale.f[0] * scale.f[1];
+            if (a.c_f32) static_cast<float*>(a.c)[at] = t;
+            else static_cast<__nv_bfloat16*>(a.c)[at] = __float2bfloat16_rn(t);
+        }
+    }
+}
+template <int COLS, int SPLIT>
+__device__ __forceinline__ void join_parts(const ProductArgs& a, const ProductScale& scale, uint32_t part, int rank, int r0, int c0) {
+    if (a.swap) join_columns<COLS, SPLIT>(a, scale, part, rank, r0, c0);
+    else join_rows<COLS, SPLIT>(a, scale, part, rank, r0, c0);
 }
 
 template <bool MX, int COLS>
-__global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_constant__ ProductArgs a,
+__global__ void __launch_bounds__(kSmallThreads, 2) k_fp4_small(const __grid_constant__ ProductArgs a,
                                                              const __grid_constant__ ProductMaps maps) {
     using S = SmallShape<COLS>;
     constexpr int kStages = S::kStages;
@@ -342,8 +480,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
             if (blockIdx.x != 0 || k - first != a.skip) copy_tile(at, &maps.codes_r, k * kCodeRow, r0, bar);
             copy_tile(at + kRowTile * kCodeRow, &maps.codes_c, k * kCodeRow, c0, bar);
             const uint32_t sf = at + kRowTile * kCodeRow + S::kCodes;
-            copy_tile(sf, &maps.scales_r, k * (MX ? 128 : 256), r0 / kFp4TileRows, bar);
-            copy_tile(sf + kScaleBytes, &maps.scales_c, k * (MX ? 128 : 256), c0 / kFp4TileRows, bar);
+            copy_scale_rows(sf, &maps.scales_r, k * (MX ? 8 : 16), r0 / kFp4TileRows, bar);
+            copy_scale_rows(sf + kScaleBytes, &maps.scales_c, k * (MX ? 8 : 16), c0 / kFp4TileRows, bar);
             if (++s == kStages) {
                 s = 0;
                 par ^= 1;
@@ -374,27 +512,41 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
     }
     __syncwarp();
     float* const part = reinterpret_cast<float*>(dyn);
+    const ProductScale scale = product_scale<MX>(a);
     if (warp >= 2) {
-        const int row = (warp & 3) * 32 + lane;
+        const int row0 = (warp & 3) * 32, row = row0 + lane;
         const bool ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.done, 0, &sh.abort, a.wait_ns));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sums = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t sums = tmem + (uint32_t(row0) << 16);
         constexpr int kGroup = COLS < 32 ? COLS : 32;
-        if (ok)                                             // the stages are free: every product is done
+        if (ok) {                                           // the stages are free: every product is done
+            if (COLS == 128 && a.split == 1) {              // whole sums: each warp stores its rows
+                float* box = part + row0 * (kStoreBytes / 128);
+                uint32_t boxes = 0;
 #pragma unroll 1
-            for (int c = 0; c < COLS; c += 32) {
-                float v[32];
-                load_acc32(sums + c, v);                    // (COLS = 16: with 16 unused columns)
-                if (a.swap) {
+                for (int c = 0; c < COLS; c += 32) {
+                    float v[32];
+                    load_acc32(sums + c, v);
+                    store_columns(a, &maps.result, scale, box, lane, r0 + row0, c0 + c, v, boxes);
+                }
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < COLS; c += 32) {
+                    float v[32];
+                    load_acc32(sums + c, v);                // (COLS = 16: with 16 unused columns)
+                    if (a.swap) {
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j) part[(c + j) * kRowTile + row] = v[j];
-                } else {
+                        for (int j = 0; j < kGroup; ++j) part[(c + j) * kRowTile + row] = v[j];
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < kGroup; j += 4)
-                        *reinterpret_cast<float4*>(part + piece_at<COLS>(row, (c + j) >> 2)) =
-                            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        for (int j = 0; j < kGroup; j += 4)
+                            *reinterpret_cast<float4*>(part + piece_at<COLS>(row, (c + j) >> 2)) =
+                                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
                 }
             }
+        }
     }
     if (sh.abort) {   // the copies this CTA has in flight land within this time
         const uint64_t until = global_ns() + 2000000ull;
@@ -404,29 +556,11 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
     __syncthreads();
     if (a.split > 1) cluster_sync();
     if (!sh.abort) {
-        const ProductScale scale = product_scale<MX>(a);
-        const uint32_t part0 = smem_u32(part);
-        if (a.swap) {                                       // columns of sums: neighbours in C's rows
-            const int share = COLS / a.split, from = rank * share * kRowTile;
-            for (int e = int(threadIdx.x); e < share * kRowTile; e += kSmallThreads) {
-                float x = 0.0f;
-                for (int q = 0; q < a.split; ++q) x += load_part(part0 + uint32_t(from + e) * 4, q, a.split);
-                store_one(a, c0 + (from + e) / kRowTile, r0 + (from + e) % kRowTile, x * scale.f[0] * scale.f[1]);
-            }
-        } else {
-            const int share = kRowTile / a.split, from = rank * share;
-            for (int e = int(threadIdx.x); e < share * (COLS / 4); e += kSmallThreads) {
-                const int row = from + e / (COLS / 4), piece = e % (COLS / 4);
-                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int q = 0; q < a.split; ++q) {
-                    const float4 y = load_part4(part0 + uint32_t(piece_at<COLS>(row, piece)) * 4, q, a.split);
-                    x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = x[j] * scale.f[0] * scale.f[1];
-                store_four(a, r0 + row, c0 + 4 * piece, x);
-            }
-        }
+        const uint32_t at = smem_u32(part);
+        if (a.split == 8) join_parts<COLS, 8>(a, scale, at, rank, r0, c0);
+        else if (a.split == 4) join_parts<COLS, 4>(a, scale, at, rank, r0, c0);
+        else if (a.split == 2) join_parts<COLS, 2>(a, scale, at, rank, r0, c0);
+        else if (COLS < 128) join_parts<COLS, 1>(a, scale, at, rank, r0, c0);
     }
     if (a.split > 1) cluster_sync();                        // the others have read this CTA's part
     if (warp == 1)
@@ -440,14 +574,11 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp4_small(const __grid_consta
 // of its own rows and of all columns.
 //
 // Tensor memory: sums of even tiles in columns 0 .. 255, of odd ones in 160 ..
-// 415, two sets of a stage's scales in 416 .. 511.  The next tile's products
-// start when the 96 columns that both sums have are stored, which is done first.
+// 415, two sets of a stage's scales behind them.  The next tile's products start
+// when the 96 columns that both sums have are read, which is done first.
 //
 //   warp 0  copies operands     warp 1  of CTA 0: issues the products
-//   warps 2..9  store (warp w: lanes 32 (w mod 4) .., every other 32 columns):
-//               32 x 32 sums to 4 KB of shared memory and from there by bulk
-//               copies of 32 rows x 64 bytes, added to C where they are to be, or
-//               singly where C's rows do not start on 16-byte boundaries
+//   warps 2..9  store (warp w: lanes 32 (w mod 4) .., every other 32 columns)
 // ---------------------------------------------------------------------------
 constexpr int kLargeStages = 5;
 constexpr int kLargeCodes = kRowTile * kCodeRow;
@@ -461,7 +592,6 @@ struct LargeShared {
     uint32_t tmem;
     volatile int abort;
 };
-constexpr int kStoreBytes = 4096;                // of a storing warp: two boxes, or 32 x 32 sums
 constexpr int kLargeSmem = kLargeStages * kLargeStage + kLargeEpiWarps * kStoreBytes + int(sizeof(LargeShared));
 static_assert(kLargeStage % 1024 == 0, "the swizzle's boundary");
 static_assert(kLargeSmem <= 227 * 1024 && kLargeSmem + 78 * 1024 > 228 * 1024, "alone on its SM");
@@ -473,58 +603,6 @@ __device__ __forceinline__ void large_tile(const ProductArgs& a, int t, int& r0,
     const int high = min(8, a.tiles_r - 8 * g);
     r0 = (8 * g + in % high) * kLargeTile;
     c0 = in / high * kLargeTile;
-}
-
-// A warp's 32 x 32 results (lane: row) by bulk copies: boxes of 32 rows x 64
-// bytes with a 64-byte swizzle, in two halves of the warp's shared memory in turn.
-__device__ __forceinline__ void store_boxes(const ProductArgs& a, const CUtensorMap* map, uint32_t smem, int lane, int r,
-                                            int c, const float* v, uint32_t& boxes) {
-    const int n = a.c_f32 ? 2 : 1, width = a.c_f32 ? 16 : 32;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h >= n || c + h * width >= a.n) break;
-        const uint32_t at = smem + (boxes++ & 1) * (kStoreBytes / 2), row = at + uint32_t(lane) * 64;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // what it held is on its way
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t to = row + (uint32_t(j) ^ (uint32_t(lane) >> 1 & 3u)) * 16;
-            uint4 w;
-            if (a.c_f32) {
-                w = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
-                               __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
-            } else {
-                w = narrow8(v + 8 * j);
-            }
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(to), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            if (a.add)
-                asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
-                             :: "l"(map), "r"(c + h * width), "r"(r), "r"(at) : "memory");
-            else
-                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
-                             :: "l"(map), "r"(c + h * width), "r"(r), "r"(at) : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-    }
-}
-// the same, four columns of four rows to a lane group, any alignment
-__device__ __forceinline__ void store_singly(const ProductArgs& a, float* box, int lane, int r, int c, const float* v) {
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<float4*>(box + piece_at<32>(lane, j >> 2)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-        const int row = i * 4 + (lane >> 3), piece = lane & 7;
-        const float4 y = *reinterpret_cast<const float4*>(box + piece_at<32>(row, piece));
-        const float x[4] = {y.x, y.y, y.z, y.w};
-        store_four(a, r + row, c + 4 * piece, x);
-    }
 }
 
 template <bool MX>
@@ -578,8 +656,8 @@ k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ Produ
                 if (skip-- != 0) copy_tile_pair(at, &maps.codes_r, k * kCodeRow, r0 + int(rank) * kRowTile, bar);
                 copy_tile_pair(at + kLargeCodes, &maps.codes_c, k * kCodeRow, c0 + int(rank) * kRowTile, bar);
                 const uint32_t sf = at + 2 * kLargeCodes;
-                copy_tile_pair(sf, &maps.scales_r, k * (MX ? 128 : 256), r0 / kFp4TileRows + int(rank), bar);
-                copy_tile_pair(sf + kScaleBytes, &maps.scales_c, k * (MX ? 128 : 256), c0 / kFp4TileRows, bar);
+                copy_scale_rows_pair(sf, &maps.scales_r, k * (MX ? 8 : 16), r0 / kFp4TileRows + int(rank), bar);
+                copy_scale_rows_pair(sf + kScaleBytes, &maps.scales_c, k * (MX ? 8 : 16), c0 / kFp4TileRows, bar);
                 if (++s == kLargeStages) {
                     s = 0;
                     par ^= 1;
@@ -620,7 +698,7 @@ k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ Produ
         const ProductScale scale = product_scale<MX>(a);
         const uint32_t clear = map_to(smem_u32(&sh.clear), 0);
         float* const box = reinterpret_cast<float*>(dyn + kLargeStages * kLargeStage + (warp - 2) * kStoreBytes);
-        uint32_t boxes = 0;                          // stored so far
+        uint32_t boxes = 0;
         int it = 0;
         for (int t = pair; t < tiles; t += pairs, ++it) {
             int r0, c0;
@@ -643,12 +721,7 @@ k_fp4_large(const __grid_constant__ ProductArgs a, const __grid_constant__ Produ
                     if (lane == 0)
                         asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(clear) : "memory");
                 }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = v[j] * scale.f[0] * scale.f[1];
-                if (r < a.m && c0 + c < a.n) {       // the warp's first row
-                    if (a.vec) store_boxes(a, &maps.result, smem_u32(box), lane, r, c0 + c, v, boxes);
-                    else store_singly(a, box, lane, r, c0 + c, v);
-                }
+                store_columns(a, &maps.result, scale, box, lane, r, c0 + c, v, boxes);   // (r: the warp's first row)
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -713,15 +786,31 @@ static int encode_operand(const dpg_fp4* q, int box_rows, int box_tiles, CUtenso
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (e == CUDA_SUCCESS) {
+        // as 128-byte rows, four to a tile: boxes of one row of 1 or 2 KB took a quarter longer
         const int64_t tiles = fp4_tiles(q->cols, q->format);
-        const cuuint64_t sdims[2] = {cuuint64_t(tiles) * (kFp4TileBytes / 8),
-                                     cuuint64_t((q->rows + kFp4TileRows - 1) / kFp4TileRows)};
-        const cuuint64_t spitch[1] = {cuuint64_t(tiles) * kFp4TileBytes};
-        const cuuint32_t sbox[2] = {q->format == DPG_MXFP4 ? 128u : 256u, cuuint32_t(box_tiles)};
-        e = fn(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, q->scales, sdims, spitch, sbox, step,
+        const cuuint64_t sdims[3] = {128, cuuint64_t(tiles) * 4, cuuint64_t((q->rows + kFp4TileRows - 1) / kFp4TileRows)};
+        const cuuint64_t spitch[2] = {128, cuuint64_t(tiles) * kFp4TileBytes};
+        const cuuint32_t sbox[3] = {128, q->format == DPG_MXFP4 ? 8u : 16u, cuuint32_t(box_tiles)}, sstep[3] = {1, 1, 1};
+        e = fn(scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q->scales, sdims, spitch, sbox, sstep,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     }
+    return e == CUDA_SUCCESS ? DPG_OK : fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
+}
+
+// C in boxes of 32 rows x 64 bytes, if its rows start on 16-byte boundaries
+static int encode_result(const ProductArgs& a, CUtensorMap* map, const char* who) {
+    if (!a.vec) return DPG_OK;
+    EncodeTiled fn = nullptr;
+    const int st = encoder(&fn, who);
+    if (st != DPG_OK) return st;
+    const int size = a.c_f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {cuuint64_t(a.n), cuuint64_t(a.m)};
+    const cuuint64_t pitch[1] = {(cuuint64_t(a.stride) * size + 15) / 16 * 16};      // (one row may have any)
+    const cuuint32_t box[2] = {cuuint32_t(64 / size), 32}, step[2] = {1, 1};
+    const CUresult e = fn(map, a.c_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dims,
+                          pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return e == CUDA_SUCCESS ? DPG_OK : fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
 }
 
@@ -732,13 +821,16 @@ static int launch_small(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     a.tiles_c = (a.cols + COLS - 1) / COLS;
     const int64_t tiles = int64_t(a.tiles_r) * a.tiles_c;
     const int stages = (a.k + kProdDepth - 1) / kProdDepth;
-    // more CTAs share a sum while that leaves them at most two to an SM and two stages each
+    // More CTAs share a sum while that leaves them two to an SM at most (64 tiles of k = 2048: 4
+    // parts 9.0 us, 8 parts, in two rounds, 17.5) and four stages each, of narrow tiles two (128 x
+    // 4096 x 4096: 4 parts 7.7 us, 8 parts 9.6; 64 x 4096 x 4096: 7.9 and 7.2).
     a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= 2 * sms && stages >= 4 * a.split) a.split *= 2;
+    while (a.split < 8 && tiles * a.split * 2 <= 2 * sms && stages >= (COLS == 128 ? 8 : 4) * a.split) a.split *= 2;
     if (tiles * a.split > 0x7FFFFFFF) return fail(DPG_ERR_INVALID_ARG, "%s: %lld tiles", who, (long long)tiles);
     ProductMaps maps;
     int st = encode_operand(r, kRowTile, 1, &maps.codes_r, &maps.scales_r, who);
     if (st == DPG_OK) st = encode_operand(c, COLS, 1, &maps.codes_c, &maps.scales_c, who);
+    if (st == DPG_OK && COLS == 128 && a.split == 1) st = encode_result(a, &maps.result, who);
     if (st != DPG_OK) return st;
     auto k = k_fp4_small<MX, COLS>;
     static std::atomic<uint64_t> once{0};
@@ -783,19 +875,8 @@ static int launch_large(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     int st = encode_operand(r, kRowTile, 1, &maps.codes_r, &maps.scales_r, who);
     if (st == DPG_OK) st = encode_operand(c, kRowTile, 2, &maps.codes_c, &maps.scales_c, who);
     if (st != DPG_OK) return st;
-    if (a.vec) {
-        EncodeTiled fn = nullptr;
-        st = encoder(&fn, who);
-        if (st != DPG_OK) return st;
-        const int size = a.c_f32 ? 4 : 2;
-        const cuuint64_t dims[2] = {cuuint64_t(a.n), cuuint64_t(a.m)};
-        const cuuint64_t pitch[1] = {cuuint64_t(a.stride) * size};
-        const cuuint32_t box[2] = {cuuint32_t(64 / size), 32}, step[2] = {1, 1};
-        const CUresult e = fn(&maps.result, a.c_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                              2, a.c, dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (e != CUDA_SUCCESS) return fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
-    }
+    st = encode_result(a, &maps.result, who);
+    if (st != DPG_OK) return st;
     const int pairs = int(tiles < sms / 2 ? tiles : sms / 2);
     static std::atomic<uint64_t> once{0};
     st = allow_smem(reinterpret_cast<const void*>(k_fp4_large<MX>), kLargeSmem, once, who);
@@ -813,7 +894,7 @@ static int product(const dpg_fp4* x, const dpg_fp4* w, ProductArgs a, cudaStream
     a.rows = a.m;
     a.cols = a.n;
     const int few = a.m < a.n ? a.m : a.n;
-    if (few > kRowTile && large >= sms / 2) return launch_large<MX>(a, x, w, sms, s, who);
+    if (few > kRowTile && large >= sms / 4) return launch_large<MX>(a, x, w, sms, s, who);
     if (few > 64) return launch_small<MX, 128>(a, x, w, sms, s, who);
     // the shorter side in the columns of the sums
     a.swap = a.m < a.n;
