@@ -59,7 +59,8 @@ struct QuantArgs {
 // the CTAs of the quantisation take the largest of them: nothing to set to zero
 // before, and no atomics (9700 on one address took 12 us).
 // ---------------------------------------------------------------------------
-constexpr int kAmaxParts = DPG_FP4_AMAX_FLOATS - 1;
+constexpr int kAmaxCtas = 152;           // a GB300's SMs
+static_assert(kAmaxCtas < DPG_FP4_AMAX_FLOATS, "room for the parts");
 
 template <bool F32>
 __device__ __forceinline__ uint32_t magnitude_bits(uint32_t w) {      // of one fp32 or two bf16 values
@@ -95,16 +96,16 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* sh) {
     __syncthreads();
     return __reduce_max_sync(0xFFFFFFFFu, sh[threadIdx.x & (W - 1)]);
 }
-constexpr int kAmaxThreads = 512;
+constexpr int kAmaxThreads = 1024;
 
 template <bool F32>
 __global__ void __launch_bounds__(kAmaxThreads) k_fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t stride,
-                                                  int32_t flat, uint32_t* parts) {
+                                                  int64_t pieces, uint32_t* parts) {
     __shared__ uint32_t sh[kAmaxThreads / 32];
     pdl_enter();
     uint32_t m = 0;
     constexpr int kPer = F32 ? 4 : 8, kFly = 8;      // elements of 16 bytes, loads in flight
-    if (flat) {                                      // rows back to back
+    if (pieces == 0) {                               // rows back to back
         const int64_t n = rows * cols, t = int64_t(blockIdx.x) * kAmaxThreads + threadIdx.x,
                       step = int64_t(gridDim.x) * kAmaxThreads;
         // up to the first 16-byte boundary, and behind the last one, singly
@@ -130,10 +131,37 @@ __global__ void __launch_bounds__(kAmaxThreads) k_fp4_amax(const void* x, int64_
                            : magnitude_bits<false>(static_cast<const uint16_t*>(x)[j]));
         }
     } else {
-        for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-            for (int64_t c = threadIdx.x; c < cols; c += kAmaxThreads)
-                m = max(m, F32 ? magnitude_bits<true>(static_cast<const uint32_t*>(x)[r * stride + c])
-                               : magnitude_bits<false>(static_cast<const uint16_t*>(x)[r * stride + c]));
+        // pieces of rows between 16-byte boundaries, those at a row's ends singly
+        const int64_t n = rows * pieces, t = int64_t(blockIdx.x) * kAmaxThreads + threadIdx.x,
+                      step = int64_t(gridDim.x) * kAmaxThreads;
+        constexpr int kSize = F32 ? 4 : 2;
+        uint32_t ends = 0;
+        auto load = [&](int64_t i, bool singly) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i >= n) return v;
+            const int64_t r = (i | pieces) > 0x7FFFFFFF ? i / pieces : int64_t(uint32_t(i) / uint32_t(pieces));
+            const unsigned char* row = static_cast<const unsigned char*>(x) + r * stride * kSize;
+            const int64_t e = (i - r * pieces) * kPer - int(reinterpret_cast<uintptr_t>(row) & 15) / kSize;
+            if (e >= 0 && e + kPer <= cols) v = *reinterpret_cast<const uint4*>(row + e * kSize);
+            else if (singly)
+                for (int64_t c = max(e, int64_t(0)); c < min(e + kPer, cols); ++c)
+                    ends = max(ends, F32 ? magnitude_bits<true>(reinterpret_cast<const uint32_t*>(row)[c])
+                                         : magnitude_bits<false>(reinterpret_cast<const uint16_t*>(row)[c]));
+            return v;
+        };
+        for (int64_t i = t; i < n; i += kFly * step) {
+            uint4 v[kFly];
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) v[u] = load(i + u * step, true);
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) m = any_magnitude<F32>(m, v[u]);
+        }
+        if (!F32) m = max(m << 16, m) & 0xFFFF0000u;
+        if (m >= 0x7F800000u) {
+            m = 0;
+            for (int64_t i = t; i < n; i += step) m = max(m, magnitude_bits4<F32>(load(i, false)));
+        }
+        m = max(m, ends);
     }
     m = block_max<kAmaxThreads / 32>(m, sh);
     if (threadIdx.x == 0) parts[blockIdx.x] = m;
@@ -642,17 +670,16 @@ __global__ void __launch_bounds__(256) k_fp4_dequantize(const __grid_constant__ 
     // below its normal numbers.
     if (!F32 && whole && b0 == b1 && !(s0 != 0.0f && s0 < 7.5e-37f)) {
         const __nv_bfloat162 s = __float2bfloat162_rn(s0);
+        uint32_t h[8];
+        F8 f;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t h[4];
-            widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), h);
+        for (int g = 0; g < 2; ++g) widen_codes(__funnelshift_r(w[g], w[g + 1], 4 * (e0 & 7)), h + 4 * g);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h[j]), s);
-                h[j] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            st_u4(row + (int64_t(e0) + 8 * g) * 2, make_uint4(h[0], h[1], h[2], h[3]));
+        for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h[j]), s);
+            f.v[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&p));
         }
+        st_f8(reinterpret_cast<float*>(row + int64_t(e0) * 2), f);
         return;
     }
 #pragma unroll
@@ -810,11 +837,13 @@ static int quantize(QuantArgs& a, int32_t dtype, int32_t format, cudaStream_t s,
     // up to 8 tiles are one cluster, whose CTAs find the largest magnitude among themselves
     if (!mx && tiles > 8) {
         const int64_t n = a.rows * a.cols;
+        const int per = f32 ? 4 : 8;
         const bool flat = a.stride == a.cols;
-        const int64_t want = flat ? (n + 16383) / 16384 : a.rows;
-        a.parts = int32_t(want < kAmaxParts ? want : kAmaxParts);
+        const int64_t pieces = flat ? 0 : (a.cols + per - 1) / per + (a.vec ? 0 : 1);
+        const int64_t want = (n + 16383) / 16384;
+        a.parts = int32_t(want < kAmaxCtas ? want : kAmaxCtas);
         const int st = launch_k(f32 ? k_fp4_amax<true> : k_fp4_amax<false>, unsigned(a.parts), kAmaxThreads, s, who, a.x, a.rows,
-                                a.cols, a.stride, int32_t(flat), reinterpret_cast<uint32_t*>(a.amax) + 1);
+                                a.cols, a.stride, pieces, reinterpret_cast<uint32_t*>(a.amax) + 1);
         if (st != DPG_OK) return st;
     }
     const int which = (f32 ? 4 : 0) + (mx ? 2 : 0) + (a.seed ? 1 : 0);

@@ -396,9 +396,9 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_c
 // three rows ahead (asynchronous copies, which only the thread itself waits for):
 // a second set of registers for the next row left one CTA to an SM.
 // ---------------------------------------------------------------------------
-// rows ahead: 128 KB to a row of 16384 fp32 columns leave one
+// rows ahead: 128 KB to a row of 16384 fp32 columns leave one; two CTAs fit an SM at 768
 template <bool F32, int T, int V>
-constexpr int rows_ahead() { return F32 && T * V == 2048 ? 1 : 3; }
+constexpr int rows_ahead() { return F32 && T * V == 2048 ? 1 : F32 && T == 32 && V == 3 ? 2 : 3; }
 
 template <bool F32, int T, int V>
 constexpr int back_smem() { return rows_ahead<F32, T, V>() * norm_threads<T>() * V * 2 * (F32 ? 32 : 16); }
@@ -513,6 +513,19 @@ __device__ __forceinline__ void back_row(const NormBackArgs& a, const BackRows<F
     }
 }
 
+// eight neighbouring sums; workspaces start on 16-byte boundaries, most on 32-byte ones
+__device__ __forceinline__ void store_sums(float* to, const float* sums) {
+    if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+        F8 f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f.v[j] = sums[j];
+        st_f8(to, f);
+    } else {
+        *reinterpret_cast<float4*>(to) = make_float4(sums[0], sums[1], sums[2], sums[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(sums[4], sums[5], sums[6], sums[7]);
+    }
+}
+
 template <bool F32, int MODE, int T, int V>
 __global__ void __launch_bounds__(norm_threads<T>(), T == 32 ? 2 : T <= 256 ? (V == 1 ? 4 : 3) : 1)
 k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
@@ -596,6 +609,14 @@ k_layer_norm_back(const __grid_constant__ NormBackArgs a) {
             for (int w = 0; w < kRows; ++w) t += sums[w * 2 * kSums + k];
             out[(k / kSums) * int64_t(a.cols) + c] = t;
         }
+    } else if (MODE != kRowOdd) {                  // (one by one, 32 bytes apart, took 4 us of 64 rows of 4096)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (group_in<MODE, T>(a.cols, lane, v)) {
+                float* at = out + column_of<MODE, T>(lane, v, 0);
+                store_sums(at, dgf[v]);
+                store_sums(at + a.cols, dbf[v]);
+            }
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -650,30 +671,40 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_dx_long(const __gri
     }
 }
 
-// Adds the parts in order: 32 columns to a CTA, 32 threads to a column, then
-// their sums along a fixed tree.
+// Adds the parts in order: 32 columns to a CTA, 16 threads to a column, then
+// their sums along a fixed tree.  (32 threads: 512 x 4096 12.8 us instead of 8.4, more
+// of 12000 columns 2 us more; 16384 x 4096 0.7 less.)
 struct NormSumArgs {
     const float* part;
     void* out[2];                  // dgain, dbias (either may be NULL)
     int32_t parts, cols, f32, add;
 };
-__global__ void __launch_bounds__(1024) k_layer_norm_sums(const __grid_constant__ NormSumArgs a) {
-    __shared__ float sh[32][33];
+constexpr int kSumRows = 16;
+__global__ void __launch_bounds__(32 * kSumRows) k_layer_norm_sums(const __grid_constant__ NormSumArgs a) {
+    __shared__ float sh[kSumRows][33];
     pdl_enter();
     const int64_t c = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31);
     const int which = blockIdx.y, row = int(threadIdx.x >> 5);
     if (!a.out[which]) return;
+    constexpr int kFly = 8;                        // loads in flight
     float s = 0.0f;
     if (c < a.cols)
-#pragma unroll 4
-        for (int p = row; p < a.parts; p += 32) s += __ldcg(a.part + (int64_t(p) * 2 + which) * a.cols + c);
+        for (int p = row; p < a.parts; p += kSumRows * kFly) {
+            float t[kFly];
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+                t[u] = p + kSumRows * u < a.parts ? __ldcg(a.part + (int64_t(p + kSumRows * u) * 2 + which) * a.cols + c) : 0.0f;
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) s += t[u];
+        }
     sh[row][threadIdx.x & 31] = s;
     __syncthreads();
-    s = sh[threadIdx.x & 31][row];                 // warp `row` adds column `row`
+    const int part = int(threadIdx.x) % kSumRows;      // kSumRows neighbouring threads add up a column
+    s = sh[part][threadIdx.x / kSumRows];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const int64_t mine = int64_t(blockIdx.x) * 32 + row;
-    if ((threadIdx.x & 31) != 0 || mine >= a.cols) return;
+    for (int o = kSumRows / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int64_t mine = int64_t(blockIdx.x) * 32 + threadIdx.x / kSumRows;
+    if (part != 0 || mine >= a.cols) return;
     if (a.f32) {
         float* p = static_cast<float*>(a.out[which]) + mine;
         *p = a.add ? *p + s : s;
@@ -700,11 +731,20 @@ static int norm_pointer(const void* p, int32_t dtype, bool may_be_null, const ch
     return DPG_OK;
 }
 
-// CTAs of a backward pass, which leave as many parts: one for 1, 8, ... rows
-static int norm_parts(int64_t rows, int64_t cols) {
+// CTAs of a backward pass, which leave as many parts: as many as the SMs hold at a
+// time.  With sums and few rows fewer: a part costs 16 bytes a column (written, and
+// read again), a CTA's next row a latency and its own bytes; both sums are equal at
+// the root of rows (110000 / cols + 20) parts (512 x 4096: 152 parts 7.8 us, 456 parts
+// 12.8 with sums, 4.7 and 3.4 without).  And no more than leave the same number of
+// rows to the longest.
+static int norm_parts(int64_t rows, int64_t cols, bool f32, bool sums) {
     const int64_t groups = cols <= 768 ? (rows + 7) / 8 : rows;
-    const int64_t most = cols > 768 && cols <= 2048 ? 4 * kNormSms : cols > 2048 && cols <= 4096 ? 3 * kNormSms : 2 * kNormSms;
-    return int(groups < 1 ? 1 : groups < most ? groups : most);
+    const int64_t held = cols <= 768 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? (f32 ? 2 : 3) : cols <= 8192 ? (f32 ? 1 : 2)
+                         : cols <= 16384 ? 1 : 2;
+    const int64_t root = int64_t(std::sqrt(double(groups) * (110000.0 / double(cols < 1 ? 1 : cols) + 20.0))) + 1;
+    const int64_t most = sums && root < held * kNormSms ? root : held * kNormSms;
+    const int64_t each = (groups + most - 1) / most;
+    return int(groups < 1 ? 1 : (groups + each - 1) / each);
 }
 
 template <bool F32, int MODE, int T, int V>
@@ -796,8 +836,8 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
 }
 
 int64_t dpg_layer_norm_workspace(int64_t rows, int64_t cols) {
-    if (rows < 0 || cols < 0 || rows > dpg::kNormMaxSide || cols > dpg::kNormMaxSide) return 0;
-    return int64_t(dpg::norm_parts(rows, cols)) * 2 * cols * int64_t(sizeof(float));
+    if (rows < 0 || cols <= 0 || rows > dpg::kNormMaxSide || cols > dpg::kNormMaxSide) return 0;
+    return int64_t(dpg::norm_parts(rows, cols, false, true)) * 2 * cols * int64_t(sizeof(float));
 }
 
 int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t rows, int64_t cols,
@@ -829,6 +869,7 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     if (sums && !workspace) return fail(DPG_ERR_INVALID_ARG, "%s: workspace is NULL", who);
     if (sums && !dpg::aligned(workspace, 16)) return fail(DPG_ERR_MISALIGNED, "%s: workspace misaligned", who);
     if (!sums && !dx) return DPG_OK;
+    const bool f32 = dtype == DPG_F32;
     dpg::NormBackArgs a{};
     a.dy = dy;
     a.x = x;
@@ -840,9 +881,8 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     a.rows = rows;
     a.cols = int32_t(cols);
     a.params_f32 = param_dtype == DPG_F32;
-    a.parts = dpg::norm_parts(rows, cols);
+    a.parts = dpg::norm_parts(rows, cols, f32, sums);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool f32 = dtype == DPG_F32;
     const bool vec = cols % 8 == 0 && dpg::aligned(x, 16) && dpg::aligned(dy, 16) && dpg::aligned(dx, 16) &&
                      dpg::aligned(gain, 16);
     if (cols <= 256) st = dpg::launch_back<32, 1>(a, f32, vec, s, who);
@@ -880,7 +920,7 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     t.add = accumulate != 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((cols + 31) / 32), 2);
-    cfg.blockDim = dim3(1024);
+    cfg.blockDim = dim3(32 * dpg::kSumRows);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
