@@ -13,11 +13,14 @@
 //     quotient whose x is not on it rounds to something else than m, and ties stay
 //     ties.  The product with the reciprocal alone is off by one unit for 11 of the
 //     56 borderlines, and would round those ties up.
-//   * stochastic: the place of y between the values, in codes, is min(2 y, y + 2,
-//     y / 2 + 4), and y goes up where the fraction of that place is above (2 u + 1)
-//     2^-17.  The threshold is an fp32 number, so y, the lines and a sum with 32,
-//     whose last place is 2^-18, may all be rounded up; then the place is an
-//     integer in units of 2^-18, and one less 4 u carries where it is above.
+//   * stochastic: between the values the place of y, in codes, is linear, and so are
+//     the bits of an fp32 number between powers of two.  2^-126 y has y's place in its
+//     bits, in units of 2^-22 codes: below y = 1, where the values are 0 and 1/2, it is
+//     subnormal, and those are 1/2 apart too.  y goes up where the fraction is above
+//     (2 u + 1) 2^-17, a whole number of units, so the place may be rounded up to one.
+//     That is done from below: x times the reciprocal, both rounded down, and one
+//     residual, whose product with the reciprocal is at most 2^-21 units short; x / s
+//     is on a whole number of units, or 1/15 from it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -175,12 +178,11 @@ __device__ __forceinline__ uint4 philox(uint64_t n, uint32_t side, uint2 key) {
     uint32_t x0 = uint32_t(n), x1 = uint32_t(n >> 32), x2 = side, x3 = 0, k0 = key.x, k1 = key.y;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
-        const uint32_t a = __umulhi(0xD2511F53u, x0), b = 0xD2511F53u * x0;
-        const uint32_t c = __umulhi(0xCD9E8D57u, x2), d = 0xCD9E8D57u * x2;
-        x0 = c ^ x1 ^ k0;
-        x2 = a ^ x3 ^ k1;
-        x1 = d;
-        x3 = b;
+        const uint64_t a = uint64_t(x0) * 0xD2511F53u, b = uint64_t(x2) * 0xCD9E8D57u;
+        x0 = uint32_t(b >> 32) ^ x1 ^ k0;
+        x2 = uint32_t(a >> 32) ^ x3 ^ k1;
+        x1 = uint32_t(b);
+        x3 = uint32_t(a);
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
@@ -201,7 +203,7 @@ struct BlockScale {
 };
 
 // of a block whose largest magnitude has the bits `top`; E4M3: unit = 2^-e, whole =
-// 2^e, inverses[byte] = 1 / its value, rounded to nearest
+// 2^e, inverses[byte] = 1 / its value (stochastic: rounded down)
 template <bool F32, bool MX>
 __device__ __forceinline__ BlockScale block_scale(uint32_t top, float unit, float whole, const float* inverses) {
     BlockScale b;
@@ -252,29 +254,22 @@ __device__ __forceinline__ uint64_t fma2_up(uint64_t a, uint64_t b, uint64_t c) 
     asm("fma.rp.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-// 32 + the place of y >= 0 between the values + 1 - 3 * 2^-18, rounded up to 2^-18
-__device__ __forceinline__ void places(uint64_t y, uint32_t* p) {
-    constexpr float one = 1.0f - 3.0f / 262144.0f;
-    const float2 a = halves_of(fma2_up(y, pair_of(2.0f, 2.0f), pair_of(32.0f + one, 32.0f + one)));
-    const float2 b = halves_of(fma2_up(y, pair_of(1.0f, 1.0f), pair_of(34.0f + one, 34.0f + one)));
-    const float2 c = halves_of(fma2_up(y, pair_of(0.5f, 0.5f), pair_of(36.0f + one, 36.0f + one)));
-    float x, y1;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a.x), "f"(b.x), "f"(c.x));
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(y1) : "f"(a.y), "f"(b.y), "f"(c.y));
-    p[0] = __float_as_uint(x);
-    p[1] = __float_as_uint(y1);
-}
-
-// p - 4 times the lower, the upper half of h
-__device__ __forceinline__ uint32_t less_low(uint32_t p, uint32_t h) {
-    uint32_t r;
-    asm("dp2a.lo.u32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(0x000000FC), "r"(p));
+__device__ __forceinline__ uint64_t mul2_up(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rp.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t less_high(uint32_t p, uint32_t h) {
-    uint32_t r;
-    asm("dp2a.lo.u32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(0x0000FC00), "r"(p));
+__device__ __forceinline__ uint64_t mul2_down(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// The code of a place in bits 24 .. 26, from the upper (HIGH) or lower half u of the
+// random bits: a quarter unit a step, 2^24 - 129 - 256 u more carries where the place
+// is above 64 u + 32 units.  `inverted` is the complement.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t round_place(uint32_t place, uint32_t inverted) {
+    return place * 4u + __byte_perm(inverted, 0x7Fu, HIGH ? 0x5324 : 0x5104);
 }
 
 // B elements of a block to codes, 8 to a word.  w: the elements as they are in
@@ -297,16 +292,13 @@ __device__ __forceinline__ void encode(const uint32_t* w, const BlockScale& b, u
                 widen2(SR ? w[at] & 0x7FFF7FFFu : w[at], lo, hi);
             }
             const uint64_t x = pair_of(lo, hi);
-            y[j] = mul2(x, inv);
-            if (!MX) {
-                y[j] = fma2(fma2(y[j], s, x), inv, y[j]);
-                // up, where it is not exact (what is left of x tells which)
-                if (SR) y[j] = fma2_up(fma2(y[j], s, x), inv, y[j]);
-            }
+            if (MX) y[j] = mul2(x, inv);
+            else if (SR) y[j] = mul2_down(x, inv), y[j] = fma2_up(fma2(y[j], s, x), inv, y[j]);
+            else y[j] = mul2(x, inv), y[j] = fma2(fma2(y[j], s, x), inv, y[j]);
         }
         if (SR) {
             const uint4 r = philox(n0 + g, side, key);
-            const uint32_t h[4] = {r.x, r.y, r.z, r.w};
+            const uint32_t h[4] = {~r.x, ~r.y, ~r.z, ~r.w};
             uint32_t lo, hi;                                // bytes that hold the signs in bit 7
             if (F32) {
                 const uint32_t* v = w + 8 * g;
@@ -317,18 +309,16 @@ __device__ __forceinline__ void encode(const uint32_t* w, const BlockScale& b, u
                 lo = __byte_perm(__byte_perm(v[0], v[1], 0x0051), __byte_perm(v[2], v[3], 0x0051), 0x5410);
                 hi = __byte_perm(__byte_perm(v[0], v[1], 0x0073), __byte_perm(v[2], v[3], 0x0073), 0x5410);
             }
-            uint32_t t[8];                                  // codes in bits 18 .. 20
+            uint32_t t[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t p[2];
-                places(y[j], p);
-                t[2 * j] = less_low(p[0], h[j]);
-                t[2 * j + 1] = less_high(p[1], h[j]);
+                const float2 p = halves_of(mul2_up(y[j], pair_of(0x1p-126f, 0x1p-126f)));
+                t[2 * j] = round_place<false>(__float_as_uint(p.x), h[j]);
+                t[2 * j + 1] = round_place<true>(__float_as_uint(p.y), h[j]);
             }
-            const uint32_t even = __byte_perm(__byte_perm(t[0], t[2], 0x0062), __byte_perm(t[4], t[6], 0x0062), 0x5410);
-            const uint32_t odd = __byte_perm(__byte_perm(t[1], t[3], 0x0062), __byte_perm(t[5], t[7], 0x0062), 0x5410);
-            uint32_t word = (hi & 0x80808080u) | ((lo & 0x80808080u) >> 4);
-            word |= ((even >> 2) & 0x07070707u) | ((odd << 2) & 0x70707070u);
+            const uint32_t even = __byte_perm(__byte_perm(t[0], t[2], 0x0073), __byte_perm(t[4], t[6], 0x0073), 0x5410);
+            const uint32_t odd = __byte_perm(__byte_perm(t[1], t[3], 0x0073), __byte_perm(t[5], t[7], 0x0073), 0x5410);
+            const uint32_t word = (odd * 16u + even) | (hi & 0x80808080u) | ((lo & 0x80808080u) >> 4);
             out[g] = b.bad ? 0u : word;
         } else {
             out[g] = b.bad ? 0u : nearest8(y);
@@ -366,9 +356,10 @@ struct TileOf {
     static constexpr int kBytes = kQuantTile * kPitch * 4;
     static constexpr int kPieces = F32 ? 32 : 16;          // 16-byte pieces of a row
     static constexpr int kPer = F32 ? 4 : 8;               // elements of a piece
-    // two CTAs of fp32 tiles fit an SM, four of bf16 ones (16384 x 4096 both sides 114 -> 92 us);
-    // random bits take long enough for few tiles to want the threads
-    static constexpr int kThreads = F32 || SR ? 512 : 256;
+    // Two CTAs of fp32 tiles fit an SM, four of bf16 ones (16384 x 4096 both sides 114 -> 92 us),
+    // with random bits three that have more registers (512 x 2: 152, 256 x 4: 140, 256 x 3: 141;
+    // 4096 x 1536 17.5, 20.5 and 17.1).
+    static constexpr int kThreads = F32 ? 512 : 256;
     static constexpr int kLoads = kQuantTile * kPieces / kThreads;
 };
 constexpr int kCodesPitch = 72;                            // bytes of a row's codes in shared memory
@@ -458,7 +449,7 @@ __device__ __forceinline__ uint32_t larger(uint32_t w) {
 }
 
 template <bool F32, bool MX, bool SR>
-__global__ void __launch_bounds__(TileOf<F32, SR>::kThreads, F32 || SR ? 2 : 4) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(TileOf<F32, SR>::kThreads, F32 ? 2 : SR ? 3 : 4) k_fp4_quantize(const __grid_constant__ QuantArgs a) {
     using T = TileOf<F32, SR>;
     constexpr int B = MX ? 32 : 16;                        // elements of a block
     constexpr int kBlocks = kQuantTile / B;                // blocks of a tile's row
@@ -488,7 +479,9 @@ __global__ void __launch_bounds__(TileOf<F32, SR>::kThreads, F32 || SR ? 2 : 4) 
     if (!MX) {
         __shared__ uint32_t sh[T::kThreads / 32];
         uint32_t m = 0;
-        if (tid < kInverses) inverses[tid] = tid == 0 || tid == 0x7F ? 0.0f : 1.0f / e4m3_value(tid);   // (block_max waits)
+        // (block_max waits)
+        if (tid < kInverses)
+            inverses[tid] = tid == 0 || tid == 0x7F ? 0.0f : SR ? __fdiv_rd(1.0f, e4m3_value(tid)) : 1.0f / e4m3_value(tid);
         if (a.parts) {
             if (tid < a.parts) m = __ldcg(reinterpret_cast<const uint32_t*>(a.amax) + 1 + tid);
         } else {
