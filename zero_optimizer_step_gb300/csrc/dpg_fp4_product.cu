@@ -786,7 +786,7 @@ static int encode_operand(const dpg_fp4* q, int box_rows, int box_tiles, CUtenso
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (e == CUDA_SUCCESS) {
-        // as 128-byte rows, four to a tile: boxes of one row of 1 or 2 KB took a quarter longer
+        // as 128-byte rows, four to a tile
         const int64_t tiles = fp4_tiles(q->cols, q->format);
         const cuuint64_t sdims[3] = {128, cuuint64_t(tiles) * 4, cuuint64_t((q->rows + kFp4TileRows - 1) / kFp4TileRows)};
         const cuuint64_t spitch[2] = {128, cuuint64_t(tiles) * kFp4TileBytes};
@@ -821,11 +821,14 @@ static int launch_small(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     a.tiles_c = (a.cols + COLS - 1) / COLS;
     const int64_t tiles = int64_t(a.tiles_r) * a.tiles_c;
     const int stages = (a.k + kProdDepth - 1) / kProdDepth;
-    // More CTAs share a sum while that leaves them two to an SM at most (64 tiles of k = 2048: 4
-    // parts 9.0 us, 8 parts, in two rounds, 17.5) and four stages each, of narrow tiles two (128 x
-    // 4096 x 4096: 4 parts 7.7 us, 8 parts 9.6; 64 x 4096 x 4096: 7.9 and 7.2).
-    a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= 2 * sms && stages >= (COLS == 128 ? 8 : 4) * a.split) a.split *= 2;
+    // CTAs share a sum where it is long enough for the exchange (two or more 128 columns wide cost 1
+    // to 2 us, a stage 0.2) and there is an SM for each, for clusters of eight two.  us with 1, 2, 4, 8:
+    // 512 x 2048 x 2048 5.5, 6.9, 8.6, 16.8; 1024 x 1024 x 8192 10.9, 9.6, 11.1, 19.2; 384 x 1024 x 16384
+    // 17.9, 13.0, 9.5, 11.7; 200 x 200 x 16384 17.9, 12.9, 9.4, 7.5; 64 x 4096 x 4096 8.8, 7.4, 5.9, 6.9;
+    // 8 x 14336 x 4096 6.7, 7.0, 9.9, 16.3.  Rows of C that start anywhere are written by all threads
+    // only then: 1111 x 777 x 512, added, 11.4 and 7.4.
+    const int least = COLS < 128 ? 8 : a.vec ? 16 : 2;
+    a.split = stages < least ? 1 : tiles * 8 <= sms / 2 && stages >= 16 ? 8 : tiles * 4 <= sms && stages >= 8 ? 4 : tiles * 2 <= sms ? 2 : 1;
     if (tiles * a.split > 0x7FFFFFFF) return fail(DPG_ERR_INVALID_ARG, "%s: %lld tiles", who, (long long)tiles);
     ProductMaps maps;
     int st = encode_operand(r, kRowTile, 1, &maps.codes_r, &maps.scales_r, who);
