@@ -680,7 +680,8 @@ int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, co
  *   dx = dy W       a = dy by row,       b = W by column
  *   dW = dy^T x     a = dy by column,    b = x by column
  * with c a slice of a flat gradient buffer or of an fp32 accumulator.
- * Products and sums on the tensor cores in fp32; k = 0 gives zeros (or c).
+ * Products and sums on the tensor cores in fp32; k = 0 gives zeros (or c).  An
+ * fp32 c that is added to may lose what is below 2^-126 (its values and sums).
  * Results are the same bits on every call.  c may not overlap a or b.
  * Every device-side wait is bounded (2 s); one that runs out leaves c
  * incomplete and records DPG_ERR_DEVICE_TIMEOUT for the device. */
@@ -712,8 +713,8 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
  * dgain, dbias: cols elements of grad_dtype (DPG_BF16: rounded once; DPG_F32),
  * aligned to their element, so they may be slices of a replica's flat gradient
  * buffer; accumulate != 0 (DPG_F32 only) adds to what they hold.  The sums over
- * the rows are in fp32, in an order fixed by the sizes: the same bits on every
- * call.  workspace: DEVICE memory of dpg_layer_norm_workspace(rows, cols) bytes,
+ * the rows are in fp32, in an order fixed by the sizes and types: the same bits on
+ * every call.  workspace: DEVICE memory of dpg_layer_norm_workspace(rows, cols) bytes,
  * 16-byte aligned (may be NULL if dgain and dbias are), used by one call at a time; it
  * need not be initialised.  rows = 0 gives zero sums. */
 int64_t dpg_layer_norm_workspace(int64_t rows, int64_t cols);
@@ -783,10 +784,10 @@ int dpg_debug_checks(const dpg_plan_t* plan, int32_t* built, int64_t* first_fail
 int dpg_debug_set_limit(int64_t limit);
 
 /* Test-only fault injection for the staged step (and for the next
- * orthogonalisation, whichever the thread calls first; there skip_unit is a
- * 64-deep stage of the first CTA's operands, or, whatever it is from 0 on, a
- * matrix on the Gram path lacks one exchanged value; the default bound is
- * 2 s): its next launch by the
+ * orthogonalisation or 4-bit product, whichever the thread calls first; there
+ * skip_unit is a stage of the first CTA's operands, 64 or 256 deep, or, whatever
+ * it is from 0 on, a matrix on the Gram path lacks one exchanged value; the
+ * default bound is 2 s): its next launch by the
  * calling thread never fetches unit `skip_unit` (-1: none), so the CTA
  * that owns it must run out its wait, and every wait is bounded by
  * `timeout_ns` (<= 0: the default 1 s).  Used to test the timeout path.

@@ -39,6 +39,7 @@ struct ProductArgs {
     int32_t m, n, k;
     int32_t c_f32, add;
     int32_t vec;                 // 16-byte accesses of C's rows are allowed
+    int32_t boxes;               // bulk copies too: they write whole 16-byte pieces, also at a row's end
     int32_t rows, cols;          // of the product as it is computed (its transpose if `swap`)
     int32_t tiles_r, tiles_c;
     int32_t swap;                // rows are C's columns
@@ -49,7 +50,7 @@ struct ProductArgs {
 
 struct ProductMaps {
     CUtensorMap codes_r, codes_c, scales_r, scales_c;
-    CUtensorMap result;          // C, where its rows start on 16-byte boundaries (large products)
+    CUtensorMap result;          // C, where `boxes`
 };
 
 // ---------------------------------------------------------------------------
@@ -319,7 +320,7 @@ __device__ __forceinline__ void store_columns(const ProductArgs& a, const CUtens
     if (r >= a.m || c >= a.n) return;
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = v[j] * scale.f[0] * scale.f[1];
-    if (a.vec) store_boxes(a, map, smem_u32(box), lane, r, c, v, boxes);
+    if (a.boxes) store_boxes(a, map, smem_u32(box), lane, r, c, v, boxes);
     else store_singly(a, box, lane, r, c, v);
 }
 
@@ -798,15 +799,15 @@ static int encode_operand(const dpg_fp4* q, int box_rows, int box_tiles, CUtenso
     return e == CUDA_SUCCESS ? DPG_OK : fail(DPG_ERR_CUDA, "%s: tensor map error %d", who, int(e));
 }
 
-// C in boxes of 32 rows x 64 bytes, if its rows start on 16-byte boundaries
+// C in boxes of 32 rows x 64 bytes, if its rows start and end on 16-byte boundaries
 static int encode_result(const ProductArgs& a, CUtensorMap* map, const char* who) {
-    if (!a.vec) return DPG_OK;
+    if (!a.boxes) return DPG_OK;
     EncodeTiled fn = nullptr;
     const int st = encoder(&fn, who);
     if (st != DPG_OK) return st;
     const int size = a.c_f32 ? 4 : 2;
     const cuuint64_t dims[2] = {cuuint64_t(a.n), cuuint64_t(a.m)};
-    const cuuint64_t pitch[1] = {(cuuint64_t(a.stride) * size + 15) / 16 * 16};      // (one row may have any)
+    const cuuint64_t pitch[1] = {cuuint64_t(a.stride) * size};
     const cuuint32_t box[2] = {cuuint32_t(64 / size), 32}, step[2] = {1, 1};
     const CUresult e = fn(map, a.c_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dims,
                           pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
@@ -827,7 +828,7 @@ static int launch_small(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     // 17.9, 13.0, 9.5, 11.7; 200 x 200 x 16384 17.9, 12.9, 9.4, 7.5; 64 x 4096 x 4096 8.8, 7.4, 5.9, 6.9;
     // 8 x 14336 x 4096 6.7, 7.0, 9.9, 16.3.  Rows of C that start anywhere are written by all threads
     // only then: 1111 x 777 x 512, added, 11.4 and 7.4.
-    const int least = COLS < 128 ? 8 : a.vec ? 16 : 2;
+    const int least = COLS < 128 ? 8 : a.boxes ? 16 : 2;
     a.split = stages < least ? 1 : tiles * 8 <= sms / 2 && stages >= 16 ? 8 : tiles * 4 <= sms && stages >= 8 ? 4 : tiles * 2 <= sms ? 2 : 1;
     if (tiles * a.split > 0x7FFFFFFF) return fail(DPG_ERR_INVALID_ARG, "%s: %lld tiles", who, (long long)tiles);
     ProductMaps maps;
@@ -951,6 +952,7 @@ int dpg_fp4_product(const dpg_fp4* x, const dpg_fp4* w, void* c, int32_t c_dtype
     a.c_f32 = c_dtype == DPG_F32;
     a.add = accumulate != 0;
     a.vec = dpg::aligned(c, 16) && (x->rows <= 1 || row_stride % (a.c_f32 ? 4 : 8) == 0);
+    a.boxes = a.vec && w->rows % (a.c_f32 ? 4 : 8) == 0;
     a.wait_ns = dpg::t_staged_timeout_ns > 0 ? uint64_t(dpg::t_staged_timeout_ns) : dpg::kProdWaitNs;
     a.skip = dpg::t_staged_skip;
     dpg::t_staged_skip = -1;
