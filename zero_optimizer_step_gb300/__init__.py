@@ -1111,30 +1111,32 @@ def _rows_of(x):
     return p, dt, n // cols if cols else 0, cols, index
 
 
-def _same(t, n: int, dtype: int, what: str, here: int):
-    """The pointer of a tensor (or None) of the dtype given."""
+def _same(t, n: int, dtype, what: str, here: int):
+    """The pointer of a tensor (or None) of the torch dtype given."""
     if t is None:
         return None
-    p, dt = _vector(t, n, what, here)
-    if dt != dtype:
-        raise TypeError(f"{what}: expected {'float32' if dtype == DPG_F32 else 'bfloat16'}, got {t.dtype}")
-    return p
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == here:
+        return t.data_ptr()
+    _vector(t, n, what, here)
+    raise TypeError(f"{what}: expected {str(dtype)[6:]}, got {t.dtype}")
 
 
 def dpg_layer_norm(x, gain, bias, eps: float, y, mean=None, rstd=None, stream=None):
     """y <- (x - mean) * rstd * gain + bias over the last dimension; mean and rstd
     (fp32, one a row) are kept for the backward pass."""
     px, dt, rows, cols, here = _rows_of(x)
+    f32 = _torch_dtypes()["f32"]
     pg, pd = _vector(gain, cols, "gain", here)
     if pd is None:
         pb, pd = _vector(bias, cols, "bias", here)
     else:
-        pb = _same(bias, cols, pd, "bias", here)
+        pb = _same(bias, cols, gain.dtype, "bias", here)
     _check(lib().dpg_layer_norm(px, dt, rows, cols, pg, pb, DPG_F32 if pd is None else pd, eps,
-                                _same(y, rows * cols, dt, "y", here), _same(mean, rows, DPG_F32, "mean", here),
-                                _same(rstd, rows, DPG_F32, "rstd", here), _stream(stream)))
+                                _same(y, rows * cols, x.dtype, "y", here), _same(mean, rows, f32, "mean", here),
+                                _same(rstd, rows, f32, "rstd", here), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def dpg_layer_norm_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace of a backward pass that sums gain's or bias's gradients."""
     return lib().dpg_layer_norm_workspace(rows, cols)
@@ -1145,13 +1147,13 @@ def dpg_layer_norm_backward(dy, x, gain, mean, rstd, dx=None, dgain=None, dbias=
     """dx, and the gradients of gain and bias summed over the rows (bf16 or fp32;
     accumulate: added to what fp32 ones hold).  Each may be None."""
     px, dt, rows, cols, here = _rows_of(x)
-    n = rows * cols
+    n, f32 = rows * cols, _torch_dtypes()["f32"]
     pg, pd = _vector(gain, cols, "gain", here)
     pdg, gd = _vector(dgain, cols, "dgain", here)
     if gd is None:
         pdb, gd = _vector(dbias, cols, "dbias", here)
     else:
-        pdb = _same(dbias, cols, gd, "dbias", here)
+        pdb = _same(dbias, cols, dgain.dtype, "dbias", here)
     if workspace is not None:
         need = dpg_layer_norm_workspace(rows, cols)
         if workspace.get_device() != here:
@@ -1160,9 +1162,9 @@ def dpg_layer_norm_backward(dy, x, gain, mean, rstd, dx=None, dgain=None, dbias=
             raise ValueError(f"workspace: needs {need} contiguous bytes")
         workspace = workspace.data_ptr()
     _check(lib().dpg_layer_norm_backward(
-        _same(dy, n, dt, "dy", here), px, dt, rows, cols, pg, DPG_F32 if pd is None else pd,
-        _same(mean, rows, DPG_F32, "mean", here), _same(rstd, rows, DPG_F32, "rstd", here),
-        _same(dx, n, dt, "dx", here), pdg, pdb, DPG_F32 if gd is None else gd, 1 if accumulate else 0, workspace,
+        _same(dy, n, x.dtype, "dy", here), px, dt, rows, cols, pg, DPG_F32 if pd is None else pd,
+        _same(mean, rows, f32, "mean", here), _same(rstd, rows, f32, "rstd", here),
+        _same(dx, n, x.dtype, "dx", here), pdg, pdb, DPG_F32 if gd is None else gd, 1 if accumulate else 0, workspace,
         _stream(stream)))
 
 
