@@ -28,13 +28,15 @@ def operand(rows, cols, fmt, seed):
     return q
 
 
-# the sum of a tile of 128 x 16, 32, 64 or 128 in one, two, four and eight parts; 37 and 38
-# tiles of 256 x 256, of which the second number takes pairs of CTAs; one row more than a tile
+# the sum of a tile of 128 x 16, 32, 64 or 128 in one, two, four and eight parts; 37 and 38,
+# 75 and 77 tiles of 256 x 256, of which the second numbers (38: with long sums) take pairs of
+# CTAs; one row more than a tile
 PATHS = [
     (16, 14000, 2100), (13, 4000, 4100), (16, 9000, 4100), (3, 700, 4300), (17, 4000, 2300), (32, 9000, 4000),
     (64, 9000, 4100), (33, 2300, 4096), (64, 16000, 300), (9000, 40, 4100),
     (700, 640, 1000), (1024, 896, 4200), (640, 640, 4100), (130, 200, 4352), (129, 65, 9000), (65, 129, 8193),
     (256, 9472, 300), (512, 4864, 300), (128, 9800, 300), (4864, 257, 260),
+    (256, 9472, 2100), (512, 4864, 2100), (4864, 257, 2111), (256, 19200, 130), (256, 19457, 130),
 ]
 
 

@@ -60,7 +60,10 @@ struct QuantArgs {
 // Largest finite magnitude, as the bits of an fp32 number: these order like the
 // numbers.  Every CTA leaves the one of its share behind the result's place, and
 // the CTAs of the quantisation take the largest of them: nothing to set to zero
-// before, and no atomics (9700 on one address took 12 us).
+// before, and no atomics (9700 on one address took 12 us).  A CTA of 1024 threads to
+// an SM, 128 KB of loads on their way: 25 us for 134 MB (5.3 TB/s, which read nothing
+// but new lines of HBM); with 255 CTAs of 512, of which some SMs had one and some two,
+// quantising 16384 x 4096 bf16 took 92 us instead of 82.
 // ---------------------------------------------------------------------------
 constexpr int kAmaxCtas = 152;           // a GB300's SMs
 static_assert(kAmaxCtas < DPG_FP4_AMAX_FLOATS, "room for the parts");
@@ -349,6 +352,11 @@ __device__ __forceinline__ uint32_t block_top(const uint32_t* w) {
 // 128 bytes apart, 16 warps to an SM, 68 us for 8192 x 4096 fp32 masters.)  Rows of
 // the tile are 16 bytes longer than a multiple of 128, so that neighbouring rows'
 // pieces lie in different banks.
+//
+// What bounds it: 14336 x 4096 fp32 masters to E8M0 58 us (297 MB, 5.1 TB/s); 16384 x
+// 4096 bf16 to E4M3 55 us beside the 25 of the largest magnitude, 10.6 instructions an
+// element and orientation, issued in 74 % of the cycles; stochastic 119 us, 23
+// instructions, of them 5 for random bits.
 // ---------------------------------------------------------------------------
 template <bool F32, bool SR>
 struct TileOf {
@@ -588,7 +596,9 @@ __global__ void __launch_bounds__(TileOf<F32, SR>::kThreads, F32 ? 2 : SR ? 3 : 
 // bytes of bf16, 64 of fp32, the 16 elements that lie there (fewer at a row's
 // ends); their codes, and their scales where a block ends among them, are
 // shifted into place, so rows may start anywhere.  (Pieces of 8 elements and
-// conversions one by one took 33 instructions an element.)
+// conversions one by one took 33 instructions an element.)  16384 x 4096 to bf16 takes
+// 30 us (172 MB, 5.7 TB/s), 38 with two stores of 16 bytes in place of one of 32; a
+// thread with pieces of four rows 39, and 7.7 instead of 3.8 at 4096 x 1536.
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 16;
 

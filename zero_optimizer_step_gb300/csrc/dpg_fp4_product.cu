@@ -8,6 +8,12 @@
 // a tile of 128 rows x 4 scales as it is stored (32 lanes x 16 bytes, copied to
 // the four quarters of the lanes).  Sums are fp32 in tensor memory; the matrices'
 // powers of two are applied to them at the end.
+//
+// Small products are bound by latency: 3.6 us for one tile of one stage (launch,
+// tensor maps, tensor memory, first copy, results), 0.2 us for each further stage,
+// and 1 to 2 us where CTAs exchange parts of a sum (8 x 14336 x 4096 6.7 us, 4.9 of
+// them the weight's bytes; 4096 x 2304 x 768 7.4).  Large ones by what their ring of
+// stages holds: see k_fp4_large.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -578,6 +584,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_fp4_small(const __grid_con
 // 415, two sets of a stage's scales behind them.  The next tile's products start
 // when the 96 columns that both sums have are read, which is done first.
 //
+// 8192 x 14336 x 4096 takes 155 us (6.2 PFLOP/s, 0.54 of six times the measured bf16
+// rate), 8192 x 8192 x 8192 155 to 162.  Products alone, without copies of codes, take
+// 124, copies alone 121, all but the stores 125: a stage is filled again 0.9 to 1.25
+// us after it was taken, and five stages are 0.9 us of products (four: 168, three:
+// 203).  Stages of half the depth, of which ten fit, with rows of 64 bytes: 250.
+//
 //   warp 0  copies operands     warp 1  of CTA 0: issues the products
 //   warps 2..9  store (warp w: lanes 32 (w mod 4) .., every other 32 columns)
 // ---------------------------------------------------------------------------
@@ -898,9 +910,14 @@ static int product(const dpg_fp4* x, const dpg_fp4* w, ProductArgs a, cudaStream
     a.rows = a.m;
     a.cols = a.n;
     const int few = a.m < a.n ? a.m : a.n;
-    if (few > kRowTile && large >= sms / 4) return launch_large<MX>(a, x, w, sms, s, who);
+    // Pairs where there is a tile of 256 x 256 for each, for longer sums for half of them (us with pairs
+    // and without: 2560 x 2560 x 1024, 100 tiles, 8.0 and 9.6; 1536 x 2048 x 8192, 48, 14.1 and 16.8; 2048
+    // x 2048 x 512, 64, 5.5 and 4.8; 1536 x 1536 x 4096, 36, 9.1 and 7.7).  A side of 128 or less would
+    // leave half of each such tile empty.
+    if (few > kRowTile && (large >= sms / 2 || (large >= sms / 4 && a.k > 2048))) return launch_large<MX>(a, x, w, sms, s, who);
     if (few > 64) return launch_small<MX, 128>(a, x, w, sms, s, who);
-    // the shorter side in the columns of the sums
+    // The shorter side in the columns of the sums, of which there may be 16, 32 or 64: 16 x 4096 x 4096
+    // 4.6 us, 64 rows 5.9, 128 rows, in tiles of 128 x 128, 7.1.
     a.swap = a.m < a.n;
     if (a.swap) {
         a.rows = a.n;

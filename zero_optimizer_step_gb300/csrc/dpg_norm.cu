@@ -6,7 +6,10 @@
 // backward 4 + 2.  A row is held in the registers of a warp (up to 1024
 // columns) or of a CTA (up to 32768 forward, 16384 backward), so that it is read
 // once: the mean, then the squares about it, then the result.  Longer rows are
-// read again from L2.
+// read again from L2.  16384 x 4096 bf16: forward 42 us (268 MB, 6.4 TB/s, 0.94 of the
+// copy's rate), backward 75 (403 MB, 5.4 TB/s), bound by its 25 instructions an
+// element beside the loads; 8192 x 768 4.6 and 11.3, bound by latency and, backward,
+// by the second kernel (2.6 us).
 //
 // Backward, a warp or a CTA keeps to the same columns over many rows, and adds
 // what each row gives to the gain's and the bias's gradients in registers; at
