@@ -211,3 +211,12 @@ def test_binding_refuses_what_it_can_see():
         dpg.dpg_fp4_product(q, q, x, stream=0)
     with pytest.raises(dpg.DpgError):
         dpg.Fp4(-1, 4)
+
+
+def test_buffers_are_not_replaced():
+    """The C description holds their addresses."""
+    q = dpg.Fp4(4, 40, dpg.DPG_MXFP4, device="cpu")
+    for name in ("codes", "scales", "amax"):
+        assert getattr(q.c, name) == getattr(q, name).data_ptr()
+        with pytest.raises(AttributeError):
+            setattr(q, name, getattr(q, name).clone())

@@ -956,20 +956,25 @@ class dpg_fp4(ctypes.Structure):
 
 class Fp4:
     """A rows x cols matrix of 4-bit codes with a scale to every 16 (DPG_NVFP4) or
-    32 (DPG_MXFP4) of a row: its device buffers and their C description."""
+    32 (DPG_MXFP4) of a row: its device buffers and their C description.  The
+    buffers are written in place (codes.copy_(...)), not replaced."""
 
     def __init__(self, rows: int, cols: int, format: int = DPG_NVFP4, device="cuda"):
         import torch
         codes, scales = ctypes.c_int64(), ctypes.c_int64()
         _check(lib().dpg_fp4_sizes(rows, cols, format, ctypes.byref(codes), ctypes.byref(scales)))
         self.rows, self.cols, self.format = int(rows), int(cols), int(format)
-        self.codes = torch.empty(codes.value, dtype=torch.uint8, device=device)
-        self.scales = torch.empty(scales.value, dtype=torch.uint8, device=device)
-        self.amax = torch.zeros(DPG_FP4_AMAX_FLOATS, dtype=torch.float32, device=device)
+        self._codes = torch.empty(codes.value, dtype=torch.uint8, device=device)
+        self._scales = torch.empty(scales.value, dtype=torch.uint8, device=device)
+        self._amax = torch.zeros(DPG_FP4_AMAX_FLOATS, dtype=torch.float32, device=device)
         self.c = dpg_fp4(self.codes.data_ptr(), self.scales.data_ptr(), self.amax.data_ptr(), self.rows,
                          self.cols, self.format)
         self._ref = ctypes.byref(self.c)
         self._device = self.codes.device.index if self.codes.is_cuda else None
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    amax = property(lambda self: self._amax)
 
 
 def _elsewhere(index, what: str):
