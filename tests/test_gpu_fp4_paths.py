@@ -183,3 +183,29 @@ def test_values_of_many_rows():
             np.testing.assert_array_equal(out.cpu().double().numpy(), want)
             out.fill_(9.0)
             assert (flat == 9.0).all()
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+def test_results_beyond_32_bits(pad):
+    """Offsets in C, and in a quantised and a dequantised matrix, of more than 2^31 elements."""
+    m, n, k = 66000, 32768, 64
+    a, b = operand(256, k, NV, 31), operand(n, k, NV, 32)
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    dpg.dpg_fp4_dequantize(a, x[-256:])
+    many = dpg.Fp4(m, k)
+    dpg.dpg_fp4_quantize(x, many)
+    c = torch.empty(m * (n + pad), dtype=torch.bfloat16, device="cuda").as_strided((m, n), (n + pad, 1))
+    dpg.dpg_fp4_product(many, b, c)
+    av, bv = values_of(a), values_of(b)
+    assert not c[:-256].any()
+    want = torch.from_numpy(av).cuda() @ torch.from_numpy(bv).cuda().T
+    bound = product_bound(av, bv, torch.bfloat16, want.cpu().numpy())
+    assert np.all((c[-256:].double() - want).abs().cpu().numpy() <= bound)
+    back, forth = dpg.Fp4(m, n), torch.empty_like(c)
+    dpg.dpg_fp4_quantize(c, back)
+    dpg.dpg_fp4_dequantize(back, forth)
+    few = dpg.Fp4(256, n)
+    dpg.dpg_fp4_quantize(c[-256:], few)
+    some = torch.empty(256, n, dtype=torch.bfloat16, device="cuda")
+    dpg.dpg_fp4_dequantize(few, some)
+    assert torch.equal(forth[-256:], some) and not forth[:-256].any()

@@ -50,3 +50,28 @@ def test_sums(rows, cols, offset, dtype):
     assert torch.equal(again, dgain)
     dpg.dpg_layer_norm_backward(dy, x, gain, mean, rstd, None, None, held, ws, accumulate=True)
     np.testing.assert_array_equal(held.cpu().numpy(), (dbias + 3.0).cpu().numpy())
+
+
+def test_offsets_beyond_32_bits():
+    rows, cols, last = 530000, 4096, 64
+    g = torch.Generator().manual_seed(1)
+    x, dy = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda"), torch.zeros(rows, cols, dtype=torch.bfloat16,
+                                                                                     device="cuda")
+    x[-last:] = torch.randn(last, cols, generator=g).cuda()
+    dy[-last:] = torch.randn(last, cols, generator=g).cuda()
+    out = []
+    for p, q in ((x, dy), (x[-last:], dy[-last:])):
+        y, dx, n = torch.empty_like(p), torch.empty_like(p), p.shape[0]
+        mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        dpg.dpg_layer_norm(p, None, None, 1e-5, y, mean, rstd)
+        ws = torch.empty(dpg.dpg_layer_norm_workspace(n, cols), dtype=torch.uint8, device="cuda")
+        dgain, dbias = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        dpg.dpg_layer_norm_backward(q, p, None, mean, rstd, dx, dgain, dbias, ws)
+        out.append((y, dx, dgain, dbias))
+    (y, dx, dgain, dbias), (y1, dx1, dgain1, dbias1) = out
+    assert torch.equal(y[-last:], y1) and torch.equal(dx[-last:], dx1)
+    assert not y[:-last].any() and not dx[:-last].any()
+    # 64 terms in another order each, and zeros: at most 70 roundings on either side
+    n = (x[-last:].double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for a, b, term in ((dgain, dgain1, dy[-last:].double() * n), (dbias, dbias1, dy[-last:].double())):
+        assert torch.all((a - b).abs() <= 140 * U * term.abs().sum(0))
