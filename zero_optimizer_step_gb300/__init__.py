@@ -1005,16 +1005,31 @@ def _fp4(q: Optional[Fp4], here: int, what: str):
     return q._ref
 
 
-@functools.lru_cache(maxsize=None)
-def _dtype_codes():
-    import torch
-    return {torch.bfloat16: DPG_BF16, torch.float32: DPG_F32}
+class _DtypeCodes(dict):
+    """DPG_BF16 and DPG_F32 by torch's types, None for others; filled on first use,
+    so that the package loads without torch."""
+
+    def __missing__(self, dtype):
+        import torch
+        self.update({torch.bfloat16: DPG_BF16, torch.float32: DPG_F32})
+        return self.setdefault(dtype, None)
+
+
+_code_of = _DtypeCodes()
+
+
+def _here(t, what: str) -> int:
+    """The current device, on which `t` has to be."""
+    index = t.get_device()
+    if _get_device is None or index != _get_device():
+        return _device_of(t, what)
+    return index
 
 
 def _matrix(t, what: str):
     """(pointer, dtype, rows, columns, row stride, device) of a two-dimensional
     tensor with neighbouring columns on the current device."""
-    dt = _dtype_codes().get(t.dtype)
+    dt = _code_of[t.dtype]
     if dt is None:
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
     if t.dim() != 2:
@@ -1023,7 +1038,7 @@ def _matrix(t, what: str):
     stride, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{what}: columns must be neighbours in memory")
-    return t.data_ptr(), dt, rows, cols, stride if rows > 1 else cols, _device_of(t, what)
+    return t.data_ptr(), dt, rows, cols, stride if rows > 1 else cols, _here(t, what)
 
 
 def _seed(seed, here: int):
@@ -1095,7 +1110,7 @@ def _vector(t, n: int, what: str, here: int):
     """(pointer, dtype) of a contiguous tensor of n elements, or (None, None)."""
     if t is None:
         return None, None
-    dt = _dtype_codes().get(t.dtype)
+    dt = _code_of[t.dtype]
     if dt is None:
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
@@ -1106,14 +1121,17 @@ def _vector(t, n: int, what: str, here: int):
 
 
 def _rows_of(x):
-    """(pointer, dtype, rows, columns, device) of contiguous rows on the current device."""
-    if x.dim() < 1:
+    """(pointer, dtype, rows, columns, elements, device) of contiguous rows on the current device."""
+    shape = x.shape
+    if not shape:
         raise ValueError("x: expected rows")
-    cols, n, index = x.shape[-1], x.numel(), x.get_device()
-    p, dt = _vector(x, n, "x", index)
-    if index < 0 or index != _current_device():
-        _elsewhere(index, "x")
-    return p, dt, n // cols if cols else 0, cols, index
+    dt = _code_of[x.dtype]
+    if dt is None:
+        raise TypeError(f"x: expected bfloat16 or float32, got {x.dtype}")
+    cols, n = shape[-1], x.numel()
+    if not x.is_contiguous():
+        raise ValueError(f"x: expected {n} contiguous elements")
+    return x.data_ptr(), dt, n // cols if cols else 0, cols, n, _here(x, "x")
 
 
 def _same(t, n: int, dtype, what: str, here: int):
@@ -1129,7 +1147,7 @@ def _same(t, n: int, dtype, what: str, here: int):
 def dpg_layer_norm(x, gain, bias, eps: float, y, mean=None, rstd=None, stream=None):
     """y <- (x - mean) * rstd * gain + bias over the last dimension; mean and rstd
     (fp32, one a row) are kept for the backward pass."""
-    px, dt, rows, cols, here = _rows_of(x)
+    px, dt, rows, cols, n, here = _rows_of(x)
     f32 = _torch_dtypes()["f32"]
     pg, pd = _vector(gain, cols, "gain", here)
     if pd is None:
@@ -1137,7 +1155,7 @@ def dpg_layer_norm(x, gain, bias, eps: float, y, mean=None, rstd=None, stream=No
     else:
         pb = _same(bias, cols, gain.dtype, "bias", here)
     _check(lib().dpg_layer_norm(px, dt, rows, cols, pg, pb, DPG_F32 if pd is None else pd, eps,
-                                _same(y, rows * cols, x.dtype, "y", here), _same(mean, rows, f32, "mean", here),
+                                _same(y, n, x.dtype, "y", here), _same(mean, rows, f32, "mean", here),
                                 _same(rstd, rows, f32, "rstd", here), _stream(stream)))
 
 
@@ -1151,8 +1169,8 @@ def dpg_layer_norm_backward(dy, x, gain, mean, rstd, dx=None, dgain=None, dbias=
                             accumulate: bool = False, stream=None):
     """dx, and the gradients of gain and bias summed over the rows (bf16 or fp32;
     accumulate: added to what fp32 ones hold).  Each may be None."""
-    px, dt, rows, cols, here = _rows_of(x)
-    n, f32 = rows * cols, _torch_dtypes()["f32"]
+    px, dt, rows, cols, n, here = _rows_of(x)
+    f32 = _torch_dtypes()["f32"]
     pg, pd = _vector(gain, cols, "gain", here)
     pdg, gd = _vector(dgain, cols, "dgain", here)
     if gd is None:
