@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_c
 // ---------------------------------------------------------------------------
 // Backward.  CTA p takes rows p, p + parts, ... (T = 32: its eight warps take
 // eight rows at a time).  A thread's groups of x and dy come through shared memory,
-// three rows ahead (asynchronous copies, which only the thread itself waits for):
+// one to four rows ahead (asynchronous copies, which only the thread itself waits for):
 // a second set of registers for the next row left one CTA to an SM.
 // ---------------------------------------------------------------------------
 // CTAs of 256 threads with bf16 rows take two rows at a time: one exchange of sums for both
@@ -423,9 +423,10 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_c
 template <bool F32, int MODE, int T>
 constexpr bool row_pairs() { return !F32 && MODE != kRowOdd && T == 256; }
 
-// rows ahead: 128 KB to a row of 16384 fp32 columns leave one; two CTAs fit an SM at 768
+// rows ahead: 128 KB to a row of 16384 fp32 columns leave one; two to a warp (8192 x 768 not
+// in L2 13.1 us, with three 14.1), which leave room for two CTAs of fp32 rows
 template <bool F32, int T, int V>
-constexpr int rows_ahead() { return !F32 && T == 256 ? 4 : F32 && T * V == 2048 ? 1 : F32 && T == 32 && V == 3 ? 2 : 3; }
+constexpr int rows_ahead() { return !F32 && T == 256 ? 4 : F32 && T * V == 2048 ? 1 : T == 32 ? 2 : 3; }
 
 template <bool F32, int T, int V>
 constexpr int back_smem() { return rows_ahead<F32, T, V>() * norm_threads<T>() * V * 2 * (F32 ? 32 : 16); }
