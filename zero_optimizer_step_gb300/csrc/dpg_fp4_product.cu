@@ -46,6 +46,7 @@ struct ProductArgs {
     int32_t c_f32, add;
     int32_t vec;                 // 16-byte accesses of C's rows are allowed
     int32_t boxes;               // bulk copies too: they write whole 16-byte pieces, also at a row's end
+    int32_t wide;                // 32-byte stores, of whole pieces (not where C is added to)
     int32_t rows, cols;          // of the product as it is computed (its transpose if `swap`)
     int32_t tiles_r, tiles_c;
     int32_t swap;                // rows are C's columns
@@ -320,13 +321,40 @@ __device__ __forceinline__ void store_singly(const ProductArgs& a, float* box, i
     }
 }
 
+// A lane's 32 results to its own row, 32 bytes at a time.  That each access is 32
+// lines of memory costs less than the way through shared memory, which operands and
+// products fill (8192 x 14336 x 4096 151 us, by boxes 155; 4096 x 8192 x 2048 29.2 and
+// 30.9; stores of 16 bytes were slower than boxes).
+__device__ __forceinline__ void store_wide(const ProductArgs& a, int lane, int r, int c, const float* v) {
+    if (r + lane >= a.m) return;
+    const int64_t at = int64_t(r + lane) * a.stride + c;
+    if (a.c_f32) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            F8 f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f.v[i] = v[j + i];
+            if (c + j < a.n) st_f8(static_cast<float*>(a.c) + at + j, f);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 16) {
+            const uint4 x = narrow8(v + j), y = narrow8(v + j + 8);
+            const F8 f = {{__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w),
+                           __uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w)}};
+            if (c + j < a.n) st_f8(reinterpret_cast<float*>(static_cast<__nv_bfloat16*>(a.c) + at + j), f);
+        }
+    }
+}
+
 // 32 columns of a warp's 32 rows from row r, column c on, scaled, into C
 __device__ __forceinline__ void store_columns(const ProductArgs& a, const CUtensorMap* map, const ProductScale& scale, float* box,
                                               int lane, int r, int c, float* v, uint32_t& boxes) {
     if (r >= a.m || c >= a.n) return;
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = v[j] * scale.f[0] * scale.f[1];
-    if (a.boxes) store_boxes(a, map, smem_u32(box), lane, r, c, v, boxes);
+    if (a.wide) store_wide(a, lane, r, c, v);
+    else if (a.boxes) store_boxes(a, map, smem_u32(box), lane, r, c, v, boxes);
     else store_singly(a, box, lane, r, c, v);
 }
 
@@ -815,7 +843,7 @@ static int encode_operand(const dpg_fp4* q, int box_rows, int box_tiles, CUtenso
 
 // C in boxes of 32 rows x 64 bytes, if its rows start and end on 16-byte boundaries
 static int encode_result(const ProductArgs& a, CUtensorMap* map, const char* who) {
-    if (!a.boxes) return DPG_OK;
+    if (!a.boxes || a.wide) return DPG_OK;
     EncodeTiled fn = nullptr;
     const int st = encoder(&fn, who);
     if (st != DPG_OK) return st;
@@ -972,6 +1000,8 @@ int dpg_fp4_product(const dpg_fp4* x, const dpg_fp4* w, void* c, int32_t c_dtype
     a.add = accumulate != 0;
     a.vec = dpg::aligned(c, 16) && (x->rows <= 1 || row_stride % (a.c_f32 ? 4 : 8) == 0);
     a.boxes = a.vec && w->rows % (a.c_f32 ? 4 : 8) == 0;
+    const int piece = a.c_f32 ? 8 : 16;
+    a.wide = !a.add && dpg::aligned(c, 32) && w->rows % piece == 0 && (x->rows <= 1 || row_stride % piece == 0);
     a.wait_ns = dpg::t_staged_timeout_ns > 0 ? uint64_t(dpg::t_staged_timeout_ns) : dpg::kProdWaitNs;
     a.skip = dpg::t_staged_skip;
     dpg::t_staged_skip = -1;
