@@ -12,7 +12,7 @@
 // Small products are bound by latency: 3.6 us for one tile of one stage (launch,
 // tensor maps, tensor memory, first copy, results), 0.2 us for each further stage,
 // and 1 to 2 us where CTAs exchange parts of a sum (8 x 14336 x 4096 6.7 us, 4.9 of
-// them the weight's bytes; 4096 x 2304 x 768 7.4).  Large ones by what their ring of
+// them the weight's bytes; 4096 x 2304 x 768 7.5).  Large ones by what their ring of
 // stages holds: see k_fp4_large.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -612,8 +612,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_fp4_small(const __grid_con
 // 415, two sets of a stage's scales behind them.  The next tile's products start
 // when the 96 columns that both sums have are read, which is done first.
 //
-// 8192 x 14336 x 4096 takes 155 us (6.2 PFLOP/s, 0.54 of six times the measured bf16
-// rate), 8192 x 8192 x 8192 155 to 162.  Products alone, without copies of codes, take
+// 8192 x 14336 x 4096 takes 152 us (6.3 PFLOP/s, 0.55 of six times the measured bf16
+// rate), 8192 x 8192 x 8192 152 to 160.  Products alone, without copies of codes, take
 // 124, copies alone 121 (18 TB/s into the SMs, 57 bytes a clock each), all but the
 // stores 125: a stage is filled again 0.9 to 1.25 us after it was taken, and five stages
 // are 0.9 us of products (four: 168, three: 203).  Stages of half the depth, of which
@@ -866,10 +866,10 @@ static int launch_small(ProductArgs a, const dpg_fp4* r, const dpg_fp4* c, int s
     const int stages = (a.k + kProdDepth - 1) / kProdDepth;
     // CTAs share a sum where it is long enough for the exchange (two or more 128 columns wide cost 1
     // to 2 us, a stage 0.2) and there is an SM for each, for clusters of eight two.  us with 1, 2, 4, 8:
-    // 512 x 2048 x 2048 5.5, 6.9, 8.6, 16.8; 1024 x 1024 x 8192 10.9, 9.6, 11.1, 19.2; 384 x 1024 x 16384
-    // 17.9, 13.0, 9.5, 11.7; 200 x 200 x 16384 17.9, 12.9, 9.4, 7.5; 64 x 4096 x 4096 8.8, 7.4, 5.9, 6.9;
-    // 8 x 14336 x 4096 6.7, 7.0, 9.9, 16.3.  Rows of C that start anywhere are written by all threads
-    // only then: 1111 x 777 x 512, added, 11.4 and 7.4.
+    // 512 x 2048 x 2048 4.9, 7.0, 8.6, 16.9; 1024 x 1024 x 8192 10.7, 10.2, 11.5, 19.8; 384 x 1024 x 16384
+    // 17.9, 13.3, 9.9, 12.1; 200 x 200 x 16384 18.4, 13.0, 9.3, 7.4; 64 x 4096 x 4096 8.8, 7.4, 5.9, 6.9;
+    // 8 x 14336 x 4096 6.7, 6.9, 9.9, 16.3.  Rows of C that start anywhere are written by all threads
+    // only then: 1111 x 777 x 512, added, 11.5 and 7.5.
     const int least = COLS < 128 ? 8 : a.boxes ? 16 : 2;
     a.split = stages < least ? 1 : tiles * 8 <= sms / 2 && stages >= 16 ? 8 : tiles * 4 <= sms && stages >= 8 ? 4 : tiles * 2 <= sms ? 2 : 1;
     if (tiles * a.split > 0x7FFFFFFF) return fail(DPG_ERR_INVALID_ARG, "%s: %lld tiles", who, (long long)tiles);
@@ -941,8 +941,8 @@ static int product(const dpg_fp4* x, const dpg_fp4* w, ProductArgs a, cudaStream
     a.cols = a.n;
     const int few = a.m < a.n ? a.m : a.n;
     // Pairs where there is a tile of 256 x 256 for each, for longer sums for half of them (us with pairs
-    // and without: 2560 x 2560 x 1024, 100 tiles, 8.0 and 9.6; 1536 x 2048 x 8192, 48, 14.1 and 16.8; 2048
-    // x 2048 x 512, 64, 5.5 and 4.8; 1536 x 1536 x 4096, 36, 9.1 and 7.7).  A side of 128 or less would
+    // and without: 2560 x 2560 x 1024, 100 tiles, 7.4 and 9.3; 1536 x 2048 x 8192, 48, 14.1 and 16.9; 2048
+    // x 2048 x 512, 64, 5.0 and 4.6; 1536 x 1536 x 4096, 36, 8.8 and 7.3).  A side of 128 or less would
     // leave half of each such tile empty.
     if (few > kRowTile && (large >= sms / 2 || (large >= sms / 4 && a.k > 2048))) return launch_large<MX>(a, x, w, sms, s, who);
     if (few > 64) return launch_small<MX, 128>(a, x, w, sms, s, who);
