@@ -684,11 +684,13 @@ int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, co
  * fp32 c that is added to may lose what is below 2^-126 (its values and sums).
  * Results are the same bits on every call.  c may not overlap a or b.
  * Every device-side wait is bounded (2 s); one that runs out leaves c
- * incomplete and records DPG_ERR_DEVICE_TIMEOUT for the device. */
+ * incomplete and is counted on the device (see dpg_fp4_status). */
 int dpg_fp4_product(const dpg_fp4* a, const dpg_fp4* b, void* c, int32_t c_dtype,
                     int64_t row_stride, int32_t accumulate, void* stream);
-/* Synchronises `stream` and returns the current device's record of such a wait
- * (DPG_OK if there is none), clearing it. */
+/* Synchronises `stream` and returns DPG_ERR_DEVICE_TIMEOUT if such a wait, of this
+ * stream's products or of another's, ran out on the current device since the last
+ * call with this stream (its first: since the library was loaded), else DPG_OK.
+ * Every stream is told once; no call takes a failure from another stream. */
 int dpg_fp4_status(void* stream);
 
 /* ---------------------------------------------------------------------------

@@ -1099,7 +1099,8 @@ def dpg_fp4_product(a: Fp4, b: Fp4, out, *, accumulate: bool = False, stream=Non
 
 
 def dpg_fp4_status(stream=None):
-    """Synchronise the stream; raise DpgError if a product timed out."""
+    """Synchronise the stream; raise DpgError if a product on the device, of this
+    stream or of another, timed out since this stream last asked."""
     _check(lib().dpg_fp4_status(_stream(stream)))
 
 

@@ -20,6 +20,10 @@
 
 #include <cstdint>
 #include <cstring>
+#include <exception>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "dpg_async.cuh"
 #include "dpg_fp4.h"
@@ -34,8 +38,10 @@ constexpr int kStoreBytes = 4096;                // of a storing warp: two boxes
 constexpr int kScaleBytes = 2048;                // room for the scales of 128 rows in a stage
 constexpr uint64_t kProdWaitNs = 2000000000ull;  // bound of every wait, unless a test sets another
 
-// 0, or the error of the first wait that ran out on this device
-__device__ int32_t g_fp4_status;
+// Waits that ran out on this device since the library was loaded.  It only counts
+// up: whoever asks compares it with what it saw before, so nothing that one stream
+// reads, and no failure that comes meanwhile, is lost to another.
+__device__ uint32_t g_fp4_failures;
 
 struct ProductArgs {
     void* c;
@@ -65,7 +71,7 @@ struct ProductMaps {
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void give_up(volatile int* abort) {
     *abort = 1;
-    atomicCAS(&g_fp4_status, 0, DPG_ERR_DEVICE_TIMEOUT);
+    atomicAdd(&g_fp4_failures, 1u);
 }
 // true once the phase of `parity` completed; false when the bound ran out or
 // another role of the CTA gave up
@@ -1018,16 +1024,30 @@ int dpg_fp4_product(const dpg_fp4* x, const dpg_fp4* w, void* c, int32_t c_dtype
 
 int dpg_fp4_status(void* stream) {
     dpg::clear_error();
-    using dpg::fail;
+    const char* who = "dpg_fp4_status";
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int dev = 0;
+    unsigned long long id = 0;       // of the stream: handles are used again, and one stands for each thread's own
     void* word = nullptr;
-    int32_t got = 0;
-    DPG_CUDA_TRY(cudaGetSymbolAddress(&word, dpg::g_fp4_status));
-    DPG_CUDA_TRY(cudaMemcpyAsync(&got, word, sizeof got, cudaMemcpyDeviceToHost, s));
-    DPG_CUDA_TRY(cudaMemsetAsync(word, 0, sizeof got, s));
+    uint32_t now = 0;
+    DPG_CUDA_TRY(cudaGetDevice(&dev));
+    DPG_CUDA_TRY(cudaStreamGetId(s, &id));
+    DPG_CUDA_TRY(cudaGetSymbolAddress(&word, dpg::g_fp4_failures));
+    DPG_CUDA_TRY(cudaMemcpyAsync(&now, word, sizeof now, cudaMemcpyDeviceToHost, s));
     DPG_CUDA_TRY(cudaStreamSynchronize(s));
-    if (got != 0) return fail(got, "dpg_fp4_product: a wait on the device ran out; its results are incomplete");
-    return DPG_OK;
+    if (now == 0) return DPG_OK;     // (nothing is kept for streams until a wait has run out)
+    try {
+        // what each stream was told of last
+        static std::mutex mu;
+        static std::map<std::pair<int, unsigned long long>, uint32_t> told;
+        std::lock_guard<std::mutex> g(mu);
+        uint32_t& before = told[{dev, id}];
+        if (before == now) return DPG_OK;
+        before = now;
+    } catch (const std::exception&) {
+        // no room to remember it: the stream is told again the next time
+    }
+    return fail(DPG_ERR_DEVICE_TIMEOUT, "%s: a wait of a product on the device ran out; its results are incomplete", who);
 }
 
 }  // extern "C"
