@@ -515,12 +515,13 @@ __device__ __forceinline__ void back_sums(const NormBackArgs& a, const BackRows<
     }
 }
 
-// dx = rstd g - rstd c1 - (x - mean) rstd^2 c2; `kept`: d and g hold x - mean and g
+// dx = (g - (x - mean) (rstd c2)) rstd - rstd c1; `KEPT`: d and g hold x - mean and g.  (The
+// square of rstd would leave fp32 from 1.8e19 on, where deviations are below 5e-20.)
 template <bool F32, int MODE, int T, int V, int GAIN, bool KEPT>
 __device__ __forceinline__ void back_row(const NormBackArgs& a, const BackRows<F32, MODE, T, V>& rows, int s, int lane,
                                          float mean, float rstd, float c1, float c2, uint64_t* d, uint64_t* g,
                                          unsigned char* dx) {
-    const uint64_t k1 = twice(-rstd * c1), k2 = twice(-rstd * rstd * c2), k = twice(rstd);
+    const uint64_t k1 = twice(-rstd * c1), k2 = twice(-rstd * c2), k = twice(rstd);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (!KEPT) {                               // (from shared memory again: registers hold the sums)
@@ -536,7 +537,7 @@ __device__ __forceinline__ void back_row(const NormBackArgs& a, const BackRows<F
         }
         uint64_t out[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) out[j] = fma2(g[j], k, fma2(d[j], k2, k1));
+        for (int j = 0; j < 4; ++j) out[j] = fma2(fma2(d[j], k2, g[j]), k, k1);
         store_group<F32, MODE, T>(dx, a.cols, lane, v, out);
     }
 }
