@@ -376,39 +376,52 @@ __global__ void __launch_bounds__(norm_threads<T>(), norm_ctas<F32, T, V>()) k_l
     }
 }
 
-// The same for rows of any length, read three times.
-constexpr int kLongThreads = 1024;
 __device__ __forceinline__ float load_one(const void* p, int32_t f32, int64_t i) {
-    return f32 ? *(static_cast<const volatile float*>(p) + i)
-               : __uint_as_float(uint32_t(*(static_cast<const volatile uint16_t*>(p) + i)) << 16);
+    return f32 ? static_cast<const float*>(p)[i] : __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
+}
+
+// The same for rows of any length, read three times.  A thread adds at most 128 terms in
+// fp32, and such sums in 64 bits: one chain of 2^14 equal terms is off by 1e-4 of its sum
+// (rows of 2^24 columns), since each addition to a long sum may be rounded the same way.
+constexpr int kLongThreads = 1024;
+constexpr int kChain = 128;
+template <bool F32, typename A>
+__device__ __forceinline__ float long_sum(const void* p, int64_t at, int cols, A add) {
+    double sum = 0.0;
+    for (int c = int(threadIdx.x); c < cols;) {
+        const int end = min(cols, c + kChain * kLongThreads);
+        float s = 0.0f;
+#pragma unroll 8
+        for (; c < end; c += kLongThreads) s = add(s, load_one(p, F32, at + c));
+        sum += double(s);
+    }
+    return float(sum);
 }
 __device__ __forceinline__ void store_one(void* p, int32_t f32, int64_t i, float v) {
     if (f32) static_cast<float*>(p)[i] = v;
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-__global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_constant__ NormArgs a, int32_t f32) {
+template <bool F32>
+__global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const __grid_constant__ NormArgs a) {
     __shared__ float sh[2][64];
     pdl_enter();
     const int64_t at = int64_t(blockIdx.x) * a.cols;
-    float s = 0.0f;
-    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) s += load_one(a.x, f32, at + c);
-    const float mean = row_sum<kLongThreads>(s, sh[0]) / float(a.cols);
-    s = 0.0f;
-    for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
-        const float d = load_one(a.x, f32, at + c) - mean;
-        s = fmaf(d, d, s);
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<kLongThreads>(s, sh[1]) / float(a.cols) + a.eps);
+    const auto add = [](float s, float x) { return s + x; };
+    const float sum = long_sum<F32>(a.x, at, a.cols, add);
+    const float mean = row_sum<kLongThreads>(sum, sh[0]) / float(a.cols);
+    const auto square = [mean](float s, float x) { return fmaf(x - mean, x - mean, s); };
+    const float squares = long_sum<F32>(a.x, at, a.cols, square);
+    const float rstd = 1.0f / sqrtf(row_sum<kLongThreads>(squares, sh[1]) / float(a.cols) + a.eps);
     if (threadIdx.x == 0 && a.mean) {
         a.mean[blockIdx.x] = mean;
         a.rstd[blockIdx.x] = rstd;
     }
     for (int c = int(threadIdx.x); c < a.cols; c += kLongThreads) {
-        float v = (load_one(a.x, f32, at + c) - mean) * rstd;
+        float v = (load_one(a.x, F32, at + c) - mean) * rstd;
         if (a.gain) v *= load_one(a.gain, a.params_f32, c);
         if (a.bias) v += load_one(a.bias, a.params_f32, c);
-        store_one(a.y, f32, at + c, v);
+        store_one(a.y, F32, at + c, v);
     }
 }
 
@@ -761,31 +774,46 @@ __global__ void __launch_bounds__(256) k_layer_norm_columns(const __grid_constan
 }
 
 constexpr int kDxThreads = 512;
-template <int W>
-__global__ void __launch_bounds__(kDxThreads, 3) k_layer_norm_dx_long(const __grid_constant__ NormBackArgs a, int32_t f32) {
+// a thread's sums of g and g n over a row, 128 terms in fp32 at a time as in long_sum
+template <int W, bool F32, int GAIN>
+__device__ __forceinline__ float2 dx_sums(const NormBackArgs& a, int64_t at, float mean, float rstd) {
+    double sum1 = 0.0, sum2 = 0.0;
+    for (int c = int(threadIdx.x) * W; c < a.cols;) {
+        const int end = min(a.cols, c + kChain * kDxThreads);
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll (W == 1 ? 4 : 1)
+        for (; c < end; c += kDxThreads * W) {
+            float g[W], x[W], k[W];
+            load_some<W>(a.dy, F32, at + c, g);
+            load_some<W>(a.x, F32, at + c, x);
+            if (GAIN) load_some<W>(a.gain, GAIN == 2, c, k);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if (GAIN) g[j] *= k[j];
+                s1 += g[j];
+                s2 = fmaf(g[j], (x[j] - mean) * rstd, s2);
+            }
+        }
+        sum1 += double(s1);
+        sum2 += double(s2);
+    }
+    return make_float2(float(sum1), float(sum2));
+}
+
+template <int W, bool F32>
+__global__ void __launch_bounds__(kDxThreads, F32 ? 2 : 3) k_layer_norm_dx_long(const __grid_constant__ NormBackArgs a) {
     __shared__ float sh[64];
     pdl_enter();
     const int64_t r = blockIdx.x, at = r * a.cols;
     const float mean = __ldg(a.mean + r), rstd = __ldg(a.rstd + r);
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = int64_t(threadIdx.x) * W; c < a.cols; c += kDxThreads * W) {
-        float g[W], x[W], k[W];
-        load_some<W>(a.dy, f32, at + c, g);
-        load_some<W>(a.x, f32, at + c, x);
-        if (a.gain) load_some<W>(a.gain, a.params_f32, c, k);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            if (a.gain) g[j] *= k[j];
-            s1 += g[j];
-            s2 = fmaf(g[j], (x[j] - mean) * rstd, s2);
-        }
-    }
-    const float2 t = row_sums<kDxThreads>(s1, s2, sh);
+    float2 t = !a.gain ? dx_sums<W, F32, 0>(a, at, mean, rstd) : a.params_f32 ? dx_sums<W, F32, 2>(a, at, mean, rstd)
+                                                                              : dx_sums<W, F32, 1>(a, at, mean, rstd);
+    t = row_sums<kDxThreads>(t.x, t.y, sh);
     const float c1 = t.x / float(a.cols), c2 = t.y / float(a.cols);
     for (int64_t c = int64_t(threadIdx.x) * W; c < a.cols; c += kDxThreads * W) {
         float g[W], x[W], k[W];
-        load_some<W>(a.dy, f32, at + c, g);
-        load_some<W>(a.x, f32, at + c, x);
+        load_some<W>(a.dy, F32, at + c, g);
+        load_some<W>(a.x, F32, at + c, x);
         if (a.gain) load_some<W>(a.gain, a.params_f32, c, k);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -793,8 +821,8 @@ __global__ void __launch_bounds__(kDxThreads, 3) k_layer_norm_dx_long(const __gr
             g[j] = rstd * (g[j] - c1 - (x[j] - mean) * rstd * c2);
         }
         if constexpr (W == 1) {
-            store_one(a.dx, f32, at + c, g[0]);
-        } else if (f32) {
+            store_one(a.dx, F32, at + c, g[0]);
+        } else if constexpr (F32) {
             float* to = static_cast<float*>(a.dx) + at + c;
             *reinterpret_cast<float4*>(to) = make_float4(g[0], g[1], g[2], g[3]);
             *reinterpret_cast<float4*>(to + 4) = make_float4(g[4], g[5], g[6], g[7]);
@@ -965,7 +993,8 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
     if (cols <= 8192) return dpg::launch_norm<256, 4>(a, f32, vec, s, who);
     if (cols <= 16384) return dpg::launch_norm<512, 4>(a, f32, vec, s, who);
     if (cols <= 32768) return dpg::launch_norm<1024, 4>(a, f32, vec, s, who);
-    return dpg::launch_k(dpg::k_layer_norm_long, unsigned(rows), dpg::kLongThreads, s, who, a, int32_t(f32));
+    return dpg::launch_k(f32 ? dpg::k_layer_norm_long<true> : dpg::k_layer_norm_long<false>, unsigned(rows), dpg::kLongThreads, s,
+                         who, a);
 }
 
 int64_t dpg_layer_norm_workspace(int64_t rows, int64_t cols) {
@@ -1040,8 +1069,11 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
             }
             st = dpg::after_launch(who);
         }
-        if (st == DPG_OK && dx && rows > 0)
-            st = dpg::launch_k(vec ? dpg::k_layer_norm_dx_long<8> : dpg::k_layer_norm_dx_long<1>, unsigned(rows), dpg::kDxThreads, s, who, a, int32_t(f32));
+        if (st == DPG_OK && dx && rows > 0) {
+            auto k = f32 ? (vec ? dpg::k_layer_norm_dx_long<8, true> : dpg::k_layer_norm_dx_long<1, true>)
+                         : (vec ? dpg::k_layer_norm_dx_long<8, false> : dpg::k_layer_norm_dx_long<1, false>);
+            st = dpg::launch_k(k, unsigned(rows), dpg::kDxThreads, s, who, a);
+        }
     }
     if (st != DPG_OK || !sums) return st;
     dpg::NormSumArgs t{};
