@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -835,12 +836,15 @@ __global__ void __launch_bounds__(kDxThreads, F32 ? 2 : 3) k_layer_norm_dx_long(
 // Adds the parts in order: 32 columns to a CTA, 16 threads to a column, then
 // their sums along a fixed tree.  (32 threads: 512 x 4096 12.8 us instead of 8.4, more
 // of 12000 columns 2 us more; 16384 x 4096 0.7 less.)
+// MANY (more than 4096 parts): no chain is longer than 256 of them; to look for the end of one
+// costs few parts 2 us (8192 x 768 19.5 -> 21.5 us with the rows' kernel).
 struct NormSumArgs {
     const float* part;
     void* out[2];                  // dgain, dbias (either may be NULL)
     int32_t parts, cols, f32, add;
 };
 constexpr int kSumRows = 16;
+template <bool MANY>
 __global__ void __launch_bounds__(32 * kSumRows) k_layer_norm_sums(const __grid_constant__ NormSumArgs a) {
     __shared__ float sh[kSumRows][33];
     pdl_enter();
@@ -848,7 +852,8 @@ __global__ void __launch_bounds__(32 * kSumRows) k_layer_norm_sums(const __grid_
     const int which = blockIdx.y, row = int(threadIdx.x >> 5);
     if (!a.out[which]) return;
     constexpr int kFly = 8;                        // loads in flight
-    float s = 0.0f;
+    float s = 0.0f, before = 0.0f;
+    int n = 0;
     if (c < a.cols)
         for (int p = row; p < a.parts; p += kSumRows * kFly) {
             float t[kFly];
@@ -857,7 +862,13 @@ __global__ void __launch_bounds__(32 * kSumRows) k_layer_norm_sums(const __grid_
                 t[u] = p + kSumRows * u < a.parts ? __ldcg(a.part + (int64_t(p + kSumRows * u) * 2 + which) * a.cols + c) : 0.0f;
 #pragma unroll
             for (int u = 0; u < kFly; ++u) s += t[u];
+            if (MANY && ++n == 256 / kFly) {
+                before += s;
+                s = 0.0f;
+                n = 0;
+            }
         }
+    if (MANY) s += before;
     sh[row][threadIdx.x & 31] = s;
     __syncthreads();
     const int part = int(threadIdx.x) % kSumRows;      // kSumRows neighbouring threads add up a column
@@ -897,13 +908,17 @@ static int norm_pointer(const void* p, int32_t dtype, bool may_be_null, const ch
 // read again), a CTA's next row a latency and its own bytes; both sums are equal at
 // the root of rows (110000 / cols + 20) parts (512 x 4096: 152 parts 7.8 us, 456 parts
 // 12.8 with sums, 4.7 and 3.4 without).  And no more than leave the same number of
-// rows to the longest.
+// rows to the longest.  With so many rows that a thread would add more than kPartRows
+// terms in one fp32 chain, each of which may be rounded the same way (16M rows of 8: 7e-5
+// of the sum), twice as many parts, three times as many, ...
+constexpr int64_t kPartRows = 1024;
 static int norm_parts(int64_t rows, int64_t cols, bool f32, bool sums) {
     const int64_t groups = cols <= 768 ? (rows + 7) / 8 : rows;
     const int64_t held = cols <= 768 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? (f32 ? 2 : 3) : cols <= 8192 ? (f32 ? 1 : 2)
                          : cols <= 16384 ? 1 : 2;
     const int64_t root = int64_t(std::sqrt(double(groups) * (110000.0 / double(cols < 1 ? 1 : cols) + 20.0))) + 1;
-    const int64_t most = sums && root < held * kNormSms ? root : held * kNormSms;
+    int64_t most = sums && root < held * kNormSms ? root : held * kNormSms;
+    if (sums && groups > most * kPartRows) most *= (groups + most * kPartRows - 1) / (most * kPartRows);
     const int64_t each = (groups + most - 1) / most;
     return int(groups < 1 ? 1 : (groups + each - 1) / each);
 }
@@ -999,7 +1014,9 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
 
 int64_t dpg_layer_norm_workspace(int64_t rows, int64_t cols) {
     if (rows < 0 || cols <= 0 || rows > dpg::kNormMaxSide || cols > dpg::kNormMaxSide) return 0;
-    return int64_t(dpg::norm_parts(rows, cols, false, true)) * 2 * cols * int64_t(sizeof(float));
+    // of the type that needs more: with many rows fp32, of which an SM holds fewer, may take more parts
+    const int parts = std::max(dpg::norm_parts(rows, cols, false, true), dpg::norm_parts(rows, cols, true, true));
+    return int64_t(parts) * 2 * cols * int64_t(sizeof(float));
 }
 
 int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t rows, int64_t cols,
@@ -1093,7 +1110,7 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = dpg::t_programmatic ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, dpg::k_layer_norm_sums, t);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, a.parts > 256 * dpg::kSumRows ? dpg::k_layer_norm_sums<true> : dpg::k_layer_norm_sums<false>, t);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return fail(DPG_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
