@@ -605,7 +605,12 @@ int dpg_muon_step(const dpg_plan_t* plan, dpg_matrices_t* mats, const void* cons
  *   DPG_MXFP4  32 elements to an E8M0 scale: value = scale * code
  * with codes E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign; an element that is -0
  * may have either zero's code).  Values are exact in
- * bf16 and fp32 down to their subnormal numbers.
+ * bf16 and fp32 down to their subnormal numbers, and below 2^128.  Few blocks hold
+ * larger ones: where the largest magnitude is above 1.5 * 2^127 = 2.55e38 (E8M0) or
+ * 1.875 * 2^127 = 3.19e38 (E4M3), elements above 3 * 2^126 = 2.55e38, or 1.375 * 2^127
+ * = 2.34e38, may go up to a value of 2^128 or more (to nearest: from 3.5 * 2^126 =
+ * 2.98e38 on, or above 1.71875 * 2^127 = 2.92e38), which dpg_fp4_dequantize writes as
+ * an infinity.
  * A block's scale is the least of its type with max|x| <= 6 * scale * 2^e, so
  * no element saturates; e is the least with amax <= 6 * 448 * 2^e and e >=
  * -126, amax the largest finite |x| of the matrix.  A block that holds a NaN
