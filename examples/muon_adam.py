@@ -112,17 +112,18 @@ def main(fp4=False):
     if fp4:
         rows, cols = [dpg.Fp4(h, d), dpg.Fp4(d, h)], [dpg.Fp4(d, h), dpg.Fp4(h, d)]
         dpg.dpg_allgather_params_fp4(shapes, matrices.master, rows, cols)
-        seed = torch.zeros(1, dtype=torch.int64, device="cuda")
+        # each layer's own, far from the other's: equal seeds would give their gradients equal bits
+        seeds = torch.arange(2, dtype=torch.int64, device="cuda") << 32
 
     for t in range(1, STEPS + 1):
         total = 0.0
         for r in range(R):                              # a replica's share of the batch
             x = torch.randn(BATCH, d, device="cuda")
             if fp4:
-                seed += 1
+                seeds += 1
                 n = Norm.apply(x.to(torch.bfloat16).requires_grad_(), *norm, vectors.slot(2, r), vectors.slot(3, r))
-                a = F.gelu(Linear4.apply(n, (rows[0], cols[0]), matrices.slot(0, r), seed) + bias)
-                y = Linear4.apply(a, (rows[1], cols[1]), matrices.slot(1, r), seed) * gain
+                a = F.gelu(Linear4.apply(n, (rows[0], cols[0]), matrices.slot(0, r), seeds[:1]) + bias)
+                y = Linear4.apply(a, (rows[1], cols[1]), matrices.slot(1, r), seeds[1:]) * gain
             else:
                 y = F.gelu(x.to(torch.bfloat16) @ w1.t() + bias) @ w2.t() * gain
             loss = (y.float() - torch.tanh(x @ target)).square().sum(1).sum()   # sums: the step divides

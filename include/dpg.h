@@ -657,6 +657,7 @@ int dpg_fp4_sizes(int64_t rows, int64_t cols, int32_t format, int64_t* code_byte
  *   with the seed as key and counter {n mod 2^32, n / 2^32, side, 0}, n = r *
  *   ceil(cols / 8) + c / 8 in the quantised matrix's own rows and columns, half
  *   word c mod 8 (low halves first), side 0 for by_row and 1 for by_col.
+ *   Equal seeds give any two matrices the same bits: give each one its own.
  * Results are the same bits on every call. */
 int dpg_fp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
                      int64_t row_stride, const int64_t* seed, const dpg_fp4* by_row,
@@ -672,7 +673,8 @@ int dpg_fp4_dequantize(const dpg_fp4* q, void* out, int32_t out_dtype, int64_t r
  * matrices of a stack, from its place in the flat fp32 masters.  by_row and
  * by_col: HOST arrays of n = the object's number of matrices, either may be
  * NULL, not both; entry k must have matrix k's rows and cols (by_col: cols and
- * rows).  seed as in dpg_fp4_quantize; matrix k takes the seed plus k.  All
+ * rows).  seed as in dpg_fp4_quantize; matrix k takes the seed plus k, so the seeds
+ * of two calls have to be n or more apart, or matrices share random bits.  All
  * arguments are checked before anything is launched. */
 int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, const int64_t* seed,
                              const dpg_fp4* by_row, const dpg_fp4* by_col, int32_t n, void* stream);

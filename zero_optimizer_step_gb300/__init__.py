@@ -1056,7 +1056,8 @@ def _seed(seed, here: int):
 def dpg_fp4_quantize(x, by_row: Optional[Fp4] = None, by_col: Optional[Fp4] = None, *, seed=None,
                      stream=None):
     """by_row <- x (bf16 or fp32 matrix), by_col <- its transpose, each in blocks
-    along its own rows; nearest values, or stochastic ones with a seed."""
+    along its own rows; nearest values, or stochastic ones with a seed (equal seeds
+    give any two matrices the same random bits)."""
     p, dt, rows, cols, stride, here = _matrix(x, "x")
     _check(lib().dpg_fp4_quantize(p, dt, rows, cols, stride, _seed(seed, here), _fp4(by_row, here, "by_row"),
                                   _fp4(by_col, here, "by_col"), _stream(stream)))
@@ -1073,7 +1074,8 @@ def dpg_fp4_dequantize(q: Fp4, out, stream=None):
 def dpg_allgather_params_fp4(mats: Matrices, master: Ptr, by_row: Optional[Sequence[Fp4]] = None,
                              by_col: Optional[Sequence[Fp4]] = None, *, seed=None, stream=None):
     """The 4-bit form of every matrix of a plan, in the order of its parameters,
-    from the flat fp32 masters; by_col holds the transposes."""
+    from the flat fp32 masters; by_col holds the transposes.  Matrix k takes the seed
+    plus k: seeds of two calls are to be as far apart as there are matrices."""
     _need(master, "f32", mats.total_padded, "master")
     here = _current_device() if master is None or isinstance(master, int) else _device_of(master, "master")
     arrays = []
