@@ -710,7 +710,8 @@ int dpg_fp4_status(void* stream);
  *   n = (x - mean_r) * rstd_r,  y = n * gain + bias
  * in fp32, y rounded once.  gain may be NULL (ones), bias may be NULL (zeros).
  * mean, rstd: `rows` floats, written for the backward pass; both NULL: not kept.
- * y may be x.  eps: finite, >= 0.
+ * y may be x.  eps: 0, or a positive number that fp32 holds.  The squares' sum is in
+ * fp32 too: a row whose is infinite (deviations beyond 1.8e19 / sqrt(cols)) has rstd 0.
  * ------------------------------------------------------------------------- */
 int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, const void* gain,
                    const void* bias, int32_t param_dtype, double eps, void* y, float* mean,

@@ -973,7 +973,9 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
     const dpg::Trace trace(who);
     int st = dpg::norm_shape(rows, cols, dtype, param_dtype, who);
     if (st != DPG_OK) return st;
-    if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(DPG_ERR_INVALID_ARG, "%s: eps %g", who, eps);
+    // (not one that fp32 makes an infinity or a zero of)
+    if (!(eps >= 0.0) || !std::isfinite(float(eps)) || (eps > 0.0 && float(eps) == 0.0f))
+        return fail(DPG_ERR_INVALID_ARG, "%s: eps %g", who, eps);
     if ((mean == nullptr) != (rstd == nullptr))
         return fail(DPG_ERR_INVALID_ARG, "%s: mean and rstd are kept together", who);
     if (rows == 0 || cols == 0) return DPG_OK;
