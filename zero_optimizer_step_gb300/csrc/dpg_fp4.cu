@@ -24,8 +24,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <exception>
+#include <vector>
 
 #include "dpg_async.cuh"
 #include "dpg_fp4.h"
@@ -799,6 +802,39 @@ static int quant_args(const void* x, int32_t dtype, int64_t rows, int64_t cols, 
     return DPG_OK;
 }
 
+// Whether every buffer of n matrices lies apart from the others: a matrix quantised
+// later would take the place of an earlier one's. (One matrix's two forms may have one
+// amax: it is the same number.)
+static int fp4_apart(const dpg_fp4* by_row, const dpg_fp4* by_col, int32_t n, const char* who) {
+    struct Span {
+        uintptr_t at, end;
+        int32_t amax_of;               // -1: codes or scales
+    };
+    try {
+        std::vector<Span> spans;
+        spans.reserve(size_t(n) * 6);
+        for (const dpg_fp4* side : {by_row, by_col})
+            for (int32_t k = 0; side && k < n; ++k) {
+                const dpg_fp4& q = side[k];
+                const uintptr_t codes = reinterpret_cast<uintptr_t>(q.codes), scales = reinterpret_cast<uintptr_t>(q.scales),
+                                amax = reinterpret_cast<uintptr_t>(q.amax);
+                spans.push_back({codes, codes + uintptr_t(q.rows * fp4_pitch(q.cols)), -1});
+                spans.push_back({scales, scales + uintptr_t((q.rows + kFp4TileRows - 1) / kFp4TileRows *
+                                                            fp4_tiles(q.cols, q.format) * kFp4TileBytes), -1});
+                if (q.format == DPG_NVFP4) spans.push_back({amax, amax + DPG_FP4_AMAX_FLOATS * sizeof(float), k});
+            }
+        std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.at < b.at; });
+        for (size_t i = 1; i < spans.size(); ++i) {
+            const Span &a = spans[i - 1], &b = spans[i];
+            if (b.at < a.end && !(a.at == b.at && a.amax_of >= 0 && a.amax_of == b.amax_of))
+                return fail(DPG_ERR_INVALID_ARG, "%s: two of the 4-bit matrices share a buffer", who);
+        }
+    } catch (const std::exception&) {
+        return fail(DPG_ERR_OOM, "%s: out of host memory", who);
+    }
+    return DPG_OK;
+}
+
 template <bool F32, bool MX, bool SR>
 static int launch_quant(const QuantArgs& a, int64_t tiles, cudaStream_t s, const char* who) {
     auto k = k_fp4_quantize<F32, MX, SR>;
@@ -938,6 +974,10 @@ int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, co
     if (!dpg::aligned(master, 32)) return fail(DPG_ERR_MISALIGNED, "%s: master misaligned", who);
     if (seed && !dpg::aligned(seed, 8)) return fail(DPG_ERR_MISALIGNED, "%s: seed misaligned", who);
     for (int pass = 0; pass < 2; ++pass) {               // all are checked before the first is launched
+        if (pass == 1) {
+            const int st = dpg::fp4_apart(by_row, by_col, n, who);
+            if (st != DPG_OK) return st;
+        }
         int32_t k = 0;
         for (int32_t q = 0; q < m.n_params; ++q) {
             const int64_t r = m.rows[size_t(q)], c = m.cols[size_t(q)];
