@@ -472,8 +472,10 @@ __device__ __forceinline__ void join_columns(const ProductArgs& a, const Product
 }
 template <int COLS, int SPLIT>
 __device__ __forceinline__ void join_parts(const ProductArgs& a, const ProductScale& scale, uint32_t part, int rank, int r0, int c0) {
-    if (a.swap) join_columns<COLS, SPLIT>(a, scale, part, rank, r0, c0);
-    else join_rows<COLS, SPLIT>(a, scale, part, rank, r0, c0);
+    if constexpr (COLS < 128) {                             // (128: never swapped, see product)
+        if (a.swap) return join_columns<COLS, SPLIT>(a, scale, part, rank, r0, c0);
+    }
+    join_rows<COLS, SPLIT>(a, scale, part, rank, r0, c0);
 }
 
 template <bool MX, int COLS>
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_fp4_small(const __grid_con
                 for (int c = 0; c < COLS; c += 32) {
                     float v[32];
                     load_acc32(sums + c, v);                // (COLS = 16: with 16 unused columns)
-                    if (a.swap) {
+                    if (COLS < 128 && a.swap) {
 #pragma unroll
                         for (int j = 0; j < kGroup; ++j) part[(c + j) * kRowTile + row] = v[j];
                     } else {
