@@ -689,7 +689,8 @@ int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, co
  * with c a slice of a flat gradient buffer or of an fp32 accumulator.
  * Products and sums on the tensor cores in fp32; k = 0 gives zeros (or c).  An
  * fp32 c that is added to may lose what is below 2^-126 (its values and sums).
- * Results are the same bits on every call.  c may not overlap a or b.
+ * Results are the same bits on every call on devices with as many SMs, by which
+ * sums are shared out.  c may not overlap a or b.
  * Every device-side wait is bounded (2 s); one that runs out leaves c
  * incomplete and is counted on the device (see dpg_fp4_status). */
 int dpg_fp4_product(const dpg_fp4* a, const dpg_fp4* b, void* c, int32_t c_dtype,

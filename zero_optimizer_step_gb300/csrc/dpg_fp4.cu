@@ -357,9 +357,11 @@ __device__ __forceinline__ uint32_t block_top(const uint32_t* w) {
 // pieces lie in different banks.
 //
 // What bounds it: 14336 x 4096 fp32 masters to E8M0 58 us (297 MB, 5.1 TB/s); 16384 x
-// 4096 bf16 to E4M3 55 us beside the 25 of the largest magnitude, 10.6 instructions an
+// 4096 bf16 to E4M3 55 us beside the 25 of the largest magnitude, 11.4 instructions an
 // element and orientation, issued in 74 % of the cycles; stochastic 119 us, 23
-// instructions, of them 5 for random bits.
+// instructions, of them 5 for random bits.  bf16 to E8M0 41 us, its bytes 30; the fp32
+// masters to E4M3 114 us, read twice for the largest magnitude, where the bytes of one reading
+// would take 44.
 // ---------------------------------------------------------------------------
 template <bool F32, bool SR>
 struct TileOf {

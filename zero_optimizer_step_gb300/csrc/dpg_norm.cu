@@ -3,13 +3,17 @@
 // dpg_layer_norm_backward in include/dpg.h).
 //
 // Both passes are streams of HBM traffic: forward 2 + 2 bytes per bf16 element,
-// backward 4 + 2.  A row is held in the registers of a warp (up to 1024
-// columns) or of a CTA (up to 32768 forward, 16384 backward), so that it is read
-// once: the mean, then the squares about it, then the result.  Longer rows are
-// read again from L2.  16384 x 4096 bf16: forward 42 us (268 MB, 6.4 TB/s, 0.94 of the
-// copy's rate), backward 75 (403 MB, 5.4 TB/s), bound by its 25 instructions an
-// element beside the loads; 8192 x 768 4.6 and 11.3, bound by latency and, backward,
-// by the second kernel (2.6 us).
+// backward 4 + 2.  Forward, a row is held in the registers of a warp (up to 1024
+// columns) or of a CTA (up to 32768), so that it is read once: the mean, then the squares
+// about it, then the result.  Backward, the rows of a warp (up to 768 columns) or of a CTA
+// (up to 16384) lie in shared memory, where they are read twice; registers hold the sums
+// over the rows.  Longer rows are read again from L2.  16384 x 4096 bf16: forward 42 us (268
+// MB, 6.4 TB/s, 0.94 of the copy's rate), backward 75 (403 MB, 5.4 TB/s), bound by its 25
+// instructions an element beside the loads; 8192 x 768 6.4 and 14 to 15.5 (4.6 and 11.3 in a
+// loop over one set of rows, which lie in L2), bound by latency and, backward, by the second
+// kernel (2.6 us).  Widths that are no multiple of 8 are moved element by element: 9000 x 771
+// 14.6 and 26.6, where the bytes would take 4.1 and 6.1.  fp32 16384 x 4096: 102 and 219, of
+// 79 and 119.
 //
 // Backward, a warp or a CTA keeps to the same columns over many rows, and adds
 // what each row gives to the gain's and the bias's gradients in registers; at
@@ -744,7 +748,7 @@ __device__ __forceinline__ void load_some(const void* p, int32_t f32, int64_t i,
 
 // Rows of any length: first the sums, CTA (columns, part) over rows part,
 // part + parts, ...; then dx, which may take the place of dy or x.  W: neighbouring
-// columns to a thread (4000 x 20000 bf16 238 us with eight; 365 with one and rows on 1024
+// columns to a thread (4000 x 20000 bf16, both kernels, 210 us with eight; 365 with one and rows on 1024
 // threads, of which one CTA fits an SM).
 template <int W>
 __global__ void __launch_bounds__(256) k_layer_norm_columns(const __grid_constant__ NormBackArgs a, int32_t f32) {
