@@ -710,7 +710,7 @@ int dpg_fp4_status(void* stream);
  *   mean_r = sum_c x / cols,  rstd_r = 1 / sqrt(sum_c (x - mean_r)^2 / cols + eps)
  *   n = (x - mean_r) * rstd_r,  y = n * gain + bias
  * in fp32, y rounded once.  gain may be NULL (ones), bias may be NULL (zeros).
- * mean, rstd: `rows` floats, written for the backward pass; both NULL: not kept.
+ * mean, rstd: `rows` floats each, written for the backward pass; both NULL: not kept.
  * y may be x.  eps: 0, or a positive number that fp32 holds.  The squares' sum is in
  * fp32 too: a row whose is infinite (deviations beyond 1.8e19 / sqrt(cols)) has rstd 0.
  * ------------------------------------------------------------------------- */
@@ -721,7 +721,7 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
  *   dx = rstd_r * (g - sum_c g / cols - n * sum_c (g * n) / cols)
  *   dgain_c = sum_r dy * n,  dbias_c = sum_r dy
  * each of dx, dgain, dbias may be NULL (not computed); dx may be dy or x.
- * dgain, dbias: cols elements of grad_dtype (DPG_BF16: rounded once; DPG_F32),
+ * dgain, dbias: cols elements each of grad_dtype (DPG_BF16: rounded once; DPG_F32),
  * aligned to their element, so they may be slices of a replica's flat gradient
  * buffer; accumulate != 0 (DPG_F32 only) adds to what they hold.  The sums over
  * the rows are in fp32, in an order fixed by the sizes and types: the same bits on

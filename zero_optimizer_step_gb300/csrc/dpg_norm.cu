@@ -990,6 +990,7 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
     if (st == DPG_OK) st = dpg::norm_pointer(mean, DPG_F32, true, "mean", who);
     if (st == DPG_OK) st = dpg::norm_pointer(rstd, DPG_F32, true, "rstd", who);
     if (st != DPG_OK) return st;
+    if (mean && mean == rstd) return fail(DPG_ERR_INVALID_ARG, "%s: mean and rstd share a buffer", who);
     dpg::NormArgs a{};
     a.x = x;
     a.gain = gain;
@@ -1053,6 +1054,7 @@ int dpg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_
     if (st != DPG_OK) return st;
     if (sums && !workspace) return fail(DPG_ERR_INVALID_ARG, "%s: workspace is NULL", who);
     if (sums && !dpg::aligned(workspace, 16)) return fail(DPG_ERR_MISALIGNED, "%s: workspace misaligned", who);
+    if (dgain && dgain == dbias) return fail(DPG_ERR_INVALID_ARG, "%s: dgain and dbias share a buffer", who);
     if (!sums && !dx) return DPG_OK;
     const bool f32 = dtype == DPG_F32;
     dpg::NormBackArgs a{};
