@@ -673,9 +673,10 @@ int dpg_fp4_dequantize(const dpg_fp4* q, void* out, int32_t out_dtype, int64_t r
  * matrices of a stack, from its place in the flat fp32 masters.  by_row and
  * by_col: HOST arrays of n = the object's number of matrices, either may be
  * NULL, not both; entry k must have matrix k's rows and cols (by_col: cols and
- * rows), and buffers of its own (its two forms may have one amax).  seed as in dpg_fp4_quantize; matrix k takes the seed plus k, so the seeds
- * of two calls have to be n or more apart, or matrices share random bits.  All
- * arguments are checked before anything is launched. */
+ * rows), and buffers of its own (its two forms may have one amax).  seed as in
+ * dpg_fp4_quantize; matrix k takes the seed plus k, so the seeds of two calls have
+ * to be n or more apart, or matrices share random bits.  All arguments are checked
+ * before anything is launched. */
 int dpg_allgather_params_fp4(const dpg_matrices_t* mats, const float* master, const int64_t* seed,
                              const dpg_fp4* by_row, const dpg_fp4* by_col, int32_t n, void* stream);
 

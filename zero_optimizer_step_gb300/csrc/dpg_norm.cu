@@ -27,6 +27,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "dpg_device.cuh"
 #include "dpg_host.h"
@@ -978,7 +979,7 @@ int dpg_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, con
     int st = dpg::norm_shape(rows, cols, dtype, param_dtype, who);
     if (st != DPG_OK) return st;
     // (not one that fp32 makes an infinity or a zero of)
-    if (!(eps >= 0.0) || !std::isfinite(float(eps)) || (eps > 0.0 && float(eps) == 0.0f))
+    if (!(eps >= 0.0 && eps <= double(std::numeric_limits<float>::max())) || (eps > 0.0 && float(eps) == 0.0f))
         return fail(DPG_ERR_INVALID_ARG, "%s: eps %g", who, eps);
     if ((mean == nullptr) != (rstd == nullptr))
         return fail(DPG_ERR_INVALID_ARG, "%s: mean and rstd are kept together", who);
